@@ -23,6 +23,7 @@ FMT_FP4, FMT_FP8 = 0, 1
 LAYOUT_ROWS, LAYOUT_BLOCK8, LAYOUT_BLOCK8R = 0, 1, 2
 OP_APPEND, OP_INDEX_FULL, OP_INDEX_REINDEX, OP_SPARSE_ATTN = range(4)
 OUT_BF16, OUT_F32 = 0, 1
+X_BF16, X_E4M3 = 0, 1
 INDEX_HEADS, INDEX_DIM, ATTN_HEADS, LATENT_DIM, BLOCK, STATUS_BYTES = 32, 128, 64, 512, 8, 256
 
 _p = ctypes.c_void_p
@@ -50,6 +51,13 @@ EXPORTS = {
                                         _p, _int, _p, _p, _sz, _p]),
     "csa2_index_reindex_noalloc": (_int, [_p, _p, _p, _i64, _p, _p, _i64, _p, _p, _i32, _p, _int, _int, _p,
                                           _p, _p]),
+    "csa2_page_plan": (_int, [_p, _p, _i64, _int, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _sz, _p]),
+    "csa2_paged_attn_workspace_bytes": (_sz, [_i64, _int, _i64, _i32, _i32, _int]),
+    "csa2_paged_attn": (_int, [_p, _i64, _int, _p, _p, _i64, _i32, _i32, _int, _p, _p, _i64, _p, _i64, _int, _int,
+                               ctypes.c_float, _p, _p, _p, _sz, _p]),
+    "csa2_rmsnorm_fp8": (_int, [_p, _i64, _p, _p, _p, _i64, _int, ctypes.c_float, _int, _p, _p, _p, _p]),
+    "csa2_fp4_matvec_workspace_bytes": (_sz, [_i64, _int, _i64]),
+    "csa2_fp4_matvec": (_int, [_p, _int, _p, _i64, _i64, _int, _p, _p, _i64, ctypes.c_float, _p, _int, _p, _sz, _p]),
     "csa2_launch_count": (_i64, []),
     "csa2_debug_wait_limit": (_int, [_i64]),
     "csa2_kernel_name": (ctypes.c_char_p, [_int]),
@@ -187,8 +195,46 @@ def csa2_sparse_attn_prefill(q_bf16, n_q, kv_codes, kv_scales, n_rows, kv_start,
         ws_bytes, _stream(stream)))
 
 
+def csa2_page_plan(cached, added, n_req, page_size, table, max_pages, free_pages, n_pages, n_free, n_free_out, q_start,
+                   kv_len, slots, pos, max_new, ws, ws_bytes, stream=None):
+    return _check("csa2_page_plan", lib.csa2_page_plan(
+        _ptr(cached), _ptr(added), n_req, page_size, _ptr(table), max_pages, _ptr(free_pages), n_pages, _ptr(n_free),
+        _ptr(n_free_out), _ptr(q_start), _ptr(kv_len), _ptr(slots), _ptr(pos), max_new, _ptr(ws), ws_bytes,
+        _stream(stream)))
+
+
+def csa2_paged_attn_workspace_bytes(n_tokens, n_heads, n_req, max_q, max_kv, window):
+    return lib.csa2_paged_attn_workspace_bytes(n_tokens, n_heads, n_req, max_q, max_kv, window)
+
+
+def csa2_paged_attn(q_bf16, n_tokens, n_heads, q_start, kv_len, n_req, max_q, max_kv, fmt, codes, scales, n_rows, table,
+                    max_pages, page_size, window, sm_scale, out, out_lse, ws, ws_bytes, stream=None):
+    return _check("csa2_paged_attn", lib.csa2_paged_attn(
+        _ptr(q_bf16), n_tokens, n_heads, _ptr(q_start), _ptr(kv_len), n_req, max_q, max_kv, fmt, _ptr(codes),
+        _ptr(scales), n_rows, _ptr(table), max_pages, page_size, window, sm_scale, _ptr(out), _ptr(out_lse), _ptr(ws),
+        ws_bytes, _stream(stream)))
+
+
+def csa2_rmsnorm_fp8(x, x_stride, residual, residual_out, weight, n, dim, eps, group, codes, scales, y_bf16, stream=None):
+    return _check("csa2_rmsnorm_fp8", lib.csa2_rmsnorm_fp8(
+        _ptr(x), x_stride, _ptr(residual), _ptr(residual_out), _ptr(weight), n, dim, eps, group, _ptr(codes),
+        _ptr(scales), _ptr(y_bf16), _stream(stream)))
+
+
+def csa2_fp4_matvec_workspace_bytes(n, k, n_out):
+    return lib.csa2_fp4_matvec_workspace_bytes(n, k, n_out)
+
+
+def csa2_fp4_matvec(x, x_fmt, x_scales, x_stride, n, k, codes, scales, n_out, alpha, out, out_dtype, ws, ws_bytes,
+                    stream=None):
+    return _check("csa2_fp4_matvec", lib.csa2_fp4_matvec(
+        _ptr(x), x_fmt, _ptr(x_scales), x_stride, n, k, _ptr(codes), _ptr(scales), n_out, alpha, _ptr(out), out_dtype,
+        _ptr(ws), ws_bytes, _stream(stream)))
+
+
 KERNELS = ("scan_blockmax", "select_blocks", "pool_score", "select_topk", "attn_split",
-           "attn_merge", "quantize_fp4", "quantize_fp8", "rope_table")
+           "attn_merge", "quantize_fp4", "quantize_fp8", "rope_table", "page_plan", "paged_attn", "paged_merge",
+           "rmsnorm_fp8", "fp4_matvec")
 
 
 def csa2_launch_count():

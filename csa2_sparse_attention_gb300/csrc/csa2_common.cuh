@@ -31,6 +31,9 @@ enum BoundsCheck : int32_t {
     CHK_ROWS = 5,        // index/attn: kv_start + n_visible > n_rows
     CHK_POOL = 6,        // reindex: pool block outside [0, ceil(n/8))
     CHK_TOPK = 7,        // attn: topk entry outside [-1, n)
+    CHK_PAGE = 8,        // paged: page id outside the cache
+    CHK_LENGTH = 9,      // paged: a request's length is negative or does not fit
+    CHK_CAPACITY = 10,   // page plan: more new tokens or pages than there are
 };
 
 __device__ __forceinline__ void record(Status* st, int32_t code, int32_t which, int32_t item,

@@ -16,7 +16,12 @@ enum KernelId {
     K_QUANT_FP4 = 6,
     K_QUANT_FP8 = 7,
     K_ROPE_TABLE = 8,
-    K_COUNT = 9
+    K_PAGE_PLAN = 9,
+    K_PAGED_ATTN = 10,
+    K_PAGED_MERGE = 11,
+    K_RMSNORM = 12,
+    K_MATVEC = 13,
+    K_COUNT = 14
 };
 
 void timer_begin(int id, cudaStream_t s);

@@ -314,12 +314,139 @@ csa2_status csa2_sparse_attn_prefill(const void* q_bf16, int64_t n_q,
                                      void* ws, size_t ws_bytes, csa2_stream_t stream);
 
 /*
+ * ---- A layer's step over a paged cache ----
+ *
+ * The next calls run a step in which every request brings a chunk of new
+ * tokens (one for a decoding request) and keeps its latents in pages: page p
+ * holds rows p*page_size .. p*page_size + page_size - 1 of a latent plane,
+ * and position i of request r is row table[r][i / page_size] * page_size +
+ * i % page_size.  In order:
+ *   csa2_rmsnorm_fp8      residual, norm and E4M3 activations
+ *   csa2_fp4_matvec       queries and latents of a few tokens, FP4 weights
+ *   csa2_page_plan        pages, rows and positions of the new tokens
+ *   csa2_quantize_append  with the plan's rows (dst_row) and positions (pos)
+ *   csa2_paged_attn       the new tokens over everything their request holds
+ * Tokens are packed: request r owns tokens q_start[r] .. q_start[r+1] - 1.
+ */
+
+/* Activations of csa2_fp4_matvec. */
+enum { CSA2_X_BF16 = 0, CSA2_X_E4M3 = 1 };
+
+/*
+ * Block tables and slot maps of a step, from the requests' lengths.
+ * Request r holds cached[r] entries in the first held = ceil(cached[r] /
+ * page_size) pages of its table row and brings added[r] new ones.  It takes
+ * need = ceil((cached[r] + added[r]) / page_size) - held pages off the end of
+ * the free list, requests in order: with o the pages that earlier requests
+ * take, table[r][held + j] = free_pages[n_free - 1 - (o + j)], j < need.
+ *   cached, added [n_req] int32.
+ *   page_size     a multiple of 8, 8..65536.
+ *   table         [n_req][max_pages] int32, in place: only the new pages'
+ *                 entries are written.
+ *   free_pages    [n_pages] int32, the free pages' ids; n_free int32[1], how
+ *                 many of them are.  n_pages: the cache's pages.
+ *   n_free_out    int32[1]: n_free minus the pages taken (may be n_free).
+ *   q_start       [n_req + 1] int32 out: exclusive sums of added.
+ *   kv_len        [n_req] int32 out: cached + added (not cached itself).
+ *   slots, pos    [max_new] int64 out: destination row and position of each
+ *                 new token, request after request; -1 behind the last one.
+ * A call that cannot be served takes nothing: where a length is negative, a
+ * request does not fit its table row, the new tokens exceed max_new or the
+ * pages n_free, the table stays as it is, n_free_out = n_free, q_start and
+ * kv_len are 0, slots and pos are -1, and the first problem is recorded in
+ * ws.  A page id outside [0, n_pages) gives slots of -1 and is recorded (a
+ * new page's table entry is then -1).  ws: CSA2_STATUS_BYTES bytes, zeroed
+ * once with csa2_status_reset.
+ */
+csa2_status csa2_page_plan(const int32_t* cached, const int32_t* added, int64_t n_req, int page_size,
+                           int32_t* table, int64_t max_pages, const int32_t* free_pages, int64_t n_pages,
+                           const int32_t* n_free, int32_t* n_free_out, int32_t* q_start, int32_t* kv_len,
+                           int64_t* slots, int64_t* pos, int64_t max_new, void* ws, size_t ws_bytes,
+                           csa2_stream_t stream);
+
+/*
+ * Causal attention of each request's new tokens over its paged latents (keys
+ * and values are the same 512-wide latent, shared by the heads).  Token i of
+ * request r sits at position t = kv_len[r] - (q_start[r+1] - q_start[r]) + i
+ * and sees positions max(0, t + 1 - window) .. t (window 0: all up to t):
+ *   l_p = sm_scale * q . c_p,  o = sum softmax(l)_p c_p.
+ *   q_bf16   [n_tokens][n_heads][512] bf16; n_heads 1..128.
+ *   q_start  [n_req + 1] int32, kv_len [n_req] int32 (csa2_page_plan's).
+ *   max_q, max_kv: host upper bounds of a request's tokens and entries.
+ *   fmt      CSA2_FMT_FP4: codes [n_rows][256] and scales [n_rows][32], as
+ *            csa2_quantize_append writes them (CSA2_LAYOUT_ROWS);
+ *            CSA2_FMT_FP8: codes are E4M3 rows [n_rows][512], scales NULL.
+ *   table    [n_req][max_pages] int32; page_size a multiple of 8, 8..65536.
+ *   out      [n_tokens][n_heads][512] bf16, rounded once from fp32 sums (the
+ *            probabilities enter the product in f16).
+ *   out_lse  [n_tokens][n_heads] fp32, natural log-sum-exp of the scaled
+ *            logits, or NULL.
+ * A token that sees nothing gets zeros and lse = -inf.  Tokens from
+ * q_start[n_req] on are left as they are.  A request whose kv_len lies
+ * outside [0, min(max_kv, max_pages * page_size)] is recorded and sees
+ * nothing; one whose tokens lie outside [0, n_tokens) or exceed max_q is
+ * recorded and skipped; a table entry outside [0, n_rows / page_size) is
+ * recorded and its page is not seen.  Latents that no token sees may hold
+ * anything, NaN included.
+ * ws: csa2_paged_attn_workspace_bytes (0 for bad sizes) for the same sizes.
+ */
+size_t csa2_paged_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
+                                       int32_t max_kv, int window);
+csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
+                            const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, int fmt,
+                            const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* table,
+                            int64_t max_pages, int page_size, int window, float sm_scale, void* out,
+                            float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and E4M3 output:
+ *   h = bf16(x + residual)  (h = x without a residual)
+ *   y = h / sqrt(mean(h^2) + eps) * weight            (fp32)
+ *   s = max|y| / 448 over the row (group 0) or each 128 channels (group 128)
+ *   codes = nearest-even E4M3 of y / s (0 where s is 0)
+ *   x            [n] rows of dim bf16, x_stride elements apart (>= dim, a
+ *                multiple of 8).
+ *   residual     [n][dim] bf16 or NULL; residual_out [n][dim] takes h (may be
+ *                residual itself; needed with a residual, else NULL).
+ *   weight       [dim] bf16.  dim: a multiple of 8, 8..16384 (group 128: a
+ *                multiple of 128).  eps >= 0, finite.
+ *   codes        [n][dim] E4M3; scales [n] or [n][dim/128] fp32.
+ *   y_bf16       [n][dim] bf16 of y, or NULL.
+ * The mean is an fp32 sum: |h| up to 2^56.  A NaN or infinite h makes the
+ * codes and the scale of the row's groups what the formula gives (NaN).
+ */
+csa2_status csa2_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                             const void* weight, int64_t n, int dim, float eps, int group, uint8_t* codes,
+                             float* scales, void* y_bf16, csa2_stream_t stream);
+
+/*
+ * Products of a few rows with FP4 weights: out[i][j] = alpha * sum_c x[i][c]
+ * W[j][c].
+ *   x            [n] rows of k elements, x_stride elements apart (>= k, a
+ *                multiple of 16): bf16 (x_fmt CSA2_X_BF16, x_scales NULL), or
+ *                E4M3 with one fp32 scale per row, x_scales [n] (CSA2_X_E4M3;
+ *                csa2_rmsnorm_fp8 with group 0 gives both).
+ *   codes, scales  W: n_out rows of k channels, [n_out][k/2] E2M1 codes and
+ *                [n_out][k/16] E4M3 scales: csa2_quantize_append of the
+ *                weights in CSA2_LAYOUT_ROWS, as n_out*k/128 rows of 128.
+ *   k            a multiple of 128, up to 65536.  n rows: any number; the
+ *                weights are read once for each 16 rows.
+ *   out          [n][n_out], bf16 (CSA2_OUT_BF16) or fp32 (CSA2_OUT_F32).
+ * ws: csa2_fp4_matvec_workspace_bytes(n, k, n_out) bytes (0 for bad sizes).
+ */
+size_t csa2_fp4_matvec_workspace_bytes(int64_t n, int k, int64_t n_out);
+csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_scales, int64_t x_stride, int64_t n, int k,
+                            const uint8_t* codes, const uint8_t* scales, int64_t n_out, float alpha, void* out,
+                            int out_dtype, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
  * Instrumentation (off by default; the compute path never depends on it).
  * csa2_launch_count: kernels launched through the library by this process.
  * csa2_timer_enable: bracket the next max_launches launches of kernel
  *   `kernel_id` (0 scan_blockmax, 1 select_blocks, 2 pool_score,
  *   3 select_topk, 4 attn_split (either attention kernel), 5 attn_merge, 6 quantize_fp4,
- *   7 quantize_fp8, 8 rope_table) with CUDA events on their stream.  Not for
+ *   7 quantize_fp8, 8 rope_table, 9 page_plan, 10 paged_attn, 11 paged_merge,
+ *   12 rmsnorm_fp8, 13 fp4_matvec) with CUDA events on their stream.  Not for
  *   use during stream capture.
  * csa2_timer_read: wait for those events, return the summed device time and
  *   the number of launches timed, and switch the timer off.

@@ -1,0 +1,597 @@
+"""The operators of a step over a paged cache against their 64-bit forms:
+page planning, causal attention of a chunk of new tokens over the pages,
+residual norm to E4M3, and FP4 products, at the sizes and masks where they
+can go wrong; graphs, streams and a whole step of them together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import csa2_oracle as O
+from oracle import paged_oracle as PO
+
+pytestmark = pytest.mark.gpu
+D = 512
+SM = 1.0 / math.sqrt(D)
+
+
+@pytest.fixture(scope="module")
+def abi():
+    from csa2_sparse_attention_gb300 import abi as A
+    return A
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16)
+
+
+def fresh_ws(abi, n):
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    abi.csa2_status_reset(ws)
+    return ws
+
+
+# --------------------------------------------------------------- page plan
+def plan_inputs(rng, cached, added, page, spare=3, extra_pages=2):
+    cached, added = np.asarray(cached, np.int32), np.asarray(added, np.int32)
+    pages = lambda n: -(-n.astype(np.int64) // page)  # noqa: E731
+    held, after = pages(cached), pages(cached + added)
+    max_pages = int(after.max(initial=1)) + extra_pages
+    n_pages = int(after.sum()) + spare
+    ids = rng.permutation(n_pages).astype(np.int32)
+    table = np.full((len(cached), max_pages), -7, np.int32)
+    at = 0
+    for r in range(len(cached)):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    free = np.full(n_pages, -9, np.int32)
+    free[:n_pages - at] = ids[at:]
+    return cached, added, table, free, n_pages - at, n_pages
+
+
+def run_plan(abi, cached, added, page, table, free, n_free, n_pages, max_new, alias=True, stream=None):
+    R = len(cached)
+    t, nf = dev(table), dev(np.array([n_free], np.int32))
+    nfo = nf if alias else torch.full((1,), -5, dtype=torch.int32, device="cuda")
+    qs = torch.full((R + 1,), -5, dtype=torch.int32, device="cuda")
+    kl = torch.full((max(R, 1),), -5, dtype=torch.int32, device="cuda")
+    sl = torch.full((max(max_new, 1),), -5, dtype=torch.int64, device="cuda")
+    po = torch.full((max(max_new, 1),), -5, dtype=torch.int64, device="cuda")
+    ws = fresh_ws(abi, abi.STATUS_BYTES)
+    c, a = dev(cached), dev(added)
+    abi.csa2_page_plan(c if R else None, a if R else None, R, page, t if t.numel() else None, table.shape[1], dev(free) if n_pages else None, n_pages,
+                       nf, nfo, qs, kl if R else None, sl if max_new else None, po if max_new else None, max_new, ws,
+                       ws.numel(), stream)
+    torch.cuda.synchronize()
+    return (t.cpu().numpy(), qs.cpu().numpy(), kl.cpu().numpy()[:R], sl.cpu().numpy()[:max_new],
+            po.cpu().numpy()[:max_new], int(nfo.item()), abi.csa2_status_fetch(ws))
+
+
+def check_plan(got, want):
+    for g, w in zip(got[:5], want[:5]):
+        np.testing.assert_array_equal(g, w)
+    assert got[5] == want[5]
+
+
+@pytest.mark.parametrize("case", [
+    ("one token", [0], [1], 8, 0), ("page full", [16, 15, 17], [1, 1, 1], 16, 2), ("nothing new", [5, 0, 9], [0, 0, 0], 8, 3),
+    ("zeros between", [0, 40, 8, 7, 0], [3, 0, 9, 0, 65], 8, 1), ("page of 200", [199, 200, 401], [2, 400, 1], 200, 0),
+    ("no room behind", [3, 100], [50, 28], 64, 0)])
+@pytest.mark.parametrize("alias", [True, False])
+def test_plan_small(abi, case, alias):
+    _, cached, added, page, tail = case
+    rng = np.random.default_rng(len(cached) + page)
+    args = plan_inputs(rng, cached, added, page)
+    cached, added, table, free, n_free, n_pages = args
+    max_new = int(added.sum()) + tail
+    got = run_plan(abi, cached, added, page, table, free, n_free, n_pages, max_new, alias)
+    check_plan(got, PO.page_plan(cached, added, page, table, free, n_free, n_pages, max_new))
+    assert got[6][0] == abi.OK
+
+
+@pytest.mark.parametrize("R,page,top", [(1, 64, 70000), (257, 16, 300), (600, 128, 90), (1030, 8, 40)])
+def test_plan_many(abi, R, page, top):
+    rng = np.random.default_rng(R)
+    cached, added = rng.integers(0, 500, R), rng.integers(0, top + 1, R)
+    added[rng.random(R) < 0.3] = 0
+    if R == 1:
+        added[0] = top
+    cached, added, table, free, n_free, n_pages = plan_inputs(rng, cached, added, page)
+    max_new = int(added.sum()) + 1000
+    got = run_plan(abi, cached, added, page, table, free, n_free, n_pages, max_new)
+    check_plan(got, PO.page_plan(cached, added, page, table, free, n_free, n_pages, max_new))
+    assert got[6][0] == abi.OK
+
+
+@pytest.mark.parametrize("what", ["pages", "tokens", "negative", "row", "free count"])
+def test_plan_that_cannot_be_served_takes_nothing(abi, what):
+    rng = np.random.default_rng(5)
+    cached, added, table, free, n_free, n_pages = plan_inputs(rng, [9, 30, 2], [20, 1, 3000], 8, extra_pages=0)
+    max_new = int(added.sum()) + 4
+    if what == "pages":
+        n_free = 100
+    elif what == "tokens":
+        max_new = int(added.sum()) - 1
+    elif what == "negative":
+        added[1] = -1
+    elif what == "row":
+        added[1] = 4000
+        max_new = 8000
+    else:
+        n_free = n_pages + 1
+    got = run_plan(abi, cached, added, 8, table, free, n_free, n_pages, max_new)
+    want = PO.page_plan(cached, added, 8, table, free, n_free, n_pages, max_new)
+    assert not want[6]
+    check_plan(got, want)
+    assert got[6][0] == abi.ERR_DEVICE_BOUNDS
+
+
+def test_plan_bad_page_ids_give_no_slots(abi):
+    rng = np.random.default_rng(6)
+    cached, added, table, free, n_free, n_pages = plan_inputs(rng, [9, 30], [20, 5], 8)
+    table[0, 1] = n_pages       # the half-filled page of request 0
+    free[n_free - 1] = -3       # its first new page
+    got = run_plan(abi, cached, added, 8, table, free, n_free, n_pages, 40)
+    want = PO.page_plan(cached, added, 8, table, free, n_free, n_pages, 40)
+    check_plan(got, want)
+    assert (want[3][:7] == -1).all() and got[6][0] == abi.ERR_DEVICE_BOUNDS
+
+
+def test_plan_empty(abi):
+    z = np.zeros(0, np.int32)
+    got = run_plan(abi, z, z, 8, np.zeros((0, 4), np.int32), np.arange(5, dtype=np.int32), 5, 5, 3)
+    assert got[1].tolist() == [0] and got[3].tolist() == [-1] * 3 and got[5] == 5
+
+
+# --------------------------------------------------------------- attention
+def cache_rows(rng, n_rows, fmt, amp=1.0):
+    x = amp * rng.standard_normal((n_rows, D)).astype(np.float32)
+    if fmt == "fp8":
+        return O.e4m3_encode(x.astype(np.float64)).astype(np.uint8), None
+    t = torch.from_numpy(x).view(n_rows, D // 16, 16)
+    s = (t.abs().amax(2) / 6.0).to(torch.float8_e4m3fn)
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    c = torch.bucketize((t / s.float().clamp(min=2.0 ** -9).unsqueeze(2)).abs(), mids) | ((t < 0).long() << 3)
+    c = c.view(n_rows, D).numpy().astype(np.uint8)
+    return (c[:, 0::2] | (c[:, 1::2] << 4)), s.view(torch.uint8).numpy()
+
+
+def attn_inputs(rng, kv_len, new, heads, page, fmt, q_amp=1.0, c_amp=1.0, tail=0):
+    kv_len, new = np.asarray(kv_len, np.int32), np.asarray(new, np.int32)
+    pages = -(-kv_len // page)
+    n_pages, max_pages = int(pages.sum()) + 2, max(1, int(pages.max()))
+    ids = rng.permutation(n_pages).astype(np.int32)
+    table = np.full((len(kv_len), max_pages), -1, np.int32)
+    at = 0
+    for r, n in enumerate(pages):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    codes, scales = cache_rows(rng, n_pages * page, fmt, c_amp)
+    q_start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(q_start[-1]) + tail
+    q = bf16(q_amp * rng.standard_normal((max(T, 1), heads, D)))[:T]
+    return dict(q=q, q_start=q_start, kv_len=kv_len, codes=codes, scales=scales, table=table, page=page, fmt=fmt, T=T, H=heads,
+                max_q=int(new.max(initial=0)), max_kv=int(kv_len.max(initial=0)))
+
+
+class Attn:
+    """The device side of one attention call."""
+
+    def __init__(self, abi, s, window=0, max_q=None, max_kv=None, ws=None, fill=7.0):
+        self.abi, self.s, self.window = abi, s, window
+        self.q, self.q_start, self.kv_len = s["q"].cuda(), dev(s["q_start"]), dev(s["kv_len"])
+        self.codes, self.scales = dev(s["codes"]), None if s["scales"] is None else dev(s["scales"])
+        self.table = dev(s["table"])
+        self.max_q = s["max_q"] if max_q is None else max_q
+        self.max_kv = s["max_kv"] if max_kv is None else max_kv
+        self.out = torch.full((s["T"], s["H"], D), fill, dtype=torch.bfloat16, device="cuda")
+        self.lse = torch.full((s["T"], s["H"]), fill, device="cuda")
+        size = abi.csa2_paged_attn_workspace_bytes(s["T"], s["H"], len(s["kv_len"]), self.max_q, self.max_kv, window)
+        assert size >= abi.STATUS_BYTES
+        self.ws = fresh_ws(abi, size) if ws is None else ws
+
+    def call(self, stream=None, lse=True):
+        s, abi = self.s, self.abi
+        abi.csa2_paged_attn(self.q, s["T"], s["H"], self.q_start, self.kv_len, len(s["kv_len"]), self.max_q, self.max_kv,
+                            abi.FMT_FP4 if s["fmt"] == "fp4" else abi.FMT_FP8, self.codes, self.scales,
+                            self.codes.shape[0], self.table, s["table"].shape[1], s["page"], self.window, SM, self.out,
+                            self.lse if lse else None, self.ws, self.ws.numel(), stream)
+
+    def result(self):
+        torch.cuda.synchronize()
+        return self.out.float().cpu().numpy().astype(np.float64), self.lse.cpu().numpy().astype(np.float64)
+
+
+def check_attn(out, lse, s, window, bad_page=None, tokens=None):
+    """Against the 64-bit form.  With u = 2^-24: a logit is a 512-term fp32 sum of exact products, off by at most
+    512 u sum|q||c| sm_scale (the true error grows with the square root; the bound is taken at 64 u), so the
+    probabilities by a factor 1 + d, d = 64 u dot sm + 2^-21 (the exponential); they enter the product rounded to
+    f16 (2^-11 relative, 2^-24 absolute below f16's normal range, against a sum of at least 1 for a largest
+    probability of at least 1), whose sums are over |c| <= big: |o - o*| <= (2 d + 2^-11 + n 2^-24) big, then bf16
+    rounds once: 2^-8 relative.  The sum of n positive terms in fp32 is off by at most n u relative in any order
+    (each partial sum rounds once), which enters the logarithm as n u and the outputs as n u |o|."""
+    T = int(s["q_start"][-1]) if tokens is None else tokens
+    want, wlse, (dot, big) = PO.paged_attention(s["q"].float().numpy(), s["q_start"], s["kv_len"], s["codes"], s["scales"],
+                                                s["table"], s["page"], window, SM, bad_page)
+    d = 64 * 2.0 ** -24 * dot * SM + 2.0 ** -21
+    tol = ((2 * d + 2.0 ** -11 + s["max_kv"] * 2.0 ** -24) * big)[..., None] + (2.0 ** -8 + s["max_kv"] * 2.0 ** -24) * np.abs(want)
+    err = np.abs(out - want)[:T]
+    assert np.isfinite(out[:T]).all()
+    assert (err <= tol[:T]).all(), (err - tol[:T]).max()
+    live = np.isfinite(wlse[:T])
+    assert np.array_equal(np.isneginf(lse[:T]), ~live)
+    assert (out[:T][~live] == 0).all()
+    ltol = d + s["max_kv"] * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(np.where(np.isfinite(wlse), wlse, 0)))
+    assert (np.abs(lse[:T][live] - wlse[:T][live]) <= ltol[:T][live]).all()
+
+
+ATTN = [
+    # kv_len, new, heads, page, fmt, window
+    ([1], [1], 64, 8, "fp4", 0),
+    ([1, 2, 127, 128, 129, 640], [1, 1, 1, 1, 1, 1], 64, 16, "fp4", 0),
+    ([700], [130], 64, 64, "fp4", 0),
+    ([300, 17, 64], [300, 17, 1], 5, 8, "fp4", 0),
+    ([515, 1, 260], [3, 1, 2], 128, 128, "fp4", 0),
+    ([900, 33], [1, 33], 1, 200, "fp8", 0),
+    ([257, 400, 80], [7, 1, 80], 16, 16, "fp8", 128),
+    ([500, 90], [40, 3], 24, 64, "fp4", 1),
+    ([385, 129], [9, 129], 40, 8, "fp8", 100),
+    ([0, 5, 0, 260], [0, 5, 0, 2], 64, 8, "fp4", 0),
+    ([2000, 1500, 1800], [1, 2, 1], 8, 64, "fp4", 1000),
+    ([3, 2], [9, 2], 64, 8, "fp4", 0),        # more tokens than entries: the first rows see nothing
+    ([0, 4], [3, 4], 64, 8, "fp8", 0),        # a request without entries
+]
+
+
+@pytest.mark.parametrize("i", range(len(ATTN)))
+def test_attention(abi, i):
+    kv, new, H, page, fmt, window = ATTN[i]
+    s = attn_inputs(np.random.default_rng(100 + i), kv, new, H, page, fmt)
+    a = Attn(abi, s, window)
+    a.call()
+    check_attn(*a.result(), s, window)
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("new", [1, 37])
+def test_attention_long_and_looser_bounds(abi, fmt, new):
+    """Long ragged requests (keys split over blocks), with host bounds above the lengths."""
+    s = attn_inputs(np.random.default_rng(9), [3000, 5, 1311], [new, 1, min(new, 3)], 64, 64, fmt)
+    a = Attn(abi, s, 0, max_q=new + 5, max_kv=9000)
+    a.call()
+    check_attn(*a.result(), s, 0)
+
+
+@pytest.mark.parametrize("q_amp", [2.0 ** -20, 2.0 ** 14, 40.0])
+def test_attention_query_ranges(abi, q_amp):
+    """Tiny and huge queries keep their precision; at 40 the softmax is one-hot and its maximum moves."""
+    s = attn_inputs(np.random.default_rng(3), [450, 130], [4, 1], 64, 16, "fp4", q_amp=q_amp, c_amp=1.0 if q_amp < 1e3 else 2.0 ** -5)
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+
+
+def test_attention_growing_logits(abi):
+    """Keys ordered so that each is seen as a new maximum, by more and more: every step rescales."""
+    s = attn_inputs(np.random.default_rng(4), [1024], [1], 64, 8, "fp8")
+    base = s["q"][0, 0].float().numpy()
+    rows = (s["table"][0, np.arange(1024) // 8].astype(np.int64) * 8 + np.arange(1024) % 8)
+    s["codes"][rows] = O.e4m3_encode((np.linspace(-8, 8, 1024)[:, None] * base[None]).astype(np.float64))
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_attention_leaves_out_what_is_masked(abi, fmt):
+    """NaN and the largest values in rows behind the sequence, outside the window, in later tokens' entries and in
+    other pages do not reach rows that do not see them; a token that sees a NaN entry is NaN as a whole."""
+    rng = np.random.default_rng(8)
+    s = attn_inputs(rng, [201, 77], [6, 2], 64, 16, fmt)
+    clean = {**s, "codes": s["codes"].copy(), "scales": None if s["scales"] is None else s["scales"].copy()}
+    row = lambda r, p: int(s["table"][r, p // 16]) * 16 + p % 16  # noqa: E731
+
+    def spoil(at):
+        if fmt == "fp8":
+            s["codes"][at, ::3] = 0x7F
+            s["codes"][at, 1::3] = 0xFE
+        else:
+            s["scales"][at, ::2] = 0x7F
+            s["scales"][at, 1::2] = 0x7E
+    for p in list(range(201, 208)) + [199, 200, 3, 64]:
+        spoil(row(0, p))
+    for p in range(77, 80):
+        spoil(row(1, p))
+    window = 100  # request 0's tokens sit at 195 .. 200: 3 and 64 are outside, 199 is seen by the last two
+    a = Attn(abi, s, window)
+    a.call()
+    out, lse = a.result()
+    assert np.isnan(out[4:6]).all() and np.isnan(lse[4:6]).all()
+    out[4:6], lse[4:6] = 0, 0
+    want = Attn(abi, clean, window)
+    want.call()
+    wout, wlse = want.result()
+    wout[4:6], wlse[4:6] = 0, 0
+    assert np.array_equal(out, wout) and np.array_equal(lse, wlse)
+
+
+def test_attention_pages_and_lengths_outside_are_recorded(abi):
+    s = attn_inputs(np.random.default_rng(11), [100, 60, 40, 50], [2, 2, 2, 2], 64, 8, "fp4")
+    n_pages = len(s["codes"]) // 8
+    s["table"][0, 3] = n_pages
+    s["table"][0, 5] = -2
+    bad = lambda i: i < 0 or i >= n_pages  # noqa: E731
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0, bad_page=bad)
+    st = abi.csa2_status_fetch(a.ws)
+    assert st[0] == abi.ERR_DEVICE_BOUNDS and st[1] == 8 and st[2] == 0
+    # a length above the bound, below zero: that request sees nothing
+    for wrong in (101, -1):
+        s2 = dict(s, kv_len=np.array([100, wrong, 40, 50], np.int32))
+        s2["table"] = np.where(bad_ids(s2["table"], n_pages), 0, s2["table"]).astype(np.int32)
+        b = Attn(abi, s2, max_kv=100)
+        b.call()
+        out, lse = b.result()
+        assert (out[2:4] == 0).all() and np.isneginf(lse[2:4]).all()
+        ref = dict(s2, kv_len=np.array([100, 0, 40, 50], np.int32))
+        check_attn(out, lse, ref, 0)
+        st = abi.csa2_status_fetch(b.ws)
+        assert st[:3] == [abi.ERR_DEVICE_BOUNDS, 9, 1]
+    # tokens above the bound: that request's rows are left as they are
+    s3 = dict(s2, kv_len=np.array([100, 60, 40, 50], np.int32), q_start=np.array([0, 2, 7, 8, 8], np.int32))
+    c = Attn(abi, s3, max_q=2)
+    c.call()
+    out, lse = c.result()
+    assert (out[2:7] == 7).all() and (lse[2:7] == 7).all()
+    assert abi.csa2_status_fetch(c.ws)[:3] == [abi.ERR_DEVICE_BOUNDS, 9, 1]
+
+
+def bad_ids(t, n):
+    return (t < 0) | (t >= n)
+
+
+def test_attention_rows_behind_the_last_token_stay(abi):
+    s = attn_inputs(np.random.default_rng(12), [90, 300], [3, 70], 16, 8, "fp4", tail=19)
+    a = Attn(abi, s)
+    a.call()
+    out, lse = a.result()
+    check_attn(out, lse, s, 0)
+    assert (out[73:] == 7).all() and (lse[73:] == 7).all()
+
+
+def test_attention_without_lse_and_twice(abi):
+    s = attn_inputs(np.random.default_rng(13), [1300, 40], [2, 40], 64, 64, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    one, _ = a.result()
+    a.out.fill_(1.0)
+    a.lse.fill_(3.0)
+    a.call(lse=False)
+    two, lse = a.result()
+    assert np.array_equal(one, two) and (lse == 3).all()
+
+
+def test_attention_graphs_streams_and_one_workspace(abi):
+    """Two captured graphs that share a workspace, replayed in order on a stream of their own with lengths and
+    inputs that change between replays, give what eager calls give."""
+    s1 = attn_inputs(np.random.default_rng(14), [2100, 700], [1, 1], 64, 64, "fp4")
+    s2 = attn_inputs(np.random.default_rng(15), [640, 1900], [5, 3], 64, 16, "fp8")
+    a, b = Attn(abi, s1), Attn(abi, s2, 128)
+    size = max(a.ws.numel(), b.ws.numel())
+    a.ws = b.ws = fresh_ws(abi, size)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for x in (a, b):
+        x.call(st)
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            x.call(torch.cuda.current_stream())
+        graphs.append(g)
+    for k in range(3):
+        a.kv_len.copy_(torch.tensor([2100 - 500 * k, 700], dtype=torch.int32))
+        b.q.mul_(-1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            for g in graphs:
+                g.replay()
+        st.synchronize()
+        check_attn(*a.result(), dict(s1, kv_len=np.array([2100 - 500 * k, 700], np.int32)), 0)
+        check_attn(*b.result(), dict(s2, q=b.q.cpu()), 128)
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+def test_attention_is_the_sparse_attention_of_all_entries(abi):
+    """Over at most 512 contiguous entries the paged call equals csa2_sparse_attn with every entry selected."""
+    n = 500
+    s = attn_inputs(np.random.default_rng(16), [n], [1], 64, 8, "fp4")
+    order = np.arange(-(-n // 8), dtype=np.int32)
+    s["table"][0, :len(order)] = order
+    a = Attn(abi, s)
+    a.call()
+    out, lse = a.result()
+    topk = torch.full((1, 512), -1, dtype=torch.int32, device="cuda")
+    topk[0, :n] = torch.arange(n, dtype=torch.int32)
+    ws = fresh_ws(abi, abi.csa2_workspace_bytes(abi.OP_SPARSE_ATTN, 1, n, 1, 512))
+    o = torch.empty(1, 64, D, dtype=torch.float32, device="cuda")
+    ls = torch.empty(1, 64, device="cuda")
+    abi.csa2_sparse_attn(a.q, 1, a.codes, a.scales, a.codes.shape[0], torch.zeros(1, dtype=torch.int64, device="cuda"),
+                         torch.tensor([n], dtype=torch.int32, device="cuda"), topk, 512, None, None, 0, SM, o, abi.OUT_F32,
+                         ls, ws, ws.numel())
+    torch.cuda.synchronize()
+    check_attn(o.cpu().numpy().astype(np.float64), ls.cpu().numpy().astype(np.float64), s, 0)
+    check_attn(out, lse, s, 0)
+
+
+# -------------------------------------------------------------------- norm
+def norm_call(abi, x, res, w, group, y=True, in_place=False, stride=None, stream=None):
+    n, dim = x.shape
+    stride = stride or dim
+    xd = torch.full((n, stride), 3.0, dtype=torch.bfloat16, device="cuda")
+    xd[:, :dim] = x.cuda()
+    rd = None if res is None else res.cuda()
+    ro = None if res is None else (rd if in_place else torch.zeros_like(rd))
+    codes = torch.zeros(n, dim, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n, dim // 128 if group else 1, device="cuda")
+    yo = torch.zeros(n, dim, dtype=torch.bfloat16, device="cuda") if y else None
+    abi.csa2_rmsnorm_fp8(xd, stride, rd, ro, w.cuda(), n, dim, 1e-6, group, codes, scales, yo, stream)
+    torch.cuda.synchronize()
+    return (None if ro is None else ro.cpu()), codes.view(torch.float8_e4m3fn).float().cpu().numpy(), scales.cpu().numpy(), \
+        None if yo is None else yo.float().cpu().numpy()
+
+
+def check_norm(h, w, group, codes, scales, y):
+    """y is off by a few fp32 roundings, e = (dim/2 + 8) 2^-24 relative at most for a serial sum's share; the sum
+    here is over a tree of at most 64-long chains: e = 48 * 2^-24.  The scale by e + 2^-24, a code's value by half
+    a step (2^-4 relative, 2^-10 absolute below E4M3's normal range) plus e of y/s."""
+    want = PO.rmsnorm(h, w, 1e-6)
+    n, dim = want.shape
+    e = 48 * 2.0 ** -24
+    g = want.reshape(n, -1, 128 if group else dim)
+    s = np.abs(g).max(axis=2) / 448.0
+    assert (np.abs(scales - s) <= (e + 2.0 ** -24) * s + 2.0 ** -150).all()
+    r = np.divide(g, s[..., None], out=np.zeros_like(g), where=s[..., None] > 0).reshape(n, dim)
+    assert (np.abs(codes - r) <= np.maximum(2.0 ** -4 * np.abs(r), 2.0 ** -10) + 4 * e * np.abs(r)).all()
+    if y is not None:
+        assert (np.abs(y - want) <= (2.0 ** -8 + e) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n,dim,group,res", [(1, 8, 0, True), (3, 128, 128, True), (9, 512, 0, False), (17, 520, 0, True),
+                                             (5, 1024, 128, False), (4, 1032, 0, True), (2, 5120, 0, True),
+                                             (3, 7168, 128, True), (1, 16384, 0, True), (1300, 640, 128, True),
+                                             (2500, 16, 0, False), (1, 16256, 128, False)])
+def test_norm(abi, n, dim, group, res):
+    rng = np.random.default_rng(dim + n)
+    amp = np.exp(rng.standard_normal((n, 1)))
+    x, w = bf16(amp * rng.standard_normal((n, dim))), bf16(1 + 0.2 * rng.standard_normal(dim))
+    r = bf16(amp * rng.standard_normal((n, dim))) if res else None
+    ro, codes, scales, y = norm_call(abi, x, r, w, group)
+    h = x if r is None else (x.float() + r.float()).to(torch.bfloat16)
+    if res:
+        assert torch.equal(ro, h)
+    check_norm(h.double().numpy(), w.double().numpy(), group, codes, scales, y)
+
+
+def test_norm_in_place_strided_and_without_bf16(abi):
+    rng = np.random.default_rng(2)
+    x, w, r = bf16(rng.standard_normal((6, 512))), bf16(rng.standard_normal(512)), bf16(rng.standard_normal((6, 512)))
+    a = norm_call(abi, x, r, w, 0, stride=600, in_place=True, y=False)
+    b = norm_call(abi, x, r, w, 0)
+    assert torch.equal(a[0], b[0]) and np.array_equal(a[1], b[1]) and np.array_equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_extremes(abi, group):
+    """Zero rows, one huge element, tiny rows (subnormal scales), zero weights."""
+    x = np.zeros((5, 256), np.float32)
+    x[1, 7] = 2.0 ** 50
+    x[2] = 2.0 ** -120
+    x[3, :128] = 1.0
+    x[4] = np.linspace(-3, 3, 256)
+    w = np.ones(256, np.float32)
+    _, codes, scales, y = norm_call(abi, bf16(x), None, bf16(w), group)
+    check_norm(bf16(x).double().numpy(), w.astype(np.float64), group, codes, scales, y)
+    assert (codes[0] == 0).all() and (scales[0] == 0).all()
+    w[:] = 2.0 ** -126
+    _, codes, scales, _ = norm_call(abi, bf16(x), None, bf16(w), group, y=False)
+    assert np.isfinite(codes).all() and np.isfinite(scales).all()
+    assert np.abs(codes[1]).max() >= 256  # a subnormal scale keeps the largest code near 448
+
+
+def test_norm_nan_and_infinity(abi):
+    x = np.ones((3, 256), np.float32)
+    x[0, 5] = np.nan
+    x[1, 200] = np.inf
+    _, codes, scales, _ = norm_call(abi, bf16(x), None, bf16(np.ones(256)), 128)
+    assert np.isnan(scales[0]).all() and np.isnan(codes[0]).all()
+    assert np.isnan(scales[1, 1]) and np.isnan(codes[1, 128:]).all()
+    assert scales[1, 0] == 0 and (codes[1, :128] == 0).all()
+    assert np.isfinite(scales[2]).all() and np.isfinite(codes[2]).all()
+
+
+# ------------------------------------------------------------------ matvec
+def weight(rng, n_out, k, amp=1.0):
+    c, s = [], []
+    for i in range(0, n_out * k, D * 4096):
+        m = min(4096, (n_out * k - i + D - 1) // D)
+        a, b = cache_rows(rng, m, "fp4", amp)
+        c.append(a.reshape(-1))
+        s.append(b.reshape(-1))
+    return np.concatenate(c)[:n_out * k // 2].reshape(n_out, k // 2), np.concatenate(s)[:n_out * k // 16].reshape(n_out, k // 16)
+
+
+def matvec_call(abi, x, xs, codes, scales, alpha, out_dtype, stride=None):
+    n, k = x.shape
+    stride = stride or k
+    xd = torch.zeros(max(n, 1), stride, dtype=x.dtype).view(torch.uint8 if x.dtype == torch.float8_e4m3fn else x.dtype)
+    xd[:n, :k] = x.view(xd.dtype)
+    xd = xd.cuda()
+    out = torch.full((max(n, 1), len(codes)), 9.0, dtype=out_dtype, device="cuda")
+    ws = fresh_ws(abi, abi.csa2_fp4_matvec_workspace_bytes(n, k, len(codes)))
+    abi.csa2_fp4_matvec(xd, abi.X_BF16 if xs is None else abi.X_E4M3, None if xs is None else dev(xs), stride, n, k, dev(codes),
+                        dev(scales), len(codes), alpha, out, abi.OUT_BF16 if out_dtype == torch.bfloat16 else abi.OUT_F32, ws,
+                        ws.numel())
+    torch.cuda.synchronize()
+    return out[:n].double().cpu().numpy()
+
+
+def check_matvec(got, x, xs, codes, scales, alpha, out_dtype):
+    """Products are exact; k terms are added in fp32 in chains of at most 512 and trees (bounded at 64 * 2^-24 of the
+    absolute sum), scaled by alpha and the row's scale in fp32, rounded once."""
+    want, reach = PO.matvec(x.double().numpy(), xs, codes, scales, alpha)
+    tol = 64 * 2.0 ** -24 * reach + (2.0 ** -8 if out_dtype == torch.bfloat16 else 0) * np.abs(want)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
+
+
+@pytest.mark.parametrize("n,k,n_out", [(1, 128, 1), (1, 5120, 512), (2, 256, 63), (3, 1536, 130), (8, 384, 1000), (9, 640, 65),
+                                       (16, 1536, 2048), (17, 128, 33), (40, 2048, 100), (1, 65536, 3), (5, 12288, 257),
+                                       (1, 8192, 4099)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_matvec(abi, n, k, n_out, fp8):
+    rng = np.random.default_rng(n * k + n_out)
+    codes, scales = weight(rng, n_out, k)
+    x = np.exp(rng.standard_normal((n, 1))) * rng.standard_normal((n, k))
+    if fp8:
+        xs = (np.abs(x).max(axis=1) / 448).astype(np.float32)
+        xt = torch.from_numpy(x / xs[:, None]).float().to(torch.float8_e4m3fn)
+    else:
+        xs, xt = None, bf16(x)
+    for dt in (torch.bfloat16, torch.float32):
+        got = matvec_call(abi, xt, xs, codes, scales, 0.37, dt, stride=k + 16 if n_out % 2 else None)
+        check_matvec(got, xt, xs, codes, scales, 0.37, dt)
+
+
+def test_matvec_ranges(abi):
+    """Rows of very different size side by side, a zero row, the largest and smallest weights."""
+    rng = np.random.default_rng(1)
+    codes, scales = weight(rng, 96, 512)
+    scales[:32] = 0x7E   # 448
+    scales[32:64] = 0x01  # 2^-9
+    codes[10] = 0x77
+    x = bf16(rng.standard_normal((4, 512)) * np.array([2.0 ** 90, 2.0 ** -90, 1.0, 0.0])[:, None])
+    got = matvec_call(abi, x, None, codes, scales, 1.0, torch.float32)
+    check_matvec(got, x, None, codes, scales, 1.0, torch.float32)
+    assert (got[3] == 0).all()
+
+
+def test_matvec_nan_stays_in_its_row(abi):
+    rng = np.random.default_rng(1)
+    codes, scales = weight(rng, 64, 256)
+    x = bf16(rng.standard_normal((5, 256)))
+    clean = matvec_call(abi, x, None, codes, scales, 1.0, torch.float32)
+    x[1, 3], x[3, 200] = float("nan"), float("inf")
+    scales = scales.copy()
+    scales[7, 2] = 0x7F
+    got = matvec_call(abi, x, None, codes, scales, 1.0, torch.float32)
+    assert np.isnan(got[1]).all() and np.isnan(got[:, 7]).all() and not np.isfinite(got[3]).any()
+    keep = np.ones(64, bool)
+    keep[7] = False
+    assert np.array_equal(got[[0, 2, 4]][:, keep], clean[[0, 2, 4]][:, keep])

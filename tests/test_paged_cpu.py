@@ -1,0 +1,134 @@
+"""Refusals of the paged-step calls: every bad argument returns before any
+launch (the pointers are never valid), and empty calls do nothing.  The
+64-bit forms are pinned by hand-worked values."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as PO
+
+
+@pytest.fixture(scope="module")
+def abi():
+    from csa2_sparse_attention_gb300 import build
+    build.build()
+    from csa2_sparse_attention_gb300 import abi as A
+    return A
+
+
+F = 1 << 20  # never dereferenced
+
+
+def args(defaults, **kw):
+    d = dict(defaults)
+    d.update(kw)
+    return [d[k] for k in defaults]
+
+
+PLAN = dict(cached=F, added=F + 64, n_req=4, page=16, table=F, max_pages=8, free=F, n_pages=32, n_free=F, n_free_out=F,
+            q_start=F, kv_len=F + 128, slots=F, pos=F, max_new=10, ws=F, ws_bytes=256, stream=None)
+ATTN = dict(q=F, n_tokens=4, heads=64, q_start=F, kv_len=F, n_req=2, max_q=2, max_kv=100, fmt=0, codes=F, scales=F, n_rows=128,
+            table=F, max_pages=8, page=16, window=0, sm_scale=0.04, out=F, lse=F, ws=F, ws_bytes=1 << 40, stream=None)
+NORM = dict(x=F, x_stride=512, residual=F, residual_out=F, weight=F, n=4, dim=512, eps=1e-6, group=0, codes=F, scales=F, y=None,
+            stream=None)
+MATVEC = dict(x=F, fmt=0, x_scales=None, x_stride=256, n=2, k=256, codes=F, scales=F, n_out=8, alpha=1.0, out=F, out_dtype=0, ws=F,
+              ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(page=0), "U"), (dict(page=12), "U"), (dict(page=65544), "U"), (dict(n_req=-1), "I"), (dict(cached=None), "I"),
+    (dict(cached=F + 4), "I"), (dict(kv_len=F), "I"), (dict(kv_len=F + 64), "I"), (dict(table=None), "I"), (dict(free=None), "I"),
+    (dict(n_free=None), "I"), (dict(n_free_out=None), "I"), (dict(q_start=None), "I"), (dict(slots=None), "I"),
+    (dict(pos=F + 8), "I"), (dict(max_new=-1), "I"), (dict(max_new=1 << 31), "I"), (dict(max_pages=-1), "I"),
+    (dict(n_pages=1 << 31), "I"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W"), (dict(ws=F + 8), "W")])
+def test_page_plan_refusals(abi, kw, status):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_page_plan(*args(PLAN, **kw)) == {"U": 2, "I": 1, "W": 6}[status]
+    assert abi.csa2_launch_count() == c0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(heads=0), "U"), (dict(heads=129), "U"), (dict(page=4), "U"), (dict(page=20), "U"), (dict(fmt=2), "U"),
+    (dict(scales=None), "I"), (dict(fmt=1), "I"), (dict(q=None), "I"), (dict(q=F + 2), "I"), (dict(q_start=None), "I"),
+    (dict(kv_len=F + 4), "I"), (dict(codes=None), "I"), (dict(table=None), "I"), (dict(out=None), "I"), (dict(lse=F + 4), "I"),
+    (dict(window=-1), "I"), (dict(sm_scale=0.0), "I"), (dict(sm_scale=float("nan")), "I"), (dict(sm_scale=float("inf")), "I"),
+    (dict(n_tokens=-1), "I"), (dict(n_req=-1), "I"), (dict(max_q=-1), "I"), (dict(max_kv=-1), "I"), (dict(n_rows=-1), "I"),
+    (dict(max_pages=1 << 31), "I"), (dict(n_tokens=(1 << 24) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W")])
+def test_paged_attn_refusals(abi, kw, status):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_paged_attn(*args(ATTN, **kw)) == {"U": 2, "I": 1, "W": 6}[status]
+    assert abi.csa2_launch_count() == c0
+
+
+def test_paged_attn_workspace(abi):
+    ws = abi.csa2_paged_attn_workspace_bytes
+    assert ws(0, 64, 0, 0, 0, 0) >= abi.STATUS_BYTES
+    for bad in ((-1, 64, 1, 1, 1, 0), (1, 0, 1, 1, 1, 0), (1, 129, 1, 1, 1, 0), (1, 64, -1, 1, 1, 0), (1, 64, 1, -1, 1, 0),
+                (1, 64, 1, 1, -1, 0), (1, 64, 1, 1, 1, -1)):
+        assert ws(*bad) == 0, bad
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dim=0), "I"), (dict(dim=12), "U"), (dict(dim=16392, x_stride=16392), "U"), (dict(group=64), "U"),
+    (dict(group=128, dim=520, x_stride=520), "U"), (dict(x_stride=504), "I"), (dict(x_stride=516), "I"), (dict(residual=None), "I"),
+    (dict(residual_out=None), "I"), (dict(x=None), "I"), (dict(weight=None), "I"), (dict(codes=None), "I"), (dict(scales=None), "I"),
+    (dict(y=F + 2), "I"), (dict(codes=F + 8), "I"), (dict(eps=-1.0), "I"), (dict(eps=float("nan")), "I"), (dict(n=-1), "I")])
+def test_rmsnorm_refusals(abi, kw, status):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_rmsnorm_fp8(*args(NORM, **kw)) == {"U": 2, "I": 1}[status]
+    assert abi.csa2_launch_count() == c0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(fmt=2), "U"), (dict(k=64, x_stride=64), "U"), (dict(k=200, x_stride=208), "U"), (dict(k=65664, x_stride=65664), "U"),
+    (dict(n_out=0), "U"), (dict(n_out=-1), "I"), (dict(n=-1), "I"), (dict(x_stride=240), "I"), (dict(x_stride=264), "I"),
+    (dict(x_scales=F), "I"), (dict(fmt=1), "I"), (dict(x=None), "I"), (dict(codes=F + 4), "I"), (dict(scales=None), "I"),
+    (dict(out=None), "I"), (dict(out_dtype=3), "I"), (dict(alpha=float("inf")), "I"), (dict(alpha=float("nan")), "I"),
+    (dict(ws=None), "W"), (dict(ws_bytes=0), "W")])
+def test_matvec_refusals(abi, kw, status):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_fp4_matvec(*args(MATVEC, **kw)) == {"U": 2, "I": 1, "W": 6}[status]
+    assert abi.csa2_launch_count() == c0
+
+
+def test_empty_calls_launch_nothing(abi):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_paged_attn(*args(ATTN, n_tokens=0)) == abi.OK
+    assert abi.lib.csa2_paged_attn(*args(ATTN, n_req=0)) == abi.OK
+    assert abi.lib.csa2_rmsnorm_fp8(*args(NORM, n=0)) == abi.OK
+    assert abi.lib.csa2_fp4_matvec(*args(MATVEC, n=0)) == abi.OK
+    assert abi.csa2_launch_count() == c0
+
+
+# ------------------------------------------------- the 64-bit forms by hand
+def test_plan_form_by_hand():
+    table = np.array([[4, -1, -1], [2, 6, -1]], np.int32)
+    free = np.array([0, 1, 3, 5, 7, 0, 0, 0], np.int32)
+    t, qs, kl, slots, pos, left, ok = PO.page_plan([7, 16], [3, 1], 8, table, free, 5, 8, 6)
+    assert ok and t.tolist() == [[4, 7, -1], [2, 6, 5]] and left == 3
+    assert qs.tolist() == [0, 3, 4] and kl.tolist() == [10, 17]
+    assert slots.tolist() == [39, 56, 57, 40, -1, -1] and pos.tolist() == [7, 8, 9, 16, -1, -1]
+
+
+@pytest.mark.parametrize("window", [0, 3])
+def test_attention_form_is_torch_attention(window):
+    rng = np.random.default_rng(0)
+    codes = rng.integers(0, 120, (40, 512)).astype(np.uint8)
+    table = np.array([[3, 0, 4]], np.int32)
+    q = rng.standard_normal((4, 2, 512)).astype(np.float32)
+    out, lse, _ = PO.paged_attention(q, [0, 4], [20], codes, None, table, 8, window, 0.04)
+    rows = np.r_[24:32, 0:8, 32:36]
+    c = torch.from_numpy(codes[rows]).view(torch.float8_e4m3fn).double()
+    t = torch.arange(16, 20)[:, None]
+    p = torch.arange(20)[None]
+    keep = (p <= t) & ((p > t - window) if window else True)
+    want = torch.nn.functional.scaled_dot_product_attention(torch.from_numpy(q).double().permute(1, 0, 2)[None], c[None, None],
+                                                            c[None, None], attn_mask=keep, scale=0.04)
+    np.testing.assert_allclose(out, want[0].permute(1, 0, 2).numpy(), rtol=1e-12, atol=1e-12)
+
+
+def test_norm_and_product_forms_by_hand():
+    assert np.allclose(PO.rmsnorm(np.array([[3.0, 4.0]]), np.array([1.0, 2.0]), 0.0), [[3 / np.sqrt(12.5), 8 / np.sqrt(12.5)]])
+    codes = np.full((1, 8), 0x21, np.uint8)  # 0.5, 1.0 in turn
+    got, reach = PO.matvec(np.arange(16.0)[None], np.array([2.0], np.float32), codes, np.array([[0x40]], np.uint8), 0.5)
+    assert got[0, 0] == 0.5 * 2 * 2 * (0.5 * 56 + 64) and reach[0, 0] == got[0, 0]
