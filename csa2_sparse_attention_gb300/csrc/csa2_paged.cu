@@ -3,109 +3,758 @@
 //   l_p = sm_scale q . c_p,  o = sum_p softmax(l)_p c_p,  c_p a 512-wide
 //   latent in FP4 (E2M1, one E4M3 scale per 16 channels) or E4M3
 //
-// One warp per (token, head): each lane holds 16 channels, the logits are warp
-// sums, and one pass over the keys keeps a running maximum and sum.
+// Rows are (token, head) pairs: 128 consecutive rows of a request make a tile
+// of the tensor cores' M, whatever the number of heads.  All heads share the
+// latents, so a key costs 2048 FLOPs a row against 288 bytes: the tensor cores
+// bound the kernel even for single tokens.
+//
+// The fp32 accumulator of 128 rows x 512 channels would fill TMEM (512
+// columns) and leave no room for the logits, so a CTA takes 128 rows and one
+// half of the output channels ("own", Y) and computes the logits over both
+// halves: 3 products of 256 channels where 2 would do.  (Sharing the logits
+// between two CTAs would move 64 KB of fp32 partial logits per 128 keys over
+// distributed shared memory at 16-24 B/clk per SM: 2700 clocks or more, against
+// the 1060 clocks of tensor time that the third product costs.)
+//
+//   TMEM  [0, 256) O   [256, 384) S   [384, 512) own half of Q, f16
+//   smem  other half of Q (64 KB), two 64 KB groups of latents, P (32 KB)
+//
+// Keys go in tiles of 128: an M = 128 MMA of K = 16 takes 64 clocks for any
+// N up to 128 (measured 64-69) and 128 for N = 256, so S wants 128 keys and O
+// 256 channels at once.  Three roles:
+//   producers (8 warps)  read the rows through the page table and decode them
+//       to f16 (exact) into shared memory, the other half's channels X first,
+//       then, as the logits' MMAs release them, the own half's Y in the same
+//       group.  One copy of Y serves S (K-major) and O (MN-major).
+//   MMA warp, per tile:  S += Q_X X^T, then O += P Y of the previous tile,
+//       then S += Q_Y Y^T: the softmax of a tile runs under the next tile's
+//       S_X, and the decoding of Y under the previous tile's O.
+//   softmax (8 warps, two threads per row)  takes S out of TMEM, keeps the
+//       running maximum and sum in fp32, writes P as f16 to shared memory.  O
+//       is rescaled only when a row's maximum grew by more than 2^8: P stays
+//       below 2^8 and the sums in fp32, so nothing is lost by waiting.
+// P is rounded to f16 (2^-11 relative, an eighth of the step of the bf16
+// output); Q goes to f16 times a power of two per row (exact down to 2^-28 of
+// the row's maximum).
+//
+// Long axes with few rows are split over CTAs in chunks of key tiles that the
+// host sizes; the partial outputs are joined by paged_merge_kernel.
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
+#include "csa2_layout.cuh"
+#include "csa2_tc.cuh"
 
+#include <atomic>
 #include <cfloat>
 
 namespace csa2 {
 
 constexpr int kPD = CSA2_LATENT_DIM;
+constexpr int kPHalf = kPD / 2;       // channels of one half
+constexpr int kPM = 128;              // rows of a tile
+constexpr int kPN = 128;              // keys of a tile
+constexpr int kPSoftWarps = 8, kPProdWarps = 8;
+constexpr int kPThreads = 32 * (kPSoftWarps + kPProdWarps + 4);  // and a warpgroup for the MMA thread
+// Registers per thread: the launch gives 96 x 640; the warpgroups pass them
+// on as 2 x 128 + 2 x 88 + 40 = 472 <= 5 x 96.
+constexpr int kPLaunchRegs = 96, kPSoftRegs = 128, kPProdRegs = 88, kPMmaRegs = 40;
+static_assert(2 * kPSoftRegs + 2 * kPProdRegs + kPMmaRegs <= 5 * kPLaunchRegs, "registers");
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
+constexpr int kPSms = 152;            // multiprocessors the split is planned for
 
+struct PagedArgs {
+    const uint8_t* q;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const int32_t* table;
+    uint8_t* out;
+    float* lse;
+    float* part_o;    // [splits][rows][512], each split's normalized output
+    float* part_lse;  // [splits][rows], log2 domain
+    Status* st;
+    uint64_t wlim;
+    int64_t n_rows_pages;  // pages of the cache
+    int64_t max_pages;
+    int64_t rows;          // n_tokens * heads
+    int64_t n_req;
+    int32_t n_tokens, heads, max_q, max_kv, page, window;
+    int32_t chunk;         // key tiles per split
+    float sm_scale;
+};
+
+// A request's tokens and entries; false when it is to be skipped.  Problems
+// go to `st` when it is not null.
+struct PagedReq {
+    int32_t q0, nq, len;
+};
+__device__ __forceinline__ bool paged_request(const PagedArgs& a, int64_t r, PagedReq& o, Status* st) {
+    o.q0 = a.q_start[r];
+    const int32_t q1 = a.q_start[r + 1];
+    o.len = a.kv_len[r];
+    if (o.q0 < 0 || q1 < o.q0 || q1 > a.n_tokens || q1 - o.q0 > a.max_q) {
+        if (st) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), q1);
+        return false;
+    }
+    o.nq = q1 - o.q0;
+    if (o.len < 0 || o.len > a.max_kv || o.len > a.max_pages * a.page) {
+        if (st) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), o.len);
+        o.len = 0;
+    }
+    return o.nq > 0;
+}
+__host__ __device__ inline int32_t paged_row_tiles(int32_t nq, int32_t heads) { return (nq * heads + kPM - 1) / kPM; }
+// Key tiles that a row tile of a request can span at most, and its splits.
+__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t heads, int32_t window) {
+    int32_t n = (len + kPN - 1) / kPN;
+    if (window > 0) {
+        const int32_t tok = (kPM - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
+        const int32_t w = (span + kPN - 1) / kPN;
+        n = n < w ? n : w;
+    }
+    return n;
+}
+__host__ __device__ inline int32_t paged_splits(int32_t tiles, int32_t chunk) {
+    return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+}
+// First key (a multiple of 8), end and key tiles of row tile ti.
+__device__ __forceinline__ void paged_tile_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
+                                                int32_t& end, int32_t& tiles) {
+    const int32_t rows = rq.nq * a.heads, r0 = ti * kPM, r1 = (r0 + kPM < rows ? r0 + kPM : rows) - 1;
+    end = rq.len - rq.nq + r1 / a.heads + 1;
+    int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.heads + 1 - a.window : 0;
+    if (lo < 0) lo = 0;
+    begin = lo & ~7;
+    tiles = end > begin ? (end - begin + kPN - 1) / kPN : 0;
+}
+
+struct PagedSmem {
+    uint8_t qx[kPM * kPHalf * 2];      // other half of Q, K-major: 8-row groups of 4096 B, 8-channel chunks of 128 B
+    uint8_t c[2][kPN * kPHalf * 2];    // latents: 8-key groups of 4096 B, 8-channel chunks of 128 B
+    uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
+    float red[2][kPM];                 // exchange between the two threads of a row
+    uint32_t hidden[2][4];             // keys of a tile without a page, a bit each
+    uint32_t nan[2][2][4];             // keys with a NaN latent (per half of the producers)
+    uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2];
+    uint64_t s_full, s_free, p_full, o_done, drain;
+    uint32_t tmem;
+    int32_t req, local;
+};
+static_assert(sizeof(PagedSmem) + 1024 <= 227 * 1024, "shared memory of the paged attention");
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
+}
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The two warps of a row quarter: a barrier, and one that gives the AND of
+// their threads' flags (so that both leave after a wait that gave up in one).
+__device__ __forceinline__ void pair_sync(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
+__device__ __forceinline__ bool pair_and(int quad, bool v) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"(1 + quad), "r"(uint32_t(v)) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* o) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t* o) {
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+        : "=r"(o[0]), "=r"(o[1]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// nonzero when one of the four E4M3 bytes is NaN (0x7F or 0xFF)
+__device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// grid: 2 CTAs (output halves) per (row tile, split), row tiles with the most
+// keys first; CTAs beyond the last one leave at once.
 template <bool FP8>
-__global__ void __launch_bounds__(256) paged_attn_kernel(
-    const uint8_t* __restrict__ q, int64_t n_tokens, int heads, const int32_t* __restrict__ q_start,
-    const int32_t* __restrict__ kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, const uint8_t* __restrict__ codes,
-    const uint8_t* __restrict__ scales, int64_t n_rows, const int32_t* __restrict__ table, int64_t max_pages, int page,
-    int window, float sm_scale, uint8_t* __restrict__ out, float* __restrict__ out_lse, Status* st) {
+__global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    PagedSmem& S = *reinterpret_cast<PagedSmem*>(smem_raw);
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int half = blockIdx.x & 1;
     grid_dep_wait();
     grid_dep_launch();
-    const int lane = lane_id();
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t tok = row / heads;
-    if (tok >= n_tokens) return;
-    int64_t lo = 0, hi = n_req;  // the request: the last one that starts at or before the token
-    while (hi - lo > 1) {
-        const int64_t m = (lo + hi) / 2;
-        if (q_start[m] <= tok) lo = m;
-        else hi = m;
-    }
-    const int64_t r = lo;
-    if (n_req == 0 || tok < q_start[r] || tok >= q_start[r + 1]) return;
-    const int32_t nq = q_start[r + 1] - q_start[r];
-    if (q_start[r] < 0 || q_start[r + 1] > n_tokens || nq > max_q) {
-        if (lane == 0) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), nq);
-        return;
-    }
-    int32_t len = kv_len[r];
-    if (len < 0 || len > max_kv || len > max_pages * page) {
-        if (lane == 0) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), len);
-        len = 0;
-    }
-    const int64_t t = int64_t(len) - nq + (tok - q_start[r]);
-    float qv[16], o[16] = {};
-    {
-        const uint4* src = reinterpret_cast<const uint4*>(q + (row * kPD + 16 * lane) * 2);
-        const uint4 a = src[0], b = src[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+
+    // ---- the CTA's request: a warp scan of the requests' work items
+    if (warp == 0) {
+        const int64_t item = blockIdx.x >> 1;
+        int64_t base = 0;
+        int32_t req = -1, local = 0;
+        for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
+            const int64_t r = r0 + lane;
+            int64_t items = 0;
+            PagedReq rq;
+            if (r < a.n_req && paged_request(a, r, rq, blockIdx.x == 0 ? a.st : nullptr))
+                items = int64_t(paged_row_tiles(rq.nq, a.heads)) *
+                        paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window), a.chunk);
+            int64_t inc = items;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qv[2 * e] = bf16_lo(w[e]), qv[2 * e + 1] = bf16_hi(w[e]);
-    }
-    float m = -INFINITY, l = 0.f;
-    const int64_t first = window && t + 1 > window ? t + 1 - window : 0;
-    for (int64_t p = first; len > 0 && p <= t; ++p) {
-        const int32_t id = table[r * max_pages + p / page];
-        const int64_t at = int64_t(id) * page + p % page;
-        if (id < 0 || at >= n_rows / page * page) {
-            if (lane == 0) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(r), id);
-            continue;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > item);
+            if (hit != 0 && req < 0) {
+                const int src = __ffs(hit) - 1;
+                req = int32_t(r0) + src;
+                local = int32_t(item - base - __shfl_sync(0xffffffffu, inc - items, src));
+                if (blockIdx.x != 0) break;  // the first CTA looks at every request
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        float c[16];
-        if (FP8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(codes + at * kPD + 16 * lane);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (lane == 0) S.req = req, S.local = local;
+    }
+    __syncthreads();
+    if (S.req < 0) return;
+    const int64_t req = S.req;
+    PagedReq rq;
+    paged_request(a, req, rq, nullptr);
+    const int32_t tiles_r = paged_row_tiles(rq.nq, a.heads);
+    const int32_t ns_r = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window), a.chunk);
+    const int32_t ti = tiles_r - 1 - S.local / ns_r, split = S.local % ns_r;
+    int32_t k_begin, k_end, k_tiles;
+    paged_tile_keys(a, rq, ti, k_begin, k_end, k_tiles);
+    const int32_t splits = paged_splits(k_tiles, a.chunk);
+    if (split >= splits) return;
+    const int32_t j0 = split * a.chunk;
+    const int32_t nt = k_tiles - j0 < a.chunk ? k_tiles - j0 : a.chunk;  // this CTA's key tiles (0: nothing to see)
+    const int32_t key0 = k_begin + j0 * kPN;
+    const int64_t flat0 = int64_t(rq.q0) * a.heads + int64_t(ti) * kPM;
+    const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
+    const int x_dim = kPHalf * (1 - half), y_dim = kPHalf * half;
+
+    if (tid == 0) {
+        for (int g = 0; g < 2; ++g) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&S.full_x[g][b], kPProdWarps);
+                mbar_init(&S.full_y[g][b], kPProdWarps);
+                mbar_init(&S.empty_x[g][b], 1);
+            }
+            mbar_init(&S.empty_o[g], 1);
+        }
+        mbar_init(&S.s_full, 1);
+        mbar_init(&S.s_free, kPSoftWarps);
+        mbar_init(&S.p_full, kPSoftWarps);
+        mbar_init(&S.o_done, 1);
+        mbar_init(&S.drain, 1);
+        mbar_init_fence();
+    }
+    if (warp == kPSoftWarps + kPProdWarps) tmem_alloc(&S.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+
+    if (warp < kPSoftWarps) {
+        regs_up<kPSoftRegs>();
+        // ================= softmax: row 32 (warp % 4) + lane, column half warp / 4
+        const int quad = warp & 3, ch = warp >> 2, row = 32 * quad + lane;
+        const uint32_t lanes = uint32_t(32 * quad) << 16;
+        const bool row_on = row < n_row;
+        const uint8_t* qrow = a.q + ((flat0 + (row_on ? row : 0)) * kPD) * 2;
+        // ---- Q: this thread's 128 channels of each half; the row's power of two from the maximum over all
+        {
+            const uint4* qx = reinterpret_cast<const uint4*>(qrow + (x_dim + 128 * ch) * 2);
+            const uint4* qy = reinterpret_cast<const uint4*>(qrow + (y_dim + 128 * ch) * 2);
+            uint4 v[16];
+            uint32_t am = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) c[e] = e4m3_value((w[e / 4] >> (8 * (e & 3))) & 255u);
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(codes + at * (kPD / 2) + 8 * lane);
-            const float s = e4m3_value(scales[at * (kPD / 16) + lane]);
+            for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t cc = ((e < 8 ? v.x : v.y) >> (4 * (e & 7))) & 15u, mm = cc & 7u;
-                const float f = mm < 2 ? 0.5f * float(mm) : __uint_as_float(((mm >> 1) + 126u) << 23 | (mm & 1u) << 22);
-                c[e] = (cc & 8u ? -f : f) * s;
+                for (int i = 0; i < 16; ++i) v[i] = row_on ? __ldg((s ? qy : qx) + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+                    am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                }
+            }
+            S.red[ch][row] = __uint_as_float(max(am & 0xFFFFu, am >> 16));
+        }
+        pair_sync(quad);
+        float sm_eff;
+        {
+            const uint32_t am = max(__float_as_uint(S.red[0][row]), __float_as_uint(S.red[1][row]));
+            int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;  // max |q| 2^-qs in [2^14, 2^15)
+            qs = qs < -100 ? -100 : qs;
+            const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
+            sm_eff = fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), FLT_MIN);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint4* src = reinterpret_cast<const uint4*>(qrow + ((s ? y_dim : x_dim) + 128 * ch) * 2);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {  // 64 channels at a time
+                    uint4 v[8];
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = row_on ? __ldg(src + 8 * b + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[4 * i + e] = f16x2(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
+                    }
+                    if (s == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(S.qx + (row >> 3) * 4096 + (16 * ch + 8 * b + i) * 128 + (row & 7) * 16) =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
+                        tmem_st32(tmem + lanes + kColQ + 64 * ch + 32 * b, o);
+                    }
+                }
+            }
+            tmem_st_wait();
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.s_free);  // phase 0: Q is in place
+
+        // ---- key tiles
+        int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys
+        if (row_on) {
+            hi_r = rq.len - rq.nq + (ti * kPM + row) / a.heads + 1;
+            lo_r = a.window > 0 ? hi_r - a.window : 0;
+        }
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int32_t j = 0; j < nt; ++j) {
+            ok = pair_and(quad, mbar_wait(&S.s_full, j & 1, a.wlim));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s0[32], s1[32];
+            tmem_ld32(tmem + lanes + kColS + 64 * ch, s0);
+            tmem_ld32(tmem + lanes + kColS + 64 * ch + 32, s1);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.s_free);  // phase j + 1: S may be overwritten
+            const int32_t c0 = key0 + j * kPN + 64 * ch;
+            const int g = j & 1;
+            const uint32_t hid0 = S.hidden[g][2 * ch], hid1 = S.hidden[g][2 * ch + 1];
+            const uint32_t nan0 = S.nan[g][0][2 * ch] | S.nan[g][1][2 * ch];
+            const uint32_t nan1 = S.nan[g][0][2 * ch + 1] | S.nan[g][1][2 * ch + 1];
+            if (__any_sync(0xffffffffu, c0 < lo_r || c0 + 64 > hi_r) || (hid0 | hid1 | nan0 | nan1) != 0) {
+                const int32_t lo = lo_r - c0, hi = hi_r - c0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if ((nan0 >> i) & 1u) s0[i] = 0x7FC00000u;
+                    if ((nan1 >> i) & 1u) s1[i] = 0x7FC00000u;
+                    if (i < lo || i >= hi || ((hid0 >> i) & 1u)) s0[i] = 0xFF800000u;
+                    if (i + 32 < lo || i + 32 >= hi || ((hid1 >> i) & 1u)) s1[i] = 0xFF800000u;
+                }
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+            S.red[ch][row] = mx;
+            pair_sync(quad);
+            mx = fmaxf(mx, S.red[ch ^ 1][row]) * sm_eff;
+            const bool grew = mx > m + 8.f;
+            if (__any_sync(0xffffffffu, grew)) {
+                const float mn = grew ? mx : m;
+                const float alpha = !grew ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
+                if (j > 0) {  // every MMA before S_Y of this tile is done, the previous O among them
+#pragma unroll 1
+                    for (int b = 0; b < 8; ++b) {
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lanes + kColO + 128 * ch + 16 * b, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st16(tmem + lanes + kColO + 128 * ch + 16 * b, o);
+                    }
+                    tmem_st_wait();
+                }
+                l *= alpha;
+                m = mn;
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            float acc[4] = {};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float e0 = ex2(fmaf(__uint_as_float(s0[i]), sm_eff, -mu));
+                const float e1 = ex2(fmaf(__uint_as_float(s1[i]), sm_eff, -mu));
+                acc[i & 1] += e0;
+                acc[2 + (i & 1)] += e1;
+                s0[i] = __float_as_uint(e0);
+                s1[i] = __float_as_uint(e1);
+            }
+            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            uint8_t* pd = S.p + (row >> 3) * 2048 + (8 * ch) * 128 + (row & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t* s = i < 4 ? s0 + 8 * i : s1 + 8 * (i - 4);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = f16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                *reinterpret_cast<uint4*>(pd + i * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full);
+        }
+        if (ok && nt > 0) ok = pair_and(quad, mbar_wait(&S.o_done, 0, a.wlim));
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), ti);
+        // ---- epilogue: O / l, this thread's 128 of the own half's channels
+        if (ok) {
+            tc_fence_after();
+            S.red[ch][row] = l;
+            pair_sync(quad);
+            l = S.red[0][row] + S.red[1][row];
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+            const int64_t flat = flat0 + row;
+            const int dim = y_dim + 128 * ch;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld32(tmem + lanes + kColO + 128 * ch + 32 * b, o);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (!row_on) continue;
+                if (splits == 1) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + (flat * kPD + dim + 32 * b) * 2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                                           __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + (int64_t(split) * a.rows + flat) * kPD + dim + 32 * b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                }
+            }
+            if (row_on && half == 0 && ch == 0) {
+                if (splits > 1)
+                    a.part_lse[int64_t(split) * a.rows + flat] = lse2;
+                else if (a.lse)
+                    a.lse[flat] = lse2 * 0.6931471805599453f;
             }
         }
-        float x = 0.f;
+    } else if (warp < kPSoftWarps + kPProdWarps) {
+        regs_down<kPProdRegs>();
+        // ================= producers: key 32 (warp % 4) + lane, 64-channel blocks hb of each 128
+        const int pw = warp - kPSoftWarps, hb = pw >> 2, kk = 32 * (pw & 3) + lane;
+        constexpr int NV = FP8 ? 4 : 2;  // 16-byte pieces of 64 channels
+        uint4 v[4][NV];                  // the four blocks of a tile: X, X, Y, Y
+        uint32_t sc[4];
+        const int32_t* trow = a.table + req * a.max_pages;
+        auto page_at = [&](int32_t j) {  // the page id of this thread's key in tile j, or -1
+            const int32_t p = key0 + j * kPN + kk;
+            return j < nt && p < k_end ? trow[p / a.page] : -1;
+        };
+        auto dims = [&](int b) { return (b < 2 ? x_dim : y_dim) + 128 * (b & 1) + 64 * hb; };
+        int64_t at = -1;  // the cache row of the tile being loaded, or -1
+        auto locate = [&](int32_t j, int32_t id) {
+            const int32_t p = key0 + j * kPN + kk;
+            at = -1;
+            if (j < nt && p < k_end) {
+                if (id >= 0 && id < a.n_rows_pages)
+                    at = int64_t(id) * a.page + p % a.page;
+                else if (hb == 0 && half == 0)
+                    record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+            }
+        };
+        auto load = [&](int b) {
+            if (at >= 0) {
+                const uint4* src = reinterpret_cast<const uint4*>(a.codes + (FP8 ? at * kPD + dims(b) : (at * kPD + dims(b)) / 2));
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x = fmaf(qv[e], c[e], x);
+                for (int i = 0; i < NV; ++i) v[b][i] = __ldg(src + i);
+                if (!FP8) sc[b] = __ldg(reinterpret_cast<const uint32_t*>(a.scales + at * (kPD / 16) + dims(b) / 16));
+            } else {
 #pragma unroll
-        for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-        x *= sm_scale;
-        const float mn = fmaxf(m, x);
-        const float f = m == -INFINITY ? 0.f : expf(m - mn), e1 = expf(x - mn);
-        m = mn;
-        l = l * f + e1;
+                for (int i = 0; i < NV; ++i) v[b][i] = make_uint4(0, 0, 0, 0);
+                sc[b] = 0;
+            }
+        };
+        int32_t id_next = page_at(0);
+        locate(0, id_next);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = fmaf(e1, c[e], o[e] * f);
+        for (int b = 0; b < 4; ++b) load(b);
+        id_next = page_at(1);
+        bool ok = true;
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            const int g = j & 1;
+            const uint32_t ph = (j >> 1) & 1;
+            const uint32_t gone = __ballot_sync(0xffffffffu, at < 0);
+            uint32_t bad = 0;
+            locate(j + 1, id_next);  // from here on `at` is the next tile's row
+            id_next = page_at(j + 2);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                // the block's place: X after the O MMAs of the tile before last, Y after this tile's S_X MMAs
+                if (b == 0 && j >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
+                if (b >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_x[g][b & 1], ph, a.wlim));
+                if (!ok) break;
+                uint8_t* dst = S.c[g] + (kk >> 3) * 4096 + (16 * (b & 1) + 8 * hb) * 128 + (kk & 7) * 16;
+                if (FP8) {
+                    uint32_t n4 = 0;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        n4 |= e4m3_nan4(v[b][i].x) | e4m3_nan4(v[b][i].y) | e4m3_nan4(v[b][i].z) | e4m3_nan4(v[b][i].w);
+                    bad |= n4;
+                    const uint32_t keep = n4 ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const uint32_t w[4] = {v[b][i].x & keep, v[b][i].y & keep, v[b][i].z & keep, v[b][i].w & keep};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) e4m3x4_f16(w[e], o + 2 * e);
+                        *reinterpret_cast<uint4*>(dst + (2 * i) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(dst + (2 * i + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                } else {
+                    const uint32_t n4 = e4m3_nan4(sc[b]);
+                    bad |= n4;
+                    uint32_t s2[2];
+                    e4m3x4_f16(n4 ? 0u : sc[b], s2);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const uint32_t w[4] = {v[b][i].x, v[b][i].y, v[b][i].z, v[b][i].w};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {  // one group of 16 channels
+                            const uint32_t s = __byte_perm(s2[i], 0, e ? 0x3232 : 0x1010);
+                            uint32_t o[8];
+                            e2m1x8_f16(w[2 * e], o);
+                            e2m1x8_f16(w[2 * e + 1], o + 4);
+#pragma unroll
+                            for (int t = 0; t < 8; ++t) o[t] = mul_f16x2(o[t], s);
+                            *reinterpret_cast<uint4*>(dst + (4 * i + 2 * e) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(dst + (4 * i + 2 * e + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                }
+                if (j + 1 < nt) load(b);
+                if (b == 3) {
+                    const uint32_t word = __ballot_sync(0xffffffffu, bad != 0);
+                    if (lane == 0) {
+                        S.nan[g][hb][pw & 3] = word;
+                        if (hb == 0) S.hidden[g][pw & 3] = gone;
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b < 2 ? &S.full_x[g][b] : &S.full_y[g][b - 2]);
+            }
+        }
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), ti);
+    } else {
+        regs_down<kPMmaRegs>();
+        if (tid == 32 * (kPSoftWarps + kPProdWarps)) {
+        // ================= MMA issue
+        constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, kPHalf, 0, false, true);
+        const uint32_t sq = smem_u32(S.qx), sp = smem_u32(S.p);
+        bool ok = true;
+        auto o_mma = [&](int32_t j) {  // O += P Y of tile j
+            ok = ok && mbar_wait(&S.p_full, j & 1, a.wlim);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t sc = smem_u32(S.c[j & 1]);
+            for (int k = 0; k < kPN / 16; ++k)
+                mma_f16_ss(tmem + kColO, umma_desc(sp + k * 256, 128, 2048), umma_desc(sc + k * 8192, 4096, 128), id_o,
+                           j > 0 || k > 0);
+        };
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            const int g = j & 1;
+            const uint32_t ph = (j >> 1) & 1, sc = smem_u32(S.c[g]);
+            ok = mbar_wait(&S.s_free, j & 1, a.wlim);  // phase 0: Q; phase j: S of the tile before has been read
+            tc_fence_after();
+            for (int b = 0; b < 2 && ok; ++b) {
+                ok = mbar_wait(&S.full_x[g][b], ph, a.wlim);
+                if (!ok) break;
+                for (int k = 8 * b; k < 8 * b + 8; ++k)
+                    mma_f16_ss(tmem + kColS, umma_desc(sq + k * 256, 128, 4096), umma_desc(sc + k * 256, 128, 4096), id_s, k > 0);
+                tc_commit(&S.empty_x[g][b]);
+            }
+            if (ok && j > 0) {
+                o_mma(j - 1);
+                if (ok) tc_commit(&S.empty_o[g ^ 1]);
+            }
+            for (int b = 0; b < 2 && ok; ++b) {
+                ok = mbar_wait(&S.full_y[g][b], ph, a.wlim);
+                if (!ok) break;
+                for (int k = 8 * b; k < 8 * b + 8; ++k)
+                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * k, umma_desc(sc + k * 256, 128, 4096), id_s, true);
+            }
+            if (ok) tc_commit(&S.s_full);
+        }
+        if (nt > 0) {
+            if (ok) o_mma(nt - 1);
+            if (ok) tc_commit(&S.o_done);
+            if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), ti);
+            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done
+            tc_commit(&S.drain);
+            mbar_wait(&S.drain, 0, kDrainNs);
+        }
+        }
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kPSoftWarps + kPProdWarps) tmem_dealloc(tmem, 512);
+}
+
+// Joins the splits of a row: weights 2^(lse_s - max lse) over the normalized
+// partial outputs.  128 threads per row, 4 channels each; rows whose tile had
+// one split were written by the attention kernel.
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = int64_t(blockIdx.x) * 2 + (threadIdx.x >> 7);
+    const int t = threadIdx.x & 127;
+    if (row >= a.rows) return;
+    const int32_t tok = int32_t(row / a.heads);
+    int64_t lo = 0, hi = a.n_req;  // the last request that starts at or before the token
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (a.q_start[mid] <= tok) lo = mid;
+        else hi = mid;
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + (row * kPD + 16 * lane) * 2);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (out_lse && lane == 0) out_lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    PagedReq rq;
+    if (!paged_request(a, lo, rq, nullptr) || tok < rq.q0 || tok >= rq.q0 + rq.nq) return;
+    int32_t begin, end, tiles;
+    paged_tile_keys(a, rq, int32_t((row - int64_t(rq.q0) * a.heads) / kPM), begin, end, tiles);
+    const int32_t splits = paged_splits(tiles, a.chunk);
+    if (splits == 1) return;
+    float m = -INFINITY;
+    for (int32_t s = 0; s < splits; ++s) m = fmaxf(m, a.part_lse[s * a.rows + row]);
+    float w = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int32_t s = 0; s < splits; ++s) {
+        const float ls = a.part_lse[s * a.rows + row];
+        const float f = ls == -INFINITY ? 0.f : ex2(ls - m);
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + (s * a.rows + row) * kPD)[t];
+        w += f;
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+    }
+    const float inv = w == 0.f ? 0.f : 1.0f / w;
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    reinterpret_cast<uint2*>(a.out + row * kPD * 2)[t] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    if (a.lse && t == 0) a.lse[row] = w == 0.f ? -INFINITY : (m + log2f(w)) * 0.6931471805599453f;
+}
+
+// How a call is split: key tiles per CTA, from the host's bounds alone.  A
+// CTA takes one (row tile, half, split); the split count is the one with the
+// least time by: waves of 152 CTAs, each a start of 5 us and 1.9 us per key
+// tile, plus the merge's pass over the partial outputs.
+struct PagedPlan {
+    int32_t chunk, splits;
+    int64_t grid;
+    size_t part_lse, part_o, total;
+};
+static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
+    PagedPlan p{};
+    if (window >= max_kv) window = 0;
+    const int64_t rows = n_tokens * n_heads;
+    int64_t tiles = rows / kPM + n_req;  // each request rounds up
+    const int64_t each = n_req * paged_row_tiles(max_q, n_heads);
+    tiles = tiles < each ? tiles : each;
+    const int32_t nt = paged_key_tiles(max_q, max_kv, n_heads, window);
+    p.chunk = nt > 0 ? nt : 1;
+    double best = 1e30;
+    for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
+        const int32_t chunk = (nt + s - 1) / s;
+        if (s > 1 && paged_splits(nt, chunk) != s) continue;
+        const double waves = double((2 * tiles * s + kPSms - 1) / kPSms);
+        double us = waves * (5.0 + 1.9 * chunk);
+        if (s > 1) us += 4.0 + double(rows) * s * kPD * 4 * 2 / 4e6;
+        if (us < best) {
+            best = us;
+            p.chunk = chunk > 0 ? chunk : 1;
+        }
+    }
+    p.splits = paged_splits(nt, p.chunk);
+    p.grid = 2 * tiles * p.splits;
+    p.part_lse = CSA2_STATUS_BYTES;
+    p.part_o = p.total = CSA2_STATUS_BYTES;
+    if (p.splits > 1) {
+        p.part_o = align256(p.part_lse + size_t(p.splits) * size_t(rows) * 4);
+        p.total = align256(p.part_o + size_t(p.splits) * size_t(rows) * kPD * 4);
+    }
+    return p;
+}
+
+// Once per device and format: the shared memory opt-in, and the register
+// count that the kernel's split of them is made for.
+static csa2_status prepare_paged(bool fp8) {
+    static std::atomic<bool> done[2][64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
+    if (done[fp8][dev].load(std::memory_order_acquire)) return CSA2_OK;
+    auto kernel = fp8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess || at.numRegs != kPLaunchRegs ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(PagedSmem))) != cudaSuccess) {
+        cudaGetLastError();
+        return CSA2_ERR_CUDA;
+    }
+    done[fp8][dev].store(true, std::memory_order_release);
+    return CSA2_OK;
 }
 
 static bool paged_sizes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
-    return n_tokens >= 0 && n_tokens <= (int64_t(1) << 24) && n_heads >= 1 && n_heads <= 128 && n_req >= 0 &&
+    return n_tokens >= 0 && n_tokens <= (int64_t(1) << 22) && n_heads >= 1 && n_heads <= 128 && n_req >= 0 &&
            n_req <= (1 << 20) && max_q >= 0 && max_kv >= 0 && window >= 0;
 }
 
@@ -115,7 +764,9 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
                                                   int32_t max_kv, int window) {
-    return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window) ? CSA2_STATUS_BYTES : 0;
+    return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window) 
+               ? paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window).total
+               : 0;
 }
 
 extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
@@ -142,11 +793,47 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
         return CSA2_ERR_WORKSPACE;
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
     cudaStream_t s = cudaStream_t(stream);
+    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
+    if (plan.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    auto kernel = fmt == CSA2_FMT_FP8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+    const csa2_status prep = prepare_paged(fmt == CSA2_FMT_FP8);
+    if (prep != CSA2_OK) return prep;
+    PagedArgs a{};
+    a.q = static_cast<const uint8_t*>(q_bf16);
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.codes = codes;
+    a.scales = scales;
+    a.table = table;
+    a.out = static_cast<uint8_t*>(out);
+    a.lse = out_lse;
+    a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_lse);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_o);
+    a.st = static_cast<Status*>(ws);
+    a.wlim = wait_limit_ns();
+    a.n_rows_pages = n_rows / page_size;
+    a.max_pages = max_pages;
+    a.rows = n_tokens * n_heads;
+    a.n_req = n_req;
+    a.n_tokens = int32_t(n_tokens);
+    a.heads = n_heads;
+    a.max_q = max_q;
+    a.max_kv = max_kv;
+    a.page = page_size;
+    a.window = window >= max_kv ? 0 : window;
+    a.chunk = plan.chunk;
+    a.sm_scale = sm_scale;
     timer_begin(K_PAGED_ATTN, s);
-    launch(fmt == CSA2_FMT_FP8 ? paged_attn_kernel<true> : paged_attn_kernel<false>,
-           dim3(unsigned(ceil_div<int64_t>(n_tokens * n_heads, 8))), 256, 0, s, 1, static_cast<const uint8_t*>(q_bf16),
-           n_tokens, n_heads, q_start, kv_len, n_req, max_q, max_kv, codes, scales, n_rows, table, max_pages, page_size,
-           window, sm_scale, static_cast<uint8_t*>(out), out_lse, static_cast<Status*>(ws));
+    const cudaError_t e = launch(kernel, dim3(unsigned(plan.grid)), kPThreads, sizeof(PagedSmem), s, 1, a);
     timer_end(K_PAGED_ATTN, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return CSA2_ERR_CUDA;
+    }
+    if (plan.splits > 1) {
+        timer_begin(K_PAGED_MERGE, s);
+        launch(paged_merge_kernel, dim3(unsigned(ceil_div<int64_t>(a.rows, 2))), 256, 0, s, 1, a);
+        timer_end(K_PAGED_MERGE, s);
+    }
     return launch_status();
 }

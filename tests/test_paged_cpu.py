@@ -53,7 +53,7 @@ def test_page_plan_refusals(abi, kw, status):
     (dict(kv_len=F + 4), "I"), (dict(codes=None), "I"), (dict(table=None), "I"), (dict(out=None), "I"), (dict(lse=F + 4), "I"),
     (dict(window=-1), "I"), (dict(sm_scale=0.0), "I"), (dict(sm_scale=float("nan")), "I"), (dict(sm_scale=float("inf")), "I"),
     (dict(n_tokens=-1), "I"), (dict(n_req=-1), "I"), (dict(max_q=-1), "I"), (dict(max_kv=-1), "I"), (dict(n_rows=-1), "I"),
-    (dict(max_pages=1 << 31), "I"), (dict(n_tokens=(1 << 24) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W")])
+    (dict(max_pages=1 << 31), "I"), (dict(n_tokens=(1 << 22) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W")])
 def test_paged_attn_refusals(abi, kw, status):
     c0 = abi.csa2_launch_count()
     assert abi.lib.csa2_paged_attn(*args(ATTN, **kw)) == {"U": 2, "I": 1, "W": 6}[status]
