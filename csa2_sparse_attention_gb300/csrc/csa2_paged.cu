@@ -29,7 +29,7 @@
 //   MMA warp, per tile:  S += Q_X X^T, then O += P Y of the previous tile,
 //       then S += Q_Y Y^T: the softmax of a tile runs under the next tile's
 //       S_X, and the decoding of Y under the previous tile's O.
-//   softmax (8 warps, two threads per row)  takes S out of TMEM, keeps the
+//   softmax (4 warps, a thread per row)  takes S out of TMEM, keeps the
 //       running maximum and sum in fp32, writes P as f16 to shared memory.  O
 //       is rescaled only when a row's maximum grew by more than 2^8: P stays
 //       below 2^8 and the sums in fp32, so nothing is lost by waiting.
@@ -53,12 +53,15 @@ constexpr int kPD = CSA2_LATENT_DIM;
 constexpr int kPHalf = kPD / 2;       // channels of one half
 constexpr int kPM = 128;              // rows of a tile
 constexpr int kPN = 128;              // keys of a tile
-constexpr int kPSoftWarps = 8, kPProdWarps = 8;
+constexpr int kPSoftWarps = 4, kPProdWarps = 8;
 constexpr int kPThreads = 32 * (kPSoftWarps + kPProdWarps + 4);  // and a warpgroup for the MMA thread
-// Registers per thread: the launch gives 96 x 640; the warpgroups pass them
-// on as 2 x 128 + 2 x 88 + 40 = 472 <= 5 x 96.
-constexpr int kPLaunchRegs = 96, kPSoftRegs = 128, kPProdRegs = 88, kPMmaRegs = 40;
-static_assert(2 * kPSoftRegs + 2 * kPProdRegs + kPMmaRegs <= 5 * kPLaunchRegs, "registers");
+// Registers per thread: the launch gives 128 x 512; the warpgroups pass them
+// on as 208 + 2 x 120 + 64 = 512 = 4 x 128.  No role spills: the latents
+// stream through what L1 the shared memory leaves (27 KB), so a spilled value
+// came back from L2 (the MMA thread issued one MMA per 300 clocks with its
+// descriptors spilled, against 64).
+constexpr int kPLaunchRegs = 128, kPSoftRegs = 208, kPProdRegs = 120, kPMmaRegs = 64;
+static_assert(kPSoftRegs + 2 * kPProdRegs + kPMmaRegs <= 4 * kPLaunchRegs, "registers");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
 constexpr int kPSms = 152;            // multiprocessors the split is planned for
 
@@ -133,11 +136,11 @@ struct PagedSmem {
     uint8_t qx[kPM * kPHalf * 2];      // other half of Q, K-major: 8-row groups of 4096 B, 8-channel chunks of 128 B
     uint8_t c[2][kPN * kPHalf * 2];    // latents: 8-key groups of 4096 B, 8-channel chunks of 128 B
     uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
-    float red[2][kPM];                 // exchange between the two threads of a row
-    uint32_t hidden[2][4];             // keys of a tile without a page, a bit each
-    uint32_t nan[2][2][4];             // keys with a NaN latent (per half of the producers)
+    alignas(16) uint16_t hidden[2][8];  // keys of a tile without a page, a bit each
+    alignas(16) uint16_t nan[2][8];     // keys with a NaN latent
+    float q_scale[kPM];                // logits' scale of each row (log2 domain)
     uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2];
-    uint64_t s_full, s_free, p_full, o_done, drain;
+    uint64_t s_full, s_free, p_full, o_done, q_done, drain;
     uint32_t tmem;
     int32_t req, local;
 };
@@ -146,20 +149,6 @@ static_assert(sizeof(PagedSmem) + 1024 <= 227 * 1024, "shared memory of the page
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
                  ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
-}
-// 32 lanes x 16 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -178,14 +167,21 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The two warps of a row quarter: a barrier, and one that gives the AND of
-// their threads' flags (so that both leave after a wait that gave up in one).
-__device__ __forceinline__ void pair_sync(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
-__device__ __forceinline__ bool pair_and(int quad, bool v) {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r) : "r"(1 + quad), "r"(uint32_t(v)) : "memory");
-    return r != 0;
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f32x2_out(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* o) {
@@ -279,10 +275,47 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         mbar_init(&S.s_free, kPSoftWarps);
         mbar_init(&S.p_full, kPSoftWarps);
         mbar_init(&S.o_done, 1);
+        mbar_init(&S.q_done, kPSoftWarps);
         mbar_init(&S.drain, 1);
         mbar_init_fence();
     }
     if (warp == kPSoftWarps + kPProdWarps) tmem_alloc(&S.tmem, 512);
+    // ---- Q to f16 times a power of two per row: 8 rows per warp, four lanes
+    // per row (64 contiguous bytes an instruction).  The other half goes to its
+    // place, the own half by way of the second group of latents into TMEM.
+    {
+        const int row = 8 * warp + (lane & 7), piece = lane >> 3;
+        const bool on = row < n_row;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (flat0 + (on ? row : 0)) * (kPD * 2)) + piece;
+        uint4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = on ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+            am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+        }
+        am = max(am & 0xFFFFu, am >> 16);
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
+        int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;  // max |q| 2^-qs in [2^14, 2^15)
+        qs = qs < -100 ? -100 : qs;
+        const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
+        if (piece == 0)
+            S.q_scale[row] = fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), FLT_MIN);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = f16x2(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
+            uint8_t* dst = (i >= 8) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
+            *reinterpret_cast<uint4*>(dst + (row >> 3) * 4096 + (4 * (i & 7) + piece) * 128 + (row & 7) * 16) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -290,68 +323,28 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
 
     if (warp < kPSoftWarps) {
         regs_up<kPSoftRegs>();
-        // ================= softmax: row 32 (warp % 4) + lane, column half warp / 4
-        const int quad = warp & 3, ch = warp >> 2, row = 32 * quad + lane;
-        const uint32_t lanes = uint32_t(32 * quad) << 16;
+        // ================= softmax: row = TMEM lane = thread
+        const int row = tid;
+        const uint32_t tm = tmem + (uint32_t(32 * warp) << 16);
         const bool row_on = row < n_row;
-        const uint8_t* qrow = a.q + ((flat0 + (row_on ? row : 0)) * kPD) * 2;
-        // ---- Q: this thread's 128 channels of each half; the row's power of two from the maximum over all
-        {
-            const uint4* qx = reinterpret_cast<const uint4*>(qrow + (x_dim + 128 * ch) * 2);
-            const uint4* qy = reinterpret_cast<const uint4*>(qrow + (y_dim + 128 * ch) * 2);
-            uint4 v[16];
-            uint32_t am = 0;
+        const float sm_eff = S.q_scale[row];
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {  // the own half of Q into TMEM, 64 channels at a time
+            uint32_t o[32];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = row_on ? __ldg((s ? qy : qx) + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-                    am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-                }
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(S.c[1] + (row >> 3) * 4096 + (8 * b + i) * 128 + (row & 7) * 16);
+                o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
             }
-            S.red[ch][row] = __uint_as_float(max(am & 0xFFFFu, am >> 16));
+            tmem_st32(tm + kColQ + 32 * b, o);
         }
-        pair_sync(quad);
-        float sm_eff;
-        {
-            const uint32_t am = max(__float_as_uint(S.red[0][row]), __float_as_uint(S.red[1][row]));
-            int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;  // max |q| 2^-qs in [2^14, 2^15)
-            qs = qs < -100 ? -100 : qs;
-            const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
-            sm_eff = fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), FLT_MIN);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const uint4* src = reinterpret_cast<const uint4*>(qrow + ((s ? y_dim : x_dim) + 128 * ch) * 2);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {  // 64 channels at a time
-                    uint4 v[8];
-                    uint32_t o[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = row_on ? __ldg(src + 8 * b + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[4 * i + e] = f16x2(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
-                    }
-                    if (s == 0) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(S.qx + (row >> 3) * 4096 + (16 * ch + 8 * b + i) * 128 + (row & 7) * 16) =
-                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else {
-                        tmem_st32(tmem + lanes + kColQ + 64 * ch + 32 * b, o);
-                    }
-                }
-            }
-            tmem_st_wait();
-        }
-        fence_async_smem();
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.s_free);  // phase 0: Q is in place
+        if (lane == 0) {
+            mbar_arrive(&S.q_done);  // the second group of latents may be filled
+            mbar_arrive(&S.s_free);  // phase 0: Q is in place
+        }
 
         // ---- key tiles
         int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys
@@ -362,50 +355,58 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int32_t j = 0; j < nt; ++j) {
-            ok = pair_and(quad, mbar_wait(&S.s_full, j & 1, a.wlim));
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full, j & 1, a.wlim));
             if (!ok) break;
             tc_fence_after();
-            uint32_t s0[32], s1[32];
-            tmem_ld32(tmem + lanes + kColS + 64 * ch, s0);
-            tmem_ld32(tmem + lanes + kColS + 64 * ch + 32, s1);
+            uint32_t s[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(tm + kColS + 32 * b, s[b]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.s_free);  // phase j + 1: S may be overwritten
-            const int32_t c0 = key0 + j * kPN + 64 * ch;
+            const int32_t c0 = key0 + j * kPN;
             const int g = j & 1;
-            const uint32_t hid0 = S.hidden[g][2 * ch], hid1 = S.hidden[g][2 * ch + 1];
-            const uint32_t nan0 = S.nan[g][0][2 * ch] | S.nan[g][1][2 * ch];
-            const uint32_t nan1 = S.nan[g][0][2 * ch + 1] | S.nan[g][1][2 * ch + 1];
-            if (__any_sync(0xffffffffu, c0 < lo_r || c0 + 64 > hi_r) || (hid0 | hid1 | nan0 | nan1) != 0) {
+            const uint4 hid = *reinterpret_cast<const uint4*>(S.hidden[g]);
+            const uint4 n4 = *reinterpret_cast<const uint4*>(S.nan[g]);
+            const uint32_t hidden[4] = {hid.x, hid.y, hid.z, hid.w}, nan[4] = {n4.x, n4.y, n4.z, n4.w};
+            if (__any_sync(0xffffffffu, c0 < lo_r || c0 + kPN > hi_r) ||
+                (hidden[0] | hidden[1] | hidden[2] | hidden[3] | nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
                 const int32_t lo = lo_r - c0, hi = hi_r - c0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if ((nan0 >> i) & 1u) s0[i] = 0x7FC00000u;
-                    if ((nan1 >> i) & 1u) s1[i] = 0x7FC00000u;
-                    if (i < lo || i >= hi || ((hid0 >> i) & 1u)) s0[i] = 0xFF800000u;
-                    if (i + 32 < lo || i + 32 >= hi || ((hid1 >> i) & 1u)) s1[i] = 0xFF800000u;
+                for (int b = 0; b < 4; ++b) {
+                    // bits of the block's columns in [lo, hi) that have a page
+                    const int32_t l0 = lo - 32 * b, h0 = hi - 32 * b;
+                    uint32_t see = l0 >= 32 || h0 <= 0 ? 0u : ~hidden[b];
+                    if (l0 > 0 && l0 < 32) see &= 0xFFFFFFFFu << l0;
+                    if (h0 > 0 && h0 < 32) see &= 0xFFFFFFFFu >> (32 - h0);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if ((nan[b] >> i) & 1u) s[b][i] = 0x7FC00000u;
+                        if (!((see >> i) & 1u)) s[b][i] = 0xFF800000u;
+                    }
                 }
             }
-            float mx = -INFINITY;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
-            S.red[ch][row] = mx;
-            pair_sync(quad);
-            mx = fmaxf(mx, S.red[ch ^ 1][row]) * sm_eff;
-            const bool grew = mx > m + 8.f;
+            for (int i = 0; i < 32; i += 2)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(s[b][i]), __uint_as_float(s[b][i + 1])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sm_eff;
+            const bool grew = top > m + 8.f;
             if (__any_sync(0xffffffffu, grew)) {
-                const float mn = grew ? mx : m;
+                const float mn = grew ? top : m;
                 const float alpha = !grew ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
                 if (j > 0) {  // every MMA before S_Y of this tile is done, the previous O among them
 #pragma unroll 1
-                    for (int b = 0; b < 8; ++b) {
-                        uint32_t o[16];
-                        tmem_ld16(tmem + lanes + kColO + 128 * ch + 16 * b, o);
+                    for (int b = 0; b < kPHalf / 32; ++b) {
+                        uint32_t o[32];
+                        tmem_ld32(tm + kColO + 32 * b, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st16(tmem + lanes + kColO + 128 * ch + 16 * b, o);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tm + kColO + 32 * b, o);
                     }
                     tmem_st_wait();
                 }
@@ -413,48 +414,49 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
                 m = mn;
             }
             const float mu = m == -INFINITY ? 0.f : m;
-            float acc[4] = {};
+            const uint64_t sm2 = f32x2(sm_eff, sm_eff), mu2 = f32x2(-mu, -mu);
+            uint64_t acc[4] = {0, 0, 0, 0};
+            uint8_t* pd = S.p + (row >> 3) * 2048 + (row & 7) * 16;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float e0 = ex2(fmaf(__uint_as_float(s0[i]), sm_eff, -mu));
-                const float e1 = ex2(fmaf(__uint_as_float(s1[i]), sm_eff, -mu));
-                acc[i & 1] += e0;
-                acc[2 + (i & 1)] += e1;
-                s0[i] = __float_as_uint(e0);
-                s1[i] = __float_as_uint(e1);
+            for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x, y;
+                        f32x2_out(fma2(f32x2(__uint_as_float(s[b][8 * i + 2 * e]), __uint_as_float(s[b][8 * i + 2 * e + 1])), sm2, mu2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        acc[e] = add2(acc[e], f32x2(x, y));
+                        w[e] = f16x2(x, y);
+                    }
+                    *reinterpret_cast<uint4*>(pd + (4 * b + i) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
-            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            uint8_t* pd = S.p + (row >> 3) * 2048 + (8 * ch) * 128 + (row & 7) * 16;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t* s = i < 4 ? s0 + 8 * i : s1 + 8 * (i - 4);
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = f16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                *reinterpret_cast<uint4*>(pd + i * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            {
+                float x, y;
+                f32x2_out(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), x, y);
+                l += x + y;
             }
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.p_full);
         }
-        if (ok && nt > 0) ok = pair_and(quad, mbar_wait(&S.o_done, 0, a.wlim));
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&S.o_done, 0, a.wlim));
         if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), ti);
-        // ---- epilogue: O / l, this thread's 128 of the own half's channels
+        // ---- epilogue: O / l, the row's 256 channels of the own half
         if (ok) {
             tc_fence_after();
-            S.red[ch][row] = l;
-            pair_sync(quad);
-            l = S.red[0][row] + S.red[1][row];
             const float inv = l == 0.f ? 0.f : 1.0f / l;
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
             const int64_t flat = flat0 + row;
-            const int dim = y_dim + 128 * ch;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+#pragma unroll 1
+            for (int b = 0; b < kPHalf / 32; ++b) {
                 uint32_t o[32];
                 if (nt > 0) {
-                    tmem_ld32(tmem + lanes + kColO + 128 * ch + 32 * b, o);
+                    tmem_ld32(tm + kColO + 32 * b, o);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
                 }
                 if (!row_on) continue;
                 if (splits == 1) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + (flat * kPD + dim + 32 * b) * 2);
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + (flat * kPD + y_dim + 32 * b) * 2);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -475,14 +477,14 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
                         dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(a.part_o + (int64_t(split) * a.rows + flat) * kPD + dim + 32 * b);
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + (int64_t(split) * a.rows + flat) * kPD + y_dim + 32 * b);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
                                              __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
                 }
             }
-            if (row_on && half == 0 && ch == 0) {
+            if (row_on && half == 0) {
                 if (splits > 1)
                     a.part_lse[int64_t(split) * a.rows + flat] = lse2;
                 else if (a.lse)
@@ -491,109 +493,145 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         }
     } else if (warp < kPSoftWarps + kPProdWarps) {
         regs_down<kPProdRegs>();
-        // ================= producers: key 32 (warp % 4) + lane, 64-channel blocks hb of each 128
-        const int pw = warp - kPSoftWarps, hb = pw >> 2, kk = 32 * (pw & 3) + lane;
-        constexpr int NV = FP8 ? 4 : 2;  // 16-byte pieces of 64 channels
-        uint4 v[4][NV];                  // the four blocks of a tile: X, X, Y, Y
-        uint32_t sc[4];
+        // ================= producers: keys 16 pw + (lane % 8) and + 8, piece lane / 8
+        // Four lanes read 64 contiguous bytes of a row, eight rows an
+        // instruction: a row per lane took 32 passes through the L1 data path
+        // for 512 bytes, which the MMAs' operand reads need (3072 passes a tile
+        // doubled the MMAs' time).  A quarter-warp stores 8 keys of one chunk:
+        // no bank conflicts.  Keys in eights share a page.
+        const int pw = warp - kPSoftWarps, k8 = lane & 7, piece = lane >> 3;
+        constexpr int NV = FP8 ? 2 : 1;  // 16-byte pieces per key and 128 channels
+        uint4 v[4][2][NV];               // the four 128-channel blocks of a tile (X, X, Y, Y) of two keys
+        uint2 sc[2];                     // FP4: the scales of block `piece` in channel order
         const int32_t* trow = a.table + req * a.max_pages;
-        auto page_at = [&](int32_t j) {  // the page id of this thread's key in tile j, or -1
-            const int32_t p = key0 + j * kPN + kk;
-            return j < nt && p < k_end ? trow[p / a.page] : -1;
-        };
-        auto dims = [&](int b) { return (b < 2 ? x_dim : y_dim) + 128 * (b & 1) + 64 * hb; };
-        int64_t at = -1;  // the cache row of the tile being loaded, or -1
-        auto locate = [&](int32_t j, int32_t id) {
-            const int32_t p = key0 + j * kPN + kk;
-            at = -1;
-            if (j < nt && p < k_end) {
-                if (id >= 0 && id < a.n_rows_pages)
-                    at = int64_t(id) * a.page + p % a.page;
-                else if (hb == 0 && half == 0)
-                    record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+        const uint8_t* src[2];           // the tile being loaded: its keys' codes (from `piece` on), null without a row
+        const uint8_t* ssrc[2];          //   and scales
+        const int64_t last_page = a.n_rows_pages;
+        const int32_t k_last = key0 + nt * kPN < k_end ? key0 + nt * kPN : k_end;  // end of this CTA's keys
+        // page ids of the warp's two key groups in 16 tiles, one per lane: a tile's are shuffled out
+        int32_t ids = -1;
+        // place within its page of the first key of the tile that is located next; a tile on is 128 keys on
+        const int32_t step_off = kPN % a.page;
+        int32_t off_t = (key0 + 16 * pw) % a.page + k8;  // groups of 8 keys share a page, so this is below it
+        auto locate = [&](int32_t j) {
+            if ((j & 15) == 0) {
+                const int32_t p = key0 + (j + (lane >> 1)) * kPN + 16 * pw + 8 * (lane & 1);
+                ids = p < k_last ? trow[p / a.page] : -1;
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (j & 15) + i);
+                const int32_t off = off_t + 8 * i >= a.page ? off_t + 8 * i - a.page : off_t + 8 * i;
+                const bool in = key0 + j * kPN + 16 * pw + 8 * i + k8 < k_last;
+                src[i] = ssrc[i] = nullptr;
+                if (in && id >= 0 && id < last_page) {
+                    const int64_t row = int64_t(id) * a.page + off;
+                    src[i] = a.codes + row * (FP8 ? kPD : kPD / 2) + 16 * piece;
+                    ssrc[i] = a.scales + row * (kPD / 16) + 8 * piece;
+                } else if (in && piece == 0 && half == 0) {
+                    record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+                }
+            }
+            off_t += step_off;
+            if (off_t >= a.page) off_t -= a.page;
+        };
+        auto load_scales = [&]() {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                sc[i] = !FP8 && src[i] ? __ldg(reinterpret_cast<const uint2*>(ssrc[i])) : make_uint2(0, 0);
         };
         auto load = [&](int b) {
-            if (at >= 0) {
-                const uint4* src = reinterpret_cast<const uint4*>(a.codes + (FP8 ? at * kPD + dims(b) : (at * kPD + dims(b)) / 2));
+            const int dim = (b < 2 ? x_dim : y_dim) + 128 * (b & 1);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) v[b][i] = __ldg(src + i);
-                if (!FP8) sc[b] = __ldg(reinterpret_cast<const uint32_t*>(a.scales + at * (kPD / 16) + dims(b) / 16));
-            } else {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < NV; ++i) v[b][i] = make_uint4(0, 0, 0, 0);
-                sc[b] = 0;
-            }
+                for (int e = 0; e < NV; ++e)
+                    v[b][i][e] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + (FP8 ? dim : dim / 2)) + 4 * e)
+                                        : make_uint4(0, 0, 0, 0);
         };
-        int32_t id_next = page_at(0);
-        locate(0, id_next);
+        locate(0);
+        load_scales();
 #pragma unroll
         for (int b = 0; b < 4; ++b) load(b);
-        id_next = page_at(1);
+        uint32_t gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
+        locate(1);  // always the tile behind the one that is decoded
         bool ok = true;
         for (int32_t j = 0; j < nt && ok; ++j) {
             const int g = j & 1;
             const uint32_t ph = (j >> 1) & 1;
-            const uint32_t gone = __ballot_sync(0xffffffffu, at < 0);
-            uint32_t bad = 0;
-            locate(j + 1, id_next);  // from here on `at` is the next tile's row
-            id_next = page_at(j + 2);
+            uint32_t bad[2] = {0, 0};
+            const uint2 sc0 = sc[0], sc1 = sc[1];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                // the block's place: X after the O MMAs of the tile before last, Y after this tile's S_X MMAs
-                if (b == 0 && j >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
+                // the block's place: X after the O MMAs of the tile before last (in the second group: after Q's
+                // own half has left it), Y after this tile's S_X MMAs
+                if (b == 0 && j >= 1)
+                    ok = __all_sync(0xffffffffu, j == 1 ? mbar_wait(&S.q_done, 0, a.wlim) : mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
                 if (b >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_x[g][b & 1], ph, a.wlim));
                 if (!ok) break;
-                uint8_t* dst = S.c[g] + (kk >> 3) * 4096 + (16 * (b & 1) + 8 * hb) * 128 + (kk & 7) * 16;
-                if (FP8) {
-                    uint32_t n4 = 0;
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
-                        n4 |= e4m3_nan4(v[b][i].x) | e4m3_nan4(v[b][i].y) | e4m3_nan4(v[b][i].z) | e4m3_nan4(v[b][i].w);
-                    bad |= n4;
-                    const uint32_t keep = n4 ? 0u : 0xFFFFFFFFu;
+                for (int i = 0; i < 2; ++i) {
+                    uint8_t* dst = S.c[g] + (2 * pw + i) * 4096 + (16 * (b & 1)) * 128 + k8 * 16;
+                    if (FP8) {
+                        uint32_t n4 = 0;
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const uint32_t w[4] = {v[b][i].x & keep, v[b][i].y & keep, v[b][i].z & keep, v[b][i].w & keep};
-                        uint32_t o[8];
+                        for (int e = 0; e < NV; ++e)
+                            n4 |= e4m3_nan4(v[b][i][e].x) | e4m3_nan4(v[b][i][e].y) | e4m3_nan4(v[b][i][e].z) |
+                                  e4m3_nan4(v[b][i][e].w);
+                        bad[i] |= n4;
+                        const uint32_t keep = n4 ? 0u : 0xFFFFFFFFu;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) e4m3x4_f16(w[e], o + 2 * e);
-                        *reinterpret_cast<uint4*>(dst + (2 * i) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(dst + (2 * i + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                } else {
-                    const uint32_t n4 = e4m3_nan4(sc[b]);
-                    bad |= n4;
-                    uint32_t s2[2];
-                    e4m3x4_f16(n4 ? 0u : sc[b], s2);
+                        for (int e = 0; e < NV; ++e) {
+                            const uint32_t w[4] = {v[b][i][e].x & keep, v[b][i][e].y & keep, v[b][i][e].z & keep, v[b][i][e].w & keep};
+                            uint32_t o[8];
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const uint32_t w[4] = {v[b][i].x, v[b][i].y, v[b][i].z, v[b][i].w};
+                            for (int t = 0; t < 4; ++t) e4m3x4_f16(w[t], o + 2 * t);
+                            *reinterpret_cast<uint4*>(dst + (8 * e + 2 * piece) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(dst + (8 * e + 2 * piece + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    } else {
+                        // scales of channels 32 piece .. + 31 of block b: 16 bits of the word that lane b of the row holds
+                        const int d = b < 2 ? (x_dim / 128) + b : (y_dim / 128) + (b - 2);
+                        const uint2 mine = i ? sc1 : sc0;
+                        const uint32_t lo = __shfl_sync(0xffffffffu, mine.x, k8 + 8 * d), hi = __shfl_sync(0xffffffffu, mine.y, k8 + 8 * d);
+                        uint32_t s2 = ((piece & 2 ? hi : lo) >> (16 * (piece & 1))) & 0xFFFFu;
+                        const uint32_t n2 = e4m3_nan4(s2);
+                        bad[i] |= n2;
+                        uint32_t ss[2];
+                        e4m3x4_f16(n2 ? 0u : s2, ss);
+                        const uint32_t w[4] = {v[b][i][0].x, v[b][i][0].y, v[b][i][0].z, v[b][i][0].w};
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {  // one group of 16 channels
-                            const uint32_t s = __byte_perm(s2[i], 0, e ? 0x3232 : 0x1010);
+                            const uint32_t s = __byte_perm(ss[0], 0, e ? 0x3232 : 0x1010);
                             uint32_t o[8];
                             e2m1x8_f16(w[2 * e], o);
                             e2m1x8_f16(w[2 * e + 1], o + 4);
 #pragma unroll
                             for (int t = 0; t < 8; ++t) o[t] = mul_f16x2(o[t], s);
-                            *reinterpret_cast<uint4*>(dst + (4 * i + 2 * e) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(dst + (4 * i + 2 * e + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                            *reinterpret_cast<uint4*>(dst + (4 * piece + 2 * e) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(dst + (4 * piece + 2 * e + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                 }
-                if (j + 1 < nt) load(b);
                 if (b == 3) {
-                    const uint32_t word = __ballot_sync(0xffffffffu, bad != 0);
+                    // per key of each eight: a bit of any of its four lanes
+                    uint32_t n0 = __ballot_sync(0xffffffffu, bad[0] != 0), n1 = __ballot_sync(0xffffffffu, bad[1] != 0);
+                    n0 |= n0 >> 16;
+                    n1 |= n1 >> 16;
+                    const uint32_t h0 = __ballot_sync(0xffffffffu, gone & 1u), h1 = __ballot_sync(0xffffffffu, gone & 2u);
                     if (lane == 0) {
-                        S.nan[g][hb][pw & 3] = word;
-                        if (hb == 0) S.hidden[g][pw & 3] = gone;
+                        S.nan[g][pw] = uint16_t(((n0 | n0 >> 8) & 0xFFu) | ((n1 | n1 >> 8) & 0xFFu) << 8);
+                        S.hidden[g][pw] = uint16_t((h0 & 0xFFu) | (h1 & 0xFFu) << 8);
                     }
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b < 2 ? &S.full_x[g][b] : &S.full_y[g][b - 2]);
+                load(b);  // the next tile's block, a tile's time ahead
+                if (b == 2) load_scales();
             }
+            gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
+            locate(j + 2);
         }
         if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), ti);
     } else {
@@ -601,38 +639,51 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         if (tid == 32 * (kPSoftWarps + kPProdWarps)) {
         // ================= MMA issue
         constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, kPHalf, 0, false, true);
-        const uint32_t sq = smem_u32(S.qx), sp = smem_u32(S.p);
+        // descriptors; a step of 16 along K is 256 bytes (K-major) or two 8-key groups (MN-major)
+        const uint64_t dq0 = umma_desc(smem_u32(S.qx), 128, 4096), dp0 = umma_desc(smem_u32(S.p), 128, 2048);
+        const uint64_t dk[2] = {umma_desc(smem_u32(S.c[0]), 128, 4096), umma_desc(smem_u32(S.c[1]), 128, 4096)};
+        const uint64_t dv[2] = {umma_desc(smem_u32(S.c[0]), 4096, 128), umma_desc(smem_u32(S.c[1]), 4096, 128)};
+        // (a value the compiler cannot know: it would keep every step's descriptor of the loop in registers, and spill)
+        auto fresh = [](uint64_t v) {
+            asm volatile("" : "+l"(v));
+            return v;
+        };
         bool ok = true;
         auto o_mma = [&](int32_t j) {  // O += P Y of tile j
             ok = ok && mbar_wait(&S.p_full, j & 1, a.wlim);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t sc = smem_u32(S.c[j & 1]);
+            const uint64_t d = fresh(j & 1 ? dv[1] : dv[0]), dp = fresh(dp0);
+#pragma unroll
             for (int k = 0; k < kPN / 16; ++k)
-                mma_f16_ss(tmem + kColO, umma_desc(sp + k * 256, 128, 2048), umma_desc(sc + k * 8192, 4096, 128), id_o,
-                           j > 0 || k > 0);
+                mma_f16_ss(tmem + kColO, dp + k * (256 >> 4), d + k * (8192 >> 4), id_o, k > 0 || j > 0);
         };
         for (int32_t j = 0; j < nt && ok; ++j) {
             const int g = j & 1;
-            const uint32_t ph = (j >> 1) & 1, sc = smem_u32(S.c[g]);
+            const uint32_t ph = (j >> 1) & 1;
+            uint64_t d = fresh(g ? dk[1] : dk[0]), dq = fresh(dq0);
             ok = mbar_wait(&S.s_free, j & 1, a.wlim);  // phase 0: Q; phase j: S of the tile before has been read
             tc_fence_after();
-            for (int b = 0; b < 2 && ok; ++b) {
-                ok = mbar_wait(&S.full_x[g][b], ph, a.wlim);
+    #pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && mbar_wait(&S.full_x[g][b], ph, a.wlim);
                 if (!ok) break;
-                for (int k = 8 * b; k < 8 * b + 8; ++k)
-                    mma_f16_ss(tmem + kColS, umma_desc(sq + k * 256, 128, 4096), umma_desc(sc + k * 256, 128, 4096), id_s, k > 0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + (8 * b + k) * (256 >> 4), id_s, k > 0 || b > 0);
                 tc_commit(&S.empty_x[g][b]);
             }
             if (ok && j > 0) {
                 o_mma(j - 1);
                 if (ok) tc_commit(&S.empty_o[g ^ 1]);
             }
-            for (int b = 0; b < 2 && ok; ++b) {
-                ok = mbar_wait(&S.full_y[g][b], ph, a.wlim);
+    #pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && mbar_wait(&S.full_y[g][b], ph, a.wlim);
                 if (!ok) break;
-                for (int k = 8 * b; k < 8 * b + 8; ++k)
-                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * k, umma_desc(sc + k * 256, 128, 4096), id_s, true);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * (8 * b + k), d + (8 * b + k) * (256 >> 4), id_s, true);
             }
             if (ok) tc_commit(&S.s_full);
         }
