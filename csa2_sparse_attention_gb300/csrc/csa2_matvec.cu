@@ -12,13 +12,17 @@
 // x goes to f16 in shared memory once per CTA, each row times a power of two
 // (exact down to 2^-28 of the row's maximum), in the order in which a lane
 // needs it.  The sum over channels is in any order as long as A and B agree:
-// lane t of a quad takes 64 consecutive channels of a 256-channel step (32
-// bytes of codes in one load, 128 contiguous bytes per weight row) and feeds
-// them four at a time to the 16 MMAs of the step, so the loads are whole lines
-// and the decoded codes need no exchange.  A CTA keeps its x and walks over the
+// lane t of a quad takes 32 consecutive channels of 128 (16 bytes of codes, 64
+// contiguous bytes per weight row) and feeds them four at a time to 8 MMAs, so
+// the decoded codes need no exchange.  A warp takes 32 rows of W, so that one
+// read of x from shared memory serves two MMAs.
+//
+// Weights come by 16-byte asynchronous copies through a ring of a warp's own
+// (2.25 KB a step, up to four steps for each of 16 warps): loads into
+// registers reached 3.1 TB/s, since a warp's six scoreboards make it wait for
+// the youngest load with the oldest.  A CTA keeps its x and walks over the
 // output channels; its warps split the channels of x (and rows of W) and add up
-// in shared memory in a fixed order.  Three steps of loads (7 KB a warp) are
-// in flight.
+// in shared memory in a fixed order.
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 #include "csa2_layout.cuh"
@@ -28,10 +32,12 @@
 
 namespace csa2 {
 
-constexpr int kMvThreads = 256, kMvWarps = kMvThreads / 32;
-constexpr int kMvStep = 256;                  // channels per step
-constexpr int kMvDepth = 3;                   // steps in flight
-constexpr size_t kMvXBytes = 200 * 1024;      // x in shared memory, per CTA
+constexpr int kMvThreads = 512, kMvWarps = kMvThreads / 32;
+constexpr int kMvStep = 128, kMvRows = 32;    // channels and rows of W per step of a warp
+constexpr int kMvStage = kMvRows * (kMvStep / 2 + kMvStep / 16);  // bytes of a step: codes, then scales
+constexpr int kMvMaxStages = 4;
+constexpr int kMvSms = 152;                   // multiprocessors the split is planned for
+constexpr size_t kMvSmem = 208 * 1024;        // x and the rings, per CTA (and the warps' sums, 16 or 32 KB)
 
 struct MatvecArgs {
     const uint8_t* x;
@@ -41,23 +47,27 @@ struct MatvecArgs {
     void* out;
     float* part;         // [slices][n][n_out] partial sums, or null
     int64_t n, x_stride, n_out, tiles;
-    int32_t k, slice;    // channels; channels per slice (a multiple of 256)
+    int32_t k, slice;    // channels; channels per slice (a multiple of 128)
     int32_t wk;          // warps over the channels; the others go over rows of W
+    int32_t x_e4m3;
     float alpha;
     int32_t out_f32;
 };
 
-struct Mv256 {
-    uint32_t w[8];
-};
-// 32 bytes that no one reads again soon
-__device__ __forceinline__ Mv256 ldg256(const uint8_t* p) {
-    Mv256 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
-                   "=r"(v.w[7])
-                 : "l"(p));
-    return v;
+// 16 bytes into shared memory past L1 (weights, read once), or 8 through it
+// (scales: the rest of the sector is other steps'); zeros where !on.
+__device__ __forceinline__ void cp16_cg(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp8_ca(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -72,30 +82,31 @@ __device__ __forceinline__ void mv_codes(uint32_t w, uint32_t s, uint32_t (&o)[4
         " mul.rn.f16x2 %0, %0, %5;\n mul.rn.f16x2 %1, %1, %5;\n mul.rn.f16x2 %2, %2, %5;\n mul.rn.f16x2 %3, %3, %5;\n}\n"
         : "=&r"(o[0]), "=&r"(o[1]), "=&r"(o[2]), "=&r"(o[3]) : "r"(w), "r"(s));
 }
-__device__ __forceinline__ void mv_scales(uint32_t w, uint32_t (&o)[4]) {  // four E4M3 scales, each as f16x2
-    uint32_t a, b;
-    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n"
-        " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n" : "=r"(a), "=r"(b) : "r"(w));
-    o[0] = __byte_perm(a, 0, 0x1010);
-    o[1] = __byte_perm(a, 0, 0x3232);
-    o[2] = __byte_perm(b, 0, 0x1010);
-    o[3] = __byte_perm(b, 0, 0x3232);
+__device__ __forceinline__ void mv_scales(uint32_t w, uint32_t& s0, uint32_t& s1) {  // two E4M3 scales, each as f16x2
+    uint32_t a;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(uint16_t(w)));
+    s0 = __byte_perm(a, 0, 0x1010);
+    s1 = __byte_perm(a, 0, 0x3232);
 }
 
 // grid (CTAs over W's rows, slices of x's channels, groups of 16 rows of x)
-template <bool FP8, int NT>
-__global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecArgs a) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+template <int NT, int STAGES>
+__global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecArgs a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ uint32_t s_max[16];
     __shared__ float s_mul[16];
-    __shared__ float s_red[2][kMvWarps][16 * NT * 8];
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
     const int64_t i0 = int64_t(blockIdx.z) * 16;
     const int rows = int(a.n - i0 < 16 ? a.n - i0 : 16);  // rows of x (NT = 1: up to 8)
     const int32_t k0 = blockIdx.y * a.slice, kn = a.k - k0 < a.slice ? a.k - k0 : a.slice;
     const int steps = (kn + kMvStep - 1) / kMvStep;
     const int wk = a.wk, wm = kMvWarps / wk, my_k = warp % wk, my_m = warp / wk;
-    const int per_tile = (steps + wk - 1) / wk;  // steps of a warp per tile of 16 wm rows of W
+    const int per_tile = (steps + wk - 1) / wk;  // steps of a warp per tile of 32 wm rows of W
+    // shared memory: rings, then the warps' sums [warp][8 NT columns][32 rows], then x
+    uint8_t* ring = smem_raw + warp * (STAGES * kMvStage);
+    float* s_red = reinterpret_cast<float*>(smem_raw + kMvWarps * STAGES * kMvStage);
+    constexpr int kRed = 8 * NT * kMvRows;
+    uint8_t* s_x = reinterpret_cast<uint8_t*>(s_red + kMvWarps * kRed);
     if (tid < 16) s_max[tid] = 0;
     grid_dep_wait();
     grid_dep_launch();
@@ -105,34 +116,50 @@ __global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecA
     const int g = lane >> 2, t = lane & 3;
     const int64_t my_tiles = (a.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x;
     const int64_t units = my_tiles * per_tile;
-    Mv256 cw[kMvDepth][2];
-    uint32_t sw[kMvDepth][2];
-    int64_t f_tile = blockIdx.x;  // the unit to be loaded next
-    int f_k = 0;
-    auto fetch = [&](int d) {
-        const int32_t c = (my_k + wk * f_k) * kMvStep + 64 * t;
+    const int64_t row8 = int64_t(a.k) * 4;  // bytes of 8 rows' codes
+    int64_t f_tile = blockIdx.x;            // the unit to be loaded next
+    int f_k = 0, f_stage = 0;
+    const uint8_t *f_code = nullptr, *f_scale = nullptr;
+    int f_left = 0;                         // rows of W from this lane's first one on
+    bool f_scale_on = false;
+    auto f_rows = [&]() {
+        const int64_t r = (f_tile * wm + my_m) * kMvRows;
+        f_left = f_tile < a.tiles ? int(a.n_out - r - g < kMvRows ? a.n_out - r - g : kMvRows) : 0;
+        f_code = a.codes + ((r + g) * a.k + k0) / 2 + 16 * t;
+        f_scale = a.scales + ((r + lane) * a.k + k0) / 16;
+        f_scale_on = f_tile < a.tiles && r + lane < a.n_out;
+    };
+    f_rows();
+    auto fetch = [&]() {
+        const int step = my_k + wk * f_k;
+        uint8_t* dst = ring + f_stage * kMvStage + lane * 16;
+        const uint8_t* src = f_code + step * (kMvStep / 2);
+        const bool in = step < steps;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t row = (f_tile * wm + my_m) * 16 + g + 8 * h;
-            if (f_tile < a.tiles && row < a.n_out && c < kn) {
-                cw[d][h] = ldg256(a.codes + (row * a.k + k0 + c) / 2);
-                sw[d][h] = __ldg(reinterpret_cast<const uint32_t*>(a.scales + (row * a.k + k0 + c) / 16));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) cw[d][h].w[e] = 0;
-                sw[d][h] = 0;
-            }
+        for (int h = 0; h < 4; ++h) {
+            const bool on = in && 8 * h < f_left;
+            cp16_cg(dst + h * 512, on ? src + h * row8 : a.codes, on);
         }
-        if (++f_k == per_tile) f_k = 0, f_tile += gridDim.x;
+        const bool son = in && f_scale_on;  // a row's 8 scales per lane
+        cp8_ca(ring + f_stage * kMvStage + 4 * 512 + lane * 8, son ? f_scale + step * (kMvStep / 16) : a.scales, son);
+        f_stage = f_stage + 1 == STAGES ? 0 : f_stage + 1;
+        if (++f_k == per_tile) {
+            f_k = 0;
+            f_tile += gridDim.x;
+            f_rows();
+        }
     };
 #pragma unroll
-    for (int d = 0; d < kMvDepth; ++d) fetch(d);
+    for (int d = 0; d < STAGES - 1; ++d) {
+        fetch();
+        cp_commit();
+    }
 
-    // ---- x: f16 in the lanes' order, [step][8-channel piece i][row][t]
+    // ---- x: f16 in the lanes' order, [128 channels][8-channel piece i][row][t]
     const int pieces = steps * (kMvStep / 8);  // per row, of 8 channels
     auto x_piece = [&](int r, int p) {
         const int64_t at = (i0 + r) * a.x_stride + k0 + 8 * p;
-        if (FP8) {
+        if (a.x_e4m3) {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.x + at));
             uint4 o;
             asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n"
@@ -146,20 +173,23 @@ __global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecA
     const int threads_per_row = kMvThreads / (rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16);
     const int xr = tid / threads_per_row, xt = tid % threads_per_row;
     __syncthreads();  // s_max is zero
-    if (!FP8 && xr < rows) {
-        uint32_t m = 0;
-        for (int p = xt; 8 * p < kn; p += threads_per_row) {
-            const uint4 v = x_piece(xr, p);
-            m = __vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
-            m = __vmaxu2(m, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    if (!a.x_e4m3) {
+        if (xr < rows) {
+            uint32_t m = 0;
+#pragma unroll 4
+            for (int p = xt; p < kn / 8; p += threads_per_row) {
+                const uint4 v = x_piece(xr, p);
+                m = __vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+                m = __vmaxu2(m, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+            }
+            m = max(m & 0xFFFFu, m >> 16);
+            atomicMax(&s_max[xr], m);
         }
-        m = max(m & 0xFFFFu, m >> 16);
-        atomicMax(&s_max[xr], m);
+        __syncthreads();
     }
-    __syncthreads();
     if (xr < rows) {
         float qf = 1.f;
-        if (!FP8) {
+        if (!a.x_e4m3) {
             int qs = s_max[xr] != 0 ? int(s_max[xr] >> 7) - 127 - 14 : 0;  // max |x| 2^-qs in [2^14, 2^15)
             qs = qs < -126 ? -126 : (qs > 126 ? 126 : qs);
             qf = __uint_as_float(uint32_t(127 - qs) << 23);
@@ -167,11 +197,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecA
         } else if (xt == 0) {
             s_mul[xr] = a.x_scales[i0 + xr];
         }
+#pragma unroll 4
         for (int p = xt; p < pieces; p += threads_per_row) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (8 * p < kn) {
                 v = x_piece(xr, p);
-                if (!FP8) {
+                if (!a.x_e4m3) {
                     uint32_t* w = &v.x;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -180,8 +211,8 @@ __global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecA
                     }
                 }
             }
-            const int c = p >> 5, pt = (p >> 3) & 3, i = p & 7;
-            *reinterpret_cast<uint4*>(smem_raw + (size_t((c * 8 + i) * rows + xr) * 4 + pt) * 16) = v;
+            const int c = p >> 4, pt = (p >> 2) & 3, i = p & 3;
+            *reinterpret_cast<uint4*>(s_x + ((c * 4 + i) * rows + xr) * 64 + pt * 16) = v;
         }
     }
     __syncthreads();
@@ -191,67 +222,82 @@ __global__ void __launch_bounds__(kMvThreads, 2) fp4_matvec_kernel(const MatvecA
 #pragma unroll
     for (int q = 0; q < NT; ++q) xoff[q] = uint32_t((8 * q + g < rows ? 8 * q + g : 0) * 4 + t) * 16;
     const uint32_t xstride = uint32_t(rows) * 64;
-    float acc[NT][4] = {};
+    float acc[2][NT][4] = {};
     int64_t tile = blockIdx.x;
-    int kk = 0, par = 0;
-    for (int64_t u0 = 0; u0 < units; u0 += kMvDepth) {
+    int kk = 0, stage = 0;
+    for (int64_t u = 0; u < units; ++u) {
+        cp_wait<STAGES - 2>();
+        __syncwarp();  // the step's copies of every lane are in; every lane is done with the stage refilled here
+        fetch();
+        cp_commit();
+        const int step = my_k + wk * kk;
+        const uint8_t* cs = ring + stage * kMvStage;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        if (step < steps) {
+            uint4 cw[4];
+            uint32_t sc[4][2];
 #pragma unroll
-        for (int d = 0; d < kMvDepth; ++d) {
-            if (u0 + d >= units) break;
-            const int step = my_k + wk * kk;
-            if (step < steps) {
-                const uint8_t* xs = smem_raw + size_t(step) * 8 * xstride;
-                uint32_t s0[4], s1[4];
-                mv_scales(sw[d][0], s0);
-                mv_scales(sw[d][1], s1);
+            for (int h = 0; h < 4; ++h) {
+                cw[h] = *reinterpret_cast<const uint4*>(cs + h * 512 + lane * 16);
+                mv_scales(*reinterpret_cast<const uint16_t*>(cs + 4 * 512 + (8 * h + g) * 8 + 2 * t), sc[h][0], sc[h][1]);
+            }
+            const uint8_t* xs = s_x + step * 4 * xstride;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < 4; ++w) {  // 8 of the lane's 32 channels
+                uint4 b[NT];
+#pragma unroll
+                for (int q = 0; q < NT; ++q) b[q] = *reinterpret_cast<const uint4*>(xs + w * xstride + xoff[q]);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
                     uint32_t r0[4], r1[4];
-                    mv_codes(cw[d][0].w[w], s0[w >> 1], r0);
-                    mv_codes(cw[d][1].w[w], s1[w >> 1], r1);
+                    const uint4 c0 = cw[2 * m], c1 = cw[2 * m + 1];
+                    mv_codes(w == 0 ? c0.x : w == 1 ? c0.y : w == 2 ? c0.z : c0.w, sc[2 * m][w >> 1], r0);
+                    mv_codes(w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w, sc[2 * m + 1][w >> 1], r1);
 #pragma unroll
                     for (int q = 0; q < NT; ++q) {
-                        const uint4 b = *reinterpret_cast<const uint4*>(xs + w * xstride + xoff[q]);
-                        mma_16816(acc[q], r0[0], r1[0], r0[1], r1[1], b.x, b.y);
-                        mma_16816(acc[q], r0[2], r1[2], r0[3], r1[3], b.z, b.w);
+                        mma_16816(acc[m][q], r0[0], r1[0], r0[1], r1[1], b[q].x, b[q].y);
+                        mma_16816(acc[m][q], r0[2], r1[2], r0[3], r1[3], b[q].z, b[q].w);
                     }
                 }
-            }
-            fetch(d);
-            if (++kk == per_tile) {  // the tile is done: add up the warps' parts and write
-                kk = 0;
-                float* mine = s_red[par][warp];
-#pragma unroll
-                for (int q = 0; q < NT; ++q) {
-                    const int col = 8 * q + 2 * t;
-                    mine[col * 16 + g] = acc[q][0];
-                    mine[(col + 1) * 16 + g] = acc[q][1];
-                    mine[col * 16 + g + 8] = acc[q][2];
-                    mine[(col + 1) * 16 + g + 8] = acc[q][3];
-                    acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
-                }
-                __syncthreads();
-                const int width = 16 * wm;
-                for (int e = tid; e < rows * width; e += kMvThreads) {
-                    const int i = e / width, j = e - i * width, m = j >> 4;
-                    float v = 0.f;
-                    for (int q = 0; q < wk; ++q) v += s_red[par][m * wk + q][i * 16 + (j & 15)];
-                    v *= s_mul[i];
-                    const int64_t row = tile * width + j;
-                    if (row < a.n_out) {
-                        if (a.part)
-                            a.part[(int64_t(blockIdx.y) * a.n + i0 + i) * a.n_out + row] = v;
-                        else if (a.out_f32)
-                            static_cast<float*>(a.out)[(i0 + i) * a.n_out + row] = a.alpha * v;
-                        else
-                            static_cast<__nv_bfloat16*>(a.out)[(i0 + i) * a.n_out + row] = __float2bfloat16_rn(a.alpha * v);
-                    }
-                }
-                par ^= 1;  // the next tile's parts go to the other buffer: one barrier per tile
-                tile += gridDim.x;
             }
         }
+        if (++kk == per_tile) {  // the tile is done: add up the warps' parts and write
+            kk = 0;
+            float* mine = s_red + warp * kRed;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    const int col = 8 * q + 2 * t, r = 16 * m + g;
+                    mine[col * kMvRows + r] = acc[m][q][0];
+                    mine[(col + 1) * kMvRows + r] = acc[m][q][1];
+                    mine[col * kMvRows + r + 8] = acc[m][q][2];
+                    mine[(col + 1) * kMvRows + r + 8] = acc[m][q][3];
+                    acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
+                }
+            __syncthreads();
+            const int width = kMvRows * wm;
+            for (int e = tid; e < rows * width; e += kMvThreads) {
+                const int i = e / width, j = e - i * width;
+                const float* from = s_red + (j >> 5) * wk * kRed + i * kMvRows + (j & 31);
+                float v = 0.f;
+                for (int q = 0; q < wk; ++q) v += from[q * kRed];
+                v *= s_mul[i];
+                const int64_t row = tile * width + j;
+                if (row < a.n_out) {
+                    if (a.part)
+                        a.part[(int64_t(blockIdx.y) * a.n + i0 + i) * a.n_out + row] = v;
+                    else if (a.out_f32)
+                        static_cast<float*>(a.out)[(i0 + i) * a.n_out + row] = a.alpha * v;
+                    else
+                        static_cast<__nv_bfloat16*>(a.out)[(i0 + i) * a.n_out + row] = __float2bfloat16_rn(a.alpha * v);
+                }
+            }
+            __syncthreads();
+            tile += gridDim.x;
+        }
     }
+    cp_wait<0>();
 }
 
 // Adds the slices' partial sums in order.
@@ -270,48 +316,57 @@ __global__ void __launch_bounds__(256) matvec_join_kernel(const float* __restric
 }
 
 struct MatvecPlan {
-    int32_t slice, slices, wk;
-    size_t x_bytes, total;
+    int32_t slice, slices, wk, stages;
+    int64_t tiles, grid;
+    size_t smem, total;
 };
 static MatvecPlan matvec_plan(int64_t n, int k, int64_t n_out) {
     MatvecPlan p{};
-    const int rows = n < 16 ? int(n > 0 ? n : 1) : 16;
+    const int rows = n < 16 ? int(n > 0 ? n : 1) : 16, nt = n > 8 ? 2 : 1;
     const int steps = (k + kMvStep - 1) / kMvStep;
-    const size_t step_bytes = size_t(rows) * kMvStep * 2;
-    const int fit = int(kMvXBytes / step_bytes);  // steps of x that a CTA can hold (25 at 16 rows)
+    const size_t step_x = size_t(rows) * kMvStep * 2, red = size_t(kMvWarps) * 8 * nt * kMvRows * 4;
+    // x's channels per CTA: what fits beside two stages (25 steps of 128 at 16 rows)
+    const int fit = int((kMvSmem - red - 2 * kMvWarps * kMvStage) / step_x);
     p.slices = (steps + fit - 1) / fit;
     const int per = (steps + p.slices - 1) / p.slices;
     p.slices = (steps + per - 1) / per;
     p.slice = per * kMvStep;
-    p.x_bytes = per * step_bytes;
-    // at least two steps of a warp per tile, so that the join over the warps stays a small part
-    p.wk = per >= 16 ? 8 : per >= 8 ? 4 : per >= 4 ? 2 : 1;
+    p.stages = int((kMvSmem - red - per * step_x) / (kMvWarps * kMvStage));
+    p.stages = p.stages < kMvMaxStages ? p.stages : kMvMaxStages;
+    p.smem = size_t(p.stages) * kMvWarps * kMvStage + red + per * step_x;
+    // warps over channels or over rows: the fewest steps of the busiest CTA, half a step for each join
+    const int64_t groups = (n + 15) / 16;
+    int64_t ctas = kMvSms / (p.slices * (groups > 0 ? groups : 1));
+    ctas = ctas < 1 ? 1 : ctas;
+    double best = 1e30;
+    for (int wk = 1; wk <= kMvWarps; wk *= 2) {
+        const int64_t tiles = (n_out + kMvRows * (kMvWarps / wk) - 1) / (kMvRows * (kMvWarps / wk));
+        const double cost = double((tiles + ctas - 1) / ctas) * ((per + wk - 1) / wk + 0.5);
+        if (cost < best) {
+            best = cost;
+            p.wk = wk;
+            p.tiles = tiles;
+            p.grid = tiles < ctas ? tiles : ctas;
+        }
+    }
     p.total = CSA2_STATUS_BYTES;
     if (p.slices > 1) p.total = align256(p.total + size_t(p.slices) * size_t(n) * size_t(n_out) * 4);
     return p;
 }
 
-template <bool FP8, int NT>
+template <int NT, int STAGES>
 static csa2_status matvec_launch(const MatvecArgs& a, const MatvecPlan& p, cudaStream_t s) {
     static std::atomic<bool> done[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(fp4_matvec_kernel<FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMvXBytes)) !=
-            cudaSuccess) {
-            cudaGetLastError();
+        if (cudaFuncSetAttribute(fp4_matvec_kernel<NT, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMvSmem)) !=
+            cudaSuccess)
             return CSA2_ERR_CUDA;
-        }
         done[dev].store(true, std::memory_order_release);
     }
-    // two CTAs per SM where both fit into its shared memory
-    const int per_sm = p.x_bytes + 20 * 1024 <= 113 * 1024 ? 2 : 1;
-    const int64_t groups = ceil_div<int64_t>(a.n, 16);
-    int64_t cap = int64_t(sm_count()) * per_sm / (p.slices * groups);
-    cap = cap < 1 ? 1 : cap;
-    const dim3 grid(unsigned(a.tiles < cap ? a.tiles : cap), unsigned(p.slices), unsigned(groups));
-    const cudaError_t e = launch(fp4_matvec_kernel<FP8, NT>, grid, kMvThreads, p.x_bytes, s, 1, a);
-    return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+    const dim3 grid(unsigned(p.grid), unsigned(p.slices), unsigned(ceil_div<int64_t>(a.n, 16)));
+    return launch(fp4_matvec_kernel<NT, STAGES>, grid, kMvThreads, p.smem, s, 1, a) == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
 
 static bool matvec_sizes(int64_t n, int k, int64_t n_out) {
@@ -353,7 +408,8 @@ extern "C" csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_
     a.n = n;
     a.x_stride = x_stride;
     a.n_out = n_out;
-    a.tiles = ceil_div<int64_t>(n_out, 16 * (kMvWarps / p.wk));
+    a.tiles = p.tiles;
+    a.x_e4m3 = x_fmt == CSA2_X_E4M3;
     a.k = k;
     a.slice = p.slice;
     a.wk = p.wk;
@@ -361,8 +417,9 @@ extern "C" csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_
     a.out_f32 = out_dtype == CSA2_OUT_F32;
     timer_begin(K_MATVEC, s);
     const bool two = n > 8;
-    const csa2_status e = x_fmt == CSA2_X_E4M3 ? (two ? matvec_launch<true, 2>(a, p, s) : matvec_launch<true, 1>(a, p, s))
-                                               : (two ? matvec_launch<false, 2>(a, p, s) : matvec_launch<false, 1>(a, p, s));
+    const csa2_status e = p.stages >= 4   ? (two ? matvec_launch<2, 4>(a, p, s) : matvec_launch<1, 4>(a, p, s))
+                          : p.stages == 3 ? (two ? matvec_launch<2, 3>(a, p, s) : matvec_launch<1, 3>(a, p, s))
+                                          : (two ? matvec_launch<2, 2>(a, p, s) : matvec_launch<1, 2>(a, p, s));
     timer_end(K_MATVEC, s);
     if (e != CSA2_OK) {
         cudaGetLastError();
