@@ -234,7 +234,7 @@ def csa2_fp4_matvec(x, x_fmt, x_scales, x_stride, n, k, codes, scales, n_out, al
 
 KERNELS = ("scan_blockmax", "select_blocks", "pool_score", "select_topk", "attn_split",
            "attn_merge", "quantize_fp4", "quantize_fp8", "rope_table", "page_plan", "paged_attn", "paged_merge",
-           "rmsnorm_fp8", "fp4_matvec")
+           "rmsnorm_fp8", "fp4_matvec", "paged_decode")
 
 
 def csa2_launch_count():

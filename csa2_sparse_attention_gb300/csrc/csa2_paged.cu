@@ -55,6 +55,13 @@ constexpr int kPM = 128;              // rows of a tile
 constexpr int kPN = 128;              // keys of a tile
 constexpr int kPSoftWarps = 4, kPProdWarps = 8;
 constexpr int kPThreads = 32 * (kPSoftWarps + kPProdWarps + 4);  // and a warpgroup for the MMA thread
+constexpr int kPTileThreads = 32 * (kPSoftWarps + 4);            // the same without producers (decoded tiles)
+// Where the latents come from: rows in pages, or tiles that paged_decode_kernel
+// laid out as shared memory holds them: per half [16 key groups][32 chunks of 8
+// channels][8 keys][16 bytes], f16.
+enum { kSrcFp4 = 0, kSrcFp8 = 1, kSrcTiles = 2 };
+constexpr int64_t kPTileBytes = int64_t(kPN) * kPD * 2;
+constexpr int kPFlagBytes = 32;       // per tile: 128 bits of keys without a page, 128 bits of keys with NaN
 // Registers per thread: the launch gives 128 x 512; the warpgroups pass them
 // on as 208 + 2 x 120 + 64 = 512 = 4 x 128.  No role spills: the latents
 // stream through what L1 the shared memory leaves (27 KB), so a spilled value
@@ -76,6 +83,8 @@ struct PagedArgs {
     float* lse;
     float* part_o;    // [splits][rows][512], each split's normalized output
     float* part_lse;  // [splits][rows], log2 domain
+    uint8_t* tiles;   // decoded tiles [n_req][span][128 KB], or null
+    uint8_t* flags;   // [n_req][span][32]
     Status* st;
     uint64_t wlim;
     int64_t n_rows_pages;  // pages of the cache
@@ -84,6 +93,7 @@ struct PagedArgs {
     int64_t n_req;
     int32_t n_tokens, heads, max_q, max_kv, page, window;
     int32_t chunk;         // key tiles per split
+    int32_t span;          // decoded tiles per request
     float sm_scale;
 };
 
@@ -113,7 +123,7 @@ __host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int3
     int32_t n = (len + kPN - 1) / kPN;
     if (window > 0) {
         const int32_t tok = (kPM - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
-        const int32_t w = (span + kPN - 1) / kPN;
+        const int32_t w = (span + kPN - 1) / kPN + 1;  // and one where the first tile begins early
         n = n < w ? n : w;
     }
     return n;
@@ -121,7 +131,14 @@ __host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int3
 __host__ __device__ inline int32_t paged_splits(int32_t tiles, int32_t chunk) {
     return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
 }
-// First key (a multiple of 8), end and key tiles of row tile ti.
+// First key that any token of the request sees, a multiple of 8: where the
+// request's decoded tiles begin.
+__device__ __forceinline__ int32_t paged_base(const PagedArgs& a, const PagedReq& rq) {
+    const int32_t lo = a.window > 0 ? rq.len - rq.nq + 1 - a.window : 0;
+    return lo > 0 ? lo & ~7 : 0;
+}
+// First key (a multiple of 8; with decoded tiles, where one begins), end and
+// key tiles of row tile ti.
 __device__ __forceinline__ void paged_tile_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
                                                 int32_t& end, int32_t& tiles) {
     const int32_t rows = rq.nq * a.heads, r0 = ti * kPM, r1 = (r0 + kPM < rows ? r0 + kPM : rows) - 1;
@@ -129,6 +146,10 @@ __device__ __forceinline__ void paged_tile_keys(const PagedArgs& a, const PagedR
     int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.heads + 1 - a.window : 0;
     if (lo < 0) lo = 0;
     begin = lo & ~7;
+    if (a.tiles != nullptr) {
+        const int32_t base = paged_base(a, rq);
+        begin = base + (begin - base) / kPN * kPN;
+    }
     tiles = end > begin ? (end - begin + kPN - 1) / kPN : 0;
 }
 
@@ -136,8 +157,10 @@ struct PagedSmem {
     uint8_t qx[kPM * kPHalf * 2];      // other half of Q, K-major: 8-row groups of 4096 B, 8-channel chunks of 128 B
     uint8_t c[2][kPN * kPHalf * 2];    // latents: 8-key groups of 4096 B, 8-channel chunks of 128 B
     uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
-    alignas(16) uint16_t hidden[2][8];  // keys of a tile without a page, a bit each
-    alignas(16) uint16_t nan[2][8];     // keys with a NaN latent
+    struct alignas(32) {
+        uint16_t hidden[8];            // keys of a tile without a page, a bit each
+        uint16_t nan[8];               // keys with a NaN latent
+    } flags[2];
     float q_scale[kPM];                // logits' scale of each row (log2 domain)
     uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2];
     uint64_t s_full, s_free, p_full, o_done, q_done, drain;
@@ -205,8 +228,11 @@ __device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return ((w & 0x7F7F7
 
 // grid: 2 CTAs (output halves) per (row tile, split), row tiles with the most
 // keys first; CTAs beyond the last one leave at once.
-template <bool FP8>
-__global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArgs a) {
+template <int SRC>
+__global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 1) paged_attn_kernel(const PagedArgs a) {
+    constexpr bool FP8 = SRC == kSrcFp8, TILES = SRC == kSrcTiles;
+    constexpr int kMmaWarp = TILES ? kPSoftWarps : kPSoftWarps + kPProdWarps;
+    constexpr int kFullCount = TILES ? 1 : kPProdWarps;  // arrivals that fill a block
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PagedSmem& S = *reinterpret_cast<PagedSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
@@ -265,8 +291,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
     if (tid == 0) {
         for (int g = 0; g < 2; ++g) {
             for (int b = 0; b < 2; ++b) {
-                mbar_init(&S.full_x[g][b], kPProdWarps);
-                mbar_init(&S.full_y[g][b], kPProdWarps);
+                mbar_init(&S.full_x[g][b], kFullCount);
+                mbar_init(&S.full_y[g][b], kFullCount);
                 mbar_init(&S.empty_x[g][b], 1);
             }
             mbar_init(&S.empty_o[g], 1);
@@ -279,12 +305,12 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         mbar_init(&S.drain, 1);
         mbar_init_fence();
     }
-    if (warp == kPSoftWarps + kPProdWarps) tmem_alloc(&S.tmem, 512);
+    if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
     // ---- Q to f16 times a power of two per row: 8 rows per warp, four lanes
     // per row (64 contiguous bytes an instruction).  The other half goes to its
     // place, the own half by way of the second group of latents into TMEM.
-    {
-        const int row = 8 * warp + (lane & 7), piece = lane >> 3;
+    for (int rg = warp; rg < kPM / 8; rg += (TILES ? kPTileThreads : kPThreads) / 32) {
+        const int row = 8 * rg + (lane & 7), piece = lane >> 3;
         const bool on = row < n_row;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (flat0 + (on ? row : 0)) * (kPD * 2)) + piece;
         uint4 v[16];
@@ -322,7 +348,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
     const uint32_t tmem = S.tmem;
 
     if (warp < kPSoftWarps) {
-        regs_up<kPSoftRegs>();
+        if (!TILES) regs_up<kPSoftRegs>();
         // ================= softmax: row = TMEM lane = thread
         const int row = tid;
         const uint32_t tm = tmem + (uint32_t(32 * warp) << 16);
@@ -367,8 +393,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
             if (lane == 0) mbar_arrive(&S.s_free);  // phase j + 1: S may be overwritten
             const int32_t c0 = key0 + j * kPN;
             const int g = j & 1;
-            const uint4 hid = *reinterpret_cast<const uint4*>(S.hidden[g]);
-            const uint4 n4 = *reinterpret_cast<const uint4*>(S.nan[g]);
+            const uint4 hid = *reinterpret_cast<const uint4*>(S.flags[g].hidden);
+            const uint4 n4 = *reinterpret_cast<const uint4*>(S.flags[g].nan);
             const uint32_t hidden[4] = {hid.x, hid.y, hid.z, hid.w}, nan[4] = {n4.x, n4.y, n4.z, n4.w};
             if (__any_sync(0xffffffffu, c0 < lo_r || c0 + kPN > hi_r) ||
                 (hidden[0] | hidden[1] | hidden[2] | hidden[3] | nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
@@ -491,7 +517,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
                     a.lse[flat] = lse2 * 0.6931471805599453f;
             }
         }
-    } else if (warp < kPSoftWarps + kPProdWarps) {
+    } else if (!TILES && warp < kPSoftWarps + kPProdWarps) {
         regs_down<kPProdRegs>();
         // ================= producers: keys 16 pw + (lane % 8) and + 8, piece lane / 8
         // Four lanes read 64 contiguous bytes of a row, eight rows an
@@ -620,8 +646,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
                     n1 |= n1 >> 16;
                     const uint32_t h0 = __ballot_sync(0xffffffffu, gone & 1u), h1 = __ballot_sync(0xffffffffu, gone & 2u);
                     if (lane == 0) {
-                        S.nan[g][pw] = uint16_t(((n0 | n0 >> 8) & 0xFFu) | ((n1 | n1 >> 8) & 0xFFu) << 8);
-                        S.hidden[g][pw] = uint16_t((h0 & 0xFFu) | (h1 & 0xFFu) << 8);
+                        S.flags[g].nan[pw] = uint16_t(((n0 | n0 >> 8) & 0xFFu) | ((n1 | n1 >> 8) & 0xFFu) << 8);
+                        S.flags[g].hidden[pw] = uint16_t((h0 & 0xFFu) | (h1 & 0xFFu) << 8);
                     }
                 }
                 fence_async_smem();
@@ -635,8 +661,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
         }
         if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), ti);
     } else {
-        regs_down<kPMmaRegs>();
-        if (tid == 32 * (kPSoftWarps + kPProdWarps)) {
+        if (!TILES) regs_down<kPMmaRegs>();
+        if (tid == 32 * kMmaWarp) {
         // ================= MMA issue
         constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, kPHalf, 0, false, true);
         // descriptors; a step of 16 along K is 256 bytes (K-major) or two 8-key groups (MN-major)
@@ -695,11 +721,134 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_attn_kernel(const PagedArg
             tc_commit(&S.drain);
             mbar_wait(&S.drain, 0, kDrainNs);
         }
+        } else if (TILES && warp == kMmaWarp + 1) {
+            // ================= tile copies: a block of 128 channels is 2 KB of each of 16 key groups
+            const uint8_t* x_src = a.tiles + (req * a.span + (key0 - paged_base(a, rq)) / kPN) * kPTileBytes;
+            const uint8_t* y_src = x_src + half * (kPTileBytes / 2);
+            x_src += (1 - half) * (kPTileBytes / 2);
+            const uint8_t* flags = a.flags + (req * a.span + (key0 - paged_base(a, rq)) / kPN) * kPFlagBytes;
+            bool ok = true;
+            int32_t last_x[2][2] = {{-1, -1}, {-1, -1}}, last_y[2][2] = {{-1, -1}, {-1, -1}};  // tiles copied last
+            auto copy = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
+                __syncwarp();
+                if (lane < kPN / 8)
+                    bulk_g2s(S.c[g] + lane * 4096 + b * 2048, src + lane * 4096 + b * 2048, 2048, bar);
+                else if (lane == kPN / 8 && fl)
+                    bulk_g2s(&S.flags[g], fl, kPFlagBytes, bar);
+                __syncwarp();
+            };
+            for (int32_t j = 0; j < nt && ok; ++j) {
+                const int g = j & 1;
+                const uint32_t ph = (j >> 1) & 1;
+                if (j >= 1)
+                    ok = __all_sync(0xffffffffu, j == 1 ? mbar_wait(&S.q_done, 0, a.wlim) : mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
+                for (int b = 0; b < 2 && ok; ++b) {
+                    copy(&S.full_x[g][b], g, b, x_src + j * kPTileBytes, nullptr);
+                    last_x[g][b] = j;
+                }
+                for (int b = 0; b < 2 && ok; ++b) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_x[g][b], ph, a.wlim));
+                    if (!ok) break;
+                    copy(&S.full_y[g][b], g, b, y_src + j * kPTileBytes, b ? flags + j * kPFlagBytes : nullptr);
+                    last_y[g][b] = j;
+                }
+            }
+            if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 9, int32_t(req), ti);
+            // every copy lands before the CTA leaves its shared memory, also after a give-up
+            for (int g = 0; g < 2; ++g)
+                for (int b = 0; b < 2; ++b) {
+                    if (last_x[g][b] >= 0) mbar_wait(&S.full_x[g][b], (last_x[g][b] >> 1) & 1, kDrainNs);
+                    if (last_y[g][b] >= 0) mbar_wait(&S.full_y[g][b], (last_y[g][b] >> 1) & 1, kDrainNs);
+                }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kPSoftWarps + kPProdWarps) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Decodes the pages of every request once into tiles of 128 keys (see
+// kSrcTiles), for calls whose requests have several row tiles: each of them
+// would decode every key again, and the decoding, not the MMAs, bounds the
+// kernel then (12,600 warp instructions a key tile).  grid (tiles, requests).
+template <bool FP8>
+__global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
+    __shared__ uint32_t s_nan[4], s_hidden[4];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t req = blockIdx.y;
+    PagedReq rq;
+    if (!paged_request(a, req, rq, nullptr)) return;
+    const int32_t base = paged_base(a, rq) + int32_t(blockIdx.x) * kPN;
+    if (base >= rq.len) return;
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, k8 = lane & 7, piece = lane >> 3;
+    uint8_t* tile = a.tiles + (req * a.span + blockIdx.x) * kPTileBytes;
+    if (tid < 4) s_nan[tid] = s_hidden[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // key groups of 8: 2 warp + i; a lane has 16 bytes of every 64
+        const int kg = 2 * warp + i, key = 8 * kg + k8;
+        const int32_t p = base + key;
+        int64_t row = -1;
+        if (p < rq.len) {
+            const int32_t id = a.table[req * a.max_pages + p / a.page];
+            if (id >= 0 && id < a.n_rows_pages)
+                row = int64_t(id) * a.page + p % a.page;
+            else if (piece == 0)
+                record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+        }
+        uint32_t bad = 0;
+        constexpr int NP = FP8 ? 8 : 4;  // 64-byte parts of a row
+        uint4 v[NP];
+        uint4 sc[2];
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+            v[e] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.codes + row * (FP8 ? kPD : kPD / 2) + 64 * e) + piece)
+                            : make_uint4(0, 0, 0, 0);
+        sc[0] = sc[1] = make_uint4(0, 0, 0, 0);
+        if (!FP8 && row >= 0) {
+            sc[0] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)));
+            sc[1] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)) + 1);
+        }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+            // channels: FP4 128 e + 32 piece .. + 31, FP8 64 e + 16 piece .. + 15
+            constexpr int NC = FP8 ? 2 : 4;
+            const int chunk = FP8 ? 8 * e + 2 * piece : 16 * e + 4 * piece;
+            uint8_t* dst = tile + (chunk >> 5) * (kPTileBytes / 2) + kg * 4096 + (chunk & 31) * 128 + k8 * 16;
+            uint32_t o[4 * NC];
+            if (FP8) {
+                const uint32_t n4 = e4m3_nan4(w[0]) | e4m3_nan4(w[1]) | e4m3_nan4(w[2]) | e4m3_nan4(w[3]);
+                bad |= n4;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) e4m3x4_f16(n4 ? 0u : w[m], o + 2 * m);
+            } else {
+                const uint32_t* s8 = &sc[0].x + 2 * e;  // the 8 scales of 128 channels
+                const uint32_t s2 = ((piece & 2 ? s8[1] : s8[0]) >> (16 * (piece & 1))) & 0xFFFFu;
+                const uint32_t n2 = e4m3_nan4(s2);
+                bad |= n2;
+                uint32_t ss[2];
+                e4m3x4_f16(n2 ? 0u : s2, ss);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t s = __byte_perm(ss[0], 0, m >= 2 ? 0x3232 : 0x1010);
+                    e2m1x8_f16(w[m], o + (4 * m) % (4 * NC));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[(4 * m + q) % (4 * NC)] = mul_f16x2(o[(4 * m + q) % (4 * NC)], s);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+        if (bad) atomicOr(&s_nan[key >> 5], 1u << (key & 31));
+        if (row < 0) atomicOr(&s_hidden[key >> 5], 1u << (key & 31));
+    }
+    __syncthreads();
+    uint32_t* fl = reinterpret_cast<uint32_t*>(a.flags + (req * a.span + blockIdx.x) * kPFlagBytes);
+    if (tid < 4) fl[tid] = s_hidden[tid], fl[4 + tid] = s_nan[tid];
 }
 
 // Joins the splits of a row: weights 2^(lse_s - max lse) over the normalized
@@ -745,15 +894,20 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     if (a.lse && t == 0) a.lse[row] = w == 0.f ? -INFINITY : (m + log2f(w)) * 0.6931471805599453f;
 }
 
-// How a call is split: key tiles per CTA, from the host's bounds alone.  A
-// CTA takes one (row tile, half, split); the split count is the one with the
-// least time by: waves of 152 CTAs, each a start of 5 us and 1.9 us per key
-// tile, plus the merge's pass over the partial outputs.
+// How a call runs, from the host's bounds alone.  A CTA takes one (row tile,
+// half, split); the split count is the one with the least time by: waves of
+// 152 CTAs, each a start of 5 us and a time per key tile, plus the merge's pass
+// over the partial outputs.
+// Requests of more than two row tiles take the latents from decoded tiles where
+// those need no more than 1 GB: 1024 tokens x 64 heads over 16K entries take
+// DECODED_MS against 3.00 ms; at one row tile a key would be decoded once
+// either way, and written and read besides.
 struct PagedPlan {
-    int32_t chunk, splits;
+    int32_t chunk, splits, span;
     int64_t grid;
-    size_t part_lse, part_o, total;
+    size_t part_lse, part_o, tiles, flags, total;
 };
+constexpr size_t kPMaxTileBytes = size_t(1) << 30;
 static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
     PagedPlan p{};
     if (window >= max_kv) window = 0;
@@ -762,13 +916,22 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     const int64_t each = n_req * paged_row_tiles(max_q, n_heads);
     tiles = tiles < each ? tiles : each;
     const int32_t nt = paged_key_tiles(max_q, max_kv, n_heads, window);
+    if (paged_row_tiles(max_q, n_heads) > 2) {
+        int64_t span = (max_kv + kPN - 1) / kPN;
+        if (window > 0) {  // from the first token's window to the last token
+            const int64_t w = (int64_t(window) + max_q + 7 + kPN - 1) / kPN;
+            span = span < w ? span : w;
+        }
+        if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) p.span = int32_t(span);
+    }
+    const double tile_us = p.span ? 2.1 : 3.4;
     p.chunk = nt > 0 ? nt : 1;
     double best = 1e30;
     for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
         const int32_t chunk = (nt + s - 1) / s;
         if (s > 1 && paged_splits(nt, chunk) != s) continue;
         const double waves = double((2 * tiles * s + kPSms - 1) / kPSms);
-        double us = waves * (5.0 + 1.9 * chunk);
+        double us = waves * (5.0 + tile_us * chunk);
         if (s > 1) us += 4.0 + double(rows) * s * kPD * 4 * 2 / 4e6;
         if (us < best) {
             best = us;
@@ -777,30 +940,36 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     }
     p.splits = paged_splits(nt, p.chunk);
     p.grid = 2 * tiles * p.splits;
-    p.part_lse = CSA2_STATUS_BYTES;
-    p.part_o = p.total = CSA2_STATUS_BYTES;
-    if (p.splits > 1) {
-        p.part_o = align256(p.part_lse + size_t(p.splits) * size_t(rows) * 4);
-        p.total = align256(p.part_o + size_t(p.splits) * size_t(rows) * kPD * 4);
-    }
+    size_t at = CSA2_STATUS_BYTES;
+    p.part_lse = at;
+    if (p.splits > 1) at = align256(at + size_t(p.splits) * size_t(rows) * 4);
+    p.part_o = at;
+    if (p.splits > 1) at = align256(at + size_t(p.splits) * size_t(rows) * kPD * 4);
+    p.flags = at;
+    at = align256(at + size_t(n_req) * p.span * kPFlagBytes);
+    p.tiles = at;
+    at += size_t(n_req) * p.span * kPTileBytes;
+    p.total = at;
     return p;
 }
 
 // Once per device and format: the shared memory opt-in, and the register
 // count that the kernel's split of them is made for.
-static csa2_status prepare_paged(bool fp8) {
-    static std::atomic<bool> done[2][64] = {};
+template <int SRC>
+static csa2_status prepare_paged() {
+    static std::atomic<bool> done[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
-    if (done[fp8][dev].load(std::memory_order_acquire)) return CSA2_OK;
-    auto kernel = fp8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+    if (done[dev].load(std::memory_order_acquire)) return CSA2_OK;
     cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess || at.numRegs != kPLaunchRegs ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(PagedSmem))) != cudaSuccess) {
+    if (cudaFuncGetAttributes(&at, paged_attn_kernel<SRC>) != cudaSuccess ||
+        (SRC != kSrcTiles && at.numRegs != kPLaunchRegs) ||
+        cudaFuncSetAttribute(paged_attn_kernel<SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(PagedSmem))) !=
+            cudaSuccess) {
         cudaGetLastError();
         return CSA2_ERR_CUDA;
     }
-    done[fp8][dev].store(true, std::memory_order_release);
+    done[dev].store(true, std::memory_order_release);
     return CSA2_OK;
 }
 
@@ -846,8 +1015,9 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     cudaStream_t s = cudaStream_t(stream);
     const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
     if (plan.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
-    auto kernel = fmt == CSA2_FMT_FP8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
-    const csa2_status prep = prepare_paged(fmt == CSA2_FMT_FP8);
+    const bool fp8 = fmt == CSA2_FMT_FP8;
+    auto kernel = plan.span ? paged_attn_kernel<kSrcTiles> : fp8 ? paged_attn_kernel<kSrcFp8> : paged_attn_kernel<kSrcFp4>;
+    const csa2_status prep = plan.span ? prepare_paged<kSrcTiles>() : fp8 ? prepare_paged<kSrcFp8>() : prepare_paged<kSrcFp4>();
     if (prep != CSA2_OK) return prep;
     PagedArgs a{};
     a.q = static_cast<const uint8_t*>(q_bf16);
@@ -860,6 +1030,11 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.lse = out_lse;
     a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_lse);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_o);
+    if (plan.span) {
+        a.tiles = reinterpret_cast<uint8_t*>(static_cast<char*>(ws) + plan.tiles);
+        a.flags = reinterpret_cast<uint8_t*>(static_cast<char*>(ws) + plan.flags);
+        a.span = plan.span;
+    }
     a.st = static_cast<Status*>(ws);
     a.wlim = wait_limit_ns();
     a.n_rows_pages = n_rows / page_size;
@@ -874,8 +1049,14 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.window = window >= max_kv ? 0 : window;
     a.chunk = plan.chunk;
     a.sm_scale = sm_scale;
+    if (plan.span) {
+        timer_begin(K_PAGED_DECODE, s);
+        launch(fp8 ? paged_decode_kernel<true> : paged_decode_kernel<false>, dim3(unsigned(plan.span), unsigned(n_req)), 256, 0,
+               s, 1, a);
+        timer_end(K_PAGED_DECODE, s);
+    }
     timer_begin(K_PAGED_ATTN, s);
-    const cudaError_t e = launch(kernel, dim3(unsigned(plan.grid)), kPThreads, sizeof(PagedSmem), s, 1, a);
+    const cudaError_t e = launch(kernel, dim3(unsigned(plan.grid)), plan.span ? kPTileThreads : kPThreads, sizeof(PagedSmem), s, 1, a);
     timer_end(K_PAGED_ATTN, s);
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -21,7 +21,8 @@ enum KernelId {
     K_PAGED_MERGE = 11,
     K_RMSNORM = 12,
     K_MATVEC = 13,
-    K_COUNT = 14
+    K_PAGED_DECODE = 14,
+    K_COUNT = 15
 };
 
 void timer_begin(int id, cudaStream_t s);

@@ -446,7 +446,7 @@ csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_scales, int
  *   `kernel_id` (0 scan_blockmax, 1 select_blocks, 2 pool_score,
  *   3 select_topk, 4 attn_split (either attention kernel), 5 attn_merge, 6 quantize_fp4,
  *   7 quantize_fp8, 8 rope_table, 9 page_plan, 10 paged_attn, 11 paged_merge,
- *   12 rmsnorm_fp8, 13 fp4_matvec) with CUDA events on their stream.  Not for
+ *   12 rmsnorm_fp8, 13 fp4_matvec, 14 paged_decode) with CUDA events on their stream.  Not for
  *   use during stream capture.
  * csa2_timer_read: wait for those events, return the summed device time and
  *   the number of launches timed, and switch the timer off.
