@@ -94,6 +94,7 @@ struct PagedArgs {
     int32_t n_tokens, heads, max_q, max_kv, page, window;
     int32_t chunk;         // key tiles per split
     int32_t span;          // decoded tiles per request
+    int32_t item;          // rows of a work item: a row tile, or the two of a cluster (decoded tiles)
     float sm_scale;
 };
 
@@ -117,12 +118,12 @@ __device__ __forceinline__ bool paged_request(const PagedArgs& a, int64_t r, Pag
     }
     return o.nq > 0;
 }
-__host__ __device__ inline int32_t paged_row_tiles(int32_t nq, int32_t heads) { return (nq * heads + kPM - 1) / kPM; }
-// Key tiles that a row tile of a request can span at most, and its splits.
-__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t heads, int32_t window) {
+__host__ __device__ inline int32_t paged_items(int32_t nq, int32_t heads, int32_t item) { return (nq * heads + item - 1) / item; }
+// Key tiles that a work item of a request can span at most, and its splits.
+__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t heads, int32_t window, int32_t item) {
     int32_t n = (len + kPN - 1) / kPN;
     if (window > 0) {
-        const int32_t tok = (kPM - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
+        const int32_t tok = (item - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
         const int32_t w = (span + kPN - 1) / kPN + 1;  // and one where the first tile begins early
         n = n < w ? n : w;
     }
@@ -138,10 +139,10 @@ __device__ __forceinline__ int32_t paged_base(const PagedArgs& a, const PagedReq
     return lo > 0 ? lo & ~7 : 0;
 }
 // First key (a multiple of 8; with decoded tiles, where one begins), end and
-// key tiles of row tile ti.
-__device__ __forceinline__ void paged_tile_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
+// key tiles of a work item.
+__device__ __forceinline__ void paged_item_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
                                                 int32_t& end, int32_t& tiles) {
-    const int32_t rows = rq.nq * a.heads, r0 = ti * kPM, r1 = (r0 + kPM < rows ? r0 + kPM : rows) - 1;
+    const int32_t rows = rq.nq * a.heads, r0 = ti * a.item, r1 = (r0 + a.item < rows ? r0 + a.item : rows) - 1;
     end = rq.len - rq.nq + r1 / a.heads + 1;
     int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.heads + 1 - a.window : 0;
     if (lo < 0) lo = 0;
@@ -180,6 +181,29 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Clusters of two CTAs: a barrier of all their threads; an arrival at the other
+// CTA's mbarrier; a commit and a bulk copy that reach both (same offsets).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t cta) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(cta));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"(uint16_t(3))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(uint16_t(3))
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -236,13 +260,15 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PagedSmem& S = *reinterpret_cast<PagedSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
-    const int half = blockIdx.x & 1;
+    // grid.x: work items, halves, and with decoded tiles the two row tiles of a cluster
+    const int half = TILES ? (blockIdx.x >> 1) & 1 : blockIdx.x & 1;
+    const int rank = TILES ? blockIdx.x & 1 : 0;
     grid_dep_wait();
     grid_dep_launch();
 
     // ---- the CTA's request: a warp scan of the requests' work items
     if (warp == 0) {
-        const int64_t item = blockIdx.x >> 1;
+        const int64_t item = blockIdx.x >> (TILES ? 2 : 1);
         int64_t base = 0;
         int32_t req = -1, local = 0;
         for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
@@ -250,8 +276,8 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             int64_t items = 0;
             PagedReq rq;
             if (r < a.n_req && paged_request(a, r, rq, blockIdx.x == 0 ? a.st : nullptr))
-                items = int64_t(paged_row_tiles(rq.nq, a.heads)) *
-                        paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window), a.chunk);
+                items = int64_t(paged_items(rq.nq, a.heads, a.item)) *
+                        paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
             int64_t inc = items;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -274,18 +300,20 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
     const int64_t req = S.req;
     PagedReq rq;
     paged_request(a, req, rq, nullptr);
-    const int32_t tiles_r = paged_row_tiles(rq.nq, a.heads);
-    const int32_t ns_r = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window), a.chunk);
-    const int32_t ti = tiles_r - 1 - S.local / ns_r, split = S.local % ns_r;
+    const int32_t items_r = paged_items(rq.nq, a.heads, a.item);
+    const int32_t ns_r = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
+    const int32_t it = items_r - 1 - S.local / ns_r, split = S.local % ns_r;
     int32_t k_begin, k_end, k_tiles;
-    paged_tile_keys(a, rq, ti, k_begin, k_end, k_tiles);
+    paged_item_keys(a, rq, it, k_begin, k_end, k_tiles);
     const int32_t splits = paged_splits(k_tiles, a.chunk);
     if (split >= splits) return;
     const int32_t j0 = split * a.chunk;
     const int32_t nt = k_tiles - j0 < a.chunk ? k_tiles - j0 : a.chunk;  // this CTA's key tiles (0: nothing to see)
     const int32_t key0 = k_begin + j0 * kPN;
-    const int64_t flat0 = int64_t(rq.q0) * a.heads + int64_t(ti) * kPM;
+    // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
+    const int32_t ti = TILES ? 2 * it + rank : it;
     const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
+    const int64_t flat0 = int64_t(rq.q0) * a.heads + (n_row > 0 ? int64_t(ti) * kPM : 0);
     const int x_dim = kPHalf * (1 - half), y_dim = kPHalf * half;
 
     if (tid == 0) {
@@ -293,16 +321,16 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&S.full_x[g][b], kFullCount);
                 mbar_init(&S.full_y[g][b], kFullCount);
-                mbar_init(&S.empty_x[g][b], 1);
+                mbar_init(&S.empty_x[g][b], TILES ? 2 : 1);  // with clusters: both CTAs' MMAs
             }
-            mbar_init(&S.empty_o[g], 1);
+            mbar_init(&S.empty_o[g], TILES ? 2 : 1);
         }
         mbar_init(&S.s_full, 1);
         mbar_init(&S.s_free, kPSoftWarps);
         mbar_init(&S.p_full, kPSoftWarps);
         mbar_init(&S.o_done, 1);
-        mbar_init(&S.q_done, kPSoftWarps);
-        mbar_init(&S.drain, 1);
+        mbar_init(&S.q_done, (TILES ? 2 : 1) * kPSoftWarps);
+        mbar_init(&S.drain, TILES ? 2 : 1);
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
@@ -343,7 +371,8 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         fence_async_smem();
     }
     tc_fence_before();
-    __syncthreads();
+    if (TILES) cluster_sync();  // the other CTA's barriers are initialized as well
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
 
@@ -369,6 +398,7 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&S.q_done);  // the second group of latents may be filled
+            if (TILES) mbar_arrive_peer(&S.q_done, rank ^ 1);
             mbar_arrive(&S.s_free);  // phase 0: Q is in place
         }
 
@@ -697,11 +727,14 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + (8 * b + k) * (256 >> 4), id_s, k > 0 || b > 0);
-                tc_commit(&S.empty_x[g][b]);
+                if (TILES) tc_commit_pair(&S.empty_x[g][b]);
+                else tc_commit(&S.empty_x[g][b]);
             }
             if (ok && j > 0) {
                 o_mma(j - 1);
-                if (ok) tc_commit(&S.empty_o[g ^ 1]);
+                // (only what a producer waits for: an arrival at the other CTA must not outlive it)
+                if (ok && TILES && j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1]);
+                if (ok && !TILES) tc_commit(&S.empty_o[g ^ 1]);
             }
     #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -717,12 +750,16 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             if (ok) o_mma(nt - 1);
             if (ok) tc_commit(&S.o_done);
             if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), ti);
-            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done
-            tc_commit(&S.drain);
+            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done (in a cluster:
+            // until both CTAs' commits have arrived here)
+            if (TILES) tc_commit_pair(&S.drain);
+            else tc_commit(&S.drain);
             mbar_wait(&S.drain, 0, kDrainNs);
         }
         } else if (TILES && warp == kMmaWarp + 1) {
-            // ================= tile copies: a block of 128 channels is 2 KB of each of 16 key groups
+            // ================= tile copies: a block of 128 channels is 2 KB of each of 16 key groups.  Each CTA of
+            // the cluster copies half of them into both: without sharing, 128 KB per key tile and CTA took 7.8 TB/s
+            // from L2 and bounded the kernel.
             const uint8_t* x_src = a.tiles + (req * a.span + (key0 - paged_base(a, rq)) / kPN) * kPTileBytes;
             const uint8_t* y_src = x_src + half * (kPTileBytes / 2);
             x_src += (1 - half) * (kPTileBytes / 2);
@@ -732,10 +769,11 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             auto copy = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
                 if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
                 __syncwarp();
-                if (lane < kPN / 8)
-                    bulk_g2s(S.c[g] + lane * 4096 + b * 2048, src + lane * 4096 + b * 2048, 2048, bar);
-                else if (lane == kPN / 8 && fl)
-                    bulk_g2s(&S.flags[g], fl, kPFlagBytes, bar);
+                const int kg = rank * (kPN / 16) + lane;
+                if (lane < kPN / 16)
+                    bulk_g2s_pair(S.c[g] + kg * 4096 + b * 2048, src + kg * 4096 + b * 2048, 2048, bar);
+                else if (lane == kPN / 16 && fl && rank == 0)
+                    bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
                 __syncwarp();
             };
             for (int32_t j = 0; j < nt && ok; ++j) {
@@ -764,7 +802,8 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (TILES) cluster_sync();  // neither CTA leaves while the other may copy or arrive here
+    else __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -870,7 +909,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     PagedReq rq;
     if (!paged_request(a, lo, rq, nullptr) || tok < rq.q0 || tok >= rq.q0 + rq.nq) return;
     int32_t begin, end, tiles;
-    paged_tile_keys(a, rq, int32_t((row - int64_t(rq.q0) * a.heads) / kPM), begin, end, tiles);
+    paged_item_keys(a, rq, int32_t((row - int64_t(rq.q0) * a.heads) / a.item), begin, end, tiles);
     const int32_t splits = paged_splits(tiles, a.chunk);
     if (splits == 1) return;
     float m = -INFINITY;
@@ -903,7 +942,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // DECODED_MS against 3.00 ms; at one row tile a key would be decoded once
 // either way, and written and read besides.
 struct PagedPlan {
-    int32_t chunk, splits, span;
+    int32_t chunk, splits, span, item;
     int64_t grid;
     size_t part_lse, part_o, tiles, flags, total;
 };
@@ -912,25 +951,30 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     PagedPlan p{};
     if (window >= max_kv) window = 0;
     const int64_t rows = n_tokens * n_heads;
-    int64_t tiles = rows / kPM + n_req;  // each request rounds up
-    const int64_t each = n_req * paged_row_tiles(max_q, n_heads);
-    tiles = tiles < each ? tiles : each;
-    const int32_t nt = paged_key_tiles(max_q, max_kv, n_heads, window);
-    if (paged_row_tiles(max_q, n_heads) > 2) {
+    p.item = kPM;
+    if (paged_items(max_q, n_heads, kPM) > 2) {
         int64_t span = (max_kv + kPN - 1) / kPN;
         if (window > 0) {  // from the first token's window to the last token
             const int64_t w = (int64_t(window) + max_q + 7 + kPN - 1) / kPN;
             span = span < w ? span : w;
         }
-        if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) p.span = int32_t(span);
+        if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) {
+            p.span = int32_t(span);
+            p.item = 2 * kPM;
+        }
     }
-    const double tile_us = p.span ? 2.1 : 3.4;
+    int64_t items = rows / p.item + n_req;  // each request rounds up
+    const int64_t each = n_req * paged_items(max_q, n_heads, p.item);
+    items = items < each ? items : each;
+    const int64_t ctas = 2 * items * (p.item / kPM);
+    const int32_t nt = paged_key_tiles(max_q, max_kv, n_heads, window, p.item);
+    const double tile_us = p.span ? 1.9 : 3.4;
     p.chunk = nt > 0 ? nt : 1;
     double best = 1e30;
     for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
         const int32_t chunk = (nt + s - 1) / s;
         if (s > 1 && paged_splits(nt, chunk) != s) continue;
-        const double waves = double((2 * tiles * s + kPSms - 1) / kPSms);
+        const double waves = double((ctas * s + kPSms - 1) / kPSms);
         double us = waves * (5.0 + tile_us * chunk);
         if (s > 1) us += 4.0 + double(rows) * s * kPD * 4 * 2 / 4e6;
         if (us < best) {
@@ -939,7 +983,7 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
         }
     }
     p.splits = paged_splits(nt, p.chunk);
-    p.grid = 2 * tiles * p.splits;
+    p.grid = ctas * p.splits;
     size_t at = CSA2_STATUS_BYTES;
     p.part_lse = at;
     if (p.splits > 1) at = align256(at + size_t(p.splits) * size_t(rows) * 4);
@@ -1048,6 +1092,7 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.page = page_size;
     a.window = window >= max_kv ? 0 : window;
     a.chunk = plan.chunk;
+    a.item = plan.item;
     a.sm_scale = sm_scale;
     if (plan.span) {
         timer_begin(K_PAGED_DECODE, s);
@@ -1056,7 +1101,8 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
         timer_end(K_PAGED_DECODE, s);
     }
     timer_begin(K_PAGED_ATTN, s);
-    const cudaError_t e = launch(kernel, dim3(unsigned(plan.grid)), plan.span ? kPTileThreads : kPThreads, sizeof(PagedSmem), s, 1, a);
+    const cudaError_t e = launch(kernel, dim3(unsigned(plan.grid)), plan.span ? kPTileThreads : kPThreads, sizeof(PagedSmem), s,
+                                 plan.span ? 2 : 1, a);
     timer_end(K_PAGED_ATTN, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
