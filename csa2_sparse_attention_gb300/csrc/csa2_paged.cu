@@ -167,8 +167,10 @@ struct PagedSmem {
     uint64_t s_full, s_free, p_full, o_done, q_done, drain;
     uint32_t tmem;
     int32_t req, local;
+    PagedReq rq;
 };
 static_assert(sizeof(PagedSmem) + 1024 <= 227 * 1024, "shared memory of the paged attention");
+static_assert(kPM * (kPHalf * 4 + 16) <= 2 * kPN * kPHalf * 2 + kPM * kPN * 2, "the epilogue's rows in the latents' and P's place");
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
@@ -205,6 +207,13 @@ __device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32
         "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(uint16_t(3))
         : "memory");
 }
+// One bulk copy shared memory -> global (addresses and size multiples of 16
+// bytes), and the wait for this thread's copies: written, not only read.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
     if (warp == 0) {
         const int64_t item = blockIdx.x >> (TILES ? 2 : 1);
         int64_t base = 0;
-        int32_t req = -1, local = 0;
+        int32_t req = -1;
         for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
             const int64_t r = r0 + lane;
             int64_t items = 0;
@@ -288,18 +297,20 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             if (hit != 0 && req < 0) {
                 const int src = __ffs(hit) - 1;
                 req = int32_t(r0) + src;
-                local = int32_t(item - base - __shfl_sync(0xffffffffu, inc - items, src));
+                if (lane == src) {
+                    S.local = int32_t(item - base - (inc - items));
+                    S.rq = rq;
+                }
                 if (blockIdx.x != 0) break;  // the first CTA looks at every request
             }
             base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) S.req = req, S.local = local;
+        if (lane == 0) S.req = req;
     }
     __syncthreads();
     if (S.req < 0) return;
     const int64_t req = S.req;
-    PagedReq rq;
-    paged_request(a, req, rq, nullptr);
+    const PagedReq rq = S.rq;
     const int32_t items_r = paged_items(rq.nq, a.heads, a.item);
     const int32_t ns_r = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
     const int32_t it = items_r - 1 - S.local / ns_r, split = S.local % ns_r;
@@ -316,6 +327,26 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
     const int64_t flat0 = int64_t(rq.q0) * a.heads + (n_row > 0 ? int64_t(ti) * kPM : 0);
     const int x_dim = kPHalf * (1 - half), y_dim = kPHalf * half;
 
+    // ---- Q: 8 rows per warp, four lanes per row (64 contiguous bytes an
+    // instruction); the first loads are under way while the CTA sets up
+    constexpr int kQWarps = 8;  // all with decoded tiles, else all but the producers
+    const int q_warp = TILES || warp < kPSoftWarps ? warp : warp - kPProdWarps;
+    const bool q_on = TILES || warp < kPSoftWarps || warp >= kMmaWarp;
+    const int q_groups = (n_row + 7) / 8;  // rows behind the last one stay what they are: they reach no other row
+    constexpr int QN = TILES ? 2 : 1;      // groups whose loads fit into the registers
+    uint4 qv[QN][16];
+    auto q_load = [&](int rg, uint4 (&v)[16]) {
+        const int row = 8 * rg + (lane & 7);
+        const bool on = row < n_row;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (flat0 + (on ? row : 0)) * (kPD * 2)) + (lane >> 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = on ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+    };
+    if (q_on) {
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+            if (q_warp + kQWarps * n < q_groups) q_load(q_warp + kQWarps * n, qv[n]);
+    }
     if (tid == 0) {
         for (int g = 0; g < 2; ++g) {
             for (int b = 0; b < 2; ++b) {
@@ -334,47 +365,71 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
-    // ---- Q to f16 times a power of two per row: 8 rows per warp, four lanes
-    // per row (64 contiguous bytes an instruction).  The other half goes to its
-    // place, the own half by way of the second group of latents into TMEM.
-    for (int rg = warp; rg < kPM / 8; rg += (TILES ? kPTileThreads : kPThreads) / 32) {
-        const int row = 8 * rg + (lane & 7), piece = lane >> 3;
-        const bool on = row < n_row;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (flat0 + (on ? row : 0)) * (kPD * 2)) + piece;
-        uint4 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = on ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-            am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-        }
-        am = max(am & 0xFFFFu, am >> 16);
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
-        int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;  // max |q| 2^-qs in [2^14, 2^15)
-        qs = qs < -100 ? -100 : qs;
-        const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
-        if (piece == 0)
-            S.q_scale[row] = fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), FLT_MIN);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = f16x2(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
-            uint8_t* dst = (i >= 8) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
-            *reinterpret_cast<uint4*>(dst + (row >> 3) * 4096 + (4 * (i & 7) + piece) * 128 + (row & 7) * 16) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        fence_async_smem();
-    }
     tc_fence_before();
     if (TILES) cluster_sync();  // the other CTA's barriers are initialized as well
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
+
+    // ---- decoded tiles: a block of 128 channels is 2 KB of each of 16 key
+    // groups.  Each CTA of the cluster copies half of them into both: without
+    // sharing, 128 KB per key tile and CTA took 7.8 TB/s from L2 and bounded the
+    // kernel.
+    const int64_t tile0 = TILES ? req * a.span + (key0 - paged_base(a, rq)) / kPN : 0;
+    auto copy_block = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
+        __syncwarp();
+        const int kg = rank * (kPN / 16) + lane;
+        if (lane < kPN / 16)
+            bulk_g2s_pair(S.c[g] + kg * 4096 + b * 2048, src + kg * 4096 + b * 2048, 2048, bar);
+        else if (lane == kPN / 16 && fl && rank == 0)
+            bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
+        __syncwarp();
+    };
+    const uint8_t* x_src = a.tiles + tile0 * kPTileBytes + (1 - half) * (kPTileBytes / 2);
+    if (TILES && warp == kMmaWarp + 1 && nt > 0)
+        for (int b = 0; b < 2; ++b) copy_block(&S.full_x[0][b], 0, b, x_src, nullptr);
+
+    // ---- Q to f16 times a power of two per row: the other half to its place, the
+    // own half by way of the second group of latents into TMEM
+    if (q_on) {
+        auto q_store = [&](int rg, const uint4 (&v)[16]) {
+            const int row = 8 * rg + (lane & 7), piece = lane >> 3;
+            uint32_t am = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+                am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+            }
+            am = max(am & 0xFFFFu, am >> 16);
+            am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
+            am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
+            int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;  // max |q| 2^-qs in [2^14, 2^15)
+            qs = qs < -100 ? -100 : qs;
+            const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
+            if (piece == 0)
+                S.q_scale[row] = fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), FLT_MIN);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = f16x2(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
+                uint8_t* dst = (i >= 8) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
+                *reinterpret_cast<uint4*>(dst + (row >> 3) * 4096 + (4 * (i & 7) + piece) * 128 + (row & 7) * 16) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        };
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+            if (q_warp + kQWarps * n < q_groups) q_store(q_warp + kQWarps * n, qv[n]);
+        if (!TILES && q_warp + kQWarps < q_groups) {
+            q_load(q_warp + kQWarps, qv[0]);
+            q_store(q_warp + kQWarps, qv[0]);
+        }
+        fence_async_smem();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kQWarps) : "memory");
+    }
 
     if (warp < kPSoftWarps) {
         if (!TILES) regs_up<kPSoftRegs>();
@@ -410,7 +465,21 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         }
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int32_t j = 0; j < nt; ++j) {
+        if (32 * warp >= n_row) {  // no rows: P stays zero
+            uint8_t* pd = S.p + (row >> 3) * 2048 + (row & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(pd + i * 128) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            for (int32_t j = 0; j < nt; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full, j & 1, a.wlim));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive(&S.s_free);
+                    mbar_arrive(&S.p_full);
+                }
+            }
+        }
+        for (int32_t j = 0; j < nt && 32 * warp < n_row; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full, j & 1, a.wlim));
             if (!ok) break;
             tc_fence_after();
@@ -502,12 +571,17 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
         }
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&S.o_done, 0, a.wlim));
         if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), ti);
-        // ---- epilogue: O / l, the row's 256 channels of the own half
-        if (ok) {
+        // ---- epilogue: O / l, the row's 256 channels of the own half.  The row
+        // is put together in shared memory (the latents' and P's, which the MMAs
+        // are done with) and leaves in one bulk copy: 16-byte stores of a row per
+        // lane took 5400 clocks.
+        if (ok && 32 * warp < n_row) {
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.0f / l;
             const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
             const int64_t flat = flat0 + row;
+            const bool whole = splits == 1;
+            uint8_t* stage = S.c[0] + row * (whole ? kPHalf * 2 + 16 : kPHalf * 4 + 16);
 #pragma unroll 1
             for (int b = 0; b < kPHalf / 32; ++b) {
                 uint32_t o[32];
@@ -518,9 +592,7 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0;
                 }
-                if (!row_on) continue;
-                if (splits == 1) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + (flat * kPD + y_dim + 32 * b) * 2);
+                if (whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -530,21 +602,29 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
                                                                            __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
                             w[e] = *reinterpret_cast<const uint32_t*>(&h);
                         }
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(stage + b * 64 + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(a.part_o + (int64_t(split) * a.rows + flat) * kPD + y_dim + 32 * b);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                        *reinterpret_cast<float4*>(stage + b * 128 + i * 16) =
+                            make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                        __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
                 }
             }
-            if (row_on && half == 0) {
-                if (splits > 1)
-                    a.part_lse[int64_t(split) * a.rows + flat] = lse2;
-                else if (a.lse)
-                    a.lse[flat] = lse2 * 0.6931471805599453f;
+            fence_async_smem();
+            if (row_on) {
+                if (whole)
+                    bulk_s2g(a.out + (flat * kPD + y_dim) * 2, stage, kPHalf * 2);
+                else
+                    bulk_s2g(a.part_o + (int64_t(split) * a.rows + flat) * kPD + y_dim, stage, kPHalf * 4);
+                if (half == 0) {
+                    if (!whole)
+                        a.part_lse[int64_t(split) * a.rows + flat] = lse2;
+                    else if (a.lse)
+                        a.lse[flat] = lse2 * 0.6931471805599453f;
+                }
+                bulk_s2g_wait();
             }
         }
     } else if (!TILES && warp < kPSoftWarps + kPProdWarps) {
@@ -757,38 +837,24 @@ __global__ void __launch_bounds__(SRC == kSrcTiles ? kPTileThreads : kPThreads, 
             mbar_wait(&S.drain, 0, kDrainNs);
         }
         } else if (TILES && warp == kMmaWarp + 1) {
-            // ================= tile copies: a block of 128 channels is 2 KB of each of 16 key groups.  Each CTA of
-            // the cluster copies half of them into both: without sharing, 128 KB per key tile and CTA took 7.8 TB/s
-            // from L2 and bounded the kernel.
-            const uint8_t* x_src = a.tiles + (req * a.span + (key0 - paged_base(a, rq)) / kPN) * kPTileBytes;
-            const uint8_t* y_src = x_src + half * (kPTileBytes / 2);
-            x_src += (1 - half) * (kPTileBytes / 2);
-            const uint8_t* flags = a.flags + (req * a.span + (key0 - paged_base(a, rq)) / kPN) * kPFlagBytes;
+            // ================= tile copies (the first X blocks are under way)
+            const uint8_t* y_src = a.tiles + tile0 * kPTileBytes + half * (kPTileBytes / 2);
+            const uint8_t* flags = a.flags + tile0 * kPFlagBytes;
             bool ok = true;
             int32_t last_x[2][2] = {{-1, -1}, {-1, -1}}, last_y[2][2] = {{-1, -1}, {-1, -1}};  // tiles copied last
-            auto copy = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
-                if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
-                __syncwarp();
-                const int kg = rank * (kPN / 16) + lane;
-                if (lane < kPN / 16)
-                    bulk_g2s_pair(S.c[g] + kg * 4096 + b * 2048, src + kg * 4096 + b * 2048, 2048, bar);
-                else if (lane == kPN / 16 && fl && rank == 0)
-                    bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
-                __syncwarp();
-            };
             for (int32_t j = 0; j < nt && ok; ++j) {
                 const int g = j & 1;
                 const uint32_t ph = (j >> 1) & 1;
                 if (j >= 1)
                     ok = __all_sync(0xffffffffu, j == 1 ? mbar_wait(&S.q_done, 0, a.wlim) : mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
                 for (int b = 0; b < 2 && ok; ++b) {
-                    copy(&S.full_x[g][b], g, b, x_src + j * kPTileBytes, nullptr);
+                    if (j > 0) copy_block(&S.full_x[g][b], g, b, x_src + j * kPTileBytes, nullptr);
                     last_x[g][b] = j;
                 }
                 for (int b = 0; b < 2 && ok; ++b) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_x[g][b], ph, a.wlim));
                     if (!ok) break;
-                    copy(&S.full_y[g][b], g, b, y_src + j * kPTileBytes, b ? flags + j * kPFlagBytes : nullptr);
+                    copy_block(&S.full_y[g][b], g, b, y_src + j * kPTileBytes, b ? flags + j * kPFlagBytes : nullptr);
                     last_y[g][b] = j;
                 }
             }
