@@ -1,0 +1,291 @@
+// Shared by the kernels of the paged attention call: arguments, the requests'
+// work items, small wrappers of instructions, number formats.
+#pragma once
+
+#include "csa2_common.cuh"
+#include "csa2_layout.cuh"
+#include "csa2_tc.cuh"
+
+namespace csa2 {
+
+constexpr int kPD = CSA2_LATENT_DIM;
+constexpr int kPHalf = kPD / 2;       // channels of one half
+constexpr int kPN = 128;              // keys of a tile
+constexpr int kPSoftWarps = 4;
+// Decoded tiles (paged_decode_kernel): per half of the channels [16 key
+// groups][32 chunks of 8 channels][8 keys][16 bytes], f16, as shared memory
+// holds them; and per tile 128 bits of keys without a page, 128 bits of keys
+// with a NaN latent.
+constexpr int64_t kPTileBytes = int64_t(kPN) * kPD * 2;
+constexpr int kPFlagBytes = 32;
+
+struct PagedArgs {
+    const uint8_t* q;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const int32_t* table;
+    uint8_t* out;
+    float* lse;
+    float* part_o;    // [splits][rows][512], each split's normalized output
+    float* part_lse;  // [splits][rows], log2 domain
+    uint8_t* tiles;   // decoded tiles [n_req][span][128 KB], or null
+    uint8_t* flags;   // [n_req][span][32]
+    Status* st;
+    uint64_t wlim;
+    int64_t n_rows_pages;  // pages of the cache
+    int64_t max_pages;
+    int64_t rows;          // n_tokens * heads
+    int64_t n_req;
+    int32_t n_tokens, heads, max_q, max_kv, page, window;
+    int32_t chunk;         // key tiles per split
+    int32_t span;          // decoded tiles per request
+    int32_t item;          // rows of a work item: a row tile, or the two of a cluster (decoded tiles)
+    float sm_scale;
+};
+
+// A request's tokens and entries; false when it is to be skipped.  Problems
+// go to `st` when it is not null.
+struct PagedReq {
+    int32_t q0, nq, len;
+};
+__device__ __forceinline__ bool paged_request(const PagedArgs& a, int64_t r, PagedReq& o, Status* st) {
+    o.q0 = a.q_start[r];
+    const int32_t q1 = a.q_start[r + 1];
+    o.len = a.kv_len[r];
+    if (o.q0 < 0 || q1 < o.q0 || q1 > a.n_tokens || q1 - o.q0 > a.max_q) {
+        if (st) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), q1);
+        return false;
+    }
+    o.nq = q1 - o.q0;
+    if (o.len < 0 || o.len > a.max_kv || o.len > a.max_pages * a.page) {
+        if (st) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), o.len);
+        o.len = 0;
+    }
+    return o.nq > 0;
+}
+__host__ __device__ inline int32_t paged_items(int32_t nq, int32_t heads, int32_t item) { return (nq * heads + item - 1) / item; }
+// Key tiles that a work item of a request can span at most, and its splits.
+__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t heads, int32_t window, int32_t item) {
+    int32_t n = (len + kPN - 1) / kPN;
+    if (window > 0) {
+        const int32_t tok = (item - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
+        const int32_t w = (span + kPN - 1) / kPN + 1;  // and one where the first tile begins early
+        n = n < w ? n : w;
+    }
+    return n;
+}
+__host__ __device__ inline int32_t paged_splits(int32_t tiles, int32_t chunk) {
+    return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+}
+// First key that any token of the request sees, a multiple of 8: where the
+// request's decoded tiles begin.
+__device__ __forceinline__ int32_t paged_base(const PagedArgs& a, const PagedReq& rq) {
+    const int32_t lo = a.window > 0 ? rq.len - rq.nq + 1 - a.window : 0;
+    return lo > 0 ? lo & ~7 : 0;
+}
+// First key (a multiple of 8; with decoded tiles, where one begins), end and
+// key tiles of a work item.
+__device__ __forceinline__ void paged_item_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
+                                                int32_t& end, int32_t& tiles) {
+    const int32_t rows = rq.nq * a.heads, r0 = ti * a.item, r1 = (r0 + a.item < rows ? r0 + a.item : rows) - 1;
+    end = rq.len - rq.nq + r1 / a.heads + 1;
+    int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.heads + 1 - a.window : 0;
+    if (lo < 0) lo = 0;
+    begin = lo & ~7;
+    if (a.tiles != nullptr) {
+        const int32_t base = paged_base(a, rq);
+        begin = base + (begin - base) / kPN * kPN;
+    }
+    tiles = end > begin ? (end - begin + kPN - 1) / kPN : 0;
+}
+
+// The bits of a tile's keys as the softmax reads them.
+struct alignas(32) PagedFlags {
+    uint16_t hidden[8];  // keys without a page, a bit each
+    uint16_t nan[8];     // keys with a NaN latent
+};
+
+// The request and place in it of work item `item`, by a scan of the requests'
+// items in one whole warp; lane 0 gets req < 0 when there are fewer.  `all`:
+// look at every request, so that each one's problems are recorded.
+struct PagedWork {
+    int32_t req, local;
+    PagedReq rq;
+};
+__device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t item, bool all, PagedWork& w) {
+    const int lane = lane_id();
+    int64_t base = 0;
+    int32_t req = -1;
+    for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
+        const int64_t r = r0 + lane;
+        int64_t items = 0;
+        PagedReq rq;
+        if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr))
+            items = int64_t(paged_items(rq.nq, a.heads, a.item)) *
+                    paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
+        int64_t inc = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > item);
+        if (hit != 0 && req < 0) {
+            const int src = __ffs(hit) - 1;
+            req = int32_t(r0) + src;
+            if (lane == src) {
+                w.local = int32_t(item - base - (inc - items));
+                w.rq = rq;
+            }
+            if (!all) break;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) w.req = req;
+}
+
+// A CTA's part of the work: row tile or group, split, key tiles.
+struct PagedPart {
+    int32_t item, split, splits, nt, key0;
+};
+// false: the split does not exist
+__device__ __forceinline__ bool paged_part(const PagedArgs& a, const PagedReq& rq, int32_t local, PagedPart& p) {
+    const int32_t ns = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
+    p.item = paged_items(rq.nq, a.heads, a.item) - 1 - local / ns;  // the ones with the most keys first
+    p.split = local % ns;
+    int32_t begin, end, tiles;
+    paged_item_keys(a, rq, p.item, begin, end, tiles);
+    p.splits = paged_splits(tiles, a.chunk);
+    const int32_t j0 = p.split * a.chunk;
+    p.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;  // 0: nothing to see
+    p.key0 = begin + j0 * kPN;
+    return p.split < p.splits;
+}
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(uint32_t(acc)));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Clusters of two CTAs: a barrier of all their threads; an arrival at the other
+// CTA's mbarrier; a commit and a bulk copy that reach both (same offsets).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t cta) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(cta));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"(uint16_t(3))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(uint16_t(3))
+        : "memory");
+}
+// One bulk copy shared memory -> global (addresses and size multiples of 16
+// bytes), and the wait for this thread's copies: written, not only read.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f32x2_out(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* o) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t* o) {
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+        : "=r"(o[0]), "=r"(o[1]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// nonzero when one of the four E4M3 bytes is NaN (0x7F or 0xFF)
+__device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Q's conversion to f16: 8 rows per warp, four lanes per row, lane piece
+// lane / 8 with 16 bytes of every 64.  The power of two of a row from its
+// maximum, max |q| 2^-qs in [2^14, 2^15): exact for elements above 2^-28 of it.
+__device__ __forceinline__ void paged_q_load(const PagedArgs& a, int64_t flat, bool on, uint4 (&v)[16]) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (on ? flat : 0) * (kPD * 2)) + (lane_id() >> 3);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = on ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ int paged_q_exponent(const uint4 (&v)[16]) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+        am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+    }
+    am = max(am & 0xFFFFu, am >> 16);
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
+    const int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;
+    return qs < -100 ? -100 : qs;
+}
+__device__ __forceinline__ uint4 paged_q_f16(uint4 v, int qs) {
+    const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
+    return make_uint4(f16x2(bf16_lo(v.x) * qf, bf16_hi(v.x) * qf), f16x2(bf16_lo(v.y) * qf, bf16_hi(v.y) * qf),
+                      f16x2(bf16_lo(v.z) * qf, bf16_hi(v.z) * qf), f16x2(bf16_lo(v.w) * qf, bf16_hi(v.w) * qf));
+}
+// The factor of a row's raw logits, log2 domain (never 0: -inf stays -inf).
+__device__ __forceinline__ float paged_q_scale(const PagedArgs& a, int qs) {
+    return fmaxf(a.sm_scale * 1.4426950408889634f * __uint_as_float(uint32_t(127 + qs) << 23), 1.1754944e-38f);
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The kernels of csa2_paged_rows.cu and csa2_paged_tiles.cu, launched on `s`.
+csa2_status paged_rows_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s);
+csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s);
+
+}  // namespace csa2

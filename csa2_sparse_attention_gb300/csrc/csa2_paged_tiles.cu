@@ -1,0 +1,556 @@
+// Causal attention of each request's new tokens over its paged latents.
+//
+//   l_p = sm_scale q . c_p,  o = sum_p softmax(l)_p c_p,  c_p a 512-wide
+//   latent in FP4 (E2M1, one E4M3 scale per 16 channels) or E4M3
+//
+// Rows are (token, head) pairs: 128 consecutive rows of a request make a tile
+// of the tensor cores' M, whatever the number of heads.  All heads share the
+// latents, so a key costs 2048 FLOPs a row against 288 bytes: the tensor cores
+// bound the kernel even for single tokens.
+//
+// The fp32 accumulator of 128 rows x 512 channels would fill TMEM (512
+// columns) and leave no room for the logits, so a CTA takes 128 rows and one
+// half of the output channels ("own", Y) and computes the logits over both
+// halves: 3 products of 256 channels where 2 would do.  (Sharing the logits
+// between two CTAs would move 64 KB of fp32 partial logits per 128 keys over
+// distributed shared memory at 16-24 B/clk per SM: 2700 clocks or more, against
+// the 1060 clocks of tensor time that the third product costs.)
+//
+//   TMEM  [0, 256) O   [256, 384) S   [384, 512) own half of Q, f16
+//   smem  other half of Q (64 KB), two 64 KB groups of latents, P (32 KB)
+//
+// Keys go in tiles of 128: an M = 128 MMA of K = 16 takes 64 clocks for any
+// N up to 128 (measured 64-69) and 128 for N = 256, so S wants 128 keys and O
+// 256 channels at once.  Three roles:
+//   producers (8 warps)  read the rows through the page table and decode them
+//       to f16 (exact) into shared memory, the other half's channels X first,
+//       then, as the logits' MMAs release them, the own half's Y in the same
+//       group.  One copy of Y serves S (K-major) and O (MN-major).
+//   MMA warp, per tile:  S += Q_X X^T, then O += P Y of the previous tile,
+//       then S += Q_Y Y^T: the softmax of a tile runs under the next tile's
+//       S_X, and the decoding of Y under the previous tile's O.
+//   softmax (4 warps, a thread per row)  takes S out of TMEM, keeps the
+//       running maximum and sum in fp32, writes P as f16 to shared memory.  O
+//       is rescaled only when a row's maximum grew by more than 2^8: P stays
+//       below 2^8 and the sums in fp32, so nothing is lost by waiting.
+// P is rounded to f16 (2^-11 relative, an eighth of the step of the bf16
+// output); Q goes to f16 times a power of two per row (exact down to 2^-28 of
+// the row's maximum).
+//
+// Long axes with few rows are split over CTAs in chunks of key tiles that the
+// host sizes; the partial outputs are joined by paged_merge_kernel.
+#include "csa2_paged.cuh"
+#include "csa2_timer.cuh"
+
+#include <atomic>
+
+namespace csa2 {
+
+constexpr int kPM = 128;                            // rows of a tile
+constexpr int kPTileThreads = 32 * (kPSoftWarps + 4);  // softmax, MMA and copy warps (and two that only bring in Q)
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
+
+struct PagedTilesSmem {
+    uint8_t qx[kPM * kPHalf * 2];      // other half of Q, K-major: 8-row groups of 4096 B, 8-channel chunks of 128 B
+    uint8_t c[2][kPN * kPHalf * 2];    // latents: 8-key groups of 4096 B, 8-channel chunks of 128 B
+    uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
+    PagedFlags flags[2];
+    float q_scale[kPM];                // logits' scale of each row (log2 domain)
+    uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2];
+    uint64_t s_full, s_free, p_full, o_done, q_done, drain;
+    uint32_t tmem;
+    PagedWork work;
+};
+static_assert(sizeof(PagedTilesSmem) + 1024 <= 227 * 1024, "shared memory of the paged attention");
+static_assert(kPM * (kPHalf * 4 + 16) <= 2 * kPN * kPHalf * 2 + kPM * kPN * 2, "the epilogue's rows in the latents' and P's place");
+
+// grid: 4 CTAs (two output halves, two row tiles of a cluster) per (pair of row
+// tiles, split), the ones with the most keys first; CTAs beyond the last one
+// leave at once.
+__global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const PagedArgs a) {
+    constexpr int kMmaWarp = kPSoftWarps, kCopyWarp = kPSoftWarps + 1;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    PagedTilesSmem& S = *reinterpret_cast<PagedTilesSmem*>(smem_raw);
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int half = (blockIdx.x >> 1) & 1, rank = blockIdx.x & 1;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 0) paged_find(a, blockIdx.x >> 2, blockIdx.x == 0, S.work);
+    __syncthreads();
+    if (S.work.req < 0) return;
+    const int64_t req = S.work.req;
+    const PagedReq rq = S.work.rq;
+    PagedPart part;
+    if (!paged_part(a, rq, S.work.local, part)) return;
+    const int32_t nt = part.nt, key0 = part.key0, split = part.split, splits = part.splits;
+    // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
+    const int32_t ti = 2 * part.item + rank;
+    const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
+    const int64_t flat0 = int64_t(rq.q0) * a.heads + (n_row > 0 ? int64_t(ti) * kPM : 0);
+    const int y_dim = kPHalf * half;
+
+    // ---- Q: two groups of 8 rows per warp; the loads are under way while the CTA sets up
+    const int q_groups = (n_row + 7) / 8;  // rows behind the last one stay what they are: they reach no other row
+    uint4 qv[2][16];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int row = 8 * (warp + 8 * n) + (lane & 7);
+        if (warp + 8 * n < q_groups) paged_q_load(a, flat0 + row, row < n_row, qv[n]);
+    }
+    if (tid == 0) {
+        for (int g = 0; g < 2; ++g) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&S.full_x[g][b], 1);
+                mbar_init(&S.full_y[g][b], 1);
+                mbar_init(&S.empty_x[g][b], 2);  // both CTAs' MMAs
+            }
+            mbar_init(&S.empty_o[g], 2);
+        }
+        mbar_init(&S.s_full, 1);
+        mbar_init(&S.s_free, kPSoftWarps);
+        mbar_init(&S.p_full, kPSoftWarps);
+        mbar_init(&S.o_done, 1);
+        mbar_init(&S.q_done, 2 * kPSoftWarps);
+        mbar_init(&S.drain, 2);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
+    tc_fence_before();
+    cluster_sync();  // the other CTA's barriers are initialized as well
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+
+    // ---- decoded tiles: a block of 128 channels is 2 KB of each of 16 key
+    // groups.  Each CTA of the cluster copies half of them into both: without
+    // sharing, 128 KB per key tile and CTA took 7.8 TB/s from L2 and bounded the
+    // kernel.
+    const int64_t tile0 = req * a.span + (key0 - paged_base(a, rq)) / kPN;
+    auto copy_block = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
+        __syncwarp();
+        const int kg = rank * (kPN / 16) + lane;
+        if (lane < kPN / 16)
+            bulk_g2s_pair(S.c[g] + kg * 4096 + b * 2048, src + kg * 4096 + b * 2048, 2048, bar);
+        else if (lane == kPN / 16 && fl && rank == 0)
+            bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
+        __syncwarp();
+    };
+    const uint8_t* x_src = a.tiles + tile0 * kPTileBytes + (1 - half) * (kPTileBytes / 2);
+    if (warp == kCopyWarp && nt > 0)
+        for (int b = 0; b < 2; ++b) copy_block(&S.full_x[0][b], 0, b, x_src, nullptr);
+
+    // ---- Q to f16 times a power of two per row: the other half to its place, the
+    // own half by way of the second group of latents into TMEM
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        if (warp + 8 * n >= q_groups) continue;
+        const int row = 8 * (warp + 8 * n) + (lane & 7), piece = lane >> 3;
+        const int qs = paged_q_exponent(qv[n]);
+        if (piece == 0) S.q_scale[row] = paged_q_scale(a, qs);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            uint8_t* dst = (i >= 8) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
+            *reinterpret_cast<uint4*>(dst + (row >> 3) * 4096 + (4 * (i & 7) + piece) * 128 + (row & 7) * 16) =
+                paged_q_f16(qv[n][i], qs);
+        }
+    }
+    fence_async_smem();
+    __syncthreads();
+
+    if (warp < kPSoftWarps) {
+        // ================= softmax: row = TMEM lane = thread
+        const int row = tid;
+        const uint32_t tm = tmem + (uint32_t(32 * warp) << 16);
+        const bool row_on = row < n_row;
+        const float sm_eff = S.q_scale[row];
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {  // the own half of Q into TMEM, 64 channels at a time
+            uint32_t o[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(S.c[1] + (row >> 3) * 4096 + (8 * b + i) * 128 + (row & 7) * 16);
+                o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+            }
+            tmem_st32(tm + kColQ + 32 * b, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&S.q_done);  // the second group of latents may be filled
+            mbar_arrive_peer(&S.q_done, rank ^ 1);
+            mbar_arrive(&S.s_free);  // phase 0: Q is in place
+        }
+
+        // ---- key tiles
+        int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys
+        if (row_on) {
+            hi_r = rq.len - rq.nq + (ti * kPM + row) / a.heads + 1;
+            lo_r = a.window > 0 ? hi_r - a.window : 0;
+        }
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        if (32 * warp >= n_row) {  // no rows: P stays zero
+            uint8_t* pd = S.p + (row >> 3) * 2048 + (row & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(pd + i * 128) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            for (int32_t j = 0; j < nt; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full, j & 1, a.wlim));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive(&S.s_free);
+                    mbar_arrive(&S.p_full);
+                }
+            }
+        }
+        for (int32_t j = 0; j < nt && 32 * warp < n_row; ++j) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full, j & 1, a.wlim));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(tm + kColS + 32 * b, s[b]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.s_free);  // phase j + 1: S may be overwritten
+            const int32_t c0 = key0 + j * kPN;
+            const int g = j & 1;
+            const uint4 hid = *reinterpret_cast<const uint4*>(S.flags[g].hidden);
+            const uint4 n4 = *reinterpret_cast<const uint4*>(S.flags[g].nan);
+            const uint32_t hidden[4] = {hid.x, hid.y, hid.z, hid.w}, nan[4] = {n4.x, n4.y, n4.z, n4.w};
+            if (__any_sync(0xffffffffu, c0 < lo_r || c0 + kPN > hi_r) ||
+                (hidden[0] | hidden[1] | hidden[2] | hidden[3] | nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
+                const int32_t lo = lo_r - c0, hi = hi_r - c0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    // bits of the block's columns in [lo, hi) that have a page
+                    const int32_t l0 = lo - 32 * b, h0 = hi - 32 * b;
+                    uint32_t see = l0 >= 32 || h0 <= 0 ? 0u : ~hidden[b];
+                    if (l0 > 0 && l0 < 32) see &= 0xFFFFFFFFu << l0;
+                    if (h0 > 0 && h0 < 32) see &= 0xFFFFFFFFu >> (32 - h0);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if ((nan[b] >> i) & 1u) s[b][i] = 0x7FC00000u;
+                        if (!((see >> i) & 1u)) s[b][i] = 0xFF800000u;
+                    }
+                }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(s[b][i]), __uint_as_float(s[b][i + 1])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sm_eff;
+            const bool grew = top > m + 8.f;
+            if (__any_sync(0xffffffffu, grew)) {
+                const float mn = grew ? top : m;
+                const float alpha = !grew ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
+                if (j > 0) {  // every MMA before S_Y of this tile is done, the previous O among them
+#pragma unroll 1
+                    for (int b = 0; b < kPHalf / 32; ++b) {
+                        uint32_t o[32];
+                        tmem_ld32(tm + kColO + 32 * b, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tm + kColO + 32 * b, o);
+                    }
+                    tmem_st_wait();
+                }
+                l *= alpha;
+                m = mn;
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            const uint64_t sm2 = f32x2(sm_eff, sm_eff), mu2 = f32x2(-mu, -mu);
+            uint64_t acc[4] = {0, 0, 0, 0};
+            uint8_t* pd = S.p + (row >> 3) * 2048 + (row & 7) * 16;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x, y;
+                        f32x2_out(fma2(f32x2(__uint_as_float(s[b][8 * i + 2 * e]), __uint_as_float(s[b][8 * i + 2 * e + 1])), sm2, mu2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        acc[e] = add2(acc[e], f32x2(x, y));
+                        w[e] = f16x2(x, y);
+                    }
+                    *reinterpret_cast<uint4*>(pd + (4 * b + i) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            {
+                float x, y;
+                f32x2_out(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), x, y);
+                l += x + y;
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full);
+        }
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&S.o_done, 0, a.wlim));
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), ti);
+        // ---- epilogue: O / l, the row's 256 channels of the own half.  The row
+        // is put together in shared memory (the latents' and P's, which the MMAs
+        // are done with) and leaves in one bulk copy: 16-byte stores of a row per
+        // lane took 5400 clocks.
+        if (ok && 32 * warp < n_row) {
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+            const int64_t flat = flat0 + row;
+            const bool whole = splits == 1;
+            uint8_t* stage = S.c[0] + row * (whole ? kPHalf * 2 + 16 : kPHalf * 4 + 16);
+#pragma unroll 1
+            for (int b = 0; b < kPHalf / 32; ++b) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld32(tm + kColO + 32 * b, o);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                                           __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        *reinterpret_cast<uint4*>(stage + b * 64 + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4*>(stage + b * 128 + i * 16) =
+                            make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                        __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                }
+            }
+            fence_async_smem();
+            if (row_on) {
+                if (whole)
+                    bulk_s2g(a.out + (flat * kPD + y_dim) * 2, stage, kPHalf * 2);
+                else
+                    bulk_s2g(a.part_o + (int64_t(split) * a.rows + flat) * kPD + y_dim, stage, kPHalf * 4);
+                if (half == 0) {
+                    if (!whole)
+                        a.part_lse[int64_t(split) * a.rows + flat] = lse2;
+                    else if (a.lse)
+                        a.lse[flat] = lse2 * kLn2;
+                }
+                bulk_s2g_wait();
+            }
+        }
+    } else if (tid == 32 * kMmaWarp) {
+        // ================= MMA issue
+        constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, kPHalf, 0, false, true);
+        // descriptors; a step of 16 along K is 256 bytes (K-major) or two 8-key groups (MN-major)
+        const uint64_t dq0 = umma_desc(smem_u32(S.qx), 128, 4096), dp0 = umma_desc(smem_u32(S.p), 128, 2048);
+        const uint64_t dk[2] = {umma_desc(smem_u32(S.c[0]), 128, 4096), umma_desc(smem_u32(S.c[1]), 128, 4096)};
+        const uint64_t dv[2] = {umma_desc(smem_u32(S.c[0]), 4096, 128), umma_desc(smem_u32(S.c[1]), 4096, 128)};
+        // (a value the compiler cannot know: it would keep every step's descriptor of the loop in registers, and spill)
+        auto fresh = [](uint64_t v) {
+            asm volatile("" : "+l"(v));
+            return v;
+        };
+        bool ok = true;
+        auto o_mma = [&](int32_t j) {  // O += P Y of tile j
+            ok = ok && mbar_wait(&S.p_full, j & 1, a.wlim);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t d = fresh(j & 1 ? dv[1] : dv[0]), dp = fresh(dp0);
+#pragma unroll
+            for (int k = 0; k < kPN / 16; ++k)
+                mma_f16_ss(tmem + kColO, dp + k * (256 >> 4), d + k * (8192 >> 4), id_o, k > 0 || j > 0);
+        };
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            const int g = j & 1;
+            const uint32_t ph = (j >> 1) & 1;
+            uint64_t d = fresh(g ? dk[1] : dk[0]), dq = fresh(dq0);
+            ok = mbar_wait(&S.s_free, j & 1, a.wlim);  // phase 0: Q; phase j: S of the tile before has been read
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && mbar_wait(&S.full_x[g][b], ph, a.wlim);
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + (8 * b + k) * (256 >> 4), id_s, k > 0 || b > 0);
+                tc_commit_pair(&S.empty_x[g][b]);
+            }
+            if (ok && j > 0) {
+                o_mma(j - 1);
+                // (only what a producer waits for: an arrival at the other CTA must not outlive it)
+                if (ok && j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1]);
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && mbar_wait(&S.full_y[g][b], ph, a.wlim);
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * (8 * b + k), d + (8 * b + k) * (256 >> 4), id_s, true);
+            }
+            if (ok) tc_commit(&S.s_full);
+        }
+        if (nt > 0) {
+            if (ok) o_mma(nt - 1);
+            if (ok) tc_commit(&S.o_done);
+            if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), ti);
+            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done (in a cluster:
+            // until both CTAs' commits have arrived here)
+            tc_commit_pair(&S.drain);
+            mbar_wait(&S.drain, 0, kDrainNs);
+        }
+    } else if (warp == kCopyWarp) {
+        // ================= tile copies (the first X blocks are under way)
+        const uint8_t* y_src = a.tiles + tile0 * kPTileBytes + half * (kPTileBytes / 2);
+        const uint8_t* flags = a.flags + tile0 * kPFlagBytes;
+        bool ok = true;
+        int32_t last_x[2][2] = {{-1, -1}, {-1, -1}}, last_y[2][2] = {{-1, -1}, {-1, -1}};  // tiles copied last
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            const int g = j & 1;
+            const uint32_t ph = (j >> 1) & 1;
+            if (j >= 1)
+                ok = __all_sync(0xffffffffu, j == 1 ? mbar_wait(&S.q_done, 0, a.wlim) : mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
+            for (int b = 0; b < 2 && ok; ++b) {
+                if (j > 0) copy_block(&S.full_x[g][b], g, b, x_src + j * kPTileBytes, nullptr);
+                last_x[g][b] = j;
+            }
+            for (int b = 0; b < 2 && ok; ++b) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_x[g][b], ph, a.wlim));
+                if (!ok) break;
+                copy_block(&S.full_y[g][b], g, b, y_src + j * kPTileBytes, b ? flags + j * kPFlagBytes : nullptr);
+                last_y[g][b] = j;
+            }
+        }
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 9, int32_t(req), ti);
+        // every copy lands before the CTA leaves its shared memory, also after a give-up
+        for (int g = 0; g < 2; ++g)
+            for (int b = 0; b < 2; ++b) {
+                if (last_x[g][b] >= 0) mbar_wait(&S.full_x[g][b], (last_x[g][b] >> 1) & 1, kDrainNs);
+                if (last_y[g][b] >= 0) mbar_wait(&S.full_y[g][b], (last_y[g][b] >> 1) & 1, kDrainNs);
+            }
+    }
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while the other may copy or arrive here
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Decodes the pages of every request once into tiles of 128 keys (see
+// kSrcTiles), for calls whose requests have several row tiles: each of them
+// would decode every key again, and the decoding, not the MMAs, bounds the
+// kernel then (12,600 warp instructions a key tile).  grid (tiles, requests).
+template <bool FP8>
+__global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
+    __shared__ uint32_t s_nan[4], s_hidden[4];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t req = blockIdx.y;
+    PagedReq rq;
+    if (!paged_request(a, req, rq, nullptr)) return;
+    const int32_t base = paged_base(a, rq) + int32_t(blockIdx.x) * kPN;
+    if (base >= rq.len) return;
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, k8 = lane & 7, piece = lane >> 3;
+    uint8_t* tile = a.tiles + (req * a.span + blockIdx.x) * kPTileBytes;
+    if (tid < 4) s_nan[tid] = s_hidden[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // key groups of 8: 2 warp + i; a lane has 16 bytes of every 64
+        const int kg = 2 * warp + i, key = 8 * kg + k8;
+        const int32_t p = base + key;
+        int64_t row = -1;
+        if (p < rq.len) {
+            const int32_t id = a.table[req * a.max_pages + p / a.page];
+            if (id >= 0 && id < a.n_rows_pages)
+                row = int64_t(id) * a.page + p % a.page;
+            else if (piece == 0)
+                record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+        }
+        uint32_t bad = 0;
+        constexpr int NP = FP8 ? 8 : 4;  // 64-byte parts of a row
+        uint4 v[NP];
+        uint4 sc[2];
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+            v[e] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.codes + row * (FP8 ? kPD : kPD / 2) + 64 * e) + piece)
+                            : make_uint4(0, 0, 0, 0);
+        sc[0] = sc[1] = make_uint4(0, 0, 0, 0);
+        if (!FP8 && row >= 0) {
+            sc[0] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)));
+            sc[1] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)) + 1);
+        }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+            // channels: FP4 128 e + 32 piece .. + 31, FP8 64 e + 16 piece .. + 15
+            constexpr int NC = FP8 ? 2 : 4;
+            const int chunk = FP8 ? 8 * e + 2 * piece : 16 * e + 4 * piece;
+            uint8_t* dst = tile + (chunk >> 5) * (kPTileBytes / 2) + kg * 4096 + (chunk & 31) * 128 + k8 * 16;
+            uint32_t o[4 * NC];
+            if (FP8) {
+                const uint32_t n4 = e4m3_nan4(w[0]) | e4m3_nan4(w[1]) | e4m3_nan4(w[2]) | e4m3_nan4(w[3]);
+                bad |= n4;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) e4m3x4_f16(n4 ? 0u : w[m], o + 2 * m);
+            } else {
+                const uint32_t* s8 = &sc[0].x + 2 * e;  // the 8 scales of 128 channels
+                const uint32_t s2 = ((piece & 2 ? s8[1] : s8[0]) >> (16 * (piece & 1))) & 0xFFFFu;
+                const uint32_t n2 = e4m3_nan4(s2);
+                bad |= n2;
+                uint32_t ss[2];
+                e4m3x4_f16(n2 ? 0u : s2, ss);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t s = __byte_perm(ss[0], 0, m >= 2 ? 0x3232 : 0x1010);
+                    e2m1x8_f16(w[m], o + (4 * m) % (4 * NC));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[(4 * m + q) % (4 * NC)] = mul_f16x2(o[(4 * m + q) % (4 * NC)], s);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+        if (bad) atomicOr(&s_nan[key >> 5], 1u << (key & 31));
+        if (row < 0) atomicOr(&s_hidden[key >> 5], 1u << (key & 31));
+    }
+    __syncthreads();
+    uint32_t* fl = reinterpret_cast<uint32_t*>(a.flags + (req * a.span + blockIdx.x) * kPFlagBytes);
+    if (tid < 4) fl[tid] = s_hidden[tid], fl[4 + tid] = s_nan[tid];
+}
+
+csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(paged_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(sizeof(PagedTilesSmem))) != cudaSuccess)
+            return CSA2_ERR_CUDA;
+        done[dev].store(true, std::memory_order_release);
+    }
+    timer_begin(K_PAGED_DECODE, s);
+    const cudaError_t e1 = launch(fp8 ? paged_decode_kernel<true> : paged_decode_kernel<false>,
+                                  dim3(unsigned(a.span), unsigned(a.n_req)), 256, 0, s, 1, a);
+    timer_end(K_PAGED_DECODE, s);
+    if (e1 != cudaSuccess) return CSA2_ERR_CUDA;
+    timer_begin(K_PAGED_ATTN, s);
+    const cudaError_t e2 = launch(paged_tiles_kernel, dim3(grid), kPTileThreads, sizeof(PagedTilesSmem), s, 2, a);
+    timer_end(K_PAGED_ATTN, s);
+    return e2 == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+}  // namespace csa2
