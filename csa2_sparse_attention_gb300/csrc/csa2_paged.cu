@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     const int64_t row = int64_t(blockIdx.x) * 2 + (threadIdx.x >> 7);
     const int t = threadIdx.x & 127;
     if (row >= a.rows) return;
-    const int32_t tok = int32_t(row / a.heads);
+    const int32_t tok = int32_t(row) / a.by_heads;
     int64_t lo = 0, hi = a.n_req;  // the last request that starts at or before the token
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) / 2;
@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     PagedReq rq;
     if (!paged_request(a, lo, rq, nullptr) || tok < rq.q0 || tok >= rq.q0 + rq.nq) return;
     int32_t begin, end, tiles;
-    paged_item_keys(a, rq, int32_t((row - int64_t(rq.q0) * a.heads) / a.item), begin, end, tiles);
-    const int32_t splits = paged_splits(tiles, a.chunk);
+    paged_item_keys(a, rq, int32_t(row - int64_t(rq.q0) * a.heads) >> a.item_log2, begin, end, tiles);
+    const int32_t splits = paged_splits(a, tiles);
     if (splits == 1) return;
     float m = -INFINITY;
     for (int32_t s = 0; s < splits; ++s) m = fmaxf(m, a.part_lse[s * a.rows + row]);
@@ -90,13 +90,13 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     const int64_t each = n_req * paged_items(max_q, n_heads, p.item);
     items = items < each ? items : each;
     ctas *= items;
-    const int32_t nt = paged_key_tiles(max_q, max_kv, n_heads, window, p.item);
+    const int32_t nt = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, p.item));
     const double tile_us = p.span ? 1.9 : 2.9;
     p.chunk = nt > 0 ? nt : 1;
     double best = 1e30;
     for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
         const int32_t chunk = (nt + s - 1) / s;
-        if (s > 1 && paged_splits(nt, chunk) != s) continue;
+        if (s > 1 && (nt + chunk - 1) / chunk != s) continue;
         const double waves = double((ctas * s + kPSms - 1) / kPSms);
         double us = waves * (8.0 + tile_us * chunk);
         if (s > 1) us += 4.0 + double(rows) * s * kPD * 4 * 2 / 4e6;
@@ -105,7 +105,7 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
             p.chunk = chunk > 0 ? chunk : 1;
         }
     }
-    p.splits = paged_splits(nt, p.chunk);
+    p.splits = nt > p.chunk ? (nt + p.chunk - 1) / p.chunk : 1;
     p.grid = ctas * p.splits;
     size_t at = CSA2_STATUS_BYTES;
     p.part_lse = at;
@@ -192,6 +192,11 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.window = window >= max_kv ? 0 : window;
     a.chunk = plan.chunk;
     a.item = plan.item;
+    a.item_log2 = plan.item == 64 ? 6 : 8;
+    a.item_tokens = paged_item_tokens(n_heads, plan.item);
+    a.by_heads = fast_div(uint32_t(n_heads));
+    a.by_page = fast_div(uint32_t(page_size));
+    a.by_chunk = fast_div(uint32_t(plan.chunk));
     a.sm_scale = sm_scale;
     const bool fp8 = fmt == CSA2_FMT_FP8;
     const csa2_status e = plan.span ? paged_tiles_launch(a, fp8, unsigned(plan.grid), s)

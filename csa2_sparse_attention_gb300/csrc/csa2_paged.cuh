@@ -19,6 +19,26 @@ constexpr int kPSoftWarps = 4;
 constexpr int64_t kPTileBytes = int64_t(kPN) * kPD * 2;
 constexpr int kPFlagBytes = 32;
 
+// n / d for 0 <= n < 2^31 by a multiplication: mul = floor(2^(31 + s) / d) + 1
+// with 2^s >= d overshoots 1 / d by less than 2^-31 d / 2^31 of n's step.  (The
+// set-up of a CTA runs once through code that the instruction cache does not
+// hold: a division by an unknown number is 25 instructions, this is three.)
+struct FastDiv {
+    uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 31};
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    f.mul = uint32_t((uint64_t(1) << (31 + s)) / d + 1);
+    f.shift = 31 + s;
+    return f;
+}
+__device__ __forceinline__ int32_t operator/(int32_t n, const FastDiv& f) {
+    return int32_t((uint64_t(uint32_t(n)) * f.mul) >> f.shift);
+}
+__device__ __forceinline__ int32_t ceil_by(int32_t n, const FastDiv& f) { return (n + int32_t(f.d) - 1) / f; }
+
 struct PagedArgs {
     const uint8_t* q;
     const int32_t* q_start;
@@ -40,8 +60,10 @@ struct PagedArgs {
     int64_t n_req;
     int32_t n_tokens, heads, max_q, max_kv, page, window;
     int32_t chunk;         // key tiles per split
+    FastDiv by_heads, by_page, by_chunk;
     int32_t span;          // decoded tiles per request
-    int32_t item;          // rows of a work item: a row tile, or the two of a cluster (decoded tiles)
+    int32_t item;          // rows of a work item: 64, or the 256 of a cluster's two tiles (decoded tiles); 2^item_log2
+    int32_t item_log2, item_tokens;
     float sm_scale;
 };
 
@@ -65,20 +87,25 @@ __device__ __forceinline__ bool paged_request(const PagedArgs& a, int64_t r, Pag
     }
     return o.nq > 0;
 }
-__host__ __device__ inline int32_t paged_items(int32_t nq, int32_t heads, int32_t item) { return (nq * heads + item - 1) / item; }
-// Key tiles that a work item of a request can span at most, and its splits.
-__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t heads, int32_t window, int32_t item) {
+// Work items of a request; key tiles that one can span at most; its splits.
+__host__ __device__ inline int32_t paged_items(int32_t nq, int32_t heads, int32_t item) {
+    return (nq * heads + item - 1) / item;
+}
+__host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int32_t window, int32_t item_tokens) {
     int32_t n = (len + kPN - 1) / kPN;
     if (window > 0) {
-        const int32_t tok = (item - 1) / heads + 2, span = window + (nq < tok ? nq : tok) + 7;
+        const int32_t span = window + (nq < item_tokens ? nq : item_tokens) + 7;
         const int32_t w = (span + kPN - 1) / kPN + 1;  // and one where the first tile begins early
         n = n < w ? n : w;
     }
     return n;
 }
-__host__ __device__ inline int32_t paged_splits(int32_t tiles, int32_t chunk) {
-    return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+// Tokens that an item's rows can belong to at most.
+inline int32_t paged_item_tokens(int32_t heads, int32_t item) { return (item - 1) / heads + 2; }
+__device__ __forceinline__ int32_t paged_splits(const PagedArgs& a, int32_t tiles) {
+    return tiles > a.chunk ? ceil_by(tiles, a.by_chunk) : 1;
 }
+
 // First key that any token of the request sees, a multiple of 8: where the
 // request's decoded tiles begin.
 __device__ __forceinline__ int32_t paged_base(const PagedArgs& a, const PagedReq& rq) {
@@ -90,8 +117,8 @@ __device__ __forceinline__ int32_t paged_base(const PagedArgs& a, const PagedReq
 __device__ __forceinline__ void paged_item_keys(const PagedArgs& a, const PagedReq& rq, int32_t ti, int32_t& begin,
                                                 int32_t& end, int32_t& tiles) {
     const int32_t rows = rq.nq * a.heads, r0 = ti * a.item, r1 = (r0 + a.item < rows ? r0 + a.item : rows) - 1;
-    end = rq.len - rq.nq + r1 / a.heads + 1;
-    int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.heads + 1 - a.window : 0;
+    end = rq.len - rq.nq + r1 / a.by_heads + 1;
+    int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.by_heads + 1 - a.window : 0;
     if (lo < 0) lo = 0;
     begin = lo & ~7;
     if (a.tiles != nullptr) {
@@ -107,61 +134,61 @@ struct alignas(32) PagedFlags {
     uint16_t nan[8];     // keys with a NaN latent
 };
 
-// The request and place in it of work item `item`, by a scan of the requests'
-// items in one whole warp; lane 0 gets req < 0 when there are fewer.  `all`:
-// look at every request, so that each one's problems are recorded.
+// A CTA's part of the work: request, item of it, split, key tiles.
 struct PagedWork {
-    int32_t req, local;
     PagedReq rq;
+    int32_t req;                 // -1: none
+    int32_t item, split, splits;
+    int32_t nt, key0;            // key tiles (0: nothing to see) and the first key
 };
-__device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t item, bool all, PagedWork& w) {
+// Finds it for the grid's `place`, in one whole warp (by a scan of the requests'
+// items), into shared memory.  `all`: look at every request, so that each one's
+// problems are recorded.
+__device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bool all, PagedWork& w) {
     const int lane = lane_id();
     int64_t base = 0;
-    int32_t req = -1;
+    bool found = false;
+    if (lane == 0) w.req = -1;
+    __syncwarp();
+#pragma unroll 1
     for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
         const int64_t r = r0 + lane;
-        int64_t items = 0;
+        int32_t n = 0, ns = 1;
         PagedReq rq;
-        if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr))
-            items = int64_t(paged_items(rq.nq, a.heads, a.item)) *
-                    paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
-        int64_t inc = items;
+        if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr)) {
+            ns = paged_splits(a, paged_key_tiles(rq.nq, rq.len, a.window, a.item_tokens));
+            n = (rq.nq * a.heads + a.item - 1) >> a.item_log2;
+        }
+        int64_t inc = int64_t(n) * ns;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += u;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > item);
-        if (hit != 0 && req < 0) {
-            const int src = __ffs(hit) - 1;
-            req = int32_t(r0) + src;
-            if (lane == src) {
-                w.local = int32_t(item - base - (inc - items));
-                w.rq = rq;
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > place);
+        if (hit != 0 && !found) {
+            found = true;
+            if (lane == __ffs(hit) - 1) {
+                const uint32_t local = uint32_t(place - base - (inc - int64_t(n) * ns));
+                const uint32_t back = local / uint32_t(ns);
+                const int32_t item = n - 1 - int32_t(back), split = int32_t(local - back * ns);  // the most keys first
+                int32_t begin, end, tiles;
+                paged_item_keys(a, rq, item, begin, end, tiles);
+                const int32_t splits = paged_splits(a, tiles), j0 = split * a.chunk;
+                if (split < splits) {
+                    w.rq = rq;
+                    w.req = int32_t(r);
+                    w.item = item;
+                    w.split = split;
+                    w.splits = splits;
+                    w.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;
+                    w.key0 = begin + j0 * kPN;
+                }
             }
             if (!all) break;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) w.req = req;
-}
-
-// A CTA's part of the work: row tile or group, split, key tiles.
-struct PagedPart {
-    int32_t item, split, splits, nt, key0;
-};
-// false: the split does not exist
-__device__ __forceinline__ bool paged_part(const PagedArgs& a, const PagedReq& rq, int32_t local, PagedPart& p) {
-    const int32_t ns = paged_splits(paged_key_tiles(rq.nq, rq.len, a.heads, a.window, a.item), a.chunk);
-    p.item = paged_items(rq.nq, a.heads, a.item) - 1 - local / ns;  // the ones with the most keys first
-    p.split = local % ns;
-    int32_t begin, end, tiles;
-    paged_item_keys(a, rq, p.item, begin, end, tiles);
-    p.splits = paged_splits(tiles, a.chunk);
-    const int32_t j0 = p.split * a.chunk;
-    p.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;  // 0: nothing to see
-    p.key0 = begin + j0 * kPN;
-    return p.split < p.splits;
 }
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
@@ -251,9 +278,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // nonzero when one of the four E4M3 bytes is NaN (0x7F or 0xFF)
 __device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Q's conversion to f16: 8 rows per warp, four lanes per row, lane piece
-// lane / 8 with 16 bytes of every 64.  The power of two of a row from its
-// maximum, max |q| 2^-qs in [2^14, 2^15): exact for elements above 2^-28 of it.
+// Q's conversion to f16: 8 rows per warp, four lanes per row, lane / 8 with 16
+// bytes of every 64.  The power of two of a row from its maximum, max |q| 2^-qs
+// in [2^14, 2^15): exact for elements above 2^-28 of it.
 __device__ __forceinline__ void paged_q_load(const PagedArgs& a, int64_t flat, bool on, uint4 (&v)[16]) {
     const uint4* src = reinterpret_cast<const uint4*>(a.q + (on ? flat : 0) * (kPD * 2)) + (lane_id() >> 3);
 #pragma unroll

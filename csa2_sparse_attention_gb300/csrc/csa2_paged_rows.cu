@@ -98,53 +98,57 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == 0) paged_find(a, blockIdx.x, blockIdx.x == 0, S.work);
-    __syncthreads();
-    if (S.work.req < 0) return;
-    const int64_t req = S.work.req;
-    const PagedReq rq = S.work.rq;
-    PagedPart part;
-    if (!paged_part(a, rq, S.work.local, part)) return;
-    const int32_t nt = part.nt, key0 = part.key0, split = part.split, splits = part.splits;
-    const int32_t row0 = part.item * kRRows;  // of the request
-    const int32_t n_row = rq.nq * a.heads - row0 < kRRows ? rq.nq * a.heads - row0 : kRRows;
-    const int64_t flat0 = int64_t(rq.q0) * a.heads + row0;
-    const int32_t k_end = rq.len - rq.nq + (row0 + n_row - 1) / a.heads + 1;
-    const int32_t k_last = key0 + nt * kPN < k_end ? key0 + nt * kPN : k_end;  // end of this CTA's keys
-
-    // ---- Q by the warps that do not bring in latents, one group of 8 rows each
-    const bool q_on = warp < kPSoftWarps || warp >= kRMmaWarp;
-    const int q_group = warp < kPSoftWarps ? warp : warp - kRProdWarps, q_row = 8 * q_group + (lane & 7);
-    uint4 qv[16];
-    if (q_on) paged_q_load(a, flat0 + q_row, q_row < n_row, qv);
-    if (tid == 0) {
-        for (int b = 0; b < 4; ++b) {
-            mbar_init(&S.full[b], kRProdWarps);
-            mbar_init(&S.empty[b], 1);
+    if (warp == 0) {
+        paged_find(a, blockIdx.x, blockIdx.x == 0, S.work);
+    } else if (warp == kRMmaWarp) {
+        if (lane == 0) {
+            for (int b = 0; b < 4; ++b) {
+                mbar_init(&S.full[b], kRProdWarps);
+                mbar_init(&S.empty[b], 1);
+            }
+            mbar_init(&S.s_full, 1);
+            mbar_init(&S.p_full, kPSoftWarps);
+            mbar_init(&S.o_done, 1);
+            mbar_init(&S.drain, 1);
+            mbar_init_fence();
         }
-        mbar_init(&S.s_full, 1);
-        mbar_init(&S.p_full, kPSoftWarps);
-        mbar_init(&S.o_done, 1);
-        mbar_init(&S.drain, 1);
-        mbar_init_fence();
-        S.fresh = n_row;
+        __syncwarp();
+        tmem_alloc(&S.tmem, 512);
+        tc_fence_before();
     }
-    if (warp == kRMmaWarp) tmem_alloc(&S.tmem, 512);
-    tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    if (q_on) {
-        const int qs = paged_q_exponent(qv), piece = lane >> 3;
+    const int64_t req = S.work.req;
+    const PagedReq rq = S.work.rq;
+    if (req < 0) {
+        if (warp == kRMmaWarp) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const int32_t nt = S.work.nt, key0 = S.work.key0, split = S.work.split, splits = S.work.splits;
+    const int32_t row0 = S.work.item * kRRows;  // of the request
+    const int32_t n_row = rq.nq * a.heads - row0 < kRRows ? rq.nq * a.heads - row0 : kRRows;
+    const int64_t flat0 = int64_t(rq.q0) * a.heads + row0;
+    const int32_t k_end = rq.len - rq.nq + (row0 + n_row - 1) / a.by_heads + 1;
+    const int32_t k_last = key0 + nt * kPN < k_end ? key0 + nt * kPN : k_end;  // end of this CTA's keys
+
+    // ---- Q by the warps that do not bring in latents, one group of 8 rows each
+    if (warp < kPSoftWarps || warp >= kRMmaWarp) {
+        const int row = 8 * (warp < kPSoftWarps ? warp : warp - kRProdWarps) + (lane & 7), piece = lane >> 3;
+        const bool on = row < n_row;
+        uint4 v[16];
+        paged_q_load(a, flat0 + row, on, v);
+        const int qs = paged_q_exponent(v);
         if (piece == 0) {
-            S.row[q_row] = make_float2(paged_q_scale(a, qs), 0.f);
+            S.row[row] = make_float2(paged_q_scale(a, qs), 0.f);
             // rows behind the last one see nothing
-            const int32_t hi = q_row < n_row ? rq.len - rq.nq + (row0 + q_row) / a.heads + 1 : 0;
-            S.keys[q_row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);
+            const int32_t hi = on ? rq.len - rq.nq + (row0 + row) / a.by_heads + 1 : 0;
+            S.keys[row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);
+            if (row == 0) S.fresh = n_row;
         }
+        uint8_t* dst = S.q + (row >> 3) * 8192 + piece * 128 + (row & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<uint4*>(S.q + (q_row >> 3) * 8192 + (4 * i + piece) * 128 + (q_row & 7) * 16) = paged_q_f16(qv[i], qs);
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 512) = paged_q_f16(v[i], qs);
         fence_async_smem();
         asm volatile("bar.sync 1, 256;" ::: "memory");
     }
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             if (lane == 0) mbar_arrive(&S.p_full);
         }
         if (ok && nt > 0) ok = soft_and(mbar_wait(&S.o_done, 0, a.wlim));
-        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), part.item);
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(req), S.work.item);
         // ---- epilogue: the rows' sums, then O / l row by row in shared memory (the latents' place), and out
         if (ok) {
             tc_fence_after();
@@ -311,9 +315,18 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 }
                 const int dim = 128 * (b >> 1) + tid;
 #pragma unroll
+                for (int c = 0; c < 32; c += 4) {  // (all loads before the stores, which could be to the same place for all
+                                                   // the compiler knows: 47 clocks a value otherwise)
+                    const float4 f = *reinterpret_cast<const float4*>(&S.alpha[32 * (b & 1) + c]);
+                    o[c] = __float_as_uint(__uint_as_float(o[c]) * f.x);
+                    o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * f.y);
+                    o[c + 2] = __float_as_uint(__uint_as_float(o[c + 2]) * f.z);
+                    o[c + 3] = __float_as_uint(__uint_as_float(o[c + 3]) * f.w);
+                }
+#pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int r = 32 * (b & 1) + c;
-                    const float v = __uint_as_float(o[c]) * S.alpha[r];
+                    const float v = __uint_as_float(o[c]);
                     if (whole)
                         reinterpret_cast<__nv_bfloat16*>(stage)[r * kPD + dim] = __float2bfloat16_rn(v);
                     else
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         // keys of one chunk: no bank conflicts.  Keys in eights share a page.
         const int pw = warp - kPSoftWarps, k8 = lane & 7, piece = lane >> 3;
         constexpr int NV = FP8 ? 2 : 1;  // 16-byte pieces per key and 128 channels
-        uint4 v[4][2][NV];               // the four blocks of a tile, of two keys
+        uint4 v[2][2][NV];               // the block to decode and the one behind it, of two keys
         uint2 sc[2];                     // FP4: the scales of block `piece`
         const int32_t* trow = a.table + req * a.max_pages;
         const uint8_t* src[2];           // the tile being loaded: its keys' codes (from `piece` on), null without a row
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         auto locate = [&](int32_t j) {
             if ((j & 15) == 0) {
                 const int32_t p = key0 + (j + (lane >> 1)) * kPN + 16 * pw + 8 * (lane & 1);
-                ids = p < k_last ? trow[p / a.page] : -1;
+                ids = p < k_last ? trow[p / a.by_page] : -1;
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -381,21 +394,23 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < NV; ++e)
-                    v[b][i][e] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + (FP8 ? 128 : 64) * b) + 4 * e)
-                                        : make_uint4(0, 0, 0, 0);
+                    v[b & 1][i][e] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + (FP8 ? 128 : 64) * b) + 4 * e)
+                                            : make_uint4(0, 0, 0, 0);
         };
         locate(0);
         load_scales();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) load(b);
-        uint32_t gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
-        locate(1);  // always the tile behind the one that is decoded
+        load(0);
+        load(1);
         bool ok = true;
         for (int32_t j = 0; j < nt && ok; ++j) {
             uint32_t bad[2] = {0, 0};
             const uint2 sc0 = sc[0], sc1 = sc[1];
+            const uint32_t gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
+#pragma unroll 1
+            for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int bb = 0; bb < 2; ++bb) {
+                const int b = 2 * b2 + bb;
                 if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[b], (j - 1) & 1, a.wlim));
                 if (!ok) break;
 #pragma unroll
@@ -405,13 +420,13 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                         uint32_t n4 = 0;
 #pragma unroll
                         for (int e = 0; e < NV; ++e)
-                            n4 |= e4m3_nan4(v[b][i][e].x) | e4m3_nan4(v[b][i][e].y) | e4m3_nan4(v[b][i][e].z) |
-                                  e4m3_nan4(v[b][i][e].w);
+                            n4 |= e4m3_nan4(v[bb][i][e].x) | e4m3_nan4(v[bb][i][e].y) | e4m3_nan4(v[bb][i][e].z) |
+                                  e4m3_nan4(v[bb][i][e].w);
                         bad[i] |= n4;
                         const uint32_t keep = n4 ? 0u : 0xFFFFFFFFu;
 #pragma unroll
                         for (int e = 0; e < NV; ++e) {
-                            const uint32_t w[4] = {v[b][i][e].x & keep, v[b][i][e].y & keep, v[b][i][e].z & keep, v[b][i][e].w & keep};
+                            const uint32_t w[4] = {v[bb][i][e].x & keep, v[bb][i][e].y & keep, v[bb][i][e].z & keep, v[bb][i][e].w & keep};
                             uint32_t o[8];
 #pragma unroll
                             for (int t = 0; t < 4; ++t) e4m3x4_f16(w[t], o + 2 * t);
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                         bad[i] |= n2;
                         uint32_t ss[2];
                         e4m3x4_f16(n2 ? 0u : s2, ss);
-                        const uint32_t w[4] = {v[b][i][0].x, v[b][i][0].y, v[b][i][0].z, v[b][i][0].w};
+                        const uint32_t w[4] = {v[bb][i][0].x, v[bb][i][0].y, v[bb][i][0].z, v[bb][i][0].w};
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {  // one group of 16 channels
                             const uint32_t s = __byte_perm(ss[0], 0, e ? 0x3232 : 0x1010);
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                         }
                     }
                 }
-                if (b == 3) {  // per key of each eight: a bit of any of its four lanes
+                if (bb == 1 && b2 == 1) {  // per key of each eight: a bit of any of its four lanes
                     uint32_t n0 = __ballot_sync(0xffffffffu, bad[0] != 0), n1 = __ballot_sync(0xffffffffu, bad[1] != 0);
                     n0 |= n0 >> 16;
                     n1 |= n1 >> 16;
@@ -454,13 +469,19 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.full[b]);
-                load(b);  // the next tile's block, a tile's time ahead
-                if (b == 2) load_scales();
+                // two blocks ahead: this tile's, then the next one's
+                if (b2 == 0) {
+                    load(b + 2);
+                } else {
+                    if (bb == 0) {
+                        locate(j + 1);
+                        load_scales();
+                    }
+                    load(b - 2);
+                }
             }
-            gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
-            locate(j + 2);
         }
-        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), part.item);
+        if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), S.work.item);
     } else {
         regs_down<kRMmaRegs>();
         if (tid == 32 * kRMmaWarp) {
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                     tc_commit(&S.o_done);
                 }
             }
-            if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), part.item);
+            if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), S.work.item);
             if (nt > 0) {  // after a give-up, TMEM and shared memory stay until the MMAs in flight are done
                 tc_commit(&S.drain);
                 mbar_wait(&S.drain, 0, kDrainNs);

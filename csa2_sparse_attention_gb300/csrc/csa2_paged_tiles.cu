@@ -78,14 +78,12 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
 
     if (warp == 0) paged_find(a, blockIdx.x >> 2, blockIdx.x == 0, S.work);
     __syncthreads();
-    if (S.work.req < 0) return;
     const int64_t req = S.work.req;
+    if (req < 0) return;
     const PagedReq rq = S.work.rq;
-    PagedPart part;
-    if (!paged_part(a, rq, S.work.local, part)) return;
-    const int32_t nt = part.nt, key0 = part.key0, split = part.split, splits = part.splits;
+    const int32_t nt = S.work.nt, key0 = S.work.key0, split = S.work.split, splits = S.work.splits;
     // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
-    const int32_t ti = 2 * part.item + rank;
+    const int32_t ti = 2 * S.work.item + rank;
     const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
     const int64_t flat0 = int64_t(rq.q0) * a.heads + (n_row > 0 ? int64_t(ti) * kPM : 0);
     const int y_dim = kPHalf * half;
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         // ---- key tiles
         int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys
         if (row_on) {
-            hi_r = rq.len - rq.nq + (ti * kPM + row) / a.heads + 1;
+            hi_r = rq.len - rq.nq + (ti * kPM + row) / a.by_heads + 1;
             lo_r = a.window > 0 ? hi_r - a.window : 0;
         }
         float m = -INFINITY, l = 0.f;
