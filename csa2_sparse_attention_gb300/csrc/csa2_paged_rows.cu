@@ -12,11 +12,11 @@
 //   O^T [4 x 128 channels x 64]  += C^T P^T  4 x 8 MMAs, M = channels, K = keys
 //
 // (an M = 128 MMA of K = 16 takes 64 clocks for any N up to 128: 4100 clocks a
-// tile).  C [128 keys][512] in f16 fills 128 KB, so the next tile is decoded
-// block by block (128 channels) as O^T is done with this one's, and its logits
-// follow block by block:  O0 O1 O2 S0' O3 S1' S2' S3'.
+// tile).  C [128 keys][512] in f16 fills 128 KB, so the next tile is decoded in
+// halves of the channels as O^T is done with this one's: the first half under
+// the second half's O^T, the second under the first half's S^T.
 //
-//   smem  Q 64 KB, C 128 KB (four blocks), P^T 16 KB      TMEM  O^T 256, S^T 64
+//   smem  Q 64 KB, C 128 KB (four blocks of 128 channels), P^T 16 KB      TMEM  O^T 256, S^T 64
 //
 // Softmax: a thread per key, the 64 rows in its registers.  The running maxima
 // stand in shared memory; a tile whose logits all stay below them + 8 (log2)
@@ -54,8 +54,8 @@ struct PagedRowsSmem {
     float alpha[kRRows], delta[kRRows];
     float red[4][kRRows];
     int fresh;                    // rows that have seen no key yet
-    PagedFlags flags[2];
-    uint64_t full[4], empty[4], s_full, p_full, o_done, drain;
+    PagedFlags flags[2][2];       // of a tile, by each team of producers
+    uint64_t full[2], empty[4], s_full, p_full, o_done, drain;  // full: of each half of the channels
     uint32_t tmem;
     PagedWork work;
 };
@@ -102,10 +102,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         paged_find(a, blockIdx.x, blockIdx.x == 0, S.work);
     } else if (warp == kRMmaWarp) {
         if (lane == 0) {
-            for (int b = 0; b < 4; ++b) {
-                mbar_init(&S.full[b], kRProdWarps);
-                mbar_init(&S.empty[b], 1);
-            }
+            for (int b = 0; b < 4; ++b) mbar_init(&S.empty[b], 1);
+            for (int b = 0; b < 2; ++b) mbar_init(&S.full[b], kRProdWarps / 2);
             mbar_init(&S.s_full, 1);
             mbar_init(&S.p_full, kPSoftWarps);
             mbar_init(&S.o_done, 1);
@@ -181,8 +179,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                     x[h][c + 1] = fmaf(x[h][c + 1], r.z, -r.w);
                 }
             const int32_t key = key0 + j * kPN + tid;
-            const PagedFlags& f = S.flags[j & 1];
-            const bool hidden = (f.hidden[tid >> 4] >> (tid & 15)) & 1, nan = (f.nan[tid >> 4] >> (tid & 15)) & 1;
+            const PagedFlags *f = S.flags[j & 1];
+            const bool hidden = (f[0].hidden[tid >> 4] >> (tid & 15)) & 1;
+            const bool nan = ((f[0].nan[tid >> 4] | f[1].nan[tid >> 4]) >> (tid & 15)) & 1;
             // the rows' key ranges are ordered: the first row's end and the last one's start bound all of them (what a row
             // behind the last one sees is of no account)
             const bool inside = key < S.keys[0].y && key >= S.keys[n_row - 1].x;
@@ -345,141 +344,120 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         }
     } else if (warp < kRMmaWarp) {
         regs_down<kRProdRegs>();
-        // ================= producers: keys 16 pw + (lane % 8) and + 8, piece lane / 8
-        // Four lanes read 64 contiguous bytes of a row, eight rows an
-        // instruction (a row per lane takes 32 passes through the L1 data path for
-        // 512 bytes, which the MMAs' operand reads need); a quarter-warp stores 8
-        // keys of one chunk: no bank conflicts.  Keys in eights share a page.
-        const int pw = warp - kPSoftWarps, k8 = lane & 7, piece = lane >> 3;
-        constexpr int NV = FP8 ? 2 : 1;  // 16-byte pieces per key and 128 channels
-        uint4 v[2][2][NV];               // the block to decode and the one behind it, of two keys
-        uint2 sc[2];                     // FP4: the scales of block `piece`
+        // ================= producers: two teams of four warps, the first with channels 0 .. 255
+        // (blocks 0 and 1), the second with the others.  A thread has keys 32 w +
+        // 8 i + (lane % 8), i < 4, and the piece lane / 8 of 64 channels.  Loads are
+        // whole lines (32 bytes a lane, four lanes a row of 128 bytes; 8 rows of 64
+        // bytes an instruction kept the load unit busy for 1200 clocks a tile); a
+        // quarter-warp stores 8 keys of one chunk: no bank conflicts.  Keys in
+        // eights share a page.
+        const int team = (warp - kPSoftWarps) >> 2, w4 = warp & 3, k8 = lane & 7, piece = lane >> 3;
+        constexpr int NV = FP8 ? 2 : 1;  // loads per key: 64 channels in 32 bytes (FP4), or 32 (E4M3)
+        U32x8 v[4][NV];
+        uint32_t sc[4];                  // FP4: the four scales of the thread's channels
         const int32_t* trow = a.table + req * a.max_pages;
-        const uint8_t* src[2];           // the tile being loaded: its keys' codes (from `piece` on), null without a row
-        const uint8_t* ssrc[2];          //   and scales
-        // page ids of the warp's two key groups in 16 tiles, one per lane: a tile's are shuffled out
+        // page ids of the warp's four key groups in 8 tiles, one per lane: a tile's are shuffled out
         int32_t ids = -1;
-        // place within its page of the first key of the tile that is located next; a tile on is 128 keys on
+        uint32_t gone = 0;               // keys of the tile without a row, a bit each
+        // place within its page of the first key of the tile that is loaded next; a tile on is 128 keys on
         const int32_t step_off = kPN % a.page;
-        int32_t off_t = (key0 + 16 * pw) % a.page + k8;  // groups of 8 keys share a page, so this is below it
-        auto locate = [&](int32_t j) {
-            if ((j & 15) == 0) {
-                const int32_t p = key0 + (j + (lane >> 1)) * kPN + 16 * pw + 8 * (lane & 1);
+        int32_t off_t = (key0 + 32 * w4) % a.page + k8;  // groups of 8 keys share a page, so this is below it
+        auto load = [&](int32_t j) {
+            if ((j & 7) == 0) {
+                const int32_t p = key0 + (j + (lane >> 2)) * kPN + 32 * w4 + 8 * (lane & 3);
                 ids = p < k_last ? trow[p / a.by_page] : -1;
             }
+            int32_t off = off_t;
+            gone = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (j & 15) + i);
-                const int32_t off = off_t + 8 * i >= a.page ? off_t + 8 * i - a.page : off_t + 8 * i;
-                const bool in = key0 + j * kPN + 16 * pw + 8 * i + k8 < k_last;
-                src[i] = ssrc[i] = nullptr;
+            for (int i = 0; i < 4; ++i) {
+                const int32_t id = __shfl_sync(0xffffffffu, ids, 4 * (j & 7) + i);
+                const bool in = key0 + j * kPN + 32 * w4 + 8 * i + k8 < k_last;
                 if (in && id >= 0 && id < a.n_rows_pages) {
                     const int64_t row = int64_t(id) * a.page + off;
-                    src[i] = a.codes + row * (FP8 ? kPD : kPD / 2) + 16 * piece;
-                    ssrc[i] = a.scales + row * (kPD / 16) + 8 * piece;
-                } else if (in && piece == 0) {
-                    record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+                    const uint8_t* src = a.codes + row * (FP8 ? kPD : kPD / 2) + team * (FP8 ? 256 : 128) + 32 * piece;
+                    // E4M3: channels 32 piece .. of each 128 of the team's 256
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) v[i][e] = ldg_32b(src + 128 * e);
+                    if (!FP8) sc[i] = __ldg(reinterpret_cast<const uint32_t*>(a.scales + row * (kPD / 16) + 16 * team) + piece);
+                } else {
+                    if (in && piece == 0 && team == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
+                    gone |= 1u << i;
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) v[i][e].w[x] = 0;
+                    sc[i] = 0;
                 }
+                off += 8;
+                if (off >= a.page) off -= a.page;
             }
             off_t += step_off;
             if (off_t >= a.page) off_t -= a.page;
         };
-        auto load_scales = [&]() {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                sc[i] = !FP8 && src[i] ? __ldg(reinterpret_cast<const uint2*>(ssrc[i])) : make_uint2(0, 0);
-        };
-        auto load = [&](int b) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int e = 0; e < NV; ++e)
-                    v[b & 1][i][e] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + (FP8 ? 128 : 64) * b) + 4 * e)
-                                            : make_uint4(0, 0, 0, 0);
-        };
-        locate(0);
-        load_scales();
         load(0);
-        load(1);
         bool ok = true;
         for (int32_t j = 0; j < nt && ok; ++j) {
-            uint32_t bad[2] = {0, 0};
-            const uint2 sc0 = sc[0], sc1 = sc[1];
-            const uint32_t gone = (src[0] ? 0u : 1u) | (src[1] ? 0u : 2u);
-#pragma unroll 1
-            for (int b2 = 0; b2 < 2; ++b2)
-#pragma unroll
-            for (int bb = 0; bb < 2; ++bb) {
-                const int b = 2 * b2 + bb;
-                if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[b], (j - 1) & 1, a.wlim));
+            uint32_t bad = 0;  // a bit per key
+            if (j >= 1) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[2 * team], (j - 1) & 1, a.wlim));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&S.empty[2 * team + 1], (j - 1) & 1, a.wlim));
                 if (!ok) break;
+            }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint8_t* dst = S.c[b] + (2 * pw + i) * 2048 + k8 * 16;
-                    if (FP8) {
+            for (int i = 0; i < 4; ++i) {
+                if (FP8) {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) {  // 32 channels of block 2 team + e
                         uint32_t n4 = 0;
 #pragma unroll
-                        for (int e = 0; e < NV; ++e)
-                            n4 |= e4m3_nan4(v[bb][i][e].x) | e4m3_nan4(v[bb][i][e].y) | e4m3_nan4(v[bb][i][e].z) |
-                                  e4m3_nan4(v[bb][i][e].w);
-                        bad[i] |= n4;
+                        for (int x = 0; x < 8; ++x) n4 |= e4m3_nan4(v[i][e].w[x]);
+                        bad |= (n4 ? 1u : 0u) << i;
                         const uint32_t keep = n4 ? 0u : 0xFFFFFFFFu;
+                        uint8_t* dst = S.c[2 * team + e] + (4 * w4 + i) * 2048 + 4 * piece * 128 + k8 * 16;
 #pragma unroll
-                        for (int e = 0; e < NV; ++e) {
-                            const uint32_t w[4] = {v[bb][i][e].x & keep, v[bb][i][e].y & keep, v[bb][i][e].z & keep, v[bb][i][e].w & keep};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) e4m3x4_f16(w[t], o + 2 * t);
-                            *reinterpret_cast<uint4*>(dst + (8 * e + 2 * piece) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(dst + (8 * e + 2 * piece + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                    } else {
-                        // scales of channels 128 b + 32 piece .. + 31: 16 bits of the word that lane b of the row holds
-                        const uint2 mine = i ? sc1 : sc0;
-                        const uint32_t lo = __shfl_sync(0xffffffffu, mine.x, k8 + 8 * b), hi = __shfl_sync(0xffffffffu, mine.y, k8 + 8 * b);
-                        const uint32_t s2 = ((piece & 2 ? hi : lo) >> (16 * (piece & 1))) & 0xFFFFu;
-                        const uint32_t n2 = e4m3_nan4(s2);
-                        bad[i] |= n2;
-                        uint32_t ss[2];
-                        e4m3x4_f16(n2 ? 0u : s2, ss);
-                        const uint32_t w[4] = {v[bb][i][0].x, v[bb][i][0].y, v[bb][i][0].z, v[bb][i][0].w};
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {  // one group of 16 channels
-                            const uint32_t s = __byte_perm(ss[0], 0, e ? 0x3232 : 0x1010);
-                            uint32_t o[8];
-                            e2m1x8_f16(w[2 * e], o);
-                            e2m1x8_f16(w[2 * e + 1], o + 4);
-#pragma unroll
-                            for (int t = 0; t < 8; ++t) o[t] = mul_f16x2(o[t], s);
-                            *reinterpret_cast<uint4*>(dst + (4 * piece + 2 * e) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(dst + (4 * piece + 2 * e + 1) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t o[4];
+                            e4m3x4_f16(v[i][e].w[2 * x] & keep, o);
+                            e4m3x4_f16(v[i][e].w[2 * x + 1] & keep, o + 2);
+                            *reinterpret_cast<uint4*>(dst + x * 128) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                     }
-                }
-                if (bb == 1 && b2 == 1) {  // per key of each eight: a bit of any of its four lanes
-                    uint32_t n0 = __ballot_sync(0xffffffffu, bad[0] != 0), n1 = __ballot_sync(0xffffffffu, bad[1] != 0);
-                    n0 |= n0 >> 16;
-                    n1 |= n1 >> 16;
-                    const uint32_t h0 = __ballot_sync(0xffffffffu, gone & 1u), h1 = __ballot_sync(0xffffffffu, gone & 2u);
-                    if (lane == 0) {
-                        S.flags[j & 1].nan[pw] = uint16_t(((n0 | n0 >> 8) & 0xFFu) | ((n1 | n1 >> 8) & 0xFFu) << 8);
-                        S.flags[j & 1].hidden[pw] = uint16_t((h0 & 0xFFu) | (h1 & 0xFFu) << 8);
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.full[b]);
-                // two blocks ahead: this tile's, then the next one's
-                if (b2 == 0) {
-                    load(b + 2);
                 } else {
-                    if (bb == 0) {
-                        locate(j + 1);
-                        load_scales();
+                    const uint32_t n4 = e4m3_nan4(sc[i]);
+                    bad |= (n4 ? 1u : 0u) << i;
+                    uint32_t ss[2];
+                    e4m3x4_f16(n4 ? 0u : sc[i], ss);
+                    uint8_t* dst = S.c[2 * team + (piece >> 1)] + (4 * w4 + i) * 2048 + 8 * (piece & 1) * 128 + k8 * 16;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {  // 8 channels; a scale serves two
+                        const uint32_t s = __byte_perm(ss[x >> 2], 0, x & 2 ? 0x3232 : 0x1010);
+                        uint32_t o[4];
+                        e2m1x8_f16(v[i][0].w[x], o);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = mul_f16x2(o[e], s);
+                        *reinterpret_cast<uint4*>(dst + x * 128) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    load(b - 2);
                 }
             }
+            {  // per key a bit of any of its four lanes, eight keys a byte
+                uint32_t nan = 0, hid = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x = __ballot_sync(0xffffffffu, (bad >> i) & 1u);
+                    x |= x >> 16;
+                    nan |= ((x | x >> 8) & 0xFFu) << (8 * i);
+                    hid |= (__ballot_sync(0xffffffffu, (gone >> i) & 1u) & 0xFFu) << (8 * i);
+                }
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t*>(S.flags[j & 1][team].nan)[w4] = nan;
+                    reinterpret_cast<uint32_t*>(S.flags[j & 1][team].hidden)[w4] = hid;
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.full[team]);
+            if (j + 1 < nt) load(j + 1);
         }
         if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 7, int32_t(req), S.work.item);
     } else {
@@ -497,7 +475,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             const uint64_t dk0 = umma_desc(smem_u32(S.c[0]), 128, 2048), dv0 = umma_desc(smem_u32(S.c[0]), 2048, 128);
             bool ok = true;
             auto s_mma = [&](int32_t j, int b) {  // S^T += C_b Q_b^T of tile j
-                ok = ok && mbar_wait(&S.full[b], j & 1, a.wlim);
+                if ((b & 1) == 0) ok = ok && mbar_wait(&S.full[b >> 1], j & 1, a.wlim);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t dk = fresh(dk0) + b * (kRBlock >> 4), dq = fresh(dq0) + b * (2048 >> 4);
@@ -520,15 +498,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 if (!ok) break;
                 tc_fence_after();
                 const bool next = j + 1 < nt;
-                o_mma(j, 0);
-                o_mma(j, 1);
-                o_mma(j, 2);
-                if (next) s_mma(j + 1, 0);
-                o_mma(j, 3);
+                for (int b = 0; b < 4; ++b) o_mma(j, b);
                 if (next) {
-                    s_mma(j + 1, 1);
-                    s_mma(j + 1, 2);
-                    s_mma(j + 1, 3);
+                    for (int b = 0; b < 4; ++b) s_mma(j + 1, b);
                     if (ok) tc_commit(&S.s_full);
                 } else if (ok) {
                     tc_commit(&S.o_done);
