@@ -227,12 +227,13 @@ __device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32
         : "memory");
 }
 // One bulk copy shared memory -> global (addresses and size multiples of 16
-// bytes), and the wait for this thread's copies: written, not only read.
+// bytes), and the wait until this thread's copies have read shared memory (what
+// they write is there when the kernel is done).
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(dst),
                  "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -290,31 +291,42 @@ __device__ __forceinline__ U32x8 ldg_32b(const uint8_t* p) {
 // nonzero when one of the four E4M3 bytes is NaN (0x7F or 0xFF)
 __device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Q's conversion to f16: 8 rows per warp, four lanes per row, lane / 8 with 16
-// bytes of every 64.  The power of two of a row from its maximum, max |q| 2^-qs
+// Q's conversion to f16: 8 rows per warp, four lanes per row, lane / 8 with 32
+// bytes of every 128.  The power of two of a row from its maximum, max |q| 2^-qs
 // in [2^14, 2^15): exact for elements above 2^-28 of it.
-__device__ __forceinline__ void paged_q_load(const PagedArgs& a, int64_t flat, bool on, uint4 (&v)[16]) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + (on ? flat : 0) * (kPD * 2)) + (lane_id() >> 3);
+__device__ __forceinline__ void paged_q_load(const PagedArgs& a, int64_t flat, bool on, U32x8 (&v)[8]) {
+    const uint8_t* src = a.q + (on ? flat : 0) * (kPD * 2) + 32 * (lane_id() >> 3);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = on ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) {
+        if (on) {
+            v[i] = ldg_32b(src + 128 * i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i].w[e] = 0;
+        }
+    }
 }
-__device__ __forceinline__ int paged_q_exponent(const uint4 (&v)[16]) {
+__device__ __forceinline__ int paged_q_exponent(const U32x8 (&v)[8]) {
     uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-        am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-    }
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) am = __vmaxu2(am, v[i].w[e] & 0x7FFF7FFFu);
     am = max(am & 0xFFFFu, am >> 16);
     am = max(am, __shfl_xor_sync(0xffffffffu, am, 8));
     am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
     const int qs = am != 0 ? int(am >> 7) - 127 - 14 : 0;
     return qs < -100 ? -100 : qs;
 }
-__device__ __forceinline__ uint4 paged_q_f16(uint4 v, int qs) {
+// Channels 64 i + 16 (lane / 8) .. + 15 of a row into two chunks, 128 bytes
+// apart.
+__device__ __forceinline__ void paged_q_store(uint8_t* dst, const U32x8& v, int qs) {
     const float qf = __uint_as_float(uint32_t(127 - qs) << 23);
-    return make_uint4(f16x2(bf16_lo(v.x) * qf, bf16_hi(v.x) * qf), f16x2(bf16_lo(v.y) * qf, bf16_hi(v.y) * qf),
-                      f16x2(bf16_lo(v.z) * qf, bf16_hi(v.z) * qf), f16x2(bf16_lo(v.w) * qf, bf16_hi(v.w) * qf));
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = f16x2(bf16_lo(v.w[e]) * qf, bf16_hi(v.w[e]) * qf);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 // The factor of a row's raw logits, log2 domain (never 0: -inf stays -inf).
 __device__ __forceinline__ float paged_q_scale(const PagedArgs& a, int qs) {

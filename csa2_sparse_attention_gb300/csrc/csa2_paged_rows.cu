@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     if (warp < kPSoftWarps || warp >= kRMmaWarp) {
         const int row = 8 * (warp < kPSoftWarps ? warp : warp - kRProdWarps) + (lane & 7), piece = lane >> 3;
         const bool on = row < n_row;
-        uint4 v[16];
+        U32x8 v[8];
         paged_q_load(a, flat0 + row, on, v);
         const int qs = paged_q_exponent(v);
         if (piece == 0) {
@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             S.keys[row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);
             if (row == 0) S.fresh = n_row;
         }
-        uint8_t* dst = S.q + (row >> 3) * 8192 + piece * 128 + (row & 7) * 16;
+        uint8_t* dst = S.q + (row >> 3) * 8192 + piece * 256 + (row & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 512) = paged_q_f16(v[i], qs);
+        for (int i = 0; i < 8; ++i) paged_q_store(dst + i * 1024, v[i], qs);
         fence_async_smem();
         asm volatile("bar.sync 1, 256;" ::: "memory");
     }

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
 
     // ---- Q: two groups of 8 rows per warp; the loads are under way while the CTA sets up
     const int q_groups = (n_row + 7) / 8;  // rows behind the last one stay what they are: they reach no other row
-    uint4 qv[2][16];
+    U32x8 qv[2][8];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int row = 8 * (warp + 8 * n) + (lane & 7);
@@ -147,10 +147,9 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         const int qs = paged_q_exponent(qv[n]);
         if (piece == 0) S.q_scale[row] = paged_q_scale(a, qs);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            uint8_t* dst = (i >= 8) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
-            *reinterpret_cast<uint4*>(dst + (row >> 3) * 4096 + (4 * (i & 7) + piece) * 128 + (row & 7) * 16) =
-                paged_q_f16(qv[n][i], qs);
+        for (int i = 0; i < 8; ++i) {
+            uint8_t* dst = (i >= 4) == (half == 1) ? S.c[1] : S.qx;  // channels 256 .. 511 are the own half of half 1
+            paged_q_store(dst + (row >> 3) * 4096 + (8 * (i & 3) + 2 * piece) * 128 + (row & 7) * 16, qv[n][i], qs);
         }
     }
     fence_async_smem();
