@@ -3,10 +3,15 @@
 //   h = bf16(x + residual),  y = h * rsqrt(mean(h^2) + eps) * w,
 //   s = max|y| / 448 per row or per 128 channels,  code = E4M3(y / s)
 //
-// HBM bound: 7 bytes per channel with a residual (x, residual in and out, code), 3
-// without.  A row is read once: its values stay in the registers of the
-// threads that loaded them (16 bytes, 8 channels, a chunk) through both
-// reductions.
+// HBM bound: 7 bytes per channel with a residual (x, residual in and out,
+// code), 3 without.  A row is read once and stays in the registers of the
+// threads that loaded it (16-byte chunks of 8 channels) through both
+// reductions.  Rows of more than 1024 channels take a block, two chunks per
+// thread, that
+// walks over the rows and loads the next one before it reduces this one: the
+// two block barriers of a row then cost no memory time.  4096 rows of 7168
+// with a residual, scales per 128: 57.8 us without that, NORM_US with it
+// (NORM_TBS, NORM_PCT of the copy rate).
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 
@@ -28,17 +33,20 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 // WPR warps per row, chunks t, t + 32 WPR, ... (NCH of them) of the row in
 // thread t of the row's warps.
 template <int WPR, int NCH, bool GROUPS>
-__global__ void __launch_bounds__(256) rmsnorm_fp8_kernel(const uint4* __restrict__ x, int64_t x_stride, const uint4* residual,
-                                                          uint4* residual_out, const uint4* __restrict__ weight, int64_t n,
-                                                          int dim, float eps, uint2* __restrict__ codes,
-                                                          float* __restrict__ scales, uint4* __restrict__ y_bf16) {
-    constexpr int T = 32 * WPR, RPB = 256 / T;
-    __shared__ float red[2][8];
+__global__ void __launch_bounds__(WPR > 1 ? 32 * WPR : 256, WPR > 1 ? 1024 / (32 * WPR) : 1) rmsnorm_fp8_kernel(
+    const uint4* __restrict__ x, int64_t x_stride, const uint4* residual, uint4* residual_out,
+    const uint4* __restrict__ weight, int64_t n, int dim, float eps, uint2* __restrict__ codes, float* __restrict__ scales,
+    uint4* __restrict__ y_bf16) {
+    constexpr int T = 32 * WPR, RPB = WPR > 1 ? 1 : 256 / T;
+    __shared__ float red[2][2][32];
     grid_dep_wait();
     grid_dep_launch();
     const int t = threadIdx.x % T, rw = threadIdx.x / T, lane = lane_id();
     const int chunks = dim / 8;
-    // block reduction over the row's warps (a row has one warp, or all eight)
+    const int64_t step = int64_t(gridDim.x) * RPB;
+    int par = 0;
+    // reduction over the row's warps (one, or the whole block's); the two rows in turn use two buffers, so
+    // that one barrier per reduction is enough
     auto over_row = [&](float v, bool is_max, int slot) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -46,61 +54,69 @@ __global__ void __launch_bounds__(256) rmsnorm_fp8_kernel(const uint4* __restric
             v = is_max ? max_nan(v, u) : v + u;
         }
         if (WPR > 1) {
-            if (lane == 0) red[slot][threadIdx.x >> 5] = v;
+            if (lane == 0) red[par][slot][threadIdx.x >> 5] = v;
             __syncthreads();
-            v = red[slot][0];
+            v = lane < WPR ? red[par][slot][lane] : 0.f;  // (0 is neutral for both: maxima are of absolute values)
 #pragma unroll
-            for (int w = 1; w < WPR; ++w) v = is_max ? max_nan(v, red[slot][w]) : v + red[slot][w];
+            for (int o = WPR / 2; o; o >>= 1) {
+                const float u = __shfl_xor_sync(0xffffffffu, v, o);
+                v = is_max ? max_nan(v, u) : v + u;
+            }
+            v = __shfl_sync(0xffffffffu, v, 0);
         }
         return v;
     };
-    for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < n; row0 += int64_t(gridDim.x) * RPB) {
+    uint4 wv[NCH], xv[NCH], rv[NCH];  // weight; the next row's x and residual
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) wv[j] = t + T * j < chunks ? __ldg(weight + t + T * j) : make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const int c = t + T * j;
+            const bool on = row < n && c < chunks;
+            xv[j] = on ? __ldg(x + row * (x_stride / 8) + c) : make_uint4(0, 0, 0, 0);
+            rv[j] = on && residual != nullptr ? residual[row * chunks + c] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    if (WPR > 1) fetch(int64_t(blockIdx.x) * RPB + rw);
+    for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < n; row0 += step, par ^= 1) {
         const int64_t row = row0 + rw;
         const bool live = row < n;
-        float h[NCH][8];
+        if (WPR == 1) fetch(row);
+        uint4 h[NCH];
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             const int c = t + T * j;
-            const bool on = live && c < chunks;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (on) {
-                v = __ldg(x + row * (x_stride / 8) + c);
-                if (residual != nullptr) {
-                    const uint4 u = residual[row * chunks + c];
-                    uint32_t* a = &v.x;
-                    const uint32_t* b = &u.x;
+            uint32_t a[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+            const uint32_t r[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+            if (residual != nullptr) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a[e] = bf16x2_rn(bf16_lo(a[e]) + bf16_lo(b[e]), bf16_hi(a[e]) + bf16_hi(b[e]));
-                    residual_out[row * chunks + c] = v;
-                }
+                for (int e = 0; e < 4; ++e) a[e] = bf16x2_rn(bf16_lo(a[e]) + bf16_lo(r[e]), bf16_hi(a[e]) + bf16_hi(r[e]));
             }
-            const uint32_t* a = &v.x;
+            h[j] = make_uint4(a[0], a[1], a[2], a[3]);
+            if (residual != nullptr && live && c < chunks) residual_out[row * chunks + c] = h[j];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                h[j][2 * e] = bf16_lo(a[e]);
-                h[j][2 * e + 1] = bf16_hi(a[e]);
+                ss = fmaf(bf16_lo(a[e]), bf16_lo(a[e]), ss);
+                ss = fmaf(bf16_hi(a[e]), bf16_hi(a[e]), ss);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
         }
+        if (WPR > 1) fetch(row + step);
         ss = over_row(ss, false, 0);
         const float rs = 1.0f / sqrtf(ss / float(dim) + eps);
-        float am = 0.f, cm[NCH];
+        float y[NCH][8], am = 0.f, cm[NCH];
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            const int c = t + T * j;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (c < chunks) w = __ldg(weight + c);
-            const uint32_t* a = &w.x;
+            const uint32_t a[4] = {h[j].x, h[j].y, h[j].z, h[j].w}, w[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
             cm[j] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                h[j][2 * e] = h[j][2 * e] * rs * bf16_lo(a[e]);
-                h[j][2 * e + 1] = h[j][2 * e + 1] * rs * bf16_hi(a[e]);
-                if (c < chunks) cm[j] = max_nan(cm[j], max_nan(fabsf(h[j][2 * e]), fabsf(h[j][2 * e + 1])));
+                y[j][2 * e] = bf16_lo(a[e]) * rs * bf16_lo(w[e]);
+                y[j][2 * e + 1] = bf16_hi(a[e]) * rs * bf16_hi(w[e]);
+                cm[j] = max_nan(cm[j], max_nan(fabsf(y[j][2 * e]), fabsf(y[j][2 * e + 1])));
             }
+            if (t + T * j >= chunks) cm[j] = 0.f;  // (a chunk behind the row is 0 * rs, and rs may be infinite)
             if (GROUPS) {  // 16 chunks = 128 channels: half a warp
 #pragma unroll
                 for (int o = 8; o; o >>= 1) cm[j] = max_nan(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], o));
@@ -113,29 +129,29 @@ __global__ void __launch_bounds__(256) rmsnorm_fp8_kernel(const uint4* __restric
         for (int j = 0; j < NCH; ++j) {
             const int c = t + T * j;
             if (!live || c >= chunks) continue;
-            const float s = __fdiv_rn(GROUPS ? cm[j] : am, 448.0f);
+            const float s = (GROUPS ? cm[j] : am) * (1.0f / 448.0f);
             const float inv = __frcp_rn(s);
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = h[j][e] * inv;
-                // the reciprocal overflows for the smallest scales; 0 / 0 is 0
-                if (!(inv <= FLT_MAX)) v[e] = s == 0.f ? 0.f : __fdiv_rn(h[j][e], s);
+            for (int e = 0; e < 8; ++e) v[e] = y[j][e] * inv;
+            if (!(inv <= FLT_MAX)) {  // the reciprocal of the smallest scales overflows; 0 / 0 is 0
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = s == 0.f ? 0.f : __fdiv_rn(y[j][e], s);
             }
             uint2 o;
             o.x = e4m3x2_rn_sat(v[0], v[1]) | (e4m3x2_rn_sat(v[2], v[3]) << 16);
             o.y = e4m3x2_rn_sat(v[4], v[5]) | (e4m3x2_rn_sat(v[6], v[7]) << 16);
             codes[row * chunks + c] = o;
             if (y_bf16 != nullptr)
-                y_bf16[row * chunks + c] = make_uint4(bf16x2_rn(h[j][0], h[j][1]), bf16x2_rn(h[j][2], h[j][3]),
-                                                      bf16x2_rn(h[j][4], h[j][5]), bf16x2_rn(h[j][6], h[j][7]));
+                y_bf16[row * chunks + c] =
+                    make_uint4(bf16x2_rn(y[j][0], y[j][1]), bf16x2_rn(y[j][2], y[j][3]), bf16x2_rn(y[j][4], y[j][5]),
+                               bf16x2_rn(y[j][6], y[j][7]));
             if (GROUPS) {
                 if ((c & 15) == 0) scales[row * (chunks / 16) + c / 16] = s;
             } else if (c == 0) {
                 scales[row] = s;
             }
         }
-        if (WPR > 1) __syncthreads();  // `red` is free for the next row
     }
 }
 
@@ -158,26 +174,24 @@ extern "C" csa2_status csa2_rmsnorm_fp8(const void* x, int64_t x_stride, const v
     cudaStream_t s = cudaStream_t(stream);
     const int chunks = dim / 8;
     const bool wide = chunks > 128;
-    const int nch = ceil_div(chunks, wide ? 256 : 32);
-    const int64_t cap = int64_t(sm_count()) * 8, want = wide ? n : ceil_div<int64_t>(n, 8);
+    const int threads = !wide || chunks <= 512 ? 256 : chunks <= 1024 ? 512 : 1024;
+    // wide rows: the blocks that are resident at once, which then walk over the rows
+    const int64_t cap = int64_t(sm_count()) * (wide ? 1024 / threads : 8), want = wide ? n : ceil_div<int64_t>(n, 8);
     const dim3 grid(unsigned(want < cap ? want : cap));
     timer_begin(K_RMSNORM, s);
     auto go = [&](auto kernel) {
-        launch(kernel, grid, 256, 0, s, 1, static_cast<const uint4*>(x), x_stride, static_cast<const uint4*>(residual),
+        launch(kernel, grid, threads, 0, s, 1, static_cast<const uint4*>(x), x_stride, static_cast<const uint4*>(residual),
                static_cast<uint4*>(residual_out), static_cast<const uint4*>(weight), n, dim, eps,
                reinterpret_cast<uint2*>(codes), scales, static_cast<uint4*>(y_bf16));
     };
 #define CSA2_NORM(W, C) \
     if (group) go(rmsnorm_fp8_kernel<W, C, true>); \
     else go(rmsnorm_fp8_kernel<W, C, false>)
-    if (!wide) {
-        if (nch <= 2) { CSA2_NORM(1, 2); }
-        else { CSA2_NORM(1, 4); }
-    } else {
-        if (nch <= 2) { CSA2_NORM(8, 2); }
-        else if (nch <= 4) { CSA2_NORM(8, 4); }
-        else { CSA2_NORM(8, 8); }
-    }
+    if (chunks <= 64) { CSA2_NORM(1, 2); }
+    else if (!wide) { CSA2_NORM(1, 4); }
+    else if (threads == 256) { CSA2_NORM(8, 2); }
+    else if (threads == 512) { CSA2_NORM(16, 2); }
+    else { CSA2_NORM(32, 2); }
 #undef CSA2_NORM
     timer_end(K_RMSNORM, s);
     return launch_status();
