@@ -35,9 +35,11 @@ namespace csa2 {
 constexpr int kMvThreads = 512, kMvWarps = kMvThreads / 32;
 constexpr int kMvStep = 128, kMvRows = 32;    // channels and rows of W per step of a warp
 constexpr int kMvStage = kMvRows * (kMvStep / 2 + kMvStep / 16);  // bytes of a step: codes, then scales
+constexpr int kMvSumStride = 36;              // a column's rows of a warp's sums: no bank conflicts
 constexpr int kMvMaxStages = 4;
+constexpr int kMvHeld = 8;                    // pieces of x that a thread holds from its first loads on
 constexpr int kMvSms = 152;                   // multiprocessors the split is planned for
-constexpr size_t kMvSmem = 208 * 1024;        // x and the rings, per CTA (and the warps' sums, 16 or 32 KB)
+constexpr size_t kMvSmem = 208 * 1024;        // x and the rings, per CTA (and the warps' sums, 18 or 36 KB)
 
 struct MatvecArgs {
     const uint8_t* x;
@@ -102,14 +104,33 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
     const int steps = (kn + kMvStep - 1) / kMvStep;
     const int wk = a.wk, wm = kMvWarps / wk, my_k = warp % wk, my_m = warp / wk;
     const int per_tile = (steps + wk - 1) / wk;  // steps of a warp per tile of 32 wm rows of W
-    // shared memory: rings, then the warps' sums [warp][8 NT columns][32 rows], then x
+    // shared memory: rings, then the warps' sums [warp][8 NT columns][36: 32 rows], then x
     uint8_t* ring = smem_raw + warp * (STAGES * kMvStage);
     float* s_red = reinterpret_cast<float*>(smem_raw + kMvWarps * STAGES * kMvStage);
-    constexpr int kRed = 8 * NT * kMvRows;
+    constexpr int kRed = 8 * NT * kMvSumStride;
     uint8_t* s_x = reinterpret_cast<uint8_t*>(s_red + kMvWarps * kRed);
     if (tid < 16) s_max[tid] = 0;
+    __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
+
+    // ---- x: the first pieces of 8 channels of this thread's row, ahead of the
+    // weights in the load unit's queue
+    const int threads_per_row = kMvThreads / (rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16);
+    const int xr = tid / threads_per_row, xt = tid % threads_per_row;
+    const bool x_on = xr < rows;
+    auto x_raw = [&](int p) {  // 8 bf16, or 8 E4M3 in the first half
+        const int64_t at = (i0 + xr) * a.x_stride + k0 + 8 * p;
+        if (!a.x_e4m3) return __ldg(reinterpret_cast<const uint4*>(a.x + 2 * at));
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.x + at));
+        return make_uint4(v.x, v.y, 0, 0);
+    };
+    uint4 xv[kMvHeld];
+#pragma unroll
+    for (int e = 0; e < kMvHeld; ++e) {
+        const int p = xt + e * threads_per_row;
+        xv[e] = x_on && p < kn / 8 ? x_raw(p) : make_uint4(0, 0, 0, 0);
+    }
 
     // ---- weights: step u of this warp is step my_k + wk (u % per_tile) of
     // the channels, of tile blockIdx.x + gridDim.x (u / per_tile)
@@ -156,38 +177,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
     }
 
     // ---- x: f16 in the lanes' order, [128 channels][8-channel piece i][row][t]
-    const int pieces = steps * (kMvStep / 8);  // per row, of 8 channels
-    auto x_piece = [&](int r, int p) {
-        const int64_t at = (i0 + r) * a.x_stride + k0 + 8 * p;
-        if (a.x_e4m3) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.x + at));
-            uint4 o;
-            asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n"
-                " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n"
-                " cvt.rn.f16x2.e4m3x2 %2, c;\n cvt.rn.f16x2.e4m3x2 %3, d;\n}\n"
-                : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(v.x), "r"(v.y));
-            return o;
-        }
-        return __ldg(reinterpret_cast<const uint4*>(a.x + 2 * at));
-    };
-    const int threads_per_row = kMvThreads / (rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16);
-    const int xr = tid / threads_per_row, xt = tid % threads_per_row;
-    __syncthreads();  // s_max is zero
     if (!a.x_e4m3) {
-        if (xr < rows) {
+        if (x_on) {
             uint32_t m = 0;
-#pragma unroll 4
-            for (int p = xt; p < kn / 8; p += threads_per_row) {
-                const uint4 v = x_piece(xr, p);
+            auto take = [&](uint4 v) {
                 m = __vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
                 m = __vmaxu2(m, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-            }
+            };
+#pragma unroll
+            for (int e = 0; e < kMvHeld; ++e) take(xv[e]);
+#pragma unroll 4
+            for (int p = xt + kMvHeld * threads_per_row; p < kn / 8; p += threads_per_row) take(x_raw(p));
             m = max(m & 0xFFFFu, m >> 16);
             atomicMax(&s_max[xr], m);
         }
         __syncthreads();
     }
-    if (xr < rows) {
+    if (x_on) {
         float qf = 1.f;
         if (!a.x_e4m3) {
             int qs = s_max[xr] != 0 ? int(s_max[xr] >> 7) - 127 - 14 : 0;  // max |x| 2^-qs in [2^14, 2^15)
@@ -197,23 +203,28 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
         } else if (xt == 0) {
             s_mul[xr] = a.x_scales[i0 + xr];
         }
-#pragma unroll 4
-        for (int p = xt; p < pieces; p += threads_per_row) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (8 * p < kn) {
-                v = x_piece(xr, p);
-                if (!a.x_e4m3) {
-                    uint32_t* w = &v.x;
+        auto put = [&](int p, uint4 v) {
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (a.x_e4m3) {
+                asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n"
+                    " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n"
+                    " cvt.rn.f16x2.e4m3x2 %2, c;\n cvt.rn.f16x2.e4m3x2 %3, d;\n}\n"
+                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(v.x), "r"(v.y));
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
-                        w[e] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * qf, bf16_hi(w[e]) * qf);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&h);
                 }
             }
             const int c = p >> 4, pt = (p >> 2) & 3, i = p & 3;
-            *reinterpret_cast<uint4*>(s_x + ((c * 4 + i) * rows + xr) * 64 + pt * 16) = v;
-        }
+            *reinterpret_cast<uint4*>(s_x + ((c * 4 + i) * rows + xr) * 64 + pt * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        };
+#pragma unroll
+        for (int e = 0; e < kMvHeld; ++e)
+            if (xt + e * threads_per_row < kn / 8) put(xt + e * threads_per_row, xv[e]);
+#pragma unroll 4
+        for (int p = xt + kMvHeld * threads_per_row; p < kn / 8; p += threads_per_row) put(p, x_raw(p));
     }
     __syncthreads();
 
@@ -269,17 +280,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     const int col = 8 * q + 2 * t, r = 16 * m + g;
-                    mine[col * kMvRows + r] = acc[m][q][0];
-                    mine[(col + 1) * kMvRows + r] = acc[m][q][1];
-                    mine[col * kMvRows + r + 8] = acc[m][q][2];
-                    mine[(col + 1) * kMvRows + r + 8] = acc[m][q][3];
+                    mine[col * kMvSumStride + r] = acc[m][q][0];
+                    mine[(col + 1) * kMvSumStride + r] = acc[m][q][1];
+                    mine[col * kMvSumStride + r + 8] = acc[m][q][2];
+                    mine[(col + 1) * kMvSumStride + r + 8] = acc[m][q][3];
                     acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
                 }
             __syncthreads();
-            const int width = kMvRows * wm;
+            const int width = kMvRows * wm, log2w = 31 - __clz(width);
             for (int e = tid; e < rows * width; e += kMvThreads) {
-                const int i = e / width, j = e - i * width;
-                const float* from = s_red + (j >> 5) * wk * kRed + i * kMvRows + (j & 31);
+                const int i = e >> log2w, j = e - (i << log2w);
+                const float* from = s_red + (j >> 5) * wk * kRed + i * kMvSumStride + (j & 31);
                 float v = 0.f;
                 for (int q = 0; q < wk; ++q) v += from[q * kRed];
                 v *= s_mul[i];
@@ -324,7 +335,7 @@ static MatvecPlan matvec_plan(int64_t n, int k, int64_t n_out) {
     MatvecPlan p{};
     const int rows = n < 16 ? int(n > 0 ? n : 1) : 16, nt = n > 8 ? 2 : 1;
     const int steps = (k + kMvStep - 1) / kMvStep;
-    const size_t step_x = size_t(rows) * kMvStep * 2, red = size_t(kMvWarps) * 8 * nt * kMvRows * 4;
+    const size_t step_x = size_t(rows) * kMvStep * 2, red = size_t(kMvWarps) * 8 * nt * kMvSumStride * 4;
     // x's channels per CTA: what fits beside two stages (25 steps of 128 at 16 rows)
     const int fit = int((kMvSmem - red - 2 * kMvWarps * kMvStage) / step_x);
     p.slices = (steps + fit - 1) / fit;
