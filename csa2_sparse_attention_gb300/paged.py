@@ -1,0 +1,146 @@
+"""A layer's step over a paged latent cache on one GPU.
+
+Every request brings a chunk of new tokens (one for a decoding request).  The
+step norms the hidden states to E4M3, projects queries and latents with FP4
+weights, plans pages and rows on the device, appends the latents (RoPE and
+FP4, or E4M3) and attends causally over everything the requests hold.
+
+This module only allocates device memory (torch) and issues C-ABI calls in
+that order; all arithmetic runs in libcsa2.so.  A step issues the same calls
+with the same pointers every time, so it can be captured in a CUDA graph: the
+lengths stay on the device, and the host's bounds max_q and max_kv size the
+launches.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import abi
+
+LATENT = abi.LATENT_DIM
+
+
+def fp4_weight(w, stream=None):
+    """FP4 form (codes [n][k/2], scales [n][k/16]) of bf16 weights w [n][k], k a multiple of 128."""
+    n, k = w.shape
+    if k % 128:
+        raise ValueError("the channels of an FP4 weight come in multiples of 128")
+    codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((n, k // 16), dtype=torch.uint8, device=w.device)
+    ws = torch.zeros(abi.STATUS_BYTES, dtype=torch.uint8, device=w.device)
+    rows = n * k // 128
+    s = stream or torch.cuda.current_stream(w.device)
+    abi.csa2_quantize_append(w.contiguous(), rows, 128, abi.FMT_FP4, abi.LAYOUT_ROWS, None, None, 0, None, rows, codes, scales,
+                             ws, ws.numel(), s)
+    return codes, scales
+
+
+class PagedLatents:
+    """Pages, block tables and latents of a batch of requests, and the calls over them."""
+
+    def __init__(self, n_req, max_tokens, n_pages, page_size, max_pages, heads=abi.ATTN_HEADS, fmt=abi.FMT_FP4, window=0,
+                 sm_scale=1.0 / math.sqrt(float(LATENT)), rope_theta=10000.0, device="cuda"):
+        d = self.dev = torch.device(device)
+        self.n_req, self.max_tokens, self.heads = n_req, max_tokens, heads
+        self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
+        self.fmt, self.window, self.sm_scale = fmt, window, sm_scale
+        self.n_rows = n_pages * page_size
+        u8, i32, i64 = torch.uint8, torch.int32, torch.int64
+        fp4 = fmt == abi.FMT_FP4
+        self.codes = torch.zeros((self.n_rows, LATENT // 2 if fp4 else LATENT), dtype=u8, device=d)
+        self.scales = torch.zeros((self.n_rows, LATENT // 16), dtype=u8, device=d) if fp4 else None
+        self.table = torch.full((n_req, max_pages), -1, dtype=i32, device=d)
+        self.free = torch.arange(n_pages - 1, -1, -1, dtype=i32, device=d)  # taken from the end: page 0 first
+        self.n_free = torch.full((1,), n_pages, dtype=i32, device=d)
+        self.cached = torch.zeros(n_req, dtype=i32, device=d)   # entries held before the step
+        self.added = torch.zeros(n_req, dtype=i32, device=d)    # new tokens of the step
+        self.kv_len = torch.zeros(n_req, dtype=i32, device=d)
+        self.q_start = torch.zeros(n_req + 1, dtype=i32, device=d)
+        self.slots = torch.zeros(max_tokens, dtype=i64, device=d)
+        self.pos = torch.zeros(max_tokens, dtype=i64, device=d)
+        self.max_pos = max_pages * page_size
+        self.rope = None
+        if fp4:
+            self.rope = torch.empty(abi.csa2_rope_table_bytes(LATENT, self.max_pos), dtype=u8, device=d)
+            abi.csa2_rope_table_init(rope_theta, LATENT, self.max_pos, self.rope, torch.cuda.current_stream(d))
+        self.out = torch.zeros((max_tokens, heads, LATENT), dtype=torch.bfloat16, device=d)
+        self.lse = torch.zeros((max_tokens, heads), dtype=torch.float32, device=d)
+        self.ws_plan = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
+        self.ws_app = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
+        self.ws_attn = None
+
+    def plan(self, stream=None):
+        """Pages, rows and positions of the step's new tokens (self.cached, self.added)."""
+        s = stream or torch.cuda.current_stream(self.dev)
+        abi.csa2_page_plan(self.cached, self.added, self.n_req, self.page_size, self.table, self.max_pages, self.free,
+                           self.n_pages, self.n_free, self.n_free, self.q_start, self.kv_len, self.slots, self.pos,
+                           self.max_tokens, self.ws_plan, self.ws_plan.numel(), s)
+
+    def append(self, latents, n_tokens, stream=None):
+        """The new tokens' bf16 latents [n_tokens][512] into the planned rows."""
+        s = stream or torch.cuda.current_stream(self.dev)
+        fp4 = self.fmt == abi.FMT_FP4
+        abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if fp4 else None, self.rope,
+                                 self.max_pos if fp4 else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
+                                 self.ws_app.numel(), s)
+
+    def workspace(self, n_tokens, max_q, max_kv):
+        """The attention's workspace for these bounds (kept, and grown where a later step needs more)."""
+        need = abi.csa2_paged_attn_workspace_bytes(n_tokens, self.heads, self.n_req, max_q, max_kv, self.window)
+        if self.ws_attn is None or self.ws_attn.numel() < need:
+            self.ws_attn = torch.zeros(need, dtype=torch.uint8, device=self.dev)
+        return self.ws_attn
+
+    def attend(self, q, n_tokens, max_q, max_kv, stream=None):
+        """out, lse of the new tokens' queries q [n_tokens][heads][512] over all entries."""
+        s = stream or torch.cuda.current_stream(self.dev)
+        ws = self.workspace(n_tokens, max_q, max_kv)
+        abi.csa2_paged_attn(q, n_tokens, self.heads, self.q_start, self.kv_len, self.n_req, max_q, max_kv, self.fmt, self.codes,
+                            self.scales, self.n_rows, self.table, self.max_pages, self.page_size, self.window, self.sm_scale,
+                            self.out, self.lse, ws, ws.numel(), s)
+        return self.out[:n_tokens], self.lse[:n_tokens]
+
+    def advance(self):
+        """After a step: what it added is cached."""
+        self.cached.copy_(self.kv_len)
+
+    def status(self):
+        """Status words of every workspace (first device-detected problem)."""
+        named = (("plan", self.ws_plan), ("append", self.ws_app), ("attn", self.ws_attn))
+        return {name: abi.csa2_status_fetch(ws) for name, ws in named if ws is not None}
+
+
+class PagedLayer:
+    """The front of an attention layer: norm, FP4 projections and the attention over a PagedLatents cache."""
+
+    def __init__(self, cache, hidden, norm_weight, wq, wlatent, eps=1e-6):
+        """norm_weight bf16 [hidden]; wq, wlatent: bf16 weights [heads * 512][hidden], [512][hidden]."""
+        self.cache, self.hidden, self.eps, self.norm_weight = cache, hidden, eps, norm_weight
+        d, T, H = cache.dev, cache.max_tokens, cache.heads
+        self.wq, self.wlatent = fp4_weight(wq), fp4_weight(wlatent)
+        self.residual = torch.zeros((T, hidden), dtype=torch.bfloat16, device=d)
+        self.x = torch.zeros((T, hidden), dtype=torch.uint8, device=d)  # E4M3
+        self.x_scales = torch.zeros(T, dtype=torch.float32, device=d)
+        self.q = torch.zeros((T, H, LATENT), dtype=torch.bfloat16, device=d)
+        self.latents = torch.zeros((T, LATENT), dtype=torch.bfloat16, device=d)
+        size = max(abi.csa2_fp4_matvec_workspace_bytes(T, hidden, H * LATENT), abi.csa2_fp4_matvec_workspace_bytes(T, hidden, LATENT))
+        self.ws = torch.zeros(size, dtype=torch.uint8, device=d)
+
+    def _project(self, w, n, n_out, out, s):
+        abi.csa2_fp4_matvec(self.x, abi.X_E4M3, self.x_scales, self.hidden, n, self.hidden, w[0], w[1], n_out, 1.0, out,
+                            abi.OUT_BF16, self.ws, self.ws.numel(), s)
+
+    def step(self, hidden, n_tokens, max_q, max_kv, stream=None):
+        """One step of n_tokens new tokens' bf16 hidden states (added to self.residual, the layer's residual stream):
+        (out, lse) of the attention."""
+        c, n = self.cache, n_tokens
+        s = stream or torch.cuda.current_stream(c.dev)
+        abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
+                             self.x, self.x_scales, None, s)
+        self._project(self.wq, n, c.heads * LATENT, self.q, s)
+        self._project(self.wlatent, n, LATENT, self.latents, s)
+        c.plan(s)
+        c.append(self.latents, n, s)
+        return c.attend(self.q, n, max_q, max_kv, s)

@@ -595,3 +595,207 @@ def test_matvec_nan_stays_in_its_row(abi):
     keep = np.ones(64, bool)
     keep[7] = False
     assert np.array_equal(got[[0, 2, 4]][:, keep], clean[[0, 2, 4]][:, keep])
+
+
+def test_matvec_weights_beyond_two_gigabytes(abi):
+    """Row offsets past 2^31 bytes: only the last rows are not zero."""
+    k, n_out = 65536, 66000
+    codes = torch.zeros(n_out, k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n_out, k // 16), 0x38, dtype=torch.uint8, device="cuda")
+    codes[-3:] = 0x22  # ones
+    x = torch.ones(2, k, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((2, n_out), 9.0, device="cuda")
+    ws = fresh_ws(abi, abi.csa2_fp4_matvec_workspace_bytes(2, k, n_out))
+    abi.csa2_fp4_matvec(x, abi.X_BF16, None, k, 2, k, codes, scales, n_out, 1.0, out, abi.OUT_F32, ws, ws.numel(), None)
+    torch.cuda.synchronize()
+    assert (out[:, :-3] == 0).all() and (out[:, -3:] == k).all()
+
+
+# ------------------------------------------------- the attention once more
+@pytest.mark.parametrize("new,fmt", [(2, "fp4"), (40, "fp8")])
+def test_attention_cache_beyond_two_gigabytes(abi, new, fmt):
+    """Rows past 2^31 bytes of the latent planes, in the few-row kernel and over decoded tiles."""
+    s = attn_inputs(np.random.default_rng(21), [300], [new], 16, 64, fmt)
+    shift = (1 << 31) // (256 if fmt == "fp4" else 512) // 64 + 17  # pages
+    n_rows = len(s["codes"]) + 64 * shift
+    a = Attn(abi, s)
+    codes = torch.empty((n_rows, s["codes"].shape[1]), dtype=torch.uint8, device="cuda")
+    codes[64 * shift:] = a.codes
+    a.codes = codes
+    if fmt == "fp4":
+        scales = torch.empty((n_rows, 32), dtype=torch.uint8, device="cuda")
+        scales[64 * shift:] = a.scales
+        a.scales = scales
+    a.table = a.table + shift
+    a.call()
+    check_attn(*a.result(), s, 0)
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_attention_gives_up_and_recovers(abi, new):
+    """With a wait limit of 1 ns every bounded wait gives up: the status says so, copies and MMAs in flight are
+    waited for, and the next call is right."""
+    s = attn_inputs(np.random.default_rng(22), [500, 300], [new, 1], 16, 16, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    one = a.result()
+    check_attn(*one, s, 0)
+    abi.csa2_debug_wait_limit(1)
+    try:
+        a.call()
+        torch.cuda.synchronize()
+    finally:
+        abi.csa2_debug_wait_limit(0)
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.ERR_TIMEOUT
+    abi.csa2_status_reset(a.ws)
+    a.out.fill_(3.0)
+    a.call()
+    two = a.result()
+    assert np.array_equal(one[0], two[0]) and np.array_equal(one[1], two[1])
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+def test_attention_of_many_requests(abi):
+    """More requests than a warp's scan step, some without tokens, some without entries."""
+    rng = np.random.default_rng(23)
+    R = 150
+    new = rng.integers(0, 3, R)
+    kv = np.where(new > 0, rng.integers(0, 200, R), rng.integers(0, 50, R))
+    s = attn_inputs(rng, kv, new, 3, 8, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+
+
+@pytest.mark.parametrize("heads,new", [(64, 4), (64, 5), (128, 2), (1, 256), (1, 257), (100, 3)])
+def test_attention_on_both_sides_of_the_kernels_border(abi, heads, new):
+    """256 rows of a request go to the few-row kernel, more to the decoded tiles."""
+    s = attn_inputs(np.random.default_rng(heads + new), [new + 150, 140], [new, 1], heads, 16, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+
+
+# ------------------------------------------------------------ a whole step
+def layer_case(abi, fmt, window, seed=31):
+    from csa2_sparse_attention_gb300 import paged
+    g = torch.Generator().manual_seed(seed)
+    R, hidden, heads, page = 3, 256, 4, 16
+    cache = paged.PagedLatents(R, 64, 40, page, 12, heads=heads, fmt=fmt, window=window)
+    w = lambda *sh: torch.randn(*sh, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    layer = paged.PagedLayer(cache, hidden, (1 + 0.1 * torch.randn(hidden, generator=g)).to(torch.bfloat16).cuda(),
+                             w(heads * D, hidden), w(D, hidden))
+    return paged, g, cache, layer
+
+
+@pytest.mark.parametrize("fmt,window", [("fp4", 0), ("fp8", 20)])
+def test_step_over_a_paged_cache(abi, fmt, window):
+    """Prompt chunks, then decoding steps beside another chunk: every stage of the step against its 64-bit form on
+    what the stage before it left, and the plan against the whole history."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4 if fmt == "fp4" else abi.FMT_FP8, window)
+    hidden, heads, page = layer.hidden, cache.heads, cache.page_size
+    table, n_free = cache.table.cpu().numpy(), cache.n_pages
+    free = cache.free.cpu().numpy()
+    cached = np.zeros(3, np.int32)
+    for added in ([30, 0, 17], [1, 25, 1], [1, 1, 1], [0, 1, 31]):
+        added = np.array(added, np.int32)
+        n = int(added.sum())
+        cache.added.copy_(torch.from_numpy(added))
+        layer.residual[:n] = torch.randn(n, hidden, generator=g).to(torch.bfloat16)
+        res = layer.residual[:n].cpu()
+        x = torch.randn(n, hidden, generator=g).to(torch.bfloat16)
+        out, lse = layer.step(x.cuda(), n, int(added.max()), int((cached + added).max()))
+        torch.cuda.synchronize()
+        for name, st in cache.status().items():
+            assert st[0] == abi.OK, (name, st)
+        # norm
+        h = (x.float() + res.float()).to(torch.bfloat16)
+        assert torch.equal(layer.residual[:n].cpu(), h)
+        codes = layer.x[:n].view(torch.float8_e4m3fn).cpu()
+        xs = layer.x_scales[:n].cpu().numpy()
+        check_norm(h.double().numpy(), layer.norm_weight.double().cpu().numpy(), 0, codes.float().numpy(), xs[:, None], None)
+        # projections
+        for wt, got in ((layer.wq, layer.q[:n].flatten(1)), (layer.wlatent, layer.latents[:n])):
+            check_matvec(got.double().cpu().numpy(), codes, xs, wt[0].cpu().numpy(), wt[1].cpu().numpy(), 1.0, torch.bfloat16)
+        # plan
+        want = PO.page_plan(cached, added, page, table, free, n_free, cache.n_pages, cache.max_tokens)
+        table, n_free = want[0], want[5]
+        check_plan((cache.table.cpu().numpy(), cache.q_start.cpu().numpy(), cache.kv_len.cpu().numpy(), cache.slots.cpu().numpy(),
+                    cache.pos.cpu().numpy(), int(cache.n_free.item())), want)
+        # append
+        slots, pos = want[3][:n], want[4][:n]
+        lat = layer.latents[:n].double().cpu().numpy()
+        cc = cache.codes.cpu().numpy()
+        cs = None if cache.scales is None else cache.scales.cpu().numpy()
+        if fmt == "fp4":
+            oc, os_ = O.append_main_latent(lat, pos)
+            assert np.mean(cc[slots] != oc) < 1e-3 and np.mean(cs[slots] != os_) < 1e-3  # ties next to a border
+        else:
+            assert np.array_equal(cc[slots], O.append_swa_fp8(lat))
+        # attention
+        s = dict(q=layer.q[:n].cpu(), q_start=want[1], kv_len=want[2], codes=cc, scales=cs, table=table, page=page, fmt=fmt, T=n,
+                 H=heads, max_q=int(added.max()), max_kv=int(want[2].max()))
+        check_attn(out.double().cpu().numpy(), lse.double().cpu().numpy(), s, window)
+        cache.advance()
+        cached = want[2].copy()
+
+
+def test_step_captured_and_replayed_is_the_eager_step(abi):
+    """A decoding step in a CUDA graph, replayed over growing lengths (the plan takes pages inside the graph), equals
+    eager steps of another cache byte for byte."""
+    runs = []
+    for captured in (False, True):
+        paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+        chunk = torch.tensor([30, 9, 17], dtype=torch.int32)
+        cache.added.copy_(chunk)
+        x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+        layer.step(x, 56, 30, 30)
+        cache.advance()
+        cache.added.fill_(1)
+        tok = torch.zeros(3, layer.hidden, dtype=torch.bfloat16, device="cuda")
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        cache.workspace(3, 1, 64)
+        graph = torch.cuda.CUDAGraph()
+        if captured:
+            with torch.cuda.graph(graph, stream=st):
+                layer.step(tok, 3, 1, 64, torch.cuda.current_stream())
+                cache.advance()
+        got = []
+        for _ in range(5):
+            tok.copy_(torch.randn(3, layer.hidden, generator=g))
+            layer.residual.zero_()
+            torch.cuda.synchronize()
+            if captured:
+                with torch.cuda.stream(st):
+                    graph.replay()
+            else:
+                layer.step(tok, 3, 1, 64)
+                cache.advance()
+            torch.cuda.synchronize()
+            got += [cache.out[:3].clone(), cache.lse[:3].clone(), cache.table.clone(), cache.kv_len.clone(), cache.codes.clone()]
+        for name, s in cache.status().items():
+            assert s[0] == abi.OK, (name, s)
+        runs.append(got)
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+def test_plan_over_several_blocks_shares_its_ticket(abi):
+    """Many tokens (several blocks), the free count in place, call after call on one workspace."""
+    rng = np.random.default_rng(41)
+    cached, added, table, free, n_free, n_pages = plan_inputs(rng, [70] * 40, [700] * 40, 16, spare=5000)
+    t, nf = dev(table), dev(np.array([n_free], np.int32))
+    c, a, f = dev(cached), dev(added), dev(free)
+    qs = torch.zeros(41, dtype=torch.int32, device="cuda")
+    kl = torch.zeros(40, dtype=torch.int32, device="cuda")
+    sl, po = (torch.zeros(30000, dtype=torch.int64, device="cuda") for _ in range(2))
+    ws = fresh_ws(abi, abi.STATUS_BYTES)
+    for _ in range(3):
+        abi.csa2_page_plan(c, a, 40, 16, t, table.shape[1], f, n_pages, nf, nf, qs, kl, sl, po, 30000, ws, ws.numel(), None)
+        torch.cuda.synchronize()
+        want = PO.page_plan(cached, added, 16, table, free, n_free, n_pages, 30000)
+        n_free = want[5]
+        table = want[0]
+        check_plan((t.cpu().numpy(), qs.cpu().numpy(), kl.cpu().numpy(), sl.cpu().numpy(), po.cpu().numpy(), int(nf.item())), want)
