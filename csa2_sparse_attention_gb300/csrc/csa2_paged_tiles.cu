@@ -73,8 +73,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     PagedTilesSmem& S = *reinterpret_cast<PagedTilesSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
     const int half = (blockIdx.x >> 1) & 1, rank = blockIdx.x & 1;
-    grid_dep_wait();
     grid_dep_launch();
+    // The set-up and Q come before the wait for the decode kernel, this launch's
+    // predecessor: it starts its dependents only after its own wait, so all that
+    // the call's inputs come from is done by then.  (Nothing is written before.)
 
     if (warp == 0) paged_find(a, blockIdx.x >> 2, blockIdx.x == 0, S.work);
     __syncthreads();
@@ -135,8 +137,6 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         __syncwarp();
     };
     const uint8_t* x_src = a.tiles + tile0 * kPTileBytes + (1 - half) * (kPTileBytes / 2);
-    if (warp == kCopyWarp && nt > 0)
-        for (int b = 0; b < 2; ++b) copy_block(&S.full_x[0][b], 0, b, x_src, nullptr);
 
     // ---- Q to f16 times a power of two per row: the other half to its place, the
     // own half by way of the second group of latents into TMEM
@@ -153,6 +153,9 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         }
     }
     fence_async_smem();
+    grid_dep_wait();  // the tiles
+    if (warp == kCopyWarp && nt > 0)
+        for (int b = 0; b < 2; ++b) copy_block(&S.full_x[0][b], 0, b, x_src, nullptr);
     __syncthreads();
 
     if (warp < kPSoftWarps) {
