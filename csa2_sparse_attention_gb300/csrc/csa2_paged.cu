@@ -57,8 +57,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // go in items of 64 rows (csa2_paged_rows.cu), longer ones in pairs of 128
 // rows over decoded tiles (csa2_paged_tiles.cu) where those need no more than
 // 1 GB.  Decoding a key once pays from a few items on: 1024 tokens x 64 heads
-// over 16K entries take 1.86 ms from tiles and ROWS_MS in items of 64 rows; a
-// single token per request would write and read 1 KB per key for nothing.
+// over 16K entries take 1.81 ms from tiles and 2.70 ms in items of 64 rows.  The
+// border, 64 heads over 8K entries: 16 requests of 4 tokens (4 items each) 124 us
+// from tiles and 122 us without, of 8 tokens 181 and 209 us; single tokens would
+// write and read 1 KB per key for nothing (115 and 45 us).
 // The split count is the one with the least time by: waves of 152 CTAs, each a
 // start and end of 8 us and a time per key tile, plus the merge's pass over the
 // partial outputs.
@@ -71,6 +73,7 @@ constexpr size_t kPMaxTileBytes = size_t(1) << 30;
 static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
     PagedPlan p{};
     if (window >= max_kv) window = 0;
+    if (max_q > n_tokens) max_q = int32_t(n_tokens);
     const int64_t rows = n_tokens * n_heads;
     p.item = 64;
     int64_t ctas = 1;  // per item and split
@@ -122,7 +125,7 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
 
 static bool paged_sizes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
     return n_tokens >= 0 && n_tokens <= (int64_t(1) << 22) && n_heads >= 1 && n_heads <= 128 && n_req >= 0 &&
-           n_req <= (1 << 20) && max_q >= 0 && max_kv >= 0 && window >= 0;
+           n_req <= (1 << 20) && max_q >= 0 && max_kv >= 0 && max_kv <= (1 << 30) && window >= 0;
 }
 
 }  // namespace csa2
@@ -131,7 +134,7 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
                                                   int32_t max_kv, int window) {
-    return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window) 
+    return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window)
                ? paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window).total
                : 0;
 }

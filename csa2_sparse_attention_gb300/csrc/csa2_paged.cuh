@@ -18,9 +18,17 @@ constexpr int kPSoftWarps = 4;
 // with a NaN latent.
 constexpr int64_t kPTileBytes = int64_t(kPN) * kPD * 2;
 constexpr int kPFlagBytes = 32;
+// Probabilities enter the products in f16 as 2^(l - b), with b lowered by this
+// much below the row's maximum when it is set, and set again once a logit lies
+// kPGrow above it: P reaches 2^15 at most and the largest one 2^7 at least, so
+// that what f16 rounds below its normal range (2^-25 each) is 2^-32 of the sum.
+// (With b at the maximum it was 2^-25: half a million keys of probability just
+// under that, 1.5 % of the output together, all rounded to zero.)
+constexpr float kPBase = 7.f, kPGrow = 15.f;
 
-// n / d for 0 <= n < 2^31 by a multiplication: mul = floor(2^(31 + s) / d) + 1
-// with 2^s >= d overshoots 1 / d by less than 2^-31 d / 2^31 of n's step.  (The
+// n / d for 0 <= n < 2^31 by a multiplication: with mul = floor(2^(31 + s) / d) + 1
+// and 2^s >= d, mul d = 2^(31 + s) + e, 0 < e <= d, so n mul / 2^(31 + s) lies
+// above n / d by n e / (d 2^(31 + s)) < 1 / d: the floor is that of n / d.  (The
 // set-up of a CTA runs once through code that the instruction cache does not
 // hold: a division by an unknown number is 25 instructions, this is three.)
 struct FastDiv {

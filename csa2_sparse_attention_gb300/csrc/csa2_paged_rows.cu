@@ -18,11 +18,11 @@
 //
 //   smem  Q 64 KB, C 128 KB (four blocks of 128 channels), P^T 16 KB      TMEM  O^T 256, S^T 64
 //
-// Softmax: a thread per key, the 64 rows in its registers.  The running maxima
-// stand in shared memory; a tile whose logits all stay below them + 8 (log2)
+// Softmax: a thread per key, the 64 rows in its registers.  The rows' bases
+// stand in shared memory; a tile whose logits all stay below kPGrow (log2) above
 // needs no reduction at all, since each thread sums its own key's
 // probabilities row by row over all tiles and the 128 threads' sums are joined
-// once at the end.  A maximum that grew by more (and the first tile) takes the
+// once at the end.  A logit above that (and the first tile) takes the
 // reduction over the keys and rescales O^T and the sums.
 #include "csa2_paged.cuh"
 #include "csa2_timer.cuh"
@@ -49,7 +49,7 @@ struct PagedRowsSmem {
     uint8_t q[kRRows * kPD * 2];  // 8-row groups of 8192 B, 8-channel chunks of 128 B
     uint8_t c[4][kRBlock];        // a tile's channels in blocks of 128
     uint8_t p[kPN * kRRows * 2];  // P^T: 8-key groups of 1024 B, 8-row chunks of 128 B
-    float2 row[kRRows];           // a row's factor of the raw logits and its maximum (log2 domain; 0 before any key)
+    float2 row[kRRows];           // a row's factor of the raw logits and its base (log2 domain; 0 before any key)
     int2 keys[kRRows];            // keys [x, y) that a row sees
     float alpha[kRRows], delta[kRRows];
     float red[4][kRRows];
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             tmem_ld32(tm + kRColS, reinterpret_cast<uint32_t(&)[32]>(x[0]));
             tmem_ld32(tm + kRColS + 32, reinterpret_cast<uint32_t(&)[32]>(x[1]));
             tmem_ld_wait();
-            // to the log2 domain, against the row's maximum
+            // to the log2 domain, against the row's base
             float top = -INFINITY;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             }
 #pragma unroll
             for (int c = 0; c < 32; ++c) top = fmaxf(top, fmaxf(x[0][c], x[1][c]));
-            if (soft_or(top > 8.f) || S.fresh > 0) {  // (S.fresh was written before a barrier that all have passed)
-                // maxima over the keys; rows that grew by more than 2^8, or see their first key, move theirs
+            if (soft_or(top > kPGrow) || S.fresh > 0) {  // (S.fresh was written before a barrier that all have passed)
+                // maxima over the keys; rows with a logit above kPGrow, or that see their first key, move their base
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[32];
@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                     const bool mine = j == 0 || (was_fresh && S.alpha[tid] < 0.f);
                     float d = 0.f, al = 1.f;
                     if (mine) {
-                        if (t > -INFINITY) d = t, al = 0.f;
+                        if (t > -INFINITY) d = t - kPBase, al = 0.f;
                         else al = -1.f;
-                    } else if (t > 8.f) {
-                        d = t;
-                        al = ex2(-t);
+                    } else if (t > kPGrow) {
+                        d = t - kPBase;
+                        al = ex2(-d);
                     }
                     still = tid < n_row && al < 0.f;
                     S.row[tid].y = m + d;

@@ -6,7 +6,13 @@
 // Rows are (token, head) pairs: 128 consecutive rows of a request make a tile
 // of the tensor cores' M, whatever the number of heads.  All heads share the
 // latents, so a key costs 2048 FLOPs a row against 288 bytes: the tensor cores
-// bound the kernel even for single tokens.
+// bound the kernel.
+//
+// The latents are decoded once per call (paged_decode_kernel, at the end of
+// this file) to tiles of 128 keys in f16, exact, laid out as shared memory holds
+// them.  With the decoding inside the attention kernel every pair of CTAs did
+// it again, 12,600 warp instructions a key tile, and 1024 tokens x 64 heads over
+// 16K entries took 2.7 ms (csa2_paged_rows.cu still does) instead of 1.85.
 //
 // The fp32 accumulator of 128 rows x 512 channels would fill TMEM (512
 // columns) and leave no room for the logits, so a CTA takes 128 rows and one
@@ -21,21 +27,29 @@
 //
 // Keys go in tiles of 128: an M = 128 MMA of K = 16 takes 64 clocks for any
 // N up to 128 (measured 64-69) and 128 for N = 256, so S wants 128 keys and O
-// 256 channels at once.  Three roles:
-//   producers (8 warps)  read the rows through the page table and decode them
-//       to f16 (exact) into shared memory, the other half's channels X first,
-//       then, as the logits' MMAs release them, the own half's Y in the same
-//       group.  One copy of Y serves S (K-major) and O (MN-major).
+// 256 channels at once.  Two CTAs with consecutive row tiles and the same half
+// form a cluster and copy half of every tile into both: alone, each took 128 KB
+// per tile, 7.8 TB/s from L2 over the GPU, which bounded the kernel (2.25 ms).
+// Three roles:
+//   copy warp  the other half's channels X of a tile first, then, as the logits'
+//       MMAs release them, the own half's Y into the same group.  One copy of Y
+//       serves S (K-major) and O (MN-major).
 //   MMA warp, per tile:  S += Q_X X^T, then O += P Y of the previous tile,
 //       then S += Q_Y Y^T: the softmax of a tile runs under the next tile's
-//       S_X, and the decoding of Y under the previous tile's O.
+//       S_X, and the copy of Y under the previous tile's O.
 //   softmax (4 warps, a thread per row)  takes S out of TMEM, keeps the
-//       running maximum and sum in fp32, writes P as f16 to shared memory.  O
-//       is rescaled only when a row's maximum grew by more than 2^8: P stays
-//       below 2^8 and the sums in fp32, so nothing is lost by waiting.
+//       running base and sum in fp32, writes P as f16 to shared memory.  O is
+//       rescaled only when a logit lies 2^15 above the base (kPGrow).
 // P is rounded to f16 (2^-11 relative, an eighth of the step of the bf16
 // output); Q goes to f16 times a power of two per row (exact down to 2^-28 of
 // the row's maximum).
+//
+// A tile takes about 4300 clocks, 3072 of them MMAs: S has one place in TMEM,
+// so the next logits wait for the softmax to have read it (about 500 clocks),
+// and the tensor cores run at 1.1-1.2 PFLOP/s of their work (one GPU: 1.87
+// measured for a large matrix product).  512 tokens x 64 heads over 8K entries:
+// 577 us, 983 TFLOP/s without the third product; 1024 tokens over 16K: 1.85 ms,
+// 1150 TFLOP/s.
 //
 // Long axes with few rows are split over CTAs in chunks of key tiles that the
 // host sizes; the partial outputs are joined by paged_merge_kernel.
@@ -76,12 +90,16 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     grid_dep_launch();
     // The set-up and Q come before the wait for the decode kernel, this launch's
     // predecessor: it starts its dependents only after its own wait, so all that
-    // the call's inputs come from is done by then.  (Nothing is written before.)
+    // the call's inputs come from is done by then, and nothing but the status word
+    // is written before.
 
     if (warp == 0) paged_find(a, blockIdx.x >> 2, blockIdx.x == 0, S.work);
     __syncthreads();
     const int64_t req = S.work.req;
-    if (req < 0) return;
+    if (req < 0) {
+        grid_dep_wait();  // (a launch behind this one may rely on the decode kernel's end)
+        return;
+    }
     const PagedReq rq = S.work.rq;
     const int32_t nt = S.work.nt, key0 = S.work.key0, split = S.work.split, splits = S.work.splits;
     // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
@@ -245,9 +263,9 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 for (int b = 0; b < 4; ++b)
                     mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(s[b][i]), __uint_as_float(s[b][i + 1])));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sm_eff;
-            const bool grew = top > m + 8.f;
+            const bool grew = top > m + kPGrow;
             if (__any_sync(0xffffffffu, grew)) {
-                const float mn = grew ? top : m;
+                const float mn = grew ? top - kPBase : m;
                 const float alpha = !grew ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
                 if (j > 0) {  // every MMA before S_Y of this tile is done, the previous O among them
 #pragma unroll 1
@@ -449,10 +467,9 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Decodes the pages of every request once into tiles of 128 keys (see
-// kSrcTiles), for calls whose requests have several row tiles: each of them
-// would decode every key again, and the decoding, not the MMAs, bounds the
-// kernel then (12,600 warp instructions a key tile).  grid (tiles, requests).
+// Decodes the pages of every request once into tiles of 128 keys (layout:
+// kPTileBytes).  1.8 KB of traffic per FP4 key: 2 % of the attention's time at 512
+// tokens x 64 heads.  grid (tiles, requests).
 template <bool FP8>
 __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
     __shared__ uint32_t s_nan[4], s_hidden[4];

@@ -370,9 +370,11 @@ csa2_status csa2_page_plan(const int32_t* cached, const int32_t* added, int64_t 
  * request r sits at position t = kv_len[r] - (q_start[r+1] - q_start[r]) + i
  * and sees positions max(0, t + 1 - window) .. t (window 0: all up to t):
  *   l_p = sm_scale * q . c_p,  o = sum softmax(l)_p c_p.
- *   q_bf16   [n_tokens][n_heads][512] bf16; n_heads 1..128.
+ *   q_bf16   [n_tokens][n_heads][512] bf16; n_heads 1..128, n_tokens up to
+ *            2^22, n_req up to 2^20.
  *   q_start  [n_req + 1] int32, kv_len [n_req] int32 (csa2_page_plan's).
- *   max_q, max_kv: host upper bounds of a request's tokens and entries.
+ *   max_q, max_kv: host upper bounds of a request's tokens and entries
+ *            (max_kv up to 2^30).
  *   fmt      CSA2_FMT_FP4: codes [n_rows][256] and scales [n_rows][32], as
  *            csa2_quantize_append writes them (CSA2_LAYOUT_ROWS);
  *            CSA2_FMT_FP8: codes are E4M3 rows [n_rows][512], scales NULL.
@@ -429,7 +431,7 @@ csa2_status csa2_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residu
  *   codes, scales  W: n_out rows of k channels, [n_out][k/2] E2M1 codes and
  *                [n_out][k/16] E4M3 scales: csa2_quantize_append of the
  *                weights in CSA2_LAYOUT_ROWS, as n_out*k/128 rows of 128.
- *   k            a multiple of 128, up to 65536.  n rows: any number; the
+ *   k            a multiple of 128, up to 65536.  n rows: up to 65536; the
  *                weights are read once for each 16 rows.
  *   out          [n][n_out], bf16 (CSA2_OUT_BF16) or fp32 (CSA2_OUT_F32).
  * ws: csa2_fp4_matvec_workspace_bytes(n, k, n_out) bytes (0 for bad sizes).

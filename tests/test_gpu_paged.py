@@ -288,6 +288,41 @@ def test_attention_growing_logits(abi):
     check_attn(*a.result(), s, 0)
 
 
+@pytest.mark.parametrize("new,reqs", [(1, 152), (152, 1)])
+def test_attention_many_small_probabilities(abi, new, reqs):
+    """Half a million keys of probability 2^-25.3 next to one of about 1: each is below f16's range, together they are
+    1.3 % of the output.  (As many rows as there are multiprocessors, so that the keys are not split: in a split of
+    their own their probabilities are not small.)  The cache holds two pages: all but the first are the same one.
+
+    Such a key enters the products with an error of at most 2^-25 against a largest probability of at least 2^7
+    (2^-32 each, n 2^-32 = 2^-13 for all), the sums and the rest as in check_attn."""
+    n = 1 << 19
+    codes = np.zeros((128, D), np.uint8)
+    codes[:64, 2] = 0x38    # page 0: 1.0 in channel 2
+    codes[64, [0, 1]] = 0x38  # page 1: 1.0 in channels 0 and 1, at its first entry
+    codes[65:, 2] = 0x38
+    table = np.zeros((reqs, n // 64), np.int32)
+    table[:, 0] = 1
+    q = torch.zeros(reqs * new, 64, D, dtype=torch.bfloat16)
+    q[:, :, 0] = 25.3 * np.log(2.0) / SM
+    q0 = float(q[0, 0, 0])
+    s = dict(q=q, q_start=np.arange(reqs + 1, dtype=np.int32) * new, kv_len=np.full(reqs, n, np.int32), codes=codes, scales=None,
+             table=table, page=64, fmt="fp8", T=reqs * new, H=64, max_q=new, max_kv=n)
+    a = Attn(abi, s)
+    a.call()
+    out, lse = a.result()
+    others = n - new + np.arange(new, dtype=np.float64)  # keys that a token sees besides the first
+    p = others * np.exp(-q0 * SM)
+    want = np.zeros((reqs, new, 64, D))
+    want[..., :2] = (1 / (1 + p))[None, :, None, None]
+    want[..., 2] = (p / (1 + p))[None, :, None]
+    d = 64 * 2.0 ** -24 * q0 * SM + 2.0 ** -21
+    tol = 2 * d + 2.0 ** -11 * want + n * 2.0 ** -32 + (2.0 ** -8 + n * 2.0 ** -24) * want
+    assert 0.012 < want[..., 2].min() and (np.abs(out.reshape(want.shape) - want) <= tol).all()
+    wlse = np.broadcast_to((q0 * SM + np.log1p(p))[None, :, None], (reqs, new, 64))
+    assert (np.abs(lse.reshape(wlse.shape) - wlse) <= d + n * 2.0 ** -24 + 2.0 ** -22 * (1 + wlse)).all()
+
+
 @pytest.mark.parametrize("fmt", ["fp4", "fp8"])
 def test_attention_leaves_out_what_is_masked(abi, fmt):
     """NaN and the largest values in rows behind the sequence, outside the window, in later tokens' entries and in

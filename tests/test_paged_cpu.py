@@ -53,7 +53,8 @@ def test_page_plan_refusals(abi, kw, status):
     (dict(kv_len=F + 4), "I"), (dict(codes=None), "I"), (dict(table=None), "I"), (dict(out=None), "I"), (dict(lse=F + 4), "I"),
     (dict(window=-1), "I"), (dict(sm_scale=0.0), "I"), (dict(sm_scale=float("nan")), "I"), (dict(sm_scale=float("inf")), "I"),
     (dict(n_tokens=-1), "I"), (dict(n_req=-1), "I"), (dict(max_q=-1), "I"), (dict(max_kv=-1), "I"), (dict(n_rows=-1), "I"),
-    (dict(max_pages=1 << 31), "I"), (dict(n_tokens=(1 << 22) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W")])
+    (dict(max_pages=1 << 31), "I"), (dict(n_tokens=(1 << 22) + 1), "U"), (dict(max_kv=(1 << 30) + 1), "U"),
+    (dict(n_req=(1 << 20) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W")])
 def test_paged_attn_refusals(abi, kw, status):
     c0 = abi.csa2_launch_count()
     assert abi.lib.csa2_paged_attn(*args(ATTN, **kw)) == {"U": 2, "I": 1, "W": 6}[status]
@@ -98,6 +99,14 @@ def test_empty_calls_launch_nothing(abi):
     assert abi.lib.csa2_rmsnorm_fp8(*args(NORM, n=0)) == abi.OK
     assert abi.lib.csa2_fp4_matvec(*args(MATVEC, n=0)) == abi.OK
     assert abi.csa2_launch_count() == c0
+
+
+def test_paged_attn_workspace_of_the_largest_bounds(abi):
+    """No size overflows: a bound on a request's tokens above the call's own changes nothing."""
+    size = abi.csa2_paged_attn_workspace_bytes
+    assert size(40, 128, 3, 2 ** 31 - 1, 1 << 30, 0) == size(40, 128, 3, 40, 1 << 30, 0) >= 256
+    assert size(1 << 22, 128, 1 << 20, 1 << 22, 1 << 30, 2 ** 31 - 1) >= 256
+    assert size(4, 64, 2, 4, (1 << 30) + 1, 0) == 0
 
 
 # ------------------------------------------------- the 64-bit forms by hand
