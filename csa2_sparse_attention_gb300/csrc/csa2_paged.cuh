@@ -149,53 +149,64 @@ struct PagedWork {
     int32_t item, split, splits;
     int32_t nt, key0;            // key tiles (0: nothing to see) and the first key
 };
-// Finds it for the grid's `place`, in one whole warp (by a scan of the requests'
-// items), into shared memory.  `all`: look at every request, so that each one's
+// Finds it for the grid's `place`, by a scan of the requests' items, into shared
+// memory; all WARPS warps of the block call it and synchronize behind it.  Up to
+// 32 requests are the first warp's alone, more go to all warps 32 each (`sums`
+// [2][WARPS] in shared memory): by one warp, 1024 requests took 0.5 us for every
+// 32, 9 of a CTA's 32 us.  `all`: look at every request, so that each one's
 // problems are recorded.
-__device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bool all, PagedWork& w) {
-    const int lane = lane_id();
-    int64_t base = 0;
-    bool found = false;
-    if (lane == 0) w.req = -1;
+template <int WARPS>
+__device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bool all, PagedWork& w, int64_t* sums) {
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    const bool wide = a.n_req > 32;
+    if (threadIdx.x == 0) w.req = -1;
     __syncwarp();
+    if (!wide && warp != 0) return;
+    int64_t base = 0;
 #pragma unroll 1
-    for (int64_t r0 = 0; r0 < a.n_req; r0 += 32) {
-        const int64_t r = r0 + lane;
+    for (int64_t r0 = 0; r0 < a.n_req; r0 += 32 * WARPS) {
+        const int64_t r = r0 + 32 * warp + lane;
         int32_t n = 0, ns = 1;
         PagedReq rq;
         if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr)) {
             ns = paged_splits(a, paged_key_tiles(rq.nq, rq.len, a.window, a.item_tokens));
             n = (rq.nq * a.heads + a.item - 1) >> a.item_log2;
         }
-        int64_t inc = int64_t(n) * ns;
+        const int64_t mine = int64_t(n) * ns;
+        int64_t inc = mine, before = base;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += u;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > place);
-        if (hit != 0 && !found) {
-            found = true;
-            if (lane == __ffs(hit) - 1) {
-                const uint32_t local = uint32_t(place - base - (inc - int64_t(n) * ns));
-                const uint32_t back = local / uint32_t(ns);
-                const int32_t item = n - 1 - int32_t(back), split = int32_t(local - back * ns);  // the most keys first
-                int32_t begin, end, tiles;
-                paged_item_keys(a, rq, item, begin, end, tiles);
-                const int32_t splits = paged_splits(a, tiles), j0 = split * a.chunk;
-                if (split < splits) {
-                    w.rq = rq;
-                    w.req = int32_t(r);
-                    w.item = item;
-                    w.split = split;
-                    w.splits = splits;
-                    w.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;
-                    w.key0 = begin + j0 * kPN;
-                }
+        if (wide) {
+            int64_t* at = sums + ((r0 / (32 * WARPS)) & 1) * WARPS;  // two halves in turn: one barrier a round is enough
+            if (lane == 31) at[warp] = inc;
+            __syncthreads();
+#pragma unroll 1
+            for (int v = 0; v < WARPS; ++v) {
+                if (v < warp) before += at[v];
+                base += at[v];
             }
-            if (!all) break;
         }
-        base += __shfl_sync(0xffffffffu, inc, 31);
+        const int64_t local = place - before - (inc - mine);
+        if (local >= 0 && local < mine) {
+            const uint32_t back = uint32_t(local) / uint32_t(ns);
+            const int32_t item = n - 1 - int32_t(back), split = int32_t(uint32_t(local) - back * ns);  // the most keys first
+            int32_t begin, end, tiles;
+            paged_item_keys(a, rq, item, begin, end, tiles);
+            const int32_t splits = paged_splits(a, tiles), j0 = split * a.chunk;
+            if (split < splits) {
+                w.rq = rq;
+                w.req = int32_t(r);
+                w.item = item;
+                w.split = split;
+                w.splits = splits;
+                w.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;
+                w.key0 = begin + j0 * kPN;
+            }
+        }
+        if (!wide || (base > place && !all)) break;
     }
 }
 

@@ -58,6 +58,7 @@ struct PagedRowsSmem {
     uint64_t full[2], empty[4], s_full, p_full, o_done, drain;  // full: of each half of the channels
     uint32_t tmem;
     PagedWork work;
+    int64_t sums[2 * kRThreads / 32];
 };
 static_assert(sizeof(PagedRowsSmem) + 1024 <= 227 * 1024, "shared memory of the few-row paged attention");
 
@@ -98,9 +99,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == 0) {
-        paged_find(a, blockIdx.x, blockIdx.x == 0, S.work);
-    } else if (warp == kRMmaWarp) {
+    paged_find<kRThreads / 32>(a, blockIdx.x, blockIdx.x == 0, S.work, S.sums);
+    if (warp == kRMmaWarp) {
         if (lane == 0) {
             for (int b = 0; b < 4; ++b) mbar_init(&S.empty[b], 1);
             for (int b = 0; b < 2; ++b) mbar_init(&S.full[b], kRProdWarps / 2);

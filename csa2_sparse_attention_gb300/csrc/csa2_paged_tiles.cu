@@ -74,6 +74,7 @@ struct PagedTilesSmem {
     uint64_t s_full, s_free, p_full, o_done, q_done, drain;
     uint32_t tmem;
     PagedWork work;
+    int64_t sums[2 * kPTileThreads / 32];
 };
 static_assert(sizeof(PagedTilesSmem) + 1024 <= 227 * 1024, "shared memory of the paged attention");
 static_assert(kPM * (kPHalf * 4 + 16) <= 2 * kPN * kPHalf * 2 + kPM * kPN * 2, "the epilogue's rows in the latents' and P's place");
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     // the call's inputs come from is done by then, and nothing but the status word
     // is written before.
 
-    if (warp == 0) paged_find(a, blockIdx.x >> 2, blockIdx.x == 0, S.work);
+    paged_find<kPTileThreads / 32>(a, blockIdx.x >> 2, blockIdx.x == 0, S.work, S.sums);
     __syncthreads();
     const int64_t req = S.work.req;
     if (req < 0) {
