@@ -10,114 +10,155 @@ namespace csa2 {
 
 constexpr int kPSms = 152;  // multiprocessors the split is planned for
 
-// Joins the splits of a row: weights 2^(lse_s - max lse) over the normalized
-// partial outputs.  128 threads per row, 4 channels each; rows whose tile had
-// one split were written by the attention kernel.
+// Joins the splits of a kernel's rows: weights 2^(lse_s - max lse) over the
+// normalized partial outputs.  128 threads per row, 4 channels each; rows whose
+// tile had one split were written by the attention kernel.
+// Two rows per CTA, or eight where most of them may not be there.
+inline __host__ __device__ int paged_merge_rows(const PagedArgs& a) { return a.behind ? 8 : 2; }
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = int64_t(blockIdx.x) * 2 + (threadIdx.x >> 7);
     const int t = threadIdx.x & 127;
-    if (row >= a.rows) return;
-    const int32_t tok = int32_t(row) / a.by_heads;
-    int64_t lo = 0, hi = a.n_req;  // the last request that starts at or before the token
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.q_start[mid] <= tok) lo = mid;
-        else hi = mid;
+#pragma unroll 1
+    for (int i = threadIdx.x >> 7; i < paged_merge_rows(a); i += 2) {
+        const int64_t prow = int64_t(blockIdx.x) * paged_merge_rows(a) + i;  // of the partial outputs
+        if (prow >= a.part_rows) return;
+        int64_t req = 0;
+        if (a.behind) {
+            req = int32_t(prow) / a.by_few;
+        } else {  // the last request that starts at or before the token
+            const int32_t tok = int32_t(prow) / a.by_heads;
+            int64_t hi = a.n_req;
+            while (hi - req > 1) {
+                const int64_t mid = (req + hi) / 2;
+                if (a.q_start[mid] <= tok) req = mid;
+                else hi = mid;
+            }
+        }
+        PagedReq rq;
+        if (!paged_request(a, req, rq, nullptr) || !paged_mine(a, rq)) continue;
+        const int64_t at = prow - (a.behind ? req * a.few_rows : int64_t(rq.q0) * a.heads);  // of the request's rows
+        if (at < 0 || at >= int64_t(rq.nq) * a.heads) continue;
+        int32_t begin, end, tiles;
+        paged_item_keys(a, rq, int32_t(at) >> a.item_log2, begin, end, tiles);
+        const int32_t splits = paged_splits(a, tiles);
+        if (splits == 1) continue;
+        const int64_t row = int64_t(rq.q0) * a.heads + at;
+        float m = -INFINITY;
+        for (int32_t s = 0; s < splits; ++s) m = fmaxf(m, a.part_lse[s * a.part_rows + prow]);
+        float w = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int32_t s = 0; s < splits; ++s) {
+            const float ls = a.part_lse[s * a.part_rows + prow];
+            const float f = ls == -INFINITY ? 0.f : ex2(ls - m);
+            const float4 v = reinterpret_cast<const float4*>(a.part_o + (s * a.part_rows + prow) * kPD)[t];
+            w += f;
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = w == 0.f ? 0.f : 1.0f / w;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        reinterpret_cast<uint2*>(a.out + row * kPD * 2)[t] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        if (a.lse && t == 0) a.lse[row] = w == 0.f ? -INFINITY : (m + log2f(w)) * kLn2;
     }
-    PagedReq rq;
-    if (!paged_request(a, lo, rq, nullptr) || tok < rq.q0 || tok >= rq.q0 + rq.nq) return;
-    int32_t begin, end, tiles;
-    paged_item_keys(a, rq, int32_t(row - int64_t(rq.q0) * a.heads) >> a.item_log2, begin, end, tiles);
-    const int32_t splits = paged_splits(a, tiles);
-    if (splits == 1) return;
-    float m = -INFINITY;
-    for (int32_t s = 0; s < splits; ++s) m = fmaxf(m, a.part_lse[s * a.rows + row]);
-    float w = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int32_t s = 0; s < splits; ++s) {
-        const float ls = a.part_lse[s * a.rows + row];
-        const float f = ls == -INFINITY ? 0.f : ex2(ls - m);
-        const float4 v = reinterpret_cast<const float4*>(a.part_o + (s * a.rows + row) * kPD)[t];
-        w += f;
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z);
-        o.w = fmaf(f, v.w, o.w);
-    }
-    const float inv = w == 0.f ? 0.f : 1.0f / w;
-    const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    reinterpret_cast<uint2*>(a.out + row * kPD * 2)[t] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-    if (a.lse && t == 0) a.lse[row] = w == 0.f ? -INFINITY : (m + log2f(w)) * kLn2;
 }
 
 // How a call runs, from the host's bounds alone.  Requests of up to 256 rows
 // go in items of 64 rows (csa2_paged_rows.cu), longer ones in pairs of 128
 // rows over decoded tiles (csa2_paged_tiles.cu) where those need no more than
-// 1 GB.  Decoding a key once pays from a few items on: 1024 tokens x 64 heads
+// 4 GB.  Decoding a key once pays from a few items on: 1024 tokens x 64 heads
 // over 16K entries take 1.81 ms from tiles and 2.70 ms in items of 64 rows.  The
 // border, 64 heads over 8K entries: 16 requests of 4 tokens (4 items each) 124 us
 // from tiles and 122 us without, of 8 tokens 181 and 209 us; single tokens would
-// write and read 1 KB per key for nothing (115 and 45 us).
-// The split count is the one with the least time by: waves of 152 CTAs, each a
-// start and end of 8 us and a time per key tile, plus the merge's pass over the
-// partial outputs.
-struct PagedPlan {
-    int32_t chunk, splits, span, item;
+// write and read 1 KB per key for nothing (115 and 45 us).  Tiles run
+// requests of any length; beside them the few-row kernel takes the short ones
+// where the call's tokens say that there are enough of those, by a sixth of the
+// longest request per request, or three quarters from 16 key tiles on.  64 heads,
+// us with both kernels and with tiles alone:
+//   512 tokens + 63 single ones, 8K   730   986     + 15 single ones   643  621
+//   256 tokens + 31 single ones, 32K 1320  1862
+//   100 tokens + 31 single ones, 500   32    48     16 x 100, 1K       360  354
+//   8 x 64 + 24 single ones, 1K       147   141     8 x 64 + 8, 1K     150  133
+// 16 heads, 8 x 64 + 8 single ones: 4K 128 and 171, 2K 84 and 98, 1K 63 and 63.
+// The split count of each is the one with the least time by: waves of 152 CTAs,
+// each a start and end of 8 us and a time per key tile, plus the merge's pass
+// over the partial outputs.
+struct PagedShare {  // of one of the kernels
+    int32_t chunk, splits;
     int64_t grid;
-    size_t part_lse, part_o, tiles, flags, total;
 };
-constexpr size_t kPMaxTileBytes = size_t(1) << 30;
-static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
-    PagedPlan p{};
-    if (window >= max_kv) window = 0;
-    if (max_q > n_tokens) max_q = int32_t(n_tokens);
-    const int64_t rows = n_tokens * n_heads;
-    p.item = 64;
-    int64_t ctas = 1;  // per item and split
-    if (paged_items(max_q, n_heads, 64) > 4) {
-        int64_t span = (max_kv + kPN - 1) / kPN;
-        if (window > 0) {  // from the first token's window to the last token
-            const int64_t w = (int64_t(window) + max_q + 7 + kPN - 1) / kPN;
-            span = span < w ? span : w;
-        }
-        if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) {
-            p.span = int32_t(span);
-            p.item = 256;
-            ctas = 4;
-        }
-    }
-    int64_t items = rows / p.item + n_req;  // each request rounds up
-    const int64_t each = n_req * paged_items(max_q, n_heads, p.item);
-    items = items < each ? items : each;
-    ctas *= items;
-    const int32_t nt = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, p.item));
-    const double tile_us = p.span ? 1.9 : 2.9;
-    p.chunk = nt > 0 ? nt : 1;
+static PagedShare paged_share(int64_t planned, int64_t most, int32_t nt, double tile_us, double merge_rows) {
+    PagedShare p{nt > 0 ? nt : 1, 1, most};
     double best = 1e30;
     for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
         const int32_t chunk = (nt + s - 1) / s;
         if (s > 1 && (nt + chunk - 1) / chunk != s) continue;
-        const double waves = double((ctas * s + kPSms - 1) / kPSms);
+        const double waves = double((planned * s + kPSms - 1) / kPSms);
         double us = waves * (8.0 + tile_us * chunk);
-        if (s > 1) us += 4.0 + double(rows) * s * kPD * 4 * 2 / 4e6;
+        if (s > 1) us += 4.0 + merge_rows * s * kPD * 4 * 2 / 4e6;
         if (us < best) {
             best = us;
             p.chunk = chunk > 0 ? chunk : 1;
         }
     }
     p.splits = nt > p.chunk ? (nt + p.chunk - 1) / p.chunk : 1;
-    p.grid = ctas * p.splits;
+    p.grid = most * p.splits;
+    return p;
+}
+struct PagedPlan {
+    PagedShare tiles{1, 1, 0}, few{1, 1, 0};  // grid 0: not launched
+    int32_t span, few_rows;
+    size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, total;
+};
+constexpr size_t kPMaxTileBytes = size_t(4) << 30;
+constexpr int32_t kPFewRows = 256;
+static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
+    PagedPlan p{};
+    if (window >= max_kv) window = 0;
+    if (max_q > n_tokens) max_q = int32_t(n_tokens);
+    const int64_t rows = n_tokens * n_heads;
+    if (int64_t(max_q) * n_heads > kPFewRows) {
+        int64_t span = (max_kv + kPN - 1) / kPN;
+        if (window > 0) {  // from the first token's window to the last token
+            const int64_t w = (int64_t(window) + max_q + 7 + kPN - 1) / kPN;
+            span = span < w ? span : w;
+        }
+        if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) p.span = int32_t(span);
+    }
+    auto items = [&](int32_t q, int32_t item) {  // each request rounds up
+        const int64_t all = rows / item + n_req, each = n_req * paged_items(q, n_heads, item);
+        return all < each ? all : each;
+    };
+    int32_t tile_keys = 0;
+    if (p.span > 0) {
+        const int64_t n = 4 * items(max_q, 256);
+        tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256));
+        p.tiles = paged_share(n, n, tile_keys, 1.9, double(rows));
+    }
+    const bool beside = p.span > 0;
+    const int64_t padded = n_req * max_q;
+    if (!beside || n_tokens <= padded / 6 || (tile_keys >= 16 && n_tokens <= padded / 4 * 3)) {
+        const int32_t q = beside ? kPFewRows / n_heads : max_q;
+        p.few_rows = beside ? q * n_heads : 0;
+        const int64_t most = items(q, 64), planned = beside ? n_req * paged_items(1, n_heads, 64) : most;  // single tokens
+        p.few = paged_share(planned, most, paged_key_tiles(q, max_kv, window, paged_item_tokens(n_heads, 64)), 2.9,
+                            beside ? double(n_req) * n_heads : double(rows));
+    }
     size_t at = CSA2_STATUS_BYTES;
-    p.part_lse = at;
-    if (p.splits > 1) at = align256(at + size_t(p.splits) * size_t(rows) * 4);
-    p.part_o = at;
-    if (p.splits > 1) at = align256(at + size_t(p.splits) * size_t(rows) * kPD * 4);
+    auto partials = [&](const PagedShare& h, int64_t n, size_t& lse, size_t& o) {
+        lse = at;
+        if (h.splits > 1) at = align256(at + size_t(h.splits) * size_t(n) * 4);
+        o = at;
+        if (h.splits > 1) at = align256(at + size_t(h.splits) * size_t(n) * kPD * 4);
+    };
+    partials(p.tiles, rows, p.tile_lse, p.tile_o);
+    partials(p.few, beside ? n_req * p.few_rows : rows, p.few_lse, p.few_o);
     p.flags = at;
     at = align256(at + size_t(n_req) * p.span * kPFlagBytes);
-    p.tiles = at;
+    p.tile_at = at;
     at += size_t(n_req) * p.span * kPTileBytes;
     p.total = at;
     return p;
@@ -164,7 +205,7 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
     cudaStream_t s = cudaStream_t(stream);
     const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
-    if (plan.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (plan.tiles.grid > INT32_MAX || plan.few.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     PagedArgs a{};
     a.q = static_cast<const uint8_t*>(q_bf16);
     a.q_start = q_start;
@@ -174,13 +215,6 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.table = table;
     a.out = static_cast<uint8_t*>(out);
     a.lse = out_lse;
-    a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_lse);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_o);
-    if (plan.span) {
-        a.tiles = reinterpret_cast<uint8_t*>(static_cast<char*>(ws) + plan.tiles);
-        a.flags = reinterpret_cast<uint8_t*>(static_cast<char*>(ws) + plan.flags);
-        a.span = plan.span;
-    }
     a.st = static_cast<Status*>(ws);
     a.wlim = wait_limit_ns();
     a.n_rows_pages = n_rows / page_size;
@@ -193,24 +227,48 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.max_kv = max_kv;
     a.page = page_size;
     a.window = window >= max_kv ? 0 : window;
-    a.chunk = plan.chunk;
-    a.item = plan.item;
-    a.item_log2 = plan.item == 64 ? 6 : 8;
-    a.item_tokens = paged_item_tokens(n_heads, plan.item);
     a.by_heads = fast_div(uint32_t(n_heads));
     a.by_page = fast_div(uint32_t(page_size));
-    a.by_chunk = fast_div(uint32_t(plan.chunk));
     a.sm_scale = sm_scale;
+    char* w = static_cast<char*>(ws);
+    auto share = [&](PagedArgs& b, const PagedShare& p, int32_t item, int32_t item_log2, size_t lse, size_t o) {
+        b.chunk = p.chunk;
+        b.by_chunk = fast_div(uint32_t(p.chunk));
+        b.item = item;
+        b.item_log2 = item_log2;
+        b.item_tokens = paged_item_tokens(n_heads, item);
+        b.part_lse = reinterpret_cast<float*>(w + lse);
+        b.part_o = reinterpret_cast<float*>(w + o);
+        b.part_rows = a.rows;
+    };
+    PagedArgs few = a;
+    const bool both = plan.tiles.grid > 0 && plan.few.grid > 0;
+    share(few, plan.few, 64, 6, plan.few_lse, plan.few_o);
+    few.rows_to = both ? kPFewRows : INT32_MAX;
+    if (both) {
+        few.behind = 1;
+        few.few_rows = plan.few_rows;
+        few.by_few = fast_div(uint32_t(plan.few_rows));
+        few.part_rows = n_req * plan.few_rows;
+    }
+    share(a, plan.tiles, 256, 8, plan.tile_lse, plan.tile_o);
+    a.tiles = reinterpret_cast<uint8_t*>(w + plan.tile_at);
+    a.flags = reinterpret_cast<uint8_t*>(w + plan.flags);
+    a.span = plan.span;
+    a.rows_over = both ? kPFewRows : 0;
+    a.rows_to = plan.tiles.grid > 0 ? INT32_MAX : 0;
     const bool fp8 = fmt == CSA2_FMT_FP8;
-    const csa2_status e = plan.span ? paged_tiles_launch(a, fp8, unsigned(plan.grid), s)
-                                    : paged_rows_launch(a, fp8, unsigned(plan.grid), s);
+    csa2_status e = CSA2_OK;
+    if (plan.tiles.grid > 0) e = paged_tiles_launch(a, fp8, unsigned(plan.tiles.grid), s);
+    if (e == CSA2_OK && plan.few.grid > 0) e = paged_rows_launch(few, fp8, unsigned(plan.few.grid), s);
     if (e != CSA2_OK) {
         cudaGetLastError();
         return e;
     }
-    if (plan.splits > 1) {
+    for (const PagedArgs* b : {&a, &few}) {
+        if ((b == &a ? plan.tiles : plan.few).splits == 1) continue;
         timer_begin(K_PAGED_MERGE, s);
-        launch(paged_merge_kernel, dim3(unsigned(ceil_div<int64_t>(a.rows, 2))), 256, 0, s, 1, a);
+        launch(paged_merge_kernel, dim3(unsigned(ceil_div<int64_t>(b->part_rows, paged_merge_rows(*b)))), 256, 0, s, 1, *b);
         timer_end(K_PAGED_MERGE, s);
     }
     return launch_status();

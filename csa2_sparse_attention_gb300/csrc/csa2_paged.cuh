@@ -56,8 +56,8 @@ struct PagedArgs {
     const int32_t* table;
     uint8_t* out;
     float* lse;
-    float* part_o;    // [splits][rows][512], each split's normalized output
-    float* part_lse;  // [splits][rows], log2 domain
+    float* part_o;    // [splits][part_rows][512], each split's normalized output
+    float* part_lse;  // [splits][part_rows], log2 domain
     uint8_t* tiles;   // decoded tiles [n_req][span][128 KB], or null
     uint8_t* flags;   // [n_req][span][32]
     Status* st;
@@ -65,13 +65,17 @@ struct PagedArgs {
     int64_t n_rows_pages;  // pages of the cache
     int64_t max_pages;
     int64_t rows;          // n_tokens * heads
+    int64_t part_rows;     // rows; behind the tile kernel n_req * few_rows, a request's from r * few_rows on
     int64_t n_req;
     int32_t n_tokens, heads, max_q, max_kv, page, window;
     int32_t chunk;         // key tiles per split
-    FastDiv by_heads, by_page, by_chunk;
+    FastDiv by_heads, by_page, by_chunk, by_few;
     int32_t span;          // decoded tiles per request
     int32_t item;          // rows of a work item: 64, or the 256 of a cluster's two tiles (decoded tiles); 2^item_log2
     int32_t item_log2, item_tokens;
+    int32_t rows_over, rows_to;  // requests of rows_over < rows <= rows_to are this kernel's
+    int32_t few_rows;      // the most rows of such a request
+    int32_t behind;        // the few-row kernel: launched behind the tile kernel, which it does not depend on
     float sm_scale;
 };
 
@@ -94,6 +98,10 @@ __device__ __forceinline__ bool paged_request(const PagedArgs& a, int64_t r, Pag
         o.len = 0;
     }
     return o.nq > 0;
+}
+__device__ __forceinline__ bool paged_mine(const PagedArgs& a, const PagedReq& rq) {
+    const int32_t rows = rq.nq * a.heads;
+    return rows > a.rows_over && rows <= a.rows_to;
 }
 // Work items of a request; key tiles that one can span at most; its splits.
 __host__ __device__ inline int32_t paged_items(int32_t nq, int32_t heads, int32_t item) {
@@ -148,6 +156,7 @@ struct PagedWork {
     int32_t req;                 // -1: none
     int32_t item, split, splits;
     int32_t nt, key0;            // key tiles (0: nothing to see) and the first key
+    int64_t out0, part0;         // the item's first row of the outputs and of the partial ones
 };
 // Finds it for the grid's `place`, by a scan of the requests' items, into shared
 // memory; all WARPS warps of the block call it and synchronize behind it.  Up to
@@ -168,7 +177,7 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
         const int64_t r = r0 + 32 * warp + lane;
         int32_t n = 0, ns = 1;
         PagedReq rq;
-        if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr)) {
+        if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr) && paged_mine(a, rq)) {
             ns = paged_splits(a, paged_key_tiles(rq.nq, rq.len, a.window, a.item_tokens));
             n = (rq.nq * a.heads + a.item - 1) >> a.item_log2;
         }
@@ -204,6 +213,8 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
                 w.splits = splits;
                 w.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;
                 w.key0 = begin + j0 * kPN;
+                w.out0 = int64_t(rq.q0) * a.heads + item * a.item;
+                w.part0 = split * a.part_rows + (a.behind ? r * a.few_rows + item * a.item : w.out0);
             }
         }
         if (!wide || (base > place && !all)) break;

@@ -97,7 +97,10 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PagedRowsSmem& S = *reinterpret_cast<PagedRowsSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
-    grid_dep_wait();
+    // Behind the tile kernel, which runs other requests of the same call: the
+    // inputs are there when that one has started (it is behind the decode
+    // kernel), so this one only has to end after it.
+    if (!a.behind) grid_dep_wait();
     grid_dep_launch();
     paged_find<kRThreads / 32>(a, blockIdx.x, blockIdx.x == 0, S.work, S.sums);
     if (warp == kRMmaWarp) {
@@ -121,12 +124,12 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     const PagedReq rq = S.work.rq;
     if (req < 0) {
         if (warp == kRMmaWarp) tmem_dealloc(tmem, 512);
+        if (a.behind) grid_dep_wait();
         return;
     }
-    const int32_t nt = S.work.nt, key0 = S.work.key0, split = S.work.split, splits = S.work.splits;
+    const int32_t nt = S.work.nt, key0 = S.work.key0, splits = S.work.splits;
     const int32_t row0 = S.work.item * kRRows;  // of the request
     const int32_t n_row = rq.nq * a.heads - row0 < kRRows ? rq.nq * a.heads - row0 : kRRows;
-    const int64_t flat0 = int64_t(rq.q0) * a.heads + row0;
     const int32_t k_end = rq.len - rq.nq + (row0 + n_row - 1) / a.by_heads + 1;
     const int32_t k_last = key0 + nt * kPN < k_end ? key0 + nt * kPN : k_end;  // end of this CTA's keys
 
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         const int row = 8 * (warp < kPSoftWarps ? warp : warp - kRProdWarps) + (lane & 7), piece = lane >> 3;
         const bool on = row < n_row;
         U32x8 v[8];
-        paged_q_load(a, flat0 + row, on, v);
+        paged_q_load(a, S.work.out0 + row, on, v);
         const int qs = paged_q_exponent(v);
         if (piece == 0) {
             S.row[row] = make_float2(paged_q_scale(a, qs), 0.f);
@@ -280,6 +283,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         // ---- epilogue: the rows' sums, then O / l row by row in shared memory (the latents' place), and out
         if (ok) {
             tc_fence_after();
+            const int64_t out0 = S.work.out0, part0 = S.work.part0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float v[32];
@@ -294,9 +298,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 const float lse2 = sum == 0.f ? -INFINITY : S.row[tid].y + log2f(sum);
                 if (tid < n_row) {
                     if (splits > 1)
-                        a.part_lse[int64_t(split) * a.rows + flat0 + tid] = lse2;
+                        a.part_lse[part0 + tid] = lse2;
                     else if (a.lse)
-                        a.lse[flat0 + tid] = lse2 * kLn2;
+                        a.lse[out0 + tid] = lse2 * kLn2;
                 }
             }
             soft_sync();
@@ -336,9 +340,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             soft_sync();
             if (tid < n_row) {
                 if (whole)
-                    bulk_s2g(a.out + (flat0 + tid) * kPD * 2, stage + tid * kPD * 2, kPD * 2);
+                    bulk_s2g(a.out + (out0 + tid) * kPD * 2, stage + tid * kPD * 2, kPD * 2);
                 else
-                    bulk_s2g(a.part_o + (int64_t(split) * a.rows + flat0 + tid) * kPD, stage + tid * kPD * 4, kPD * 4);
+                    bulk_s2g(a.part_o + (part0 + tid) * kPD, stage + tid * kPD * 4, kPD * 4);
                 bulk_s2g_wait();
             }
         }
@@ -516,6 +520,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     tc_fence_before();
     __syncthreads();
     if (warp == kRMmaWarp) tmem_dealloc(tmem, 512);
+    if (a.behind) grid_dep_wait();
 }
 
 template <bool FP8>

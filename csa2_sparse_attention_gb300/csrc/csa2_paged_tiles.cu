@@ -362,10 +362,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 if (whole)
                     bulk_s2g(a.out + (flat * kPD + y_dim) * 2, stage, kPHalf * 2);
                 else
-                    bulk_s2g(a.part_o + (int64_t(split) * a.rows + flat) * kPD + y_dim, stage, kPHalf * 4);
+                    bulk_s2g(a.part_o + (int64_t(split) * a.part_rows + flat) * kPD + y_dim, stage, kPHalf * 4);
                 if (half == 0) {
                     if (!whole)
-                        a.part_lse[int64_t(split) * a.rows + flat] = lse2;
+                        a.part_lse[int64_t(split) * a.part_rows + flat] = lse2;
                     else if (a.lse)
                         a.lse[flat] = lse2 * kLn2;
                 }
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
 
 // Decodes the pages of every request once into tiles of 128 keys (layout:
 // kPTileBytes).  1.8 KB of traffic per FP4 key: 2 % of the attention's time at 512
-// tokens x 64 heads.  grid (tiles, requests).
+// tokens x 64 heads.  grid (tiles, requests); the few-row kernel's requests have none.
 template <bool FP8>
 __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
     __shared__ uint32_t s_nan[4], s_hidden[4];
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
     grid_dep_launch();
     const int64_t req = blockIdx.y;
     PagedReq rq;
-    if (!paged_request(a, req, rq, nullptr)) return;
+    if (!paged_request(a, req, rq, nullptr) || !paged_mine(a, rq)) return;
     const int32_t base = paged_base(a, rq) + int32_t(blockIdx.x) * kPN;
     if (base >= rq.len) return;
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, k8 = lane & 7, piece = lane >> 3;

@@ -703,6 +703,37 @@ def test_attention_of_many_requests(abi):
     check_attn(*a.result(), s, 0)
 
 
+@pytest.mark.parametrize("kv_len,new,heads,window,fmt", [
+    ([900, 2300, 2200, 40, 1, 0, 2100, 2049], [1, 300, 1, 4, 1, 0, 2, 1], 64, 0, "fp4"),   # both kernels, the short ones' keys split
+    ([2600, 2300, 2048, 2500, 700], [40, 1, 1, 1, 2], 100, 0, "fp8"),                     # both, keys of both split
+    ([600, 90, 31, 600, 80, 300, 300, 300], [90, 1, 1, 3, 2, 1, 1, 1], 32, 100, "fp4"),   # both, short window
+    ([300, 90, 31, 600], [90, 90, 1, 3], 32, 0, "fp8")])                                  # tiles alone
+def test_attention_long_and_short_requests_together(abi, kv_len, new, heads, window, fmt):
+    """Short requests beside long ones may take a kernel of their own; tokens behind the last request stay as they are,
+    a request with bad bounds is recorded and skipped, and a replayed graph gives the same bits."""
+    s = attn_inputs(np.random.default_rng(21), kv_len, new, heads, 16, fmt, tail=3)
+    a = Attn(abi, s, window)
+    a.call()
+    out, lse = a.result()
+    check_attn(out, lse, s, window)
+    T = int(s["q_start"][-1])
+    assert (out[T:] == 7).all() and (lse[T:] == 7).all()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.call(torch.cuda.current_stream())
+    a.out.fill_(5), a.lse.fill_(5)
+    g.replay(), g.replay()
+    out2, lse2 = a.result()
+    assert np.array_equal(out2[:T], out[:T]) and np.array_equal(lse2[:T], lse[:T]) and (out2[T:] == 5).all()
+    assert abi.csa2_status_fetch(a.ws)[0] == 0
+    a.kv_len[0] = 1 << 20  # outside the table row: sees nothing
+    a.call()
+    out3, lse3 = a.result()
+    n = int(s["q_start"][1])
+    assert (out3[:n] == 0).all() and np.isneginf(lse3[:n]).all() and np.array_equal(out3[n:T], out[n:T])
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.ERR_DEVICE_BOUNDS
+
+
 @pytest.mark.parametrize("heads,new", [(64, 4), (64, 5), (128, 2), (1, 256), (1, 257), (100, 3)])
 def test_attention_on_both_sides_of_the_kernels_border(abi, heads, new):
     """256 rows of a request go to the few-row kernel, more to the decoded tiles."""
