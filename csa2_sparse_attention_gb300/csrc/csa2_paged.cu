@@ -18,7 +18,7 @@ inline __host__ __device__ int paged_merge_rows(const PagedArgs& a) { return a.b
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     grid_dep_wait();
     grid_dep_launch();
-    const int t = threadIdx.x & 127;
+    const int t = threadIdx.x & 127, lane = lane_id();
 #pragma unroll 1
     for (int i = threadIdx.x >> 7; i < paged_merge_rows(a); i += 2) {
         const int64_t prow = int64_t(blockIdx.x) * paged_merge_rows(a) + i;  // of the partial outputs
@@ -44,19 +44,29 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
         const int32_t splits = paged_splits(a, tiles);
         if (splits == 1) continue;
         const int64_t row = int64_t(rq.q0) * a.heads + at;
-        float m = -INFINITY;
-        for (int32_t s = 0; s < splits; ++s) m = fmaxf(m, a.part_lse[s * a.part_rows + prow]);
-        float w = 0.f;
+        // a lane per split (there are at most 32), and eight splits' loads under way
+        float m = lane < splits ? a.part_lse[lane * a.part_rows + prow] : -INFINITY, f = m;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        f = f == -INFINITY ? 0.f : ex2(f - m);
+        float w = f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+        const float4* src = reinterpret_cast<const float4*>(a.part_o + prow * kPD) + t;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int32_t s = 0; s < splits; ++s) {
-            const float ls = a.part_lse[s * a.part_rows + prow];
-            const float f = ls == -INFINITY ? 0.f : ex2(ls - m);
-            const float4 v = reinterpret_cast<const float4*>(a.part_o + (s * a.part_rows + prow) * kPD)[t];
-            w += f;
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
+        for (int32_t s0 = 0; s0 < splits; s0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                v[s] = s0 + s < splits ? src[(s0 + s) * a.part_rows * (kPD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const float fs = __shfl_sync(0xffffffffu, f, s0 + s);
+                o.x = fmaf(fs, v[s].x, o.x);
+                o.y = fmaf(fs, v[s].y, o.y);
+                o.z = fmaf(fs, v[s].z, o.z);
+                o.w = fmaf(fs, v[s].w, o.w);
+            }
         }
         const float inv = w == 0.f ? 0.f : 1.0f / w;
         const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
