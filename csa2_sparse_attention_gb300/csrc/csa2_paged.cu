@@ -9,6 +9,7 @@
 namespace csa2 {
 
 constexpr int kPSms = 152;  // multiprocessors the split is planned for
+constexpr int kPSlotReqs = 256;  // a request per thread of the tile kernel's block
 
 // Joins the splits of a kernel's rows: weights 2^(lse_s - max lse) over the
 // normalized partial outputs.  128 threads per row, 4 channels each; rows whose
@@ -19,6 +20,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     const int t = threadIdx.x & 127, lane = lane_id();
+    const int32_t chunk = a.slots ? *a.chunk_out : a.chunk;
 #pragma unroll 1
     for (int i = threadIdx.x >> 7; i < paged_merge_rows(a); i += 2) {
         const int64_t prow = int64_t(blockIdx.x) * paged_merge_rows(a) + i;  // of the partial outputs
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
         if (at < 0 || at >= int64_t(rq.nq) * a.heads) continue;
         int32_t begin, end, tiles;
         paged_item_keys(a, rq, int32_t(at) >> a.item_log2, begin, end, tiles);
-        const int32_t splits = paged_splits(a, tiles);
+        const int32_t splits = paged_splits(tiles, chunk);
         if (splits == 1) continue;
         const int64_t row = int64_t(rq.q0) * a.heads + at;
         // a lane per split (there are at most 32), and eight splits' loads under way
@@ -95,18 +97,24 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // 16 heads, 8 x 64 + 8 single ones: 4K 128 and 171, 2K 84 and 98, 1K 63 and 63.
 // The split count of each is the one with the least time by: waves of 152 CTAs,
 // each a start and end of 8 us and a time per key tile, plus the merge's pass
-// over the partial outputs.
+// over the partial outputs.  That is for requests as long as max_kv; with up to
+// kPSlotReqs requests the kernels then shorten the splits by the real lengths
+// (paged_chunk), down to half: 16 single tokens x 64 heads over 2K to 8K entries
+// took 42.0 us without that and 34.6 us with it.
 struct PagedShare {  // of one of the kernels
-    int32_t chunk, splits;
-    int64_t grid;
+    int32_t chunk = 1, splits = 1;         // as the partial outputs are sized
+    int32_t chunk_min = 1, slots = 0;      // see PagedArgs
+    int64_t grid = 0;                      // 0: not launched
 };
-static PagedShare paged_share(int64_t planned, int64_t most, int32_t nt, double tile_us, double merge_rows) {
-    PagedShare p{nt > 0 ? nt : 1, 1, most};
+static PagedShare paged_share(int64_t planned, int64_t most, int ctas, int64_t n_req, int32_t nt, double tile_us,
+                              double merge_rows) {
+    PagedShare p;
+    p.chunk = nt > 0 ? nt : 1;
     double best = 1e30;
     for (int s = 1; s <= 32 && s <= (nt > 0 ? nt : 1); ++s) {
         const int32_t chunk = (nt + s - 1) / s;
         if (s > 1 && (nt + chunk - 1) / chunk != s) continue;
-        const double waves = double((planned * s + kPSms - 1) / kPSms);
+        const double waves = double((planned * ctas * s + kPSms - 1) / kPSms);
         double us = waves * (8.0 + tile_us * chunk);
         if (s > 1) us += 4.0 + merge_rows * s * kPD * 4 * 2 / 4e6;
         if (us < best) {
@@ -116,10 +124,19 @@ static PagedShare paged_share(int64_t planned, int64_t most, int32_t nt, double 
     }
     p.splits = nt > p.chunk ? (nt + p.chunk - 1) / p.chunk : 1;
     p.grid = most * p.splits;
+    if (p.splits > 1 && n_req <= kPSlotReqs && p.chunk < (1 << 16)) {
+        const int cap = p.splits < 16 ? 2 * p.splits : 32;
+        p.chunk_min = (nt + cap - 1) / cap;
+        p.splits = (nt + p.chunk_min - 1) / p.chunk_min;
+        p.slots = kPSms / ctas;
+        const int64_t full = most * p.splits < p.slots ? most * p.splits : p.slots;
+        p.grid = p.grid > full ? p.grid : full;
+    }
+    p.grid *= ctas;
     return p;
 }
 struct PagedPlan {
-    PagedShare tiles{1, 1, 0}, few{1, 1, 0};  // grid 0: not launched
+    PagedShare tiles, few;
     int32_t span, few_rows;
     size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, total;
 };
@@ -144,9 +161,9 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     };
     int32_t tile_keys = 0;
     if (p.span > 0) {
-        const int64_t n = 4 * items(max_q, 256);
+        const int64_t n = items(max_q, 256);
         tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256));
-        p.tiles = paged_share(n, n, tile_keys, 1.9, double(rows));
+        p.tiles = paged_share(n, n, 4, n_req, tile_keys, 1.9, double(rows));
     }
     const bool beside = p.span > 0;
     const int64_t padded = n_req * max_q;
@@ -154,7 +171,7 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
         const int32_t q = beside ? kPFewRows / n_heads : max_q;
         p.few_rows = beside ? q * n_heads : 0;
         const int64_t most = items(q, 64), planned = beside ? n_req * paged_items(1, n_heads, 64) : most;  // single tokens
-        p.few = paged_share(planned, most, paged_key_tiles(q, max_kv, window, paged_item_tokens(n_heads, 64)), 2.9,
+        p.few = paged_share(planned, most, 1, n_req, paged_key_tiles(q, max_kv, window, paged_item_tokens(n_heads, 64)), 2.9,
                             beside ? double(n_req) * n_heads : double(rows));
     }
     size_t at = CSA2_STATUS_BYTES;
@@ -243,7 +260,9 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     char* w = static_cast<char*>(ws);
     auto share = [&](PagedArgs& b, const PagedShare& p, int32_t item, int32_t item_log2, size_t lse, size_t o) {
         b.chunk = p.chunk;
-        b.by_chunk = fast_div(uint32_t(p.chunk));
+        b.chunk_min = p.chunk_min;
+        b.slots = p.slots;
+        b.chunk_out = reinterpret_cast<int32_t*>(w + CSA2_STATUS_BYTES / 2) + (item == 64);
         b.item = item;
         b.item_log2 = item_log2;
         b.item_tokens = paged_item_tokens(n_heads, item);

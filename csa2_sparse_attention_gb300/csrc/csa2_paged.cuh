@@ -45,7 +45,6 @@ inline FastDiv fast_div(uint32_t d) {
 __device__ __forceinline__ int32_t operator/(int32_t n, const FastDiv& f) {
     return int32_t((uint64_t(uint32_t(n)) * f.mul) >> f.shift);
 }
-__device__ __forceinline__ int32_t ceil_by(int32_t n, const FastDiv& f) { return (n + int32_t(f.d) - 1) / f; }
 
 struct PagedArgs {
     const uint8_t* q;
@@ -68,8 +67,12 @@ struct PagedArgs {
     int64_t part_rows;     // rows; behind the tile kernel n_req * few_rows, a request's from r * few_rows on
     int64_t n_req;
     int32_t n_tokens, heads, max_q, max_kv, page, window;
-    int32_t chunk;         // key tiles per split
-    FastDiv by_heads, by_page, by_chunk, by_few;
+    // Key tiles per split; with `slots` the kernel lowers it, not below chunk_min,
+    // to what spreads the requests' real lengths over that many items, and leaves
+    // it at *chunk_out for the merge.
+    int32_t chunk, chunk_min, slots;
+    int32_t* chunk_out;
+    FastDiv by_heads, by_page, by_few;
     int32_t span;          // decoded tiles per request
     int32_t item;          // rows of a work item: 64, or the 256 of a cluster's two tiles (decoded tiles); 2^item_log2
     int32_t item_log2, item_tokens;
@@ -118,8 +121,20 @@ __host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int3
 }
 // Tokens that an item's rows can belong to at most.
 inline int32_t paged_item_tokens(int32_t heads, int32_t item) { return (item - 1) / heads + 2; }
-__device__ __forceinline__ int32_t paged_splits(const PagedArgs& a, int32_t tiles) {
-    return tiles > a.chunk ? ceil_by(tiles, a.by_chunk) : 1;
+__device__ __forceinline__ int32_t paged_splits(int32_t tiles, int32_t chunk) {
+    if (tiles <= chunk) return 1;
+    int32_t n = int32_t(__fdividef(float(tiles), float(chunk)));  // 32 at most, so off by one at most
+    n += n * chunk < tiles;
+    return n + (n * chunk < tiles);
+}
+// With I items of T key tiles in all, splits of c tiles make at most T / c + I of
+// them: the least c with no more than `slots`.
+__device__ __forceinline__ int32_t paged_chunk(const PagedArgs& a, uint32_t items, uint32_t tiles) {
+    const uint32_t slots = uint32_t(a.slots);
+    if (items >= slots || tiles >= uint32_t(a.chunk) * (slots - items)) return a.chunk;
+    int32_t c = int32_t(__fdividef(float(tiles), float(slots - items)));
+    while (uint32_t(c) * (slots - items) < tiles) ++c;
+    return c > a.chunk_min ? c : a.chunk_min;
 }
 
 // First key that any token of the request sees, a multiple of 8: where the
@@ -163,7 +178,7 @@ struct PagedWork {
 // 32 requests are the first warp's alone, more go to all warps 32 each (`sums`
 // [2][WARPS] in shared memory): by one warp, 1024 requests took 0.5 us for every
 // 32, 9 of a CTA's 32 us.  `all`: look at every request, so that each one's
-// problems are recorded.
+// problems are recorded.  (`slots`: at most 32 requests, or 32 per warp.)
 template <int WARPS>
 __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bool all, PagedWork& w, int64_t* sums) {
     const int lane = lane_id(), warp = threadIdx.x >> 5;
@@ -175,12 +190,29 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
 #pragma unroll 1
     for (int64_t r0 = 0; r0 < a.n_req; r0 += 32 * WARPS) {
         const int64_t r = r0 + 32 * warp + lane;
-        int32_t n = 0, ns = 1;
+        int32_t n = 0, tiles = 0, chunk = a.chunk;
         PagedReq rq;
         if (r < a.n_req && paged_request(a, r, rq, all ? a.st : nullptr) && paged_mine(a, rq)) {
-            ns = paged_splits(a, paged_key_tiles(rq.nq, rq.len, a.window, a.item_tokens));
+            tiles = paged_key_tiles(rq.nq, rq.len, a.window, a.item_tokens);
             n = (rq.nq * a.heads + a.item - 1) >> a.item_log2;
         }
+        if (a.slots) {
+            // each bounded so that 256 of them are below 2^32 (the host sees to it that chunk * slots is below 2^24)
+            const int64_t all_tiles = int64_t(n) * tiles;
+            uint32_t si = __reduce_add_sync(0xffffffffu, n < (1 << 24) - 1 ? uint32_t(n) : (1u << 24) - 1);
+            uint32_t st = __reduce_add_sync(0xffffffffu, all_tiles < (1 << 24) - 1 ? uint32_t(all_tiles) : (1u << 24) - 1);
+            if (wide) {
+                if (lane == 0) sums[warp] = si, sums[WARPS + warp] = st;
+                __syncthreads();
+                si = st = 0;
+#pragma unroll 1
+                for (int v = 0; v < WARPS; ++v) si += uint32_t(sums[v]), st += uint32_t(sums[WARPS + v]);
+                __syncthreads();
+            }
+            chunk = paged_chunk(a, si, st);
+            if (all && threadIdx.x == 0) *a.chunk_out = chunk;
+        }
+        const int32_t ns = paged_splits(tiles, chunk);
         const int64_t mine = int64_t(n) * ns;
         int64_t inc = mine, before = base;
 #pragma unroll
@@ -202,16 +234,16 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
         if (local >= 0 && local < mine) {
             const uint32_t back = uint32_t(local) / uint32_t(ns);
             const int32_t item = n - 1 - int32_t(back), split = int32_t(uint32_t(local) - back * ns);  // the most keys first
-            int32_t begin, end, tiles;
-            paged_item_keys(a, rq, item, begin, end, tiles);
-            const int32_t splits = paged_splits(a, tiles), j0 = split * a.chunk;
+            int32_t begin, end, seen;
+            paged_item_keys(a, rq, item, begin, end, seen);
+            const int32_t splits = paged_splits(seen, chunk), j0 = split * chunk;
             if (split < splits) {
                 w.rq = rq;
                 w.req = int32_t(r);
                 w.item = item;
                 w.split = split;
                 w.splits = splits;
-                w.nt = tiles - j0 < a.chunk ? tiles - j0 : a.chunk;
+                w.nt = seen - j0 < chunk ? seen - j0 : chunk;
                 w.key0 = begin + j0 * kPN;
                 w.out0 = int64_t(rq.q0) * a.heads + item * a.item;
                 w.part0 = split * a.part_rows + (a.behind ? r * a.few_rows + item * a.item : w.out0);

@@ -703,6 +703,30 @@ def test_attention_of_many_requests(abi):
     check_attn(*a.result(), s, 0)
 
 
+@pytest.mark.parametrize("reqs,new,heads,longest", [(1, 1, 64, 8192), (5, 3, 64, 5000), (33, 1, 64, 3000), (60, 1, 128, 1500),
+                                                    (200, 1, 5, 2000), (3, 40, 64, 2100), (40, 6, 16, 1100), (257, 1, 64, 700)])
+def test_attention_splits_by_the_requests_lengths(abi, reqs, new, heads, longest):
+    """Lengths from one entry to the longest, so that the splits are far from those planned for the longest alone; the
+    same calls with host bounds far above the lengths, and with a second set of lengths in the same workspace."""
+    rng = np.random.default_rng(31)
+    lens = lambda: np.maximum(rng.integers(0, 1 + longest * np.arange(1, reqs + 1) // reqs), 1)  # noqa: E731
+    kv_len = lens()
+    kv_len[-1] = longest
+    s = attn_inputs(rng, kv_len, np.minimum(new, kv_len), heads, 16, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+    b = Attn(abi, s, max_kv=4 * longest)
+    b.call()
+    check_attn(*b.result(), s, 0)
+    assert abi.csa2_status_fetch(a.ws)[0] == 0 and abi.csa2_status_fetch(b.ws)[0] == 0
+    short = np.minimum(s["kv_len"], np.maximum(lens(), np.diff(s["q_start"]))).astype(np.int32)
+    s2 = {**s, "kv_len": short}
+    c = Attn(abi, s2, max_kv=longest, ws=a.ws)
+    c.call()
+    check_attn(*c.result(), s2, 0)
+
+
 @pytest.mark.parametrize("kv_len,new,heads,window,fmt", [
     ([900, 2300, 2200, 40, 1, 0, 2100, 2049], [1, 300, 1, 4, 1, 0, 2, 1], 64, 0, "fp4"),   # both kernels, the short ones' keys split
     ([2600, 2300, 2048, 2500, 700], [40, 1, 1, 1, 2], 100, 0, "fp8"),                     # both, keys of both split
