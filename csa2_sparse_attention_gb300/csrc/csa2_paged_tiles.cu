@@ -469,54 +469,53 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
 }
 
 // Decodes the pages of every request once into tiles of 128 keys (layout:
-// kPTileBytes).  1.8 KB of traffic per FP4 key: 2 % of the attention's time at 512
-// tokens x 64 heads.  grid (tiles, requests); the few-row kernel's requests have none.
+// kPTileBytes).  1.8 KB of traffic per FP4 key: 1 % of the attention's time at 512
+// tokens x 64 heads.  grid (blocks of a request, requests).  A block takes 32 keys
+// at a time, a warp 8 keys and half of their channels: with whole tiles per
+// block, calls of a few tiles took 3 us longer.  The requests' real lengths are
+// not the host's, and the few-row kernel's requests have no tiles: the blocks of
+// a request walk over its tiles, since 17,000 blocks, most of them without work,
+// cost 13 us.
 template <bool FP8>
 __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
-    __shared__ uint32_t s_nan[4], s_hidden[4];
+    __shared__ uint32_t s_nan[2], s_hidden[2];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t req = blockIdx.y;
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, k8 = lane & 7, piece = lane >> 3;
     PagedReq rq;
     if (!paged_request(a, req, rq, nullptr) || !paged_mine(a, rq)) return;
-    const int32_t base = paged_base(a, rq) + int32_t(blockIdx.x) * kPN;
-    if (base >= rq.len) return;
-    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, k8 = lane & 7, piece = lane >> 3;
-    uint8_t* tile = a.tiles + (req * a.span + blockIdx.x) * kPTileBytes;
-    if (tid < 4) s_nan[tid] = s_hidden[tid] = 0;
+    const int32_t base = paged_base(a, rq), quarters = (rq.len - base + 31) / 32;
+    if (tid < 2) s_nan[tid] = s_hidden[tid] = 0;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // key groups of 8: 2 warp + i; a lane has 16 bytes of every 64
-        const int kg = 2 * warp + i, key = 8 * kg + k8;
-        const int32_t p = base + key;
+    int par = 0;
+    for (int32_t n = blockIdx.x; n < ((quarters + 3) & ~3); n += gridDim.x, par ^= 1) {
+        const int32_t j = n >> 2, quarter = n & 3;
+        const int key = 32 * quarter + 8 * (warp >> 1) + k8, half = warp & 1;
+        uint8_t* dst = a.tiles + (req * a.span + j) * kPTileBytes + half * (kPTileBytes / 2) + (key >> 3) * 4096 + k8 * 16;
+        const int32_t p = base + j * kPN + key;
         int64_t row = -1;
         if (p < rq.len) {
-            const int32_t id = a.table[req * a.max_pages + p / a.page];
+            const int32_t page = p / a.by_page, id = a.table[req * a.max_pages + page];
             if (id >= 0 && id < a.n_rows_pages)
-                row = int64_t(id) * a.page + p % a.page;
-            else if (piece == 0)
+                row = int64_t(id) * a.page + (p - page * a.page);
+            else if (piece == 0 && half == 0)
                 record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(req), id);
         }
-        uint32_t bad = 0;
-        constexpr int NP = FP8 ? 8 : 4;  // 64-byte parts of a row
-        uint4 v[NP];
-        uint4 sc[2];
+        constexpr int NP = FP8 ? 4 : 2;  // 64-byte parts of the half row; a lane has 16 bytes of each
+        uint4 v[NP], sc = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < NP; ++e)
-            v[e] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.codes + row * (FP8 ? kPD : kPD / 2) + 64 * e) + piece)
+            v[e] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.codes + row * (FP8 ? kPD : kPD / 2) + 64 * (NP * half + e)) + piece)
                             : make_uint4(0, 0, 0, 0);
-        sc[0] = sc[1] = make_uint4(0, 0, 0, 0);
-        if (!FP8 && row >= 0) {
-            sc[0] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)));
-            sc[1] = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)) + 1);
-        }
+        if (!FP8 && row >= 0) sc = __ldg(reinterpret_cast<const uint4*>(a.scales + row * (kPD / 16)) + half);
+        uint32_t bad = 0;
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
             const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-            // channels: FP4 128 e + 32 piece .. + 31, FP8 64 e + 16 piece .. + 15
+            // chunks of 8 channels: FP4 4 piece .. of each 16, FP8 2 piece .. of each 8
             constexpr int NC = FP8 ? 2 : 4;
-            const int chunk = FP8 ? 8 * e + 2 * piece : 16 * e + 4 * piece;
-            uint8_t* dst = tile + (chunk >> 5) * (kPTileBytes / 2) + kg * 4096 + (chunk & 31) * 128 + k8 * 16;
+            uint8_t* to = dst + (FP8 ? 8 * e + 2 * piece : 16 * e + 4 * piece) * 128;
             uint32_t o[4 * NC];
             if (FP8) {
                 const uint32_t n4 = e4m3_nan4(w[0]) | e4m3_nan4(w[1]) | e4m3_nan4(w[2]) | e4m3_nan4(w[3]);
@@ -524,8 +523,8 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m) e4m3x4_f16(n4 ? 0u : w[m], o + 2 * m);
             } else {
-                const uint32_t* s8 = &sc[0].x + 2 * e;  // the 8 scales of 128 channels
-                const uint32_t s2 = ((piece & 2 ? s8[1] : s8[0]) >> (16 * (piece & 1))) & 0xFFFFu;
+                const uint32_t lo = e ? sc.z : sc.x, hi = e ? sc.w : sc.y;  // the 8 scales of 128 channels
+                const uint32_t s2 = ((piece & 2 ? hi : lo) >> (16 * (piece & 1))) & 0xFFFFu;
                 const uint32_t n2 = e4m3_nan4(s2);
                 bad |= n2;
                 uint32_t ss[2];
@@ -540,14 +539,17 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                *reinterpret_cast<uint4*>(to + c * 128) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
-        if (bad) atomicOr(&s_nan[key >> 5], 1u << (key & 31));
-        if (row < 0) atomicOr(&s_hidden[key >> 5], 1u << (key & 31));
+        if (bad) atomicOr(&s_nan[par], 1u << (key & 31));
+        if (row < 0) atomicOr(&s_hidden[par], 1u << (key & 31));
+        __syncthreads();
+        if (tid == 0) {  // (the next 32 keys use the other pair)
+            uint32_t* fl = reinterpret_cast<uint32_t*>(a.flags + (req * a.span + j) * kPFlagBytes);
+            fl[quarter] = s_hidden[par], fl[4 + quarter] = s_nan[par];
+            s_hidden[par] = s_nan[par] = 0;
+        }
     }
-    __syncthreads();
-    uint32_t* fl = reinterpret_cast<uint32_t*>(a.flags + (req * a.span + blockIdx.x) * kPFlagBytes);
-    if (tid < 4) fl[tid] = s_hidden[tid], fl[4 + tid] = s_nan[tid];
 }
 
 csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
@@ -561,8 +563,9 @@ csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cuda
         done[dev].store(true, std::memory_order_release);
     }
     timer_begin(K_PAGED_DECODE, s);
+    const int64_t quarters = int64_t(a.span) * 4, some = 4096 / a.n_req > 32 ? 4096 / a.n_req : 32;
     const cudaError_t e1 = launch(fp8 ? paged_decode_kernel<true> : paged_decode_kernel<false>,
-                                  dim3(unsigned(a.span), unsigned(a.n_req)), 256, 0, s, 1, a);
+                                  dim3(unsigned(quarters < some ? quarters : some), unsigned(a.n_req)), 256, 0, s, 1, a);
     timer_end(K_PAGED_DECODE, s);
     if (e1 != cudaSuccess) return CSA2_ERR_CUDA;
     timer_begin(K_PAGED_ATTN, s);
