@@ -62,6 +62,7 @@ namespace csa2 {
 
 constexpr int kPM = 128;                            // rows of a tile
 constexpr int kPTileThreads = 32 * (kPSoftWarps + 4);  // softmax, MMA and copy warps (and two that only bring in Q)
+constexpr int kPBlockBytes = kPN * 128 * 2;             // of a tile: 128 channels
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
 
 struct PagedTilesSmem {
@@ -148,10 +149,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     auto copy_block = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
         if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
         __syncwarp();
-        const int kg = rank * (kPN / 16) + lane;
-        if (lane < kPN / 16)
-            bulk_g2s_pair(S.c[g] + kg * 4096 + b * 2048, src + kg * 4096 + b * 2048, 2048, bar);
-        else if (lane == kPN / 16 && fl && rank == 0)
+        const uint32_t at = b * kPBlockBytes + rank * (kPBlockBytes / 2);
+        if (lane == 0)
+            bulk_g2s_pair(S.c[g] + at, src + at, kPBlockBytes / 2, bar);
+        else if (lane == 1 && fl && rank == 0)
             bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
         __syncwarp();
     };
@@ -374,11 +375,11 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         }
     } else if (tid == 32 * kMmaWarp) {
         // ================= MMA issue
-        constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, kPHalf, 0, false, true);
+        constexpr uint32_t id_s = idesc_f16(kPM, kPN, 0, false, false), id_o = idesc_f16(kPM, 128, 0, false, true);
         // descriptors; a step of 16 along K is 256 bytes (K-major) or two 8-key groups (MN-major)
         const uint64_t dq0 = umma_desc(smem_u32(S.qx), 128, 4096), dp0 = umma_desc(smem_u32(S.p), 128, 2048);
-        const uint64_t dk[2] = {umma_desc(smem_u32(S.c[0]), 128, 4096), umma_desc(smem_u32(S.c[1]), 128, 4096)};
-        const uint64_t dv[2] = {umma_desc(smem_u32(S.c[0]), 4096, 128), umma_desc(smem_u32(S.c[1]), 4096, 128)};
+        const uint64_t dk[2] = {umma_desc(smem_u32(S.c[0]), 128, 2048), umma_desc(smem_u32(S.c[1]), 128, 2048)};
+        const uint64_t dv[2] = {umma_desc(smem_u32(S.c[0]), 2048, 128), umma_desc(smem_u32(S.c[1]), 2048, 128)};
         // (a value the compiler cannot know: it would keep every step's descriptor of the loop in registers, and spill)
         auto fresh = [](uint64_t v) {
             asm volatile("" : "+l"(v));
@@ -391,8 +392,11 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             tc_fence_after();
             const uint64_t d = fresh(j & 1 ? dv[1] : dv[0]), dp = fresh(dp0);
 #pragma unroll
-            for (int k = 0; k < kPN / 16; ++k)
-                mma_f16_ss(tmem + kColO, dp + k * (256 >> 4), d + k * (8192 >> 4), id_o, k > 0 || j > 0);
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < kPN / 16; ++k)
+                    mma_f16_ss(tmem + kColO + 128 * b, dp + k * (256 >> 4), d + b * (kPBlockBytes >> 4) + k * (4096 >> 4), id_o,
+                               k > 0 || j > 0);
         };
         for (int32_t j = 0; j < nt && ok; ++j) {
             const int g = j & 1;
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + (8 * b + k) * (256 >> 4), id_s, k > 0 || b > 0);
+                    mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + b * (kPBlockBytes >> 4) + k * (256 >> 4), id_s, k > 0 || b > 0);
                 tc_commit_pair(&S.empty_x[g][b]);
             }
             if (ok && j > 0) {
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * (8 * b + k), d + (8 * b + k) * (256 >> 4), id_s, true);
+                    mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * (8 * b + k), d + b * (kPBlockBytes >> 4) + k * (256 >> 4), id_s, true);
             }
             if (ok) tc_commit(&S.s_full);
         }
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
     for (int32_t n = blockIdx.x; n < ((quarters + 3) & ~3); n += gridDim.x, par ^= 1) {
         const int32_t j = n >> 2, quarter = n & 3;
         const int key = 32 * quarter + 8 * (warp >> 1) + k8, half = warp & 1;
-        uint8_t* dst = a.tiles + (req * a.span + j) * kPTileBytes + half * (kPTileBytes / 2) + (key >> 3) * 4096 + k8 * 16;
+        uint8_t* dst = a.tiles + (req * a.span + j) * kPTileBytes + half * (kPTileBytes / 2) + (key >> 3) * 2048 + k8 * 16;
         const int32_t p = base + j * kPN + key;
         int64_t row = -1;
         if (p < rq.len) {
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
             const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
             // chunks of 8 channels: FP4 4 piece .. of each 16, FP8 2 piece .. of each 8
             constexpr int NC = FP8 ? 2 : 4;
-            uint8_t* to = dst + (FP8 ? 8 * e + 2 * piece : 16 * e + 4 * piece) * 128;
+            uint8_t* to = dst + (FP8 ? (e >> 1) * kPBlockBytes + (8 * (e & 1) + 2 * piece) * 128 : e * kPBlockBytes + 4 * piece * 128);
             uint32_t o[4 * NC];
             if (FP8) {
                 const uint32_t n4 = e4m3_nan4(w[0]) | e4m3_nan4(w[1]) | e4m3_nan4(w[2]) | e4m3_nan4(w[3]);
