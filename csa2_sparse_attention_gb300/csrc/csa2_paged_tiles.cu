@@ -34,9 +34,12 @@
 //   copy warp  the other half's channels X of a tile first, then, as the logits'
 //       MMAs release them, the own half's Y into the same group.  One copy of Y
 //       serves S (K-major) and O (MN-major).
-//   MMA warp, per tile:  S += Q_X X^T, then O += P Y of the previous tile,
-//       then S += Q_Y Y^T: the softmax of a tile runs under the next tile's
-//       S_X, and the copy of Y under the previous tile's O.
+//   MMA warp, per tile:  S += Q_X X^T, O += P Y of the previous tile for 128
+//       channels, S += Q_Y Y^T, then the other 128 channels of O.  The softmax of
+//       a tile runs under the next tile's S_X, the copy of Y under the first half
+//       of O, and the read of S out of TMEM under the second (with all of O
+//       between the two parts of S the tensor cores waited for that read: 583 us where
+//       it is 567).
 //   softmax (4 warps, a thread per row)  takes S out of TMEM, keeps the
 //       running base and sum in fp32, writes P as f16 to shared memory.  O is
 //       rescaled only when a logit lies 2^15 above the base (kPGrow).
@@ -44,12 +47,11 @@
 // output); Q goes to f16 times a power of two per row (exact down to 2^-28 of
 // the row's maximum).
 //
-// A tile takes about 4300 clocks, 3072 of them MMAs: S has one place in TMEM,
-// so the next logits wait for the softmax to have read it (about 500 clocks),
-// and the tensor cores run at 1.1-1.2 PFLOP/s of their work (one GPU: 1.87
-// measured for a large matrix product).  512 tokens x 64 heads over 8K entries:
-// 577 us, 983 TFLOP/s without the third product; 1024 tokens over 16K: 1.85 ms,
-// 1150 TFLOP/s.
+// A tile takes about 4150 clocks, 3072 of them MMAs: a block that is released
+// is there again some 1500 clocks later, and S has one place in TMEM, so the next
+// logits wait for the softmax to have read it.  512 tokens x 64 heads over 8K
+// entries: 567 us, 1000 TFLOP/s without the third product; 1024 tokens over 16K:
+// 1.82 ms, 1170 TFLOP/s.
 //
 // Long axes with few rows are split over CTAs in chunks of key tiles that the
 // host sizes; the partial outputs are joined by paged_merge_kernel.
@@ -71,8 +73,8 @@ struct PagedTilesSmem {
     uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
     PagedFlags flags[2];
     float q_scale[kPM];                // logits' scale of each row (log2 domain)
-    uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2];
-    uint64_t s_full, s_free, p_full, o_done, q_done, drain;
+    uint64_t full_x[2][2], full_y[2][2], empty_x[2][2], empty_o[2][2];
+    uint64_t s_full, s_free, p_full, p_free, o_done, q_done, drain;
     uint32_t tmem;
     PagedWork work;
     int64_t sums[2 * kPTileThreads / 32];
@@ -124,12 +126,13 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 mbar_init(&S.full_x[g][b], 1);
                 mbar_init(&S.full_y[g][b], 1);
                 mbar_init(&S.empty_x[g][b], 2);  // both CTAs' MMAs
+                mbar_init(&S.empty_o[g][b], 2);
             }
-            mbar_init(&S.empty_o[g], 2);
         }
         mbar_init(&S.s_full, 1);
         mbar_init(&S.s_free, kPSoftWarps);
         mbar_init(&S.p_full, kPSoftWarps);
+        mbar_init(&S.p_free, 1);
         mbar_init(&S.o_done, 1);
         mbar_init(&S.q_done, 2 * kPSoftWarps);
         mbar_init(&S.drain, 2);
@@ -266,10 +269,15 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                     mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(s[b][i]), __uint_as_float(s[b][i + 1])));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sm_eff;
             const bool grew = top > m + kPGrow;
+            if (j > 0) {  // the previous tile's O, which the next products' P and a new base have to come after
+                ok = __all_sync(0xffffffffu, mbar_wait(&S.p_free, (j - 1) & 1, a.wlim));
+                if (!ok) break;
+                tc_fence_after();
+            }
             if (__any_sync(0xffffffffu, grew)) {
                 const float mn = grew ? top - kPBase : m;
                 const float alpha = !grew ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
-                if (j > 0) {  // every MMA before S_Y of this tile is done, the previous O among them
+                if (j > 0) {
 #pragma unroll 1
                     for (int b = 0; b < kPHalf / 32; ++b) {
                         uint32_t o[32];
@@ -386,17 +394,14 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             return v;
         };
         bool ok = true;
-        auto o_mma = [&](int32_t j) {  // O += P Y of tile j
-            ok = ok && mbar_wait(&S.p_full, j & 1, a.wlim);
+        auto o_mma = [&](int32_t j, int b) {  // O += P Y of tile j, 128 channels
+            if (b == 0) ok = ok && mbar_wait(&S.p_full, j & 1, a.wlim);
             if (!ok) return;
             tc_fence_after();
-            const uint64_t d = fresh(j & 1 ? dv[1] : dv[0]), dp = fresh(dp0);
+            const uint64_t d = fresh(j & 1 ? dv[1] : dv[0]) + b * (kPBlockBytes >> 4), dp = fresh(dp0);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int k = 0; k < kPN / 16; ++k)
-                    mma_f16_ss(tmem + kColO + 128 * b, dp + k * (256 >> 4), d + b * (kPBlockBytes >> 4) + k * (4096 >> 4), id_o,
-                               k > 0 || j > 0);
+            for (int k = 0; k < kPN / 16; ++k)
+                mma_f16_ss(tmem + kColO + 128 * b, dp + k * (256 >> 4), d + k * (4096 >> 4), id_o, k > 0 || j > 0);
         };
         for (int32_t j = 0; j < nt && ok; ++j) {
             const int g = j & 1;
@@ -414,9 +419,9 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 tc_commit_pair(&S.empty_x[g][b]);
             }
             if (ok && j > 0) {
-                o_mma(j - 1);
-                // (only what a producer waits for: an arrival at the other CTA must not outlive it)
-                if (ok && j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1]);
+                o_mma(j - 1, 0);
+                // (only what the copies wait for: an arrival at the other CTA must not outlive it)
+                if (ok && j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1][0]);
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -427,9 +432,14 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                     mma_f16_ts(tmem + kColS, tmem + kColQ + 8 * (8 * b + k), d + b * (kPBlockBytes >> 4) + k * (256 >> 4), id_s, true);
             }
             if (ok) tc_commit(&S.s_full);
+            if (ok && j > 0) {
+                o_mma(j - 1, 1);
+                tc_commit(&S.p_free);
+                if (j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1][1]);
+            }
         }
         if (nt > 0) {
-            if (ok) o_mma(nt - 1);
+            for (int b = 0; b < 2; ++b) o_mma(nt - 1, b);
             if (ok) tc_commit(&S.o_done);
             if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), ti);
             // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done (in a cluster:
@@ -446,9 +456,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         for (int32_t j = 0; j < nt && ok; ++j) {
             const int g = j & 1;
             const uint32_t ph = (j >> 1) & 1;
-            if (j >= 1)
-                ok = __all_sync(0xffffffffu, j == 1 ? mbar_wait(&S.q_done, 0, a.wlim) : mbar_wait(&S.empty_o[g], ph ^ 1, a.wlim));
-            for (int b = 0; b < 2 && ok; ++b) {
+            for (int b = 0; b < 2; ++b) {
+                if (j == 1 && b == 0) ok = __all_sync(0xffffffffu, mbar_wait(&S.q_done, 0, a.wlim));
+                if (j > 1) ok = __all_sync(0xffffffffu, mbar_wait(&S.empty_o[g][b], ph ^ 1, a.wlim));
+                if (!ok) break;
                 if (j > 0) copy_block(&S.full_x[g][b], g, b, x_src + j * kPTileBytes, nullptr);
                 last_x[g][b] = j;
             }
