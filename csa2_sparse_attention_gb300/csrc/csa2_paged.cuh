@@ -12,10 +12,10 @@ constexpr int kPD = CSA2_LATENT_DIM;
 constexpr int kPHalf = kPD / 2;       // channels of one half
 constexpr int kPN = 128;              // keys of a tile
 constexpr int kPSoftWarps = 4;
-// Decoded tiles (paged_decode_kernel): per half of the channels [16 key
-// groups][32 chunks of 8 channels][8 keys][16 bytes], f16, as shared memory
-// holds them; and per tile 128 bits of keys without a page, 128 bits of keys
-// with a NaN latent.
+// Decoded tiles (paged_decode_kernel): blocks of 128 channels, [16 key groups]
+// [16 chunks of 8 channels][8 keys][16 bytes] in f16 each, as shared memory holds
+// them; and per tile 128 bits of keys without a page, 128 bits of keys with a NaN
+// latent.
 constexpr int64_t kPTileBytes = int64_t(kPN) * kPD * 2;
 constexpr int kPFlagBytes = 32;
 // Probabilities enter the products in f16 as 2^(l - b), with b lowered by this

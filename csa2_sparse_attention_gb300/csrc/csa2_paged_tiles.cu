@@ -69,7 +69,7 @@ constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
 
 struct PagedTilesSmem {
     uint8_t qx[kPM * kPHalf * 2];      // other half of Q, K-major: 8-row groups of 4096 B, 8-channel chunks of 128 B
-    uint8_t c[2][kPN * kPHalf * 2];    // latents: 8-key groups of 4096 B, 8-channel chunks of 128 B
+    uint8_t c[2][kPN * kPHalf * 2];    // latents: per 128 channels 8-key groups of 2048 B, 8-channel chunks of 128 B
     uint8_t p[kPM * kPN * 2];          // P: 8-row groups of 2048 B, 8-key chunks of 128 B
     PagedFlags flags[2];
     float q_scale[kPM];                // logits' scale of each row (log2 domain)
