@@ -9,7 +9,11 @@ This module only allocates device memory (torch) and issues C-ABI calls in
 that order; all arithmetic runs in libcsa2.so.  A step issues the same calls
 with the same pointers every time, so it can be captured in a CUDA graph: the
 lengths stay on the device, and the host's bounds max_q and max_kv size the
-launches.
+launches.  A captured step keeps its workspace when a later one needs a larger;
+the first step with larger bounds runs outside a capture.
+
+Calls go to the given stream, or the current one; the device has to be the
+current device.
 """
 from __future__ import annotations
 
@@ -22,16 +26,30 @@ from . import abi
 LATENT = abi.LATENT_DIM
 
 
-def fp4_weight(w, stream=None):
-    """FP4 form (codes [n][k/2], scales [n][k/16]) of bf16 weights w [n][k], k a multiple of 128."""
+def _stream(dev, stream):
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the current device is not {dev}")
+    return torch.cuda.current_stream(dev) if stream is None else stream
+
+
+def _rows(name, x, n, shape, dtype=torch.bfloat16):
+    """x has at least n contiguous rows of this shape."""
+    if x.dtype != dtype or tuple(x.shape[1:]) != tuple(shape) or x.shape[0] < n or not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} rows of {tuple(shape)}, at least {n} of them, not {x.dtype} {tuple(x.shape)}")
+
+
+def fp4_weight(w):
+    """FP4 form (codes [n][k/2], scales [n][k/16]) of bf16 weights w [n][k], k a multiple of 128, on the current stream."""
     n, k = w.shape
+    if w.dtype != torch.bfloat16:
+        raise ValueError("an FP4 weight is made of bf16 weights")
     if k % 128:
         raise ValueError("the channels of an FP4 weight come in multiples of 128")
+    s = _stream(w.device, None)
     codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
     scales = torch.empty((n, k // 16), dtype=torch.uint8, device=w.device)
     ws = torch.zeros(abi.STATUS_BYTES, dtype=torch.uint8, device=w.device)
     rows = n * k // 128
-    s = stream or torch.cuda.current_stream(w.device)
     abi.csa2_quantize_append(w.contiguous(), rows, 128, abi.FMT_FP4, abi.LAYOUT_ROWS, None, None, 0, None, rows, codes, scales,
                              ws, ws.numel(), s)
     return codes, scales
@@ -42,7 +60,10 @@ class PagedLatents:
 
     def __init__(self, n_req, max_tokens, n_pages, page_size, max_pages, heads=abi.ATTN_HEADS, fmt=abi.FMT_FP4, window=0,
                  sm_scale=1.0 / math.sqrt(float(LATENT)), rope_theta=10000.0, device="cuda"):
-        d = self.dev = torch.device(device)
+        d = torch.device(device)
+        if d.type == "cuda" and d.index is None:
+            d = torch.device("cuda", torch.cuda.current_device())
+        self.dev = d
         self.n_req, self.max_tokens, self.heads = n_req, max_tokens, heads
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self.fmt, self.window, self.sm_scale = fmt, window, sm_scale
@@ -64,23 +85,31 @@ class PagedLatents:
         self.rope = None
         if fp4:
             self.rope = torch.empty(abi.csa2_rope_table_bytes(LATENT, self.max_pos), dtype=u8, device=d)
-            abi.csa2_rope_table_init(rope_theta, LATENT, self.max_pos, self.rope, torch.cuda.current_stream(d))
+            abi.csa2_rope_table_init(rope_theta, LATENT, self.max_pos, self.rope, _stream(d, None))
         self.out = torch.zeros((max_tokens, heads, LATENT), dtype=torch.bfloat16, device=d)
         self.lse = torch.zeros((max_tokens, heads), dtype=torch.float32, device=d)
         self.ws_plan = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
         self.ws_app = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
         self.ws_attn = None
+        self._captured, self._kept = False, []  # the workspace is in a graph; earlier ones that are
+
+    def _tokens(self, n):
+        if not 0 <= n <= self.max_tokens:
+            raise ValueError(f"{n} tokens: the cache's buffers are for up to {self.max_tokens}")
 
     def plan(self, stream=None):
         """Pages, rows and positions of the step's new tokens (self.cached, self.added)."""
-        s = stream or torch.cuda.current_stream(self.dev)
+        s = _stream(self.dev, stream)
         abi.csa2_page_plan(self.cached, self.added, self.n_req, self.page_size, self.table, self.max_pages, self.free,
                            self.n_pages, self.n_free, self.n_free, self.q_start, self.kv_len, self.slots, self.pos,
                            self.max_tokens, self.ws_plan, self.ws_plan.numel(), s)
 
     def append(self, latents, n_tokens, stream=None):
-        """The new tokens' bf16 latents [n_tokens][512] into the planned rows."""
-        s = stream or torch.cuda.current_stream(self.dev)
+        """The new tokens' bf16 latents [n_tokens][512] into the planned rows.  Rows behind the planned tokens (a padded
+        batch) are stored nowhere; the first of them is in the append's status."""
+        self._tokens(n_tokens)
+        _rows("latents", latents, n_tokens, (LATENT,))
+        s = _stream(self.dev, stream)
         fp4 = self.fmt == abi.FMT_FP4
         abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if fp4 else None, self.rope,
                                  self.max_pos if fp4 else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
@@ -89,13 +118,26 @@ class PagedLatents:
     def workspace(self, n_tokens, max_q, max_kv):
         """The attention's workspace for these bounds (kept, and grown where a later step needs more)."""
         need = abi.csa2_paged_attn_workspace_bytes(n_tokens, self.heads, self.n_req, max_q, max_kv, self.window)
+        if need == 0:
+            raise ValueError("the attention does not run calls of these sizes")
+        capturing = torch.cuda.is_current_stream_capturing()
         if self.ws_attn is None or self.ws_attn.numel() < need:
+            if capturing:
+                raise RuntimeError("a step with these bounds has to run once before it is captured: its workspace grows")
+            if self._captured:
+                self._kept.append(self.ws_attn)
+                self._captured = False
+            torch.cuda.synchronize(self.dev)  # whatever stream still uses the old one
             self.ws_attn = torch.zeros(need, dtype=torch.uint8, device=self.dev)
+            torch.cuda.synchronize(self.dev)
+        self._captured = self._captured or capturing
         return self.ws_attn
 
     def attend(self, q, n_tokens, max_q, max_kv, stream=None):
         """out, lse of the new tokens' queries q [n_tokens][heads][512] over all entries."""
-        s = stream or torch.cuda.current_stream(self.dev)
+        self._tokens(n_tokens)
+        _rows("q", q, n_tokens, (self.heads, LATENT))
+        s = _stream(self.dev, stream)
         ws = self.workspace(n_tokens, max_q, max_kv)
         abi.csa2_paged_attn(q, n_tokens, self.heads, self.q_start, self.kv_len, self.n_req, max_q, max_kv, self.fmt, self.codes,
                             self.scales, self.n_rows, self.table, self.max_pages, self.page_size, self.window, self.sm_scale,
@@ -108,8 +150,11 @@ class PagedLatents:
 
     def status(self):
         """Status words of every workspace (first device-detected problem)."""
-        named = (("plan", self.ws_plan), ("append", self.ws_app), ("attn", self.ws_attn))
-        return {name: abi.csa2_status_fetch(ws) for name, ws in named if ws is not None}
+        named = {"plan": abi.csa2_status_fetch(self.ws_plan), "append": abi.csa2_status_fetch(self.ws_app)}
+        attn = [abi.csa2_status_fetch(ws) for ws in self._kept + [self.ws_attn] if ws is not None]
+        if attn:
+            named["attn"] = next((st for st in attn if st[0] != abi.OK), attn[-1])
+        return named
 
 
 class PagedLayer:
@@ -117,8 +162,12 @@ class PagedLayer:
 
     def __init__(self, cache, hidden, norm_weight, wq, wlatent, eps=1e-6):
         """norm_weight bf16 [hidden]; wq, wlatent: bf16 weights [heads * 512][hidden], [512][hidden]."""
-        self.cache, self.hidden, self.eps, self.norm_weight = cache, hidden, eps, norm_weight
         d, T, H = cache.dev, cache.max_tokens, cache.heads
+        for name, w, shape in (("norm_weight", norm_weight, (hidden,)), ("wq", wq, (H * LATENT, hidden)),
+                               ("wlatent", wlatent, (LATENT, hidden))):
+            if w.dtype != torch.bfloat16 or tuple(w.shape) != shape or w.device != d:
+                raise ValueError(f"{name}: bf16 {shape} on {d}, not {w.dtype} {tuple(w.shape)} on {w.device}")
+        self.cache, self.hidden, self.eps, self.norm_weight = cache, hidden, eps, norm_weight.contiguous()
         self.wq, self.wlatent = fp4_weight(wq), fp4_weight(wlatent)
         self.residual = torch.zeros((T, hidden), dtype=torch.bfloat16, device=d)
         self.x = torch.zeros((T, hidden), dtype=torch.uint8, device=d)  # E4M3
@@ -134,9 +183,12 @@ class PagedLayer:
 
     def step(self, hidden, n_tokens, max_q, max_kv, stream=None):
         """One step of n_tokens new tokens' bf16 hidden states (added to self.residual, the layer's residual stream):
-        (out, lse) of the attention."""
+        (out, lse) of the attention.  n_tokens above the planned ones (a padded batch) leaves the rows behind them of
+        out and lse as they are; see PagedLatents.append."""
         c, n = self.cache, n_tokens
-        s = stream or torch.cuda.current_stream(c.dev)
+        c._tokens(n)
+        _rows("hidden", hidden, n, (self.hidden,))
+        s = _stream(c.dev, stream)
         abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
                              self.x, self.x_scales, None, s)
         self._project(self.wq, n, c.heads * LATENT, self.q, s)

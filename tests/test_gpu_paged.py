@@ -872,6 +872,85 @@ def test_step_captured_and_replayed_is_the_eager_step(abi):
         assert torch.equal(a, b)
 
 
+def test_captured_step_keeps_its_workspace(abi):
+    """A larger eager step between replays takes a workspace of its own; a step that would need a larger one inside a
+    capture is refused."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    cache.added.copy_(torch.tensor([30, 9, 17], dtype=torch.int32))
+    x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+    layer.step(x, 56, 30, 30)
+    cache.advance()
+    q = layer.q[:3].clone()
+    cache.added.fill_(0)
+    cache.plan()
+    cache.q_start.copy_(torch.tensor([0, 1, 2, 3], dtype=torch.int32))  # (a query over what is there)
+    cache.workspace(3, 1, 32)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(q, 3, 1, 32)
+    held = cache.ws_attn
+    graph.replay()
+    torch.cuda.synchronize()
+    want = cache.out[:3].clone()
+    need = abi.csa2_paged_attn_workspace_bytes(3, cache.heads, 3, 3, 1 << 16, 0)
+    assert need > held.numel()
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            cache.attend(q, 3, 3, 1 << 16)
+    cache.attend(q, 3, 3, 1 << 16)
+    assert cache.ws_attn is not held and any(w is held for w in cache._kept)
+    cache.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.out[:3], want) and cache.status()["attn"][0] == abi.OK
+
+
+def test_padded_step(abi):
+    """More tokens than the lengths give: the rows behind change nothing but the append's status."""
+    runs = []
+    for pad in (0, 5):
+        paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+        cache.added.copy_(torch.tensor([20, 0, 7], dtype=torch.int32))
+        x = torch.randn(32, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+        cache.out.fill_(3), cache.lse.fill_(3)
+        layer.step(x, 27 + pad, 20, 20)
+        torch.cuda.synchronize()
+        assert (cache.out[27:] == 3).all() and (cache.lse[27:] == 3).all()
+        st = cache.status()
+        assert st["plan"][0] == st["attn"][0] == abi.OK
+        assert st["append"][0] == (abi.ERR_DEVICE_BOUNDS if pad else abi.OK)
+        runs.append((cache.out[:27].clone(), cache.codes.clone(), cache.scales.clone(), cache.table.clone()))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new", [[10, 6, 1, 1], [130, 9, 1, 3]])
+def test_attention_of_more_tokens_than_entries(abi, new):
+    """Lengths below the new tokens': the tokens before position 0 see nothing."""
+    s = attn_inputs(np.random.default_rng(17), [3, 0, 1, 200], new, 64, 16, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    check_attn(*a.result(), s, 0)
+    assert abi.csa2_status_fetch(a.ws)[0] == 0
+
+
+@pytest.mark.parametrize("new", [2, 9])
+def test_attention_nan_and_infinite_queries_stay_in_their_rows(abi, new):
+    s = attn_inputs(np.random.default_rng(19), [300, 150], [new, new], 64, 16, "fp4")
+    a = Attn(abi, s)
+    a.call()
+    want, wlse = a.result()
+    a.q[0, 5, 17] = float("nan")
+    a.q[new - 1, 63, 300] = float("inf")
+    a.q[new, 0, 0] = -float("inf")
+    a.call()
+    out, lse = a.result()
+    for t, h in ((0, 5), (new - 1, 63), (new, 0)):
+        assert np.isnan(out[t, h]).all() and np.isnan(lse[t, h])
+        out[t, h], lse[t, h] = want[t, h], wlse[t, h]
+    assert np.array_equal(out, want) and np.array_equal(lse, wlse)
+
+
 def test_plan_over_several_blocks_shares_its_ticket(abi):
     """Many tokens (several blocks), the free count in place, call after call on one workspace."""
     rng = np.random.default_rng(41)

@@ -109,6 +109,23 @@ def test_paged_attn_workspace_of_the_largest_bounds(abi):
     assert size(4, 64, 2, 4, (1 << 30) + 1, 0) == 0
 
 
+def test_cache_refusals(abi):
+    """What does not fit the cache's buffers is refused before any call."""
+    from csa2_sparse_attention_gb300 import paged
+    c = paged.PagedLatents(2, 8, 4, 16, 2, heads=4, fmt=abi.FMT_FP8, device="cpu")
+    bf = torch.bfloat16
+    c0 = abi.csa2_launch_count()
+    for bad in (lambda: c.append(torch.zeros(9, 512, dtype=bf), 9), lambda: c.append(torch.zeros(4, 512, dtype=bf), 5),
+                lambda: c.append(torch.zeros(8, 512), 8), lambda: c.append(torch.zeros(8, 256, dtype=bf), 8),
+                lambda: c.append(torch.zeros(512, 8, dtype=bf).t(), 8), lambda: c.append(torch.zeros(8, 512, dtype=bf), -1),
+                lambda: c.attend(torch.zeros(9, 4, 512, dtype=bf), 9, 1, 1), lambda: c.attend(torch.zeros(8, 5, 512, dtype=bf), 8, 1, 1),
+                lambda: c.workspace(8, 1, (1 << 31) - 1), lambda: paged.fp4_weight(torch.zeros(4, 200, dtype=bf)),
+                lambda: paged.fp4_weight(torch.zeros(4, 256))):
+        with pytest.raises(ValueError):
+            bad()
+    assert abi.csa2_launch_count() == c0
+
+
 # ------------------------------------------------- the 64-bit forms by hand
 def test_plan_form_by_hand():
     table = np.array([[4, -1, -1], [2, 6, -1]], np.int32)
