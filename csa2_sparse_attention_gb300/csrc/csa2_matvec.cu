@@ -50,7 +50,8 @@ struct MatvecArgs {
     float* part;         // [slices][n][n_out] partial sums, or null
     int64_t n, x_stride, n_out, tiles;
     int32_t k, slice;    // channels; channels per slice (a multiple of 128)
-    int32_t wk;          // warps over the channels; the others go over rows of W
+    int32_t wk, wm;      // warps over the channels, warps over rows of W (what is left of 16 idles)
+    int32_t by_wm;       // 65536 / wm + 1: n * by_wm >> 16 is n / wm for n < 256
     int32_t x_e4m3;
     float alpha;
     int32_t out_f32;
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
     const int rows = int(a.n - i0 < 16 ? a.n - i0 : 16);  // rows of x (NT = 1: up to 8)
     const int32_t k0 = blockIdx.y * a.slice, kn = a.k - k0 < a.slice ? a.k - k0 : a.slice;
     const int steps = (kn + kMvStep - 1) / kMvStep;
-    const int wk = a.wk, wm = kMvWarps / wk, my_k = warp % wk, my_m = warp / wk;
+    const int wk = a.wk, wm = a.wm, my_k = warp % wk, my_m = warp / wk;
+    const int my_steps = my_m < wm ? steps : 0;    // (an idle warp has none)
     const int per_tile = (steps + wk - 1) / wk;  // steps of a warp per tile of 32 wm rows of W
     // shared memory: rings, then the warps' sums [warp][8 NT columns][36: 32 rows], then x
     uint8_t* ring = smem_raw + warp * (STAGES * kMvStage);
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
         const int step = my_k + wk * f_k;
         uint8_t* dst = ring + f_stage * kMvStage + lane * 16;
         const uint8_t* src = f_code + step * (kMvStep / 2);
-        const bool in = step < steps;
+        const bool in = step < my_steps;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const bool on = in && 8 * h < f_left;
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
         const int step = my_k + wk * kk;
         const uint8_t* cs = ring + stage * kMvStage;
         stage = stage + 1 == STAGES ? 0 : stage + 1;
-        if (step < steps) {
+        if (step < my_steps) {
             uint4 cw[4];
             uint32_t sc[4][2];
 #pragma unroll
@@ -287,9 +289,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
                     acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.f;
                 }
             __syncthreads();
-            const int width = kMvRows * wm, log2w = 31 - __clz(width);
+            const int width = kMvRows * wm;
             for (int e = tid; e < rows * width; e += kMvThreads) {
-                const int i = e >> log2w, j = e - (i << log2w);
+                const int i = ((e >> 5) * a.by_wm) >> 16, j = e - i * width;
                 const float* from = s_red + (j >> 5) * wk * kRed + i * kMvSumStride + (j & 31);
                 float v = 0.f;
                 for (int q = 0; q < wk; ++q) v += from[q * kRed];
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(256) matvec_join_kernel(const float* __restric
 }
 
 struct MatvecPlan {
-    int32_t slice, slices, wk, stages;
+    int32_t slice, slices, wk, wm, stages;
     int64_t tiles, grid;
     size_t smem, total;
 };
@@ -345,21 +347,27 @@ static MatvecPlan matvec_plan(int64_t n, int k, int64_t n_out) {
     p.stages = int((kMvSmem - red - per * step_x) / (kMvWarps * kMvStage));
     p.stages = p.stages < kMvMaxStages ? p.stages : kMvMaxStages;
     p.smem = size_t(p.stages) * kMvWarps * kMvStage + red + per * step_x;
-    // warps over channels or over rows: the fewest steps of the busiest CTA, half a step for each join
+    // warps over channels and rows: the fewest steps of the busiest CTA, half a
+    // step for each join, and less the fewer warps share the issue slots.  (With 16
+    // warps always, powers of two each way: 5 x 896 -> 20000 8.0 us, 1 x 4096 ->
+    // 12288 11.4 us; so 6.6 and 10.6.)
     const int64_t groups = (n + 15) / 16;
     int64_t ctas = kMvSms / (p.slices * (groups > 0 ? groups : 1));
     ctas = ctas < 1 ? 1 : ctas;
     double best = 1e30;
-    for (int wk = 1; wk <= kMvWarps; wk *= 2) {
-        const int64_t tiles = (n_out + kMvRows * (kMvWarps / wk) - 1) / (kMvRows * (kMvWarps / wk));
-        const double cost = double((tiles + ctas - 1) / ctas) * ((per + wk - 1) / wk + 0.5);
+    for (int wk = 1; wk <= kMvWarps; ++wk) {
+        const int64_t blocks = (n_out + kMvRows - 1) / kMvRows, most = ctas * (kMvWarps / wk);
+        const int64_t rounds = (blocks + most - 1) / most;
+        const int64_t wm = (blocks + ctas * rounds - 1) / (ctas * rounds);  // no more than these rounds need
+        const double cost = double(rounds) * ((per + wk - 1) / wk + 0.5) * (0.7 + 0.3 * double(wk * wm) / kMvWarps);
         if (cost < best) {
             best = cost;
             p.wk = wk;
-            p.tiles = tiles;
-            p.grid = tiles < ctas ? tiles : ctas;
+            p.wm = int(wm);
         }
     }
+    p.tiles = (n_out + kMvRows * p.wm - 1) / (kMvRows * p.wm);
+    p.grid = p.tiles < ctas ? p.tiles : ctas;
     p.total = CSA2_STATUS_BYTES;
     if (p.slices > 1) p.total = align256(p.total + size_t(p.slices) * size_t(n) * size_t(n_out) * 4);
     return p;
@@ -405,10 +413,10 @@ extern "C" csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_
     for (const void* p : {x, static_cast<const void*>(codes), static_cast<const void*>(scales),
                           static_cast<const void*>(out), static_cast<const void*>(x_scales)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    if (!ws || !aligned16(ws) || ws_bytes < csa2_fp4_matvec_workspace_bytes(n, k, n_out)) return CSA2_ERR_WORKSPACE;
+    const MatvecPlan p = matvec_plan(n, k, n_out);
+    if (!ws || !aligned16(ws) || ws_bytes < p.total) return CSA2_ERR_WORKSPACE;
     if (n == 0) return CSA2_OK;
     cudaStream_t s = cudaStream_t(stream);
-    const MatvecPlan p = matvec_plan(n, k, n_out);
     MatvecArgs a{};
     a.x = static_cast<const uint8_t*>(x);
     a.x_scales = x_scales;
@@ -424,6 +432,8 @@ extern "C" csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_
     a.k = k;
     a.slice = p.slice;
     a.wk = p.wk;
+    a.wm = p.wm;
+    a.by_wm = 65536 / p.wm + 1;
     a.alpha = alpha;
     a.out_f32 = out_dtype == CSA2_OUT_F32;
     timer_begin(K_MATVEC, s);

@@ -226,12 +226,10 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
                           static_cast<const void*>(table), static_cast<const void*>(out),
                           static_cast<const void*>(out_lse)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    if (!ws || !aligned16(ws) ||
-        ws_bytes < csa2_paged_attn_workspace_bytes(n_tokens, n_heads, n_req, max_q, max_kv, window))
-        return CSA2_ERR_WORKSPACE;
+    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
+    if (!ws || !aligned16(ws) || ws_bytes < plan.total) return CSA2_ERR_WORKSPACE;
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
     cudaStream_t s = cudaStream_t(stream);
-    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
     if (plan.tiles.grid > INT32_MAX || plan.few.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     PagedArgs a{};
     a.q = static_cast<const uint8_t*>(q_bf16);

@@ -604,6 +604,16 @@ def test_matvec(abi, n, k, n_out, fp8):
         check_matvec(got, xt, xs, codes, scales, 0.37, dt)
 
 
+@pytest.mark.parametrize("n,k,n_out", [(1, 4096, 6000), (5, 896, 20000), (16, 768, 32768), (3, 1408, 9333), (12, 640, 14592)])
+def test_matvec_splits_of_the_warps(abi, n, k, n_out):
+    """Sizes whose warps are no powers of two each way, or not all in use."""
+    rng = np.random.default_rng(n + k)
+    codes, scales = weight(rng, n_out, k)
+    x = bf16(rng.standard_normal((n, k)))
+    got = matvec_call(abi, x, None, codes, scales, 1.0, torch.float32)
+    check_matvec(got, x, None, codes, scales, 1.0, torch.float32)
+
+
 def test_matvec_ranges(abi):
     """Rows of very different size side by side, a zero row, the largest and smallest weights."""
     rng = np.random.default_rng(1)
