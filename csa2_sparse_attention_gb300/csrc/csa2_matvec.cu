@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
 #pragma unroll 4
         for (int p = xt + kMvHeld * threads_per_row; p < kn / 8; p += threads_per_row) put(p, x_raw(p));
     }
+    if (tid < rows * 16) reinterpret_cast<uint4*>(s_x + steps * rows * 256)[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
 
     // ---- the walk
@@ -246,31 +247,31 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MatvecA
         const int step = my_k + wk * kk;
         const uint8_t* cs = ring + stage * kMvStage;
         stage = stage + 1 == STAGES ? 0 : stage + 1;
-        if (step < my_steps) {
-            uint4 cw[4];
-            uint32_t sc[4][2];
+        // (without a branch the loads run ahead of the products: a step behind the last one has zero weights, and reads
+        // the zeros behind x; 4 x 8192 -> 28672 28.2 -> 27.2 us)
+        uint4 cw[4];
+        uint32_t sc[4][2];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                cw[h] = *reinterpret_cast<const uint4*>(cs + h * 512 + lane * 16);
-                mv_scales(*reinterpret_cast<const uint16_t*>(cs + 4 * 512 + (8 * h + g) * 8 + 2 * t), sc[h][0], sc[h][1]);
-            }
-            const uint8_t* xs = s_x + step * 4 * xstride;
+        for (int h = 0; h < 4; ++h) {
+            cw[h] = *reinterpret_cast<const uint4*>(cs + h * 512 + lane * 16);
+            mv_scales(*reinterpret_cast<const uint16_t*>(cs + 4 * 512 + (8 * h + g) * 8 + 2 * t), sc[h][0], sc[h][1]);
+        }
+        const uint8_t* xs = s_x + (step < steps ? step : steps) * 4 * xstride;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {  // 8 of the lane's 32 channels
-                uint4 b[NT];
+        for (int w = 0; w < 4; ++w) {  // 8 of the lane's 32 channels
+            uint4 b[NT];
 #pragma unroll
-                for (int q = 0; q < NT; ++q) b[q] = *reinterpret_cast<const uint4*>(xs + w * xstride + xoff[q]);
+            for (int q = 0; q < NT; ++q) b[q] = *reinterpret_cast<const uint4*>(xs + w * xstride + xoff[q]);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t r0[4], r1[4];
-                    const uint4 c0 = cw[2 * m], c1 = cw[2 * m + 1];
-                    mv_codes(w == 0 ? c0.x : w == 1 ? c0.y : w == 2 ? c0.z : c0.w, sc[2 * m][w >> 1], r0);
-                    mv_codes(w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w, sc[2 * m + 1][w >> 1], r1);
+            for (int m = 0; m < 2; ++m) {
+                uint32_t r0[4], r1[4];
+                const uint4 c0 = cw[2 * m], c1 = cw[2 * m + 1];
+                mv_codes(w == 0 ? c0.x : w == 1 ? c0.y : w == 2 ? c0.z : c0.w, sc[2 * m][w >> 1], r0);
+                mv_codes(w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w, sc[2 * m + 1][w >> 1], r1);
 #pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        mma_16816(acc[m][q], r0[0], r1[0], r0[1], r1[1], b[q].x, b[q].y);
-                        mma_16816(acc[m][q], r0[2], r1[2], r0[3], r1[3], b[q].z, b[q].w);
-                    }
+                for (int q = 0; q < NT; ++q) {
+                    mma_16816(acc[m][q], r0[0], r1[0], r0[1], r1[1], b[q].x, b[q].y);
+                    mma_16816(acc[m][q], r0[2], r1[2], r0[3], r1[3], b[q].z, b[q].w);
                 }
             }
         }
@@ -338,19 +339,19 @@ static MatvecPlan matvec_plan(int64_t n, int k, int64_t n_out) {
     const int rows = n < 16 ? int(n > 0 ? n : 1) : 16, nt = n > 8 ? 2 : 1;
     const int steps = (k + kMvStep - 1) / kMvStep;
     const size_t step_x = size_t(rows) * kMvStep * 2, red = size_t(kMvWarps) * 8 * nt * kMvSumStride * 4;
-    // x's channels per CTA: what fits beside two stages (25 steps of 128 at 16 rows)
-    const int fit = int((kMvSmem - red - 2 * kMvWarps * kMvStage) / step_x);
+    // x's channels per CTA and a step of zeros: what fits beside two stages (24 steps of 128 at 16 rows)
+    const int fit = int((kMvSmem - red - 2 * kMvWarps * kMvStage) / step_x) - 1;
     p.slices = (steps + fit - 1) / fit;
     const int per = (steps + p.slices - 1) / p.slices;
     p.slices = (steps + per - 1) / per;
     p.slice = per * kMvStep;
-    p.stages = int((kMvSmem - red - per * step_x) / (kMvWarps * kMvStage));
+    p.stages = int((kMvSmem - red - (per + 1) * step_x) / (kMvWarps * kMvStage));
     p.stages = p.stages < kMvMaxStages ? p.stages : kMvMaxStages;
-    p.smem = size_t(p.stages) * kMvWarps * kMvStage + red + per * step_x;
+    p.smem = size_t(p.stages) * kMvWarps * kMvStage + red + (per + 1) * step_x;
     // warps over channels and rows: the fewest steps of the busiest CTA, half a
     // step for each join, and less the fewer warps share the issue slots.  (With 16
     // warps always, powers of two each way: 5 x 896 -> 20000 8.0 us, 1 x 4096 ->
-    // 12288 11.4 us; so 6.6 and 10.6.)
+    // 12288 11.4 us; so 7.0 and 11.0.)
     const int64_t groups = (n + 15) / 16;
     int64_t ctas = kMvSms / (p.slices * (groups > 0 ? groups : 1));
     ctas = ctas < 1 ? 1 : ctas;
