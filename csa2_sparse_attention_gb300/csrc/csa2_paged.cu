@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // over 16K entries take 1.81 ms from tiles and 2.70 ms in items of 64 rows.  The
 // border, 64 heads over 8K entries: 16 requests of 4 tokens (4 items each) 124 us
 // from tiles and 122 us without, of 8 tokens 181 and 209 us; single tokens would
-// write and read 1 KB per key for nothing (115 and 45 us).  Tiles run
+// write and read 1 KB per key for nothing (115 and 45 us).  Nor does it pay where
+// an item sees four tiles or fewer (1024 tokens with a window of 128, 64 heads:
+// 128 us from tiles, 118 without; 4 x 512 with 512, 6 tiles: 334 and 350).  Tiles run
 // requests of any length; beside them the few-row kernel takes the short ones
 // where the call's tokens say that there are enough of those, by a sixth of the
 // longest request per request, or three quarters from 16 key tiles on.  64 heads,
@@ -141,13 +143,14 @@ struct PagedPlan {
     size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, total;
 };
 constexpr size_t kPMaxTileBytes = size_t(4) << 30;
-constexpr int32_t kPFewRows = 256;
+constexpr int32_t kPFewRows = 256, kPFewTiles = 4;
 static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
     PagedPlan p{};
     if (window >= max_kv) window = 0;
     if (max_q > n_tokens) max_q = int32_t(n_tokens);
     const int64_t rows = n_tokens * n_heads;
-    if (int64_t(max_q) * n_heads > kPFewRows) {
+    const int32_t tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256));
+    if (int64_t(max_q) * n_heads > kPFewRows && tile_keys > kPFewTiles) {
         int64_t span = (max_kv + kPN - 1) / kPN;
         if (window > 0) {  // from the first token's window to the last token
             const int64_t w = (int64_t(window) + max_q + 7 + kPN - 1) / kPN;
@@ -159,10 +162,8 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
         const int64_t all = rows / item + n_req, each = n_req * paged_items(q, n_heads, item);
         return all < each ? all : each;
     };
-    int32_t tile_keys = 0;
     if (p.span > 0) {
         const int64_t n = items(max_q, 256);
-        tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256));
         p.tiles = paged_share(n, n, 4, n_req, tile_keys, 1.9, double(rows));
     }
     const bool beside = p.span > 0;

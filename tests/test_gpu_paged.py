@@ -768,6 +768,15 @@ def test_attention_long_and_short_requests_together(abi, kv_len, new, heads, win
     assert abi.csa2_status_fetch(a.ws)[0] == abi.ERR_DEVICE_BOUNDS
 
 
+@pytest.mark.parametrize("kv,new,window", [(512, 30, 0), (513, 30, 0), (900, 40, 250), (900, 40, 400), (2000, 300, 128)])
+def test_attention_on_both_sides_of_few_tiles(abi, kv, new, window):
+    """Long chunks that see four key tiles or fewer go to the few-row kernel, others to the decoded tiles."""
+    s = attn_inputs(np.random.default_rng(kv + new), [kv, kv // 2, 7], [new, min(new, kv // 2), 7], 32, 16, "fp8")
+    a = Attn(abi, s, window)
+    a.call()
+    check_attn(*a.result(), s, window)
+
+
 @pytest.mark.parametrize("heads,new", [(64, 4), (64, 5), (128, 2), (1, 256), (1, 257), (100, 3)])
 def test_attention_on_both_sides_of_the_kernels_border(abi, heads, new):
     """256 rows of a request go to the few-row kernel, more to the decoded tiles."""
