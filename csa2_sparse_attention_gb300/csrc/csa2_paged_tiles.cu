@@ -47,7 +47,7 @@
 // output); Q goes to f16 times a power of two per row (exact down to 2^-28 of
 // the row's maximum).
 //
-// A tile takes about 4150 clocks, 3072 of them MMAs: a block that is released
+// A tile takes about 4150 clocks, three quarters of them MMAs: a block that is released
 // is there again some 1500 clocks later, and S has one place in TMEM, so the next
 // logits wait for the softmax to have read it.  512 tokens x 64 heads over 8K
 // entries: 567 us, 1000 TFLOP/s without the third product; 1024 tokens over 16K:
