@@ -1,6 +1,6 @@
 // Causal attention over paged latents: the call's plan, its entry points and
 // the join of its splits (the kernels: csa2_paged_rows.cu for requests of up to
-// 256 (token, head) rows, csa2_paged_tiles.cu for more).
+// 256 (token, head) rows or four key tiles, csa2_paged_tiles.cu for more).
 #include "csa2_paged.cuh"
 #include "csa2_timer.cuh"
 

@@ -1,12 +1,12 @@
 // Causal attention over paged latents for requests of few rows (single tokens
-// and short chunks): 64 (token, head) rows per CTA, all 512 channels.
+// and short chunks) and for chunks that see few keys: 64 (token, head) rows per
+// CTA, all 512 channels.
 //
 // With few rows every key is decoded for one or a few CTAs only, and the
-// decoding, not the MMAs, costs the most: a CTA of 128 rows and half of the
-// output channels (csa2_paged_tiles.cu) decodes each key for both halves, 5700
-// clocks per 128 keys and half, and leaves half of its rows empty at 64 heads.
-// Transposed, the products need one copy of a decoded tile and 64 columns of
-// TMEM per 128 channels:
+// decoding costs as much as the MMAs.  A CTA of 128 rows and half of the output
+// channels (csa2_paged_tiles.cu) would need each key decoded for both halves,
+// and at 64 heads half of its rows stay empty.  Transposed, the products need
+// one copy of a decoded tile and 64 columns of TMEM per 128 channels:
 //
 //   S^T [128 keys x 64 rows]     = C Q^T     32 MMAs, M = keys, K = channels
 //   O^T [4 x 128 channels x 64]  += C^T P^T  4 x 8 MMAs, M = channels, K = keys
