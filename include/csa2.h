@@ -390,6 +390,8 @@ csa2_status csa2_page_plan(const int32_t* cached, const int32_t* added, int64_t 
  * recorded and skipped; a table entry outside [0, n_rows / page_size) is
  * recorded and its page is not seen.  Latents that no token sees may hold
  * anything, NaN included.
+ * The same call gives the same bits every time; the keys are split by the
+ * lengths of all requests, so an output's last bits can depend on the others.
  * ws: csa2_paged_attn_workspace_bytes (0 for bad sizes) for the same sizes.
  */
 size_t csa2_paged_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
