@@ -323,12 +323,13 @@ def test_attention_many_small_probabilities(abi, new, reqs):
     assert (np.abs(lse.reshape(wlse.shape) - wlse) <= d + n * 2.0 ** -24 + 2.0 ** -22 * (1 + wlse)).all()
 
 
+@pytest.mark.parametrize("more,window", [(0, 100), (700, 600)])  # (the few-row kernel, decoded tiles)
 @pytest.mark.parametrize("fmt", ["fp4", "fp8"])
-def test_attention_leaves_out_what_is_masked(abi, fmt):
+def test_attention_leaves_out_what_is_masked(abi, fmt, more, window):
     """NaN and the largest values in rows behind the sequence, outside the window, in later tokens' entries and in
     other pages do not reach rows that do not see them; a token that sees a NaN entry is NaN as a whole."""
     rng = np.random.default_rng(8)
-    s = attn_inputs(rng, [201, 77], [6, 2], 64, 16, fmt)
+    s = attn_inputs(rng, [201 + more, 77 + more], [6, 2], 64, 16, fmt)
     clean = {**s, "codes": s["codes"].copy(), "scales": None if s["scales"] is None else s["scales"].copy()}
     row = lambda r, p: int(s["table"][r, p // 16]) * 16 + p % 16  # noqa: E731
 
@@ -339,11 +340,12 @@ def test_attention_leaves_out_what_is_masked(abi, fmt):
         else:
             s["scales"][at, ::2] = 0x7F
             s["scales"][at, 1::2] = 0x7E
-    for p in list(range(201, 208)) + [199, 200, 3, 64]:
+    end = [16 * (-(-n // 16)) for n in s["kv_len"]]
+    for p in list(range(201 + more, end[0])) + [199 + more, 200 + more, 3, 64]:
         spoil(row(0, p))
-    for p in range(77, 80):
+    for p in range(77 + more, end[1]):
         spoil(row(1, p))
-    window = 100  # request 0's tokens sit at 195 .. 200: 3 and 64 are outside, 199 is seen by the last two
+    # request 0's tokens sit at 195 .. 200 + more: 3 and 64 are outside, 199 + more is seen by the last two
     a = Attn(abi, s, window)
     a.call()
     out, lse = a.result()
@@ -388,13 +390,69 @@ def test_attention_pages_and_lengths_outside_are_recorded(abi):
     assert abi.csa2_status_fetch(c.ws)[:3] == [abi.ERR_DEVICE_BOUNDS, 9, 1]
 
 
+def test_attention_over_tiles_records_pages_and_lengths(abi):
+    """The same for requests whose keys are decoded to tiles."""
+    s = attn_inputs(np.random.default_rng(11), [100, 60, 40, 50], [6, 7, 5, 9], 64, 8, "fp4")
+    n_pages = len(s["codes"]) // 8
+    good = s["table"].copy()
+    s["table"][0, 3] = n_pages
+    s["table"][0, 5] = -2
+    a = Attn(abi, s, max_kv=1000)
+    a.call()
+    check_attn(*a.result(), s, 0, bad_page=lambda i: i < 0 or i >= n_pages)
+    st = abi.csa2_status_fetch(a.ws)
+    assert st[0] == abi.ERR_DEVICE_BOUNDS and st[1] == 8 and st[2] == 0
+    for wrong in (105, -1):  # the table's rows hold 104 entries
+        b = Attn(abi, dict(s, table=good, kv_len=np.array([100, wrong, 40, 50], np.int32)), max_kv=1000)
+        b.call()
+        out, lse = b.result()
+        assert (out[6:13] == 0).all() and np.isneginf(lse[6:13]).all()
+        check_attn(out, lse, dict(s, table=good, kv_len=np.array([100, 0, 40, 50], np.int32)), 0)
+        assert abi.csa2_status_fetch(b.ws)[:3] == [abi.ERR_DEVICE_BOUNDS, 9, 1]
+    c = Attn(abi, dict(s, table=good, q_start=np.array([0, 6, 18, 18, 27], np.int32)), max_q=9, max_kv=1000)
+    c.call()
+    out, lse = c.result()
+    assert (out[6:18] == 7).all() and (lse[6:18] == 7).all() and (out[:6] != 7).any()
+    assert abi.csa2_status_fetch(c.ws)[:3] == [abi.ERR_DEVICE_BOUNDS, 9, 1]
+
+
+@pytest.mark.parametrize("i", range(len(ATTN)))
+def test_attention_with_a_loose_bound(abi, i):
+    """The cases of test_attention with a bound that takes chunks to the decoded tiles (without a window)."""
+    kv_len, new, heads, page, fmt, window = ATTN[i]
+    s = attn_inputs(np.random.default_rng(200 + i), kv_len, new, heads, page, fmt)
+    a = Attn(abi, s, window, max_kv=max(kv_len) + 600)
+    a.call()
+    check_attn(*a.result(), s, window)
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+def test_attention_of_both_kinds_on_two_streams(abi):
+    """Calls that run both kernels, on two streams at once with workspaces of their own, give the same bits as alone."""
+    calls = []
+    for k in range(2):
+        s = attn_inputs(np.random.default_rng(50 + k), [2600, 2300, 900, 2100], [40 + k, 1, 2, 1], 64, 16, ("fp4", "fp8")[k])
+        a = Attn(abi, s)
+        a.call()
+        calls.append((a, a.result()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for (a, _), st in zip(calls, streams):
+            a.call(st)
+    torch.cuda.synchronize()
+    for a, (out, lse) in calls:
+        got = a.result()
+        assert np.array_equal(got[0], out) and np.array_equal(got[1], lse) and abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
 def bad_ids(t, n):
     return (t < 0) | (t >= n)
 
 
-def test_attention_rows_behind_the_last_token_stay(abi):
+@pytest.mark.parametrize("bound", [300, 1000])
+def test_attention_rows_behind_the_last_token_stay(abi, bound):
     s = attn_inputs(np.random.default_rng(12), [90, 300], [3, 70], 16, 8, "fp4", tail=19)
-    a = Attn(abi, s)
+    a = Attn(abi, s, max_kv=bound)
     a.call()
     out, lse = a.result()
     check_attn(out, lse, s, 0)
@@ -657,13 +715,13 @@ def test_matvec_weights_beyond_two_gigabytes(abi):
 
 
 # ------------------------------------------------- the attention once more
-@pytest.mark.parametrize("new,fmt", [(2, "fp4"), (40, "fp8")])
+@pytest.mark.parametrize("new,fmt", [(2, "fp4"), (2, "fp8"), (40, "fp4"), (40, "fp8")])
 def test_attention_cache_beyond_two_gigabytes(abi, new, fmt):
     """Rows past 2^31 bytes of the latent planes, in the few-row kernel and over decoded tiles."""
     s = attn_inputs(np.random.default_rng(21), [300], [new], 16, 64, fmt)
     shift = (1 << 31) // (256 if fmt == "fp4" else 512) // 64 + 17  # pages
     n_rows = len(s["codes"]) + 64 * shift
-    a = Attn(abi, s)
+    a = Attn(abi, s, max_kv=1000)
     codes = torch.empty((n_rows, s["codes"].shape[1]), dtype=torch.uint8, device="cuda")
     codes[64 * shift:] = a.codes
     a.codes = codes
@@ -677,12 +735,13 @@ def test_attention_cache_beyond_two_gigabytes(abi, new, fmt):
     assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
 
 
-@pytest.mark.parametrize("new", [2, 40])
-def test_attention_gives_up_and_recovers(abi, new):
+@pytest.mark.parametrize("kv,new,bound", [([500, 300], [2, 1], 500), ([500, 300], [40, 1], 500), ([500, 300], [40, 1], 1000),
+                                          ([2600, 2300, 900], [40, 1, 1], 2600)])  # few rows, few tiles, tiles, both kernels
+def test_attention_gives_up_and_recovers(abi, kv, new, bound):
     """With a wait limit of 1 ns every bounded wait gives up: the status says so, copies and MMAs in flight are
     waited for, and the next call is right."""
-    s = attn_inputs(np.random.default_rng(22), [500, 300], [new, 1], 16, 16, "fp4")
-    a = Attn(abi, s)
+    s = attn_inputs(np.random.default_rng(22), kv, new, 16, 16, "fp4")
+    a = Attn(abi, s, max_kv=bound)
     a.call()
     one = a.result()
     check_attn(*one, s, 0)
@@ -943,20 +1002,21 @@ def test_padded_step(abi):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bound", [200, 1000])
 @pytest.mark.parametrize("new", [[10, 6, 1, 1], [130, 9, 1, 3]])
-def test_attention_of_more_tokens_than_entries(abi, new):
+def test_attention_of_more_tokens_than_entries(abi, new, bound):
     """Lengths below the new tokens': the tokens before position 0 see nothing."""
     s = attn_inputs(np.random.default_rng(17), [3, 0, 1, 200], new, 64, 16, "fp4")
-    a = Attn(abi, s)
+    a = Attn(abi, s, max_kv=bound)
     a.call()
     check_attn(*a.result(), s, 0)
     assert abi.csa2_status_fetch(a.ws)[0] == 0
 
 
-@pytest.mark.parametrize("new", [2, 9])
-def test_attention_nan_and_infinite_queries_stay_in_their_rows(abi, new):
+@pytest.mark.parametrize("new,bound", [(2, 300), (9, 300), (9, 1000)])
+def test_attention_nan_and_infinite_queries_stay_in_their_rows(abi, new, bound):
     s = attn_inputs(np.random.default_rng(19), [300, 150], [new, new], 64, 16, "fp4")
-    a = Attn(abi, s)
+    a = Attn(abi, s, max_kv=bound)
     a.call()
     want, wlse = a.result()
     a.q[0, 5, 17] = float("nan")
