@@ -78,6 +78,7 @@ struct PagedArgs {
     int32_t item_log2, item_tokens;
     int32_t rows_over, rows_to;  // requests of rows_over < rows <= rows_to are this kernel's
     int32_t few_rows;      // the most rows of such a request
+    int32_t tail;          // one request whose last items are split (paged_tail)
     int32_t behind;        // the few-row kernel: launched behind the tile kernel, which it does not depend on
     float sm_scale;
 };
@@ -135,6 +136,18 @@ __device__ __forceinline__ int32_t paged_chunk(const PagedArgs& a, uint32_t item
     int32_t c = int32_t(__fdividef(float(tiles), float(slots - items)));
     while (uint32_t(c) * (slots - items) < tiles) ++c;
     return c > a.chunk_min ? c : a.chunk_min;
+}
+
+// One long request is rarely a whole number of waves: its last items (those
+// with the fewest keys), what is left of whole waves of kPTailSlots, are split
+// where two or more fit into the place of one.  `items`: how many are split,
+// `splits`: into how many.
+constexpr int32_t kPTailSlots = 38, kPTailTiles = 12;  // clusters of 4 CTAs at a time; key tiles that are worth it
+__host__ __device__ inline void paged_tail(int32_t n, int32_t tiles, int32_t& items, int32_t& splits) {
+    items = n % kPTailSlots;
+    splits = items > 0 ? kPTailSlots / items : 1;
+    if (splits > 8) splits = 8;
+    if (splits < 2 || tiles < kPTailTiles) items = 0, splits = 1;
 }
 
 // First key that any token of the request sees, a multiple of 8: where the
@@ -213,7 +226,9 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
             if (all && threadIdx.x == 0) *a.chunk_out = chunk;
         }
         const int32_t ns = paged_splits(tiles, chunk);
-        const int64_t mine = int64_t(n) * ns;
+        int32_t tail = 0, tail_splits = 1;
+        if (a.tail) paged_tail(n, tiles, tail, tail_splits);
+        const int64_t mine = int64_t(n) * ns + tail * (tail_splits - 1);
         int64_t inc = mine, before = base;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -233,9 +248,15 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
         const int64_t local = place - before - (inc - mine);
         if (local >= 0 && local < mine) {
             const uint32_t back = uint32_t(local) / uint32_t(ns);
-            const int32_t item = n - 1 - int32_t(back), split = int32_t(uint32_t(local) - back * ns);  // the most keys first
+            int32_t item = n - 1 - int32_t(back), split = int32_t(uint32_t(local) - back * ns);  // the most keys first
+            if (local >= n - tail && tail > 0) {
+                const int32_t k = int32_t(local) - (n - tail);
+                item = tail - 1 - k / tail_splits;
+                split = k % tail_splits;
+            }
             int32_t begin, end, seen;
             paged_item_keys(a, rq, item, begin, end, seen);
+            if (item < tail) chunk = (seen + tail_splits - 1) / tail_splits;
             const int32_t splits = paged_splits(seen, chunk), j0 = split * chunk;
             if (split < splits) {
                 w.rq = rq;
@@ -246,7 +267,8 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
                 w.nt = seen - j0 < chunk ? seen - j0 : chunk;
                 w.key0 = begin + j0 * kPN;
                 w.out0 = int64_t(rq.q0) * a.heads + item * a.item;
-                w.part0 = split * a.part_rows + (a.behind ? r * a.few_rows + item * a.item : w.out0);
+                w.part0 = item < tail ? (int64_t(split) * tail + item) * a.item
+                                      : split * a.part_rows + (a.behind ? r * a.few_rows + item * a.item : w.out0);
             }
         }
         if (!wide || (base > place && !all)) break;

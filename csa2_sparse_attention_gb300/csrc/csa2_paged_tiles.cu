@@ -39,7 +39,7 @@
 //       a tile runs under the next tile's S_X, the copy of Y under the first half
 //       of O, and the read of S out of TMEM under the second (with all of O
 //       between the two parts of S the tensor cores waited for that read: 583 us where
-//       it is 567).
+//       it was 567, 512 tokens x 64 heads over 8K).
 //   softmax (4 warps, a thread per row)  takes S out of TMEM, keeps the
 //       running base and sum in fp32, writes P as f16 to shared memory.  O is
 //       rescaled only when a logit lies 2^15 above the base (kPGrow).
@@ -50,7 +50,7 @@
 // A tile takes about 4150 clocks, three quarters of them MMAs: a block that is released
 // is there again some 1500 clocks later, and S has one place in TMEM, so the next
 // logits wait for the softmax to have read it.  512 tokens x 64 heads over 8K
-// entries: 567 us, 1000 TFLOP/s without the third product; 1024 tokens over 16K:
+// entries: 521 us, 1090 TFLOP/s without the third product; 1024 tokens over 16K:
 // 1.82 ms, 1170 TFLOP/s.
 //
 // Long axes with few rows are split over CTAs in chunks of key tiles that the
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         return;
     }
     const PagedReq rq = S.work.rq;
-    const int32_t nt = S.work.nt, key0 = S.work.key0, split = S.work.split, splits = S.work.splits;
+    const int32_t nt = S.work.nt, key0 = S.work.key0, splits = S.work.splits;
     // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
     const int32_t ti = 2 * S.work.item + rank;
     const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                 if (whole)
                     bulk_s2g(a.out + (flat * kPD + y_dim) * 2, stage, kPHalf * 2);
                 else
-                    bulk_s2g(a.part_o + (int64_t(split) * a.part_rows + flat) * kPD + y_dim, stage, kPHalf * 4);
+                    bulk_s2g(a.part_o + (S.work.part0 + rank * kPM + row) * kPD + y_dim, stage, kPHalf * 4);
                 if (half == 0) {
                     if (!whole)
-                        a.part_lse[int64_t(split) * a.part_rows + flat] = lse2;
+                        a.part_lse[S.work.part0 + rank * kPM + row] = lse2;
                     else if (a.lse)
                         a.lse[flat] = lse2 * kLn2;
                 }

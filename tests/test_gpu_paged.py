@@ -836,6 +836,22 @@ def test_attention_on_both_sides_of_few_tiles(abi, kv, new, window):
     check_attn(*a.result(), s, window)
 
 
+@pytest.mark.parametrize("new,kv,window,fmt,loose", [(152, 1700, 0, "fp4", 0), (156, 1700, 0, "fp8", 0), (161, 2100, 1600, "fp4", 0),
+                                                     (199, 1650, 0, "fp4", 0), (227, 1600, 0, "fp4", 0), (30, 1600, 0, "fp4", 169),
+                                                     (153, 155, 0, "fp4", 1700), (100, 2000, 0, "fp8", 100)])
+def test_attention_of_one_long_chunk(abi, new, kv, window, fmt, loose):
+    """One request of whole waves of rows and some more, whose last rows' keys may be split: 38 items of 256 rows and 0,
+    1, 3, 12 (and a broken one) and 19 more, fewer than a wave under looser bounds, and too few keys to split."""
+    s = attn_inputs(np.random.default_rng(new), [kv], [new], 64, 16, fmt, tail=loose if loose < 1000 else 0)
+    a = Attn(abi, s, window, max_q=new + (loose if loose < 1000 else 0), max_kv=max(kv, loose))
+    for _ in range(2):
+        a.out.fill_(7), a.lse.fill_(7)
+        a.call()
+        out, lse = a.result()
+        check_attn(out, lse, s, window)
+        assert (out[new:] == 7).all() and (lse[new:] == 7).all() and abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
 @pytest.mark.parametrize("heads,new", [(64, 4), (64, 5), (128, 2), (1, 256), (1, 257), (100, 3)])
 def test_attention_on_both_sides_of_the_kernels_border(abi, heads, new):
     """256 rows of a request go to the few-row kernel, more to the decoded tiles."""
