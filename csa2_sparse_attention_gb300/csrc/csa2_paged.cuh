@@ -360,16 +360,21 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// 32 bytes by one load
+// 32 bytes from a 16-byte aligned address: one load where it is 32-byte aligned
+// (all rows of an operand are, or none), two otherwise.
 struct U32x8 {
     uint32_t w[8];
 };
 __device__ __forceinline__ U32x8 ldg_32b(const uint8_t* p) {
     U32x8 v;
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
-                   "=r"(v.w[7])
-                 : "l"(p));
+    asm volatile(
+        "{\n .reg .pred one;\n .reg .b64 t;\n and.b64 t, %8, 16;\n setp.eq.u64 one, t, 0;\n"
+        " @one ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        " @!one ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%8];\n"
+        " @!one ld.global.nc.v4.b32 {%4,%5,%6,%7}, [%8+16];\n}\n"
+        : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+          "=r"(v.w[7])
+        : "l"(p));
     return v;
 }
 // nonzero when one of the four E4M3 bytes is NaN (0x7F or 0xFF)

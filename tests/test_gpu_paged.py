@@ -1063,3 +1063,62 @@ def test_plan_over_several_blocks_shares_its_ticket(abi):
         n_free = want[5]
         table = want[0]
         check_plan((t.cpu().numpy(), qs.cpu().numpy(), kl.cpu().numpy(), sl.cpu().numpy(), po.cpu().numpy(), int(nf.item())), want)
+
+
+# ------------------------------------------------ what a call may be given
+def at16(t):
+    """The same tensor 16 bytes behind a 32-byte boundary."""
+    v = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")[16:].view(t.dtype).view(t.shape)
+    assert v.data_ptr() % 32 == 16
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("kv,new,window,bound", [
+    ([500, 33, 300], [2, 1, 3], 0, 500), ([300, 90], [40, 9], 0, 300), ([700, 300], [40, 1], 0, 1000),
+    ([2600, 2300, 900], [40, 1, 1], 0, 2600), ([900, 300], [40, 30], 400, 900)])  # few rows, few tiles, tiles, both, window
+def test_attention_of_pointers_at_16_bytes(abi, kv, new, window, bound, fmt):
+    """Every operand 16-byte aligned and no more: the bits of the call on 256-byte aligned ones."""
+    s = attn_inputs(np.random.default_rng(61), kv, new, 64, 16, fmt)
+    a = Attn(abi, s, window, max_kv=bound)
+    a.call()
+    want = a.result()
+    check_attn(*want, s, window)
+    for name in ("q", "q_start", "kv_len", "codes", "scales", "table", "out", "lse", "ws"):
+        if getattr(a, name) is not None:
+            setattr(a, name, at16(getattr(a, name)))
+    a.out.fill_(7), a.lse.fill_(7)
+    a.call()
+    got = a.result()
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    assert abi.csa2_status_fetch(a.ws)[0] == abi.OK
+
+
+def test_products_norms_and_plans_of_pointers_at_16_bytes(abi):
+    rng = np.random.default_rng(62)
+    codes, scales = (at16(dev(v)) for v in weight(rng, 300, 640))
+    ws = fresh_ws(abi, abi.csa2_fp4_matvec_workspace_bytes(5, 640, 300) + 16)[16:]
+    out = at16(torch.zeros(5, 300, device="cuda"))
+    for xt, xs in ((bf16(rng.standard_normal((5, 640))), None),
+                   (torch.randn(5, 640, generator=torch.Generator().manual_seed(1)).to(torch.float8_e4m3fn), np.ones(5, np.float32))):
+        abi.csa2_fp4_matvec(at16(xt.cuda().view(torch.uint8)), abi.X_BF16 if xs is None else abi.X_E4M3,
+                            None if xs is None else at16(dev(xs)), 640, 5, 640, codes, scales, 300, 1.0, out, abi.OUT_F32, ws,
+                            ws.numel())
+        torch.cuda.synchronize()
+        check_matvec(out.double().cpu().numpy(), xt, xs, codes.cpu().numpy(), scales.cpu().numpy(), 1.0, torch.float32)
+    x, w = bf16(rng.standard_normal((9, 640))), bf16(rng.standard_normal(640))
+    res, y = at16(torch.zeros(9, 640, dtype=torch.bfloat16, device="cuda")), at16(torch.zeros(9, 640, dtype=torch.bfloat16, device="cuda"))
+    c, sc = at16(torch.zeros(9, 640, dtype=torch.uint8, device="cuda")), at16(torch.zeros(9, 5, device="cuda"))
+    abi.csa2_rmsnorm_fp8(at16(x.cuda()), 640, res, res, at16(w.cuda()), 9, 640, 1e-6, 128, c, sc, y)
+    torch.cuda.synchronize()
+    check_norm(x.double().numpy(), w.double().numpy(), 128, c.view(torch.float8_e4m3fn).double().cpu().numpy(),
+               sc.cpu().numpy(), y.double().cpu().numpy())
+    cached, added, table, free, n_free, n_pages = plan_inputs(rng, [9, 30], [20, 5], 8)
+    t, q, k = at16(dev(table)), *(at16(torch.zeros(n, dtype=torch.int32, device="cuda")) for n in (3, 2))
+    sl, po = (at16(torch.zeros(40, dtype=torch.int64, device="cuda")) for _ in range(2))
+    nf, ws = at16(dev(np.array([n_free], np.int32))), fresh_ws(abi, abi.STATUS_BYTES + 16)[16:]
+    abi.csa2_page_plan(at16(dev(cached)), at16(dev(added)), 2, 8, t, table.shape[1], at16(dev(free)), n_pages, nf, nf, q, k, sl, po, 40,
+                       ws, ws.numel())
+    torch.cuda.synchronize()
+    check_plan(tuple(v.cpu().numpy() for v in (t, q, k, sl, po)) + (int(nf.item()),),
+               PO.page_plan(cached, added, 8, table, free, n_free, n_pages, 40))
