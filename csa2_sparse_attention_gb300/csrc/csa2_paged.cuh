@@ -74,7 +74,7 @@ struct PagedArgs {
     int32_t* chunk_out;
     FastDiv by_heads, by_page, by_few;
     int32_t span;          // decoded tiles per request
-    int32_t item;          // rows of a work item: 64, or the 256 of a cluster's two tiles (decoded tiles); 2^item_log2
+    int32_t item;          // rows of a work item: 64, or the 256 of two row tiles (decoded tiles); 2^item_log2
     int32_t item_log2, item_tokens;
     int32_t rows_over, rows_to;  // requests of rows_over < rows <= rows_to are this kernel's
     int32_t few_rows;      // the most rows of such a request
@@ -142,7 +142,7 @@ __device__ __forceinline__ int32_t paged_chunk(const PagedArgs& a, uint32_t item
 // with the fewest keys), what is left of whole waves of kPTailSlots, are split
 // where two or more fit into the place of one.  `items`: how many are split,
 // `splits`: into how many.
-constexpr int32_t kPTailSlots = 38, kPTailTiles = 12;  // clusters of 4 CTAs at a time; key tiles that are worth it
+constexpr int32_t kPTailSlots = 38, kPTailTiles = 12;  // items of 4 CTAs at a time; key tiles that are worth it
 __host__ __device__ inline void paged_tail(int32_t n, int32_t tiles, int32_t& items, int32_t& splits) {
     items = n % kPTailSlots;
     splits = items > 0 ? kPTailSlots / items : 1;
@@ -286,29 +286,6 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-// Clusters of two CTAs: a barrier of all their threads; an arrival at the other
-// CTA's mbarrier; a commit and a bulk copy that reach both (same offsets).
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t cta) {
-    uint32_t at;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(cta));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
-}
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     smem_u32(bar)),
-                 "h"(uint16_t(3))
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(uint16_t(3))
-        : "memory");
 }
 // One bulk copy shared memory -> global (addresses and size multiples of 16
 // bytes), and the wait until this thread's copies have read shared memory (what

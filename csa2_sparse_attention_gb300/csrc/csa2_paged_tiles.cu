@@ -27,10 +27,8 @@
 //
 // Keys go in tiles of 128: an M = 128 MMA of K = 16 takes 64 clocks for any
 // N up to 128 (measured 64-69) and 128 for N = 256, so S wants 128 keys and O
-// 256 channels at once.  Two CTAs with consecutive row tiles and the same half
-// form a cluster and copy half of every tile into both: alone, each took 128 KB
-// per tile, 7.8 TB/s from L2 over the GPU, which bounded the kernel (2.25 ms).
-// Three roles:
+// 256 channels at once.  Every CTA copies its own 128 KB per tile, 9.1 TB/s from L2
+// over the GPU for 1024 tokens over 16K, with plain bulk copies.  Three roles:
 //   copy warp  the other half's channels X of a tile first, then, as the logits'
 //       MMAs release them, the own half's Y into the same group.  One copy of Y
 //       serves S (K-major) and O (MN-major).
@@ -82,9 +80,8 @@ struct PagedTilesSmem {
 static_assert(sizeof(PagedTilesSmem) + 1024 <= 227 * 1024, "shared memory of the paged attention");
 static_assert(kPM * (kPHalf * 4 + 16) <= 2 * kPN * kPHalf * 2 + kPM * kPN * 2, "the epilogue's rows in the latents' and P's place");
 
-// grid: 4 CTAs (two output halves, two row tiles of a cluster) per (pair of row
-// tiles, split), the ones with the most keys first; CTAs beyond the last one
-// leave at once.
+// grid: 4 CTAs (two output halves, two row tiles) per (pair of row tiles, split),
+// the ones with the most keys first; CTAs beyond the last one leave at once.
 __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const PagedArgs a) {
     constexpr int kMmaWarp = kPSoftWarps, kCopyWarp = kPSoftWarps + 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -100,16 +97,16 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     paged_find<kPTileThreads / 32>(a, blockIdx.x >> 2, blockIdx.x == 0, S.work, S.sums);
     __syncthreads();
     const int64_t req = S.work.req;
-    if (req < 0) {
+    const PagedReq rq = S.work.rq;
+    const int32_t nt = S.work.nt, key0 = S.work.key0, splits = S.work.splits;
+    // the CTA's row tile (an item's second one may be behind the request's rows)
+    const int32_t ti = 2 * S.work.item + rank;
+    const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
+    if (req < 0 || n_row <= 0) {
         grid_dep_wait();  // (a launch behind this one may rely on the decode kernel's end)
         return;
     }
-    const PagedReq rq = S.work.rq;
-    const int32_t nt = S.work.nt, key0 = S.work.key0, splits = S.work.splits;
-    // the CTA's row tile (a cluster's second one may be behind the request's rows: it then only helps to copy)
-    const int32_t ti = 2 * S.work.item + rank;
-    const int32_t n_row = rq.nq * a.heads - ti * kPM < kPM ? rq.nq * a.heads - ti * kPM : kPM;
-    const int64_t flat0 = int64_t(rq.q0) * a.heads + (n_row > 0 ? int64_t(ti) * kPM : 0);
+    const int64_t flat0 = int64_t(rq.q0) * a.heads + int64_t(ti) * kPM;
     const int y_dim = kPHalf * half;
 
     // ---- Q: two groups of 8 rows per warp; the loads are under way while the CTA sets up
@@ -125,8 +122,8 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&S.full_x[g][b], 1);
                 mbar_init(&S.full_y[g][b], 1);
-                mbar_init(&S.empty_x[g][b], 2);  // both CTAs' MMAs
-                mbar_init(&S.empty_o[g][b], 2);
+                mbar_init(&S.empty_x[g][b], 1);
+                mbar_init(&S.empty_o[g][b], 1);
             }
         }
         mbar_init(&S.s_full, 1);
@@ -134,29 +131,25 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         mbar_init(&S.p_full, kPSoftWarps);
         mbar_init(&S.p_free, 1);
         mbar_init(&S.o_done, 1);
-        mbar_init(&S.q_done, 2 * kPSoftWarps);
-        mbar_init(&S.drain, 2);
+        mbar_init(&S.q_done, kPSoftWarps);
+        mbar_init(&S.drain, 1);
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
     tc_fence_before();
-    cluster_sync();  // the other CTA's barriers are initialized as well
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
 
-    // ---- decoded tiles: a block of 128 channels is 2 KB of each of 16 key
-    // groups.  Each CTA of the cluster copies half of them into both: without
-    // sharing, 128 KB per key tile and CTA took 7.8 TB/s from L2 and bounded the
-    // kernel.
+    // ---- decoded tiles: a block of 128 channels is 2 KB of each of 16 key groups
     const int64_t tile0 = req * a.span + (key0 - paged_base(a, rq)) / kPN;
     auto copy_block = [&](uint64_t* bar, int g, int b, const uint8_t* src, const uint8_t* fl) {
         if (lane == 0) mbar_arrive_expect_tx(bar, kPN * 128 * 2 + (fl ? kPFlagBytes : 0));
         __syncwarp();
-        const uint32_t at = b * kPBlockBytes + rank * (kPBlockBytes / 2);
         if (lane == 0)
-            bulk_g2s_pair(S.c[g] + at, src + at, kPBlockBytes / 2, bar);
-        else if (lane == 1 && fl && rank == 0)
-            bulk_g2s_pair(&S.flags[g], fl, kPFlagBytes, bar);
+            bulk_g2s(S.c[g] + b * kPBlockBytes, src + b * kPBlockBytes, kPBlockBytes, bar);
+        else if (lane == 1 && fl)
+            bulk_g2s(&S.flags[g], fl, kPFlagBytes, bar);
         __syncwarp();
     };
     const uint8_t* x_src = a.tiles + tile0 * kPTileBytes + (1 - half) * (kPTileBytes / 2);
@@ -202,7 +195,6 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&S.q_done);  // the second group of latents may be filled
-            mbar_arrive_peer(&S.q_done, rank ^ 1);
             mbar_arrive(&S.s_free);  // phase 0: Q is in place
         }
 
@@ -416,12 +408,11 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_f16_ss(tmem + kColS, dq + (8 * b + k) * (256 >> 4), d + b * (kPBlockBytes >> 4) + k * (256 >> 4), id_s, k > 0 || b > 0);
-                tc_commit_pair(&S.empty_x[g][b]);
+                tc_commit(&S.empty_x[g][b]);
             }
             if (ok && j > 0) {
                 o_mma(j - 1, 0);
-                // (only what the copies wait for: an arrival at the other CTA must not outlive it)
-                if (ok && j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1][0]);
+                if (ok && j + 1 < nt) tc_commit(&S.empty_o[g ^ 1][0]);
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -435,16 +426,15 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             if (ok && j > 0) {
                 o_mma(j - 1, 1);
                 tc_commit(&S.p_free);
-                if (j + 1 < nt) tc_commit_pair(&S.empty_o[g ^ 1][1]);
+                if (j + 1 < nt) tc_commit(&S.empty_o[g ^ 1][1]);
             }
         }
         if (nt > 0) {
             for (int b = 0; b < 2; ++b) o_mma(nt - 1, b);
             if (ok) tc_commit(&S.o_done);
             if (!ok) record(a.st, CSA2_ERR_TIMEOUT, 8, int32_t(req), ti);
-            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done (in a cluster:
-            // until both CTAs' commits have arrived here)
-            tc_commit_pair(&S.drain);
+            // after a give-up anywhere, TMEM and shared memory stay until the MMAs in flight are done
+            tc_commit(&S.drain);
             mbar_wait(&S.drain, 0, kDrainNs);
         }
     } else if (warp == kCopyWarp) {
@@ -479,7 +469,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             }
     }
     tc_fence_before();
-    cluster_sync();  // neither CTA leaves while the other may copy or arrive here
+    __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -584,7 +574,7 @@ csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cuda
     timer_end(K_PAGED_DECODE, s);
     if (e1 != cudaSuccess) return CSA2_ERR_CUDA;
     timer_begin(K_PAGED_ATTN, s);
-    const cudaError_t e2 = launch(paged_tiles_kernel, dim3(grid), kPTileThreads, sizeof(PagedTilesSmem), s, 2, a);
+    const cudaError_t e2 = launch(paged_tiles_kernel, dim3(grid), kPTileThreads, sizeof(PagedTilesSmem), s, 1, a);
     timer_end(K_PAGED_ATTN, s);
     return e2 == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

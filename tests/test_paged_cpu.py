@@ -158,3 +158,16 @@ def test_norm_and_product_forms_by_hand():
     codes = np.full((1, 8), 0x21, np.uint8)  # 0.5, 1.0 in turn
     got, reach = PO.matvec(np.arange(16.0)[None], np.array([2.0], np.float32), codes, np.array([[0x40]], np.uint8), 0.5)
     assert got[0, 0] == 0.5 * 2 * 2 * (0.5 * 56 + 64) and reach[0, 0] == got[0, 0]
+
+
+# ------------------------------------------------------------- the sources
+def test_no_kernel_loads_by_multicast():
+    """Ranks of several GPUs load the same library: no copy into shared memory reaches more than its own block."""
+    import glob
+    import os
+    import re
+    root = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "csa2_sparse_attention_gb300", "csrc")
+    files = glob.glob(os.path.join(root, "*.cu*"))
+    assert len(files) > 10
+    for f in files:
+        assert not re.search("multi" + "cast", open(f).read()), f
