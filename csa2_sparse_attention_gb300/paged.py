@@ -145,8 +145,8 @@ class PagedLatents:
         return self.out[:n_tokens], self.lse[:n_tokens]
 
     def advance(self):
-        """After a step: what it added is cached."""
-        self.cached.copy_(self.kv_len)
+        """After a step: what it added is cached.  A step whose plan was refused added nothing (its kv_len are all 0)."""
+        self.cached.copy_(torch.where(self.kv_len.any(), self.kv_len, self.cached))
 
     def status(self):
         """Status words of every workspace (first device-detected problem)."""

@@ -1122,3 +1122,61 @@ def test_products_norms_and_plans_of_pointers_at_16_bytes(abi):
     torch.cuda.synchronize()
     check_plan(tuple(v.cpu().numpy() for v in (t, q, k, sl, po)) + (int(nf.item()),),
                PO.page_plan(cached, added, 8, table, free, n_free, n_pages, 40))
+
+
+# -------------------------------------------------- the cache between steps
+def cache_step(cache, g, added, captured=None):
+    """One step of random latents and queries (n tokens in all) over the cache, eager or by replaying a graph."""
+    q, lat = captured[1:] if captured else (torch.empty(16, cache.heads, D, dtype=torch.bfloat16, device="cuda"),
+                                            torch.empty(16, D, dtype=torch.bfloat16, device="cuda"))
+    q.copy_(torch.randn(q.shape, generator=g)), lat.copy_(torch.randn(lat.shape, generator=g))
+    cache.added.copy_(torch.tensor(added, dtype=torch.int32))
+
+    def calls():
+        cache.plan()
+        cache.append(lat, 16)
+        cache.attend(q, 16, 16, 96)
+        cache.advance()
+    torch.cuda.synchronize()
+    if captured is None:
+        calls()
+    elif captured[0] is None:
+        cache.workspace(16, 16, 96)
+        captured[0] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured[0]):
+            calls()
+    if captured:
+        captured[0].replay()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("refused", [[0, 97, 0], [16, 40, 16], [-1, 1, 1]])  # a table row too short, too few pages, a bad length
+def test_refused_step_leaves_the_cache_as_it_was(abi, captured, refused):
+    """A step that the plan refuses, advanced over like any other, changes nothing: the steps behind it are those of a
+    cache that never saw it."""
+    from csa2_sparse_attention_gb300 import paged
+    runs = []
+    for also in (False, True):
+        cache = paged.PagedLatents(3, 97, 7, 16, 6, heads=4, fmt=abi.FMT_FP4)
+        g, use = torch.Generator().manual_seed(3), [None, torch.zeros(16, 4, D, dtype=torch.bfloat16, device="cuda"),
+                                                    torch.zeros(16, D, dtype=torch.bfloat16, device="cuda")] if captured else None
+        cache_step(cache, g, [10, 4, 2], use)
+        cache_step(cache, g, [6, 9, 1], use)
+        if also:
+            before = [t.clone() for t in (cache.cached, cache.table, cache.n_free, cache.codes, cache.scales)]
+            assert cache.cached.tolist() == [16, 13, 3] and cache.status()["plan"][0] == abi.OK
+            state = g.get_state()
+            cache_step(cache, g, refused, use)
+            g.set_state(state)
+            assert cache.status()["plan"][0] == abi.ERR_DEVICE_BOUNDS
+            for got, want in zip((cache.cached, cache.table, cache.n_free, cache.codes, cache.scales), before):
+                assert torch.equal(got, want)
+        cache_step(cache, g, [1, 14, 1], use)
+        cache_step(cache, g, [0, 1, 15], use)
+        cache.advance()  # once more changes nothing
+        assert cache.cached.tolist() == [17, 28, 19]
+        runs.append([t.clone() for t in (cache.cached, cache.table, cache.n_free, cache.kv_len, cache.codes, cache.scales, cache.out,
+                                         cache.lse)])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
