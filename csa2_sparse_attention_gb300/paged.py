@@ -144,14 +144,17 @@ class PagedLatents:
                             self.out, self.lse, ws, ws.numel(), s)
         return self.out[:n_tokens], self.lse[:n_tokens]
 
-    def advance(self):
-        """After a step: what it added is cached.  A step whose plan was refused added nothing (its kv_len are all 0)."""
-        self.cached.copy_(torch.where(self.kv_len.any(), self.kv_len, self.cached))
+    def advance(self, stream=None):
+        """After a step, on its stream: what it added is cached.  A step whose plan was refused added nothing (its kv_len
+        are all 0)."""
+        with torch.cuda.stream(_stream(self.dev, stream)):
+            self.cached.copy_(torch.where(self.kv_len.any(), self.kv_len, self.cached))
 
-    def status(self):
-        """Status words of every workspace (first device-detected problem)."""
-        named = {"plan": abi.csa2_status_fetch(self.ws_plan), "append": abi.csa2_status_fetch(self.ws_app)}
-        attn = [abi.csa2_status_fetch(ws) for ws in self._kept + [self.ws_attn] if ws is not None]
+    def status(self, stream=None):
+        """Status words of every workspace (first device-detected problem), behind what runs on the stream so far."""
+        s = _stream(self.dev, stream)
+        named = {"plan": abi.csa2_status_fetch(self.ws_plan, s), "append": abi.csa2_status_fetch(self.ws_app, s)}
+        attn = [abi.csa2_status_fetch(ws, s) for ws in self._kept + [self.ws_attn] if ws is not None]
         if attn:
             named["attn"] = next((st for st in attn if st[0] != abi.OK), attn[-1])
         return named

@@ -1180,3 +1180,38 @@ def test_refused_step_leaves_the_cache_as_it_was(abi, captured, refused):
                                          cache.lse)])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def test_advance_and_status_of_a_step_on_another_stream(abi):
+    """The step's stream is held up by other work: what advance() and status() take from the step comes behind it."""
+    runs = []
+    for apart in (False, True):
+        paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+        st = torch.cuda.Stream() if apart else None
+        x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+        tok = torch.randn(3, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+        cache.workspace(56, 30, 64)
+        torch.cuda.synchronize()
+        for added, rows in (([30, 9, 17], x), ([1, 1, 1], tok)):
+            cache.added.copy_(torch.tensor(added, dtype=torch.int32))
+            layer.residual.zero_()
+            torch.cuda.synchronize()
+            if apart:
+                with torch.cuda.stream(st):
+                    torch.cuda._sleep(200_000_000)
+            layer.step(rows, len(rows), 30, 64, st)
+            cache.advance(st)
+            torch.cuda.synchronize()
+        cache.table[0, 1] = cache.n_pages
+        assert cache.cached.tolist() == [31, 10, 18]
+        cache.added.fill_(0)
+        cache.added[0] = 1  # its page is the one outside
+        torch.cuda.synchronize()
+        if apart:
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(200_000_000)
+        layer.step(tok[:1], 1, 30, 64, st)
+        assert cache.status(st)["plan"][0] == cache.status(st)["attn"][0] == abi.ERR_DEVICE_BOUNDS
+        runs.append((cache.cached.clone(), cache.codes.clone(), cache.out[:3].clone()))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
