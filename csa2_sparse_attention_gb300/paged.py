@@ -29,6 +29,8 @@ LATENT = abi.LATENT_DIM
 def _stream(dev, stream):
     if dev.index != torch.cuda.current_device():
         raise ValueError(f"the current device is not {dev}")
+    if isinstance(stream, int):  # a cudaStream_t, as the C calls take it
+        return torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
     return torch.cuda.current_stream(dev) if stream is None else stream
 
 
@@ -115,12 +117,14 @@ class PagedLatents:
                                  self.max_pos if fp4 else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
                                  self.ws_app.numel(), s)
 
-    def workspace(self, n_tokens, max_q, max_kv):
-        """The attention's workspace for these bounds (kept, and grown where a later step needs more)."""
+    def workspace(self, n_tokens, max_q, max_kv, stream=None):
+        """The attention's workspace for these bounds (kept, and grown where a later step needs more; not while `stream`,
+        or the current one, is being captured)."""
         need = abi.csa2_paged_attn_workspace_bytes(n_tokens, self.heads, self.n_req, max_q, max_kv, self.window)
         if need == 0:
             raise ValueError("the attention does not run calls of these sizes")
-        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(_stream(self.dev, stream)):
+            capturing = torch.cuda.is_current_stream_capturing()
         if self.ws_attn is None or self.ws_attn.numel() < need:
             if capturing:
                 raise RuntimeError("a step with these bounds has to run once before it is captured: its workspace grows")
@@ -138,7 +142,7 @@ class PagedLatents:
         self._tokens(n_tokens)
         _rows("q", q, n_tokens, (self.heads, LATENT))
         s = _stream(self.dev, stream)
-        ws = self.workspace(n_tokens, max_q, max_kv)
+        ws = self.workspace(n_tokens, max_q, max_kv, s)
         abi.csa2_paged_attn(q, n_tokens, self.heads, self.q_start, self.kv_len, self.n_req, max_q, max_kv, self.fmt, self.codes,
                             self.scales, self.n_rows, self.table, self.max_pages, self.page_size, self.window, self.sm_scale,
                             self.out, self.lse, ws, ws.numel(), s)

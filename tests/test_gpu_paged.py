@@ -1215,3 +1215,37 @@ def test_advance_and_status_of_a_step_on_another_stream(abi):
         runs.append((cache.cached.clone(), cache.codes.clone(), cache.out[:3].clone()))
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("handle", [False, True])  # the stream as an object, as a number
+def test_capture_on_the_given_stream(abi, handle):
+    """A stream that is being captured while another one is current: its step's workspace stays in the graph, and one
+    that would have to grow it is refused without ending the capture."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    cache.added.copy_(torch.tensor([30, 9, 17], dtype=torch.int32))
+    layer.step(torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda(), 56, 30, 64)
+    cache.advance()
+    cache.added.fill_(0)
+    cache.plan()
+    cache.q_start.copy_(torch.tensor([0, 1, 2, 3], dtype=torch.int32))  # (a query over what is there)
+    q = layer.q[:3].clone()
+    cache.attend(q, 3, 1, 64)
+    torch.cuda.synchronize()
+    want, held = cache.out[:3].clone(), cache.ws_attn
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    given = st.cuda_stream if handle else st
+    with torch.cuda.stream(st):
+        graph.capture_begin(capture_error_mode="thread_local")
+    try:
+        cache.attend(q, 3, 1, 64, given)
+        with pytest.raises(RuntimeError, match="captured"):
+            cache.attend(q, 3, 3, 1 << 16, given)
+    finally:
+        with torch.cuda.stream(st):
+            graph.capture_end()
+    cache.attend(q, 3, 3, 1 << 16)
+    assert cache.ws_attn is not held and any(w is held for w in cache._kept)
+    cache.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.out[:3], want) and cache.status()["attn"][0] == abi.OK
