@@ -128,11 +128,13 @@ class PagedLatents:
         if self.ws_attn is None or self.ws_attn.numel() < need:
             if capturing:
                 raise RuntimeError("a step with these bounds has to run once before it is captured: its workspace grows")
-            if self._captured:
-                self._kept.append(self.ws_attn)
-                self._captured = False
             torch.cuda.synchronize(self.dev)  # whatever stream still uses the old one
-            self.ws_attn = torch.zeros(need, dtype=torch.uint8, device=self.dev)
+            old, self.ws_attn = self.ws_attn, torch.zeros(need, dtype=torch.uint8, device=self.dev)
+            if self._captured:
+                self._kept.append(old)
+                self._captured = False
+            elif old is not None:
+                self.ws_attn[:16].copy_(old[:16])  # a problem on record stays on record
             torch.cuda.synchronize(self.dev)
         self._captured = self._captured or capturing
         return self.ws_attn

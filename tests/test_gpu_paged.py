@@ -1249,3 +1249,21 @@ def test_capture_on_the_given_stream(abi, handle):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(cache.out[:3], want) and cache.status()["attn"][0] == abi.OK
+
+
+def test_status_outlives_its_workspace(abi):
+    """A problem that a step recorded is still there after a larger step took another workspace."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    cache.added.copy_(torch.tensor([30, 9, 17], dtype=torch.int32))
+    x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+    layer.step(x, 56, 20, 64)  # request 0 brings more than max_q
+    first = cache.status()["attn"]
+    assert first == [abi.ERR_DEVICE_BOUNDS, 9, 0, 30]
+    held = cache.ws_attn
+    for kv in (1000, 1 << 16):
+        cache.attend(layer.q, 56, 30, kv)
+        assert cache.ws_attn is not held and not cache._kept and cache.status()["attn"] == first
+        held = cache.ws_attn
+    abi.csa2_status_reset(cache.ws_attn)
+    cache.attend(layer.q, 56, 30, 64)
+    assert cache.ws_attn is held and cache.status()["attn"][0] == abi.OK
