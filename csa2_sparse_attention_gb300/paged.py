@@ -17,6 +17,7 @@ current device.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 
 import torch
@@ -65,6 +66,13 @@ class PagedLatents:
         d = torch.device(device)
         if d.type == "cuda" and d.index is None:
             d = torch.device("cuda", torch.cuda.current_device())
+        if n_req < 1 or max_tokens < 1 or n_pages < 1 or max_pages < 1:
+            raise ValueError("a cache has a request, a token of a step, a page and a place for it")
+        if page_size < 8 or page_size > 65536 or page_size % 8 or not 1 <= heads <= 128:
+            raise ValueError(f"pages of {page_size} entries or {heads} heads: multiples of 8 up to 65536, and up to 128 heads")
+        if fmt not in (abi.FMT_FP4, abi.FMT_FP8) or window < 0 or \
+                not 0.0 < ctypes.c_float(sm_scale).value < torch.finfo(torch.float32).max:
+            raise ValueError(f"format {fmt}, window {window}, scale {sm_scale}")
         self.dev = d
         self.n_req, self.max_tokens, self.heads = n_req, max_tokens, heads
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
@@ -198,6 +206,7 @@ class PagedLayer:
         c._tokens(n)
         _rows("hidden", hidden, n, (self.hidden,))
         s = _stream(c.dev, stream)
+        c.workspace(n, max_q, max_kv, s)  # what refuses the step refuses it before the residual, pages and lengths change
         abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
                              self.x, self.x_scales, None, s)
         self._project(self.wq, n, c.heads * LATENT, self.q, s)

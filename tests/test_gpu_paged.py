@@ -1267,3 +1267,33 @@ def test_status_outlives_its_workspace(abi):
     abi.csa2_status_reset(cache.ws_attn)
     cache.attend(layer.q, 56, 30, 64)
     assert cache.ws_attn is held and cache.status()["attn"][0] == abi.OK
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_refused_bounds_leave_the_step_undone(abi, captured):
+    """A step whose bounds are refused (too large, or a capture that would need a larger workspace) has changed nothing."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+    cache.added.copy_(torch.tensor([30, 9, 17], dtype=torch.int32))
+    layer.step(x, 56, 30, 64)
+    cache.advance()
+    cache.added.fill_(1)
+    state = lambda: [t.clone() for t in (layer.residual, layer.x, layer.q, cache.table, cache.n_free, cache.kv_len, cache.q_start,  # noqa: E731
+                                         cache.slots, cache.codes, cache.out)]
+    before = state()
+    torch.cuda.synchronize()
+    if captured:
+        with pytest.raises(RuntimeError, match="captured"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                layer.step(x, 3, 1, 1 << 16)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):  # what was captured before the refusal, if a caller goes on
+            with pytest.raises(RuntimeError, match="captured"):
+                layer.step(x, 3, 1, 1 << 16)
+        graph.replay()
+    else:
+        with pytest.raises(ValueError):
+            layer.step(x, 3, 1, (1 << 30) + 1)
+    torch.cuda.synchronize()
+    for a, b in zip(state(), before):
+        assert torch.equal(a, b)

@@ -171,3 +171,15 @@ def test_no_kernel_loads_by_multicast():
     assert len(files) > 10
     for f in files:
         assert not re.search("multi" + "cast", open(f).read()), f
+
+
+@pytest.mark.parametrize("kw", [dict(n_req=0), dict(max_tokens=0), dict(n_pages=0), dict(max_pages=0), dict(page_size=12),
+                                dict(page_size=0), dict(page_size=65544), dict(heads=0), dict(heads=129), dict(fmt=2), dict(window=-1),
+                                dict(sm_scale=0.0), dict(sm_scale=1e-50), dict(sm_scale=float("nan")), dict(sm_scale=float("inf"))])
+def test_cache_that_no_step_can_use(abi, kw):
+    """Refused when it is made, not in the middle of its first step."""
+    from csa2_sparse_attention_gb300 import paged
+    good = dict(n_req=2, max_tokens=8, n_pages=4, page_size=16, max_pages=2, heads=4, fmt=abi.FMT_FP8, device="cpu")
+    paged.PagedLatents(**good)
+    with pytest.raises(ValueError):
+        paged.PagedLatents(**{**good, **kw})
