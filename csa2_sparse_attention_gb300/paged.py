@@ -35,8 +35,10 @@ def _stream(dev, stream):
     return torch.cuda.current_stream(dev) if stream is None else stream
 
 
-def _rows(name, x, n, shape, dtype=torch.bfloat16):
-    """x has at least n contiguous rows of this shape."""
+def _rows(name, x, n, shape, dev, dtype=torch.bfloat16):
+    """x has at least n contiguous rows of this shape on the device."""
+    if x.device != dev:
+        raise ValueError(f"{name}: on {x.device}, not on {dev}")
     if x.dtype != dtype or tuple(x.shape[1:]) != tuple(shape) or x.shape[0] < n or not x.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} rows of {tuple(shape)}, at least {n} of them, not {x.dtype} {tuple(x.shape)}")
 
@@ -118,7 +120,7 @@ class PagedLatents:
         """The new tokens' bf16 latents [n_tokens][512] into the planned rows.  Rows behind the planned tokens (a padded
         batch) are stored nowhere; the first of them is in the append's status."""
         self._tokens(n_tokens)
-        _rows("latents", latents, n_tokens, (LATENT,))
+        _rows("latents", latents, n_tokens, (LATENT,), self.dev)
         s = _stream(self.dev, stream)
         fp4 = self.fmt == abi.FMT_FP4
         abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if fp4 else None, self.rope,
@@ -150,7 +152,7 @@ class PagedLatents:
     def attend(self, q, n_tokens, max_q, max_kv, stream=None):
         """out, lse of the new tokens' queries q [n_tokens][heads][512] over all entries."""
         self._tokens(n_tokens)
-        _rows("q", q, n_tokens, (self.heads, LATENT))
+        _rows("q", q, n_tokens, (self.heads, LATENT), self.dev)
         s = _stream(self.dev, stream)
         ws = self.workspace(n_tokens, max_q, max_kv, s)
         abi.csa2_paged_attn(q, n_tokens, self.heads, self.q_start, self.kv_len, self.n_req, max_q, max_kv, self.fmt, self.codes,
@@ -204,7 +206,7 @@ class PagedLayer:
         out and lse as they are; see PagedLatents.append."""
         c, n = self.cache, n_tokens
         c._tokens(n)
-        _rows("hidden", hidden, n, (self.hidden,))
+        _rows("hidden", hidden, n, (self.hidden,), c.dev)
         s = _stream(c.dev, stream)
         c.workspace(n, max_q, max_kv, s)  # what refuses the step refuses it before the residual, pages and lengths change
         abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,

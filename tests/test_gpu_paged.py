@@ -1297,3 +1297,13 @@ def test_refused_bounds_leave_the_step_undone(abi, captured):
     torch.cuda.synchronize()
     for a, b in zip(state(), before):
         assert torch.equal(a, b)
+
+
+def test_step_refuses_host_tensors(abi):
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    c0 = abi.csa2_launch_count()
+    with pytest.raises(ValueError, match="hidden: on cpu"):
+        layer.step(torch.zeros(3, layer.hidden, dtype=torch.bfloat16), 3, 1, 64)
+    with pytest.raises(ValueError, match="q: on cpu"):
+        cache.attend(torch.zeros(3, cache.heads, D, dtype=torch.bfloat16), 3, 1, 64)
+    assert abi.csa2_launch_count() == c0

@@ -183,3 +183,16 @@ def test_cache_that_no_step_can_use(abi, kw):
     paged.PagedLatents(**good)
     with pytest.raises(ValueError):
         paged.PagedLatents(**{**good, **kw})
+
+
+def test_rows_on_another_device_are_refused(abi):
+    """A pointer of another device's memory never reaches a kernel."""
+    from csa2_sparse_attention_gb300 import paged
+    c = paged.PagedLatents(2, 8, 4, 16, 2, heads=4, fmt=abi.FMT_FP8, device="cpu")
+    rows = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="meta")  # noqa: E731
+    c0 = abi.csa2_launch_count()
+    with pytest.raises(ValueError, match="latents: on meta"):
+        c.append(rows(8, 512), 8)
+    with pytest.raises(ValueError, match="q: on meta"):
+        c.attend(rows(8, 4, 512), 8, 1, 1)
+    assert abi.csa2_launch_count() == c0
