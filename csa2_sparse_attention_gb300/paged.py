@@ -182,6 +182,10 @@ class PagedLayer:
     def __init__(self, cache, hidden, norm_weight, wq, wlatent, eps=1e-6):
         """norm_weight bf16 [hidden]; wq, wlatent: bf16 weights [heads * 512][hidden], [512][hidden]."""
         d, T, H = cache.dev, cache.max_tokens, cache.heads
+        sizes = [abi.csa2_fp4_matvec_workspace_bytes(T, hidden, n) for n in (H * LATENT, LATENT)]
+        if 0 in sizes or hidden > 16384 or not 0.0 <= ctypes.c_float(eps).value < math.inf:
+            raise ValueError(f"a layer of {hidden} channels for steps of {T} tokens, eps {eps}: multiples of 128 up to 16384, up to "
+                             "65536 tokens")
         for name, w, shape in (("norm_weight", norm_weight, (hidden,)), ("wq", wq, (H * LATENT, hidden)),
                                ("wlatent", wlatent, (LATENT, hidden))):
             if w.dtype != torch.bfloat16 or tuple(w.shape) != shape or w.device != d:
@@ -193,8 +197,7 @@ class PagedLayer:
         self.x_scales = torch.zeros(T, dtype=torch.float32, device=d)
         self.q = torch.zeros((T, H, LATENT), dtype=torch.bfloat16, device=d)
         self.latents = torch.zeros((T, LATENT), dtype=torch.bfloat16, device=d)
-        size = max(abi.csa2_fp4_matvec_workspace_bytes(T, hidden, H * LATENT), abi.csa2_fp4_matvec_workspace_bytes(T, hidden, LATENT))
-        self.ws = torch.zeros(size, dtype=torch.uint8, device=d)
+        self.ws = torch.zeros(max(sizes), dtype=torch.uint8, device=d)
 
     def _project(self, w, n, n_out, out, s):
         abi.csa2_fp4_matvec(self.x, abi.X_E4M3, self.x_scales, self.hidden, n, self.hidden, w[0], w[1], n_out, 1.0, out,

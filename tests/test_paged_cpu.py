@@ -196,3 +196,16 @@ def test_rows_on_another_device_are_refused(abi):
     with pytest.raises(ValueError, match="q: on meta"):
         c.attend(rows(8, 4, 512), 8, 1, 1)
     assert abi.csa2_launch_count() == c0
+
+
+@pytest.mark.parametrize("kw", [dict(hidden=200), dict(hidden=16512), dict(tokens=65537), dict(eps=-1.0), dict(eps=float("nan")),
+                                dict(eps=float("inf"))])
+def test_layer_that_no_step_can_use(abi, kw):
+    """Sizes that the norm or the products do not run are refused when the layer is made."""
+    from csa2_sparse_attention_gb300 import paged
+    use = {**dict(hidden=256, tokens=4, eps=1e-6), **kw}
+    c = paged.PagedLatents(1, 4, 1, 8, 1, heads=1, fmt=abi.FMT_FP8, device="cpu")
+    c.max_tokens = use["tokens"]
+    w = lambda *shape: torch.zeros(1, dtype=torch.bfloat16).expand(*shape)  # noqa: E731
+    with pytest.raises(ValueError, match="channels for steps"):
+        paged.PagedLayer(c, use["hidden"], w(use["hidden"]), w(512, use["hidden"]), w(512, use["hidden"]), use["eps"])
