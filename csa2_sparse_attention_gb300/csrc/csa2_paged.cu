@@ -38,7 +38,22 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
             }
         }
         PagedReq rq;
-        if (!paged_request(a, req, rq, nullptr) || !paged_mine(a, rq)) continue;
+        bool found = paged_request(a, req, rq, nullptr);
+        if (!a.behind && !a.tail) {
+            // A token behind the last request, or q_start is out of order, where the search above leads anywhere: the
+            // attention kernel took every request with good bounds all the same, so look at all of them.
+            const int32_t tok = int32_t(prow) / a.by_heads;
+            auto owns = [&](const PagedReq& o) { return tok >= o.q0 && tok - o.q0 < o.nq; };
+            found = found && owns(rq);
+            if (!found) {
+                int32_t own = INT32_MAX;
+                for (int64_t r = lane; r < a.n_req && own == INT32_MAX; r += 32)
+                    if (paged_request(a, r, rq, nullptr) && owns(rq)) own = int32_t(r);
+                own = __reduce_min_sync(0xffffffffu, own);
+                found = own != INT32_MAX && paged_request(a, own, rq, nullptr);
+            }
+        }
+        if (!found || !paged_mine(a, rq)) continue;
         const int64_t at = prow - (a.behind ? req * a.few_rows : a.tail ? 0 : int64_t(rq.q0) * a.heads);  // of the request's rows
         if (at < 0 || at >= int64_t(rq.nq) * a.heads) continue;
         int32_t begin, end, tiles;

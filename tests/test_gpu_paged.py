@@ -1307,3 +1307,27 @@ def test_step_refuses_host_tensors(abi):
     with pytest.raises(ValueError, match="q: on cpu"):
         cache.attend(torch.zeros(3, cache.heads, D, dtype=torch.bfloat16), 3, 1, 64)
     assert abi.csa2_launch_count() == c0
+
+
+@pytest.mark.parametrize("n,kv", [(1, 3000), (4, 2000), (40, 4000)])  # few rows; tiles; with split keys
+@pytest.mark.parametrize("order", ["behind it", "before it", "empty ones"])
+def test_attention_of_good_requests_beside_token_bounds_out_of_order(abi, n, kv, order):
+    """A request whose tokens run past the call's, or backwards, is recorded and skipped; the one beside it is whole."""
+    rng = np.random.default_rng(71)
+    if order == "before it":    # tokens n .. 2n - 1 are the last request's
+        s = attn_inputs(rng, [30, 40, kv], [n, 0, n], 64, 16, "fp4")
+        starts, mine = [0, 1000 + n, n, 2 * n], [n, n, n, 2 * n]
+    elif order == "behind it":  # tokens 0 .. n - 1 are the first one's
+        s = attn_inputs(rng, [kv, 50, 60, 0], [n, 0, 0, 0], 64, 16, "fp4")
+        starts, mine = [0, n, -1, 0, 0], [0, n, n, n, n]
+    else:
+        s = attn_inputs(rng, [20, kv, 60, 70, 80, 90], [0, n, 0, 0, 0, 0], 64, 16, "fp4")
+        starts, mine = [0, 0, n, -5, -5, -2, 0], [0, 0, n, n, n, n, n]
+    a = Attn(abi, dict(s, q_start=np.array(starts, np.int32)), max_q=n)
+    a.call()
+    out, lse = a.result()
+    first = mine[0]
+    assert (out[:first] == 7).all() and (lse[:first] == 7).all()
+    out[:first], lse[:first] = 0, -np.inf
+    check_attn(out, lse, dict(s, q_start=np.array(mine, np.int32)), 0)
+    assert abi.csa2_status_fetch(a.ws)[:2] == [abi.ERR_DEVICE_BOUNDS, 9]
