@@ -122,6 +122,8 @@ class PagedLatents:
         self._tokens(n_tokens)
         _rows("latents", latents, n_tokens, (LATENT,), self.dev)
         s = _stream(self.dev, stream)
+        if n_tokens == 0:
+            return
         fp4 = self.fmt == abi.FMT_FP4
         abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if fp4 else None, self.rope,
                                  self.max_pos if fp4 else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
@@ -155,6 +157,8 @@ class PagedLatents:
         _rows("q", q, n_tokens, (self.heads, LATENT), self.dev)
         s = _stream(self.dev, stream)
         ws = self.workspace(n_tokens, max_q, max_kv, s)
+        if n_tokens == 0:
+            return self.out[:0], self.lse[:0]
         abi.csa2_paged_attn(q, n_tokens, self.heads, self.q_start, self.kv_len, self.n_req, max_q, max_kv, self.fmt, self.codes,
                             self.scales, self.n_rows, self.table, self.max_pages, self.page_size, self.window, self.sm_scale,
                             self.out, self.lse, ws, ws.numel(), s)
@@ -212,10 +216,11 @@ class PagedLayer:
         _rows("hidden", hidden, n, (self.hidden,), c.dev)
         s = _stream(c.dev, stream)
         c.workspace(n, max_q, max_kv, s)  # what refuses the step refuses it before the residual, pages and lengths change
-        abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
-                             self.x, self.x_scales, None, s)
-        self._project(self.wq, n, c.heads * LATENT, self.q, s)
-        self._project(self.wlatent, n, LATENT, self.latents, s)
+        if n > 0:
+            abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
+                                 self.x, self.x_scales, None, s)
+            self._project(self.wq, n, c.heads * LATENT, self.q, s)
+            self._project(self.wlatent, n, LATENT, self.latents, s)
         c.plan(s)
         c.append(self.latents, n, s)
         return c.attend(self.q, n, max_q, max_kv, s)

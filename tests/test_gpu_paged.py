@@ -1331,3 +1331,28 @@ def test_attention_of_good_requests_beside_token_bounds_out_of_order(abi, n, kv,
     out[:first], lse[:first] = 0, -np.inf
     check_attn(out, lse, dict(s, q_start=np.array(mine, np.int32)), 0)
     assert abi.csa2_status_fetch(a.ws)[:2] == [abi.ERR_DEVICE_BOUNDS, 9]
+
+
+def test_step_of_no_tokens(abi):
+    """An idle step, with an empty tensor: nothing but the plan's outputs changes, and the next step goes on."""
+    runs = []
+    for idle in (False, True):
+        paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+        x = torch.randn(56, layer.hidden, generator=g).to(torch.bfloat16).cuda()
+        cache.added.copy_(torch.tensor([30, 9, 17], dtype=torch.int32))
+        layer.step(x, 56, 30, 64)
+        cache.advance()
+        if idle:
+            cache.added.zero_()
+            out, lse = layer.step(x[:0], 0, 0, 64)
+            assert out.shape == (0, cache.heads, D) and lse.shape == (0, cache.heads)
+            cache.append(layer.latents[:0], 0)
+            cache.advance()
+            assert cache.kv_len.tolist() == cache.cached.tolist() == [30, 9, 17] and not cache.q_start.any()
+        cache.added.fill_(1)
+        layer.step(x[:3], 3, 1, 64)
+        torch.cuda.synchronize()
+        assert all(st[0] == abi.OK for st in cache.status().values())
+        runs.append([t.clone() for t in (cache.out, cache.lse, cache.codes, cache.table, cache.n_free, layer.residual)])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
