@@ -9,7 +9,17 @@ This module only allocates device memory (torch) and issues C-ABI calls in
 that order; all arithmetic runs in libcsa2.so.  A step issues the same calls
 with the same pointers every time, so it can be captured in a CUDA graph: the
 lengths stay on the device, and the host's bounds max_q and max_kv size the
-launches.  A captured step keeps its workspace when a later one needs a larger;
+launches.
+
+Positions: FP4 latents are rotated by RoPE as they are appended (channel pairs
+(2i, 2i+1) by pos * theta^(-2i/512)), unless the cache is made with rope_theta
+None; E4M3 latents are stored as they are.  Nothing here rotates queries: over
+a cache that rotates, attend() takes queries that the caller has rotated by
+their positions (cache.pos), and step() a function that does so; the logits
+then depend on distances alone.  Without it they depend on where the keys lie.
+Keys are also the values, so outputs are sums of latents as they are stored.
+
+A captured step keeps its workspace when a later one needs a larger;
 the first step with larger bounds runs outside a capture.
 
 Calls go to the given stream, or the current one; the device has to be the
@@ -19,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 
 import torch
 
@@ -61,7 +72,8 @@ def fp4_weight(w):
 
 
 class PagedLatents:
-    """Pages, block tables and latents of a batch of requests, and the calls over them."""
+    """Pages, block tables and latents of a batch of requests, and the calls over them.  rope_theta None: FP4 latents are
+    stored without rotation, as E4M3 ones always are."""
 
     def __init__(self, n_req, max_tokens, n_pages, page_size, max_pages, heads=abi.ATTN_HEADS, fmt=abi.FMT_FP4, window=0,
                  sm_scale=1.0 / math.sqrt(float(LATENT)), rope_theta=10000.0, device="cuda"):
@@ -95,7 +107,7 @@ class PagedLatents:
         self.pos = torch.zeros(max_tokens, dtype=i64, device=d)
         self.max_pos = max_pages * page_size
         self.rope = None
-        if fp4:
+        if fp4 and rope_theta is not None:
             self.rope = torch.empty(abi.csa2_rope_table_bytes(LATENT, self.max_pos), dtype=u8, device=d)
             abi.csa2_rope_table_init(rope_theta, LATENT, self.max_pos, self.rope, _stream(d, None))
         self.out = torch.zeros((max_tokens, heads, LATENT), dtype=torch.bfloat16, device=d)
@@ -124,9 +136,9 @@ class PagedLatents:
         s = _stream(self.dev, stream)
         if n_tokens == 0:
             return
-        fp4 = self.fmt == abi.FMT_FP4
-        abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if fp4 else None, self.rope,
-                                 self.max_pos if fp4 else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
+        turn = self.rope is not None
+        abi.csa2_quantize_append(latents, n_tokens, LATENT, self.fmt, abi.LAYOUT_ROWS, self.pos if turn else None, self.rope,
+                                 self.max_pos if turn else 0, self.slots, self.n_rows, self.codes, self.scales, self.ws_app,
                                  self.ws_app.numel(), s)
 
     def workspace(self, n_tokens, max_q, max_kv, stream=None):
@@ -181,7 +193,8 @@ class PagedLatents:
 
 
 class PagedLayer:
-    """The front of an attention layer: norm, FP4 projections and the attention over a PagedLatents cache."""
+    """The front of an attention layer: norm, FP4 projections and the attention over a PagedLatents cache.  Without a
+    rotary embedding where the cache does not rotate; where it does, see step()'s `rotate`."""
 
     def __init__(self, cache, hidden, norm_weight, wq, wlatent, eps=1e-6):
         """norm_weight bf16 [hidden]; wq, wlatent: bf16 weights [heads * 512][hidden], [512][hidden]."""
@@ -202,19 +215,28 @@ class PagedLayer:
         self.q = torch.zeros((T, H, LATENT), dtype=torch.bfloat16, device=d)
         self.latents = torch.zeros((T, LATENT), dtype=torch.bfloat16, device=d)
         self.ws = torch.zeros(max(sizes), dtype=torch.uint8, device=d)
+        self._told = False  # of queries that are not rotated
 
     def _project(self, w, n, n_out, out, s):
         abi.csa2_fp4_matvec(self.x, abi.X_E4M3, self.x_scales, self.hidden, n, self.hidden, w[0], w[1], n_out, 1.0, out,
                             abi.OUT_BF16, self.ws, self.ws.numel(), s)
 
-    def step(self, hidden, n_tokens, max_q, max_kv, stream=None):
+    def step(self, hidden, n_tokens, max_q, max_kv, stream=None, rotate=None):
         """One step of n_tokens new tokens' bf16 hidden states (added to self.residual, the layer's residual stream):
         (out, lse) of the attention.  n_tokens above the planned ones (a padded batch) leaves the rows behind them of
-        out and lse as they are; see PagedLatents.append."""
+        out and lse as they are; see PagedLatents.append.
+
+        rotate(q, pos): called once the plan is made, with the step's stream current, to turn the queries
+        q [n_tokens][heads][512] in place by their positions pos (-1 behind the planned tokens), as the cache turns the
+        latents; it may run inside a capture."""
         c, n = self.cache, n_tokens
         c._tokens(n)
         _rows("hidden", hidden, n, (self.hidden,), c.dev)
         s = _stream(c.dev, stream)
+        if rotate is None and c.rope is not None and not self._told:
+            warnings.warn("the cache rotates its latents and the step's queries are not rotated: logits depend on where the "
+                          "keys lie (rotate=, or a cache with rope_theta=None)")
+            self._told = True
         c.workspace(n, max_q, max_kv, s)  # what refuses the step refuses it before the residual, pages and lengths change
         if n > 0:
             abi.csa2_rmsnorm_fp8(hidden, self.hidden, self.residual, self.residual, self.norm_weight, n, self.hidden, self.eps, 0,
@@ -222,5 +244,8 @@ class PagedLayer:
             self._project(self.wq, n, c.heads * LATENT, self.q, s)
             self._project(self.wlatent, n, LATENT, self.latents, s)
         c.plan(s)
+        if rotate is not None and n > 0:
+            with torch.cuda.stream(s):
+                rotate(self.q[:n], c.pos[:n])
         c.append(self.latents, n, s)
         return c.attend(self.q, n, max_q, max_kv, s)

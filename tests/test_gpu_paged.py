@@ -1356,3 +1356,78 @@ def test_step_of_no_tokens(abi):
         runs.append([t.clone() for t in (cache.out, cache.lse, cache.codes, cache.table, cache.n_free, layer.residual)])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def turned(q, pos, theta=10000.0):
+    """Queries [n][heads][512] turned in place by their positions, pairs (2i, 2i+1), in 64 bits, rounded once."""
+    ang = pos[:, None, None].double() * theta ** (-torch.arange(D // 2, device=q.device).double() * 2 / D)
+    e, o = q[..., 0::2].double(), q[..., 1::2].double()
+    q.copy_(torch.stack((e * ang.cos() - o * ang.sin(), e * ang.sin() + o * ang.cos()), -1).flatten(-2))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_step_with_rotated_queries(abi, captured):
+    """Queries are turned by the plan's positions between the products and the attention: a chunk, then single tokens."""
+    paged, g, cache, layer = layer_case(abi, abi.FMT_FP4, 0)
+    tok = torch.zeros(56, layer.hidden, dtype=torch.bfloat16, device="cuda")
+    for added in ([30, 9, 17], [1, 1, 1]):
+        n, graph = sum(added), torch.cuda.CUDAGraph()
+        cache.added.copy_(torch.tensor(added, dtype=torch.int32))
+        tok[:n] = torch.randn(n, layer.hidden, generator=g).to(torch.bfloat16)
+        layer.residual.zero_()
+        if captured:
+            cache.workspace(n, 30, 64)
+            with torch.cuda.graph(graph):
+                layer.step(tok[:n], n, 30, 64, rotate=turned)
+            graph.replay()
+        else:
+            layer.step(tok[:n], n, 30, 64, rotate=turned)
+        torch.cuda.synchronize()
+        assert all(st[0] == abi.OK for st in cache.status().values()) and cache.pos[:n].min() >= 0
+        xs, w = layer.x_scales[:n].cpu().numpy(), [t.cpu().numpy() for t in layer.wq]
+        raw, reach = PO.matvec(layer.x[:n].view(torch.float8_e4m3fn).double().cpu().numpy(), xs, *w, 1.0)
+        turn = lambda v: O.rope(v.reshape(-1, D), np.repeat(cache.pos[:n].cpu().numpy(), cache.heads)).reshape(n, -1)  # noqa: E731
+        # the product's fp32 sum and its rounding to bf16 (2^-8 relative), times at most sqrt(2) for a turned pair, and one more
+        pair = np.repeat(np.hypot(raw[:, 0::2], raw[:, 1::2]), 2, axis=1)
+        tol = 1.5 * (2.0 ** -8 * pair + 64 * 2.0 ** -24 * np.repeat(np.maximum(reach[:, 0::2], reach[:, 1::2]), 2, axis=1)) + 2.0 ** -8 * pair
+        q = layer.q[:n].double().cpu().numpy().reshape(n, -1)
+        assert (np.abs(q - turn(raw)) <= tol).all() and (np.abs(q - raw) > tol).any()
+        s = dict(q=layer.q[:n].cpu(), q_start=cache.q_start.cpu().numpy(), kv_len=cache.kv_len.cpu().numpy(),
+                 codes=cache.codes.cpu().numpy(), scales=cache.scales.cpu().numpy(), table=cache.table.cpu().numpy(), page=cache.page_size,
+                 fmt="fp4", T=n, H=cache.heads, max_q=30, max_kv=64)
+        check_attn(cache.out[:n].double().cpu().numpy(), cache.lse[:n].double().cpu().numpy(), s, 0)
+        cache.advance()
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_step_without_a_rotary_embedding_goes_by_distances(abi, fmt):
+    """A cache that does not rotate: the same tokens behind 48 others, outside the window of all but the first ones, have
+    the same latents and (up to the order of fp32 sums, bounded as in check_attn) the same outputs."""
+    from csa2_sparse_attention_gb300 import paged
+    R, hidden, window = 1, 256, 16
+    g = torch.Generator().manual_seed(5)
+    w = lambda *sh: torch.randn(*sh, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    weights = (w(hidden), w(4 * D, hidden), w(D, hidden))
+    before, x = w(48, hidden), w(40, hidden)
+    runs = []
+    for shift in (False, True):
+        cache = paged.PagedLatents(R, 64, 8, 16, 8, heads=4, fmt=abi.FMT_FP4 if fmt == "fp4" else abi.FMT_FP8, window=window, rope_theta=None)
+        layer = paged.PagedLayer(cache, hidden, *weights)
+        for rows in ([before, x] if shift else [x]):
+            cache.added.fill_(len(rows))
+            layer.residual.zero_()
+            layer.step(rows, len(rows), 64, 128)
+            cache.advance()
+        torch.cuda.synchronize()
+        assert all(st[0] == abi.OK for st in cache.status().values())
+        slots = cache.slots[:40].cpu().numpy()
+        codes, scales = cache.codes.cpu().numpy(), None if fmt == "fp8" else cache.scales.cpu().numpy()
+        s = dict(q=layer.q[:40].cpu(), q_start=cache.q_start.cpu().numpy(), kv_len=cache.kv_len.cpu().numpy(), codes=codes, scales=scales,
+                 table=cache.table.cpu().numpy(), page=16, fmt=fmt, T=40, H=4, max_q=40, max_kv=int(cache.kv_len[0]))
+        check_attn(cache.out[:40].double().cpu().numpy(), cache.lse[:40].double().cpu().numpy(), s, window)
+        want, wlse, _ = PO.paged_attention(s["q"].float().numpy(), s["q_start"], s["kv_len"], codes, scales, s["table"], 16, window, SM)
+        runs.append((codes[slots], None if scales is None else scales[slots], want[window:], wlse[window:], layer.q[:40].cpu()))
+    a, b = runs
+    assert torch.equal(a[4], b[4]) and np.array_equal(a[0], b[0]) and (a[1] is None or np.array_equal(a[1], b[1]))
+    np.testing.assert_allclose(a[2], b[2], rtol=0, atol=1e-12 * np.abs(a[2]).max())
+    np.testing.assert_allclose(a[3], b[3], rtol=1e-12)

@@ -209,3 +209,22 @@ def test_layer_that_no_step_can_use(abi, kw):
     w = lambda *shape: torch.zeros(1, dtype=torch.bfloat16).expand(*shape)  # noqa: E731
     with pytest.raises(ValueError, match="channels for steps"):
         paged.PagedLayer(c, use["hidden"], w(use["hidden"]), w(512, use["hidden"]), w(512, use["hidden"]), use["eps"])
+
+
+def test_a_cache_without_rotation(abi):
+    """rope_theta None has no table, and what is appended is given no positions."""
+    from csa2_sparse_attention_gb300 import paged
+    c = paged.PagedLatents(2, 8, 4, 16, 2, heads=4, fmt=abi.FMT_FP4, rope_theta=None, device="cpu")
+    assert c.rope is None and c.scales is not None
+
+
+def test_turned_queries_go_by_distances():
+    """The rotation of queries and keys alike leaves logits that a shift of all positions does not change."""
+    from oracle import csa2_oracle as O
+    rng = np.random.default_rng(0)
+    q, k = rng.standard_normal((5, 512)), rng.standard_normal((9, 512))
+    at = lambda t, p, shift: O.rope(q, t + shift) @ O.rope(k, p + shift).T  # noqa: E731
+    t, p = np.arange(4, 9), np.arange(9)
+    # angles up to 2^17 in 64 bits: off by 2^-35, of 512 products of size 10 at most
+    np.testing.assert_allclose(at(t, p, 0), at(t, p, 100000), rtol=0, atol=512 * 10 * 2.0 ** -35)
+    assert np.abs(q @ O.rope(k, p).T - q @ O.rope(k, p + 1).T).max() > 1  # (with keys alone turned it does)
