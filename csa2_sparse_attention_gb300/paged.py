@@ -46,6 +46,12 @@ def _stream(dev, stream):
     return torch.cuda.current_stream(dev) if stream is None else stream
 
 
+def _made(dev):
+    """What the current stream has filled is there for calls on any other one."""
+    if dev.type == "cuda":
+        torch.cuda.current_stream(dev).synchronize()
+
+
 def _rows(name, x, n, shape, dev, dtype=torch.bfloat16):
     """x has at least n contiguous rows of this shape on the device."""
     if x.device != dev:
@@ -116,6 +122,7 @@ class PagedLatents:
         self.ws_app = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
         self.ws_attn = None
         self._captured, self._kept = False, []  # the workspace is in a graph; earlier ones that are
+        _made(d)
 
     def _tokens(self, n):
         if not 0 <= n <= self.max_tokens:
@@ -216,6 +223,7 @@ class PagedLayer:
         self.latents = torch.zeros((T, LATENT), dtype=torch.bfloat16, device=d)
         self.ws = torch.zeros(max(sizes), dtype=torch.uint8, device=d)
         self._told = False  # of queries that are not rotated
+        _made(d)
 
     def _project(self, w, n, n_out, out, s):
         abi.csa2_fp4_matvec(self.x, abi.X_E4M3, self.x_scales, self.hidden, n, self.hidden, w[0], w[1], n_out, 1.0, out,

@@ -1431,3 +1431,27 @@ def test_step_without_a_rotary_embedding_goes_by_distances(abi, fmt):
     assert torch.equal(a[4], b[4]) and np.array_equal(a[0], b[0]) and (a[1] is None or np.array_equal(a[1], b[1]))
     np.testing.assert_allclose(a[2], b[2], rtol=0, atol=1e-12 * np.abs(a[2]).max())
     np.testing.assert_allclose(a[3], b[3], rtol=1e-12)
+
+
+def test_step_on_another_stream_than_the_cache_was_made_on(abi):
+    """The stream that fills a new cache and its weights is held up: a step on another one finds them filled."""
+    from csa2_sparse_attention_gb300 import paged
+    g = torch.Generator().manual_seed(2)
+    w = lambda *sh: torch.randn(*sh, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    weights, x, added = (w(256), w(4 * D, 256), w(D, 256)), w(56, 256), torch.tensor([30, 9, 17], dtype=torch.int32).cuda()
+    runs = []
+    for apart in (False, True):
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream() if apart else torch.cuda.current_stream()
+        if apart:
+            torch.cuda._sleep(200_000_000)
+        cache = paged.PagedLatents(3, 64, 40, 16, 12, heads=4, fmt=abi.FMT_FP4)
+        layer = paged.PagedLayer(cache, 256, *weights)
+        with torch.cuda.stream(st):
+            cache.added.copy_(added)
+            layer.step(x, 56, 30, 30, st)
+        torch.cuda.synchronize()
+        assert all(s[0] == abi.OK for s in cache.status().values())
+        runs.append([t.clone() for t in (cache.out, cache.lse, cache.codes, cache.table, cache.n_free, layer.residual)])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
