@@ -9,8 +9,12 @@
 // reductions.  Rows of more than 1024 channels take a block, two chunks per
 // thread, that walks over the rows and loads the next one before it reduces
 // this one: the two block barriers of a row then cost no memory time.  4096 rows
-// of 7168 with a residual, scales per 128: 57.8 us without that, 37.3 us with it
-// (5.5 TB/s, 82 % of the copy rate).
+// of 7168 with a residual, scales per 128: 57.8 us without that, 37.8 us with it
+// (5.5 TB/s, 81 % of the copy rate).
+//
+// Codes are those of the exact quotient y / s (the root cancels in it): y times
+// a rounded reciprocal of s, 37.3 us, put a code in ten thousand on the wrong
+// side of a border, since products of bf16 numbers lie on borders that often.
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 
@@ -26,6 +30,29 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_near(float x) {  // off by 2^-23
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two floats in one register pair, and their products: half of the issue slots.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 
@@ -104,18 +131,25 @@ __global__ void __launch_bounds__(WPR > 1 ? 32 * WPR : 256, WPR > 1 ? 1024 / (32
         if (WPR > 1) fetch(row + step);
         ss = over_row(ss, false, 0);
         const float rs = 1.0f / sqrtf(ss / float(dim) + eps);
-        float y[NCH][8], am = 0.f, cm[NCH];
+        // rs = p2 f with a power of two p2: a = h p2 w is exact (16 bits), y = a f
+        const uint32_t rb = __float_as_uint(rs);
+        const bool plain = (rb >> 23) - 1u < 254u;
+        const float p2 = plain ? __uint_as_float(rb & 0x7F800000u) : 1.0f;
+        const float f = plain ? __uint_as_float((rb & 0x007FFFFFu) | 0x3F800000u) : rs;
+        const uint64_t pp = pair(p2, p2);
+        uint64_t y[NCH][4];  // a
+        float am = 0.f, cm[NCH];  // maxima of |a|
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             const uint32_t a[4] = {h[j].x, h[j].y, h[j].z, h[j].w}, w[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
             cm[j] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                y[j][2 * e] = bf16_lo(a[e]) * rs * bf16_lo(w[e]);
-                y[j][2 * e + 1] = bf16_hi(a[e]) * rs * bf16_hi(w[e]);
-                cm[j] = max_nan(cm[j], max_nan(fabsf(y[j][2 * e]), fabsf(y[j][2 * e + 1])));
+                y[j][e] = mul_pair(mul_pair(pair(bf16_lo(a[e]), bf16_hi(a[e])), pp), pair(bf16_lo(w[e]), bf16_hi(w[e])));
+                float lo, hi;
+                unpair(y[j][e], lo, hi);
+                cm[j] = max_nan(cm[j], max_nan(fabsf(lo), fabsf(hi)));
             }
-            if (t + T * j >= chunks) cm[j] = 0.f;  // (a chunk behind the row is 0 * rs, and rs may be infinite)
             if (GROUPS) {  // 16 chunks = 128 channels: half a warp
 #pragma unroll
                 for (int o = 8; o; o >>= 1) cm[j] = max_nan(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], o));
@@ -128,23 +162,40 @@ __global__ void __launch_bounds__(WPR > 1 ? 32 * WPR : 256, WPR > 1 ? 1024 / (32
         for (int j = 0; j < NCH; ++j) {
             const int c = t + T * j;
             if (!live || c >= chunks) continue;
-            const float s = (GROUPS ? cm[j] : am) * (1.0f / 448.0f);
-            const float inv = __frcp_rn(s);
+            // y / s = 448 a / max|a|, a quotient of numbers of 19 and 16 bits: it lies on a border of two codes, or 2^-21 of
+            // it away or more.  Times a reciprocal of twice the bits it is off by 2^-24 and exact where it has few bits
+            // itself, so the codes are those of the exact quotient.
+            const float top = GROUPS ? cm[j] : am, inv0 = rcp_near(top), inv = 448.0f * inv0;
+            const float inv2 = fmaf(-top, inv, 448.0f) * inv0, s = top * (f * (1.0f / 448.0f));
             float v[8];
+            const uint64_t i1 = pair(inv, inv), i2 = pair(inv2, inv2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = y[j][e] * inv;
-            if (!(inv <= FLT_MAX)) {  // the reciprocal of the smallest scales overflows; 0 / 0 is 0
+            for (int e = 0; e < 4; ++e) unpair(fma_pair(y[j][e], i1, mul_pair(y[j][e], i2)), v[2 * e], v[2 * e + 1]);
+            if (!(plain && top >= 0x1p-90f && top <= 0x1p90f)) {  // infinities, NaN, zeros (0 / 0 is 0), the ends of the range
+                const uint64_t ff = pair(f, f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = s == 0.f ? 0.f : __fdiv_rn(y[j][e], s);
+                for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    unpair(mul_pair(y[j][e], ff), lo, hi);
+                    v[2 * e] = s == 0.f ? 0.f : __fdiv_rn(lo, s);
+                    v[2 * e + 1] = s == 0.f ? 0.f : __fdiv_rn(hi, s);
+                }
             }
             uint2 o;
             o.x = e4m3x2_rn_sat(v[0], v[1]) | (e4m3x2_rn_sat(v[2], v[3]) << 16);
             o.y = e4m3x2_rn_sat(v[4], v[5]) | (e4m3x2_rn_sat(v[6], v[7]) << 16);
             codes[row * chunks + c] = o;
-            if (y_bf16 != nullptr)
-                y_bf16[row * chunks + c] =
-                    make_uint4(bf16x2_rn(y[j][0], y[j][1]), bf16x2_rn(y[j][2], y[j][3]), bf16x2_rn(y[j][4], y[j][5]),
-                               bf16x2_rn(y[j][6], y[j][7]));
+            if (y_bf16 != nullptr) {
+                const uint64_t ff = pair(f, f);
+                uint32_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    unpair(mul_pair(y[j][e], ff), lo, hi);
+                    b[e] = bf16x2_rn(lo, hi);
+                }
+                y_bf16[row * chunks + c] = make_uint4(b[0], b[1], b[2], b[3]);
+            }
             if (GROUPS) {
                 if ((c & 15) == 0) scales[row * (chunks / 16) + c / 16] = s;
             } else if (c == 0) {

@@ -407,7 +407,7 @@ csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, c
  *   h = bf16(x + residual)  (h = x without a residual)
  *   y = h / sqrt(mean(h^2) + eps) * weight            (fp32)
  *   s = max|y| / 448 over the row (group 0) or each 128 channels (group 128)
- *   codes = nearest-even E4M3 of y / s (0 where s is 0)
+ *   codes = nearest-even E4M3 of y / s (0 where s is 0), both unrounded
  *   x            [n] rows of dim bf16, x_stride elements apart (>= dim, a
  *                multiple of 8).
  *   residual     [n][dim] bf16 or NULL; residual_out [n][dim] takes h (may be
@@ -416,8 +416,9 @@ csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, c
  *                multiple of 128).  eps >= 0, finite.
  *   codes        [n][dim] E4M3; scales [n] or [n][dim/128] fp32.
  *   y_bf16       [n][dim] bf16 of y, or NULL.
- * The mean is an fp32 sum: |h| up to 2^56.  A NaN or infinite h makes the
- * codes and the scale of the row's groups what the formula gives (NaN).
+ * The mean is an fp32 sum: |h| up to 2^56 (where eps is 0, rows of 2^-60 and
+ * more).  A NaN or infinite h makes the codes and the scale of the row's
+ * groups what the formula gives (NaN).
  */
 csa2_status csa2_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual, void* residual_out,
                              const void* weight, int64_t n, int dim, float eps, int group, uint8_t* codes,

@@ -1455,3 +1455,23 @@ def test_step_on_another_stream_than_the_cache_was_made_on(abi):
         runs.append([t.clone() for t in (cache.out, cache.lse, cache.codes, cache.table, cache.n_free, layer.residual)])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,dim,group", [(40, 16, 0), (30, 512, 0), (20, 1024, 128), (9, 1032, 0), (16, 5120, 0), (12, 7168, 128),
+                                         (3, 16384, 0)])
+@pytest.mark.parametrize("values", ["random", "whole numbers"])
+def test_norm_codes_are_those_of_the_exact_quotient(abi, n, dim, group, values):
+    """y / s = 448 h w / max|h w| whatever the root is: products of 16 bits, whose quotients lie on a border of two codes
+    (then 64 bits have them exactly) or at least 2^-21 of it away.  So the codes can be compared for equality; whole
+    numbers lie on borders often."""
+    rng = np.random.default_rng(dim)
+    if values == "random":
+        x, w = bf16(np.exp(3 * rng.standard_normal((n, 1))) * rng.standard_normal((n, dim))), bf16(1 + 0.2 * rng.standard_normal(dim))
+    else:
+        x, w = bf16(rng.integers(-112, 113, (n, dim)) * 2.0 ** rng.integers(-20, 20, (n, 1))), bf16(2.0 ** rng.integers(-1, 2, dim))
+    _, codes, scales, y = norm_call(abi, x, None, w, group)
+    h, wd = x.double().numpy(), w.double().numpy()
+    check_norm(h, wd, group, codes, scales, y)
+    a = (h * wd).reshape(n, -1, group or dim)
+    want = O.e4m3_decode(O.e4m3_encode(448.0 * a / np.abs(a).max(axis=2, keepdims=True))).reshape(n, dim)
+    assert np.array_equal(codes, want)
