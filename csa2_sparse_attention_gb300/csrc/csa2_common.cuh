@@ -137,6 +137,17 @@ __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
 // grid_dep_launch() then lets the next kernel start its own launch.  A kernel
 // allocates TMEM only after grid_dep_wait(), so it never waits on columns
 // held by its predecessor.
+//
+// Two kernels of the paged attention start earlier: paged_tiles_kernel, always
+// launched directly behind paged_decode_kernel, and paged_rows_kernel behind
+// both.  Every CTA of the decode kernel lets its dependents start only after its
+// own wait, so when a CTA of either runs, all work before the call is done and
+// visible: they read the call's inputs and write the status word, the split count
+// and (the second one) outputs that none of the three kernels reads.  What the
+// decode kernel writes is read after grid_dep_wait(), and every CTA waits before
+// it ends, so that whatever comes behind them finds all of it.  Their shared
+// memory keeps two of these kernels' CTAs, and so their TMEM, off one
+// multiprocessor; a foreign kernel's columns come free without their help.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

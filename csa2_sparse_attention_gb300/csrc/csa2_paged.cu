@@ -107,23 +107,28 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // go in items of 64 rows (csa2_paged_rows.cu), longer ones in pairs of 128
 // rows over decoded tiles (csa2_paged_tiles.cu) where those need no more than
 // 4 GB.  Decoding a key once pays from a few items on: 1024 tokens x 64 heads
-// over 16K entries take 1.81 ms from tiles and 2.70 ms in items of 64 rows.  The
-// border, 64 heads over 8K entries: 16 requests of 4 tokens (4 items each) 124 us
-// from tiles and 122 us without, of 8 tokens 181 and 209 us; single tokens would
-// write and read 1 KB per key for nothing (115 and 45 us).  Nor does it pay where
-// an item sees four tiles or fewer (1024 tokens with a window of 128, 64 heads:
-// 128 us from tiles, 118 without; 4 x 512 with 512, 6 tiles: 334 and 350).  Tiles run
+// over 16K entries take 1.79 ms from tiles and 2.69 ms in items of 64 rows.  The
+// border, 64 heads over 8K entries: 16 requests of 4 tokens (4 items each) 135 us
+// from tiles and 125 us without, of 8 tokens 191 and 209 us; single tokens would
+// write and read 1 KB per key for nothing (125 and 43 us).  About where an item
+// sees four tiles it stops paying as well (64 heads, 1024 tokens with a window of
+// 128, 3 tiles: 115 us from tiles, 120 without; 100 tokens + 31 single ones over
+// 500, 5 tiles: 32 and 26; 4 x 512 with 512, 6 tiles: 310 and 354).  Tiles run
 // requests of any length; beside them the few-row kernel takes the short ones
 // where the call's tokens say that there are enough of those, by a sixth of the
 // longest request per request, or three quarters from 16 key tiles on.  64 heads,
 // us with both kernels and with tiles alone:
-//   512 tokens + 63 single ones, 8K   730   986     + 15 single ones   643  621
-//   256 tokens + 31 single ones, 32K 1320  1862
-//   100 tokens + 31 single ones, 500   32    48     16 x 100, 1K       360  354
-//   8 x 64 + 24 single ones, 1K       147   141     8 x 64 + 8, 1K     150  133
-// 16 heads, 8 x 64 + 8 single ones: 4K 128 and 171, 2K 84 and 98, 1K 63 and 63.
+//   512 tokens + 63 single ones, 8K   727   865     + 15 single ones   630  638
+//   256 tokens + 31 single ones, 32K 1345  2008
+//   100 tokens + 31 single ones, 500   32    39     16 x 100, 1K       340  324
+//   8 x 64 + 24 single ones, 1K       158   130     8 x 64 + 8, 1K     142  123
+//   8 x 64 + 24 single ones, 8K       658   687     8 x 64 + 8, 8K     647  646
+// 16 heads, 8 x 64 + 24 single ones: 8K 238 and 375, 2K 84 and 112.  With few
+// single tokens over less than 8K the tiles alone would be the faster (8 x 64 + 8,
+// 16 heads: 8K 258 and 238, 4K 120 and 102, 2K 78 and 56): a row tile behind a
+// request's rows leaves at once.  The border stands where it was when it did not.
 // One request's last wave is filled by splitting its last items (paged_tail): 512
-// tokens x 64 heads over 8K, 128 items in 3.4 waves, 567 us without and 521 with.
+// tokens x 64 heads over 8K, 128 items in 3.4 waves, 567 us without and 523 with.
 // The split count of each is the one with the least time by: waves of 152 CTAs,
 // each a start and end of 8 us and a time per key tile, plus the merge's pass
 // over the partial outputs.  That is for requests as long as max_kv; with up to

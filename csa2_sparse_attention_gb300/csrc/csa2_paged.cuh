@@ -23,7 +23,7 @@ constexpr int kPFlagBytes = 32;
 // kPGrow above it: P reaches 2^15 at most and the largest one 2^7 at least, so
 // that what f16 rounds below its normal range (2^-25 each) is 2^-32 of the sum.
 // (With b at the maximum it was 2^-25: half a million keys of probability just
-// under that, 1.5 % of the output together, all rounded to zero.)
+// under that, 1.3 % of the output together, all rounded to zero.)
 constexpr float kPBase = 7.f, kPGrow = 15.f;
 
 // n / d for 0 <= n < 2^31 by a multiplication: with mul = floor(2^(31 + s) / d) + 1

@@ -12,7 +12,7 @@
 // this file) to tiles of 128 keys in f16, exact, laid out as shared memory holds
 // them.  With the decoding inside the attention kernel every pair of CTAs did
 // it again, 12,600 warp instructions a key tile, and 1024 tokens x 64 heads over
-// 16K entries took 2.7 ms (csa2_paged_rows.cu still does) instead of 1.85.
+// 16K entries took 2.7 ms (csa2_paged_rows.cu still does) instead of 1.84.
 //
 // The fp32 accumulator of 128 rows x 512 channels would fill TMEM (512
 // columns) and leave no room for the logits, so a CTA takes 128 rows and one
@@ -27,7 +27,7 @@
 //
 // Keys go in tiles of 128: an M = 128 MMA of K = 16 takes 64 clocks for any
 // N up to 128 (measured 64-69) and 128 for N = 256, so S wants 128 keys and O
-// 256 channels at once.  Every CTA copies its own 128 KB per tile, 9.1 TB/s from L2
+// 256 channels at once.  Every CTA copies its own 128 KB per tile, 9.0 TB/s from L2
 // over the GPU for 1024 tokens over 16K, with plain bulk copies.  Three roles:
 //   copy warp  the other half's channels X of a tile first, then, as the logits'
 //       MMAs release them, the own half's Y into the same group.  One copy of Y
@@ -48,8 +48,8 @@
 // A tile takes about 4150 clocks, three quarters of them MMAs: a block that is released
 // is there again some 1500 clocks later, and S has one place in TMEM, so the next
 // logits wait for the softmax to have read it.  512 tokens x 64 heads over 8K
-// entries: 521 us, 1090 TFLOP/s without the third product; 1024 tokens over 16K:
-// 1.82 ms, 1170 TFLOP/s.
+// entries: 523 us, 1090 TFLOP/s without the third product; 1024 tokens over 16K:
+// 1.84 ms, 1160 TFLOP/s.
 //
 // Long axes with few rows are split over CTAs in chunks of key tiles that the
 // host sizes; the partial outputs are joined by paged_merge_kernel.

@@ -201,7 +201,11 @@ class PagedLatents:
 
 class PagedLayer:
     """The front of an attention layer: norm, FP4 projections and the attention over a PagedLatents cache.  Without a
-    rotary embedding where the cache does not rotate; where it does, see step()'s `rotate`."""
+    rotary embedding where the cache does not rotate; where it does, see step()'s `rotate`.
+
+    residual [max_tokens][hidden], the layer's residual stream, goes by the step's tokens: step() adds to its first n_tokens
+    rows, so before every step they are set to what the tokens bring from the layer before (zeros at the first one).  A
+    step that the plan refuses leaves out and lse as they were: status() tells."""
 
     def __init__(self, cache, hidden, norm_weight, wq, wlatent, eps=1e-6):
         """norm_weight bf16 [hidden]; wq, wlatent: bf16 weights [heads * 512][hidden], [512][hidden]."""

@@ -388,7 +388,8 @@ csa2_status csa2_page_plan(const int32_t* cached, const int32_t* added, int64_t 
  * outside [0, min(max_kv, max_pages * page_size)] is recorded and sees
  * nothing; one whose tokens lie outside [0, n_tokens) or exceed max_q is
  * recorded and skipped; a table entry outside [0, n_rows / page_size) is
- * recorded and its page is not seen.  Latents that no token sees may hold
+ * recorded and its page is not seen.  (Where n_tokens, n_req or max_q is 0
+ * nothing is launched, and nothing recorded.)  Latents that no token sees may hold
  * anything, NaN included.
  * The same call gives the same bits every time; the keys are split by the
  * lengths of all requests, so an output's last bits can depend on the others.
