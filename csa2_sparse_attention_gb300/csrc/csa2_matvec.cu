@@ -417,6 +417,10 @@ extern "C" csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_
     const MatvecPlan p = matvec_plan(n, k, n_out);
     if (!ws || !aligned16(ws) || ws_bytes < p.total) return CSA2_ERR_WORKSPACE;
     if (n == 0) return CSA2_OK;
+    const char *x0 = static_cast<const char*>(x), *o0 = static_cast<const char*>(out);
+    if (o0 < x0 + (size_t(n - 1) * x_stride + k) * (x_fmt == CSA2_X_BF16 ? 2 : 1) &&
+        x0 < o0 + size_t(n) * n_out * (out_dtype == CSA2_OUT_F32 ? 4 : 2))
+        return CSA2_ERR_INVALID_ARG;
     cudaStream_t s = cudaStream_t(stream);
     MatvecArgs a{};
     a.x = static_cast<const uint8_t*>(x);

@@ -275,6 +275,9 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
     if (!ws || !aligned16(ws) || ws_bytes < plan.total) return CSA2_ERR_WORKSPACE;
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
+    const size_t bytes = size_t(n_tokens) * n_heads * kPD * 2;  // of the queries and of the outputs
+    const char *q0 = static_cast<const char*>(q_bf16), *o0 = static_cast<const char*>(out);
+    if (o0 < q0 + bytes && q0 < o0 + bytes) return CSA2_ERR_INVALID_ARG;
     cudaStream_t s = cudaStream_t(stream);
     if (plan.tiles.grid > INT32_MAX || plan.few.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     PagedArgs a{};

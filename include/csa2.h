@@ -380,7 +380,7 @@ csa2_status csa2_page_plan(const int32_t* cached, const int32_t* added, int64_t 
  *            CSA2_FMT_FP8: codes are E4M3 rows [n_rows][512], scales NULL.
  *   table    [n_req][max_pages] int32; page_size a multiple of 8, 8..65536.
  *   out      [n_tokens][n_heads][512] bf16, rounded once from fp32 sums (the
- *            probabilities enter the product in f16).
+ *            probabilities enter the product in f16); apart from q_bf16.
  *   out_lse  [n_tokens][n_heads] fp32, natural log-sum-exp of the scaled
  *            logits, or NULL.
  * A token that sees nothing gets zeros and lse = -inf.  Tokens from
@@ -437,7 +437,8 @@ csa2_status csa2_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residu
  *                weights in CSA2_LAYOUT_ROWS, as n_out*k/128 rows of 128.
  *   k            a multiple of 128, up to 65536.  n rows: up to 65536; the
  *                weights are read once for each 16 rows.
- *   out          [n][n_out], bf16 (CSA2_OUT_BF16) or fp32 (CSA2_OUT_F32).
+ *   out          [n][n_out], bf16 (CSA2_OUT_BF16) or fp32 (CSA2_OUT_F32);
+ *                apart from x.  Sums and alpha times them are fp32.
  * ws: csa2_fp4_matvec_workspace_bytes(n, k, n_out) bytes (0 for bad sizes).
  */
 size_t csa2_fp4_matvec_workspace_bytes(int64_t n, int k, int64_t n_out);

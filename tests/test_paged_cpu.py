@@ -228,3 +228,20 @@ def test_turned_queries_go_by_distances():
     # angles up to 2^17 in 64 bits: off by 2^-35, of 512 products of size 10 at most
     np.testing.assert_allclose(at(t, p, 0), at(t, p, 100000), rtol=0, atol=512 * 10 * 2.0 ** -35)
     assert np.abs(q @ O.rope(k, p).T - q @ O.rope(k, p + 1).T).max() > 1  # (with keys alone turned it does)
+
+
+@pytest.mark.parametrize("out", [F, F + 16, F + 4 * 64 * 1024 - 16, F - 16, F - 4 * 64 * 1024 + 16])
+def test_attention_into_its_queries_is_refused(abi, out):
+    """Blocks read queries after others have written outputs."""
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_paged_attn(*args(ATTN, out=out)) == abi.ERR_INVALID_ARG
+    assert abi.csa2_launch_count() == c0
+
+
+@pytest.mark.parametrize("kw", [dict(out=F), dict(out=F + 2 * 256 * 2 - 16), dict(out=F + 2 * 300 * 2, x_stride=352),
+                                dict(out=F - 16), dict(out=F - 2 * 8 * 4 + 16, out_dtype=1),
+                                dict(out=F + 2 * 256 - 16, fmt=1, x_scales=4 * F)])
+def test_products_into_their_rows_are_refused(abi, kw):
+    c0 = abi.csa2_launch_count()
+    assert abi.lib.csa2_fp4_matvec(*args(MATVEC, **kw)) == abi.ERR_INVALID_ARG
+    assert abi.csa2_launch_count() == c0
