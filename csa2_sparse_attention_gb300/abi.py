@@ -25,6 +25,7 @@ OP_APPEND, OP_INDEX_FULL, OP_INDEX_REINDEX, OP_SPARSE_ATTN = range(4)
 OUT_BF16, OUT_F32 = 0, 1
 X_BF16, X_E4M3 = 0, 1
 INDEX_HEADS, INDEX_DIM, ATTN_HEADS, LATENT_DIM, BLOCK, STATUS_BYTES = 32, 128, 64, 512, 8, 256
+TREE_NODES, LOGPROBS_TOP = 1024, 64
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -58,6 +59,15 @@ EXPORTS = {
     "csa2_rmsnorm_fp8": (_int, [_p, _i64, _p, _p, _p, _i64, _int, ctypes.c_float, _int, _p, _p, _p, _p]),
     "csa2_fp4_matvec_workspace_bytes": (_sz, [_i64, _int, _i64]),
     "csa2_fp4_matvec": (_int, [_p, _int, _p, _i64, _i64, _int, _p, _p, _i64, ctypes.c_float, _p, _int, _p, _sz, _p]),
+    "csa2_head_norm_rope": (_int, [_p, _i64, _int, _p, _p, _p, _i64, _p, _i64, ctypes.c_float, _p, _p, _i64, _int, _p, _i64,
+                                   _p, _p, _p, _sz, _p]),
+    "csa2_tree_plan": (_int, [_p, _p, _p, _i64, _i64, _i32, _int, _p, _p, _int, _p, _sz, _p]),
+    "csa2_tree_attn_workspace_bytes": (_sz, [_i64, _int, _i64, _i32, _i32, _int]),
+    "csa2_tree_attn": (_int, [_p, _i64, _int, _p, _p, _i64, _i32, _i32, _p, _p, _int, _int, _p, _p, _i64, _p, _i64, _int, _int,
+                              ctypes.c_float, _p, _p, _p, _sz, _p]),
+    "csa2_token_logprobs": (_int, [_p, _int, _i64, _i64, _i64, ctypes.c_float, _p, _int, _p, _p, _p, _int, _p, _p, _p, _sz, _p]),
+    "csa2_tree_commit": (_int, [_p, _p, _p, _p, _p, _i64, _i64, _i32, _int, _p, _p, _i64, _p, _i64, _int, _p, _i64, _p, _p, _p, _p,
+                                _p, _p, _p, _sz, _p]),
     "csa2_launch_count": (_i64, []),
     "csa2_debug_wait_limit": (_int, [_i64]),
     "csa2_kernel_name": (ctypes.c_char_p, [_int]),
@@ -232,9 +242,52 @@ def csa2_fp4_matvec(x, x_fmt, x_scales, x_stride, n, k, codes, scales, n_out, al
         _ptr(ws), ws_bytes, _stream(stream)))
 
 
+def csa2_head_norm_rope(q_bf16, q_stride, n_heads, q_weight, q_out, latents, lat_stride, lat_weight, n, eps, pos, rope_table,
+                        rope_max_pos, fmt, dst_row, n_rows, dst_codes, dst_scales, ws, ws_bytes, stream=None):
+    return _check("csa2_head_norm_rope", lib.csa2_head_norm_rope(
+        _ptr(q_bf16), q_stride, n_heads, _ptr(q_weight), _ptr(q_out), _ptr(latents), lat_stride, _ptr(lat_weight), n, eps,
+        _ptr(pos), _ptr(rope_table), rope_max_pos, fmt, _ptr(dst_row), n_rows, _ptr(dst_codes), _ptr(dst_scales), _ptr(ws),
+        ws_bytes, _stream(stream)))
+
+
+def csa2_tree_plan(parent, q_start, kv_len, n_req, n_tokens, max_q, window, pos, mask, mask_words, ws, ws_bytes, stream=None):
+    return _check("csa2_tree_plan", lib.csa2_tree_plan(
+        _ptr(parent), _ptr(q_start), _ptr(kv_len), n_req, n_tokens, max_q, window, _ptr(pos), _ptr(mask), mask_words, _ptr(ws),
+        ws_bytes, _stream(stream)))
+
+
+def csa2_tree_attn_workspace_bytes(n_tokens, n_heads, n_req, max_q, max_kv, window):
+    return lib.csa2_tree_attn_workspace_bytes(n_tokens, n_heads, n_req, max_q, max_kv, window)
+
+
+def csa2_tree_attn(q_bf16, n_tokens, n_heads, q_start, kv_len, n_req, max_q, max_kv, pos, mask, mask_words, fmt, codes, scales,
+                   n_rows, table, max_pages, page_size, window, sm_scale, out, out_lse, ws, ws_bytes, stream=None):
+    return _check("csa2_tree_attn", lib.csa2_tree_attn(
+        _ptr(q_bf16), n_tokens, n_heads, _ptr(q_start), _ptr(kv_len), n_req, max_q, max_kv, _ptr(pos), _ptr(mask), mask_words, fmt,
+        _ptr(codes), _ptr(scales), n_rows, _ptr(table), max_pages, page_size, window, sm_scale, _ptr(out), _ptr(out_lse), _ptr(ws),
+        ws_bytes, _stream(stream)))
+
+
+def csa2_token_logprobs(logits, dtype, stride, n, vocab, scale, tokens, given, logprobs, lse, entropy, top, ids, best, ws, ws_bytes,
+                        stream=None):
+    """`stride` counts the elements between rows; the last argument is the CUDA stream."""
+    return _check("csa2_token_logprobs", lib.csa2_token_logprobs(
+        _ptr(logits), dtype, stride, n, vocab, scale, _ptr(tokens), given, _ptr(logprobs), _ptr(lse), _ptr(entropy), top, _ptr(ids),
+        _ptr(best), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def csa2_tree_commit(parent, token, choice, q_start, kv_len, n_req, n_tokens, max_q, fmt, codes, scales, n_rows, table, max_pages,
+                     page_size, free_pages, n_pages, n_free, n_free_out, cached, path, accepted, next_token, ws, ws_bytes,
+                     stream=None):
+    return _check("csa2_tree_commit", lib.csa2_tree_commit(
+        _ptr(parent), _ptr(token), _ptr(choice), _ptr(q_start), _ptr(kv_len), n_req, n_tokens, max_q, fmt, _ptr(codes), _ptr(scales),
+        n_rows, _ptr(table), max_pages, page_size, _ptr(free_pages), n_pages, _ptr(n_free), _ptr(n_free_out), _ptr(cached), _ptr(path),
+        _ptr(accepted), _ptr(next_token), _ptr(ws), ws_bytes, _stream(stream)))
+
+
 KERNELS = ("scan_blockmax", "select_blocks", "pool_score", "select_topk", "attn_split",
            "attn_merge", "quantize_fp4", "quantize_fp8", "rope_table", "page_plan", "paged_attn", "paged_merge",
-           "rmsnorm_fp8", "fp4_matvec", "paged_decode")
+           "rmsnorm_fp8", "fp4_matvec", "paged_decode", "head_norm_rope", "tree_plan", "token_logprobs", "tree_commit")
 
 
 def csa2_launch_count():

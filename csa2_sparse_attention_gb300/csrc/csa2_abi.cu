@@ -52,7 +52,8 @@ void timer_end(int id, cudaStream_t s) {
 static const char* kKernelNames[K_COUNT] = {
     "scan_blockmax", "select_blocks", "pool_score", "select_topk", "attn_split",
     "attn_merge", "quantize_fp4", "quantize_fp8", "rope_table",
-    "page_plan", "paged_attn", "paged_merge", "rmsnorm_fp8", "fp4_matvec", "paged_decode"};
+    "page_plan", "paged_attn", "paged_merge", "rmsnorm_fp8", "fp4_matvec", "paged_decode",
+    "head_norm_rope", "tree_plan", "token_logprobs", "tree_commit"};
 }  // namespace csa2
 
 using namespace csa2;

@@ -34,6 +34,8 @@ enum BoundsCheck : int32_t {
     CHK_PAGE = 8,        // paged: page id outside the cache
     CHK_LENGTH = 9,      // paged: a request's length is negative or does not fit
     CHK_CAPACITY = 10,   // page plan: more new tokens or pages than there are
+    CHK_PARENT = 11,     // tree: a node's parent is not an earlier node of its request
+    CHK_TOKEN = 12,      // log probabilities: a token outside the vocabulary
 };
 
 __device__ __forceinline__ void record(Status* st, int32_t code, int32_t which, int32_t item,
@@ -159,6 +161,11 @@ __host__ __device__ constexpr T ceil_div(T a, T b) { return (a + b - 1) / b; }
 // Host-side helpers shared by the entry points.
 namespace csa2 {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether two buffers of so many bytes share one (a null pointer shares none).
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+    return x && y && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
 csa2_status launch_status();  // maps cudaGetLastError to a csa2_status
 int sm_count();               // the current device's multiprocessors (queried once per device)
 uint64_t wait_limit_ns();      // the bounded waits' limit, passed to every launch (2 s by default)

@@ -1,0 +1,362 @@
+// Norms of every head's query and of the latents, and their rotation by
+// position, in one pass: queries leave in bf16, latents as rows of the cache.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w,   (y_2i, y_2i+1) turned by p theta^(-2i/512)
+//
+// HBM bound: 1 KB in and 1 KB out per (token, head).  A warp has a row of 512
+// channels, 16 contiguous ones a lane (one 32-byte load and store), so that a
+// lane's rotations and weights stay in its registers over the heads of its
+// token and the norm is one warp's sum.  Latents have a warp each, in the first
+// blocks.
+//
+// Latents are rounded to 4 or 8 bits as 64-bit arithmetic would: the fp32
+// result carries a bound of its error, and a group of 16 channels in which a
+// scale or a code lies nearer to a border than that is done again in fp64.
+#include "csa2_common.cuh"
+#include "csa2_round.cuh"
+#include "csa2_timer.cuh"
+
+#include <cfloat>
+
+namespace csa2 {
+
+constexpr int kHD = CSA2_LATENT_DIM;
+constexpr int kHWarps = 8;
+
+struct HeadArgs {
+    const uint8_t* q;
+    const uint8_t* q_weight;
+    uint8_t* q_out;
+    const uint8_t* lat;
+    const uint8_t* lat_weight;
+    const int64_t* pos;
+    const float2* table;   // null: no rotation
+    const int64_t* dst;
+    uint8_t* codes;
+    uint8_t* scales;
+    Status* st;
+    int64_t q_stride, lat_stride, n, max_pos, n_rows;  // strides in elements
+    int64_t n_units, lat_blocks;                       // query units; blocks that take latents
+    int32_t heads, per_unit, units;                    // heads of a unit, units of a token
+    int32_t n_hi;
+    float eps;
+};
+
+struct Row32 {
+    uint32_t w[8];
+};
+// 32 bytes from or to a 16-byte aligned address: one access where it is 32-byte
+// aligned.  (Plain loads: the outputs may be the inputs.)
+__device__ __forceinline__ Row32 load32(const uint8_t* p) {
+    Row32 v;
+    if ((reinterpret_cast<uintptr_t>(p) & 16) == 0) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                       "=r"(v.w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 16);
+        v.w[0] = a.x, v.w[1] = a.y, v.w[2] = a.z, v.w[3] = a.w, v.w[4] = b.x, v.w[5] = b.y, v.w[6] = b.z, v.w[7] = b.w;
+    }
+    return v;
+}
+__device__ __forceinline__ void store32(uint8_t* p, const Row32& v) {
+    if ((reinterpret_cast<uintptr_t>(p) & 16) == 0) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]),
+                     "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7]), "l"(p) : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+    }
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Sum of a lane's 16 squares, in pairs: off by 5 * 2^-24 of it at most.
+__device__ __forceinline__ float squares(const Row32& x) {
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = fmaf(bf16_lo(x.w[e]), bf16_lo(x.w[e]), bf16_hi(x.w[e]) * bf16_hi(x.w[e]));
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+// 1 / sqrt(mean + eps); a row of zeros stays one, also where eps is 0.
+__device__ __forceinline__ float root_of(float ss, float eps) { return ss == 0.f ? 0.f : 1.0f / sqrtf(fmaf(ss, 1.0f / kHD, eps)); }
+
+// Cosines and sines of a lane's 8 pairs at position p (csa2_rope_table_init's
+// table: the angle of p = 1024 hi + lo by addition).
+__device__ __forceinline__ void turns(const HeadArgs& a, int64_t p, int lane, float (&c)[8], float (&s)[8]) {
+    const float4* th = reinterpret_cast<const float4*>(a.table + (p >> 10) * (kHD / 2) + 8 * lane);
+    const float4* tl = reinterpret_cast<const float4*>(a.table + (int64_t(a.n_hi) + (p & 1023)) * (kHD / 2) + 8 * lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 h = __ldg(th + j), l = __ldg(tl + j);
+        c[2 * j] = fmaf(h.x, l.x, -h.y * l.y), s[2 * j] = fmaf(h.y, l.x, h.x * l.y);
+        c[2 * j + 1] = fmaf(h.z, l.z, -h.w * l.w), s[2 * j + 1] = fmaf(h.w, l.z, h.z * l.w);
+    }
+}
+
+// A token's queries: per_unit heads in a warp.
+template <bool NORM, bool TURN>
+__device__ __forceinline__ void head_queries(const HeadArgs& a, int64_t unit) {
+    const int lane = lane_id();
+    const int64_t t = unit / a.units;
+    const int h0 = int(unit - t * a.units) * a.per_unit;
+    const int h1 = h0 + a.per_unit < a.heads ? h0 + a.per_unit : a.heads;
+    const uint8_t* src = a.q + (t * a.q_stride + int64_t(h0) * kHD) * 2 + 32 * lane;
+    uint8_t* dst = a.q_out + (t * a.heads + h0) * int64_t(kHD * 2) + 32 * lane;
+    const int64_t p = a.pos != nullptr ? __ldg(a.pos + t) : 0;
+    Row32 x = load32(src), w;
+    if (NORM) w = load32(a.q_weight + 32 * lane);
+    if (p < 0 || (TURN && p >= a.max_pos)) {
+        if (p != -1 && h0 == 0 && lane == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_POSITION, int32_t(t), int32_t(p));
+        return;
+    }
+    float c[8], s[8];
+    if (TURN) turns(a, p, lane, c, s);
+    for (int h = h0; h < h1; ++h) {
+        const Row32 v = x;
+        src += kHD * 2;
+        if (h + 1 < h1) x = load32(src);
+        const float rs = NORM ? root_of(sum_lanes(squares(v)), a.eps) : 1.f;
+        Row32 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float y0 = bf16_lo(v.w[e]), y1 = bf16_hi(v.w[e]);
+            if (NORM) y0 = y0 * bf16_lo(w.w[e]) * rs, y1 = y1 * bf16_hi(w.w[e]) * rs;
+            if (TURN) {
+                const float z = fmaf(y0, c[e], -y1 * s[e]);
+                y1 = fmaf(y0, s[e], y1 * c[e]);
+                y0 = z;
+            }
+            o.w[e] = bf16x2_of(y0, y1);
+        }
+        store32(dst, o);
+        dst += kHD * 2;
+    }
+}
+
+// A token's latent.  The error of y, relative to |h0| + |h1| of its pair (h the
+// normed values): the sum of squares 10 * 2^-24 (5 in a lane, 5 over lanes), so
+// its root 5; mean and eps, root and reciprocal 2 together; the product 1 (x w
+// is exact); the rotation 5 (cosines within 1.5 * 2^-23 of their values after the
+// angles' addition, two roundings).  13 * 2^-24 < 2^-20.
+template <bool FP8>
+__device__ __forceinline__ void head_latent(const HeadArgs& a, int64_t t) {
+    const int lane = lane_id();
+    const Row32 x = load32(a.lat + t * a.lat_stride * 2 + 32 * lane);
+    const bool norm = a.lat_weight != nullptr, turn = a.table != nullptr;
+    Row32 w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w.w[e] = 0x3F803F80u;
+    if (norm) w = load32(a.lat_weight + 32 * lane);
+    const int64_t p = a.pos != nullptr ? __ldg(a.pos + t) : 0, row = a.dst != nullptr ? __ldg(a.dst + t) : t;
+    if (p < 0 || (turn && p >= a.max_pos)) {
+        if (p != -1 && lane == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_POSITION, int32_t(t), int32_t(p));
+        return;
+    }
+    if (row < 0 || row >= a.n_rows) {
+        if (row != -1 && lane == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_DST_ROW, int32_t(t), int32_t(row));
+        return;
+    }
+    const float rs = norm ? root_of(sum_lanes(squares(x)), a.eps) : 1.f;
+    float y[16], bnd[8];  // bnd[j]: how far pair j's values may be off
+    float c[8], s[8];
+    if (turn) turns(a, p, lane, c, s);
+    bool whole = true;  // no NaN or infinity
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float h0 = bf16_lo(x.w[e]) * bf16_lo(w.w[e]) * rs, h1 = bf16_hi(x.w[e]) * bf16_hi(w.w[e]) * rs;
+        bnd[e] = norm || turn ? 0x1p-20f * (fabsf(h0) + fabsf(h1)) : 0.f;
+        y[2 * e] = turn ? fmaf(h0, c[e], -h1 * s[e]) : h0;
+        y[2 * e + 1] = turn ? fmaf(h0, s[e], h1 * c[e]) : h1;
+        whole = whole && fabsf(y[2 * e]) <= FLT_MAX && fabsf(y[2 * e + 1]) <= FLT_MAX && bnd[e] <= FLT_MAX;
+    }
+    uint32_t sb = 0, cw[4] = {0, 0, 0, 0};
+    bool risky = false;
+    if (FP8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t two = e4m3x2_rn_sat(y[2 * j], y[2 * j + 1]);
+            cw[j >> 1] |= two << (16 * (j & 1));
+            const float a0 = fabsf(y[2 * j]), a1 = fabsf(y[2 * j + 1]);
+            risky |= whole && (e4m3x2_rn_sat(fmaxf(a0 - bnd[j], 0.f), fmaxf(a1 - bnd[j], 0.f)) != e4m3x2_rn_sat(a0 + bnd[j], a1 + bnd[j]));
+        }
+    } else if (whole) {
+        float amax = 0.f, bmax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(y[e]));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bmax = fmaxf(bmax, bnd[j]);
+        // amax / 6 by a multiply: its error (< 2^-22 relative) sits inside mq
+        const float q6 = amax * (1.0f / 6.0f), mq = fmaf(q6, 0x1p-20f, bmax * (1.0f / 6.0f) * 1.001f);
+        sb = e4m3x2_rn_sat(q6, 0.f) & 0xFF;
+        const uint32_t span = e4m3x2_rn_sat(fmaxf(q6 - mq, 0.f), q6 + mq);
+        risky = (span & 0xFF) != (span >> 8);
+        const float sc = e4m3_value(sb);
+        if (sc > 0.f) {
+            const float inv = __frcp_rn(sc);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float r0 = y[2 * j] * inv, r1 = y[2 * j + 1] * inv;
+                cw[j >> 2] |= e2m1x2_rn_sat(r0, r1) << (8 * (j & 3));
+                const float a0 = fabsf(r0), a1 = fabsf(r1);
+                const float m0 = fmaf(a0, 0x1p-22f, bnd[j] * inv * 1.001f), m1 = fmaf(a1, 0x1p-22f, bnd[j] * inv * 1.001f);
+                risky |= e2m1x2_rn_sat(fmaxf(a0 - m0, 0.f), fmaxf(a1 - m1, 0.f)) != e2m1x2_rn_sat(a0 + m0, a1 + m1);
+            }
+        }
+    } else {
+        sb = 0x7F;  // a scale of NaN: what attends to the latent gets NaN
+    }
+    if (__any_sync(0xffffffffu, risky)) {
+        // the row's sum of squares in fp64, then the groups near a border
+        double ss = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double lo = double(bf16_lo(x.w[e])), hi = double(bf16_hi(x.w[e]));
+            ss = fma(lo, lo, fma(hi, hi, ss));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (risky) {
+            const double rs64 = !norm ? 1.0 : ss == 0.0 ? 0.0 : 1.0 / sqrt(ss / double(kHD) + double(a.eps));
+            const double2* t64 = reinterpret_cast<const double2*>(a.table + int64_t(a.n_hi + 1024) * (kHD / 2));
+            const int64_t rh = (p >> 10) * (kHD / 2) + 8 * lane, rl = (int64_t(a.n_hi) + (p & 1023)) * (kHD / 2) + 8 * lane;
+            double z[16], top = 0.0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double h0 = double(bf16_lo(x.w[e])) * double(bf16_lo(w.w[e])) * rs64;
+                const double h1 = double(bf16_hi(x.w[e])) * double(bf16_hi(w.w[e])) * rs64;
+                z[2 * e] = h0, z[2 * e + 1] = h1;
+                if (turn) {
+                    const double2 h = t64[rh + e], l = t64[rl + e];
+                    const double c64 = fma(h.x, l.x, -h.y * l.y), s64 = fma(h.y, l.x, h.x * l.y);
+                    z[2 * e] = fma(h0, c64, -h1 * s64);
+                    z[2 * e + 1] = fma(h0, s64, h1 * c64);
+                }
+                top = fmax(top, fmax(fabs(z[2 * e]), fabs(z[2 * e + 1])));
+            }
+            cw[0] = cw[1] = cw[2] = cw[3] = 0;
+            if (FP8) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    cw[e >> 2] |= (e4m3_rne_f64(fabs(z[e])) | (signbit(z[e]) ? 0x80u : 0u)) << (8 * (e & 3));
+            } else {
+                sb = e4m3_rne_f64(top / 6.0);
+                const double s64 = double(e4m3_value(sb));
+                if (s64 > 0.0) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) cw[e >> 3] |= e2m1_code_f64(z[e], s64) << (4 * (e & 7));
+                }
+            }
+        }
+    }
+    if (FP8) {
+        *reinterpret_cast<uint4*>(a.codes + row * kHD + 16 * lane) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+    } else {
+        *reinterpret_cast<uint2*>(a.codes + row * (kHD / 2) + 8 * lane) = make_uint2(cw[0], cw[1]);
+        a.scales[row * (kHD / 16) + lane] = uint8_t(sb);
+    }
+}
+
+template <bool NORM, bool TURN, bool FP8>
+__global__ void __launch_bounds__(32 * kHWarps) head_norm_rope_kernel(const HeadArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5;
+    if (int64_t(blockIdx.x) < a.lat_blocks) {
+        const int64_t t = int64_t(blockIdx.x) * kHWarps + warp;
+        if (t < a.n) head_latent<FP8>(a, t);
+        return;
+    }
+    const int64_t unit = (int64_t(blockIdx.x) - a.lat_blocks) * kHWarps + warp;
+    if (unit < a.n_units) head_queries<NORM, TURN>(a, unit);
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" csa2_status csa2_head_norm_rope(const void* q, int64_t q_stride, int n_heads, const void* q_weight, void* q_out,
+                                           const void* latents, int64_t lat_stride, const void* lat_weight, int64_t n, float eps,
+                                           const int64_t* pos, const void* rope_table, int64_t rope_max_pos, int fmt,
+                                           const int64_t* dst_row, int64_t n_rows, uint8_t* dst_codes, uint8_t* dst_scales,
+                                           void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    if (n < 0 || n_rows < 0 || !(eps >= 0.f) || !(eps <= FLT_MAX)) return CSA2_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+    if (!q && !latents) return CSA2_ERR_INVALID_ARG;
+    if (n > (int64_t(1) << 22)) return CSA2_ERR_UNSUPPORTED;
+    if ((q == nullptr) != (q_out == nullptr) || (!q && q_weight) || (!latents && lat_weight)) return CSA2_ERR_INVALID_ARG;
+    for (const void* p : {q, q_weight, static_cast<const void*>(q_out), latents, lat_weight, static_cast<const void*>(pos), rope_table,
+                          static_cast<const void*>(dst_row), static_cast<const void*>(dst_codes),
+                          static_cast<const void*>(dst_scales)})
+        if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    if (rope_table && (!pos || rope_max_pos <= 0 || rope_max_pos > (int64_t(1) << 31))) return CSA2_ERR_INVALID_ARG;
+    if (q) {
+        if (n_heads < 1 || n_heads > 128) return CSA2_ERR_UNSUPPORTED;
+        const int64_t row = int64_t(n_heads) * kHD;
+        if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 31)) return CSA2_ERR_INVALID_ARG;
+        // the outputs are the queries themselves, or apart from them
+        if (!(q == q_out && q_stride == row) && overlap(q, ((n - 1) * q_stride + row) * 2, q_out, n * row * 2))
+            return CSA2_ERR_INVALID_ARG;
+    }
+    if (latents) {
+        if (fmt != CSA2_FMT_FP4 && fmt != CSA2_FMT_FP8) return CSA2_ERR_UNSUPPORTED;
+        if (lat_stride < kHD || lat_stride % 8 || lat_stride > (int64_t(1) << 31)) return CSA2_ERR_INVALID_ARG;
+        if (!dst_codes || (fmt == CSA2_FMT_FP4) != (dst_scales != nullptr)) return CSA2_ERR_INVALID_ARG;
+        if (!dst_row && n > n_rows) return CSA2_ERR_INVALID_ARG;
+        // what is written lies apart from what is read and from each other
+        const int64_t in = ((n - 1) * lat_stride + kHD) * 2, cb = n_rows * (fmt == CSA2_FMT_FP4 ? kHD / 2 : kHD), sb = n_rows * (kHD / 16);
+        const int64_t qi = q ? ((n - 1) * q_stride + int64_t(n_heads) * kHD) * 2 : 0, qo = q ? n * n_heads * int64_t(kHD) * 2 : 0;
+        if (overlap(latents, in, q_out, qo) || overlap(latents, in, dst_codes, cb) || overlap(latents, in, dst_scales, sb) ||
+            overlap(dst_codes, cb, dst_scales, sb) || overlap(q, qi, dst_codes, cb) || overlap(q, qi, dst_scales, sb) ||
+            overlap(q_out, qo, dst_codes, cb) || overlap(q_out, qo, dst_scales, sb))
+            return CSA2_ERR_INVALID_ARG;
+    }
+    if (n == 0) return CSA2_OK;
+    HeadArgs a{};
+    a.q = static_cast<const uint8_t*>(q);
+    a.q_weight = static_cast<const uint8_t*>(q_weight);
+    a.q_out = static_cast<uint8_t*>(q_out);
+    a.lat = static_cast<const uint8_t*>(latents);
+    a.lat_weight = static_cast<const uint8_t*>(lat_weight);
+    a.pos = pos;
+    a.table = static_cast<const float2*>(rope_table);
+    a.dst = dst_row;
+    a.codes = dst_codes;
+    a.scales = dst_scales;
+    a.st = static_cast<Status*>(ws);
+    a.q_stride = q_stride;
+    a.lat_stride = lat_stride;
+    a.n = n;
+    a.max_pos = rope_max_pos;
+    a.n_rows = n_rows;
+    a.n_hi = rope_table ? int(ceil_div<int64_t>(rope_max_pos, 1024)) : 0;
+    a.eps = eps;
+    a.lat_blocks = latents ? ceil_div<int64_t>(n, kHWarps) : 0;
+    if (q) {
+        // as many heads to a warp as leave every multiprocessor its warps
+        a.heads = n_heads;
+        const int64_t per = n * n_heads / (int64_t(sm_count()) * 64);
+        a.per_unit = int32_t(per < 1 ? 1 : per > 8 ? 8 : per);
+        a.units = ceil_div(a.heads, a.per_unit);
+        a.n_units = n * a.units;
+    }
+    const dim3 grid(unsigned(a.lat_blocks + ceil_div<int64_t>(a.n_units, kHWarps)));
+    cudaStream_t s = cudaStream_t(stream);
+    timer_begin(K_HEAD, s);
+    auto go = [&](auto kernel) { launch(kernel, grid, 32 * kHWarps, 0, s, 1, a); };
+    const bool f8 = fmt == CSA2_FMT_FP8;
+    if (a.q_weight && a.table) f8 ? go(head_norm_rope_kernel<true, true, true>) : go(head_norm_rope_kernel<true, true, false>);
+    else if (a.q_weight) f8 ? go(head_norm_rope_kernel<true, false, true>) : go(head_norm_rope_kernel<true, false, false>);
+    else if (a.table) f8 ? go(head_norm_rope_kernel<false, true, true>) : go(head_norm_rope_kernel<false, true, false>);
+    else f8 ? go(head_norm_rope_kernel<false, false, true>) : go(head_norm_rope_kernel<false, false, false>);
+    timer_end(K_HEAD, s);
+    return launch_status();
+}

@@ -1,0 +1,545 @@
+// Log-sum-exp, entropy, log probabilities of given tokens and the top
+// alternatives of rows of logits, in one pass over them.
+//
+//   y = (x - m) s,  S = sum e^y,  lse = m s + log S,
+//   log p(t) = y_t - log S,  entropy = log S - sum(e^y y) / S      (m = max x)
+//
+// HBM bound: the logits, once.  A row is one block's, or is cut into slices for
+// a cluster of up to eight, whose blocks leave their parts in shared memory for
+// the first of them to join: no workspace, one launch.  A thread takes groups of
+// four 16-byte vectors and keeps its own base b for the exponentials, which moves
+// only when a value lies 2^4 above it, so that the running maximum costs a maximum
+// and a test per group.  (Not further: sum(e^y y) against b turns into that
+// against m by sum * (b - m), which cancels for what lies above b.)
+//
+// The k largest: every group's maximum stays in shared memory.  The k-th largest
+// of the threads' maxima, found bit by bit, has k values at or above it; the few
+// groups that reach it are read again (from L2) and their values at or above it
+// ranked by counting.
+#include "csa2_common.cuh"
+#include "csa2_timer.cuh"
+
+#include <atomic>
+#include <cfloat>
+#include <climits>
+
+namespace csa2 {
+
+constexpr int kLThreads = 512, kLWarps = kLThreads / 32;
+constexpr int kLGroup = 4;         // vectors of a group
+constexpr int kLMaxTurns = 32;     // groups of a thread
+constexpr int kLTop = CSA2_LOGPROBS_TOP;
+constexpr int kLCands = 1024;      // values that are ranked
+constexpr int kLMaxCluster = 8;
+constexpr float kLFloor = -160.f;  // exponents below it are nothing in fp32
+
+struct LogArgs {
+    const uint8_t* x;
+    const int64_t* tokens;
+    float* logprobs;
+    float* lse;
+    float* entropy;
+    int32_t* ids;
+    float* best;
+    Status* st;
+    int64_t stride;     // elements
+    int32_t vocab, given, top, slice;  // vectors of a slice
+    float scale;        // of the logits
+};
+
+struct LogSmem {
+    unsigned long long cand[kLCands];  // (key of the value, ~index): larger values, then lower indices, are larger
+    unsigned long long list[kLTop];    // the slice's largest, in order
+    float max, sum, tilt;              // of the slice: m, S, sum(e^y y)
+    int bad, listed, n_cand;
+    float red[3][kLWarps];
+    int redi[kLWarps];
+    // the first block's join
+    unsigned long long all[kLMaxCluster][kLTop];
+    int all_n[kLMaxCluster];
+    float all_f[kLMaxCluster][3];
+    int all_bad;
+};
+
+__device__ __forceinline__ unsigned long long ranked(float v, int32_t index) {
+    return (static_cast<unsigned long long>(float_key(v)) << 32) | uint32_t(~uint32_t(index));
+}
+__device__ __forceinline__ float nan_max(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two floats in a register pair: half of the issue slots.
+__device__ __forceinline__ uint64_t both(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void each(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t add_both(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_both(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_both(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// sum += v with what the sum's rounding leaves behind in `rest` (a long tail next
+// to a large term would vanish one by one: 2^-25 of the sum each, and twenty times
+// that of the entropy).
+__device__ __forceinline__ void add_kept(float& sum, float& rest, float v) {
+    const float y = v + rest, t = sum + y;
+    rest = y - (t - sum);
+    sum = t;
+}
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
+}
+// The same variable of another block of the cluster.
+template <typename T>
+__device__ __forceinline__ uint32_t peer(const T* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_u32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ unsigned long long peer_u64(uint32_t a) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
+}
+
+// Rows begin anywhere: vectors are the 16-byte pieces of memory that hold the
+// row, `head` elements of the first one lie before it.
+template <typename T>
+struct RowView {
+    static constexpr int E = 16 / sizeof(T);
+    const uint8_t* base;  // of vector 0
+    int32_t head, vocab;
+    __device__ __forceinline__ RowView(const LogArgs& a, int64_t row) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) + row * a.stride * int64_t(sizeof(T));
+        head = int32_t(at & 15) / int32_t(sizeof(T));
+        base = reinterpret_cast<const uint8_t*>(at & ~uintptr_t(15));
+        vocab = a.vocab;
+    }
+    __device__ __forceinline__ int32_t vectors() const { return (head + vocab + E - 1) / E; }
+    // E values of vector v; what lies outside the row is -inf
+    __device__ __forceinline__ uint4 load(int32_t v) const {
+        const int32_t i0 = v * E - head;
+        if (i0 >= 0 && i0 + E <= vocab) return __ldg(reinterpret_cast<const uint4*>(base) + v);
+        uint32_t w[4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = i0 + e >= 0 && i0 + e < vocab ? __ldg(reinterpret_cast<const uint32_t*>(base) + 4 * int64_t(v) + e) : 0xFF800000u;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t two[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t i = i0 + 2 * e + k;
+                    two[k] = i >= 0 && i < vocab ? __ldg(reinterpret_cast<const uint16_t*>(base) + 8 * int64_t(v) + 2 * e + k) : 0xFF80u;
+                }
+                w[e] = two[0] | (two[1] << 16);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void values(const uint4& v, float (&x)[E]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4) {
+                x[e] = __uint_as_float(w[e]);
+            } else {
+                x[2 * e] = bf16_lo(w[e]);
+                x[2 * e + 1] = bf16_hi(w[e]);
+            }
+        }
+    }
+};
+
+// The sum of v over the block's earlier threads, and over all of them.
+__device__ __forceinline__ int block_before(LogSmem& S, int v, int& all) {
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    __syncthreads();  // the last use of redi
+    if (lane == 31) S.redi[warp] = inc;
+    __syncthreads();
+    int before = inc - v;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kLWarps; ++w) {
+        if (w < warp) before += S.redi[w];
+        all += S.redi[w];
+    }
+    return before;
+}
+
+// The k largest of the slice, in order, to S.list (fewer where fewer are above -inf).
+template <typename T>
+__device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& row, int32_t v0, int32_t v1, int turns, float mine, int k) {
+    constexpr int E = RowView<T>::E;
+    const int tid = threadIdx.x;
+    // the k-th largest of the threads' maxima (0 where fewer have any)
+    uint32_t bar = 0;
+    {
+        const uint32_t key = mine > -INFINITY ? float_key(mine) : 0u;
+#pragma unroll 1
+        for (int b = 31; b >= (sizeof(T) == 2 ? 16 : 0); --b) {
+            const uint32_t up = bar | (1u << b);
+            if (__syncthreads_count(key >= up) >= k) bar = up;
+        }
+    }
+    const uint32_t low = float_key(-INFINITY) + 1;  // -inf is no alternative
+    if (bar < low) bar = low;
+    // visits the values of the groups whose maximum's key is `from` or more
+    auto visit = [&](uint32_t from, auto f) {
+        for (int j = 0; j < turns; ++j) {
+            if (float_key(groups[j * kLThreads + tid]) < from) continue;
+#pragma unroll
+            for (int g = 0; g < kLGroup; ++g) {
+                const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                if (v >= v1) continue;
+                float x[E];
+                row.values(row.load(v), x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) f(x[e], v * E - row.head + e);
+            }
+        }
+    };
+    auto collect = [&](unsigned long long from) {
+        visit(uint32_t(from >> 32), [&](float x, int32_t i) {
+            const unsigned long long c = ranked(x, i);
+            if (c >= from) {
+                const int at = atomicAdd(&S.n_cand, 1);
+                if (at < kLCands) S.cand[at] = c;
+            }
+        });
+    };
+    auto collect_all = [&](unsigned long long from) {  // how many there are
+        __syncthreads();
+        if (tid == 0) S.n_cand = 0;
+        __syncthreads();
+        collect(from);
+        __syncthreads();
+        return S.n_cand;
+    };
+    int n = collect_all(static_cast<unsigned long long>(bar) << 32);
+    if (n > kLCands) {
+        // Many values at the bar, as where a mask leaves less than k of a row above its own value: the ones above it, and the
+        // first ones at it in the row's order.
+        n = collect_all(static_cast<unsigned long long>(bar + 1) << 32);
+        if (n < k) {
+            for (int j = 0; j < turns && n < k; ++j) {
+                const bool near = float_key(groups[j * kLThreads + tid]) >= bar;
+                for (int g = 0; g < kLGroup && n < k; ++g) {
+                    const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                    uint32_t bits = 0;  // of the vector's values at the bar
+                    if (near && v < v1) {
+                        float x[E];
+                        row.values(row.load(v), x);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) == bar) << e;
+                    }
+                    int all, at = n + block_before(S, __popc(bits), all);
+                    for (; bits != 0 && at < k; bits &= bits - 1, ++at)
+                        S.cand[at] = ranked(key_float(bar), v * E - row.head + __ffs(bits) - 1);
+                    n = n + all < k ? n + all : k;
+                }
+            }
+        } else if (n > kLCands) {
+            // Many different ones, in the places of few threads: the k-th largest pair of value and index, bit by bit.
+            unsigned long long edge = 0;
+#pragma unroll 1
+            for (int b = 63; b >= 0; --b) {
+                const unsigned long long up = edge | (1ull << b);
+                int some = 0, all;
+                visit(uint32_t(up >> 32) > low ? uint32_t(up >> 32) : low, [&](float x, int32_t i) { some += ranked(x, i) >= up; });
+                block_before(S, some, all);
+                if (all >= k) edge = up;
+            }
+            n = collect_all(edge);
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < n; i += kLThreads) {
+        const unsigned long long c = S.cand[i];
+        int at = 0;
+        for (int j = 0; j < n; ++j) at += S.cand[j] > c;
+        if (at < k) S.list[at] = c;
+    }
+    if (tid == 0) S.listed = n < k ? n : k;
+    __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLThreads, 2) token_logprobs_kernel(const LogArgs a, int cluster) {
+    constexpr int E = RowView<T>::E;
+    extern __shared__ __align__(16) float groups[];  // maxima of the groups, [turn][thread]
+    __shared__ LogSmem S;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int64_t r = blockIdx.x / uint32_t(cluster);
+    const int rank = int(blockIdx.x) - int(r) * cluster;
+    const RowView<T> row(a, r);
+    const int32_t nv = row.vectors(), v0 = rank * a.slice < nv ? rank * a.slice : nv, v1 = v0 + a.slice < nv ? v0 + a.slice : nv;
+    const int turns = (v1 - v0 + kLThreads * kLGroup - 1) / (kLThreads * kLGroup);
+    const float c = a.scale * 1.4426950408889634f, reach = 4.f / c;
+    // the given tokens' logits, while the row comes in
+    float x_given = -INFINITY;
+    if (rank == 0 && tid < a.given) {
+        const int64_t id = a.tokens[r * a.given + tid];
+        if (id >= 0 && id < a.vocab)
+            x_given = sizeof(T) == 4 ? reinterpret_cast<const float*>(a.x)[r * a.stride + id]
+                                     : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(a.x)[r * a.stride + id]) << 16);
+        else if (id != -1)
+            record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_TOKEN, int32_t(r), int32_t(id));
+    }
+    // ---- one pass: base, sum and tilt of a thread, its maximum, its groups' maxima
+    float base = __uint_as_float(0x7FC00000u), sum = 0.f, tilt = 0.f, top = -INFINITY, sum_rest = 0.f, tilt_rest = 0.f;
+    bool bad = false;
+    for (int j = 0; j < turns; ++j) {
+        uint4 v[kLGroup];
+#pragma unroll
+        for (int g = 0; g < kLGroup; ++g) {
+            const int32_t at = v0 + (j * kLGroup + g) * kLThreads + tid;
+            v[g] = at < v1 ? row.load(at) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                                            : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kLGroup; ++g) {
+            float x[E];
+            row.values(v[g], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) m = nan_max(m, x[e]);
+        }
+        groups[j * kLThreads + tid] = m;
+        if (!(m <= base + reach)) {  // the first group, one far above the base, NaN
+            if (!(m < INFINITY)) bad = true;
+            const float b = fmaxf(m, -FLT_MAX);
+            const float d = (base - b) * c, f = sum == 0.f ? 0.f : exp2_of(d);
+            tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
+            sum = f == 0.f ? 0.f : f * sum;
+            sum_rest *= f, tilt_rest *= f;
+            base = b;
+        }
+        top = fmaxf(top, m);
+        uint64_t gs[2] = {0, 0}, gt[2] = {0, 0};
+        const uint64_t minus = both(-base, -base), cc = both(c, c);
+#pragma unroll
+        for (int g = 0; g < kLGroup; ++g) {
+            float x[E];
+            row.values(v[g], x);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                float y0, y1;
+                each(mul_both(add_both(both(x[e], x[e + 1]), minus), cc), y0, y1);
+                y0 = fmaxf(y0, kLFloor), y1 = fmaxf(y1, kLFloor);
+                const uint64_t p = both(exp2_of(y0), exp2_of(y1));
+                gs[(e >> 1) & 1] = add_both(gs[(e >> 1) & 1], p);
+                gt[(e >> 1) & 1] = fma_both(p, both(y0, y1), gt[(e >> 1) & 1]);
+            }
+        }
+        float s0, s1, t0, t1;
+        each(add_both(gs[0], gs[1]), s0, s1);
+        each(add_both(gt[0], gt[1]), t0, t1);
+        add_kept(sum, sum_rest, s0 + s1);
+        add_kept(tilt, tilt_rest, t0 + t1);
+    }
+    sum += sum_rest, tilt += tilt_rest;
+    // ---- the slice's: everything against its maximum
+    float m = top;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) S.red[0][warp] = m;
+    const bool any_bad = __syncthreads_or(bad);
+    m = S.red[0][lane & (kLWarps - 1)];
+#pragma unroll
+    for (int o = kLWarps / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    {
+        const float d = sum == 0.f ? 0.f : (base - m) * c, f = sum == 0.f ? 0.f : exp2_of(d);
+        tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
+        sum = f * sum;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        tilt += __shfl_xor_sync(0xffffffffu, tilt, o);
+    }
+    if (lane == 0) S.red[1][warp] = sum, S.red[2][warp] = tilt;
+    if (a.top > 0 && !any_bad) top_of_slice<T>(S, groups, row, v0, v1, turns, top, a.top);
+    else if (tid == 0) S.listed = 0;
+    __syncthreads();
+    if (tid == 0) {
+        float s = 0.f, t = 0.f;
+        for (int w = 0; w < kLWarps; ++w) s += S.red[1][w], t += S.red[2][w];
+        S.max = m, S.sum = s, S.tilt = t, S.bad = any_bad;
+    }
+    // ---- the row's
+    if (cluster > 1) {
+        cluster_meet();
+        if (rank == 0) {
+            if (tid < cluster) {
+                S.all_f[tid][0] = __uint_as_float(peer_u32(peer(&S.max, tid)));
+                S.all_f[tid][1] = __uint_as_float(peer_u32(peer(&S.sum, tid)));
+                S.all_f[tid][2] = __uint_as_float(peer_u32(peer(&S.tilt, tid)));
+                S.all_n[tid] = int(peer_u32(peer(&S.listed, tid)));
+            }
+            int b = tid < cluster ? int(peer_u32(peer(&S.bad, tid))) : 0;
+            for (int i = tid; i < cluster * a.top; i += kLThreads) {
+                const int q = i / a.top, e = i - q * a.top;
+                S.all[q][e] = peer_u64(peer(&S.list[e], q));  // (behind its last one: whatever is there)
+            }
+            b = __syncthreads_or(b);
+            if (tid == 0) S.all_bad = b;
+        }
+        cluster_meet();  // the others' parts are read
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+        if (tid == 0) {
+            S.all_f[0][0] = S.max, S.all_f[0][1] = S.sum, S.all_f[0][2] = S.tilt;
+            S.all_n[0] = S.listed;
+            S.all_bad = S.bad;
+        }
+        for (int i = tid; i < a.top; i += kLThreads) S.all[0][i] = S.list[i];
+        __syncthreads();
+    }
+    float big = -INFINITY;
+    for (int q = 0; q < cluster; ++q) big = fmaxf(big, S.all_f[q][0]);
+    float s = 0.f, t = 0.f;
+    int total = 0;
+    for (int q = 0; q < cluster; ++q) {
+        const float sq = S.all_f[q][1], d = sq == 0.f ? 0.f : (S.all_f[q][0] - big) * c, f = sq == 0.f ? 0.f : exp2_of(d);
+        s = fmaf(f, sq, s);
+        t = f == 0.f ? t : fmaf(f, fmaf(sq, d, S.all_f[q][2]), t);
+        total += S.all_n[q];
+    }
+    const bool none = s == 0.f, nan = S.all_bad != 0;  // nothing above -inf; NaN or infinity among them
+    const float log_s = logf(s), not_a = __uint_as_float(0x7FC00000u);
+    if (tid == 0) {
+        if (a.lse) a.lse[r] = nan ? not_a : none ? -INFINITY : fmaf(big, a.scale, log_s);
+        if (a.entropy) a.entropy[r] = nan ? not_a : none ? 0.f : log_s - t / s * 0.6931471805599453f;
+    }
+    if (tid < a.given)
+        a.logprobs[r * a.given + tid] = nan ? not_a : none || x_given == -INFINITY ? -INFINITY : (x_given - big) * a.scale - log_s;
+    // alternatives: a value's place is how many of all lists are larger (none where a slice has NaN, whatever the others list)
+    if (tid >= (nan ? 0 : total) && tid < a.top) {
+        a.ids[r * a.top + tid] = -1;
+        a.best[r * a.top + tid] = nan ? not_a : -INFINITY;
+    }
+    for (int i = tid; i < cluster * a.top && !nan; i += kLThreads) {
+        const int q = i / a.top, e = i - q * a.top;
+        if (e >= S.all_n[q]) continue;
+        const unsigned long long v = S.all[q][e];
+        int at = e;
+        for (int o = 0; o < cluster; ++o) {
+            if (o == q) continue;
+            int lo = 0, hi = S.all_n[o];  // how many of list o are larger
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (S.all[o][mid] > v) lo = mid + 1;
+                else hi = mid;
+            }
+            at += lo;
+        }
+        if (at < a.top) {
+            a.ids[r * a.top + at] = int32_t(~uint32_t(v));
+            a.best[r * a.top + at] = (key_float(uint32_t(v >> 32)) - big) * a.scale - log_s;
+        }
+    }
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+template <typename T>
+static csa2_status logprobs_launch(LogArgs a, int64_t n, int cluster, size_t smem, cudaStream_t s) {
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kLMaxTurns * kLThreads * int(sizeof(float))) != cudaSuccess)
+            return CSA2_ERR_CUDA;
+        done[dev].store(true, std::memory_order_release);
+    }
+    timer_begin(K_LOGPROBS, s);
+    launch(token_logprobs_kernel<T>, dim3(unsigned(n * cluster)), kLThreads, smem, s, unsigned(cluster), a, cluster);
+    timer_end(K_LOGPROBS, s);
+    return launch_status();
+}
+
+extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_t stride, int64_t n, int64_t vocab, float scale,
+                                           const int64_t* tokens, int given, float* logprobs, float* lse, float* entropy, int top,
+                                           int32_t* ids, float* best, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    if (n < 0 || vocab < 1 || given < 0 || top < 0 || !(scale > 0.f) || !(scale <= FLT_MAX)) return CSA2_ERR_INVALID_ARG;
+    if (dtype != CSA2_OUT_BF16 && dtype != CSA2_OUT_F32) return CSA2_ERR_UNSUPPORTED;
+    if (n > (1 << 24) || vocab > (1 << 21) || given > kLTop || top > kLTop || !(scale >= 0x1p-20f) || !(scale <= 0x1p20f))
+        return CSA2_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+    if (!logits || stride < vocab || stride > (int64_t(1) << 40)) return CSA2_ERR_INVALID_ARG;
+    if (given > 0 && (!tokens || !logprobs)) return CSA2_ERR_INVALID_ARG;
+    if (top > 0 && (!ids || !best)) return CSA2_ERR_INVALID_ARG;
+    for (const void* p : {logits, static_cast<const void*>(tokens), static_cast<const void*>(logprobs), static_cast<const void*>(lse),
+                          static_cast<const void*>(entropy), static_cast<const void*>(ids), static_cast<const void*>(best)})
+        if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    const int64_t size = dtype == CSA2_OUT_BF16 ? 2 : 4, in = ((n - 1) * stride + vocab) * size;
+    if (overlap(logits, in, logprobs, n * given * 4) || overlap(logits, in, lse, n * 4) || overlap(logits, in, entropy, n * 4) ||
+        overlap(logits, in, ids, n * top * 4) || overlap(logits, in, best, n * top * 4))
+        return CSA2_ERR_INVALID_ARG;
+    LogArgs a{};
+    a.x = static_cast<const uint8_t*>(logits);
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.ids = ids;
+    a.best = best;
+    a.st = static_cast<Status*>(ws);
+    a.stride = stride;
+    a.vocab = int32_t(vocab);
+    a.given = given;
+    a.top = top;
+    a.scale = scale;
+    // A row in as many slices as keep all multiprocessors busy and leave a slice a vector per thread; and so many that the
+    // groups' maxima find room.
+    const int64_t nv = vocab * size / 16 + 2;  // vectors of a row, wherever it begins
+    int cluster = 1;
+    while (cluster < kLMaxCluster && ((n * cluster * 2 <= 2 * int64_t(sm_count()) && nv / (2 * cluster) >= kLThreads) ||
+                                      ceil_div<int64_t>(ceil_div<int64_t>(nv, cluster), kLThreads * kLGroup) > kLMaxTurns))
+        cluster *= 2;
+    a.slice = int32_t(ceil_div<int64_t>(nv, cluster));
+    const int64_t turns = ceil_div<int64_t>(a.slice, kLThreads * kLGroup);
+    if (turns > kLMaxTurns || n * cluster > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    const size_t smem = size_t(turns) * kLThreads * sizeof(float);
+    return dtype == CSA2_OUT_BF16 ? logprobs_launch<__nv_bfloat16>(a, n, cluster, smem, cudaStream_t(stream))
+                                  : logprobs_launch<float>(a, n, cluster, smem, cudaStream_t(stream));
+}

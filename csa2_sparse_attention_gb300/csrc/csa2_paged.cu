@@ -8,6 +8,7 @@
 
 namespace csa2 {
 
+constexpr int kTreeNodes = CSA2_TREE_NODES;  // of a request
 constexpr int kPSms = 152;  // multiprocessors the split is planned for
 constexpr int kPSlotReqs = 256;  // a request per thread of the tile kernel's block
 
@@ -176,12 +177,12 @@ struct PagedPlan {
 };
 constexpr size_t kPMaxTileBytes = size_t(4) << 30;
 constexpr int32_t kPFewRows = 256, kPFewTiles = 4;
-static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window) {
+static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window, bool tree) {
     PagedPlan p{};
     if (window >= max_kv) window = 0;
     if (max_q > n_tokens) max_q = int32_t(n_tokens);
     const int64_t rows = n_tokens * n_heads;
-    const int32_t tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256));
+    const int32_t tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256, tree));
     if (int64_t(max_q) * n_heads > kPFewRows && tile_keys > kPFewTiles) {
         int64_t span = (max_kv + kPN - 1) / kPN;
         if (window > 0) {  // from the first token's window to the last token
@@ -211,7 +212,7 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
         const int32_t q = beside ? kPFewRows / n_heads : max_q;
         p.few_rows = beside ? q * n_heads : 0;
         const int64_t most = items(q, 64), planned = beside ? n_req * paged_items(1, n_heads, 64) : most;  // single tokens
-        p.few = paged_share(planned, most, 1, n_req, paged_key_tiles(q, max_kv, window, paged_item_tokens(n_heads, 64)), 2.9,
+        p.few = paged_share(planned, most, 1, n_req, paged_key_tiles(q, max_kv, window, paged_item_tokens(n_heads, 64, tree)), 2.9,
                             beside ? double(n_req) * n_heads : double(rows));
     }
     size_t at = CSA2_STATUS_BYTES;
@@ -249,15 +250,23 @@ using namespace csa2;
 extern "C" size_t csa2_paged_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
                                                   int32_t max_kv, int window) {
     return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window)
-               ? paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window).total
+               ? paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window, false).total
                : 0;
 }
 
-extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
-                                       const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, int fmt,
-                                       const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* table,
-                                       int64_t max_pages, int page_size, int window, float sm_scale, void* out,
-                                       float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+extern "C" size_t csa2_tree_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q,
+                                                 int32_t max_kv, int window) {
+    return paged_sizes(n_tokens, n_heads, n_req, max_q, max_kv, window) && max_q <= kTreeNodes
+               ? paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window, true).total
+               : 0;
+}
+
+// Both calls; a tree's mask and positions are null for the causal one.
+static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
+                              const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, const int64_t* pos,
+                              const uint32_t* mask, int mask_words, int fmt, const uint8_t* codes, const uint8_t* scales,
+                              int64_t n_rows, const int32_t* table, int64_t max_pages, int page_size, int window,
+                              float sm_scale, void* out, float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream) {
     if (n_tokens < 0 || n_req < 0 || max_q < 0 || max_kv < 0 || window < 0 || n_rows < 0 || max_pages < 0 ||
         max_pages > INT32_MAX)
         return CSA2_ERR_INVALID_ARG;
@@ -272,7 +281,7 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
                           static_cast<const void*>(table), static_cast<const void*>(out),
                           static_cast<const void*>(out_lse)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window);
+    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window, mask != nullptr);
     if (!ws || !aligned16(ws) || ws_bytes < plan.total) return CSA2_ERR_WORKSPACE;
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
     const size_t bytes = size_t(n_tokens) * n_heads * kPD * 2;  // of the queries and of the outputs
@@ -304,6 +313,9 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
     a.by_heads = fast_div(uint32_t(n_heads));
     a.by_page = fast_div(uint32_t(page_size));
     a.sm_scale = sm_scale;
+    a.mask = mask;
+    a.pos = pos;
+    a.words = mask_words;
     char* w = static_cast<char*>(ws);
     auto share = [&](PagedArgs& b, const PagedShare& p, int32_t item, int32_t item_log2, size_t lse, size_t o) {
         b.chunk = p.chunk;
@@ -312,7 +324,7 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
         b.chunk_out = reinterpret_cast<int32_t*>(w + CSA2_STATUS_BYTES / 2) + (item == 64);
         b.item = item;
         b.item_log2 = item_log2;
-        b.item_tokens = paged_item_tokens(n_heads, item);
+        b.item_tokens = paged_item_tokens(n_heads, item, mask != nullptr);
         b.part_lse = reinterpret_cast<float*>(w + lse);
         b.part_o = reinterpret_cast<float*>(w + o);
         b.part_rows = a.rows;
@@ -350,4 +362,26 @@ extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int
         timer_end(K_PAGED_MERGE, s);
     }
     return launch_status();
+}
+
+extern "C" csa2_status csa2_paged_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
+                                       const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, int fmt,
+                                       const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* table,
+                                       int64_t max_pages, int page_size, int window, float sm_scale, void* out,
+                                       float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    return paged_call(q_bf16, n_tokens, n_heads, q_start, kv_len, n_req, max_q, max_kv, nullptr, nullptr, 0, fmt, codes, scales,
+                      n_rows, table, max_pages, page_size, window, sm_scale, out, out_lse, ws, ws_bytes, stream);
+}
+
+extern "C" csa2_status csa2_tree_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
+                                      const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv,
+                                      const int64_t* pos, const uint32_t* mask, int mask_words, int fmt,
+                                      const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* table,
+                                      int64_t max_pages, int page_size, int window, float sm_scale, void* out,
+                                      float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    if (max_q > kTreeNodes) return CSA2_ERR_UNSUPPORTED;
+    if (!pos || !mask || !aligned16(pos) || !aligned16(mask) || max_q < 0 || mask_words != ceil_div(max_q, 32))
+        return CSA2_ERR_INVALID_ARG;
+    return paged_call(q_bf16, n_tokens, n_heads, q_start, kv_len, n_req, max_q, max_kv, pos, mask, mask_words, fmt, codes, scales,
+                      n_rows, table, max_pages, page_size, window, sm_scale, out, out_lse, ws, ws_bytes, stream);
 }

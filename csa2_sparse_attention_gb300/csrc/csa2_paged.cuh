@@ -81,7 +81,31 @@ struct PagedArgs {
     int32_t tail;          // one request whose last items are split (paged_tail)
     int32_t behind;        // the few-row kernel: launched behind the tile kernel, which it does not depend on
     float sm_scale;
+    // Trees (null otherwise): a token sees the positions before its request's
+    // tokens (within the window behind its own position) and those of its
+    // request's tokens whose bit is set in its row of the mask.
+    const uint32_t* mask;  // [n_tokens][words]
+    const int64_t* pos;    // [n_tokens]; below 0: sees nothing
+    int32_t words;
 };
+
+// Bits off .. off + 31 of a mask row (0 outside of it).
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int32_t words, int32_t off) {
+    if (off <= -32 || off >= 32 * words) return 0;
+    if (off < 0) return __ldg(row) << -off;
+    const int32_t w = off >> 5;
+    const uint32_t lo = __ldg(row + w), hi = w + 1 < words ? __ldg(row + w + 1) : 0;
+    return __funnelshift_r(lo, hi, off & 31);
+}
+// Bits of the keys k .. k + 31 that lie in [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int32_t k, int32_t lo, int32_t hi) {
+    const int32_t l = lo - k, h = hi - k;
+    if (l >= 32 || h <= 0) return 0;
+    uint32_t v = 0xFFFFFFFFu;
+    if (l > 0) v &= 0xFFFFFFFFu << l;
+    if (h < 32) v &= 0xFFFFFFFFu >> (32 - h);
+    return v;
+}
 
 // A request's tokens and entries; false when it is to be skipped.  Problems
 // go to `st` when it is not null.
@@ -120,8 +144,9 @@ __host__ __device__ inline int32_t paged_key_tiles(int32_t nq, int32_t len, int3
     }
     return n;
 }
-// Tokens that an item's rows can belong to at most.
-inline int32_t paged_item_tokens(int32_t heads, int32_t item) { return (item - 1) / heads + 2; }
+// Tokens that an item's rows can belong to at most; of a tree, whose window begins
+// at its request's first token for all of them, as many as the request has.
+inline int32_t paged_item_tokens(int32_t heads, int32_t item, bool tree) { return tree ? INT32_MAX : (item - 1) / heads + 2; }
 __device__ __forceinline__ int32_t paged_splits(int32_t tiles, int32_t chunk) {
     if (tiles <= chunk) return 1;
     int32_t n = int32_t(__fdividef(float(tiles), float(chunk)));  // 32 at most, so off by one at most
@@ -162,7 +187,8 @@ __device__ __forceinline__ void paged_item_keys(const PagedArgs& a, const PagedR
                                                 int32_t& end, int32_t& tiles) {
     const int32_t rows = rq.nq * a.heads, r0 = ti * a.item, r1 = (r0 + a.item < rows ? r0 + a.item : rows) - 1;
     end = rq.len - rq.nq + r1 / a.by_heads + 1;
-    int32_t lo = a.window > 0 ? rq.len - rq.nq + r0 / a.by_heads + 1 - a.window : 0;
+    // (a tree's later tokens may lie as far up as its first one)
+    int32_t lo = a.window > 0 ? rq.len - rq.nq + (a.mask != nullptr ? 0 : r0 / a.by_heads) + 1 - a.window : 0;
     if (lo < 0) lo = 0;
     begin = lo & ~7;
     if (a.tiles != nullptr) {

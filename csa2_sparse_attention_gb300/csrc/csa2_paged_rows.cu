@@ -53,6 +53,8 @@ struct PagedRowsSmem {
     int2 keys[kRRows];            // keys [x, y) that a row sees
     float alpha[kRRows], delta[kRRows];
     float red[4][kRRows];
+    uint32_t see[4][kRRows];      // trees: of a tile, the keys that a row sees, 32 a word
+    int tok[kRRows];              // a row's token, -1 where it sees nothing
     int fresh;                    // rows that have seen no key yet
     PagedFlags flags[2][2];       // of a tile, by each team of producers
     uint64_t full[2], empty[4], s_full, p_full, o_done, drain;  // full: of each half of the channels
@@ -92,7 +94,7 @@ __device__ __forceinline__ float over_lanes(float (&v)[32]) {
 
 // grid: one CTA per (64 rows of a request, split), the ones with the most keys
 // first; CTAs beyond the last one leave at once.
-template <bool FP8>
+template <bool FP8, bool TREE>
 __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     PagedRowsSmem& S = *reinterpret_cast<PagedRowsSmem*>(smem_raw);
@@ -144,7 +146,14 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             S.row[row] = make_float2(paged_q_scale(a, qs), 0.f);
             // rows behind the last one see nothing
             const int32_t hi = on ? rq.len - rq.nq + (row0 + row) / a.by_heads + 1 : 0;
-            S.keys[row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);
+            if (TREE) {  // the positions before the request's tokens
+                const int32_t tok = on ? rq.q0 + (row0 + row) / a.by_heads : 0;
+                const int64_t p = on ? __ldg(a.pos + tok) : -1;
+                S.tok[row] = p >= 0 ? tok : -1;
+                S.keys[row] = make_int2(a.window > 0 ? int32_t(p < hi - 1 ? p : hi - 1) + 1 - a.window : 0, p >= 0 ? rq.len - rq.nq : 0);
+            } else {
+                S.keys[row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);
+            }
             if (row == 0) S.fresh = n_row;
         }
         uint8_t* dst = S.q + (row >> 3) * 8192 + piece * 256 + (row & 7) * 16;
@@ -163,6 +172,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
 #pragma unroll
         for (int c = 0; c < kRRows; ++c) l[c] = 0.f;
         bool ok = true;
+        const int32_t first = rq.len - rq.nq;  // the request's first token
+        const bool blind = TREE && soft_or(tid < n_row && S.tok[tid] < 0);
         for (int32_t j = 0; j < nt; ++j) {
             ok = soft_and(mbar_wait(&S.s_full, j & 1, a.wlim));
             if (!ok) break;
@@ -185,10 +196,41 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             const PagedFlags *f = S.flags[j & 1];
             const bool hidden = (f[0].hidden[tid >> 4] >> (tid & 15)) & 1;
             const bool nan = ((f[0].nan[tid >> 4] | f[1].nan[tid >> 4]) >> (tid & 15)) & 1;
+            if (TREE) {
+                // tiles behind the first token, or where a window can begin (a token lies no further down than its place)
+                const int32_t t0 = key0 + j * kPN;
+                const bool part = blind || t0 + kPN > first || (a.window > 0 && t0 < k_end - a.window);
+                if (part) {  // (the last tile's bits were read before this tile's first barrier)
+                    const int row = tid >> 1;
+                    const int2 k = S.keys[row];
+                    const int tok = S.tok[row];
+#pragma unroll
+                    for (int w = 2 * (tid & 1); w < 2 * (tid & 1) + 2; ++w) {
+                        uint32_t v = range_bits(t0 + 32 * w, k.x, k.y);
+                        if (tok >= 0) v |= tree_bits(a.mask + int64_t(tok) * a.words, a.words, t0 + 32 * w - first);
+                        S.see[w][row] = v;
+                    }
+                    soft_sync();
+                }
+                if (part || __any_sync(0xffffffffu, hidden || nan)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const uint4 v = part ? *reinterpret_cast<const uint4*>(&S.see[warp][32 * h + c]) : make_uint4(~0u, ~0u, ~0u, ~0u);
+                            const uint32_t see[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (nan) x[h][c + e] = __uint_as_float(0x7FC00000u);
+                                if (hidden || !((see[e] >> lane) & 1u)) x[h][c + e] = -INFINITY;
+                            }
+                        }
+                }
+            }
             // the rows' key ranges are ordered: the first row's end and the last one's start bound all of them (what a row
             // behind the last one sees is of no account)
-            const bool inside = key < S.keys[0].y && key >= S.keys[n_row - 1].x;
-            if (__any_sync(0xffffffffu, hidden || nan || !inside)) {
+            const bool inside = TREE || (key < S.keys[0].y && key >= S.keys[n_row - 1].x);
+            if (!TREE && __any_sync(0xffffffffu, hidden || nan || !inside)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -523,7 +565,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     if (a.behind) grid_dep_wait();
 }
 
-template <bool FP8>
+template <bool FP8, bool TREE>
 static csa2_status rows_launch(const PagedArgs& a, unsigned grid, cudaStream_t s) {
     // once per device: the shared memory opt-in, and the register count that the kernel's split of them is made for
     static std::atomic<bool> done[64] = {};
@@ -531,20 +573,21 @@ static csa2_status rows_launch(const PagedArgs& a, unsigned grid, cudaStream_t s
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
         cudaFuncAttributes at;
-        if (cudaFuncGetAttributes(&at, paged_rows_kernel<FP8>) != cudaSuccess || at.numRegs != kRLaunchRegs ||
-            cudaFuncSetAttribute(paged_rows_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncGetAttributes(&at, paged_rows_kernel<FP8, TREE>) != cudaSuccess || at.numRegs != kRLaunchRegs ||
+            cudaFuncSetAttribute(paged_rows_kernel<FP8, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(sizeof(PagedRowsSmem))) != cudaSuccess)
             return CSA2_ERR_CUDA;
         done[dev].store(true, std::memory_order_release);
     }
     timer_begin(K_PAGED_ATTN, s);
-    const cudaError_t e = launch(paged_rows_kernel<FP8>, dim3(grid), kRThreads, sizeof(PagedRowsSmem), s, 1, a);
+    const cudaError_t e = launch(paged_rows_kernel<FP8, TREE>, dim3(grid), kRThreads, sizeof(PagedRowsSmem), s, 1, a);
     timer_end(K_PAGED_ATTN, s);
     return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
 
 csa2_status paged_rows_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
-    return fp8 ? rows_launch<true>(a, grid, s) : rows_launch<false>(a, grid, s);
+    if (a.mask != nullptr) return fp8 ? rows_launch<true, true>(a, grid, s) : rows_launch<false, true>(a, grid, s);
+    return fp8 ? rows_launch<true, false>(a, grid, s) : rows_launch<false, false>(a, grid, s);
 }
 
 }  // namespace csa2

@@ -82,6 +82,7 @@ static_assert(kPM * (kPHalf * 4 + 16) <= 2 * kPN * kPHalf * 2 + kPM * kPN * 2, "
 
 // grid: 4 CTAs (two output halves, two row tiles) per (pair of row tiles, split),
 // the ones with the most keys first; CTAs beyond the last one leave at once.
+template <bool TREE>
 __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const PagedArgs a) {
     constexpr int kMmaWarp = kPSoftWarps, kCopyWarp = kPSoftWarps + 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -199,10 +200,19 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
         }
 
         // ---- key tiles
-        int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys
+        int32_t lo_r = 0, hi_r = INT32_MAX;  // the row's keys (of a tree, those before the request's tokens)
+        const uint32_t* mask = nullptr;
         if (row_on) {
-            hi_r = rq.len - rq.nq + (ti * kPM + row) / a.by_heads + 1;
-            lo_r = a.window > 0 ? hi_r - a.window : 0;
+            const int32_t at = (ti * kPM + row) / a.by_heads;
+            hi_r = rq.len - rq.nq + at + 1;
+            if (TREE) {
+                const int64_t p = __ldg(a.pos + rq.q0 + at);
+                if (p >= 0) mask = a.mask + int64_t(rq.q0 + at) * a.words;
+                lo_r = a.window > 0 ? int32_t(p < hi_r - 1 ? p : hi_r - 1) + 1 - a.window : 0;
+                hi_r = p >= 0 ? rq.len - rq.nq : 0;
+            } else {
+                lo_r = a.window > 0 ? hi_r - a.window : 0;
+            }
         }
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -238,14 +248,12 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
             const uint32_t hidden[4] = {hid.x, hid.y, hid.z, hid.w}, nan[4] = {n4.x, n4.y, n4.z, n4.w};
             if (__any_sync(0xffffffffu, c0 < lo_r || c0 + kPN > hi_r) ||
                 (hidden[0] | hidden[1] | hidden[2] | hidden[3] | nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
-                const int32_t lo = lo_r - c0, hi = hi_r - c0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    // bits of the block's columns in [lo, hi) that have a page
-                    const int32_t l0 = lo - 32 * b, h0 = hi - 32 * b;
-                    uint32_t see = l0 >= 32 || h0 <= 0 ? 0u : ~hidden[b];
-                    if (l0 > 0 && l0 < 32) see &= 0xFFFFFFFFu << l0;
-                    if (h0 > 0 && h0 < 32) see &= 0xFFFFFFFFu >> (32 - h0);
+                    // bits of the block's columns that the row sees and that have a page
+                    uint32_t see = range_bits(c0 + 32 * b, lo_r, hi_r);
+                    if (TREE && mask != nullptr) see |= tree_bits(mask, a.words, c0 + 32 * b - (rq.len - rq.nq));
+                    see &= ~hidden[b];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         if ((nan[b] >> i) & 1u) s[b][i] = 0x7FC00000u;
@@ -557,12 +565,13 @@ __global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
     }
 }
 
-csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
+template <bool TREE>
+static csa2_status tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
     static std::atomic<bool> done[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(paged_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_tiles_kernel<TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(sizeof(PagedTilesSmem))) != cudaSuccess)
             return CSA2_ERR_CUDA;
         done[dev].store(true, std::memory_order_release);
@@ -574,9 +583,13 @@ csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cuda
     timer_end(K_PAGED_DECODE, s);
     if (e1 != cudaSuccess) return CSA2_ERR_CUDA;
     timer_begin(K_PAGED_ATTN, s);
-    const cudaError_t e2 = launch(paged_tiles_kernel, dim3(grid), kPTileThreads, sizeof(PagedTilesSmem), s, 1, a);
+    const cudaError_t e2 = launch(paged_tiles_kernel<TREE>, dim3(grid), kPTileThreads, sizeof(PagedTilesSmem), s, 1, a);
     timer_end(K_PAGED_ATTN, s);
     return e2 == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+csa2_status paged_tiles_launch(const PagedArgs& a, bool fp8, unsigned grid, cudaStream_t s) {
+    return a.mask != nullptr ? tiles_launch<true>(a, fp8, grid, s) : tiles_launch<false>(a, fp8, grid, s);
 }
 
 }  // namespace csa2

@@ -22,7 +22,11 @@ enum KernelId {
     K_RMSNORM = 12,
     K_MATVEC = 13,
     K_PAGED_DECODE = 14,
-    K_COUNT = 15
+    K_HEAD = 15,
+    K_TREE_PLAN = 16,
+    K_LOGPROBS = 17,
+    K_TREE_COMMIT = 18,
+    K_COUNT = 19
 };
 
 void timer_begin(int id, cudaStream_t s);

@@ -1,0 +1,315 @@
+// Trees of drafted tokens: positions and ancestor masks before a step, and the
+// commit of the accepted path after it.
+#include "csa2_common.cuh"
+#include "csa2_timer.cuh"
+
+namespace csa2 {
+
+constexpr int kTreeMost = CSA2_TREE_NODES;  // nodes of a request
+constexpr int kTreeThreads = 128;
+
+// A request's nodes [q0, q0 + nq) and the position of the first one; nq is 0
+// where it has none, or a bound does not hold (recorded).
+struct TreeReq {
+    int32_t q0, nq, first, len;
+    bool good;
+};
+__device__ __forceinline__ TreeReq tree_request(const int32_t* q_start, const int32_t* kv_len, int64_t r, int64_t n_tokens,
+                                                int32_t max_q, int64_t max_len, Status* st) {
+    TreeReq o;
+    o.q0 = q_start[r];
+    const int32_t q1 = q_start[r + 1];
+    o.len = kv_len[r];
+    o.nq = q1 - o.q0;
+    o.first = o.len - o.nq;
+    o.good = o.q0 >= 0 && q1 >= o.q0 && q1 <= n_tokens && o.nq <= max_q;
+    if (!o.good) o.nq = 0;
+    if (o.good && (o.len < o.nq || o.len > max_len)) o.good = false;
+    if (!o.good && threadIdx.x == 0) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_LENGTH, int32_t(r), o.nq == 0 ? q1 : o.len);
+    return o;
+}
+
+// Positions and masks: a block per request, a thread per node that walks up to
+// the root, first to its depth, then along the part inside the window.  Ancestors
+// come in falling order, so a word of the mask is finished when the walk leaves it
+// and goes out once.
+__global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const int32_t* __restrict__ parent,
+                                                                 const int32_t* __restrict__ q_start,
+                                                                 const int32_t* __restrict__ kv_len, int64_t n_tokens,
+                                                                 int32_t max_q, int32_t window, int64_t* __restrict__ pos,
+                                                                 uint32_t* __restrict__ mask, int32_t words, Status* st) {
+    __shared__ int16_t up[kTreeMost];  // -2: not an earlier node
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t r = blockIdx.x;
+    const TreeReq t = tree_request(q_start, kv_len, r, n_tokens, max_q, INT32_MAX, st);
+    for (int i = threadIdx.x; i < t.nq; i += kTreeThreads) {
+        const int32_t p = parent[t.q0 + i];
+        const bool ok = p >= -1 && p < i;
+        if (!ok) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, p);
+        up[i] = ok && t.good ? int16_t(p) : int16_t(-2);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < t.nq; i += kTreeThreads) {
+        int depth = -1, at = i;
+        while (at >= 0) at = up[at], ++depth;
+        const bool lost = at == -2;  // sees nothing
+        pos[t.q0 + i] = lost ? -1 : int64_t(t.first) + depth;
+        uint32_t* row = mask + int64_t(t.q0 + i) * words;
+        const int lowest = lost ? INT32_MAX : window > 0 && depth >= window ? window : depth + 1;  // nodes to set
+        int w = words - 1, left = lost ? 0 : lowest;
+        uint32_t bits = 0;
+        for (at = i; left > 0; --left, at = up[at]) {
+            while (w > (at >> 5)) row[w--] = bits, bits = 0;
+            bits |= 1u << (at & 31);
+        }
+        while (w >= 0) row[w--] = bits, bits = 0;
+    }
+}
+
+struct CommitArgs {
+    const int32_t* parent;
+    const int64_t* token;
+    const int64_t* choice;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    uint8_t* codes;
+    uint8_t* scales;
+    const int32_t* table;
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* n_free_out;
+    int32_t* cached;
+    int32_t* path;
+    int32_t* accepted;
+    int64_t* next;
+    Status* st;
+    unsigned* ticket;
+    int64_t n_req, n_tokens, row_pages, max_pages, n_pages;
+    int32_t max_q, page, code_chunks, chunks;  // 16-byte chunks of a row's codes, and of codes and scales
+};
+
+constexpr int kCommitRows = 32, kCommitHeld = 8;  // rows moved at a time; chunks that a thread holds of them
+
+__device__ __forceinline__ int64_t commit_pages(int64_t n, int page) { return (n + page - 1) / page; }
+
+// A block per request.  Every node looks whether it continues its parent: the
+// lowest one that does is kept in shared memory, so the path is a walk of a few
+// dependent shared loads.  Its rows move down by batches, all of a batch loaded
+// before any is stored: node path[j] >= j, so what a batch stores no later batch
+// loads.  The last block to come by gives the pages back, in the order that undoes
+// the plan's taking.
+__global__ void __launch_bounds__(kTreeThreads) tree_commit_kernel(const CommitArgs a) {
+    __shared__ int32_t best[kTreeMost];
+    __shared__ int16_t path[kTreeMost];
+    __shared__ int64_t src[kCommitRows], dst[kCommitRows];
+    __shared__ int64_t sums[2][kTreeThreads / 32];
+    __shared__ int s_len;
+    __shared__ bool last;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int64_t r = blockIdx.x;
+    const TreeReq t = tree_request(a.q_start, a.kv_len, r, a.n_tokens, a.max_q, a.max_pages * a.page, a.st);
+    for (int i = tid; i < t.nq; i += kTreeThreads) best[i] = INT32_MAX;
+    __syncthreads();
+    if (t.good) {
+        for (int i = tid; i < t.nq; i += kTreeThreads) {
+            const int32_t p = a.parent[t.q0 + i];
+            if (p < -1 || p >= i) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, p);
+            else if (p >= 0 && a.token[t.q0 + i] == a.choice[t.q0 + p]) atomicMin(&best[p], i);
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int n = 0;
+        if (t.good && t.nq > 0 && a.parent[t.q0] == -1)
+            for (int32_t at = 0; at != INT32_MAX; at = best[at]) path[n++] = int16_t(at);
+        s_len = n;
+        a.accepted[r] = n;
+        a.next[r] = n > 0 ? a.choice[t.q0 + path[n - 1]] : -1;
+        if (t.good && t.nq > 0) a.cached[r] = t.first + n;
+    }
+    __syncthreads();
+    const int len = s_len;
+    for (int i = tid; i < t.nq; i += kTreeThreads) a.path[t.q0 + i] = i < len ? path[i] : -1;
+    // ---- rows, from the first one that moves
+    if (a.codes != nullptr) {
+        int j0 = 0;
+        while (j0 < len && path[j0] == j0) ++j0;
+        for (; j0 < len; j0 += kCommitRows) {
+            const int n = len - j0 < kCommitRows ? len - j0 : kCommitRows;
+            if (tid < 2 * n) {  // rows of the cache, -1 where a page is none
+                const int j = j0 + (tid >> 1);
+                const int32_t p = t.first + (tid & 1 ? path[j] : j);
+                const int32_t page = p / a.page, id = a.table[r * a.max_pages + page];
+                const bool ok = id >= 0 && id < a.row_pages;
+                if (!ok) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(r), id);
+                (tid & 1 ? src : dst)[tid >> 1] = ok ? int64_t(id) * a.page + (p - page * a.page) : -1;
+            }
+            __syncthreads();
+            uint4 v[kCommitHeld];
+            auto place = [&](int i, const int64_t* rows) -> uint4* {
+                const int j = i / a.chunks, c = i - j * a.chunks;
+                return c < a.code_chunks ? reinterpret_cast<uint4*>(a.codes) + rows[j] * a.code_chunks + c
+                                         : reinterpret_cast<uint4*>(a.scales) + rows[j] * (a.chunks - a.code_chunks) + c - a.code_chunks;
+            };
+            auto moved = [&](int i) { return i < n * a.chunks && src[i / a.chunks] >= 0 && dst[i / a.chunks] >= 0; };
+#pragma unroll
+            for (int k = 0; k < kCommitHeld; ++k) {
+                const int i = tid + k * kTreeThreads;
+                if (moved(i)) v[k] = *place(i, src);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kCommitHeld; ++k) {
+                const int i = tid + k * kTreeThreads;
+                if (moved(i)) *place(i, dst) = v[k];
+            }
+            __syncthreads();
+        }
+    }
+    // ---- pages, by the last block
+    if (tid == 0) {
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+        if (last) *a.ticket = 0;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const int64_t have = *a.n_free;
+    int64_t total = 0, base = 0;
+    for (int pass = 0; pass < 2; ++pass) {  // how many there are, then each one's place
+        for (int64_t r0 = 0; r0 < a.n_req; r0 += kTreeThreads) {
+            const int64_t q = r0 + tid;
+            int64_t from = 0, to = 0, mine = 0;
+            if (q < a.n_req) {
+                const int32_t q0 = a.q_start[q], q1 = a.q_start[q + 1], kv = a.kv_len[q];
+                const bool good = q0 >= 0 && q1 > q0 && q1 <= a.n_tokens && q1 - q0 <= a.max_q && kv >= q1 - q0 && kv <= a.max_pages * a.page;
+                if (good) from = commit_pages(kv - (q1 - q0) + __ldcg(a.accepted + q), a.page), to = commit_pages(kv, a.page);
+                for (int64_t j = from; j < to; ++j) {
+                    const int32_t id = a.table[q * a.max_pages + j];
+                    if (id >= 0 && id < a.n_pages) ++mine;
+                    else if (pass == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(q), id);
+                }
+            }
+            int64_t inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            if (lane == 31) sums[0][warp] = inc;
+            __syncthreads();
+            int64_t before = 0, all = 0;
+            for (int w = 0; w < kTreeThreads / 32; ++w) {
+                if (w < warp) before += sums[0][w];
+                all += sums[0][w];
+            }
+            __syncthreads();
+            if (pass == 0) {
+                total += all;
+            } else {
+                int64_t at = have + total - 1 - (base + before + inc - mine);
+                for (int64_t j = from; j < to; ++j) {
+                    const int32_t id = a.table[q * a.max_pages + j];
+                    if (id >= 0 && id < a.n_pages) a.free_pages[at--] = id;
+                }
+                base += all;
+            }
+        }
+        if (have < 0 || have + total > a.n_pages) {  // a free list that has no room for them: nothing goes back
+            if (tid == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_CAPACITY, 2, int32_t(have));
+            total = 0;
+            break;
+        }
+    }
+    if (tid == 0) *a.n_free_out = int32_t(have + total);
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" csa2_status csa2_tree_plan(const int32_t* parent, const int32_t* q_start, const int32_t* kv_len, int64_t n_req,
+                                      int64_t n_tokens, int32_t max_q, int window, int64_t* pos, uint32_t* mask, int mask_words,
+                                      void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    if (n_req < 0 || n_tokens < 0 || max_q < 0 || window < 0) return CSA2_ERR_INVALID_ARG;
+    if (n_req > (1 << 20) || n_tokens > (1 << 22) || max_q > kTreeMost) return CSA2_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+    if (!parent || !q_start || !kv_len || !pos || !mask || mask_words != ceil_div(max_q, 32)) return CSA2_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(q_start), static_cast<const void*>(kv_len),
+                          static_cast<const void*>(pos), static_cast<const void*>(mask)})
+        if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    const int64_t nm = n_tokens * mask_words * 4;
+    if (overlap(pos, 8 * n_tokens, parent, 4 * n_tokens) || overlap(mask, nm, parent, 4 * n_tokens) || overlap(mask, nm, pos, 8 * n_tokens))
+        return CSA2_ERR_INVALID_ARG;
+    if (n_req == 0 || n_tokens == 0 || max_q == 0) return CSA2_OK;
+    cudaStream_t s = cudaStream_t(stream);
+    timer_begin(K_TREE_PLAN, s);
+    launch(tree_plan_kernel, dim3(unsigned(n_req)), kTreeThreads, 0, s, 1, parent, q_start, kv_len, n_tokens, max_q, window, pos, mask,
+           mask_words, static_cast<Status*>(ws));
+    timer_end(K_TREE_PLAN, s);
+    return launch_status();
+}
+
+extern "C" csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* token, const int64_t* choice, const int32_t* q_start,
+                                        const int32_t* kv_len, int64_t n_req, int64_t n_tokens, int32_t max_q, int fmt,
+                                        uint8_t* codes, uint8_t* scales, int64_t n_rows, const int32_t* table, int64_t max_pages,
+                                        int page_size, int32_t* free_pages, int64_t n_pages, const int32_t* n_free,
+                                        int32_t* n_free_out, int32_t* cached, int32_t* path, int32_t* accepted, int64_t* next,
+                                        void* ws, size_t ws_bytes, csa2_stream_t stream) {
+    if (n_req < 0 || n_tokens < 0 || max_q < 0 || n_rows < 0 || max_pages < 0 || max_pages > INT32_MAX || n_pages < 0 ||
+        n_pages > INT32_MAX)
+        return CSA2_ERR_INVALID_ARG;
+    if (n_req > (1 << 20) || n_tokens > (1 << 22) || max_q > kTreeMost) return CSA2_ERR_UNSUPPORTED;
+    if (page_size < 8 || page_size > 65536 || page_size % 8) return CSA2_ERR_UNSUPPORTED;
+    if (codes && fmt != CSA2_FMT_FP4 && fmt != CSA2_FMT_FP8) return CSA2_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+    if (codes ? (fmt == CSA2_FMT_FP4) != (scales != nullptr) : scales != nullptr) return CSA2_ERR_INVALID_ARG;
+    if (!parent || !token || !choice || !q_start || !kv_len || !table || !free_pages || !n_free || !n_free_out || !cached || !path ||
+        !accepted || !next)
+        return CSA2_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(token), static_cast<const void*>(choice),
+                          static_cast<const void*>(q_start), static_cast<const void*>(kv_len), static_cast<const void*>(codes),
+                          static_cast<const void*>(scales), static_cast<const void*>(table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(cached), static_cast<const void*>(path), static_cast<const void*>(accepted),
+                          static_cast<const void*>(next)})
+        if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    // (every block reads lengths after others have written theirs)
+    if (cached == kv_len || accepted == kv_len || cached == accepted) return CSA2_ERR_INVALID_ARG;
+    if (n_req == 0) return CSA2_OK;
+    CommitArgs a{};
+    a.parent = parent;
+    a.token = token;
+    a.choice = choice;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.codes = codes;
+    a.scales = scales;
+    a.table = table;
+    a.free_pages = free_pages;
+    a.n_free = n_free;
+    a.n_free_out = n_free_out;
+    a.cached = cached;
+    a.path = path;
+    a.accepted = accepted;
+    a.next = next;
+    a.st = static_cast<Status*>(ws);
+    a.ticket = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + 64);
+    a.n_req = n_req;
+    a.n_tokens = n_tokens;
+    a.row_pages = n_rows / page_size;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.max_q = max_q;
+    a.page = page_size;
+    a.code_chunks = fmt == CSA2_FMT_FP4 ? 16 : 32;
+    a.chunks = fmt == CSA2_FMT_FP4 ? 18 : 32;
+    cudaStream_t s = cudaStream_t(stream);
+    timer_begin(K_TREE_COMMIT, s);
+    launch(tree_commit_kernel, dim3(unsigned(n_req)), kTreeThreads, 0, s, 1, a);
+    timer_end(K_TREE_COMMIT, s);
+    return launch_status();
+}

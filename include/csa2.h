@@ -67,6 +67,8 @@ enum {
 #define CSA2_LATENT_DIM 512   /* shared main latent (K = V)                 */
 #define CSA2_BLOCK 8          /* positions per pool block                   */
 #define CSA2_STATUS_BYTES 256 /* status area at the start of every ws       */
+#define CSA2_TREE_NODES 1024  /* nodes of a request's tree                  */
+#define CSA2_LOGPROBS_TOP 64  /* alternatives, and given tokens, of a row   */
 
 /* Formats and layouts for csa2_quantize_append. */
 enum { CSA2_FMT_FP4 = 0, CSA2_FMT_FP8 = 1 };
@@ -447,13 +449,165 @@ csa2_status csa2_fp4_matvec(const void* x, int x_fmt, const float* x_scales, int
                             int out_dtype, void* ws, size_t ws_bytes, csa2_stream_t stream);
 
 /*
+ * Norms of every head's query and of the latents, turned by their positions
+ * and stored, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (without a weight: y = x), then
+ *   pairs (2i, 2i+1) turned by pos * theta^(-2i/512) where a table is given.
+ *   q_bf16       [n] rows of n_heads x 512, q_stride elements apart (>=
+ *                n_heads * 512, a multiple of 8); n_heads 1..128; n up to 2^22.
+ *   q_weight     [512] bf16, of every head; NULL: no norm.
+ *   q_out        [n][n_heads][512] bf16, rounded once from fp32; q_bf16 itself
+ *                where its rows stand close together, or apart from it.
+ *   latents      [n] rows of 512 bf16, lat_stride elements apart; lat_weight as
+ *                q_weight.  They go to cache rows dst_row[i] (NULL: row i) of
+ *                dst_codes / dst_scales in CSA2_LAYOUT_ROWS, in the form `fmt`
+ *                (see csa2_quantize_append): nearest codes of y in 64-bit
+ *                arithmetic.  A group of 16 with NaN or infinity gets a scale
+ *                of NaN (FP4); E4M3 keeps NaN and takes infinities to 448.
+ *   pos          [n] int64, or NULL without a table.  rope_table as in
+ *                csa2_quantize_append (theta and positions are the table's), or
+ *                NULL: nothing is turned.
+ *   Queries or latents may be NULL (with their weight and outputs): only the
+ *   other ones are done then.
+ * A token of position -1 (behind a padded step's last one) is left out, its
+ * q_out and cache row stay as they are; so does a latent of dst_row -1.  Other
+ * positions outside [0, rope_max_pos) (below 0 without a table) and rows outside
+ * [0, n_rows) are left out and recorded.  Sums of squares are fp32: |x| up to
+ * 2^56, and where eps is 0 rows of 2^-60 and more (a row of zeros stays one).
+ * What is written lies apart from what is read.  ws: CSA2_STATUS_BYTES bytes.
+ */
+csa2_status csa2_head_norm_rope(const void* q_bf16, int64_t q_stride, int n_heads, const void* q_weight, void* q_out,
+                                const void* latents, int64_t lat_stride, const void* lat_weight, int64_t n, float eps,
+                                const int64_t* pos, const void* rope_table, int64_t rope_max_pos, int fmt,
+                                const int64_t* dst_row, int64_t n_rows, uint8_t* dst_codes, uint8_t* dst_scales, void* ws,
+                                size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * ---- Steps whose new tokens are trees of drafted ones ----
+ *
+ * A request's tokens of the step are the nodes of a tree, in an order that puts
+ * a parent before its children: parent[q_start[r] + i] is the place of node i's
+ * parent among the request's nodes (below i), or -1 for one that continues the
+ * cached entries.  (A chain, parent i - 1, is an ordinary chunk.)  Node i's
+ * latent is entry kv_len - nodes + i of its request, csa2_page_plan's slot; its
+ * position is that of the first node plus its depth:
+ *   csa2_page_plan, csa2_tree_plan   slots; positions and masks
+ *   csa2_head_norm_rope or csa2_quantize_append   by those positions
+ *   csa2_tree_attn                   in every layer
+ *   csa2_token_logprobs              the model's choice after every node
+ *   csa2_tree_commit                 what was accepted stays
+ * Requests bring up to 1024 nodes.
+ *
+ * csa2_tree_plan:
+ *   parent       [n_tokens] int32; q_start, kv_len as csa2_page_plan gives them;
+ *                max_q: host upper bound of a request's nodes (up to 1024).
+ *   pos          [n_tokens] int64 out: kv_len - nodes + depth.
+ *   mask         [n_tokens][mask_words] 32-bit words out, mask_words =
+ *                ceil(max_q / 32): bit j of node i's row (word j / 32, bit j %
+ *                32) is set where j is i or an ancestor of it and, with a window,
+ *                lies fewer than `window` levels above it.
+ * A node whose parent is none of the earlier ones is recorded; it and what
+ * descends from it get pos = -1 and an empty mask, and see nothing.  A request
+ * whose kv_len is below its nodes is recorded, and all its nodes get that; one
+ * whose tokens lie outside [0, n_tokens) or exceed max_q is recorded and skipped.
+ * Tokens behind q_start[n_req] are left as they are.  ws: CSA2_STATUS_BYTES.
+ */
+csa2_status csa2_tree_plan(const int32_t* parent, const int32_t* q_start, const int32_t* kv_len, int64_t n_req,
+                           int64_t n_tokens, int32_t max_q, int window, int64_t* pos, uint32_t* mask, int mask_words,
+                           void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * csa2_paged_attn for trees: node i of request r sees
+ *   - the entries before the request's nodes, p < kv_len - nodes, with a window
+ *     those of max(0, pos + 1 - window) <= p, and
+ *   - the request's nodes whose bits its mask row has.
+ * pos and mask are csa2_tree_plan's for the same window; a node of pos below 0
+ * sees nothing.  (With other masks: bits at and behind the nodes' number, and
+ * above the node's own, are to be 0.  A pos above kv_len - nodes + i counts as
+ * that.)  Everything else, max_q up to 1024 apart, is as in csa2_paged_attn; the
+ * same chains give the same bits as there where no window is set.
+ * ws: csa2_tree_attn_workspace_bytes (0 for bad sizes) for the same sizes.
+ */
+size_t csa2_tree_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv,
+                                      int window);
+csa2_status csa2_tree_attn(const void* q_bf16, int64_t n_tokens, int n_heads, const int32_t* q_start,
+                           const int32_t* kv_len, int64_t n_req, int32_t max_q, int32_t max_kv, const int64_t* pos,
+                           const uint32_t* mask, int mask_words, int fmt, const uint8_t* codes, const uint8_t* scales,
+                           int64_t n_rows, const int32_t* table, int64_t max_pages, int page_size, int window,
+                           float sm_scale, void* out, float* out_lse, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * Rows of logits x: with m = max x, y = (x - m) * scale and S = sum e^y,
+ *   lse = m * scale + log S, entropy = log S - sum(e^y y) / S,
+ *   log probability of token t: y_t - log S.
+ *   logits       [n] rows of vocab elements, stride elements apart (>= vocab;
+ *                rows may begin anywhere), bf16 (dtype CSA2_OUT_BF16) or fp32
+ *                (CSA2_OUT_F32).  vocab 1..2^21, n up to 2^24.
+ *   scale        of the logits (one over a temperature), 2^-20..2^20.
+ *   tokens       [n][given] int64, given 0..64; logprobs [n][given] fp32 out.  A
+ *                token of -1 is none: -inf.  Others outside [0, vocab) give -inf
+ *                and are recorded.
+ *   lse, entropy [n] fp32 out, or NULL.
+ *   top          0..64 alternatives: ids [n][top] int32 and best [n][top] fp32 out,
+ *                the tokens of the largest logits and their log probabilities,
+ *                largest first, equal logits by the lower token.  A logit of -inf
+ *                is no alternative: behind the last one ids are -1, best -inf.
+ * A row of -inf alone: lse and log probabilities -inf, entropy 0.  A row with NaN
+ * or +infinity: NaN, and ids -1.  Sums are fp32.  The outputs lie apart from the
+ * logits.  ws: CSA2_STATUS_BYTES bytes.
+ */
+csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_t stride, int64_t n, int64_t vocab, float scale,
+                                const int64_t* tokens, int given, float* logprobs, float* lse, float* entropy, int top,
+                                int32_t* ids, float* best, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * The commit of a step of trees.  From each request's node 0 (whose parent is to
+ * be -1; it is the token that was sure before the step) the path goes on to the
+ * child whose token is the choice at its parent, the lowest of several, as long
+ * as there is one.
+ *   token        [n_tokens] int64, the nodes' tokens; choice [n_tokens] int64, what
+ *                the model goes on with after each node (its first alternative, or
+ *                a sample).
+ *   parent, q_start, kv_len, max_q: as in csa2_tree_plan.
+ *   codes, scales  the cache's planes (n_rows rows in the form fmt), or codes and
+ *                scales NULL: no rows are moved.  The row of the path's j-th node
+ *                goes to the request's entry kv_len - nodes + j.
+ *   table        [n_req][max_pages] int32.  Pages that hold none of the kept
+ *                entries go back to the end of free_pages [n_pages], in the order
+ *                that undoes csa2_page_plan's taking; their table entries stay.
+ *                n_free int32[1], n_free_out int32[1] (may be n_free).
+ *   cached       [n_req] int32 out: kv_len - nodes + accepted; left as it is where
+ *                a request has no nodes.  Not kv_len itself.
+ *   path         [n_tokens] int32 out: at q_start[r] + j the place of the path's
+ *                j-th node among the request's nodes, -1 behind the last one.
+ *   accepted     [n_req] int32 out: nodes of the path (0 without nodes).
+ *   next         [n_req] int64 out: the choice at the path's last node, the token
+ *                that the next step begins with; -1 where there is none.
+ * A request with bad bounds (as in csa2_tree_plan, or a kv_len beyond its table
+ * row) is recorded and keeps nothing of the step: accepted 0, no rows moved, no
+ * pages back, cached as it was.  A node with a bad parent is recorded and
+ * accepted never; without a first node of parent -1 nothing is accepted.  A page
+ * outside the cache is recorded, and its rows are not moved, or it does not go
+ * back; where the free list has no room, that is recorded and nothing goes back.
+ * The step is done once: again on the same planes it would move rows that have
+ * moved.  ws: CSA2_STATUS_BYTES bytes, zeroed once with csa2_status_reset.
+ */
+csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* token, const int64_t* choice, const int32_t* q_start,
+                             const int32_t* kv_len, int64_t n_req, int64_t n_tokens, int32_t max_q, int fmt, uint8_t* codes,
+                             uint8_t* scales, int64_t n_rows, const int32_t* table, int64_t max_pages, int page_size,
+                             int32_t* free_pages, int64_t n_pages, const int32_t* n_free, int32_t* n_free_out,
+                             int32_t* cached, int32_t* path, int32_t* accepted, int64_t* next, void* ws, size_t ws_bytes,
+                             csa2_stream_t stream);
+
+/*
  * Instrumentation (off by default; the compute path never depends on it).
  * csa2_launch_count: kernels launched through the library by this process.
  * csa2_timer_enable: bracket the next max_launches launches of kernel
  *   `kernel_id` (0 scan_blockmax, 1 select_blocks, 2 pool_score,
  *   3 select_topk, 4 attn_split (either attention kernel), 5 attn_merge, 6 quantize_fp4,
  *   7 quantize_fp8, 8 rope_table, 9 page_plan, 10 paged_attn, 11 paged_merge,
- *   12 rmsnorm_fp8, 13 fp4_matvec, 14 paged_decode) with CUDA events on their stream.  Not for
+ *   12 rmsnorm_fp8, 13 fp4_matvec, 14 paged_decode, 15 head_norm_rope, 16 tree_plan,
+ *   17 token_logprobs, 18 tree_commit) with CUDA events on their stream.  Not for
  *   use during stream capture.
  * csa2_timer_read: wait for those events, return the summed device time and
  *   the number of launches timed, and switch the timer off.
