@@ -12,10 +12,10 @@
 // and a test per group.  (Not further: sum(e^y y) against b turns into that
 // against m by sum * (b - m), which cancels for what lies above b.)
 //
-// The k largest: every group's maximum stays in shared memory.  The k-th largest
-// of the threads' maxima, found bit by bit, has k values at or above it; the few
-// groups that reach it are read again (from L2) and their values at or above it
-// ranked by counting.
+// The k largest: every group's maximum stays in shared memory.  One warp finds the
+// k-th largest of the threads' maxima to 16 bits, which k values reach; the few
+// groups that do are read again (from L2), a vector a thread, and their values that
+// do are ranked by counting.
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 
@@ -25,11 +25,12 @@
 
 namespace csa2 {
 
-constexpr int kLThreads = 512, kLWarps = kLThreads / 32;
+constexpr int kLThreads = 256, kLWarps = kLThreads / 32;
 constexpr int kLGroup = 4;         // vectors of a group
-constexpr int kLMaxTurns = 32;     // groups of a thread
+constexpr int kLMaxTurns = 64;     // groups of a thread
 constexpr int kLTop = CSA2_LOGPROBS_TOP;
 constexpr int kLCands = 1024;      // values that are ranked
+constexpr int kLHits = 512;        // groups that are read again at once
 constexpr int kLMaxCluster = 8;
 constexpr float kLFloor = -160.f;  // exponents below it are nothing in fp32
 
@@ -51,7 +52,9 @@ struct LogSmem {
     unsigned long long cand[kLCands];  // (key of the value, ~index): larger values, then lower indices, are larger
     unsigned long long list[kLTop];    // the slice's largest, in order
     float max, sum, tilt;              // of the slice: m, S, sum(e^y y)
-    int bad, listed, n_cand;
+    int bad, listed, n_cand, n_hits;
+    uint32_t keys[kLThreads], bar;     // of the threads' maxima, and the one that is reached
+    uint16_t hits[kLHits];
     float red[3][kLWarps];
     int redi[kLWarps];
     // the first block's join
@@ -203,18 +206,54 @@ template <typename T>
 __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& row, int32_t v0, int32_t v1, int turns, float mine, int k) {
     constexpr int E = RowView<T>::E;
     const int tid = threadIdx.x;
-    // the k-th largest of the threads' maxima (0 where fewer have any)
-    uint32_t bar = 0;
-    {
-        const uint32_t key = mine > -INFINITY ? float_key(mine) : 0u;
+    // the k-th largest of the threads' maxima, rounded down to 16 bits (0 where fewer have any)
+    S.keys[tid] = mine > -INFINITY ? float_key(mine) : 0u;
+    if (tid == 0) S.n_hits = S.n_cand = 0;
+    __syncthreads();
+    auto kth = [&](uint32_t bar, int from, int to) {  // its bits `from` down to `to`, by the first warp
+        if (tid < 32) {
+            uint32_t own[kLThreads / 32];
+#pragma unroll
+            for (int i = 0; i < kLThreads / 32; ++i) own[i] = S.keys[32 * i + tid];
 #pragma unroll 1
-        for (int b = 31; b >= (sizeof(T) == 2 ? 16 : 0); --b) {
-            const uint32_t up = bar | (1u << b);
-            if (__syncthreads_count(key >= up) >= k) bar = up;
+            for (int b = from; b >= to; --b) {
+                const uint32_t up = bar | (1u << b);
+                uint32_t n = 0;
+#pragma unroll
+                for (int i = 0; i < kLThreads / 32; ++i) n += own[i] >= up;
+                if (__reduce_add_sync(0xffffffffu, n) >= uint32_t(k)) bar = up;
+            }
+            if (tid == 0) S.bar = bar;
         }
-    }
+        __syncthreads();
+        return S.bar;
+    };
+    uint32_t bar = kth(0, 31, 16);
     const uint32_t low = float_key(-INFINITY) + 1;  // -inf is no alternative
     if (bar < low) bar = low;
+    for (int j = 0; j < turns; ++j)
+        if (float_key(groups[j * kLThreads + tid]) >= bar) {
+            const int at = atomicAdd(&S.n_hits, 1);
+            if (at < kLHits) S.hits[at] = uint16_t(j * kLThreads + tid);
+        }
+    __syncthreads();
+    const int n_hits = S.n_hits;
+    if (n_hits <= kLHits) {
+        for (int i = tid; i < kLGroup * n_hits; i += kLThreads) {
+            const int group = S.hits[i / kLGroup], j = group / kLThreads;
+            const int32_t v = v0 + (j * kLGroup + i % kLGroup) * kLThreads + (group - j * kLThreads);
+            if (v >= v1) continue;
+            float x[E];
+            row.values(row.load(v), x);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (float_key(x[e]) >= bar) {
+                    const int at = atomicAdd(&S.n_cand, 1);
+                    if (at < kLCands) S.cand[at] = ranked(x[e], v * E - row.head + e);
+                }
+        }
+        __syncthreads();
+    }
     // visits the values of the groups whose maximum's key is `from` or more
     auto visit = [&](uint32_t from, auto f) {
         for (int j = 0; j < turns; ++j) {
@@ -247,10 +286,13 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
         __syncthreads();
         return S.n_cand;
     };
-    int n = collect_all(static_cast<unsigned long long>(bar) << 32);
-    if (n > kLCands) {
+    int n = S.n_cand;
+    if (n_hits > kLHits || n > kLCands) {
         // Many values at the bar, as where a mask leaves less than k of a row above its own value: the ones above it, and the
         // first ones at it in the row's order.
+        __syncthreads();
+        bar = kth(bar & 0xFFFF0000u, 15, 0);
+        if (bar < low) bar = low;
         n = collect_all(static_cast<unsigned long long>(bar + 1) << 32);
         if (n < k) {
             for (int j = 0; j < turns && n < k; ++j) {
@@ -296,7 +338,7 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLThreads, 2) token_logprobs_kernel(const LogArgs a, int cluster) {
+__global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogArgs a, int cluster) {
     constexpr int E = RowView<T>::E;
     extern __shared__ __align__(16) float groups[];  // maxima of the groups, [turn][thread]
     __shared__ LogSmem S;
@@ -322,14 +364,21 @@ __global__ void __launch_bounds__(kLThreads, 2) token_logprobs_kernel(const LogA
     // ---- one pass: base, sum and tilt of a thread, its maximum, its groups' maxima
     float base = __uint_as_float(0x7FC00000u), sum = 0.f, tilt = 0.f, top = -INFINITY, sum_rest = 0.f, tilt_rest = 0.f;
     bool bad = false;
-    for (int j = 0; j < turns; ++j) {
-        uint4 v[kLGroup];
+    uint4 next[kLGroup];
+    auto fetch = [&](int j) {
 #pragma unroll
         for (int g = 0; g < kLGroup; ++g) {
             const int32_t at = v0 + (j * kLGroup + g) * kLThreads + tid;
-            v[g] = at < v1 ? row.load(at) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
-                                                            : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+            next[g] = at < v1 ? row.load(at) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                                               : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
         }
+    };
+    fetch(0);
+    for (int j = 0; j < turns; ++j) {
+        uint4 v[kLGroup];
+#pragma unroll
+        for (int g = 0; g < kLGroup; ++g) v[g] = next[g];
+        if (j + 1 < turns) fetch(j + 1);
         float m = -INFINITY;
 #pragma unroll
         for (int g = 0; g < kLGroup; ++g) {
@@ -533,7 +582,7 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
     // groups' maxima find room.
     const int64_t nv = vocab * size / 16 + 2;  // vectors of a row, wherever it begins
     int cluster = 1;
-    while (cluster < kLMaxCluster && ((n * cluster * 2 <= 2 * int64_t(sm_count()) && nv / (2 * cluster) >= kLThreads) ||
+    while (cluster < kLMaxCluster && ((n * cluster * 2 <= 4 * int64_t(sm_count()) && nv / (2 * cluster) >= kLThreads) ||
                                       ceil_div<int64_t>(ceil_div<int64_t>(nv, cluster), kLThreads * kLGroup) > kLMaxTurns))
         cluster *= 2;
     a.slice = int32_t(ceil_div<int64_t>(nv, cluster));

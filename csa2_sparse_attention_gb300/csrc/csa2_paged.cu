@@ -104,6 +104,102 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     }
 }
 
+// Joins the pieces of a tree call's items that several groups hold (WalkCut), with
+// weights 2^(lse_p - max lse) over the pieces' normalized outputs.  Up to four
+// pieces (shares): a warp a row, eight rows at a time.  More (few items, cut up): two
+// rows at a time, 128 threads each, eight pieces' loads under way.  (By warps, the
+// 34 pieces of 4 items took 29 us; two rows at a time, the 150 pairs of 16 x 8
+// nodes x 64 heads over 8K 9 us more than by warps.)  Every block looks up all cuts
+// (152 at most) and takes its part of what there is to do: blocks for every group
+// and row would mostly find nothing.
+__global__ void __launch_bounds__(256) paged_walk_merge_kernel(const PagedArgs a) {
+    __shared__ int32_t s_end[256], s_warp[8];  // tasks of the cuts up to and with each
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, t = tid & 127, lane = lane_id(), warp = tid >> 5;
+    int32_t inc = 0;
+    if (tid + 1 < a.groups) {
+        const WalkCut& cut = a.cuts[tid + 1];
+        inc = cut.pieces > 4 ? (cut.rows + 1) / 2 : cut.pieces > 0 ? (cut.rows + 7) / 8 : 0;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    for (int v = 0; v < warp; ++v) inc += s_warp[v];
+    s_end[tid] = inc;
+    __syncthreads();
+    for (int32_t task = blockIdx.x; task < s_end[255]; task += gridDim.x) {
+        int c = 0;  // the first cut that ends behind the task
+#pragma unroll
+        for (int step = 128; step; step >>= 1)
+            if (s_end[c + step - 1] <= task) c += step;
+        const WalkCut cut = a.cuts[c + 1];
+        const int32_t nth = task - (c ? s_end[c - 1] : 0);
+        const int32_t row = cut.pieces > 4 ? 2 * nth + (tid >> 7) : 8 * nth + warp;
+        if (row >= cut.rows) continue;
+        auto at = [&](int32_t p) { return (2 * (c + p) + (p == 0 ? cut.slot : 0)) * int64_t(a.item) + row; };
+        float m = -INFINITY, sum = 0.f;
+        for (int32_t p = lane; p < cut.pieces; p += 32) m = fmaxf(m, a.part_lse[at(p)]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        auto store = [&](int q, float4 o, float inv) {  // channels 4 q ..
+            const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+            reinterpret_cast<uint2*>(a.out + (cut.out0 + row) * kPD * 2)[q] =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        };
+        if (cut.pieces <= 4) {
+            const float l = lane < cut.pieces ? a.part_lse[at(lane)] : -INFINITY, w = l == -INFINITY ? 0.f : ex2(l - m);
+            float f[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) f[p] = __shfl_sync(0xffffffffu, w, p);
+            sum = (f[0] + f[1]) + (f[2] + f[3]);
+            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll 1
+            for (int q = lane; q < kPD / 4; q += 64) {
+                float4 v[4][2];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        v[p][e] = p < cut.pieces ? reinterpret_cast<const float4*>(a.part_o + at(p) * kPD)[q + 32 * e]
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        o.x = fmaf(f[p], v[p][e].x, o.x), o.y = fmaf(f[p], v[p][e].y, o.y), o.z = fmaf(f[p], v[p][e].z, o.z),
+                        o.w = fmaf(f[p], v[p][e].w, o.w);
+                    store(q + 32 * e, o, inv);
+                }
+            }
+            if (a.lse && lane == 0) a.lse[cut.out0 + row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            continue;
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int32_t p0 = 0; p0 < cut.pieces; p0 += 8) {
+            const float l = lane < 8 && p0 + lane < cut.pieces ? a.part_lse[at(p0 + lane)] : -INFINITY, w = l == -INFINITY ? 0.f : ex2(l - m);
+            float4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                v[p] = p0 + p < cut.pieces ? reinterpret_cast<const float4*>(a.part_o + at(p0 + p) * kPD)[t] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const float f = __shfl_sync(0xffffffffu, w, p);
+                sum += f;
+                o.x = fmaf(f, v[p].x, o.x), o.y = fmaf(f, v[p].y, o.y), o.z = fmaf(f, v[p].z, o.z), o.w = fmaf(f, v[p].w, o.w);
+            }
+        }
+        store(t, o, sum == 0.f ? 0.f : 1.0f / sum);
+        if (a.lse && t == 0) a.lse[cut.out0 + row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    }
+}
+static_assert(kPSms <= 256, "a thread a cut");
+
 // How a call runs, from the host's bounds alone.  Requests of up to 256 rows
 // go in items of 64 rows (csa2_paged_rows.cu), longer ones in pairs of 128
 // rows over decoded tiles (csa2_paged_tiles.cu) where those need no more than
@@ -136,6 +232,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 // kPSlotReqs requests the kernels then shorten the splits by the real lengths
 // (paged_chunk), down to half: 16 single tokens x 64 heads over 2K to 8K entries
 // took 42.0 us without that and 34.6 us with it.
+// Trees of several requests go to the few-row kernel with its items laid out by
+// their real lengths (walk_first), where they are enough for most multiprocessors,
+// see enough keys, and have 1024 rows each or less on average; 64 heads, us so and
+// as above:
+//   16 requests over 2K to 8K, up to 3 nodes 58 55, 5 77 198, 8 108 188, 12 151 186, 16 195 222, 24 274 292, 32 352 317
+//   4 over 2K to 8K, up to 8 nodes 51 63, 16 76 89, 32 129 160, 64 238 224; 24 x up to 45 x 16 heads, window 128: 26 21
+//   64 over 512 to 2K, up to 8 nodes 131 146, 16 230 220; 32 over 4K to 16K, up to 8 nodes 327 442
+constexpr int64_t kWalkRows = 48 * 64, kWalkMost = 1024;
+constexpr int32_t kWalkTiles = 8;
 struct PagedShare {  // of one of the kernels
     int32_t chunk = 1, splits = 1;         // as the partial outputs are sized
     int32_t chunk_min = 1, slots = 0;      // see PagedArgs
@@ -173,7 +278,8 @@ static PagedShare paged_share(int64_t planned, int64_t most, int ctas, int64_t n
 struct PagedPlan {
     PagedShare tiles, few;
     int32_t span, few_rows, tail;
-    size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, total;
+    int32_t groups;  // trees: of the few-row kernel alone, by walk_first
+    size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, cuts, total;
 };
 constexpr size_t kPMaxTileBytes = size_t(4) << 30;
 constexpr int32_t kPFewRows = 256, kPFewTiles = 4;
@@ -183,6 +289,16 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     if (max_q > n_tokens) max_q = int32_t(n_tokens);
     const int64_t rows = n_tokens * n_heads;
     const int32_t tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256, tree));
+    if (tree && n_req >= 2 && (rows >= kWalkRows || int64_t(max_q) * n_heads > kPFewRows) && rows <= n_req * kWalkMost &&
+        tile_keys >= kWalkTiles) {
+        p.groups = kPSms;
+        p.few.grid = kPSms;
+        p.few_lse = CSA2_STATUS_BYTES;
+        p.few_o = align256(p.few_lse + kPSms * 2 * 64 * 4);
+        p.cuts = p.few_o + size_t(kPSms) * 2 * 64 * kPD * 4;
+        p.total = align256(p.cuts + kPSms * sizeof(WalkCut));
+        return p;
+    }
     if (int64_t(max_q) * n_heads > kPFewRows && tile_keys > kPFewTiles) {
         int64_t span = (max_kv + kPN - 1) / kPN;
         if (window > 0) {  // from the first token's window to the last token
@@ -281,7 +397,8 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
                           static_cast<const void*>(table), static_cast<const void*>(out),
                           static_cast<const void*>(out_lse)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window, mask != nullptr);
+    const bool tree = mask != nullptr;
+    const PagedPlan plan = paged_plan(n_tokens, n_heads, n_req, max_q, max_kv, window, tree);
     if (!ws || !aligned16(ws) || ws_bytes < plan.total) return CSA2_ERR_WORKSPACE;
     if (n_tokens == 0 || n_req == 0 || max_q == 0) return CSA2_OK;
     const size_t bytes = size_t(n_tokens) * n_heads * kPD * 2;  // of the queries and of the outputs
@@ -324,7 +441,7 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
         b.chunk_out = reinterpret_cast<int32_t*>(w + CSA2_STATUS_BYTES / 2) + (item == 64);
         b.item = item;
         b.item_log2 = item_log2;
-        b.item_tokens = paged_item_tokens(n_heads, item, mask != nullptr);
+        b.item_tokens = paged_item_tokens(n_heads, item, tree);
         b.part_lse = reinterpret_cast<float*>(w + lse);
         b.part_o = reinterpret_cast<float*>(w + o);
         b.part_rows = a.rows;
@@ -344,6 +461,8 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
     a.flags = reinterpret_cast<uint8_t*>(w + plan.flags);
     a.span = plan.span;
     a.rows_over = both ? kPFewRows : 0;
+    few.groups = plan.groups;
+    few.cuts = reinterpret_cast<WalkCut*>(w + plan.cuts);
     a.tail = plan.tail;
     if (plan.tail) a.part_rows = kPTailSlots / 2 * 256;  // rows that may have been split
     a.rows_to = plan.tiles.grid > 0 ? INT32_MAX : 0;
@@ -354,6 +473,12 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
     if (e != CSA2_OK) {
         cudaGetLastError();
         return e;
+    }
+    if (plan.groups > 0) {
+        timer_begin(K_PAGED_MERGE, s);
+        launch(paged_walk_merge_kernel, dim3(unsigned(8 * sm_count())), 256, 0, s, 1, few);
+        timer_end(K_PAGED_MERGE, s);
+        return launch_status();
     }
     for (const PagedArgs* b : {&a, &few}) {
         if ((b == &a ? plan.tiles : plan.few).splits == 1 && !b->tail) continue;

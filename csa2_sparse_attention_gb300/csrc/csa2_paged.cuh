@@ -87,6 +87,15 @@ struct PagedArgs {
     const uint32_t* mask;  // [n_tokens][words]
     const int64_t* pos;    // [n_tokens]; below 0: sees nothing
     int32_t words;
+    int32_t groups;        // of a tree: CTAs that walk over the items (walk_first), 0: a CTA a split (paged_find)
+    struct WalkCut* cuts;  // [groups]
+};
+// An item whose second piece is the first item of group g: paged_walk_merge_kernel
+// joins its pieces, from group g - 1's on.
+struct WalkCut {
+    int64_t out0;          // its first row of the outputs
+    int32_t rows, pieces;  // its rows; 0 pieces: none
+    int32_t slot, pad[3];  // of the first piece (the others are their groups' first)
 };
 
 // Bits off .. off + 31 of a mask row (0 outside of it).
@@ -211,6 +220,11 @@ struct PagedWork {
     int32_t item, split, splits;
     int32_t nt, key0;            // key tiles (0: nothing to see) and the first key
     int64_t out0, part0;         // the item's first row of the outputs and of the partial ones
+    // Trees: the request's items and the key tiles of each, and what is left of the group's share from the item's start
+    // on; of the group's first item, whether others hold pieces of it.
+    int32_t items, tiles;
+    int64_t left;
+    WalkCut cut;
 };
 // Finds it for the grid's `place`, by a scan of the requests' items, into shared
 // memory; all WARPS warps of the block call it and synchronize behind it.  Up to
@@ -298,6 +312,208 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
             }
         }
         if (!wide || (base > place && !all)) break;
+    }
+}
+
+// Trees of several requests, the few-row kernel's: the grid is one wave, and the
+// requests' items are laid out over it by their real key tiles, in one of two ways:
+//   pieces  every item is cut into pieces of at most c tiles, the least c with no
+//           more pieces than CTAs; a CTA takes one.
+//   shares  every CTA walks over an equal share of all items' tiles in order, an
+//           item's start counted as kWalkStart more; shares begin and end anywhere
+//           in an item, so a CTA starts on two items or more.
+// (walk_cut has the border.)  A CTA leaves two pieces at most that are no whole
+// items: its first item's and a later one's.  64 heads, FP4, us so and with splits
+// of one length for all requests: 16 requests of up to 8 nodes over 2K to 8K WALK_A;
+// 32 of 8 over 4K to 16K WALK_B; 4 of 16 over 2K to 8K WALK_C.
+constexpr int32_t kWalkStart = 4;  // key tiles' time of an item's start and end
+constexpr int32_t kWalkLeast = 2;  // tiles of a piece, and weight of a share
+struct WalkSums {
+    int64_t items, tiles;  // of all requests: items, and their tiles
+};
+// By pieces a CTA has c tiles and a start, by shares an even part of all tiles and
+// two starts.
+__device__ __forceinline__ int64_t walk_cut(const PagedArgs& a, const WalkSums& all) {  // c, or 0: by shares
+    if (all.items >= a.groups) return 0;
+    const int64_t n = a.groups - all.items;
+    int64_t c = int64_t(__fdividef(float(all.tiles), float(n)));  // below 2^24 within one of the quotient, and enough above
+    while (c * n < all.tiles) c += 1 + (all.tiles - c * n) / n;
+    if (c < kWalkLeast) c = kWalkLeast;
+    return c * a.groups <= all.tiles + kWalkStart * int64_t(a.groups) || c == kWalkLeast ? c : 0;
+}
+// Weight of a group's share, all but the last ones' equal.  (By a float's division,
+// a little above the quotient: a whole number's takes a hundred instructions, and
+// every block asks.)
+__device__ __forceinline__ int64_t walk_share(const PagedArgs& a, int64_t total) {
+    const int64_t n = int64_t(__fdividef(float(total), float(a.groups)) * (1.0f + 0x1p-19f)) + 1;
+    return n > kWalkLeast ? n : kWalkLeast;
+}
+// A request's items, all with the key tiles of the whole request; pieces of an item
+// of `cut` tiles each at most, evened out.
+__device__ __forceinline__ void walk_items(const PagedArgs& a, int64_t r, PagedReq& rq, int32_t& items, int32_t& tiles, Status* st) {
+    items = tiles = 0;
+    if (r >= a.n_req || !paged_request(a, r, rq, st) || !paged_mine(a, rq)) return;
+    const int32_t base = paged_base(a, rq);
+    items = (rq.nq * a.heads + a.item - 1) >> a.item_log2;
+    tiles = rq.len > base ? (rq.len - base + kPN - 1) / kPN : 0;
+}
+__device__ __forceinline__ int32_t walk_pieces(int32_t tiles, int64_t cut, int32_t& per) {
+    per = tiles;
+    if (tiles <= cut) return 1;
+    const int32_t n = (tiles + int32_t(cut) - 1) / int32_t(cut);
+    per = (tiles + n - 1) / n;
+    return (tiles + per - 1) / per;
+}
+// Tiles [j0, j1) of w's item into the rest of w.
+__device__ __forceinline__ void walk_piece(const PagedArgs& a, PagedWork& w, int64_t j0, int64_t j1, int64_t slot) {
+    const int32_t rows = w.rq.nq * a.heads, r0 = w.item * a.item, r1 = (r0 + a.item < rows ? r0 + a.item : rows) - 1;
+    const int32_t base = paged_base(a, w.rq), end = w.rq.len - w.rq.nq + r1 / a.by_heads + 1;
+    const int32_t seen = end > base ? (end - base + kPN - 1) / kPN : 0;  // behind them no row of the item sees a key
+    const int32_t last = int32_t(j1) < seen ? int32_t(j1) : seen;
+    w.split = 0;
+    w.splits = j0 == 0 && j1 == w.tiles ? 1 : 2;
+    w.nt = last > j0 ? last - int32_t(j0) : 0;
+    w.key0 = base + int32_t(j0) * kPN;
+    w.out0 = int64_t(w.rq.q0) * a.heads + r0;
+    w.part0 = slot * a.item;
+}
+// By shares, the group's part of w's item, `off` into it, to the end of the share
+// (w.left from the item's start); w.nt is -1 where it has none.
+__device__ __forceinline__ void walk_part(const PagedArgs& a, PagedWork& w, int64_t off, int64_t slot) {
+    const int64_t j0 = off > kWalkStart ? off - kWalkStart : 0;
+    const int64_t j1 = w.left - kWalkStart < w.tiles ? w.left - kWalkStart : w.tiles;
+    if (w.tiles > 0 ? j1 <= j0 : off != 0) w.nt = -1;
+    else walk_piece(a, w, j0, j1, slot);
+}
+// The item behind w's into `to` (which may be w), by one warp.
+__device__ __forceinline__ void walk_next(const PagedArgs& a, const PagedWork& w, PagedWork& to, int64_t group) {
+    const int lane = lane_id();
+    const int64_t left = w.left - (w.tiles + kWalkStart);
+    int64_t req = left > 0 ? w.req : -1;
+    PagedReq rq = w.rq;
+    int32_t item = w.item + 1, items = w.items, tiles = w.tiles;
+    if (left > 0 && item >= items) {
+        item = 0;
+        req = -1;
+        for (int64_t r0 = w.req + 1; r0 < a.n_req; r0 += 32) {
+            walk_items(a, r0 + lane, rq, items, tiles, nullptr);
+            const uint32_t some = __ballot_sync(0xffffffffu, items > 0);
+            if (some == 0) continue;
+            const int from = __ffs(some) - 1;
+            req = r0 + from;
+            rq.q0 = __shfl_sync(0xffffffffu, rq.q0, from), rq.nq = __shfl_sync(0xffffffffu, rq.nq, from);
+            rq.len = __shfl_sync(0xffffffffu, rq.len, from);
+            items = __shfl_sync(0xffffffffu, items, from), tiles = __shfl_sync(0xffffffffu, tiles, from);
+            break;
+        }
+    }
+    __syncwarp();  // (`to` may be w)
+    if (lane == 0) {
+        to.req = int32_t(req);
+        if (req >= 0) {
+            to.rq = rq;
+            to.item = item;
+            to.items = items;
+            to.tiles = tiles;
+            to.left = left;
+            walk_part(a, to, 0, 2 * group + 1);
+            if (to.nt < 0) to.req = -1;  // the share ends before the item's first tile
+        }
+    }
+}
+// The group's first item into w, by all WARPS warps of the block, which synchronize
+// behind it.  (`sums` as in paged_find.)
+template <int WARPS>
+__device__ __forceinline__ void walk_first(const PagedArgs& a, int64_t group, bool all, PagedWork& w, int64_t* sums) {
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    const bool wide = a.n_req > 32;
+    if (threadIdx.x == 0) w.req = -1, w.cut.pieces = 0;
+    __syncwarp();
+    if (!wide && warp != 0) return;
+    PagedReq rq;
+    int32_t items = 0, tiles = 0;
+    WalkSums total{0, 0};
+    for (int64_t r0 = 0; r0 < a.n_req; r0 += 32 * WARPS) {
+        walk_items(a, r0 + 32 * warp + lane, rq, items, tiles, all ? a.st : nullptr);
+        total.items += items;
+        total.tiles += int64_t(items) * tiles;
+        if (!wide) break;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        total.items += __shfl_xor_sync(0xffffffffu, total.items, o);
+        total.tiles += __shfl_xor_sync(0xffffffffu, total.tiles, o);
+    }
+    if (wide) {
+        if (lane == 0) sums[warp] = total.items, sums[WARPS + warp] = total.tiles;
+        __syncthreads();
+        total.items = total.tiles = 0;
+#pragma unroll 1
+        for (int v = 0; v < WARPS; ++v) total.items += sums[v], total.tiles += sums[WARPS + v];
+        __syncthreads();
+    }
+    const int64_t cut = walk_cut(a, total), weight = total.tiles + total.items * kWalkStart;
+    const int64_t share = cut > 0 ? 1 : walk_share(a, weight), from = group * share;
+    int64_t base = 0;
+#pragma unroll 1
+    for (int64_t r0 = 0; r0 < a.n_req; r0 += 32 * WARPS) {
+        const int64_t r = r0 + 32 * warp + lane;
+        if (wide) walk_items(a, r, rq, items, tiles, nullptr);
+        int32_t per = 0;
+        const int64_t each = cut > 0 ? walk_pieces(tiles, cut, per) : tiles + kWalkStart, mine = items * each;
+        int64_t inc = mine, before = base;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (wide) {
+            int64_t* at = sums + ((r0 / (32 * WARPS)) & 1) * WARPS;
+            if (lane == 31) at[warp] = inc;
+            __syncthreads();
+#pragma unroll 1
+            for (int v = 0; v < WARPS; ++v) {
+                if (v < warp) before += at[v];
+                base += at[v];
+            }
+        }
+        const int64_t local = from - before - (inc - mine);
+        const bool here = local >= 0 && local < mine;
+        if (here) {
+            const int64_t item = mine < (int64_t(1) << 32) ? int64_t(uint32_t(local) / uint32_t(each)) : local / each;
+            const int64_t off = local - item * each;
+            w.rq = rq;
+            w.req = int32_t(r);
+            w.item = int32_t(item);
+            w.items = items;
+            w.tiles = tiles;
+            int32_t pieces = 0, slot = 0;
+            if (cut > 0) {
+                w.left = 0;
+                walk_piece(a, w, off * per, (off + 1) * per < tiles ? (off + 1) * per : tiles, 2 * group);
+                if (off == 1) pieces = int32_t(each);
+            } else {
+                w.left = off + (from + share < weight ? share : weight - from);
+                walk_part(a, w, off, 2 * group);
+                const int64_t back = off - share;  // where the share before this one begins
+                if (group > 0 && off > kWalkStart && back <= kWalkStart) {
+                    for (pieces = 2; off + (pieces - 1) * share < each; ++pieces) {}
+                    slot = back < 0;
+                }
+            }
+            if (pieces > 0) {
+                const int32_t rows = rq.nq * a.heads - w.item * a.item;
+                w.cut.out0 = w.out0;
+                w.cut.rows = rows < a.item ? rows : a.item;
+                w.cut.pieces = pieces;
+                w.cut.slot = slot;
+            }
+        }
+        if (__any_sync(0xffffffffu, here)) {
+            __syncwarp();
+            if (w.nt < 0) walk_next(a, w, w, group);  // an item without keys that an earlier share has
+        }
+        if (!wide || base > from) break;
     }
 }
 
