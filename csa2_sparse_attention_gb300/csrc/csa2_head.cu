@@ -112,7 +112,8 @@ __device__ __forceinline__ void head_queries(const HeadArgs& a, int64_t unit) {
     const uint8_t* src = a.q + (t * a.q_stride + int64_t(h0) * kHD) * 2 + 32 * lane;
     uint8_t* dst = a.q_out + (t * a.heads + h0) * int64_t(kHD * 2) + 32 * lane;
     const int64_t p = a.pos != nullptr ? __ldg(a.pos + t) : 0;
-    Row32 x = load32(src), w;
+    Row32 x = load32(src), ahead = x, w;  // the next two heads are under way
+    if (h0 + 1 < h1) ahead = load32(src + kHD * 2);
     if (NORM) w = load32(a.q_weight + 32 * lane);
     if (p < 0 || (TURN && p >= a.max_pos)) {
         if (p != -1 && h0 == 0 && lane == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_POSITION, int32_t(t), int32_t(p));
@@ -122,8 +123,9 @@ __device__ __forceinline__ void head_queries(const HeadArgs& a, int64_t unit) {
     if (TURN) turns(a, p, lane, c, s);
     for (int h = h0; h < h1; ++h) {
         const Row32 v = x;
+        x = ahead;
+        if (h + 2 < h1) ahead = load32(src + 2 * kHD * 2);
         src += kHD * 2;
-        if (h + 1 < h1) x = load32(src);
         const float rs = NORM ? root_of(sum_lanes(squares(v)), a.eps) : 1.f;
         Row32 o;
 #pragma unroll
@@ -142,11 +144,35 @@ __device__ __forceinline__ void head_queries(const HeadArgs& a, int64_t unit) {
     }
 }
 
+// 1 / sqrt(mean + eps) in fp64, by the warp: rs, off by 2^-21 at most, improved by
+// two of Newton's steps (the error becomes 1.5 times its square each time).
+__device__ __forceinline__ double root_of64(const Row32& x, float rs, float eps) {
+    double ss[2] = {0.0, 0.0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // (the square of a bf16 number is exact in fp32)
+        ss[e & 1] += double(bf16_lo(x.w[e]) * bf16_lo(x.w[e]));
+        ss[e & 1] += double(bf16_hi(x.w[e]) * bf16_hi(x.w[e]));
+    }
+    double v = ss[0] + ss[1];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (v == 0.0) return 0.0;
+    v = fma(v, 1.0 / kHD, double(eps));
+    double r = double(rs);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(r, 0.5 * fma(-v * r, r, 1.0), r);
+    return r;
+}
+
 // A token's latent.  The error of y, relative to |h0| + |h1| of its pair (h the
 // normed values): the sum of squares 10 * 2^-24 (5 in a lane, 5 over lanes), so
 // its root 5; mean and eps, root and reciprocal 2 together; the product 1 (x w
 // is exact); the rotation 5 (cosines within 1.5 * 2^-23 of their values after the
 // angles' addition, two roundings).  13 * 2^-24 < 2^-20.
+//
+// Where the values within that error of y have different codes, that value is
+// computed again in fp64: in a few of a thousand groups.  (All 16 of the group took
+// 8 us, which a call of 16 tokens as often had as not.)
 template <bool FP8>
 __device__ __forceinline__ void head_latent(const HeadArgs& a, int64_t t) {
     const int lane = lane_id();
@@ -178,17 +204,43 @@ __device__ __forceinline__ void head_latent(const HeadArgs& a, int64_t t) {
         y[2 * e + 1] = turn ? fmaf(h0, s[e], h1 * c[e]) : h1;
         whole = whole && fabsf(y[2 * e]) <= FLT_MAX && fabsf(y[2 * e + 1]) <= FLT_MAX && bnd[e] <= FLT_MAX;
     }
-    uint32_t sb = 0, cw[4] = {0, 0, 0, 0};
-    bool risky = false;
+    double rs64 = -1.0;  // not there yet
+    auto need64 = [&](bool some) {  // by the whole warp
+        if (rs64 >= 0.0 || !__any_sync(0xffffffffu, some)) return;
+        rs64 = norm ? root_of64(x, rs, a.eps) : 1.0;
+    };
+    auto exact = [&](int e) {  // value e of the lane in fp64
+        uint32_t xw = x.w[0], ww = w.w[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (j == e >> 1) xw = x.w[j], ww = w.w[j];
+        const double h0 = double(bf16_lo(xw) * bf16_lo(ww)) * rs64, h1 = double(bf16_hi(xw) * bf16_hi(ww)) * rs64;
+        if (!turn) return e & 1 ? h1 : h0;
+        const double2* t64 = reinterpret_cast<const double2*>(a.table + int64_t(a.n_hi + 1024) * (kHD / 2));
+        const int j = 8 * lane + (e >> 1);
+        const double2 h = t64[(p >> 10) * (kHD / 2) + j], l = t64[(int64_t(a.n_hi) + (p & 1023)) * (kHD / 2) + j];
+        const double c64 = fma(h.x, l.x, -h.y * l.y), s64 = fma(h.y, l.x, h.x * l.y);
+        return e & 1 ? fma(h0, s64, h1 * c64) : fma(h0, c64, -h1 * s64);
+    };
+    uint32_t sb = 0, cw[4] = {0, 0, 0, 0}, risky = 0;  // risky: a bit per value
     if (FP8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t two = e4m3x2_rn_sat(y[2 * j], y[2 * j + 1]);
-            cw[j >> 1] |= two << (16 * (j & 1));
+            cw[j >> 1] |= e4m3x2_rn_sat(y[2 * j], y[2 * j + 1]) << (16 * (j & 1));
             const float a0 = fabsf(y[2 * j]), a1 = fabsf(y[2 * j + 1]);
-            risky |= whole && (e4m3x2_rn_sat(fmaxf(a0 - bnd[j], 0.f), fmaxf(a1 - bnd[j], 0.f)) != e4m3x2_rn_sat(a0 + bnd[j], a1 + bnd[j]));
+            const uint32_t differ = e4m3x2_rn_sat(fmaxf(a0 - bnd[j], 0.f), fmaxf(a1 - bnd[j], 0.f)) ^ e4m3x2_rn_sat(a0 + bnd[j], a1 + bnd[j]);
+            if (whole) risky |= (differ & 0xFF ? 1u : 0u) << (2 * j) | (differ >> 8 ? 1u : 0u) << (2 * j + 1);
         }
-    } else if (whole) {
+        need64(risky != 0);
+        for (; risky != 0; risky &= risky - 1) {
+            const int e = __ffs(risky) - 1;
+            const double z = exact(e);
+            const uint32_t code = e4m3_rne_f64(fabs(z)) | (signbit(z) ? 0x80u : 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i == e >> 2) cw[i] = (cw[i] & ~(0xFFu << (8 * (e & 3)))) | code << (8 * (e & 3));
+        }
+    } else {
         float amax = 0.f, bmax = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(y[e]));
@@ -196,65 +248,39 @@ __device__ __forceinline__ void head_latent(const HeadArgs& a, int64_t t) {
         for (int j = 0; j < 8; ++j) bmax = fmaxf(bmax, bnd[j]);
         // amax / 6 by a multiply: its error (< 2^-22 relative) sits inside mq
         const float q6 = amax * (1.0f / 6.0f), mq = fmaf(q6, 0x1p-20f, bmax * (1.0f / 6.0f) * 1.001f);
-        sb = e4m3x2_rn_sat(q6, 0.f) & 0xFF;
-        const uint32_t span = e4m3x2_rn_sat(fmaxf(q6 - mq, 0.f), q6 + mq);
-        risky = (span & 0xFF) != (span >> 8);
+        const uint32_t span = e4m3x2_rn_sat(fmaxf(q6 - mq, 0.f), q6 + mq), lo = span & 0xFF, hi = span >> 8;
+        sb = whole ? e4m3x2_rn_sat(q6, 0.f) & 0xFF : 0x7Fu;  // a scale of NaN: what attends to the latent gets NaN
+        const bool unsure = whole && lo != hi;
+        need64(unsure);
+        if (unsure) {  // the largest of those that may be the largest one
+            double top = 0.0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) risky |= (fabsf(y[e]) + 2.f * bmax >= amax ? 1u : 0u) << e;
+            for (; risky != 0; risky &= risky - 1) top = fmax(top, fabs(exact(__ffs(risky) - 1)));
+            sb = e4m3_rne_f64(top / 6.0);
+        }
         const float sc = e4m3_value(sb);
+        float inv = 0.f;
         if (sc > 0.f) {
-            const float inv = __frcp_rn(sc);
+            inv = __frcp_rn(sc);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float r0 = y[2 * j] * inv, r1 = y[2 * j + 1] * inv;
                 cw[j >> 2] |= e2m1x2_rn_sat(r0, r1) << (8 * (j & 3));
                 const float a0 = fabsf(r0), a1 = fabsf(r1);
                 const float m0 = fmaf(a0, 0x1p-22f, bnd[j] * inv * 1.001f), m1 = fmaf(a1, 0x1p-22f, bnd[j] * inv * 1.001f);
-                risky |= e2m1x2_rn_sat(fmaxf(a0 - m0, 0.f), fmaxf(a1 - m1, 0.f)) != e2m1x2_rn_sat(a0 + m0, a1 + m1);
+                const uint32_t differ = e2m1x2_rn_sat(fmaxf(a0 - m0, 0.f), fmaxf(a1 - m1, 0.f)) ^ e2m1x2_rn_sat(a0 + m0, a1 + m1);
+                risky |= (differ & 0xF ? 1u : 0u) << (2 * j) | (differ >> 4 ? 1u : 0u) << (2 * j + 1);
             }
         }
-    } else {
-        sb = 0x7F;  // a scale of NaN: what attends to the latent gets NaN
-    }
-    if (__any_sync(0xffffffffu, risky)) {
-        // the row's sum of squares in fp64, then the groups near a border
-        double ss = 0.0;
+        need64(risky != 0);
+        for (; risky != 0; risky &= risky - 1) {
+            const int e = __ffs(risky) - 1;
+            const double z = exact(e);
+            const uint32_t code = e2m1_code_f64(z, double(sc));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const double lo = double(bf16_lo(x.w[e])), hi = double(bf16_hi(x.w[e]));
-            ss = fma(lo, lo, fma(hi, hi, ss));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (risky) {
-            const double rs64 = !norm ? 1.0 : ss == 0.0 ? 0.0 : 1.0 / sqrt(ss / double(kHD) + double(a.eps));
-            const double2* t64 = reinterpret_cast<const double2*>(a.table + int64_t(a.n_hi + 1024) * (kHD / 2));
-            const int64_t rh = (p >> 10) * (kHD / 2) + 8 * lane, rl = (int64_t(a.n_hi) + (p & 1023)) * (kHD / 2) + 8 * lane;
-            double z[16], top = 0.0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double h0 = double(bf16_lo(x.w[e])) * double(bf16_lo(w.w[e])) * rs64;
-                const double h1 = double(bf16_hi(x.w[e])) * double(bf16_hi(w.w[e])) * rs64;
-                z[2 * e] = h0, z[2 * e + 1] = h1;
-                if (turn) {
-                    const double2 h = t64[rh + e], l = t64[rl + e];
-                    const double c64 = fma(h.x, l.x, -h.y * l.y), s64 = fma(h.y, l.x, h.x * l.y);
-                    z[2 * e] = fma(h0, c64, -h1 * s64);
-                    z[2 * e + 1] = fma(h0, s64, h1 * c64);
-                }
-                top = fmax(top, fmax(fabs(z[2 * e]), fabs(z[2 * e + 1])));
-            }
-            cw[0] = cw[1] = cw[2] = cw[3] = 0;
-            if (FP8) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    cw[e >> 2] |= (e4m3_rne_f64(fabs(z[e])) | (signbit(z[e]) ? 0x80u : 0u)) << (8 * (e & 3));
-            } else {
-                sb = e4m3_rne_f64(top / 6.0);
-                const double s64 = double(e4m3_value(sb));
-                if (s64 > 0.0) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) cw[e >> 3] |= e2m1_code_f64(z[e], s64) << (4 * (e & 7));
-                }
-            }
+            for (int i = 0; i < 2; ++i)
+                if (i == e >> 3) cw[i] = (cw[i] & ~(0xFu << (4 * (e & 7)))) | code << (4 * (e & 7));
         }
     }
     if (FP8) {
@@ -266,7 +292,7 @@ __device__ __forceinline__ void head_latent(const HeadArgs& a, int64_t t) {
 }
 
 template <bool NORM, bool TURN, bool FP8>
-__global__ void __launch_bounds__(32 * kHWarps) head_norm_rope_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(32 * kHWarps, 3) head_norm_rope_kernel(const HeadArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5;

@@ -7,10 +7,12 @@
 // HBM bound: the logits, once.  A row is one block's, or is cut into slices for
 // a cluster of up to eight, whose blocks leave their parts in shared memory for
 // the first of them to join: no workspace, one launch.  A thread takes groups of
-// four 16-byte vectors and keeps its own base b for the exponentials, which moves
-// only when a value lies 2^4 above it, so that the running maximum costs a maximum
-// and a test per group.  (Not further: sum(e^y y) against b turns into that
-// against m by sum * (b - m), which cancels for what lies above b.)
+// four 16-byte vectors and keeps its own base b for the exponentials, 2^4 above a
+// group's maximum and moved only when a value lies 2^4 above it, so that the
+// running maximum costs a maximum and a test per group.  (Not further: sum(e^y y)
+// against b turns into that against m by sum * (b - m), which cancels.)  A block
+// walks over rows and has the next one's first vectors under way while it joins its
+// threads' parts.
 //
 // The k largest: every group's maximum stays in shared memory.  One warp finds the
 // k-th largest of the threads' maxima to 16 bits, which k values reach; the few
@@ -33,6 +35,7 @@ constexpr int kLCands = 1024;      // values that are ranked
 constexpr int kLHits = 512;        // groups that are read again at once
 constexpr int kLMaxCluster = 8;
 constexpr float kLFloor = -160.f;  // exponents below it are nothing in fp32
+constexpr float kLReach = 4.f;     // a thread's base: this far above a maximum, moved for a value this far above it
 
 struct LogArgs {
     const uint8_t* x;
@@ -43,7 +46,7 @@ struct LogArgs {
     int32_t* ids;
     float* best;
     Status* st;
-    int64_t stride;     // elements
+    int64_t stride, n;  // elements; rows
     int32_t vocab, given, top, slice;  // vectors of a slice
     float scale;        // of the logits
 };
@@ -128,6 +131,37 @@ __device__ __forceinline__ unsigned long long peer_u64(uint32_t a) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t nan_max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A thread's sums against its base: y = x c - base in the log2 domain (c the scale
+// times log2 e, a product inside one fused operation; base a whole number, so that
+// it is exact), sum = sum 2^y, tilt = sum 2^y y.  Where |x c| passes 2^22 (masks of
+// the type's lowest value alone, before anything else) y = (x - raw) c instead.
+struct LogPart {
+    float base = __builtin_nanf(""), raw = 0.f, floor = 0.f;  // floor: values that far down are nothing
+    float sum = 0.f, sum_rest = 0.f, tilt = 0.f, tilt_rest = 0.f;
+    bool plain = true;
+    // How far x lies above the base, log2 domain (NaN before there is one).
+    __device__ __forceinline__ float over(float x, float c) const { return plain ? fmaf(x, c, -base) : (x - raw) * c; }
+    __device__ __forceinline__ void move(float m, float c) {
+        const float b = rintf(m * c) + kLReach;
+        const bool to_plain = fabsf(b) <= 0x1p22f;
+        const float d = sum == 0.f ? 0.f : plain && to_plain ? base - b : (to_plain ? fmaf(m, c, -b) : 0.f) - over(m, c);
+        const float f = sum == 0.f ? 0.f : exp2_of(d);
+        tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
+        sum = f == 0.f ? 0.f : f * sum;
+        sum_rest *= f, tilt_rest *= f;
+        plain = to_plain;
+        base = b;
+        raw = fmaxf(m, -FLT_MAX);
+        floor = (b + kLFloor) / c;
+    }
+};
+
 // Rows begin anywhere: vectors are the 16-byte pieces of memory that hold the
 // row, `head` elements of the first one lie before it.
 template <typename T>
@@ -164,6 +198,35 @@ struct RowView {
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // Of a group's words (2 E pairs of values): the largest value (NaN if one is), values below a floor raised to it, a pair.
+    static __device__ __forceinline__ float most(const uint32_t (&w)[4 * kLGroup]) {
+        if constexpr (sizeof(T) == 4) {
+            float m[2] = {__uint_as_float(w[0]), __uint_as_float(w[1])};
+#pragma unroll
+            for (int e = 2; e < 4 * kLGroup; ++e) m[e & 1] = nan_max(m[e & 1], __uint_as_float(w[e]));
+            return nan_max(m[0], m[1]);
+        } else {
+            uint32_t m[2] = {w[0], w[1]};
+#pragma unroll
+            for (int e = 2; e < 4 * kLGroup; ++e) m[e & 1] = nan_max_bf16x2(m[e & 1], w[e]);
+            m[0] = nan_max_bf16x2(m[0], m[1]);
+            return nan_max(bf16_lo(m[0]), bf16_hi(m[0]));
+        }
+    }
+    static __device__ __forceinline__ void at_least(uint32_t (&w)[4 * kLGroup], float floor) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 4 * kLGroup; ++e) w[e] = __float_as_uint(fmaxf(__uint_as_float(w[e]), floor));
+        } else {
+            const uint32_t f = __float_as_uint(floor), b = (f + (f >> 31 ? 0xFFFFu : 0u)) >> 16, two = b | (b << 16);  // rounded down
+#pragma unroll
+            for (int e = 0; e < 4 * kLGroup; ++e) w[e] = nan_max_bf16x2(w[e], two);
+        }
+    }
+    static __device__ __forceinline__ uint64_t pair(const uint32_t (&w)[4 * kLGroup], int e) {
+        if constexpr (sizeof(T) == 4) return both(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+        else return both(bf16_lo(w[e]), bf16_hi(w[e]));
     }
     static __device__ __forceinline__ void values(const uint4& v, float (&x)[E]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -216,12 +279,16 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
 #pragma unroll
             for (int i = 0; i < kLThreads / 32; ++i) own[i] = S.keys[32 * i + tid];
 #pragma unroll 1
-            for (int b = from; b >= to; --b) {
-                const uint32_t up = bar | (1u << b);
-                uint32_t n = 0;
+            for (int b = from - 1; b >= to; b -= 2) {  // two bits at a time
+                uint32_t n[3] = {0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < kLThreads / 32; ++i) n += own[i] >= up;
-                if (__reduce_add_sync(0xffffffffu, n) >= uint32_t(k)) bar = up;
+                for (int i = 0; i < kLThreads / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) n[e] += own[i] >= (bar | (uint32_t(e + 1) << b));
+                uint32_t bits = 0;
+#pragma unroll
+                for (int e = 0; e < 3; ++e) bits += __reduce_add_sync(0xffffffffu, n[e]) >= uint32_t(k);
+                bar |= bits << b;
             }
             if (tid == 0) S.bar = bar;
         }
@@ -231,8 +298,9 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
     uint32_t bar = kth(0, 31, 16);
     const uint32_t low = float_key(-INFINITY) + 1;  // -inf is no alternative
     if (bar < low) bar = low;
+    const float reached = key_float(bar);
     for (int j = 0; j < turns; ++j)
-        if (float_key(groups[j * kLThreads + tid]) >= bar) {
+        if (groups[j * kLThreads + tid] >= reached) {
             const int at = atomicAdd(&S.n_hits, 1);
             if (at < kLHits) S.hits[at] = uint16_t(j * kLThreads + tid);
         }
@@ -345,182 +413,204 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
-    const int64_t r = blockIdx.x / uint32_t(cluster);
+    const int64_t step = gridDim.x / uint32_t(cluster);
+    int64_t r = blockIdx.x / uint32_t(cluster);
     const int rank = int(blockIdx.x) - int(r) * cluster;
-    const RowView<T> row(a, r);
-    const int32_t nv = row.vectors(), v0 = rank * a.slice < nv ? rank * a.slice : nv, v1 = v0 + a.slice < nv ? v0 + a.slice : nv;
-    const int turns = (v1 - v0 + kLThreads * kLGroup - 1) / (kLThreads * kLGroup);
-    const float c = a.scale * 1.4426950408889634f, reach = 4.f / c;
-    // the given tokens' logits, while the row comes in
-    float x_given = -INFINITY;
-    if (rank == 0 && tid < a.given) {
-        const int64_t id = a.tokens[r * a.given + tid];
-        if (id >= 0 && id < a.vocab)
-            x_given = sizeof(T) == 4 ? reinterpret_cast<const float*>(a.x)[r * a.stride + id]
-                                     : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(a.x)[r * a.stride + id]) << 16);
-        else if (id != -1)
-            record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_TOKEN, int32_t(r), int32_t(id));
-    }
-    // ---- one pass: base, sum and tilt of a thread, its maximum, its groups' maxima
-    float base = __uint_as_float(0x7FC00000u), sum = 0.f, tilt = 0.f, top = -INFINITY, sum_rest = 0.f, tilt_rest = 0.f;
-    bool bad = false;
+    const float c = a.scale * 1.4426950408889634f;
     uint4 next[kLGroup];
-    auto fetch = [&](int j) {
+    auto fetch = [&](const RowView<T>& row, int32_t v1, int32_t at) {  // vectors at .. of a slice that ends at v1
+        const int32_t behind = at + kLGroup * kLThreads;
+        if ((at > 0 || row.head == 0) && behind <= v1 && behind * E <= row.head + row.vocab) {  // every one lies within the row
+            const uint4* p = reinterpret_cast<const uint4*>(row.base) + at + tid;
 #pragma unroll
-        for (int g = 0; g < kLGroup; ++g) {
-            const int32_t at = v0 + (j * kLGroup + g) * kLThreads + tid;
-            next[g] = at < v1 ? row.load(at) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
-                                                               : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+            for (int g = 0; g < kLGroup; ++g) next[g] = __ldg(p + g * kLThreads);
+        } else {
+#pragma unroll
+            for (int g = 0; g < kLGroup; ++g) {
+                const int32_t v = at + g * kLThreads + tid;
+                next[g] = v < v1 ? row.load(v) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                                                 : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+            }
         }
     };
-    fetch(0);
-    for (int j = 0; j < turns; ++j) {
-        uint4 v[kLGroup];
-#pragma unroll
-        for (int g = 0; g < kLGroup; ++g) v[g] = next[g];
-        if (j + 1 < turns) fetch(j + 1);
-        float m = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kLGroup; ++g) {
-            float x[E];
-            row.values(v[g], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) m = nan_max(m, x[e]);
-        }
-        groups[j * kLThreads + tid] = m;
-        if (!(m <= base + reach)) {  // the first group, one far above the base, NaN
-            if (!(m < INFINITY)) bad = true;
-            const float b = fmaxf(m, -FLT_MAX);
-            const float d = (base - b) * c, f = sum == 0.f ? 0.f : exp2_of(d);
-            tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
-            sum = f == 0.f ? 0.f : f * sum;
-            sum_rest *= f, tilt_rest *= f;
-            base = b;
-        }
-        top = fmaxf(top, m);
-        uint64_t gs[2] = {0, 0}, gt[2] = {0, 0};
-        const uint64_t minus = both(-base, -base), cc = both(c, c);
-#pragma unroll
-        for (int g = 0; g < kLGroup; ++g) {
-            float x[E];
-            row.values(v[g], x);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                float y0, y1;
-                each(mul_both(add_both(both(x[e], x[e + 1]), minus), cc), y0, y1);
-                y0 = fmaxf(y0, kLFloor), y1 = fmaxf(y1, kLFloor);
-                const uint64_t p = both(exp2_of(y0), exp2_of(y1));
-                gs[(e >> 1) & 1] = add_both(gs[(e >> 1) & 1], p);
-                gt[(e >> 1) & 1] = fma_both(p, both(y0, y1), gt[(e >> 1) & 1]);
-            }
-        }
-        float s0, s1, t0, t1;
-        each(add_both(gs[0], gs[1]), s0, s1);
-        each(add_both(gt[0], gt[1]), t0, t1);
-        add_kept(sum, sum_rest, s0 + s1);
-        add_kept(tilt, tilt_rest, t0 + t1);
-    }
-    sum += sum_rest, tilt += tilt_rest;
-    // ---- the slice's: everything against its maximum
-    float m = top;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) S.red[0][warp] = m;
-    const bool any_bad = __syncthreads_or(bad);
-    m = S.red[0][lane & (kLWarps - 1)];
-#pragma unroll
-    for (int o = kLWarps / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    auto first = [&](const RowView<T>& row) { const int32_t nv = row.vectors(); return rank * a.slice < nv ? rank * a.slice : nv; };
+    auto end = [&](const RowView<T>& row) { const int32_t nv = row.vectors(); return (rank + 1) * a.slice < nv ? (rank + 1) * a.slice : nv; };
     {
-        const float d = sum == 0.f ? 0.f : (base - m) * c, f = sum == 0.f ? 0.f : exp2_of(d);
-        tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
-        sum = f * sum;
+        const RowView<T> row(a, r);
+        fetch(row, end(row), first(row));
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        tilt += __shfl_xor_sync(0xffffffffu, tilt, o);
-    }
-    if (lane == 0) S.red[1][warp] = sum, S.red[2][warp] = tilt;
-    if (a.top > 0 && !any_bad) top_of_slice<T>(S, groups, row, v0, v1, turns, top, a.top);
-    else if (tid == 0) S.listed = 0;
-    __syncthreads();
-    if (tid == 0) {
-        float s = 0.f, t = 0.f;
-        for (int w = 0; w < kLWarps; ++w) s += S.red[1][w], t += S.red[2][w];
-        S.max = m, S.sum = s, S.tilt = t, S.bad = any_bad;
-    }
-    // ---- the row's
-    if (cluster > 1) {
-        cluster_meet();
-        if (rank == 0) {
-            if (tid < cluster) {
-                S.all_f[tid][0] = __uint_as_float(peer_u32(peer(&S.max, tid)));
-                S.all_f[tid][1] = __uint_as_float(peer_u32(peer(&S.sum, tid)));
-                S.all_f[tid][2] = __uint_as_float(peer_u32(peer(&S.tilt, tid)));
-                S.all_n[tid] = int(peer_u32(peer(&S.listed, tid)));
-            }
-            int b = tid < cluster ? int(peer_u32(peer(&S.bad, tid))) : 0;
-            for (int i = tid; i < cluster * a.top; i += kLThreads) {
-                const int q = i / a.top, e = i - q * a.top;
-                S.all[q][e] = peer_u64(peer(&S.list[e], q));  // (behind its last one: whatever is there)
-            }
-            b = __syncthreads_or(b);
-            if (tid == 0) S.all_bad = b;
+    for (; r < a.n; r += step) {
+        const RowView<T> row(a, r);
+        const int32_t v0 = first(row), v1 = end(row);
+        const int turns = (v1 - v0 + kLThreads * kLGroup - 1) / (kLThreads * kLGroup);
+        // the given tokens' logits, while the row comes in
+        float x_given = -INFINITY;
+        if (rank == 0 && tid < a.given) {
+            const int64_t id = a.tokens[r * a.given + tid];
+            if (id >= 0 && id < a.vocab)
+                x_given = sizeof(T) == 4 ? reinterpret_cast<const float*>(a.x)[r * a.stride + id]
+                                         : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(a.x)[r * a.stride + id]) << 16);
+            else if (id != -1)
+                record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_TOKEN, int32_t(r), int32_t(id));
         }
-        cluster_meet();  // the others' parts are read
-        if (rank != 0) return;
-    } else {
+        // ---- one pass: base, sum and tilt of a thread, its maximum, its groups' maxima
+        LogPart part;
+        float top = -INFINITY;
+        bool bad = false;
+        for (int j = 0; j < turns; ++j) {
+            uint32_t w[4 * kLGroup];
+#pragma unroll
+            for (int g = 0; g < kLGroup; ++g)
+                w[4 * g] = next[g].x, w[4 * g + 1] = next[g].y, w[4 * g + 2] = next[g].z, w[4 * g + 3] = next[g].w;
+            if (j + 1 < turns) fetch(row, v1, v0 + (j + 1) * kLGroup * kLThreads);
+            const float m = RowView<T>::most(w);
+            groups[j * kLThreads + tid] = m;
+            if (!(part.over(m, c) <= kLReach)) {  // the first group, one far above the base, NaN
+                if (!(m < INFINITY)) bad = true;
+                part.move(m, c);
+            }
+            top = fmaxf(top, m);
+            if (part.plain) {
+                RowView<T>::at_least(w, part.floor);
+                uint64_t gs[2] = {0, 0}, gt[2] = {0, 0};
+                const uint64_t minus = both(-part.base, -part.base), cc = both(c, c);
+#pragma unroll
+                for (int e = 0; e < 2 * E; ++e) {
+                    float y0, y1;
+                    each(fma_both(RowView<T>::pair(w, e), cc, minus), y0, y1);
+                    const float p0 = exp2_of(y0), p1 = exp2_of(y1);
+                    gs[e & 1] = add_both(gs[e & 1], both(p0, p1));
+                    gt[e & 1] = fma_both(both(p0, p1), both(y0, y1), gt[e & 1]);
+                }
+                float s0, s1, t0, t1;
+                each(add_both(gs[0], gs[1]), s0, s1);
+                each(add_both(gt[0], gt[1]), t0, t1);
+                add_kept(part.sum, part.sum_rest, s0 + s1);
+                add_kept(part.tilt, part.tilt_rest, t0 + t1);
+            } else if (m > -INFINITY) {
+                float s0 = 0.f, t0 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 2 * E; ++e) {
+                    float x[2];
+                    each(RowView<T>::pair(w, e), x[0], x[1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float y = fmaxf((x[i] - part.raw) * c, kLFloor), p = exp2_of(y);
+                        s0 += p;
+                        t0 = fmaf(p, y, t0);
+                    }
+                }
+                add_kept(part.sum, part.sum_rest, s0);
+                add_kept(part.tilt, part.tilt_rest, t0);
+            }
+        }
+        if (r + step < a.n) {
+            const RowView<T> ahead(a, r + step);
+            fetch(ahead, end(ahead), first(ahead));
+        }
+        float sum = part.sum + part.sum_rest, tilt = part.tilt + part.tilt_rest;
+        // ---- the slice's: everything against its maximum
+        float m = top;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) S.red[0][warp] = m;
+        const bool any_bad = __syncthreads_or(bad);
+        m = S.red[0][lane & (kLWarps - 1)];
+#pragma unroll
+        for (int o = kLWarps / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        {
+            const float d = sum == 0.f ? 0.f : -part.over(m, c), f = sum == 0.f ? 0.f : exp2_of(d);
+            tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
+            sum = f * sum;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            tilt += __shfl_xor_sync(0xffffffffu, tilt, o);
+        }
+        if (lane == 0) S.red[1][warp] = sum, S.red[2][warp] = tilt;
+        if (a.top > 0 && !any_bad) top_of_slice<T>(S, groups, row, v0, v1, turns, top, a.top);
+        else if (tid == 0) S.listed = 0;
         __syncthreads();
         if (tid == 0) {
-            S.all_f[0][0] = S.max, S.all_f[0][1] = S.sum, S.all_f[0][2] = S.tilt;
-            S.all_n[0] = S.listed;
-            S.all_bad = S.bad;
+            float s = 0.f, t = 0.f;
+            for (int w = 0; w < kLWarps; ++w) s += S.red[1][w], t += S.red[2][w];
+            S.max = m, S.sum = s, S.tilt = t, S.bad = any_bad;
         }
-        for (int i = tid; i < a.top; i += kLThreads) S.all[0][i] = S.list[i];
-        __syncthreads();
-    }
-    float big = -INFINITY;
-    for (int q = 0; q < cluster; ++q) big = fmaxf(big, S.all_f[q][0]);
-    float s = 0.f, t = 0.f;
-    int total = 0;
-    for (int q = 0; q < cluster; ++q) {
-        const float sq = S.all_f[q][1], d = sq == 0.f ? 0.f : (S.all_f[q][0] - big) * c, f = sq == 0.f ? 0.f : exp2_of(d);
-        s = fmaf(f, sq, s);
-        t = f == 0.f ? t : fmaf(f, fmaf(sq, d, S.all_f[q][2]), t);
-        total += S.all_n[q];
-    }
-    const bool none = s == 0.f, nan = S.all_bad != 0;  // nothing above -inf; NaN or infinity among them
-    const float log_s = logf(s), not_a = __uint_as_float(0x7FC00000u);
-    if (tid == 0) {
-        if (a.lse) a.lse[r] = nan ? not_a : none ? -INFINITY : fmaf(big, a.scale, log_s);
-        if (a.entropy) a.entropy[r] = nan ? not_a : none ? 0.f : log_s - t / s * 0.6931471805599453f;
-    }
-    if (tid < a.given)
-        a.logprobs[r * a.given + tid] = nan ? not_a : none || x_given == -INFINITY ? -INFINITY : (x_given - big) * a.scale - log_s;
-    // alternatives: a value's place is how many of all lists are larger (none where a slice has NaN, whatever the others list)
-    if (tid >= (nan ? 0 : total) && tid < a.top) {
-        a.ids[r * a.top + tid] = -1;
-        a.best[r * a.top + tid] = nan ? not_a : -INFINITY;
-    }
-    for (int i = tid; i < cluster * a.top && !nan; i += kLThreads) {
-        const int q = i / a.top, e = i - q * a.top;
-        if (e >= S.all_n[q]) continue;
-        const unsigned long long v = S.all[q][e];
-        int at = e;
-        for (int o = 0; o < cluster; ++o) {
-            if (o == q) continue;
-            int lo = 0, hi = S.all_n[o];  // how many of list o are larger
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (S.all[o][mid] > v) lo = mid + 1;
-                else hi = mid;
+        // ---- the row's
+        if (cluster > 1) {
+            cluster_meet();
+            if (rank == 0) {
+                if (tid < cluster) {
+                    S.all_f[tid][0] = __uint_as_float(peer_u32(peer(&S.max, tid)));
+                    S.all_f[tid][1] = __uint_as_float(peer_u32(peer(&S.sum, tid)));
+                    S.all_f[tid][2] = __uint_as_float(peer_u32(peer(&S.tilt, tid)));
+                    S.all_n[tid] = int(peer_u32(peer(&S.listed, tid)));
+                }
+                int b = tid < cluster ? int(peer_u32(peer(&S.bad, tid))) : 0;
+                for (int i = tid; i < cluster * a.top; i += kLThreads) {
+                    const int q = i / a.top, e = i - q * a.top;
+                    S.all[q][e] = peer_u64(peer(&S.list[e], q));  // (behind its last one: whatever is there)
+                }
+                b = __syncthreads_or(b);
+                if (tid == 0) S.all_bad = b;
             }
-            at += lo;
+            cluster_meet();  // the others' parts are read
+            if (rank != 0) continue;
+        } else {
+            __syncthreads();
+            if (tid == 0) {
+                S.all_f[0][0] = S.max, S.all_f[0][1] = S.sum, S.all_f[0][2] = S.tilt;
+                S.all_n[0] = S.listed;
+                S.all_bad = S.bad;
+            }
+            for (int i = tid; i < a.top; i += kLThreads) S.all[0][i] = S.list[i];
+            __syncthreads();
         }
-        if (at < a.top) {
-            a.ids[r * a.top + at] = int32_t(~uint32_t(v));
-            a.best[r * a.top + at] = (key_float(uint32_t(v >> 32)) - big) * a.scale - log_s;
+        float big = -INFINITY;
+        for (int q = 0; q < cluster; ++q) big = fmaxf(big, S.all_f[q][0]);
+        float s = 0.f, t = 0.f;
+        int total = 0;
+        for (int q = 0; q < cluster; ++q) {
+            const float sq = S.all_f[q][1], d = sq == 0.f ? 0.f : (S.all_f[q][0] - big) * c, f = sq == 0.f ? 0.f : exp2_of(d);
+            s = fmaf(f, sq, s);
+            t = f == 0.f ? t : fmaf(f, fmaf(sq, d, S.all_f[q][2]), t);
+            total += S.all_n[q];
         }
+        const bool none = s == 0.f, nan = S.all_bad != 0;  // nothing above -inf; NaN or infinity among them
+        const float log_s = logf(s), not_a = __uint_as_float(0x7FC00000u);
+        if (tid == 0) {
+            if (a.lse) a.lse[r] = nan ? not_a : none ? -INFINITY : fmaf(big, a.scale, log_s);
+            if (a.entropy) a.entropy[r] = nan ? not_a : none ? 0.f : log_s - t / s * 0.6931471805599453f;
+        }
+        if (tid < a.given)
+            a.logprobs[r * a.given + tid] = nan ? not_a : none || x_given == -INFINITY ? -INFINITY : (x_given - big) * a.scale - log_s;
+        // alternatives: a value's place is how many of all lists are larger (none where a slice has NaN, whatever the others list)
+        if (tid >= (nan ? 0 : total) && tid < a.top) {
+            a.ids[r * a.top + tid] = -1;
+            a.best[r * a.top + tid] = nan ? not_a : -INFINITY;
+        }
+        for (int i = tid; i < cluster * a.top && !nan; i += kLThreads) {
+            const int q = i / a.top, e = i - q * a.top;
+            if (e >= S.all_n[q]) continue;
+            const unsigned long long v = S.all[q][e];
+            int at = e;
+            for (int o = 0; o < cluster; ++o) {
+                if (o == q) continue;
+                int lo = 0, hi = S.all_n[o];  // how many of list o are larger
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (S.all[o][mid] > v) lo = mid + 1;
+                    else hi = mid;
+                }
+                at += lo;
+            }
+            if (at < a.top) {
+                a.ids[r * a.top + at] = int32_t(~uint32_t(v));
+                a.best[r * a.top + at] = (key_float(uint32_t(v >> 32)) - big) * a.scale - log_s;
+            }
+        }
+        __syncthreads();  // the next row writes where this one's parts were read
     }
 }
 
@@ -540,7 +630,10 @@ static csa2_status logprobs_launch(LogArgs a, int64_t n, int cluster, size_t sme
         done[dev].store(true, std::memory_order_release);
     }
     timer_begin(K_LOGPROBS, s);
-    launch(token_logprobs_kernel<T>, dim3(unsigned(n * cluster)), kLThreads, smem, s, unsigned(cluster), a, cluster);
+    // blocks that are resident at once walk over the rows (a cluster is made for few rows, one each)
+    const int64_t most = 4 * int64_t(sm_count());
+    launch(token_logprobs_kernel<T>, dim3(unsigned(cluster > 1 || n < most ? n * cluster : most)), kLThreads, smem, s, unsigned(cluster), a,
+           cluster);
     timer_end(K_LOGPROBS, s);
     return launch_status();
 }
@@ -574,6 +667,7 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
     a.best = best;
     a.st = static_cast<Status*>(ws);
     a.stride = stride;
+    a.n = n;
     a.vocab = int32_t(vocab);
     a.given = given;
     a.top = top;
