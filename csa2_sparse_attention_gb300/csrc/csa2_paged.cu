@@ -232,15 +232,18 @@ static_assert(kPSms <= 256, "a thread a cut");
 // kPSlotReqs requests the kernels then shorten the splits by the real lengths
 // (paged_chunk), down to half: 16 single tokens x 64 heads over 2K to 8K entries
 // took 42.0 us without that and 34.6 us with it.
-// Trees of several requests go to the few-row kernel with its items laid out by
-// their real lengths (walk_first), where they are enough for most multiprocessors,
-// see enough keys, and have 1024 rows each or less on average; 64 heads, us so and
-// as above:
-//   16 requests over 2K to 8K, up to 3 nodes 58 55, 5 77 198, 8 108 188, 12 151 186, 16 195 222, 24 274 292, 32 352 317
-//   4 over 2K to 8K, up to 8 nodes 51 63, 16 76 89, 32 129 160, 64 238 224; 24 x up to 45 x 16 heads, window 128: 26 21
-//   64 over 512 to 2K, up to 8 nodes 131 146, 16 230 220; 32 over 4K to 16K, up to 8 nodes 327 442
-constexpr int64_t kWalkRows = 48 * 64, kWalkMost = 1024;
-constexpr int32_t kWalkTiles = 8;
+// Trees of several requests that see enough key tiles are laid out by their real
+// lengths (walk_first): in the few-row kernel with 512 rows each or less on average
+// and enough rows for most multiprocessors, in row tiles with more, up to three
+// items for each group of four CTAs.  64 heads, up to so many nodes over so many
+// entries, us in the few-row kernel, in row tiles and as above:
+//   16 requests, 2K to 8K: 3 nodes 58 - 55, 5 79 100 200, 8 110 123 188, 12 154 160 185, 16 194 187 222, 24 275 256 292,
+//     32 352 318 317, 64 - 565 520
+//   4, 2K to 8K: 6 46 49 75, 8 51 52 63, 12 67 63 70, 16 76 71 91, 32 129 108 157;  2: 8 38 39 37, 32 73 70 81
+//   8: 8 of 512 to 2K 37 37 57, 32 of them - 72 65, 64 of them - 113 110;  64: 8 of 512 to 2K 132 147 147, 16 233 221 220
+//   24 of up to 45 x 16 heads, window 128: 26 - 21
+constexpr int64_t kWalkRows = 48 * 64, kWalkMost = 512, kWalkTileRows = 3 * 38 * 256;
+constexpr int32_t kWalkKeys = 8, kWalkTileKeys = 24;  // key tiles
 struct PagedShare {  // of one of the kernels
     int32_t chunk = 1, splits = 1;         // as the partial outputs are sized
     int32_t chunk_min = 1, slots = 0;      // see PagedArgs
@@ -278,9 +281,19 @@ static PagedShare paged_share(int64_t planned, int64_t most, int ctas, int64_t n
 struct PagedPlan {
     PagedShare tiles, few;
     int32_t span, few_rows, tail;
-    int32_t groups;  // trees: of the few-row kernel alone, by walk_first
+    int32_t groups;  // trees: of one of the kernels alone, by walk_first
     size_t tile_lse, tile_o, few_lse, few_o, tile_at, flags, cuts, total;
 };
+// Two pieces of an item a group of CTAs, and its WalkCut.
+static void walk_plan(PagedPlan& p, int32_t groups, int32_t item, PagedShare& kernel, size_t& lse, size_t& o) {
+    const size_t rows = size_t(groups) * 2 * item;
+    p.groups = groups;
+    kernel.grid = kPSms;
+    lse = CSA2_STATUS_BYTES;
+    o = align256(lse + rows * 4);
+    p.cuts = o + rows * kPD * 4;
+    p.total = align256(p.cuts + groups * sizeof(WalkCut));
+}
 constexpr size_t kPMaxTileBytes = size_t(4) << 30;
 constexpr int32_t kPFewRows = 256, kPFewTiles = 4;
 static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv, int window, bool tree) {
@@ -290,13 +303,8 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
     const int64_t rows = n_tokens * n_heads;
     const int32_t tile_keys = paged_key_tiles(max_q, max_kv, window, paged_item_tokens(n_heads, 256, tree));
     if (tree && n_req >= 2 && (rows >= kWalkRows || int64_t(max_q) * n_heads > kPFewRows) && rows <= n_req * kWalkMost &&
-        tile_keys >= kWalkTiles) {
-        p.groups = kPSms;
-        p.few.grid = kPSms;
-        p.few_lse = CSA2_STATUS_BYTES;
-        p.few_o = align256(p.few_lse + kPSms * 2 * 64 * 4);
-        p.cuts = p.few_o + size_t(kPSms) * 2 * 64 * kPD * 4;
-        p.total = align256(p.cuts + kPSms * sizeof(WalkCut));
+        tile_keys >= kWalkKeys) {
+        walk_plan(p, kPSms, 64, p.few, p.few_lse, p.few_o);
         return p;
     }
     if (int64_t(max_q) * n_heads > kPFewRows && tile_keys > kPFewTiles) {
@@ -306,6 +314,13 @@ static PagedPlan paged_plan(int64_t n_tokens, int n_heads, int64_t n_req, int32_
             span = span < w ? span : w;
         }
         if (n_req <= 65535 && size_t(n_req) * size_t(span) * kPTileBytes <= kPMaxTileBytes) p.span = int32_t(span);
+    }
+    if (tree && n_req >= 2 && p.span > 0 && tile_keys >= kWalkTileKeys && rows <= kWalkTileRows) {
+        walk_plan(p, kPSms / 4, 256, p.tiles, p.tile_lse, p.tile_o);
+        p.flags = p.total;
+        p.tile_at = align256(p.flags + size_t(n_req) * p.span * kPFlagBytes);
+        p.total = p.tile_at + size_t(n_req) * p.span * kPTileBytes;
+        return p;
     }
     auto items = [&](int32_t q, int32_t item) {  // each request rounds up
         const int64_t all = rows / item + n_req, each = n_req * paged_items(q, n_heads, item);
@@ -461,8 +476,8 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
     a.flags = reinterpret_cast<uint8_t*>(w + plan.flags);
     a.span = plan.span;
     a.rows_over = both ? kPFewRows : 0;
-    few.groups = plan.groups;
-    few.cuts = reinterpret_cast<WalkCut*>(w + plan.cuts);
+    a.groups = few.groups = plan.groups;
+    a.cuts = few.cuts = reinterpret_cast<WalkCut*>(w + plan.cuts);
     a.tail = plan.tail;
     if (plan.tail) a.part_rows = kPTailSlots / 2 * 256;  // rows that may have been split
     a.rows_to = plan.tiles.grid > 0 ? INT32_MAX : 0;
@@ -476,7 +491,7 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
     }
     if (plan.groups > 0) {
         timer_begin(K_PAGED_MERGE, s);
-        launch(paged_walk_merge_kernel, dim3(unsigned(8 * sm_count())), 256, 0, s, 1, few);
+        launch(paged_walk_merge_kernel, dim3(unsigned(8 * sm_count())), 256, 0, s, 1, plan.few.grid > 0 ? few : a);
         timer_end(K_PAGED_MERGE, s);
         return launch_status();
     }

@@ -315,17 +315,19 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
     }
 }
 
-// Trees of several requests, the few-row kernel's: the grid is one wave, and the
-// requests' items are laid out over it by their real key tiles, in one of two ways:
+// Trees of several requests: the grid is one wave, and the requests' items are laid
+// out over it by their real key tiles, in one of two ways:
 //   pieces  every item is cut into pieces of at most c tiles, the least c with no
-//           more pieces than CTAs; a CTA takes one.
-//   shares  every CTA walks over an equal share of all items' tiles in order, an
+//           more pieces than groups of CTAs; a group takes one.
+//   shares  every group walks over an equal share of all items' tiles in order, an
 //           item's start counted as kWalkStart more; shares begin and end anywhere
-//           in an item, so a CTA starts on two items or more.
-// (walk_cut has the border.)  A CTA leaves two pieces at most that are no whole
-// items: its first item's and a later one's.  64 heads, FP4, us so and with splits
-// of one length for all requests: 16 requests of up to 8 nodes over 2K to 8K WALK_A;
-// 32 of 8 over 4K to 16K WALK_B; 4 of 16 over 2K to 8K WALK_C.
+//           in an item, so a group starts on two items or more.
+// (walk_cut has the border.)  A group is one CTA of the few-row kernel, or the four
+// of a pair of row tiles; it leaves two pieces at most that are no whole items: its
+// first item's and a later one's.  64 heads, FP4, us so and with one split length
+// for all requests: 16 requests of up to 8 nodes over 2K to 8K 109 and 188, 32 of 8
+// over 4K to 16K 331 and 441 (few-row kernel); 4 of up to 32 over 2K to 8K 108 and
+// 157, 8 of up to 64 over 4K to 16K 564 and 600 (row tiles).
 constexpr int32_t kWalkStart = 4;  // key tiles' time of an item's start and end
 constexpr int32_t kWalkLeast = 2;  // tiles of a piece, and weight of a share
 struct WalkSums {
