@@ -255,16 +255,16 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 const bool nan = ((f[0].nan[tid >> 4] | f[1].nan[tid >> 4]) >> (tid & 15)) & 1;
                 if (TREE) {
                     // tiles behind the first token, or where a window can begin (a token lies no further down than its place)
-                    const int32_t t0 = key0 + j * kPN;
-                    const bool part = blind || t0 + kPN > first || (a.window > 0 && t0 < k_end - a.window);
+                    const int32_t from = key0 + j * kPN;
+                    const bool part = blind || from + kPN > first || (a.window > 0 && from < k_end - a.window);
                     if (part) {  // (the last tile's bits were read before this tile's first barrier)
                         const int row = tid >> 1;
                         const int2 k = S.keys[row];
                         const int tok = S.tok[row];
 #pragma unroll
                         for (int w = 2 * (tid & 1); w < 2 * (tid & 1) + 2; ++w) {
-                            uint32_t v = range_bits(t0 + 32 * w, k.x, k.y);
-                            if (tok >= 0) v |= tree_bits(a.mask + int64_t(tok) * a.words, a.words, t0 + 32 * w - first);
+                            uint32_t v = range_bits(from + 32 * w, k.x, k.y);
+                            if (tok >= 0) v |= tree_bits(a.mask + int64_t(tok) * a.words, a.words, from + 32 * w - first);
                             S.see[w][row] = v;
                         }
                         soft_sync();
