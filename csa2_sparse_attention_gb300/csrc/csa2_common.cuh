@@ -166,6 +166,21 @@ inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
     return x && y && na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
+// Whether what a call writes lies apart from what it reads and from each other.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+template <size_t N, size_t M>
+inline bool apart(const Span (&out)[N], const Span (&in)[M]) {
+    for (size_t i = 0; i < N; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return false;
+        for (const Span& s : in)
+            if (overlap(out[i].p, out[i].bytes, s.p, s.bytes)) return false;
+    }
+    return true;
+}
 csa2_status launch_status();  // maps cudaGetLastError to a csa2_status
 int sm_count();               // the current device's multiprocessors (queried once per device)
 uint64_t wait_limit_ns();      // the bounded waits' limit, passed to every launch (2 s by default)

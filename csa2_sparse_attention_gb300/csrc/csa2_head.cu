@@ -368,24 +368,28 @@ extern "C" csa2_status csa2_head_norm_rope(const void* q, int64_t q_stride, int 
         if (n_heads < 1 || n_heads > 128) return CSA2_ERR_UNSUPPORTED;
         const int64_t row = int64_t(n_heads) * kHD;
         if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 31)) return CSA2_ERR_INVALID_ARG;
-        // the outputs are the queries themselves, or apart from them
-        if (!(q == q_out && q_stride == row) && overlap(q, ((n - 1) * q_stride + row) * 2, q_out, n * row * 2))
-            return CSA2_ERR_INVALID_ARG;
     }
     if (latents) {
         if (fmt != CSA2_FMT_FP4 && fmt != CSA2_FMT_FP8) return CSA2_ERR_UNSUPPORTED;
         if (lat_stride < kHD || lat_stride % 8 || lat_stride > (int64_t(1) << 31)) return CSA2_ERR_INVALID_ARG;
         if (!dst_codes || (fmt == CSA2_FMT_FP4) != (dst_scales != nullptr)) return CSA2_ERR_INVALID_ARG;
         if (!dst_row && n > n_rows) return CSA2_ERR_INVALID_ARG;
-        // what is written lies apart from what is read and from each other
-        const int64_t in = ((n - 1) * lat_stride + kHD) * 2, cb = n_rows * (fmt == CSA2_FMT_FP4 ? kHD / 2 : kHD), sb = n_rows * (kHD / 16);
-        const int64_t qi = q ? ((n - 1) * q_stride + int64_t(n_heads) * kHD) * 2 : 0, qo = q ? n * n_heads * int64_t(kHD) * 2 : 0;
-        if (overlap(latents, in, q_out, qo) || overlap(latents, in, dst_codes, cb) || overlap(latents, in, dst_scales, sb) ||
-            overlap(dst_codes, cb, dst_scales, sb) || overlap(q, qi, dst_codes, cb) || overlap(q, qi, dst_scales, sb) ||
-            overlap(q_out, qo, dst_codes, cb) || overlap(q_out, qo, dst_scales, sb))
-            return CSA2_ERR_INVALID_ARG;
     }
     if (n == 0) return CSA2_OK;
+    // what is written lies apart from what is read and from each other; or the queries are turned in place
+    const int64_t q_row = q ? int64_t(n_heads) * kHD : 0;
+    const bool in_place = q == q_out && q_stride == q_row;
+    const int64_t row_codes = fmt == CSA2_FMT_FP4 ? kHD / 2 : kHD, cells = latents ? n_rows : 0;
+    const Span outs[] = {{q_out, n * q_row * 2}, {dst_codes, cells * row_codes}, {dst_scales, cells * (kHD / 16)}};
+    const int64_t positions = rope_table ? ceil_div<int64_t>(rope_max_pos, 1024) + 1024 : 0;
+    const Span ins[] = {{in_place ? nullptr : q, q ? ((n - 1) * q_stride + q_row) * 2 : 0},
+                        {latents, latents ? ((n - 1) * lat_stride + kHD) * 2 : 0},
+                        {q_weight, kHD * 2},
+                        {lat_weight, kHD * 2},
+                        {pos, n * 8},
+                        {dst_row, n * 8},
+                        {rope_table, positions * (kHD / 2) * 24}};
+    if (!apart(outs, ins)) return CSA2_ERR_INVALID_ARG;
     HeadArgs a{};
     a.q = static_cast<const uint8_t*>(q);
     a.q_weight = static_cast<const uint8_t*>(q_weight);

@@ -646,7 +646,7 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
     if (n > (1 << 24) || vocab > (1 << 21) || given > kLTop || top > kLTop || !(scale >= 0x1p-20f) || !(scale <= 0x1p20f))
         return CSA2_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
-    if (!logits || stride < vocab || stride > (int64_t(1) << 40)) return CSA2_ERR_INVALID_ARG;
+    if (!logits || stride < vocab || stride > (int64_t(1) << 36)) return CSA2_ERR_INVALID_ARG;
     if (given > 0 && (!tokens || !logprobs)) return CSA2_ERR_INVALID_ARG;
     if (top > 0 && (!ids || !best)) return CSA2_ERR_INVALID_ARG;
     for (const void* p : {logits, static_cast<const void*>(tokens), static_cast<const void*>(logprobs), static_cast<const void*>(lse),
@@ -654,9 +654,9 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
     if (n == 0) return CSA2_OK;
     const int64_t size = dtype == CSA2_OUT_BF16 ? 2 : 4, in = ((n - 1) * stride + vocab) * size;
-    if (overlap(logits, in, logprobs, n * given * 4) || overlap(logits, in, lse, n * 4) || overlap(logits, in, entropy, n * 4) ||
-        overlap(logits, in, ids, n * top * 4) || overlap(logits, in, best, n * top * 4))
-        return CSA2_ERR_INVALID_ARG;
+    const Span outs[] = {{logprobs, n * given * 4}, {lse, n * 4}, {entropy, n * 4}, {ids, n * top * 4}, {best, n * top * 4}};
+    const Span ins[] = {{logits, in}, {tokens, n * given * 8}};
+    if (!apart(outs, ins)) return CSA2_ERR_INVALID_ARG;
     LogArgs a{};
     a.x = static_cast<const uint8_t*>(logits);
     a.tokens = tokens;

@@ -29,42 +29,62 @@ __device__ __forceinline__ TreeReq tree_request(const int32_t* q_start, const in
     return o;
 }
 
-// Positions and masks: a block per request, a thread per node that walks up to
-// the root, first to its depth, then along the part inside the window.  Ancestors
-// come in falling order, so a word of the mask is finished when the walk leaves it
-// and goes out once.
-__global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const int32_t* __restrict__ parent,
-                                                                 const int32_t* __restrict__ q_start,
-                                                                 const int32_t* __restrict__ kv_len, int64_t n_tokens,
-                                                                 int32_t max_q, int32_t window, int64_t* __restrict__ pos,
-                                                                 uint32_t* __restrict__ mask, int32_t words, Status* st) {
-    __shared__ int16_t up[kTreeMost];  // -2: not an earlier node
+// Positions and masks: a block per request, a thread per node.  A warp has the
+// nodes of one word of a mask: five rounds of pointer jumping by shuffles give each
+// its ancestors within the word and the nearest one before it.  A row is then a walk
+// from word to word, at most 32 dependent loads from shared memory however deep
+// the tree is (from node to node it was one for each, on lanes that part ways: a
+// chain of 1024 took 217 us).
+//
+// Bound by the launch: 16 x 8 and 8 x 64 nodes 1.6 us, 192 x 61 1.8, a chain of
+// 1024 18 (its rows' words, a node's behind one another, go out one by one).
+__global__ void __launch_bounds__(kTreeMost) tree_plan_kernel(const int32_t* __restrict__ parent,
+                                                              const int32_t* __restrict__ q_start,
+                                                              const int32_t* __restrict__ kv_len, int64_t n_tokens,
+                                                              int32_t max_q, int32_t window, int64_t* __restrict__ pos,
+                                                              uint32_t* __restrict__ mask, int32_t words, Status* st) {
+    __shared__ uint32_t within[kTreeMost];  // a node and its ancestors of the same word
+    __shared__ int16_t before[kTreeMost];   // the nearest ancestor of an earlier word; -1: none; -2: lost, a parent was bad
     grid_dep_wait();
     grid_dep_launch();
     const int64_t r = blockIdx.x;
     const TreeReq t = tree_request(q_start, kv_len, r, n_tokens, max_q, INT32_MAX, st);
-    for (int i = threadIdx.x; i < t.nq; i += kTreeThreads) {
-        const int32_t p = parent[t.q0 + i];
-        const bool ok = p >= -1 && p < i;
-        if (!ok) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, p);
-        up[i] = ok && t.good ? int16_t(p) : int16_t(-2);
+    const int i = threadIdx.x;  // (a block has a thread for each of max_q nodes)
+    int up = -1;
+    if (i < t.nq) {
+        up = parent[t.q0 + i];
+        const bool ok = up >= -1 && up < i;
+        if (!ok) record(st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, up);
+        if (!ok || !t.good) up = -2;
     }
+    uint32_t bits = 1u << (i & 31);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const uint32_t its = __shfl_sync(0xffffffffu, bits, up & 31);
+        const int next = __shfl_sync(0xffffffffu, up, up & 31);
+        if (up >= 0 && (up ^ i) < 32) bits |= its, up = next;
+    }
+    within[i] = bits;
+    before[i] = int16_t(up);
     __syncthreads();
-    for (int i = threadIdx.x; i < t.nq; i += kTreeThreads) {
-        int depth = -1, at = i;
-        while (at >= 0) at = up[at], ++depth;
-        const bool lost = at == -2;  // sees nothing
-        pos[t.q0 + i] = lost ? -1 : int64_t(t.first) + depth;
-        uint32_t* row = mask + int64_t(t.q0 + i) * words;
-        const int lowest = lost ? INT32_MAX : window > 0 && depth >= window ? window : depth + 1;  // nodes to set
-        int w = words - 1, left = lost ? 0 : lowest;
-        uint32_t bits = 0;
-        for (at = i; left > 0; --left, at = up[at]) {
-            while (w > (at >> 5)) row[w--] = bits, bits = 0;
-            bits |= 1u << (at & 31);
+    if (i >= t.nq) return;
+    uint32_t* row = mask + int64_t(t.q0 + i) * words;
+    int depth = 0, at = i, left = window > 0 ? window : kTreeMost;  // nodes that a window leaves, the nearest ones
+    for (int w = words - 1; w >= 0; --w) {
+        uint32_t b = 0;
+        if (at >> 5 == w) {
+            b = within[at];
+            at = before[at];
+            const int n = __popc(b);
+            depth += n;
+            for (int k = left; k < n; ++k) b &= b - 1;
+            left = left > n ? left - n : 0;
         }
-        while (w >= 0) row[w--] = bits, bits = 0;
+        row[w] = b;
     }
+    if (at == -2)  // sees nothing
+        for (int w = 0; w < words; ++w) row[w] = 0;
+    pos[t.q0 + i] = at == -2 ? -1 : int64_t(t.first) + depth - 1;
 }
 
 struct CommitArgs {
@@ -84,7 +104,7 @@ struct CommitArgs {
     int32_t* accepted;
     int64_t* next;
     Status* st;
-    unsigned* ticket;
+    unsigned long long* ticket;  // blocks that came by << 32 | pages that they give back
     int64_t n_req, n_tokens, row_pages, max_pages, n_pages;
     int32_t max_q, page, code_chunks, chunks;  // 16-byte chunks of a row's codes, and of codes and scales
 };
@@ -98,37 +118,75 @@ __device__ __forceinline__ int64_t commit_pages(int64_t n, int page) { return (n
 // dependent shared loads.  Its rows move down by batches, all of a batch loaded
 // before any is stored: node path[j] >= j, so what a batch stores no later batch
 // loads.  The last block to come by gives the pages back, in the order that undoes
-// the plan's taking.
+// the plan's taking: the ticket carries the number of pages beside the blocks', and
+// the place of a request's pages is a scan.
+//
+// Bound by a chain of dependent accesses: bounds, then nodes and table together,
+// walk, rows; in the last block lengths, table, free list.  16 x 8 nodes 6.6 us, 192 x
+// 61 9.9 (tables read twice over and counted by the last block: 7.4 and 13).
 __global__ void __launch_bounds__(kTreeThreads) tree_commit_kernel(const CommitArgs a) {
+    __shared__ int64_t choice[kTreeMost];
     __shared__ int32_t best[kTreeMost];
     __shared__ int16_t path[kTreeMost];
+    __shared__ int32_t pages[kTreeMost / 8 + 1];  // of the step's entries
     __shared__ int64_t src[kCommitRows], dst[kCommitRows];
-    __shared__ int64_t sums[2][kTreeThreads / 32];
+    __shared__ int32_t sums[kTreeThreads / 32];
     __shared__ int s_len;
+    __shared__ unsigned s_total;
     __shared__ bool last;
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
     const int64_t r = blockIdx.x;
     const TreeReq t = tree_request(a.q_start, a.kv_len, r, a.n_tokens, a.max_q, a.max_pages * a.page, a.st);
-    for (int i = tid; i < t.nq; i += kTreeThreads) best[i] = INT32_MAX;
-    __syncthreads();
-    if (t.good) {
-        for (int i = tid; i < t.nq; i += kTreeThreads) {
-            const int32_t p = a.parent[t.q0 + i];
-            if (p < -1 || p >= i) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, p);
-            else if (p >= 0 && a.token[t.q0 + i] == a.choice[t.q0 + p]) atomicMin(&best[p], i);
+    const bool some = t.good && t.nq > 0;
+    const int page0 = some ? t.first / a.page : 0, n_pages = some ? (t.len - 1) / a.page - page0 + 1 : 0;
+    for (int j = tid; j < n_pages; j += kTreeThreads) {
+        const int32_t id = a.table[r * a.max_pages + page0 + j];
+        if (id < 0 || id >= a.n_pages || (a.codes != nullptr && id >= a.row_pages))
+            record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(r), id);
+        pages[j] = id;
+    }
+    if (some) {
+        int32_t p[kTreeMost / kTreeThreads];
+        int64_t tok[kTreeMost / kTreeThreads];
+#pragma unroll
+        for (int k = 0; k < kTreeMost / kTreeThreads; ++k) {
+            const int i = tid + k * kTreeThreads;
+            if (i < t.nq) p[k] = a.parent[t.q0 + i], tok[k] = a.token[t.q0 + i], choice[i] = a.choice[t.q0 + i], best[i] = INT32_MAX;
         }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kTreeMost / kTreeThreads; ++k) {
+            const int i = tid + k * kTreeThreads;
+            if (i >= t.nq) break;
+            if (p[k] < -1 || p[k] >= i) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PARENT, t.q0 + i, p[k]);
+            else if (p[k] >= 0 && tok[k] == choice[p[k]]) atomicMin(&best[p[k]], i);
+        }
+        if (tid == 0) s_len = p[0];  // (0's parent)
     }
     __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
         int n = 0;
-        if (t.good && t.nq > 0 && a.parent[t.q0] == -1)
-            for (int32_t at = 0; at != INT32_MAX; at = best[at]) path[n++] = int16_t(at);
-        s_len = n;
-        a.accepted[r] = n;
-        a.next[r] = n > 0 ? a.choice[t.q0 + path[n - 1]] : -1;
-        if (t.good && t.nq > 0) a.cached[r] = t.first + n;
+        if (lane == 0) {
+            if (some && s_len == -1)
+                for (int32_t at = 0; at != INT32_MAX; at = best[at]) path[n++] = int16_t(at);
+            a.accepted[r] = n;
+            a.next[r] = n > 0 ? choice[path[n - 1]] : -1;
+            if (some) a.cached[r] = t.first + n;
+            __threadfence();
+        }
+        n = __shfl_sync(0xffffffffu, n, 0);
+        unsigned back = 0;  // pages that hold no kept entry
+        for (int j = int(commit_pages(t.first + n, a.page)) - page0 + lane; j < n_pages; j += 32) back += pages[j] >= 0 && pages[j] < a.n_pages;
+        back = __reduce_add_sync(0xffffffffu, back);
+        if (lane == 0) {
+            s_len = n;
+            const unsigned long long was = atomicAdd(a.ticket, (1ull << 32) + back);
+            last = unsigned(was >> 32) == gridDim.x - 1;
+            s_total = unsigned(was) + back;
+            if (last) *a.ticket = 0;
+        }
     }
     __syncthreads();
     const int len = s_len;
@@ -141,11 +199,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_commit_kernel(const CommitA
             const int n = len - j0 < kCommitRows ? len - j0 : kCommitRows;
             if (tid < 2 * n) {  // rows of the cache, -1 where a page is none
                 const int j = j0 + (tid >> 1);
-                const int32_t p = t.first + (tid & 1 ? path[j] : j);
-                const int32_t page = p / a.page, id = a.table[r * a.max_pages + page];
-                const bool ok = id >= 0 && id < a.row_pages;
-                if (!ok) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(r), id);
-                (tid & 1 ? src : dst)[tid >> 1] = ok ? int64_t(id) * a.page + (p - page * a.page) : -1;
+                const int32_t p = t.first + (tid & 1 ? path[j] : j), page = p / a.page, id = pages[page - page0];
+                (tid & 1 ? src : dst)[tid >> 1] = id >= 0 && id < a.row_pages ? int64_t(id) * a.page + (p - page * a.page) : -1;
             }
             __syncthreads();
             uint4 v[kCommitHeld];
@@ -170,60 +225,46 @@ __global__ void __launch_bounds__(kTreeThreads) tree_commit_kernel(const CommitA
         }
     }
     // ---- pages, by the last block
-    if (tid == 0) {
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-        if (last) *a.ticket = 0;
-    }
-    __syncthreads();
     if (!last) return;
     __threadfence();
-    const int64_t have = *a.n_free;
-    int64_t total = 0, base = 0;
-    for (int pass = 0; pass < 2; ++pass) {  // how many there are, then each one's place
-        for (int64_t r0 = 0; r0 < a.n_req; r0 += kTreeThreads) {
-            const int64_t q = r0 + tid;
-            int64_t from = 0, to = 0, mine = 0;
-            if (q < a.n_req) {
-                const int32_t q0 = a.q_start[q], q1 = a.q_start[q + 1], kv = a.kv_len[q];
-                const bool good = q0 >= 0 && q1 > q0 && q1 <= a.n_tokens && q1 - q0 <= a.max_q && kv >= q1 - q0 && kv <= a.max_pages * a.page;
-                if (good) from = commit_pages(kv - (q1 - q0) + __ldcg(a.accepted + q), a.page), to = commit_pages(kv, a.page);
-                for (int64_t j = from; j < to; ++j) {
-                    const int32_t id = a.table[q * a.max_pages + j];
-                    if (id >= 0 && id < a.n_pages) ++mine;
-                    else if (pass == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_PAGE, int32_t(q), id);
-                }
-            }
-            int64_t inc = mine;
+    const int64_t have = *a.n_free, total = s_total;
+    if (have < 0 || have + total > a.n_pages) {  // a free list that has no room for them: nothing goes back
+        if (tid == 0) {
+            record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_CAPACITY, 2, int32_t(have));
+            *a.n_free_out = int32_t(have);
+        }
+        return;
+    }
+    int64_t base = have + total;  // a request's pages end there
+    for (int64_t r0 = 0; r0 < a.n_req; r0 += kTreeThreads) {
+        const int64_t q = r0 + tid;
+        const int32_t* ids = a.table + q * a.max_pages;
+        int64_t from = 0, to = 0;
+        int32_t mine = 0;
+        if (q < a.n_req) {
+            const int32_t q0 = a.q_start[q], q1 = a.q_start[q + 1], kv = a.kv_len[q], kept = __ldcg(a.accepted + q);
+            const bool good = q0 >= 0 && q1 > q0 && q1 <= a.n_tokens && q1 - q0 <= a.max_q && kv >= q1 - q0 && kv <= a.max_pages * a.page;
+            if (good) from = commit_pages(kv - (q1 - q0) + kept, a.page), to = commit_pages(kv, a.page);
+            for (int64_t j = from; j < to; ++j) mine += ids[j] >= 0 && ids[j] < a.n_pages;
+        }
+        int32_t inc = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += u;
-            }
-            if (lane == 31) sums[0][warp] = inc;
-            __syncthreads();
-            int64_t before = 0, all = 0;
-            for (int w = 0; w < kTreeThreads / 32; ++w) {
-                if (w < warp) before += sums[0][w];
-                all += sums[0][w];
-            }
-            __syncthreads();
-            if (pass == 0) {
-                total += all;
-            } else {
-                int64_t at = have + total - 1 - (base + before + inc - mine);
-                for (int64_t j = from; j < to; ++j) {
-                    const int32_t id = a.table[q * a.max_pages + j];
-                    if (id >= 0 && id < a.n_pages) a.free_pages[at--] = id;
-                }
-                base += all;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
         }
-        if (have < 0 || have + total > a.n_pages) {  // a free list that has no room for them: nothing goes back
-            if (tid == 0) record(a.st, CSA2_ERR_DEVICE_BOUNDS, CHK_CAPACITY, 2, int32_t(have));
-            total = 0;
-            break;
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        int32_t before = 0, all = 0;
+        for (int w = 0; w < kTreeThreads / 32; ++w) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
         }
+        __syncthreads();
+        int64_t at = base - (before + inc - mine);
+        for (int64_t j = from; j < to; ++j)
+            if (ids[j] >= 0 && ids[j] < a.n_pages) a.free_pages[--at] = ids[j];
+        base -= all;
     }
     if (tid == 0) *a.n_free_out = int32_t(have + total);
 }
@@ -242,13 +283,14 @@ extern "C" csa2_status csa2_tree_plan(const int32_t* parent, const int32_t* q_st
     for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(q_start), static_cast<const void*>(kv_len),
                           static_cast<const void*>(pos), static_cast<const void*>(mask)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    const int64_t nm = n_tokens * mask_words * 4;
-    if (overlap(pos, 8 * n_tokens, parent, 4 * n_tokens) || overlap(mask, nm, parent, 4 * n_tokens) || overlap(mask, nm, pos, 8 * n_tokens))
-        return CSA2_ERR_INVALID_ARG;
     if (n_req == 0 || n_tokens == 0 || max_q == 0) return CSA2_OK;
+    // what is written lies apart from what is read and from each other
+    const Span out[] = {{pos, 8 * n_tokens}, {mask, n_tokens * mask_words * 4}};
+    const Span in[] = {{parent, 4 * n_tokens}, {q_start, 4 * (n_req + 1)}, {kv_len, 4 * n_req}};
+    if (!apart(out, in)) return CSA2_ERR_INVALID_ARG;
     cudaStream_t s = cudaStream_t(stream);
     timer_begin(K_TREE_PLAN, s);
-    launch(tree_plan_kernel, dim3(unsigned(n_req)), kTreeThreads, 0, s, 1, parent, q_start, kv_len, n_tokens, max_q, window, pos, mask,
+    launch(tree_plan_kernel, dim3(unsigned(n_req)), ceil_div(max_q, 32) * 32, 0, s, 1, parent, q_start, kv_len, n_tokens, max_q, window, pos, mask,
            mask_words, static_cast<Status*>(ws));
     timer_end(K_TREE_PLAN, s);
     return launch_status();
@@ -277,9 +319,14 @@ extern "C" csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* to
                           static_cast<const void*>(cached), static_cast<const void*>(path), static_cast<const void*>(accepted),
                           static_cast<const void*>(next)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    // (every block reads lengths after others have written theirs)
-    if (cached == kv_len || accepted == kv_len || cached == accepted) return CSA2_ERR_INVALID_ARG;
     if (n_req == 0) return CSA2_OK;
+    // what is written lies apart from what is read and from each other (blocks read what others are done with)
+    const int64_t row_codes = fmt == CSA2_FMT_FP4 ? 256 : 512;
+    const Span out[] = {{codes, codes ? n_rows * row_codes : 0}, {scales, scales ? n_rows * 32 : 0}, {free_pages, 4 * n_pages},
+                            {n_free_out, 4}, {cached, 4 * n_req}, {path, 4 * n_tokens}, {accepted, 4 * n_req}, {next, 8 * n_req}};
+    const Span in[] = {{parent, 4 * n_tokens}, {token, 8 * n_tokens}, {choice, 8 * n_tokens}, {q_start, 4 * (n_req + 1)},
+                           {kv_len, 4 * n_req}, {table, 4 * n_req * max_pages}, {n_free, n_free == n_free_out ? 0 : 4}};
+    if (!apart(out, in)) return CSA2_ERR_INVALID_ARG;
     CommitArgs a{};
     a.parent = parent;
     a.token = token;
@@ -297,7 +344,7 @@ extern "C" csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* to
     a.accepted = accepted;
     a.next = next;
     a.st = static_cast<Status*>(ws);
-    a.ticket = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + 64);
+    a.ticket = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + 64);
     a.n_req = n_req;
     a.n_tokens = n_tokens;
     a.row_pages = n_rows / page_size;

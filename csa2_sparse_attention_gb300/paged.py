@@ -134,6 +134,7 @@ class PagedLatents:
         self.accepted = torch.zeros(n_req, dtype=i32, device=d)
         self.next = torch.full((n_req,), -1, dtype=i64, device=d)
         self.ws_tree = torch.zeros(abi.STATUS_BYTES, dtype=u8, device=d)
+        self._words = None  # of a mask's row, as tree() laid it out
         self.ws_attn = None
         self._captured, self._kept = False, []  # the workspace is in a graph; earlier ones that are
         _made(d)
@@ -231,6 +232,7 @@ class PagedLatents:
         self._tokens(n_tokens)
         self._nodes(max_q, parent=(parent, n_tokens, torch.int32))
         s = _stream(self.dev, stream)
+        self._words = (max_q + 31) // 32
         if n_tokens == 0 or max_q == 0:
             return
         abi.csa2_tree_plan(parent, self.q_start, self.kv_len, self.n_req, n_tokens, max_q, self.window, self.pos, self.mask,
@@ -242,6 +244,8 @@ class PagedLatents:
         self._tokens(n_tokens)
         self._nodes(max_q)
         _rows("q", q, n_tokens, (self.heads, LATENT), self.dev)
+        if self._words != (max_q + 31) // 32:
+            raise ValueError(f"{max_q} nodes of a request: not the bound that tree() had")
         s = _stream(self.dev, stream)
         ws = self.workspace(n_tokens, max_q, max_kv, s, tree=True)
         if n_tokens == 0:

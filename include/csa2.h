@@ -510,7 +510,8 @@ csa2_status csa2_head_norm_rope(const void* q_bf16, int64_t q_stride, int n_head
  * descends from it get pos = -1 and an empty mask, and see nothing.  A request
  * whose kv_len is below its nodes is recorded, and all its nodes get that; one
  * whose tokens lie outside [0, n_tokens) or exceed max_q is recorded and skipped.
- * Tokens behind q_start[n_req] are left as they are.  ws: CSA2_STATUS_BYTES.
+ * Tokens behind q_start[n_req] are left as they are.  What is written lies apart
+ * from what is read.  ws: CSA2_STATUS_BYTES.
  */
 csa2_status csa2_tree_plan(const int32_t* parent, const int32_t* q_start, const int32_t* kv_len, int64_t n_req,
                            int64_t n_tokens, int32_t max_q, int window, int64_t* pos, uint32_t* mask, int mask_words,
@@ -577,7 +578,7 @@ csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_t stride, i
  *                that undoes csa2_page_plan's taking; their table entries stay.
  *                n_free int32[1], n_free_out int32[1] (may be n_free).
  *   cached       [n_req] int32 out: kv_len - nodes + accepted; left as it is where
- *                a request has no nodes.  Not kv_len itself.
+ *                a request has no nodes.
  *   path         [n_tokens] int32 out: at q_start[r] + j the place of the path's
  *                j-th node among the request's nodes, -1 behind the last one.
  *   accepted     [n_req] int32 out: nodes of the path (0 without nodes).
@@ -590,7 +591,9 @@ csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_t stride, i
  * outside the cache is recorded, and its rows are not moved, or it does not go
  * back; where the free list has no room, that is recorded and nothing goes back.
  * The step is done once: again on the same planes it would move rows that have
- * moved.  ws: CSA2_STATUS_BYTES bytes, zeroed once with csa2_status_reset.
+ * moved.  Path entries behind q_start[n_req] are left as they are.  What is written
+ * lies apart from what is read (n_free_out apart).  ws: CSA2_STATUS_BYTES bytes,
+ * zeroed once with csa2_status_reset.
  */
 csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* token, const int64_t* choice, const int32_t* q_start,
                              const int32_t* kv_len, int64_t n_req, int64_t n_tokens, int32_t max_q, int fmt, uint8_t* codes,

@@ -290,6 +290,17 @@ def test_plan_records_bad_parents_and_lengths(abi):
     assert abi.csa2_status_fetch(p.ws)[0] == abi.ERR_DEVICE_BOUNDS
 
 
+@pytest.mark.parametrize("window", [0, 40])
+def test_plan_loses_what_descends_from_a_bad_parent(abi, window):
+    """Over several words of the mask, with nodes beside it that keep theirs."""
+    parent = trees(np.random.default_rng(1), [200, 9], "chain")
+    parent[70] = 71
+    parent[150] = 30
+    p = Plan(abi, parent, starts([200, 9]), [300, 9], window)
+    assert p.call().check()[2:] == [70, 71]
+    assert (p.pos[70:150] == -1).all() and (p.pos[:70] >= 0).all() and (p.pos[150:209] >= 0).all()
+
+
 # --------------------------------------------------------------- attention
 class Tree:
     """Plan and attention of trees over the pages of attn_inputs."""

@@ -32,11 +32,11 @@ PLAN = dict(parent=F, q_start=F, kv_len=F, n_req=2, n_tokens=40, max_q=33, windo
 ATTN = dict(q=F, n_tokens=4, heads=64, q_start=F, kv_len=F, n_req=2, max_q=2, max_kv=100, pos=F, mask=F, words=1, fmt=0, codes=F,
             scales=F, n_rows=128, table=F, max_pages=8, page=16, window=0, sm_scale=0.04, out=FAR, lse=F, ws=F, ws_bytes=1 << 40,
             stream=None)
-LOGP = dict(x=F, dtype=0, stride=1000, n=3, vocab=1000, scale=1.0, tokens=F, given=2, logprobs=FAR, lse=FAR, entropy=FAR, top=5, ids=FAR,
-            best=FAR, ws=F, ws_bytes=256, stream=None)
-COMMIT = dict(parent=F, token=F, choice=F, q_start=F, kv_len=F, n_req=2, n_tokens=9, max_q=5, fmt=0, codes=F, scales=F, n_rows=64, table=F,
-              max_pages=4, page=16, free=F, n_pages=4, n_free=F, n_free_out=F, cached=2 * F, path=F, accepted=3 * F, next=F, ws=F,
-              ws_bytes=256, stream=None)
+LOGP = dict(x=F, dtype=0, stride=1000, n=3, vocab=1000, scale=1.0, tokens=F, given=2, logprobs=FAR, lse=2 * FAR, entropy=3 * FAR, top=5,
+            ids=4 * FAR, best=5 * FAR, ws=F, ws_bytes=256, stream=None)
+COMMIT = dict(parent=F, token=F, choice=F, q_start=F, kv_len=F, n_req=2, n_tokens=9, max_q=5, fmt=0, codes=5 * FAR, scales=6 * FAR, n_rows=64,
+              table=F, max_pages=4, page=16, free=7 * FAR, n_pages=4, n_free=8 * FAR, n_free_out=8 * FAR, cached=FAR, path=2 * FAR,
+              accepted=3 * FAR, next=4 * FAR, ws=F, ws_bytes=256, stream=None)
 STATUS = {"I": 1, "U": 2, "W": 6}
 
 
@@ -56,7 +56,8 @@ def refused(abi, name, defaults, kw, status):
     (dict(scales=None), "I"), (dict(codes=None), "I"), (dict(dst=None, n_rows=3), "I"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W"),
     (dict(ws=F + 8), "W"),
     (dict(q_out=F + 1024), "I"), (dict(q_out=F, q_stride=65 * 512), "I"), (dict(q_out=2 * FAR + 16), "I"), (dict(q_out=2 * FAR - 16), "I"),
-    (dict(codes=2 * FAR), "I"), (dict(codes=FAR + 64), "I"), (dict(scales=3 * FAR + 64 * 256 - 16), "I"), (dict(scales=F), "I")])
+    (dict(codes=2 * FAR), "I"), (dict(codes=FAR + 64), "I"), (dict(scales=3 * FAR + 64 * 256 - 16), "I"), (dict(scales=F), "I"),
+    (dict(pos=FAR + 32), "I"), (dict(dst=3 * FAR), "I"), (dict(qw=FAR + 4096), "I"), (dict(table=4 * FAR - 64), "I")])
 def test_head_refusals(abi, kw, status):
     refused(abi, "csa2_head_norm_rope", HEADS, kw, status)
 
@@ -66,7 +67,7 @@ def test_head_refusals(abi, kw, status):
     (dict(mask=None), "I"), (dict(mask=F + 4), "I"), (dict(words=1), "I"), (dict(words=3), "I"), (dict(window=-1), "I"), (dict(n_req=-1), "I"),
     (dict(n_tokens=-1), "I"), (dict(max_q=-1), "I"), (dict(max_q=1025, words=33), "U"), (dict(n_tokens=(1 << 22) + 1), "U"),
     (dict(n_req=(1 << 20) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=0), "W"), (dict(pos=F), "I"), (dict(mask=F + 16), "I"),
-    (dict(mask=FAR + 8 * 40 - 16), "I")])
+    (dict(mask=FAR + 8 * 40 - 16), "I"), (dict(q_start=FAR), "I"), (dict(kv_len=2 * FAR + 8 * 40 - 16), "I")])
 def test_plan_refusals(abi, kw, status):
     refused(abi, "csa2_tree_plan", PLAN, kw, status)
 
@@ -87,7 +88,8 @@ def test_attention_refusals(abi, kw, status):
     (dict(given=-1), "I"), (dict(given=65), "U"), (dict(top=-1), "I"), (dict(top=65), "U"), (dict(tokens=None), "I"), (dict(logprobs=None), "I"),
     (dict(ids=None), "I"), (dict(best=None), "I"), (dict(tokens=F + 8), "I"), (dict(lse=FAR + 4), "I"), (dict(best=FAR + 8), "I"),
     (dict(ws=None), "W"), (dict(ws_bytes=255), "W"), (dict(lse=F), "I"), (dict(ids=F + 5984), "I"), (dict(entropy=F - 0 + 16), "I"),
-    (dict(best=F - 32), "I"), (dict(logprobs=F + 2000), "I")])
+    (dict(best=F - 32), "I"), (dict(logprobs=F + 2000), "I"), (dict(tokens=2 * FAR), "I"), (dict(entropy=2 * FAR), "I"),
+    (dict(best=4 * FAR + 48), "I"), (dict(stride=(1 << 36) + 4), "I")])
 def test_logprobs_refusals(abi, kw, status):
     refused(abi, "csa2_token_logprobs", LOGP, kw, status)
 
@@ -99,7 +101,9 @@ def test_logprobs_refusals(abi, kw, status):
     (dict(scales=None), "I"), (dict(codes=None), "I"), (dict(fmt=1), "I"), (dict(fmt=2), "U"), (dict(page=12), "U"), (dict(page=0), "U"),
     (dict(n_req=-1), "I"), (dict(n_tokens=-1), "I"), (dict(max_q=-1), "I"), (dict(n_rows=-1), "I"), (dict(max_pages=-1), "I"),
     (dict(n_pages=1 << 31), "I"), (dict(max_q=1025), "U"), (dict(n_req=(1 << 20) + 1), "U"), (dict(ws=None), "W"), (dict(ws_bytes=255), "W"),
-    (dict(cached=F), "I"), (dict(accepted=F), "I"), (dict(accepted=2 * F), "I")])
+    (dict(cached=F), "I"), (dict(accepted=F), "I"), (dict(accepted=FAR), "I"), (dict(path=F + 16), "I"), (dict(next=F + 64), "I"),
+    (dict(free=F), "I"), (dict(codes=F - 64), "I"), (dict(scales=5 * FAR + 64 * 256 - 16), "I"), (dict(n_free_out=7 * FAR + 12), "I"),
+    (dict(n_free=FAR + 4), "I"), (dict(table=2 * FAR + 32), "I"), (dict(next=3 * FAR), "I")])
 def test_commit_refusals(abi, kw, status):
     refused(abi, "csa2_tree_commit", COMMIT, kw, status)
 
@@ -137,7 +141,7 @@ def test_cache_refusals(abi):
                 lambda: c.append_heads(q, lat, 8, latent_norm=torch.zeros(512)), lambda: c.append_heads(q, lat, 8, eps=-1.0),
                 lambda: c.append_heads(q, lat.to("meta"), 8), lambda: c.tree(par, 9, 4), lambda: c.tree(par, 8, 9), lambda: c.tree(par, 8, -1),
                 lambda: c.tree(tok, 8, 4), lambda: c.tree(par[:4], 8, 4), lambda: c.attend_tree(q, 8, 9, 16), lambda: c.attend_tree(q, 9, 4, 16),
-                lambda: c.attend_tree(q[:, :2], 8, 4, 16), lambda: c.workspace(8, 4, (1 << 31) - 1, tree=True), lambda: c.workspace(8, 1025, 16, tree=True),
+                lambda: c.attend_tree(q[:, :2], 8, 4, 16), lambda: c.attend_tree(q, 8, 4, 16), lambda: c.workspace(8, 4, (1 << 31) - 1, tree=True), lambda: c.workspace(8, 1025, 16, tree=True),
                 lambda: c.commit(par, tok, tok[:3], 8, 4), lambda: c.commit(par, par, tok, 8, 4), lambda: c.commit(par, tok, tok, 8, 9),
                 lambda: c.commit(tok, tok, tok, 8, 4), lambda: c.commit(par.to("meta"), tok, tok, 8, 4)):
         with pytest.raises(ValueError):
