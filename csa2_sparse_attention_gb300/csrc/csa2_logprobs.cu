@@ -14,16 +14,17 @@
 // walks over rows and has the next one's first vectors under way while it joins its
 // threads' parts.
 //
-// The k largest: every group's maximum stays in shared memory.  One warp finds the
-// k-th largest of the threads' maxima to 16 bits, which k values reach; the few
-// groups that do are read again (from L2), a vector a thread, and their values that
-// do are ranked by counting.
+// The k largest: every group's maximum stays in shared memory.  The threads form
+// teams, and the k-th largest of the teams' maxima is a value that k values reach;
+// the few groups that do are read again (from L2), a vector a thread, and their
+// values that do are ranked by counting.
 #include "csa2_common.cuh"
 #include "csa2_timer.cuh"
 
 #include <atomic>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 namespace csa2 {
 
@@ -33,6 +34,10 @@ constexpr int kLMaxTurns = 64;     // groups of a thread
 constexpr int kLTop = CSA2_LOGPROBS_TOP;
 constexpr int kLCands = 1024;      // values that are ranked
 constexpr int kLHits = 512;        // groups that are read again at once
+// Teams: 32 of 8 threads for up to kLFew alternatives, 128 of 2 for more (threads that
+// far apart, so that neighbours' values fall into different ones).  Of random values,
+// 30 of 256 threads' maxima reach the 20th largest of 32 teams', 75 the 64th of 128.
+constexpr int kLFew = 24;
 constexpr int kLMaxCluster = 8;
 constexpr float kLFloor = -160.f;  // exponents below it are nothing in fp32
 constexpr float kLReach = 4.f;     // a thread's base: this far above a maximum, moved for a value this far above it
@@ -56,7 +61,7 @@ struct LogSmem {
     unsigned long long list[kLTop];    // the slice's largest, in order
     float max, sum, tilt;              // of the slice: m, S, sum(e^y y)
     int bad, listed, n_cand, n_hits;
-    uint32_t keys[kLThreads], bar;     // of the threads' maxima, and the one that is reached
+    uint32_t keys[kLThreads];          // of the threads' maxima
     uint16_t hits[kLHits];
     float red[3][kLWarps];
     int redi[kLWarps];
@@ -110,9 +115,8 @@ __device__ __forceinline__ void add_kept(float& sum, float& rest, float v) {
     rest = y - (t - sum);
     sum = t;
 }
-__device__ __forceinline__ void cluster_meet() {
-    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 // The same variable of another block of the cluster.
 template <typename T>
 __device__ __forceinline__ uint32_t peer(const T* p, uint32_t rank) {
@@ -269,131 +273,139 @@ template <typename T>
 __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& row, int32_t v0, int32_t v1, int turns, float mine, int k) {
     constexpr int E = RowView<T>::E;
     const int tid = threadIdx.x;
-    // the k-th largest of the threads' maxima, rounded down to 16 bits (0 where fewer have any)
+    const int lane = tid & 31;
     S.keys[tid] = mine > -INFINITY ? float_key(mine) : 0u;
     if (tid == 0) S.n_hits = S.n_cand = 0;
     __syncthreads();
-    auto kth = [&](uint32_t bar, int from, int to) {  // its bits `from` down to `to`, by the first warp
-        if (tid < 32) {
-            uint32_t own[kLThreads / 32];
+    // the k-th largest of the teams' maxima (0 where fewer have any), by every warp
+    uint32_t bar = 0;
+    auto reach = [&](auto teams) {
+        constexpr int N = decltype(teams)::value / 32;
+        uint32_t own[N];
+        int n[N] = {};
 #pragma unroll
-            for (int i = 0; i < kLThreads / 32; ++i) own[i] = S.keys[32 * i + tid];
-#pragma unroll 1
-            for (int b = from - 1; b >= to; b -= 2) {  // two bits at a time
-                uint32_t n[3] = {0, 0, 0};
+        for (int i = 0; i < N; ++i) {
+            own[i] = S.keys[32 * i + lane];
 #pragma unroll
-                for (int i = 0; i < kLThreads / 32; ++i)
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) n[e] += own[i] >= (bar | (uint32_t(e + 1) << b));
-                uint32_t bits = 0;
-#pragma unroll
-                for (int e = 0; e < 3; ++e) bits += __reduce_add_sync(0xffffffffu, n[e]) >= uint32_t(k);
-                bar |= bits << b;
+            for (int j = i + N; j < kLThreads / 32; j += N) {
+                const uint32_t u = S.keys[32 * j + lane];
+                own[i] = own[i] > u ? own[i] : u;
             }
-            if (tid == 0) S.bar = bar;
         }
-        __syncthreads();
-        return S.bar;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t u = __shfl_sync(0xffffffffu, own[i], j);
+#pragma unroll
+                for (int e = 0; e < N; ++e) n[e] += u >= own[e];
+            }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (n[i] >= k && own[i] > bar) bar = own[i];
+        bar = __reduce_max_sync(0xffffffffu, bar);
     };
-    uint32_t bar = kth(0, 31, 16);
+    if (k <= kLFew) reach(std::integral_constant<int, 32>());
+    else reach(std::integral_constant<int, 128>());
     const uint32_t low = float_key(-INFINITY) + 1;  // -inf is no alternative
     if (bar < low) bar = low;
-    const float reached = key_float(bar);
-    for (int j = 0; j < turns; ++j)
-        if (groups[j * kLThreads + tid] >= reached) {
-            const int at = atomicAdd(&S.n_hits, 1);
-            if (at < kLHits) S.hits[at] = uint16_t(j * kLThreads + tid);
-        }
-    __syncthreads();
-    const int n_hits = S.n_hits;
-    if (n_hits <= kLHits) {
-        for (int i = tid; i < kLGroup * n_hits; i += kLThreads) {
-            const int group = S.hits[i / kLGroup], j = group / kLThreads;
-            const int32_t v = v0 + (j * kLGroup + i % kLGroup) * kLThreads + (group - j * kLThreads);
-            if (v >= v1) continue;
-            float x[E];
-            row.values(row.load(v), x);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (float_key(x[e]) >= bar) {
-                    const int at = atomicAdd(&S.n_cand, 1);
-                    if (at < kLCands) S.cand[at] = ranked(x[e], v * E - row.head + e);
-                }
+    // The values at the bar or above; where they are too many for the lists, as where a mask leaves less than k above its
+    // own value, those above it.
+    int n;
+    uint32_t from = bar;
+#pragma unroll 1
+    for (;; ++from) {
+        const float reached = key_float(from);
+        for (int j = 0; j < turns; ++j) {
+            const uint32_t those = __ballot_sync(0xffffffffu, groups[j * kLThreads + tid] >= reached);
+            if (those == 0) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&S.n_hits, __popc(those));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(those & ((1u << lane) - 1));
+            if ((those >> lane & 1) && at < kLHits) S.hits[at] = uint16_t(j * kLThreads + tid);
         }
         __syncthreads();
-    }
-    // visits the values of the groups whose maximum's key is `from` or more
-    auto visit = [&](uint32_t from, auto f) {
-        for (int j = 0; j < turns; ++j) {
-            if (float_key(groups[j * kLThreads + tid]) < from) continue;
-#pragma unroll
-            for (int g = 0; g < kLGroup; ++g) {
-                const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+        const int n_hits = S.n_hits;
+        n = INT_MAX;
+        if (n_hits <= kLHits) {
+            for (int i = tid; i < kLGroup * n_hits; i += kLThreads) {
+                const int group = S.hits[i / kLGroup], j = group / kLThreads;
+                const int32_t v = v0 + (j * kLGroup + i % kLGroup) * kLThreads + (group - j * kLThreads);
                 if (v >= v1) continue;
                 float x[E];
                 row.values(row.load(v), x);
+                uint32_t bits = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) f(x[e], v * E - row.head + e);
+                for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) >= from) << e;
+                if (bits == 0) continue;
+                int at = atomicAdd(&S.n_cand, __popc(bits));
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (bits >> e & 1) {
+                        if (at < kLCands) S.cand[at] = ranked(x[e], v * E - row.head + e);
+                        ++at;
+                    }
+            }
+            __syncthreads();
+            n = S.n_cand;
+        }
+        if (n <= kLCands || from > bar) break;
+        __syncthreads();
+        if (tid == 0) S.n_hits = S.n_cand = 0;
+        __syncthreads();
+    }
+    if (n < k && from > bar) {  // the first ones at the bar, in the row's order
+        const float reached = key_float(bar);
+        for (int j = 0; j < turns && n < k; ++j) {
+            const bool near = groups[j * kLThreads + tid] >= reached;
+            for (int g = 0; g < kLGroup && n < k; ++g) {
+                const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                uint32_t bits = 0;  // of the vector's values at the bar
+                if (near && v < v1) {
+                    float x[E];
+                    row.values(row.load(v), x);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) == bar) << e;
+                }
+                int all, at = n + block_before(S, __popc(bits), all);
+                for (; bits != 0 && at < k; bits &= bits - 1, ++at)
+                    S.cand[at] = ranked(key_float(bar), v * E - row.head + __ffs(bits) - 1);
+                n = n + all < k ? n + all : k;
             }
         }
-    };
-    auto collect = [&](unsigned long long from) {
-        visit(uint32_t(from >> 32), [&](float x, int32_t i) {
-            const unsigned long long c = ranked(x, i);
-            if (c >= from) {
-                const int at = atomicAdd(&S.n_cand, 1);
-                if (at < kLCands) S.cand[at] = c;
-            }
-        });
-    };
-    auto collect_all = [&](unsigned long long from) {  // how many there are
         __syncthreads();
-        if (tid == 0) S.n_cand = 0;
-        __syncthreads();
-        collect(from);
-        __syncthreads();
-        return S.n_cand;
-    };
-    int n = S.n_cand;
-    if (n_hits > kLHits || n > kLCands) {
-        // Many values at the bar, as where a mask leaves less than k of a row above its own value: the ones above it, and the
-        // first ones at it in the row's order.
-        __syncthreads();
-        bar = kth(bar & 0xFFFF0000u, 15, 0);
-        if (bar < low) bar = low;
-        n = collect_all(static_cast<unsigned long long>(bar + 1) << 32);
-        if (n < k) {
-            for (int j = 0; j < turns && n < k; ++j) {
-                const bool near = float_key(groups[j * kLThreads + tid]) >= bar;
-                for (int g = 0; g < kLGroup && n < k; ++g) {
-                    const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
-                    uint32_t bits = 0;  // of the vector's values at the bar
-                    if (near && v < v1) {
-                        float x[E];
-                        row.values(row.load(v), x);
+    } else if (n > kLCands) {
+        // Many different ones, in the places of few threads: the k-th largest pair of value and index, bit by bit.
+        auto visit = [&](uint32_t from, auto f) {  // the values of the groups whose maximum's key is `from` or more
+            for (int j = 0; j < turns; ++j) {
+                if (float_key(groups[j * kLThreads + tid]) < from) continue;
 #pragma unroll
-                        for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) == bar) << e;
-                    }
-                    int all, at = n + block_before(S, __popc(bits), all);
-                    for (; bits != 0 && at < k; bits &= bits - 1, ++at)
-                        S.cand[at] = ranked(key_float(bar), v * E - row.head + __ffs(bits) - 1);
-                    n = n + all < k ? n + all : k;
+                for (int g = 0; g < kLGroup; ++g) {
+                    const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                    if (v >= v1) continue;
+                    float x[E];
+                    row.values(row.load(v), x);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) f(x[e], v * E - row.head + e);
                 }
             }
-        } else if (n > kLCands) {
-            // Many different ones, in the places of few threads: the k-th largest pair of value and index, bit by bit.
-            unsigned long long edge = 0;
+        };
+        unsigned long long edge = 0;
 #pragma unroll 1
-            for (int b = 63; b >= 0; --b) {
-                const unsigned long long up = edge | (1ull << b);
-                int some = 0, all;
-                visit(uint32_t(up >> 32) > low ? uint32_t(up >> 32) : low, [&](float x, int32_t i) { some += ranked(x, i) >= up; });
-                block_before(S, some, all);
-                if (all >= k) edge = up;
-            }
-            n = collect_all(edge);
+        for (int b = 63; b >= 0; --b) {
+            const unsigned long long up = edge | (1ull << b);
+            int some = 0, all;
+            visit(uint32_t(up >> 32) > low ? uint32_t(up >> 32) : low, [&](float x, int32_t i) { some += ranked(x, i) >= up; });
+            block_before(S, some, all);
+            if (all >= k) edge = up;
         }
+        if (tid == 0) S.n_cand = 0;
         __syncthreads();
+        visit(uint32_t(edge >> 32), [&](float x, int32_t i) {
+            if (ranked(x, i) >= edge) S.cand[atomicAdd(&S.n_cand, 1)] = ranked(x, i);  // (k of them)
+        });
+        __syncthreads();
+        n = S.n_cand;
     }
     for (int i = tid; i < n; i += kLThreads) {
         const unsigned long long c = S.cand[i];
@@ -539,7 +551,8 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
         }
         // ---- the row's
         if (cluster > 1) {
-            cluster_meet();
+            cluster_arrive();
+            cluster_wait();
             if (rank == 0) {
                 if (tid < cluster) {
                     S.all_f[tid][0] = __uint_as_float(peer_u32(peer(&S.max, tid)));
@@ -555,8 +568,11 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
                 b = __syncthreads_or(b);
                 if (tid == 0) S.all_bad = b;
             }
-            cluster_meet();  // the others' parts are read
-            if (rank != 0) continue;
+            cluster_arrive();  // the others' parts are read
+            if (rank != 0) {
+                cluster_wait();
+                continue;
+            }
         } else {
             __syncthreads();
             if (tid == 0) {
@@ -595,15 +611,15 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
             if (e >= S.all_n[q]) continue;
             const unsigned long long v = S.all[q][e];
             int at = e;
-            for (int o = 0; o < cluster; ++o) {
-                if (o == q) continue;
-                int lo = 0, hi = S.all_n[o];  // how many of list o are larger
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (S.all[o][mid] > v) lo = mid + 1;
-                    else hi = mid;
-                }
-                at += lo;
+            if (cluster > 1) {
+                int larger[kLMaxCluster] = {};  // of every list, its own among them: searched side by side
+                for (int half = 1 << (31 - __clz(a.top)); half > 0; half >>= 1)
+#pragma unroll
+                    for (int o = 0; o < kLMaxCluster; ++o)
+                        if (o < cluster && larger[o] + half <= S.all_n[o] && S.all[o][larger[o] + half - 1] > v) larger[o] += half;
+                at = 0;
+#pragma unroll
+                for (int o = 0; o < kLMaxCluster; ++o) at += larger[o];
             }
             if (at < a.top) {
                 a.ids[r * a.top + at] = int32_t(~uint32_t(v));
@@ -611,6 +627,7 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
             }
         }
         __syncthreads();  // the next row writes where this one's parts were read
+        if (cluster > 1) cluster_wait();
     }
 }
 
@@ -672,12 +689,18 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
     a.given = given;
     a.top = top;
     a.scale = scale;
-    // A row in as many slices as keep all multiprocessors busy and leave a slice a vector per thread; and so many that the
-    // groups' maxima find room.
+    // A row in slices, so that all multiprocessors have a block of at least a vector per thread, or two blocks of 16 vectors
+    // per thread; and so many that the groups' maxima find room.  (us, with 1 / 2 / 4 / 8 slices and 20 alternatives: 30 rows
+    // of 32000 fp32 8.2 / 8.2 / 7.9 / 8.8, 61 rows 8.2 / 8.4 / 8.4 / 11; 61 of 100003 14 / 13 / 11 / 14, 152 of them
+    // 24 / 19 / 26 / 26; 76 of 131072 bf16 13 / 11.5 / 15 / 19: clusters of four and more are not placed evenly.)
     const int64_t nv = vocab * size / 16 + 2;  // vectors of a row, wherever it begins
+    auto fits = [&](int64_t c) {
+        const int64_t sms = sm_count(), per_thread = nv / (c * kLThreads);
+        return (n * c <= sms && per_thread >= 1) || (n * c <= (c == 2 ? 2 * sms : sms * 13 / 8) && per_thread >= 16);
+    };
     int cluster = 1;
-    while (cluster < kLMaxCluster && ((n * cluster * 2 <= 4 * int64_t(sm_count()) && nv / (2 * cluster) >= kLThreads) ||
-                                      ceil_div<int64_t>(ceil_div<int64_t>(nv, cluster), kLThreads * kLGroup) > kLMaxTurns))
+    while (cluster < kLMaxCluster &&
+           (fits(2 * cluster) || ceil_div<int64_t>(ceil_div<int64_t>(nv, cluster), kLThreads * kLGroup) > kLMaxTurns))
         cluster *= 2;
     a.slice = int32_t(ceil_div<int64_t>(nv, cluster));
     const int64_t turns = ceil_div<int64_t>(a.slice, kLThreads * kLGroup);

@@ -665,6 +665,27 @@ def test_logprobs_masks_and_ties(abi, dtype, V):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [9, 320])
+def test_logprobs_of_few_values_above_a_mask(abi, dtype, n):
+    """Masks of the lowest value or -inf that leave less than there are alternatives, or hardly more; the lowest value
+    itself among -inf; rows that fall and rise, so that neighbours hold the largest."""
+    rng = np.random.default_rng(8)
+    V = 30011
+    x = logits(rng, n, V, dtype)
+    low = torch.finfo(dtype).min
+    for r in range(n):
+        kept = rng.choice(V, (0, 3, 19, 20, 21, 33, 64, 200, 1500)[r % 9], replace=False)
+        y = torch.full((V,), low if r % 2 else -math.inf, dtype=dtype)
+        y[kept] = x[r, kept]
+        x[r] = y
+    x[0, 5:5 * 7:5] = low
+    x[4 % n] = torch.linspace(9.0, -9.0, V).to(dtype)
+    x[7 % n] = torch.linspace(-9.0, 9.0, V).to(dtype)
+    Logp(abi, x, picks(rng, n, V, 1), 20).call().check()
+    Logp(abi, x[:9], None, 64).call().check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_logprobs_of_alternatives_in_few_places(abi, dtype):
     """The large values all lie in what a few threads see: more of them than are ranked at once."""
     E = 4 if dtype == torch.float32 else 8
