@@ -242,7 +242,7 @@ static_assert(kPSms <= 256, "a thread a cut");
 //   4, 2K to 8K: 6 46 49 75, 8 51 52 63, 12 67 63 70, 16 76 71 91, 32 129 108 157;  2: 8 38 39 37, 32 73 70 81
 //   8: 8 of 512 to 2K 37 37 57, 32 of them - 72 65, 64 of them - 113 110;  64: 8 of 512 to 2K 132 147 147, 16 233 221 220
 //   24 of up to 45 x 16 heads, window 128: 26 - 21
-constexpr int64_t kWalkRows = 48 * 64, kWalkMost = 512, kWalkTileRows = 3 * 38 * 256;
+constexpr int64_t kWalkRows = 45 * 64, kWalkMost = 512, kWalkTileRows = 3 * 38 * 256;
 constexpr int32_t kWalkKeys = 8, kWalkTileKeys = 24;  // key tiles
 struct PagedShare {  // of one of the kernels
     int32_t chunk = 1, splits = 1;         // as the partial outputs are sized

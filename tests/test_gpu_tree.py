@@ -527,11 +527,71 @@ def test_attention_many_requests(abi):
     assert Tree(abi, s, trees(rng, nodes)).call().check()[0] == abi.OK
 
 
+def walk_inputs(rng, n_req, H, kind, longest, page, fmt):
+    """Requests of very unequal numbers of nodes and entries, some without any; "few": with one of more than 256 rows (or
+    very many), "tiles": of more than 512 rows on average."""
+    if kind == "few":
+        nodes = rng.integers(0, 4, n_req)
+        nodes[n_req // 3] = 256 // H + 3
+    else:
+        nodes = rng.integers(0, 1024 // H + 6, n_req)
+        nodes[-1] = 0
+    cached = (longest * rng.random(n_req) ** 4).astype(np.int64)
+    cached[n_req // 2], cached[0] = longest, 0
+    nodes[n_req // 2] = max(nodes[n_req // 2], 1)
+    s = attn_inputs(rng, cached + nodes, nodes, H, page, fmt, tail=1)
+    return s, trees(rng, nodes)
+
+
+@pytest.mark.parametrize("n_req,H,kind,longest,page,fmt,window", [
+    (2, 64, "few", 1100, 16, "fp4", 0), (3, 16, "few", 5000, 64, "fp8", 0), (33, 8, "few", 1500, 8, "fp4", 0), (40, 8, "few", 1300, 8, "fp8", 1050),
+    (150, 8, "few", 1100, 16, "fp4", 0), (600, 8, "few", 1200, 8, "fp4", 0), (2, 64, "tiles", 3400, 64, "fp4", 0),
+    (5, 64, "tiles", 4100, 16, "fp8", 3200), (35, 32, "tiles", 3300, 16, "fp4", 0)])
+def test_attention_walks(abi, n_req, H, kind, longest, page, fmt, window):
+    """Several requests' items laid out by their real lengths: more of them than groups of CTAs and fewer, more requests than
+    a warp and than a block look at at once."""
+    rng = np.random.default_rng(n_req + H)
+    s, parent = walk_inputs(rng, n_req, H, kind, longest, page, fmt)
+    t = Tree(abi, s, parent, window).call()
+    assert t.check()[0] == abi.OK
+    first, lse = t.out.clone(), t.lse.clone()
+    t.call()
+    assert t.check()[0] == abi.OK and torch.equal(first, t.out) and torch.equal(lse, t.lse)
+
+
+@pytest.mark.parametrize("n_req,H,kind,longest", [(40, 8, "few", 1300), (12, 64, "tiles", 3300)])
+def test_attention_walks_around_bad_requests(abi, n_req, H, kind, longest):
+    """Requests whose token bounds do not hold are skipped and recorded, and all others are as before."""
+    rng = np.random.default_rng(18)
+    s, parent = walk_inputs(rng, n_req, H, kind, longest, 16, "fp4")
+    t = Tree(abi, s, parent).call()
+    assert t.check()[0] == abi.OK
+    out, lse = t.out.clone(), t.lse.clone()
+    for place, value in ((n_req // 4, s["T"] + 9), (n_req - 2, -3)):
+        bad = s["q_start"].copy()
+        bad[place] = value
+        t.q_start.copy_(dev(bad))
+        t.out.fill_(7.0)
+        t.lse.fill_(7.0)
+        t.call()
+        torch.cuda.synchronize()
+        assert abi.csa2_status_fetch(t.ws)[0] == abi.ERR_DEVICE_BOUNDS
+        abi.csa2_status_reset(t.ws)
+        left = np.zeros(s["T"], bool)
+        left[s["q_start"][place - 1]:s["q_start"][place + 1]] = True
+        left[s["q_start"][-1]:] = True
+        assert (t.out[left] == 7).all() and (t.lse[left] == 7).all()
+        a, b = f64(t.out)[~left], f64(out)[~left]
+        assert np.abs(a - b).max() <= 2.0 ** -6 * np.abs(b).max()
+        a, b = f64(t.lse)[~left], f64(lse)[~left]
+        assert np.array_equal(np.isneginf(a), np.isneginf(b)) and np.abs(a - b)[np.isfinite(b)].max() <= 2.0 ** -14
+
+
 def test_attention_gives_up_and_recovers(abi):
     """Bounded waits that run out are recorded, and the next call is as if nothing had been."""
     rng = np.random.default_rng(17)
-    for nodes in ([5, 3], [70, 66]):
-        s = attn_inputs(rng, np.array([900, 400]) + nodes, nodes, 64, 16, "fp4")
+    for nodes, longest in (([5, 3], 900), ([70, 66], 900), ([70, 66], 3300)):
+        s = attn_inputs(rng, np.array([longest, 400]) + nodes, nodes, 64, 16, "fp4")
         t = Tree(abi, s, trees(rng, nodes))
         t.call()
         torch.cuda.synchronize()
