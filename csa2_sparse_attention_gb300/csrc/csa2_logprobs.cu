@@ -666,11 +666,12 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
     if (!logits || stride < vocab || stride > (int64_t(1) << 36)) return CSA2_ERR_INVALID_ARG;
     if (given > 0 && (!tokens || !logprobs)) return CSA2_ERR_INVALID_ARG;
     if (top > 0 && (!ids || !best)) return CSA2_ERR_INVALID_ARG;
-    for (const void* p : {logits, static_cast<const void*>(tokens), static_cast<const void*>(logprobs), static_cast<const void*>(lse),
-                          static_cast<const void*>(entropy), static_cast<const void*>(ids), static_cast<const void*>(best)})
+    for (const void* p : {static_cast<const void*>(logprobs), static_cast<const void*>(lse), static_cast<const void*>(entropy),
+                          static_cast<const void*>(ids), static_cast<const void*>(best)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
-    if (n == 0) return CSA2_OK;
     const int64_t size = dtype == CSA2_OUT_BF16 ? 2 : 4, in = ((n - 1) * stride + vocab) * size;
+    if (reinterpret_cast<uintptr_t>(logits) % uint64_t(size) || reinterpret_cast<uintptr_t>(tokens) % 8) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
     const Span outs[] = {{logprobs, n * given * 4}, {lse, n * 4}, {entropy, n * 4}, {ids, n * top * 4}, {best, n * top * 4}};
     const Span ins[] = {{logits, in}, {tokens, n * given * 8}};
     if (!apart(outs, ins)) return CSA2_ERR_INVALID_ARG;

@@ -542,12 +542,13 @@ csa2_status csa2_tree_attn(const void* q_bf16, int64_t n_tokens, int n_heads, co
  *   lse = m * scale + log S, entropy = log S - sum(e^y y) / S,
  *   log probability of token t: y_t - log S.
  *   logits       [n] rows of vocab elements, stride elements apart (>= vocab;
- *                rows may begin anywhere), bf16 (dtype CSA2_OUT_BF16) or fp32
- *                (CSA2_OUT_F32).  vocab 1..2^21, n up to 2^24.
+ *                rows, the first one too, may begin at any element), bf16 (dtype
+ *                CSA2_OUT_BF16) or fp32 (CSA2_OUT_F32).  vocab 1..2^21, n up to
+ *                2^24.
  *   scale        of the logits (one over a temperature), 2^-20..2^20.
- *   tokens       [n][given] int64, given 0..64; logprobs [n][given] fp32 out.  A
- *                token of -1 is none: -inf.  Others outside [0, vocab) give -inf
- *                and are recorded.
+ *   tokens       [n][given] int64 (8-byte aligned), given 0..64; logprobs
+ *                [n][given] fp32 out.  A token of -1 is none: -inf.  Others
+ *                outside [0, vocab) give -inf and are recorded.
  *   lse, entropy [n] fp32 out, or NULL.
  *   top          0..64 alternatives: ids [n][top] int32 and best [n][top] fp32 out,
  *                the tokens of the largest logits and their log probabilities,

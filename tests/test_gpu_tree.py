@@ -610,16 +610,17 @@ def test_attention_gives_up_and_recovers(abi):
 # ------------------------------------------------------- log probabilities
 class Logp:
     def __init__(self, abi, x, tokens, top, scale=1.0, gap=0, shift=0):
-        """x: a CPU tensor [n][V] of bf16 or fp32; rows `gap` elements apart, the first one `shift` elements in (of a
-        16-byte aligned row that begins at 0: shift goes into the row's view)."""
+        """x: a CPU tensor [n][V] of bf16 or fp32; rows `gap` elements apart, the first one `shift` elements behind a 16-byte
+        border, the tokens as many behind theirs."""
         self.abi, self.top, self.scale = abi, top, scale
         n, V = x.shape
         self.n, self.V, self.x64 = n, V, x.double().numpy()
-        self.flat = torch.full((n * (V + gap) + 64,), float("nan"), dtype=x.dtype)
-        self.flat[:n * (V + gap)].view(n, V + gap)[:, :V] = x
-        self.flat = self.flat.cuda()
+        self.flat = torch.full((n * (V + gap) + 64 + shift,), float("nan"), dtype=x.dtype)
+        self.flat[shift:shift + n * (V + gap)].view(n, V + gap)[:, :V] = x
+        self.flat = self.flat.cuda()[shift:]
         self.stride = V + gap
-        self.tokens = dev(np.asarray(tokens, np.int64)) if tokens is not None and np.size(tokens) else None
+        flat = np.concatenate([np.zeros(shift), np.ravel(tokens)]).astype(np.int64) if tokens is not None else None
+        self.tokens = dev(flat)[shift:] if flat is not None and np.size(tokens) else None
         self.tok64 = np.asarray(tokens).reshape(n, -1) if tokens is not None else np.zeros((n, 0), np.int64)
         self.given = self.tok64.shape[1]
         f = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
@@ -688,6 +689,13 @@ def picks(rng, n, V, given):
 def test_logprobs(abi, n, V, given, top, gap, dtype):
     rng = np.random.default_rng(n + V)
     assert Logp(abi, logits(rng, n, V, dtype), picks(rng, n, V, given), top, gap=gap).call().check()[0] == abi.OK
+
+
+@pytest.mark.parametrize("dtype,shift", [(torch.float32, 1), (torch.float32, 3), (torch.bfloat16, 1), (torch.bfloat16, 6)])
+@pytest.mark.parametrize("n,V,gap", [(1, 3, 0), (1, 5001, 0), (7, 8192, 0), (5, 40001, 2)])
+def test_logprobs_of_rows_from_any_element(abi, dtype, shift, n, V, gap):
+    rng = np.random.default_rng(n + V)
+    Logp(abi, logits(rng, n, V, dtype), picks(rng, n, V, 1), 3, gap=gap, shift=shift).call().check()
 
 
 @pytest.mark.parametrize("scale", [2.0 ** -20, 0.1, 1.25, 37.0, 2.0 ** 20])

@@ -82,11 +82,11 @@ def test_attention_refusals(abi, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(x=None), "I"), (dict(x=F + 4), "I"), (dict(dtype=2), "U"), (dict(stride=999), "I"), (dict(n=-1), "I"), (dict(vocab=0), "I"),
+    (dict(x=None), "I"), (dict(x=F + 1), "I"), (dict(x=F + 2, dtype=1), "I"), (dict(dtype=2), "U"), (dict(stride=999), "I"), (dict(n=-1), "I"), (dict(vocab=0), "I"),
     (dict(vocab=(1 << 21) + 1, stride=1 << 22), "U"), (dict(n=(1 << 24) + 1), "U"), (dict(scale=0.0), "I"), (dict(scale=-1.0), "I"),
     (dict(scale=float("nan")), "I"), (dict(scale=float("inf")), "I"), (dict(scale=2.0 ** -21), "U"), (dict(scale=2.0 ** 21), "U"),
     (dict(given=-1), "I"), (dict(given=65), "U"), (dict(top=-1), "I"), (dict(top=65), "U"), (dict(tokens=None), "I"), (dict(logprobs=None), "I"),
-    (dict(ids=None), "I"), (dict(best=None), "I"), (dict(tokens=F + 8), "I"), (dict(lse=FAR + 4), "I"), (dict(best=FAR + 8), "I"),
+    (dict(ids=None), "I"), (dict(best=None), "I"), (dict(tokens=F + 4), "I"), (dict(lse=FAR + 4), "I"), (dict(best=FAR + 8), "I"),
     (dict(ws=None), "W"), (dict(ws_bytes=255), "W"), (dict(lse=F), "I"), (dict(ids=F + 5984), "I"), (dict(entropy=F - 0 + 16), "I"),
     (dict(best=F - 32), "I"), (dict(logprobs=F + 2000), "I"), (dict(tokens=2 * FAR), "I"), (dict(entropy=2 * FAR), "I"),
     (dict(best=4 * FAR + 48), "I"), (dict(stride=(1 << 36) + 4), "I")])
