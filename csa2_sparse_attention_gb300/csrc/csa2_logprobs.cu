@@ -37,7 +37,7 @@ namespace csa2 {
 
 constexpr int kLThreads = 256, kLWarps = kLThreads / 32;
 constexpr int kLGroup = 4;         // vectors of a group
-constexpr int kLMaxTurns = 64;     // groups of a thread
+constexpr int kLMaxTurns = 65;     // groups of a thread: 2^21 fp32 values in eight slices, and a vector for where a row begins
 constexpr int kLTop = CSA2_LOGPROBS_TOP;
 constexpr int kLCands = 1024;      // values that are ranked
 constexpr int kLHits = 512;        // groups that are read again at once

@@ -790,6 +790,15 @@ def test_logprobs_tokens_outside_are_recorded(abi):
         assert st[0] == abi.ERR_DEVICE_BOUNDS and st[2] == 1
 
 
+@pytest.mark.parametrize("dtype,gap,shift", [(torch.float32, 0, 0), (torch.float32, 1, 3), (torch.bfloat16, 3, 7)])
+def test_logprobs_of_the_largest_vocabulary(abi, dtype, gap, shift):
+    rng = np.random.default_rng(9)
+    V = 1 << 21
+    x = logits(rng, 2, V, dtype)
+    x[0, V - 1], x[1, 0] = 40.0, 40.0
+    Logp(abi, x, np.array([[V - 1], [0]]), 2, gap=gap, shift=shift).call().check()
+
+
 def test_logprobs_beyond_two_gigabytes(abi):
     """Rows behind 2^31 bytes and elements, and the largest vocabulary."""
     V = 1 << 21
