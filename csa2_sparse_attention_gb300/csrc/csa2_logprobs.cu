@@ -35,11 +35,10 @@
 
 namespace csa2 {
 
-constexpr int kLThreads = 256, kLWarps = kLThreads / 32;
+constexpr int kLThreads = 256;     // of a block; 128 or 64 for many short rows
 constexpr int kLGroup = 4;         // vectors of a group
 constexpr int kLMaxTurns = 65;     // groups of a thread: 2^21 fp32 values in eight slices, and a vector for where a row begins
 constexpr int kLTop = CSA2_LOGPROBS_TOP;
-constexpr int kLCands = 1024;      // values that are ranked
 constexpr int kLHits = 512;        // groups that are read again at once
 // Teams: 32 of 8 threads for up to kLFew alternatives, 128 of 2 for more (threads that
 // far apart, so that neighbours' values fall into different ones).  Of random values,
@@ -63,19 +62,22 @@ struct LogArgs {
     float scale;        // of the logits
 };
 
+template <int NT>
 struct LogSmem {
-    unsigned long long cand[kLCands];  // (key of the value, ~index): larger values, then lower indices, are larger
+    static constexpr int NC = NT == kLThreads ? kLMaxCluster : 1;
+    static constexpr int kCands = NT == kLThreads ? 1024 : 512;  // values that are ranked
+    unsigned long long cand[kCands];   // (key of the value, ~index): larger values, then lower indices, are larger
     unsigned long long list[kLTop];    // the slice's largest, in order
     float max, sum, tilt;              // of the slice: m, S, sum(e^y y)
-    int bad, listed, n_cand, n_hits;
-    uint32_t keys[kLThreads];          // of the threads' maxima
+    int bad, listed, n_cand, n_ties, n_hits;
+    uint32_t keys[NT];                 // of the threads' maxima
     uint16_t hits[kLHits];
-    float red[3][kLWarps];
-    int redi[kLWarps];
+    float red[3][NT / 32];
+    int redi[NT / 32];
     // the first block's join
-    unsigned long long all[kLMaxCluster][kLTop];
-    int all_n[kLMaxCluster];
-    float all_f[kLMaxCluster][3];
+    unsigned long long all[NC][kLTop];
+    int all_n[NC];
+    float all_f[NC][3];
     int all_bad;
 };
 
@@ -254,7 +256,8 @@ struct RowView {
 };
 
 // The sum of v over the block's earlier threads, and over all of them.
-__device__ __forceinline__ int block_before(LogSmem& S, int v, int& all) {
+template <int NT>
+__device__ __forceinline__ int block_before(LogSmem<NT>& S, int v, int& all) {
     const int lane = lane_id(), warp = threadIdx.x >> 5;
     int inc = v;
 #pragma unroll
@@ -268,7 +271,7 @@ __device__ __forceinline__ int block_before(LogSmem& S, int v, int& all) {
     int before = inc - v;
     all = 0;
 #pragma unroll
-    for (int w = 0; w < kLWarps; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += S.redi[w];
         all += S.redi[w];
     }
@@ -276,13 +279,13 @@ __device__ __forceinline__ int block_before(LogSmem& S, int v, int& all) {
 }
 
 // The k largest of the slice, in order, to S.list (fewer where fewer are above -inf).
-template <typename T>
-__device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& row, int32_t v0, int32_t v1, int turns, float mine, int k) {
+template <int NT, typename T>
+__device__ void top_of_slice(LogSmem<NT>& S, const float* groups, const RowView<T>& row, int32_t v0, int32_t v1, int turns, float mine, int k) {
     constexpr int E = RowView<T>::E;
     const int tid = threadIdx.x;
     const int lane = tid & 31;
     S.keys[tid] = mine > -INFINITY ? float_key(mine) : 0u;
-    if (tid == 0) S.n_hits = S.n_cand = 0;
+    if (tid == 0) S.n_hits = S.n_cand = S.n_ties = 0;
     __syncthreads();
     // the k-th largest of the teams' maxima (0 where fewer have any), by every warp
     uint32_t bar = 0;
@@ -294,7 +297,7 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
         for (int i = 0; i < N; ++i) {
             own[i] = S.keys[32 * i + lane];
 #pragma unroll
-            for (int j = i + N; j < kLThreads / 32; j += N) {
+            for (int j = i + N; j < NT / 32; j += N) {
                 const uint32_t u = S.keys[32 * j + lane];
                 own[i] = own[i] > u ? own[i] : u;
             }
@@ -313,50 +316,52 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
         bar = __reduce_max_sync(0xffffffffu, bar);
     };
     if (k <= kLFew) reach(std::integral_constant<int, 32>());
-    else reach(std::integral_constant<int, 128>());
+    else reach(std::integral_constant<int, (NT < 128 ? NT : 128)>());
     const uint32_t low = float_key(-INFINITY) + 1;  // -inf is no alternative
     if (bar < low) bar = low;
-    // The values at the bar or above; where they are too many for the lists, as where a mask leaves less than k above its
-    // own value, those above it.
+    // The values at the bar or above; where they are too many for the lists, or many and most of them equal, as where a mask
+    // leaves less than k above its own value, those above it.  (They are ranked in n^2 steps: 1000 of them by 256 threads
+    // took 25 us a row.)
     int n;
     uint32_t from = bar;
 #pragma unroll 1
     for (;; ++from) {
         const float reached = key_float(from);
         for (int j = 0; j < turns; ++j) {
-            const uint32_t those = __ballot_sync(0xffffffffu, groups[j * kLThreads + tid] >= reached);
+            const uint32_t those = __ballot_sync(0xffffffffu, groups[j * NT + tid] >= reached);
             if (those == 0) continue;
             int at = 0;
             if (lane == 0) at = atomicAdd(&S.n_hits, __popc(those));
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(those & ((1u << lane) - 1));
-            if ((those >> lane & 1) && at < kLHits) S.hits[at] = uint16_t(j * kLThreads + tid);
+            if ((those >> lane & 1) && at < kLHits) S.hits[at] = uint16_t(j * NT + tid);
         }
         __syncthreads();
         const int n_hits = S.n_hits;
         n = INT_MAX;
         if (n_hits <= kLHits) {
-            for (int i = tid; i < kLGroup * n_hits; i += kLThreads) {
-                const int group = S.hits[i / kLGroup], j = group / kLThreads;
-                const int32_t v = v0 + (j * kLGroup + i % kLGroup) * kLThreads + (group - j * kLThreads);
+            for (int i = tid; i < kLGroup * n_hits; i += NT) {
+                const int group = S.hits[i / kLGroup], j = group / NT;
+                const int32_t v = v0 + (j * kLGroup + i % kLGroup) * NT + (group - j * NT);
                 if (v >= v1) continue;
                 float x[E];
                 row.values(row.load(v), x);
-                uint32_t bits = 0;
+                uint32_t bits = 0, ties = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) >= from) << e;
+                for (int e = 0; e < E; ++e) bits |= uint32_t(float_key(x[e]) >= from) << e, ties |= uint32_t(float_key(x[e]) == from) << e;
                 if (bits == 0) continue;
                 int at = atomicAdd(&S.n_cand, __popc(bits));
+                if (ties != 0) atomicAdd(&S.n_ties, __popc(ties));
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (bits >> e & 1) {
-                        if (at < kLCands) S.cand[at] = ranked(x[e], v * E - row.head + e);
+                        if (at < LogSmem<NT>::kCands) S.cand[at] = ranked(x[e], v * E - row.head + e);
                         ++at;
                     }
             }
             __syncthreads();
             n = S.n_cand;
         }
-        if (n <= kLCands || from > bar) break;
+        if (from > bar || n <= (2 * S.n_ties > n ? 2 * kLTop : LogSmem<NT>::kCands)) break;
         __syncthreads();
         if (tid == 0) S.n_hits = S.n_cand = 0;
         __syncthreads();
@@ -364,9 +369,9 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
     if (n < k && from > bar) {  // the first ones at the bar, in the row's order
         const float reached = key_float(bar);
         for (int j = 0; j < turns && n < k; ++j) {
-            const bool near = groups[j * kLThreads + tid] >= reached;
+            const bool near = groups[j * NT + tid] >= reached;
             for (int g = 0; g < kLGroup && n < k; ++g) {
-                const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                const int32_t v = v0 + (j * kLGroup + g) * NT + tid;
                 uint32_t bits = 0;  // of the vector's values at the bar
                 if (near && v < v1) {
                     float x[E];
@@ -381,14 +386,14 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
             }
         }
         __syncthreads();
-    } else if (n > kLCands) {
+    } else if (n > LogSmem<NT>::kCands) {
         // Many different ones, in the places of few threads: the k-th largest pair of value and index, bit by bit.
         auto visit = [&](uint32_t from, auto f) {  // the values of the groups whose maximum's key is `from` or more
             for (int j = 0; j < turns; ++j) {
-                if (float_key(groups[j * kLThreads + tid]) < from) continue;
+                if (float_key(groups[j * NT + tid]) < from) continue;
 #pragma unroll
                 for (int g = 0; g < kLGroup; ++g) {
-                    const int32_t v = v0 + (j * kLGroup + g) * kLThreads + tid;
+                    const int32_t v = v0 + (j * kLGroup + g) * NT + tid;
                     if (v >= v1) continue;
                     float x[E];
                     row.values(row.load(v), x);
@@ -414,7 +419,7 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
         __syncthreads();
         n = S.n_cand;
     }
-    for (int i = tid; i < n; i += kLThreads) {
+    for (int i = tid; i < n; i += NT) {
         const unsigned long long c = S.cand[i];
         int at = 0;
         for (int j = 0; j < n; ++j) at += S.cand[j] > c;
@@ -424,11 +429,11 @@ __device__ void top_of_slice(LogSmem& S, const float* groups, const RowView<T>& 
     __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogArgs a, int cluster) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) token_logprobs_kernel(const LogArgs a, int cluster) {
     constexpr int E = RowView<T>::E;
     extern __shared__ __align__(16) float groups[];  // maxima of the groups, [turn][thread]
-    __shared__ LogSmem S;
+    __shared__ LogSmem<NT> S;
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
@@ -438,15 +443,15 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
     const float c = a.scale * 1.4426950408889634f;
     uint4 next[kLGroup];
     auto fetch = [&](const RowView<T>& row, int32_t v1, int32_t at) {  // vectors at .. of a slice that ends at v1
-        const int32_t behind = at + kLGroup * kLThreads;
+        const int32_t behind = at + kLGroup * NT;
         if ((at > 0 || row.head == 0) && behind <= v1 && behind * E <= row.head + row.vocab) {  // every one lies within the row
             const uint4* p = reinterpret_cast<const uint4*>(row.base) + at + tid;
 #pragma unroll
-            for (int g = 0; g < kLGroup; ++g) next[g] = __ldg(p + g * kLThreads);
+            for (int g = 0; g < kLGroup; ++g) next[g] = __ldg(p + g * NT);
         } else {
 #pragma unroll
             for (int g = 0; g < kLGroup; ++g) {
-                const int32_t v = at + g * kLThreads + tid;
+                const int32_t v = at + g * NT + tid;
                 next[g] = v < v1 ? row.load(v) : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
                                                                  : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
             }
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
     for (; r < a.n; r += step) {
         const RowView<T> row(a, r);
         const int32_t v0 = first(row), v1 = end(row);
-        const int turns = (v1 - v0 + kLThreads * kLGroup - 1) / (kLThreads * kLGroup);
+        const int turns = (v1 - v0 + NT * kLGroup - 1) / (NT * kLGroup);
         // the given tokens' logits, while the row comes in
         float x_given = -INFINITY;
         if (rank == 0 && tid < a.given) {
@@ -481,9 +486,9 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
 #pragma unroll
             for (int g = 0; g < kLGroup; ++g)
                 w[4 * g] = next[g].x, w[4 * g + 1] = next[g].y, w[4 * g + 2] = next[g].z, w[4 * g + 3] = next[g].w;
-            if (j + 1 < turns) fetch(row, v1, v0 + (j + 1) * kLGroup * kLThreads);
+            if (j + 1 < turns) fetch(row, v1, v0 + (j + 1) * kLGroup * NT);
             const float m = RowView<T>::most(w);
-            groups[j * kLThreads + tid] = m;
+            groups[j * NT + tid] = m;
             if (!(part.over(m, c) <= kLReach)) {  // the first group, one far above the base, NaN
                 if (!(m < INFINITY)) bad = true;
                 part.move(m, c);
@@ -534,9 +539,9 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) S.red[0][warp] = m;
         const bool any_bad = __syncthreads_or(bad);
-        m = S.red[0][lane & (kLWarps - 1)];
+        m = S.red[0][lane & (NT / 32 - 1)];
 #pragma unroll
-        for (int o = kLWarps / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = NT / 64; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         {
             const float d = sum == 0.f ? 0.f : -part.over(m, c), f = sum == 0.f ? 0.f : exp2_of(d);
             tilt = f == 0.f ? 0.f : f * fmaf(sum, d, tilt);
@@ -548,12 +553,12 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
             tilt += __shfl_xor_sync(0xffffffffu, tilt, o);
         }
         if (lane == 0) S.red[1][warp] = sum, S.red[2][warp] = tilt;
-        if (a.top > 0 && !any_bad) top_of_slice<T>(S, groups, row, v0, v1, turns, top, a.top);
+        if (a.top > 0 && !any_bad) top_of_slice<NT, T>(S, groups, row, v0, v1, turns, top, a.top);
         else if (tid == 0) S.listed = 0;
         __syncthreads();
         if (tid == 0) {
             float s = 0.f, t = 0.f;
-            for (int w = 0; w < kLWarps; ++w) s += S.red[1][w], t += S.red[2][w];
+            for (int w = 0; w < NT / 32; ++w) s += S.red[1][w], t += S.red[2][w];
             S.max = m, S.sum = s, S.tilt = t, S.bad = any_bad;
         }
         // ---- the row's
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
                     S.all_n[tid] = int(peer_u32(peer(&S.listed, tid)));
                 }
                 int b = tid < cluster ? int(peer_u32(peer(&S.bad, tid))) : 0;
-                for (int i = tid; i < cluster * a.top; i += kLThreads) {
+                for (int i = tid; i < cluster * a.top; i += NT) {
                     const int q = i / a.top, e = i - q * a.top;
                     S.all[q][e] = peer_u64(peer(&S.list[e], q));  // (behind its last one: whatever is there)
                 }
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
                 S.all_n[0] = S.listed;
                 S.all_bad = S.bad;
             }
-            for (int i = tid; i < a.top; i += kLThreads) S.all[0][i] = S.list[i];
+            for (int i = tid; i < a.top; i += NT) S.all[0][i] = S.list[i];
             __syncthreads();
         }
         float big = -INFINITY;
@@ -613,20 +618,20 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
             a.ids[r * a.top + tid] = -1;
             a.best[r * a.top + tid] = nan ? not_a : -INFINITY;
         }
-        for (int i = tid; i < cluster * a.top && !nan; i += kLThreads) {
+        for (int i = tid; i < cluster * a.top && !nan; i += NT) {
             const int q = i / a.top, e = i - q * a.top;
             if (e >= S.all_n[q]) continue;
             const unsigned long long v = S.all[q][e];
             int at = e;
             if (cluster > 1) {
-                int larger[kLMaxCluster] = {};  // of every list, its own among them: searched side by side
+                int larger[LogSmem<NT>::NC] = {};  // of every list, its own among them: searched side by side
                 for (int half = 1 << (31 - __clz(a.top)); half > 0; half >>= 1)
 #pragma unroll
-                    for (int o = 0; o < kLMaxCluster; ++o)
+                    for (int o = 0; o < LogSmem<NT>::NC; ++o)
                         if (o < cluster && larger[o] + half <= S.all_n[o] && S.all[o][larger[o] + half - 1] > v) larger[o] += half;
                 at = 0;
 #pragma unroll
-                for (int o = 0; o < kLMaxCluster; ++o) at += larger[o];
+                for (int o = 0; o < LogSmem<NT>::NC; ++o) at += larger[o];
             }
             if (at < a.top) {
                 a.ids[r * a.top + at] = int32_t(~uint32_t(v));
@@ -642,22 +647,24 @@ __global__ void __launch_bounds__(kLThreads, 4) token_logprobs_kernel(const LogA
 
 using namespace csa2;
 
-template <typename T>
-static csa2_status logprobs_launch(LogArgs a, int64_t n, int cluster, size_t smem, cudaStream_t s) {
+template <typename T, int NT>
+static csa2_status logprobs_launch(const LogArgs& a, int cluster, cudaStream_t s) {
+    const int64_t turns = ceil_div<int64_t>(a.slice, NT * kLGroup);
+    if (turns > kLMaxTurns || a.n * cluster > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     static std::atomic<bool> done[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA2_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kLMaxTurns * kLThreads * int(sizeof(float))) != cudaSuccess)
+        if (cudaFuncSetAttribute(token_logprobs_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kLMaxTurns * NT * int(sizeof(float))) != cudaSuccess)
             return CSA2_ERR_CUDA;
         done[dev].store(true, std::memory_order_release);
     }
     timer_begin(K_LOGPROBS, s);
     // blocks that are resident at once walk over the rows (a cluster is made for few rows, one each)
-    const int64_t most = 4 * int64_t(sm_count());
-    launch(token_logprobs_kernel<T>, dim3(unsigned(cluster > 1 || n < most ? n * cluster : most)), kLThreads, smem, s, unsigned(cluster), a,
-           cluster);
+    const int64_t most = 1024 / NT * int64_t(sm_count());
+    launch(token_logprobs_kernel<T, NT>, dim3(unsigned(cluster > 1 || a.n < most ? a.n * cluster : most)), NT,
+           size_t(turns) * NT * sizeof(float), s, unsigned(cluster), a, cluster);
     timer_end(K_LOGPROBS, s);
     return launch_status();
 }
@@ -711,9 +718,23 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_
            (fits(2 * cluster) || ceil_div<int64_t>(ceil_div<int64_t>(nv, cluster), kLThreads * kLGroup) > kLMaxTurns))
         cluster *= 2;
     a.slice = int32_t(ceil_div<int64_t>(nv, cluster));
-    const int64_t turns = ceil_div<int64_t>(a.slice, kLThreads * kLGroup);
-    if (turns > kLMaxTurns || n * cluster > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
-    const size_t smem = size_t(turns) * kLThreads * sizeof(float);
-    return dtype == CSA2_OUT_BF16 ? logprobs_launch<__nv_bfloat16>(a, n, cluster, smem, cudaStream_t(stream))
-                                  : logprobs_launch<float>(a, n, cluster, smem, cudaStream_t(stream));
+    cudaStream_t st = cudaStream_t(stream);
+    // More rows than 256-thread blocks at once: smaller blocks, whose rows' starts and ends, and last rounds, go side by side.
+    // (us with 256 / 128 / 64 threads, 20 alternatives: 2048 rows of 1000 fp32 22 / 13 / 9, of 5003 27 / 19 / 15, of 16000
+    // 39 / 33 / 30, of 50021 86 / 77 / -; 1200 rows of 16000 22 / 19 / 21, of 65536 39 / 34 / - in
+    // bf16 and 57 / 54 / - in fp32; but 620 rows of 32000 bf16 18 / 20 / 19, of 50021 24 / 27 / -, fp32 36 / 31 / -, whose
+    // rows wait for memory rather than for instructions.  Longer rows' maxima leave little L1 beside eight blocks: 2048 of
+    // 131072 bf16 104 / 110, 1200 of 100003 fp32 81 / 141.  64 threads are few for 64 alternatives: 2048 of 5003
+    // 53 / 37 / 191.)
+    const int64_t sms = sm_count();
+    int threads = kLThreads;
+    if (cluster == 1 && n > 4 * sms) {
+        if (top <= kLFew && nv <= (n >= 12 * sms ? 4096 : 2560)) threads = 64;
+        else if (size == 4 ? nv - 2 <= 16384 : nv - 2 <= 12800 && n >= 6 * sms) threads = 128;
+    }
+    auto go = [&](auto type) {
+        using T = decltype(type);
+        return threads == 64 ? logprobs_launch<T, 64>(a, 1, st) : threads == 128 ? logprobs_launch<T, 128>(a, 1, st) : logprobs_launch<T, kLThreads>(a, cluster, st);
+    };
+    return dtype == CSA2_OUT_BF16 ? go(__nv_bfloat16()) : go(float());
 }

@@ -691,6 +691,23 @@ def test_logprobs(abi, n, V, given, top, gap, dtype):
     assert Logp(abi, logits(rng, n, V, dtype), picks(rng, n, V, given), top, gap=gap).call().check()[0] == abi.OK
 
 
+@pytest.mark.parametrize("n,V,top,gap", [(700, 1000, 20, 0), (700, 3001, 24, 1), (2000, 260, 5, 0), (1900, 1, 1, 3), (1000, 5003, 25, 0),
+                                         (640, 2500, 64, 4), (2500, 7, 64, 0), (930, 17001, 0, 0), (1830, 9001, 1, 0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_logprobs_of_many_short_rows(abi, n, V, top, gap, dtype):
+    """Blocks of fewer threads, which walk over several rows; masks of both kinds on some of them."""
+    rng = np.random.default_rng(n + V)
+    x = logits(rng, n, V, dtype)
+    for r in range(n):
+        if r % 5 < 2:
+            kept = rng.random(V) < (1.0, 0.3, 0.02, 0.001)[r % 4]
+            x[r][torch.from_numpy(~kept)] = -math.inf if r % 5 else torch.finfo(dtype).min
+    x[2 % n] = 1.5
+    x[7 % n] = torch.linspace(3.0, -3.0, V).to(dtype)
+    x[8 % n, V // 2] = math.nan
+    assert Logp(abi, x, picks(rng, n, V, 2), top, gap=gap).call().check()[0] == abi.OK
+
+
 @pytest.mark.parametrize("dtype,shift", [(torch.float32, 1), (torch.float32, 3), (torch.bfloat16, 1), (torch.bfloat16, 6)])
 @pytest.mark.parametrize("n,V,gap", [(1, 3, 0), (1, 5001, 0), (7, 8192, 0), (5, 40001, 2)])
 def test_logprobs_of_rows_from_any_element(abi, dtype, shift, n, V, gap):
