@@ -159,7 +159,10 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
     }
 
     // ---- Q: groups of 8 rows; of a row its factor and its keys
-    auto q_place = [&](int row, const U32x8 (&v)[8]) {
+    auto q_pos = [&](int row) {  // of a tree's token; loaded before the queries, so that it is there with them
+        return TREE && row < it.n_row ? __ldg(a.pos + it.rq.q0 + (it.row0 + row) / a.by_heads) : int64_t(-1);
+    };
+    auto q_place = [&](int row, const U32x8 (&v)[8], int64_t p) {
         const int piece = lane >> 3;
         const bool on = row < it.n_row;
         const int qs = paged_q_exponent(v);
@@ -168,9 +171,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             // rows behind the last one see nothing
             const int32_t hi = on ? it.rq.len - it.rq.nq + (it.row0 + row) / a.by_heads + 1 : 0;
             if (TREE) {  // the positions before the request's tokens
-                const int32_t tok = on ? it.rq.q0 + (it.row0 + row) / a.by_heads : 0;
-                const int64_t p = on ? __ldg(a.pos + tok) : -1;
-                S.tok[row] = p >= 0 ? tok : -1;
+                S.tok[row] = p >= 0 ? it.rq.q0 + (it.row0 + row) / a.by_heads : -1;
                 S.keys[row] = make_int2(a.window > 0 ? int32_t(p < hi - 1 ? p : hi - 1) + 1 - a.window : 0,
                                         p >= 0 ? it.rq.len - it.rq.nq : 0);
             } else {
@@ -189,8 +190,9 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         if (walk && tid == 0) a.cuts[blockIdx.x] = S.work[0].cut;
         const int row = 8 * (warp < kPSoftWarps ? warp : warp - kRProdWarps) + (lane & 7);
         U32x8 v[8];
+        const int64_t p = q_pos(row);
         paged_q_load(a, it.out0 + row, row < it.n_row, v);
-        q_place(row, v);
+        q_place(row, v, p);
         asm volatile("bar.sync 1, 256;" ::: "memory");
     }
     int32_t t0 = 0, done = 0, turn = 0;  // key tiles before this item, items with any, items
@@ -216,13 +218,15 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         do {
             if (TREE && turn > 0) {
                 U32x8 v[2][8];
+                int64_t p[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = 8 * (warp + kPSoftWarps * i) + (lane & 7);
+                    p[i] = q_pos(row);
                     paged_q_load(a, it.out0 + row, row < it.n_row, v[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) q_place(8 * (warp + kPSoftWarps * i) + (lane & 7), v[i]);
+                for (int i = 0; i < 2; ++i) q_place(8 * (warp + kPSoftWarps * i) + (lane & 7), v[i], p[i]);
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             }
             const int32_t nt = it.nt, key0 = it.key0, n_row = it.n_row, k_end = it.k_end, splits = it.splits;
@@ -377,12 +381,10 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.p_full);
             }
-            if (ok && nt > 0) ok = soft_and(mbar_wait(&S.o_done, done & 1, a.wlim));
-            if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(it.req), it.item);
-            // ---- epilogue: the rows' sums, then O / l row by row in shared memory (the latents' place), and out
+            // ---- epilogue: the rows' sums, while the last O^T is under way; then O / l row by row in shared memory (the latents'
+            // place), and out
+            const int64_t out0 = it.out0, part0 = it.part0;
             if (ok) {
-                tc_fence_after();
-                const int64_t out0 = it.out0, part0 = it.part0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[32];
@@ -402,7 +404,11 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                             a.lse[out0 + tid] = lse2 * kLn2;
                     }
                 }
-                soft_sync();
+                ok = nt > 0 ? soft_and(mbar_wait(&S.o_done, done & 1, a.wlim)) : soft_and(true);
+            }
+            if (!ok && lane == 0) record(a.st, CSA2_ERR_TIMEOUT, 6, int32_t(it.req), it.item);
+            if (ok) {
+                tc_fence_after();
                 const bool whole = splits == 1;
                 uint8_t* stage = S.c[0];
 #pragma unroll 1
