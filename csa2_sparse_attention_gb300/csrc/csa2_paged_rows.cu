@@ -235,7 +235,24 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             for (int c = 0; c < kRRows; ++c) l[c] = 0.f;
             const int32_t first = it.rq.len - it.rq.nq;  // the request's first token
             const bool blind = TREE && soft_or(tid < n_row && S.tok[tid] < 0);
+            auto in_part = [&](int32_t from) { return blind || from + kPN > first || (a.window > 0 && from < k_end - a.window); };
             for (int32_t j = 0; j < nt; ++j) {
+                // trees: tiles behind the first token, or where a window can begin (a token lies no further down than its place);
+                // the bits are made before the logits are there (the last tile's were read before its last barrier)
+                if (TREE) {
+                    const int32_t from = key0 + j * kPN;
+                    if (in_part(from)) {
+                        const int row = tid >> 1;
+                        const int2 k = S.keys[row];
+                        const int tok = S.tok[row];
+#pragma unroll 1
+                        for (int w = 2 * (tid & 1); w < 2 * (tid & 1) + 2; ++w) {
+                            uint32_t v = range_bits(from + 32 * w, k.x, k.y);
+                            if (tok >= 0) v |= tree_bits(a.mask + int64_t(tok) * a.words, a.words, from + 32 * w - first);
+                            S.see[w][row] = v;
+                        }
+                    }
+                }
                 ok = soft_and(mbar_wait(&S.s_full, (t0 + j) & 1, a.wlim));
                 if (!ok) break;
                 tc_fence_after();
@@ -258,21 +275,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 const bool hidden = (f[0].hidden[tid >> 4] >> (tid & 15)) & 1;
                 const bool nan = ((f[0].nan[tid >> 4] | f[1].nan[tid >> 4]) >> (tid & 15)) & 1;
                 if (TREE) {
-                    // tiles behind the first token, or where a window can begin (a token lies no further down than its place)
-                    const int32_t from = key0 + j * kPN;
-                    const bool part = blind || from + kPN > first || (a.window > 0 && from < k_end - a.window);
-                    if (part) {  // (the last tile's bits were read before this tile's first barrier)
-                        const int row = tid >> 1;
-                        const int2 k = S.keys[row];
-                        const int tok = S.tok[row];
-#pragma unroll
-                        for (int w = 2 * (tid & 1); w < 2 * (tid & 1) + 2; ++w) {
-                            uint32_t v = range_bits(from + 32 * w, k.x, k.y);
-                            if (tok >= 0) v |= tree_bits(a.mask + int64_t(tok) * a.words, a.words, from + 32 * w - first);
-                            S.see[w][row] = v;
-                        }
-                        soft_sync();
-                    }
+                    const bool part = in_part(key0 + j * kPN);
                     if (part || __any_sync(0xffffffffu, hidden || nan)) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
@@ -475,8 +478,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             int32_t ids = -1;
             uint32_t gone = 0;               // keys of the tile without a row, a bit each
             // place within its page of the first key of the tile that is loaded next; a tile on is 128 keys on
-            const int32_t step_off = kPN % a.page;
-            int32_t off_t = (key0 + 32 * w4) % a.page + k8;  // groups of 8 keys share a page, so this is below it
+            const int32_t step_off = kPN - kPN / a.by_page * a.page;
+            int32_t off_t = key0 + 32 * w4 - (key0 + 32 * w4) / a.by_page * a.page + k8;  // groups of 8 keys share a page, so this is below it
             auto load = [&](int32_t j) {
                 if ((j & 7) == 0) {
                     const int32_t p = key0 + (j + (lane >> 2)) * kPN + 32 * w4 + 8 * (lane & 3);
