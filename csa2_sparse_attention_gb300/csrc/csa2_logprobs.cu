@@ -19,7 +19,7 @@
 // the few groups that do are read again (from L2), a vector a thread, and their
 // values that do are ranked by counting.
 //
-// Measured: 2048 rows of 131072 bf16 88 us without alternatives (6.1 TB/s, 90 % of
+// Measured: 2048 rows of 131072 bf16 87 us without alternatives (6.2 TB/s, 91 % of
 // the card's copy rate) and 103 with 20 of them (5.2 TB/s: four blocks a
 // multiprocessor rank at about the same time, and 3.4 rows a block are a last round
 // for a third of them; 70 % of the issue slots are taken); 121 rows of 100003 fp32, a
