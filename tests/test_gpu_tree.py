@@ -1023,6 +1023,67 @@ def test_commit_undoes_the_plan(abi):
     assert abi.csa2_status_fetch(ws)[0] == abi.OK
 
 
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_rows_behind_four_gigabytes(abi, fmt):
+    """Latents go to, are attended to in and move within pages whose bytes lie beyond 32 bits."""
+    page, width = 16, 256 if fmt == "fp4" else 512
+    n_pages = (9 << 29) // (width * page)
+    n_rows = n_pages * page
+    rng = np.random.default_rng(19)
+    n, H = 40, 8
+    small = Heads(abi, rng, n, H, fmt, turn=False)
+    codes = torch.empty((n_rows, width), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n_rows, 32), dtype=torch.uint8, device="cuda") if fmt == "fp4" else None
+    table = np.array([[n_pages - 1, n_pages // 2, n_pages - 3]], np.int32)
+    p = np.arange(n)
+    rows = dev(table[0, p // page].astype(np.int64) * page + p % page)
+    f = abi.FMT_FP4 if fmt == "fp4" else abi.FMT_FP8
+    abi.csa2_head_norm_rope(None, 0, 0, None, None, small.lat, small.l_stride, small.lw, n, 1e-6, None, None, 0, f, rows, n_rows, codes, scales,
+                            small.ws, small.ws.numel())
+    want_c, want_s = torch.zeros((n, width), dtype=torch.uint8, device="cuda"), torch.zeros((n, 32), dtype=torch.uint8, device="cuda")
+    abi.csa2_head_norm_rope(None, 0, 0, None, None, small.lat, small.l_stride, small.lw, n, 1e-6, None, None, 0, f, None, n, want_c,
+                            want_s if fmt == "fp4" else None, small.ws, small.ws.numel())
+    assert torch.equal(codes[rows], want_c) and (scales is None or torch.equal(scales[rows], want_s))
+    # 24 nodes on 16 entries, as in a cache of three pages
+    parent = trees(rng, [24])
+    s = dict(q=bf16(rng.standard_normal((24, H, D))), q_start=starts([24]), kv_len=np.array([n], np.int32), codes=np.zeros((48, width), np.uint8),
+             scales=np.zeros((48, 32), np.uint8) if fmt == "fp4" else None, table=np.array([[0, 1, 2]], np.int32), page=page, fmt=fmt, T=24, H=H,
+             max_q=24, max_kv=n)
+    s["codes"][:n] = want_c.cpu().numpy()
+    if fmt == "fp4":
+        s["scales"][:n] = want_s.cpu().numpy()
+    t = Tree(abi, s, parent).call()
+    assert t.check()[0] == abi.OK
+    near = t.out.clone()
+    t.codes, t.scales, t.table = codes, scales, dev(table)
+    t.call()
+    torch.cuda.synchronize()
+    assert torch.equal(near, t.out)
+    tok, i32 = torch.zeros(24, dtype=torch.int64, device="cuda"), lambda v, m: torch.full((m,), v, dtype=torch.int32, device="cuda")  # noqa: E731
+    free, nf, path, acc, cached, nxt = i32(0, n_pages), i32(0, 1), i32(0, 24), i32(0, 1), i32(0, 1), torch.zeros(1, dtype=torch.int64, device="cuda")
+    abi.csa2_tree_commit(t.par, tok, tok, t.q_start, t.kv_len, 1, 24, 24, f, codes, scales, n_rows, t.table, 3, page, free, n_pages, nf, nf, cached,
+                         path, acc, nxt, t.ws, t.ws.numel())
+    torch.cuda.synchronize()
+    k = int(acc[0])
+    assert k > 1 and int(cached[0]) == 16 + k
+    src = 16 + path[:k].long()
+    assert (src != torch.arange(16, 16 + k, device="cuda")).any()
+    assert torch.equal(codes[rows[16:16 + k]], want_c[src]) and (scales is None or torch.equal(scales[rows[16:16 + k]], want_s[src]))
+    assert torch.equal(codes[rows[:16]], want_c[:16]) and abi.csa2_status_fetch(t.ws)[0] == abi.OK
+
+
+@pytest.mark.parametrize("cached,nodes", [([30, 9], [5, 3]), ([1200, 300, 40], [8, 2, 5]), ([700], [90]), ([3300, 100], [70, 66])])
+def test_attention_without_lse(abi, cached, nodes):
+    s = attn_inputs(np.random.default_rng(20), np.asarray(cached) + nodes, nodes, 64, 16, "fp4")
+    t = Tree(abi, s, trees(np.random.default_rng(1), nodes)).call()
+    assert t.check()[0] == abi.OK
+    out, t.lse = t.out.clone(), None
+    t.out.fill_(7.0)
+    t.call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, t.out)
+
+
 # --------------------------------------------------------- steps together
 def tree_layer(abi, fmt, window, norms, seed=0, theta=10000.0):
     from csa2_sparse_attention_gb300 import paged
