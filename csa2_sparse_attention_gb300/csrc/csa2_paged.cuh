@@ -328,7 +328,9 @@ __device__ __forceinline__ void paged_find(const PagedArgs& a, int64_t place, bo
 // for all requests: 16 requests of up to 8 nodes over 2K to 8K 109 and 188, 32 of 8
 // over 4K to 16K 331 and 441 (few-row kernel); 4 of up to 32 over 2K to 8K 108 and
 // 157, 8 of up to 64 over 4K to 16K 564 and 600 (row tiles).
-constexpr int32_t kWalkStart = 4;  // key tiles' time of an item's start and end
+// Key tiles' time of an item's start and end: as 2, 3, 4 or 6, 11 requests of up to 32 nodes x 32 heads over 2K take 48,
+// 45, 48, 50 us, 14 of 38 x 16 over 6K 93, 91, 94, 97, 16 of 8 x 64 over 8K 110, 109, 109, 113.
+constexpr int32_t kWalkStart = 3;
 constexpr int32_t kWalkLeast = 2;  // tiles of a piece, and weight of a share
 struct WalkSums {
     int64_t items, tiles;  // of all requests: items, and their tiles
