@@ -49,7 +49,7 @@ struct PagedRowsSmem {
     uint8_t q[kRRows * kPD * 2];  // 8-row groups of 8192 B, 8-channel chunks of 128 B
     uint8_t c[4][kRBlock];        // a tile's channels in blocks of 128
     uint8_t p[kPN * kRRows * 2];  // P^T: 8-key groups of 1024 B, 8-row chunks of 128 B
-    float2 row[kRRows];           // a row's factor of the raw logits and its base (log2 domain; 0 before any key)
+    float fac[kRRows], neg[kRRows];  // a row's factor of the raw logits, and minus its base (log2 domain; 0 before any key)
     int2 keys[kRRows];            // keys [x, y) that a row sees
     float alpha[kRRows], delta[kRRows];
     float red[4][kRRows];
@@ -74,6 +74,20 @@ __device__ __forceinline__ bool soft_or(bool v) {
     return r != 0;
 }
 __device__ __forceinline__ bool soft_and(bool v) { return !soft_or(!v); }
+
+// Two fp32 operations in one: (x0, x1) = (x0, x1) f + n; (x0, x1) += (p0, p1).
+__device__ __forceinline__ void fma_pair(float& x0, float& x1, uint64_t f, uint64_t n) {
+    asm("{\n .reg .b64 v;\n mov.b64 v, {%0, %1};\n fma.rn.f32x2 v, v, %2, %3;\n mov.b64 {%0, %1}, v;\n}\n" : "+f"(x0), "+f"(x1) : "l"(f), "l"(n));
+}
+__device__ __forceinline__ void add_pair(float& x0, float& x1, float p0, float p1) {
+    asm("{\n .reg .b64 v, w;\n mov.b64 v, {%0, %1};\n mov.b64 w, {%2, %3};\n add.rn.f32x2 v, v, w;\n mov.b64 {%0, %1}, v;\n}\n"
+        : "+f"(x0), "+f"(x1) : "f"(p0), "f"(p1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // Over a warp's lanes, 32 values each: lane l gets the maximum or sum of v[l].
 // Every round a lane keeps half of its values and takes the partner's half.
@@ -167,7 +181,8 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
         const bool on = row < it.n_row;
         const int qs = paged_q_exponent(v);
         if (piece == 0) {
-            S.row[row] = make_float2(paged_q_scale(a, qs), 0.f);
+            S.fac[row] = paged_q_scale(a, qs);
+            S.neg[row] = 0.f;
             // rows behind the last one see nothing
             const int32_t hi = on ? it.rq.len - it.rq.nq + (it.row0 + row) / a.by_heads + 1 : 0;
             if (TREE) {  // the positions before the request's tokens
@@ -265,10 +280,11 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float4 r = *reinterpret_cast<const float4*>(&S.row[32 * h + c]);
-                        x[h][c] = fmaf(x[h][c], r.x, -r.y);
-                        x[h][c + 1] = fmaf(x[h][c + 1], r.z, -r.w);
+                    for (int c = 0; c < 32; c += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&S.fac[32 * h + c]);
+                        const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(&S.neg[32 * h + c]);
+                        fma_pair(x[h][c], x[h][c + 1], f.x, n.x);
+                        fma_pair(x[h][c + 2], x[h][c + 3], f.y, n.y);
                     }
                 const int32_t key = key0 + j * kPN + tid;
                 const PagedFlags *f = S.flags[(t0 + j) & 1];
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                         }
                 }
 #pragma unroll
-                for (int c = 0; c < 32; ++c) top = fmaxf(top, fmaxf(x[0][c], x[1][c]));
+                for (int c = 0; c < 32; ++c) top = max3(top, x[0][c], x[1][c]);
                 if (soft_or(top > kPGrow) || S.fresh > 0) {  // (S.fresh was written before a barrier that all have passed)
                     // maxima over the keys; rows with a logit above kPGrow, or that see their first key, move their base
 #pragma unroll
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                     int still = 0;
                     if (tid < kRRows) {
                         const float t = fmaxf(fmaxf(S.red[0][tid], S.red[1][tid]), fmaxf(S.red[2][tid], S.red[3][tid]));
-                        const float m = S.row[tid].y;
+                        const float m = -S.neg[tid];
                         // alpha < 0 marks a row that has seen no key before this tile (set below); first tile: all
                         const bool mine = j == 0 || (was_fresh && S.alpha[tid] < 0.f);
                         float d = 0.f, al = 1.f;
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                             al = ex2(-d);
                         }
                         still = tid < n_row && al < 0.f;
-                        S.row[tid].y = m + d;
+                        S.neg[tid] = -(m + d);
                         S.delta[tid] = d;
                         S.alpha[tid] = al;
                     }
@@ -373,8 +389,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float p0 = ex2(x[h][c + 2 * e]), p1 = ex2(x[h][c + 2 * e + 1]);
-                            l[32 * h + c + 2 * e] += p0;
-                            l[32 * h + c + 2 * e + 1] += p1;
+                            add_pair(l[32 * h + c + 2 * e], l[32 * h + c + 2 * e + 1], p0, p1);
                             w[e] = f16x2(p0, p1);
                         }
                         *reinterpret_cast<uint4*>(pd + (4 * h + c / 8) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 if (tid < kRRows) {
                     const float sum = (S.red[0][tid] + S.red[1][tid]) + (S.red[2][tid] + S.red[3][tid]);
                     S.alpha[tid] = sum == 0.f ? 0.f : 1.0f / sum;
-                    const float lse2 = sum == 0.f ? -INFINITY : S.row[tid].y + log2f(sum);
+                    const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - S.neg[tid];
                     if (tid < n_row) {
                         if (splits > 1)
                             a.part_lse[part0 + tid] = lse2;
