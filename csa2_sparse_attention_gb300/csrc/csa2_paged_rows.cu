@@ -293,17 +293,21 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
                 if (TREE) {
                     const bool part = in_part(key0 + j * kPN);
                     if (part || __any_sync(0xffffffffu, hidden || nan)) {
+                        if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (nan) x[0][c] = x[1][c] = __uint_as_float(0x7FC00000u);
+                        }
+                        const uint32_t bit = hidden ? 0u : 1u << lane;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
                                 const uint4 v = part ? *reinterpret_cast<const uint4*>(&S.see[warp][32 * h + c]) : make_uint4(~0u, ~0u, ~0u, ~0u);
-                                const uint32_t see[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (nan) x[h][c + e] = __uint_as_float(0x7FC00000u);
-                                    if (hidden || !((see[e] >> lane) & 1u)) x[h][c + e] = -INFINITY;
-                                }
+                                if (!(v.x & bit)) x[h][c] = -INFINITY;
+                                if (!(v.y & bit)) x[h][c + 1] = -INFINITY;
+                                if (!(v.z & bit)) x[h][c + 2] = -INFINITY;
+                                if (!(v.w & bit)) x[h][c + 3] = -INFINITY;
                             }
                     }
                 }
