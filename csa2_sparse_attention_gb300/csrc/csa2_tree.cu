@@ -9,7 +9,8 @@ constexpr int kTreeMost = CSA2_TREE_NODES;  // nodes of a request
 constexpr int kTreeThreads = 128;
 
 // A request's nodes [q0, q0 + nq) and the position of the first one; nq is 0
-// where it has none, or a bound does not hold (recorded).
+// where it has none, or a token bound does not hold.  Without `good`, which such
+// a bound and a length that does not hold take (recorded), `first` is anything.
 struct TreeReq {
     int32_t q0, nq, first, len;
     bool good;
@@ -20,8 +21,8 @@ __device__ __forceinline__ TreeReq tree_request(const int32_t* q_start, const in
     o.q0 = q_start[r];
     const int32_t q1 = q_start[r + 1];
     o.len = kv_len[r];
-    o.nq = q1 - o.q0;
-    o.first = o.len - o.nq;
+    o.nq = int32_t(uint32_t(q1) - uint32_t(o.q0));  // (bounds may be anything, and the differences wrap around)
+    o.first = int32_t(uint32_t(o.len) - uint32_t(o.nq));
     o.good = o.q0 >= 0 && q1 >= o.q0 && q1 <= n_tokens && o.nq <= max_q;
     if (!o.good) o.nq = 0;
     if (o.good && (o.len < o.nq || o.len > max_len)) o.good = false;
@@ -178,7 +179,9 @@ __global__ void __launch_bounds__(kTreeThreads) tree_commit_kernel(const CommitA
         }
         n = __shfl_sync(0xffffffffu, n, 0);
         unsigned back = 0;  // pages that hold no kept entry
-        for (int j = int(commit_pages(t.first + n, a.page)) - page0 + lane; j < n_pages; j += 32) back += pages[j] >= 0 && pages[j] < a.n_pages;
+        // (none of a request whose bounds do not hold: `first` may be anything then, and `pages` holds nothing)
+        const int back0 = some ? int(commit_pages(t.first + n, a.page)) - page0 : 0;
+        for (int j = back0 + lane; j < n_pages; j += 32) back += pages[j] >= 0 && pages[j] < a.n_pages;
         back = __reduce_add_sync(0xffffffffu, back);
         if (lane == 0) {
             s_len = n;

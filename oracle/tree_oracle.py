@@ -116,15 +116,16 @@ def token_logprobs(x, scale, tokens, top):
     return logprobs, lse, entropy, ids, best
 
 
-def tree_commit(parent, token, choice, q_start, kv_len, page, planes, table, free, n_free, n_pages, cached, n_tokens):
-    """(path, accepted, next, cached, free, n_free, planes) after a step whose bounds are good."""
+def tree_commit(parent, token, choice, q_start, kv_len, page, planes, table, free, n_free, n_pages, cached, n_tokens, bad=()):
+    """(path, accepted, next, cached, free, n_free, planes) after a step; the requests of `bad` are those whose bounds do not
+    hold, which keep nothing (kv_len, q_start otherwise good)."""
     R = len(kv_len)
     path, accepted, nxt = np.full(n_tokens, -1, np.int32), np.zeros(R, np.int32), np.full(R, -1, np.int64)
     cached, free, planes = cached.copy(), free.copy(), [p.copy() for p in planes]
     back = []
     for r in range(R):
         a, n, L = int(q_start[r]), int(q_start[r + 1]) - int(q_start[r]), int(kv_len[r])
-        if n == 0:
+        if n == 0 or r in bad:
             continue
         way = []
         if parent[a] == -1:
