@@ -382,10 +382,12 @@ __device__ __forceinline__ void walk_piece(const PagedArgs& a, PagedWork& w, int
     w.part0 = slot * a.item;
 }
 // By shares, the group's part of w's item, `off` into it, to the end of the share
-// (w.left from the item's start); w.nt is -1 where it has none.
+// (w.left from the item's start); w.nt is -1 where it has none.  An item without
+// tiles is whole, and its zeros are of the group whose share has its start, also
+// where the share ends within the start's weight.
 __device__ __forceinline__ void walk_part(const PagedArgs& a, PagedWork& w, int64_t off, int64_t slot) {
     const int64_t j0 = off > kWalkStart ? off - kWalkStart : 0;
-    const int64_t j1 = w.left - kWalkStart < w.tiles ? w.left - kWalkStart : w.tiles;
+    const int64_t j1 = w.tiles > 0 && w.left - kWalkStart < w.tiles ? w.left - kWalkStart : w.tiles;
     if (w.tiles > 0 ? j1 <= j0 : off != 0) w.nt = -1;
     else walk_piece(a, w, j0, j1, slot);
 }

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from oracle import tree_oracle as TO
-from tests.test_gpu_tree import Commit, abi  # noqa: F401
+from tests.test_gpu_paged import attn_inputs
+from tests.test_gpu_tree import Commit, Tree, abi, dev, f64, trees, walk_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,73 @@ def test_commit_gives_no_pages_back_for_bad_requests(abi, fmt, what, value):
     np.testing.assert_array_equal(got[:held], path[:held] if what == "kv_len" else np.full(held, -7))
     assert (got[c.T:] == -7).all()
     assert abi.csa2_status_fetch(c.ws)[0] == abi.ERR_DEVICE_BOUNDS
+
+
+# --------------------------------------------------------------- attention
+def requests_of(q_start, r):
+    return slice(int(q_start[r]), int(q_start[r + 1]))
+
+
+# (the few-row kernel twice, row tiles; all by shares)
+@pytest.mark.parametrize("n_req,nodes,cached,spread", [(32, 8, 2048, 1), (32, 8, 2048, 40), (24, 16, 3100, 40)])
+@pytest.mark.parametrize("empty", ["no entries", "too many", "negative"])
+def test_attention_writes_requests_without_keys(abi, n_req, nodes, cached, spread, empty):
+    """Several requests' trees laid out by their lengths, one of them without keys, each in turn: its rows are zeros and -inf
+    wherever a group's share ends, and the others' are as with all of them."""
+    rng = np.random.default_rng(n_req)
+    n = [nodes] * n_req
+    s = attn_inputs(rng, cached - rng.integers(0, spread, n_req) + n, n, 64, 64, "fp4", tail=1)
+    t = Tree(abi, s, trees(rng, n)).call()
+    assert t.check()[0] == abi.OK
+    out, lse = t.out.clone(), t.lse.clone()
+    big = float(out[:s["q_start"][-1]].abs().max())
+    for r in range(n_req):
+        kv = s["kv_len"].copy()
+        kv[r] = {"no entries": 0, "too many": s["max_kv"] + 1 + r, "negative": -1 - 300 * r}[empty]
+        t.kv_len.copy_(dev(kv))
+        t.out.fill_(7.0)
+        t.lse.fill_(7.0)
+        t.call()
+        torch.cuda.synchronize()
+        own = requests_of(s["q_start"], r)
+        assert (t.out[own] == 0).all() and torch.isneginf(t.lse[own]).all(), r
+        others = torch.ones(s["T"], dtype=torch.bool, device="cuda")
+        others[own] = False
+        assert (t.out[others].float() - out[others].float()).abs().max() <= 2.0 ** -6 * big, r
+        assert (t.lse[others] - lse[others]).abs().max() <= 2.0 ** -14, r
+        assert abi.csa2_status_fetch(t.ws)[0] == abi.ERR_DEVICE_BOUNDS
+        abi.csa2_status_reset(t.ws)
+
+
+@pytest.mark.parametrize("n_req,H,kind,longest,window", [
+    (40, 8, "few", 1300, 0), (33, 64, "few", 1200, 1050), (150, 8, "few", 1100, 0), (12, 64, "tiles", 3300, 0), (35, 32, "tiles", 3300, 3200)])
+@pytest.mark.parametrize("seed", range(3))
+def test_attention_walks_over_many_requests_without_keys(abi, n_req, H, kind, longest, window, seed):
+    """Half of the requests have fewer entries than nodes or none, at random, beside short and long ones."""
+    rng = np.random.default_rng(seed)
+    s, parent = walk_inputs(rng, n_req, H, kind, longest, 16, "fp4")
+    nodes = np.diff(s["q_start"])
+    for r in np.flatnonzero(rng.random(n_req) < 0.5):
+        if r != n_req // 2 and nodes[r] > 0:
+            s["kv_len"][r] = 0 if rng.random() < 0.7 else rng.integers(0, nodes[r])
+    t = Tree(abi, s, parent, window).call()
+    t.check()
+
+
+@pytest.mark.parametrize("n_req,H,kind,longest,page,fmt,window", [
+    (3, 16, "few", 5000, 64, "fp8", 0), (33, 8, "few", 1500, 8, "fp4", 0), (40, 8, "few", 1300, 8, "fp8", 1050),
+    (600, 8, "few", 1200, 8, "fp4", 0), (2, 64, "tiles", 3400, 64, "fp4", 0), (5, 64, "tiles", 4100, 16, "fp8", 3200),
+    (35, 32, "tiles", 3300, 16, "fp4", 0)])
+def test_attention_walks_write_every_row_again(abi, n_req, H, kind, longest, page, fmt, window):
+    """A second call over outputs that hold something else gives the first one's bits."""
+    rng = np.random.default_rng(n_req + H)
+    s, parent = walk_inputs(rng, n_req, H, kind, longest, page, fmt)
+    t = Tree(abi, s, parent, window).call()
+    torch.cuda.synchronize()
+    out, lse = t.out.clone(), t.lse.clone()
+    t.out.fill_(5.0)
+    t.lse.fill_(5.0)
+    t.call()
+    torch.cuda.synchronize()
+    T = int(s["q_start"][-1])
+    assert torch.equal(out[:T], t.out[:T]) and torch.equal(lse[:T], t.lse[:T]) and (t.out[T:] == 5).all() and (t.lse[T:] == 5).all()
