@@ -313,9 +313,8 @@ extern "C" csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* to
     if (codes && fmt != CSA2_FMT_FP4 && fmt != CSA2_FMT_FP8) return CSA2_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < CSA2_STATUS_BYTES || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
     if (codes ? (fmt == CSA2_FMT_FP4) != (scales != nullptr) : scales != nullptr) return CSA2_ERR_INVALID_ARG;
-    if (!parent || !token || !choice || !q_start || !kv_len || !table || !free_pages || !n_free || !n_free_out || !cached || !path ||
-        !accepted || !next)
-        return CSA2_ERR_INVALID_ARG;
+    if (!q_start || !kv_len || !table || !free_pages || !n_free || !n_free_out || !cached || !accepted || !next) return CSA2_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!parent || !token || !choice || !path)) return CSA2_ERR_INVALID_ARG;
     for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(token), static_cast<const void*>(choice),
                           static_cast<const void*>(q_start), static_cast<const void*>(kv_len), static_cast<const void*>(codes),
                           static_cast<const void*>(scales), static_cast<const void*>(table), static_cast<const void*>(free_pages),

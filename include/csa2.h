@@ -570,7 +570,9 @@ csa2_status csa2_token_logprobs(const void* logits, int dtype, int64_t stride, i
  *   token        [n_tokens] int64, the nodes' tokens; choice [n_tokens] int64, what
  *                the model goes on with after each node (its first alternative, or
  *                a sample).
- *   parent, q_start, kv_len, max_q: as in csa2_tree_plan.
+ *   parent, q_start, kv_len, max_q: as in csa2_tree_plan.  (parent, token, choice
+ *                and path may be NULL where n_tokens is 0: accepted and next are
+ *                those of requests without nodes then.)
  *   codes, scales  the cache's planes (n_rows rows in the form fmt), or codes and
  *                scales NULL: no rows are moved.  The row of the path's j-th node
  *                goes to the request's entry kv_len - nodes + j.

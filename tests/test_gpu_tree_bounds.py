@@ -6,7 +6,7 @@ import torch
 
 from oracle import tree_oracle as TO
 from tests.test_gpu_paged import attn_inputs
-from tests.test_gpu_tree import Commit, Tree, abi, dev, f64, trees, walk_inputs  # noqa: F401
+from tests.test_gpu_tree import Commit, Tree, abi, dev, f64, tree_layer, trees, walk_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,6 +37,48 @@ def test_commit_gives_no_pages_back_for_bad_requests(abi, fmt, what, value):
     np.testing.assert_array_equal(got[:held], path[:held] if what == "kv_len" else np.full(held, -7))
     assert (got[c.T:] == -7).all()
     assert abi.csa2_status_fetch(c.ws)[0] == abi.ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("added", [[0, 0, 0], [4, 0, 6]])
+def test_steps_without_tokens_are_committed(abi, added):
+    """A step of no tokens, first of all and after one that had some, through the layer and the cache: nothing is accepted,
+    lengths, pages and entries stay."""
+    paged, g, cache, layer = tree_layer(abi, abi.FMT_FP4, 0, True)
+    if any(added):
+        n = sum(added)
+        cache.added.copy_(torch.tensor(added, dtype=torch.int32))
+        par = dev(trees(np.random.default_rng(0), added, "chain"))
+        layer.step(torch.randn(n, 256, generator=g).to(torch.bfloat16).cuda(), n, max(added), max(added), parent=par)
+        tok = torch.zeros(n, dtype=torch.int64, device="cuda")
+        cache.commit(par, tok, tok, n, max(added))
+        torch.cuda.synchronize()
+        assert cache.accepted.tolist() == added and cache.next.tolist() == [0, -1, 0]
+    before = [x.clone() for x in (cache.cached, cache.n_free, cache.free, cache.codes, cache.scales, cache.table, cache.path)]
+    assert cache.cached.tolist() == added
+    cache.added.zero_()
+    none = lambda t: torch.zeros(0, dtype=t, device="cuda")  # noqa: E731
+    out, lse = layer.step(torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda"), 0, 0, 10, parent=none(torch.int32))
+    path, accepted, nxt = cache.commit(none(torch.int32), none(torch.int64), none(torch.int64), 0, 0)
+    torch.cuda.synchronize()
+    assert len(out) == len(path) == 0 and accepted.tolist() == [0, 0, 0] and nxt.tolist() == [-1, -1, -1]
+    for a, b in zip((cache.cached, cache.n_free, cache.free, cache.codes, cache.scales, cache.table, cache.path), before):
+        assert torch.equal(a, b)
+    for name, st in cache.status().items():
+        assert st[0] == abi.OK, (name, st)
+
+
+def test_commit_of_no_tokens_records_what_is_left_of_others(abi):
+    """Without tokens, token bounds of an earlier step do not hold: recorded, and nothing is read or moved."""
+    c = Commit(abi, np.random.default_rng(22), [20, 9], [3, 7], 8, "fp4").upload()
+    a, d = abi, c.d
+    a.csa2_tree_commit(None, None, None, d["q_start"], d["kv_len"], 2, 0, 7, a.FMT_FP4, c.dp[0], c.dp[1], c.planes[0].shape[0], d["table"],
+                       c.max_pages, 8, d["free"], c.n_pages, c.nf, c.nf, c.cached, None, c.accepted, c.next, c.ws, c.ws.numel())
+    torch.cuda.synchronize()
+    assert c.accepted.tolist() == [0, 0] and c.next.tolist() == [-1, -1] and c.cached.tolist() == c.cached0.tolist()
+    assert int(c.nf.item()) == c.n_free and (d["free"].cpu().numpy() == c.free).all()
+    for got, want in zip(c.dp, c.planes):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+    assert a.csa2_status_fetch(c.ws)[0] == a.ERR_DEVICE_BOUNDS
 
 
 # --------------------------------------------------------------- attention
