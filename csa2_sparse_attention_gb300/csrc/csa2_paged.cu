@@ -419,6 +419,14 @@ static csa2_status paged_call(const void* q_bf16, int64_t n_tokens, int n_heads,
     const size_t bytes = size_t(n_tokens) * n_heads * kPD * 2;  // of the queries and of the outputs
     const char *q0 = static_cast<const char*>(q_bf16), *o0 = static_cast<const char*>(out);
     if (o0 < q0 + bytes && q0 < o0 + bytes) return CSA2_ERR_INVALID_ARG;
+    if (tree) {  // what is written lies apart from what is read and from each other
+        const int64_t rows = n_tokens * n_heads, row_codes = fmt == CSA2_FMT_FP4 ? kPD / 2 : kPD;
+        const Span outs[] = {{out, rows * kPD * 2}, {out_lse, rows * 4}};
+        const Span ins[] = {{q_bf16, rows * kPD * 2}, {q_start, 4 * (n_req + 1)}, {kv_len, 4 * n_req}, {pos, 8 * n_tokens},
+                            {mask, n_tokens * mask_words * 4}, {codes, n_rows * row_codes}, {scales, n_rows * (kPD / 16)},
+                            {table, 4 * n_req * max_pages}};
+        if (!apart(outs, ins)) return CSA2_ERR_INVALID_ARG;
+    }
     cudaStream_t s = cudaStream_t(stream);
     if (plan.tiles.grid > INT32_MAX || plan.few.grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     PagedArgs a{};

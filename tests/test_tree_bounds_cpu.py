@@ -1,0 +1,22 @@
+"""Refusals of the calls of a step of trees beyond those of test_tree_cpu.py: no launch, no pointer that is valid."""
+import pytest
+
+from tests.test_tree_cpu import abi, refused  # noqa: F401
+
+FAR = 1 << 40  # never dereferenced
+
+
+# 4 tokens x 64 heads: 262144 bytes of outputs, 1024 of log-sum-exps; 128 rows of 256 and 32 bytes; every buffer on its own
+ATTN = dict(q=FAR, n_tokens=4, heads=64, q_start=2 * FAR, kv_len=3 * FAR, n_req=2, max_q=2, max_kv=100, pos=4 * FAR, mask=5 * FAR, words=1,
+            fmt=0, codes=6 * FAR, scales=7 * FAR, n_rows=128, table=8 * FAR, max_pages=8, page=16, window=0, sm_scale=0.04, out=9 * FAR,
+            lse=10 * FAR, ws=11 * FAR, ws_bytes=1 << 39, stream=None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=9 * FAR), dict(lse=9 * FAR + 262128), dict(lse=9 * FAR - 1008), dict(out=10 * FAR + 1008), dict(lse=FAR + 262128),
+    dict(lse=2 * FAR), dict(lse=3 * FAR - 1008), dict(lse=4 * FAR + 16), dict(lse=5 * FAR), dict(lse=6 * FAR + 128 * 256 - 16),
+    dict(lse=7 * FAR + 128 * 32 - 16), dict(lse=8 * FAR + 48), dict(out=2 * FAR - 262128), dict(out=3 * FAR), dict(out=4 * FAR + 16),
+    dict(out=5 * FAR - 16), dict(out=6 * FAR + 128 * 256 - 16), dict(out=6 * FAR + 128 * 512 - 16, fmt=1, scales=None), dict(out=7 * FAR - 262128),
+    dict(out=8 * FAR + 48)])
+def test_attention_outputs_over_inputs_are_refused(abi, kw):
+    refused(abi, "csa2_tree_attn", ATTN, kw, "I")
