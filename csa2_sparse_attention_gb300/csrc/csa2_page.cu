@@ -174,6 +174,9 @@ extern "C" csa2_status csa2_page_plan(const int32_t* cached, const int32_t* adde
                           static_cast<const void*>(table), static_cast<const void*>(free_pages),
                           static_cast<const void*>(slots), static_cast<const void*>(pos)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    for (const int32_t* p : {n_free, static_cast<const int32_t*>(n_free_out), static_cast<const int32_t*>(q_start),
+                             static_cast<const int32_t*>(kv_len)})
+        if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t)) return CSA2_ERR_INVALID_ARG;
     cudaStream_t s = cudaStream_t(stream);
     // 1024 tokens per CTA (four per thread), at most two CTAs per SM
     int64_t grid = ceil_div<int64_t>(max_new, 1024);

@@ -321,6 +321,8 @@ extern "C" csa2_status csa2_tree_commit(const int32_t* parent, const int64_t* to
                           static_cast<const void*>(cached), static_cast<const void*>(path), static_cast<const void*>(accepted),
                           static_cast<const void*>(next)})
         if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+    for (const int32_t* p : {n_free, static_cast<const int32_t*>(n_free_out)})  // (one number, which may lie among others)
+        if (reinterpret_cast<uintptr_t>(p) % sizeof(int32_t)) return CSA2_ERR_INVALID_ARG;
     if (n_req == 0) return CSA2_OK;
     // what is written lies apart from what is read and from each other (blocks read what others are done with)
     const int64_t row_codes = fmt == CSA2_FMT_FP4 ? 256 : 512;

@@ -1,7 +1,7 @@
 """Refusals of the calls of a step of trees beyond those of test_tree_cpu.py: no launch, no pointer that is valid."""
 import pytest
 
-from tests.test_tree_cpu import abi, refused  # noqa: F401
+from tests.test_tree_cpu import COMMIT, abi, refused  # noqa: F401
 
 FAR = 1 << 40  # never dereferenced
 
@@ -20,3 +20,19 @@ ATTN = dict(q=FAR, n_tokens=4, heads=64, q_start=2 * FAR, kv_len=3 * FAR, n_req=
     dict(out=8 * FAR + 48)])
 def test_attention_outputs_over_inputs_are_refused(abi, kw):
     refused(abi, "csa2_tree_attn", ATTN, kw, "I")
+
+
+@pytest.mark.parametrize("name", ["n_free", "n_free_out"])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_commit_counts_that_no_load_can_reach_are_refused(abi, name, by):
+    refused(abi, "csa2_tree_commit", COMMIT, {name: 9 * FAR + by}, "I")
+
+
+PAGES = dict(cached=FAR, added=2 * FAR, n_req=2, page=16, table=3 * FAR, max_pages=4, free=4 * FAR, n_pages=8, n_free=5 * FAR, n_free_out=5 * FAR,
+             q_start=6 * FAR, kv_len=7 * FAR, slots=8 * FAR, pos=9 * FAR, max_new=6, ws=10 * FAR, ws_bytes=256, stream=None)
+
+
+@pytest.mark.parametrize("name", ["n_free", "n_free_out", "q_start", "kv_len"])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_page_plan_numbers_that_no_load_can_reach_are_refused(abi, name, by):
+    refused(abi, "csa2_page_plan", PAGES, {name: 11 * FAR + by}, "I")
