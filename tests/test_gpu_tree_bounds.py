@@ -6,9 +6,65 @@ import torch
 
 from oracle import tree_oracle as TO
 from tests.test_gpu_paged import attn_inputs
-from tests.test_gpu_tree import Commit, Tree, abi, dev, f64, tree_layer, trees, walk_inputs  # noqa: F401
+from tests.test_gpu_tree import Commit, Heads, Tree, abi, dev, f64, tree_layer, trees, walk_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+D = 512
+
+
+# ------------------------------------------------------------- head norms
+def set_rows(h, q, lat):
+    """The values of q [n][heads * 512] and lat [n][512] as the call's inputs."""
+    h.q[:, :h.heads * D] = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    h.lat[:, :D] = torch.from_numpy(lat).to(torch.bfloat16).cuda()
+    h.x64, h.lat64 = f64(h.q)[:h.n, :h.heads * D].reshape(h.n, h.heads, D), f64(h.lat)[:h.n, :D]
+
+
+@pytest.mark.parametrize("fmt,turn", [("fp4", True), ("fp4", False), ("fp8", True)])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_heads_at_the_largest_values(abi, fmt, turn, eps):
+    """Values up to 2^56: rows that are full of them, of one alone, and random ones; the bounds of Heads.check hold (sums of
+    squares reach 512 * 2^112, far below fp32's largest number)."""
+    rng = np.random.default_rng(23)
+    h = Heads(abi, rng, 24, 3, fmt, turn=turn)
+    most = 2.0 ** 56
+    q, lat = (np.clip(2.0 ** 55 * rng.standard_normal((24, w)), -most, most) for w in (3 * D, D))
+    for x in (q, lat):
+        x[0] = most
+        x[1] = np.where(rng.random(x.shape[1]) < 0.5, most, -most)
+        x[2] = 0
+        x[2, ::D] = -most
+        x[3, 5::D] = most
+    set_rows(h, q, lat)
+    assert h.q.abs().max() == most and h.lat.abs().max() == most
+    h.call(eps=eps).check(eps=float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("fmt,turn", [("fp4", True), ("fp4", False), ("fp8", True)])
+def test_heads_at_the_smallest_rows_without_eps(abi, fmt, turn):
+    """Rows whose largest value is 2^-60, eps 0.  The mean of the squares of k such values is k 2^-129, where fp32 steps by
+    2^-149: off by 2^-21 / k relative, its root by 2^-22 / k.  Where k is small the sum of squares rounds less for it (k - 1
+    times): root 2^-24 ((k - 1) / 2 + 4 / k) below the 5 * 2^-24 that are counted for it up to k = 10, and beyond that the
+    mean's part is below 2^-25."""
+    rng = np.random.default_rng(24)
+    h = Heads(abi, rng, 24, 3, fmt, turn=turn)
+    least = 2.0 ** -60
+    q, lat = (np.clip(2.0 ** -61 * rng.standard_normal((24, w)), -least, least) for w in (3 * D, D))
+    for x in (q, lat):
+        x[:, 7::D] = least  # in every row and head
+        x[0] = least
+        x[1] = 0
+        x[1, ::D] = -least
+        for k in range(2, 12):
+            x[k] = 0
+            for j in range(k):
+                x[k, 40 * j::D] = least * (1 if j else 1.5)
+        x[12] = 2.0 ** -75 * rng.standard_normal(x.shape[1])
+        x[12, 100::D] = least
+        x[13] = 2.0 ** -120 * rng.standard_normal(x.shape[1])
+        x[13, 200::D] = 1.25 * least
+    set_rows(h, q, lat)
+    h.call(eps=0.0).check(eps=0.0)
 
 
 # ------------------------------------------------------------------ commit
