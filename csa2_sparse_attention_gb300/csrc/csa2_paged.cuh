@@ -106,6 +106,12 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int32_t words
     const uint32_t lo = __ldg(row + w), hi = w + 1 < words ? __ldg(row + w + 1) : 0;
     return __funnelshift_r(lo, hi, off & 31);
 }
+// The position of a node for its window: within [first, place], the request's first
+// node's and the one that it would have in a chain.  Key tiles begin at the first
+// node's window, so a position of the caller's below it has nothing more to see.
+__device__ __forceinline__ int32_t tree_position(int64_t pos, int32_t first, int32_t place) {
+    return pos <= first ? first : pos < place ? int32_t(pos) : place;
+}
 // Bits of the keys k .. k + 31 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t range_bits(int32_t k, int32_t lo, int32_t hi) {
     const int32_t l = lo - k, h = hi - k;

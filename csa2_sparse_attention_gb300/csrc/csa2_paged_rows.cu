@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kRThreads, 1) paged_rows_kernel(const PagedArg
             const int32_t hi = on ? it.rq.len - it.rq.nq + (it.row0 + row) / a.by_heads + 1 : 0;
             if (TREE) {  // the positions before the request's tokens
                 S.tok[row] = p >= 0 ? it.rq.q0 + (it.row0 + row) / a.by_heads : -1;
-                S.keys[row] = make_int2(a.window > 0 ? int32_t(p < hi - 1 ? p : hi - 1) + 1 - a.window : 0,
+                S.keys[row] = make_int2(a.window > 0 ? tree_position(p, it.rq.len - it.rq.nq, hi - 1) + 1 - a.window : 0,
                                         p >= 0 ? it.rq.len - it.rq.nq : 0);
             } else {
                 S.keys[row] = make_int2(a.window > 0 ? hi - a.window : 0, hi);

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
                     if (TREE) {
                         const int64_t p = __ldg(a.pos + rq.q0 + at);
                         if (p >= 0) mask = a.mask + int64_t(rq.q0 + at) * a.words;
-                        lo_r = a.window > 0 ? int32_t(p < hi_r - 1 ? p : hi_r - 1) + 1 - a.window : 0;
+                        lo_r = a.window > 0 ? tree_position(p, rq.len - rq.nq, hi_r - 1) + 1 - a.window : 0;
                         hi_r = p >= 0 ? rq.len - rq.nq : 0;
                     } else {
                         lo_r = a.window > 0 ? hi_r - a.window : 0;

@@ -525,9 +525,9 @@ csa2_status csa2_tree_plan(const int32_t* parent, const int32_t* q_start, const 
  * pos and mask are csa2_tree_plan's for the same window; a node of pos below 0
  * sees nothing.  (With other masks: bits at and behind the nodes' number, and
  * above the node's own, are to be 0.  A pos above kv_len - nodes + i counts as
- * that.)  What is written lies apart from what is read and from each other.
- * Everything else, max_q up to 1024 apart, is as in csa2_paged_attn (the keys are
- * split in other places than there).
+ * that, one below kv_len - nodes as the first node's.)  What is written lies
+ * apart from what is read and from each other.  Everything else, max_q up to 1024
+ * apart, is as in csa2_paged_attn (the keys are split in other places than there).
  * ws: csa2_tree_attn_workspace_bytes (0 for bad sizes) for the same sizes.
  */
 size_t csa2_tree_attn_workspace_bytes(int64_t n_tokens, int n_heads, int64_t n_req, int32_t max_q, int32_t max_kv,

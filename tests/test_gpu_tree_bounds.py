@@ -4,9 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged_oracle as PO
 from oracle import tree_oracle as TO
 from tests.test_gpu_paged import attn_inputs
-from tests.test_gpu_tree import Commit, Heads, Tree, abi, dev, f64, tree_layer, trees, walk_inputs  # noqa: F401
+from tests.test_gpu_tree import SM, U, Commit, Heads, Tree, abi, dev, f64, tree_layer, trees, walk_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 D = 512
@@ -205,3 +206,49 @@ def test_attention_walks_write_every_row_again(abi, n_req, H, kind, longest, pag
     torch.cuda.synchronize()
     T = int(s["q_start"][-1])
     assert torch.equal(out[:T], t.out[:T]) and torch.equal(lse[:T], t.lse[:T]) and (t.out[T:] == 5).all() and (t.lse[T:] == 5).all()
+
+
+@pytest.mark.parametrize("cached,nodes,H,window", [
+    ([130, 301], [40, 9], 16, 20), ([700], [16], 64, 100), ([1500, 1290, 40], [12, 40, 3], 8, 1050), ([900, 1000], [90, 70], 64, 300),
+    ([3500, 3300], [70, 66], 64, 3100)])
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_attention_positions_of_the_caller(abi, cached, nodes, H, window, fmt):
+    """Positions that csa2_tree_plan does not give: below the request's first node, where they count as that one's, and above
+    the node's place, where they count as it.  (Both kernels, split as for one request and for several.)"""
+    rng = np.random.default_rng(25)
+    s = attn_inputs(rng, np.asarray(cached) + nodes, nodes, H, 16, fmt)
+    parent = trees(rng, nodes)
+    t = Tree(abi, s, parent, window).plan()
+    mask = np.zeros((s["T"], t.words), np.uint64)
+    see, low = [], []
+    for r, n in enumerate(nodes):
+        a, first = int(s["q_start"][r]), cached[r]
+        for i in range(n):
+            p = int(rng.choice([0, max(0, first - window), max(0, first - 9), first - 1, first, first + i // 2, first + i, first + i + 1, 1 << 40]))
+            t.pos[a + i] = p
+            own = np.flatnonzero(rng.random(i + 1) < 0.3)
+            for j in own:
+                mask[a + i, j // 32] |= np.uint64(1 << (j % 32))
+            low.append(max(0, min(max(p, first), first + i) + 1 - window))
+            see.append(np.concatenate([np.arange(low[-1], first), first + own]))
+    t.mask.copy_(dev(mask.astype(np.uint32).view(np.int32)))
+    t.plan = lambda stream=None: t
+    t.call()
+    torch.cuda.synchronize()
+    assert abi.csa2_status_fetch(t.ws)[0] == abi.OK
+    out, lse, q = f64(t.out), f64(t.lse), f64(t.q)
+    for r, n in enumerate(nodes):
+        a = int(s["q_start"][r])
+        p = np.arange(cached[r] + n)
+        rows = s["table"][r, p // 16].astype(np.int64) * 16 + p % 16
+        c = PO.latent_rows(s["codes"][rows], None if s["scales"] is None else s["scales"][rows])
+        for i in range(a, a + n):
+            k = c[see[i]]
+            x = SM * q[i] @ k.T
+            m = x.max(1, keepdims=True)
+            e = np.exp(x - m)
+            want, wl = e / e.sum(1, keepdims=True) @ k, (m + np.log(e.sum(1, keepdims=True)))[:, 0]
+            d = 64 * U * np.max(np.abs(q[i]) @ np.abs(k).T) * SM + 2.0 ** -21  # (as in Tree.check)
+            big = np.abs(k).max()
+            assert (np.abs(out[i] - want) <= (2 * d + 2.0 ** -11 + len(p) * U) * big + (2.0 ** -8 + len(p) * U) * np.abs(want)).all(), (r, i - a)
+            assert (np.abs(lse[i] - wl) <= d + len(p) * U + 2.0 ** -22 * (1 + np.abs(wl))).all(), (r, i - a)
