@@ -68,6 +68,12 @@ def _rows(name, x, n, shape, dev, dtype=torch.bfloat16):
         raise ValueError(f"{name}: contiguous {dtype} rows of {tuple(shape)}, at least {n} of them, not {x.dtype} {tuple(x.shape)}")
 
 
+def _at16(name, x):
+    """x begins on a 16-byte boundary, which a view into other data may not."""
+    if x.data_ptr() % 16:
+        raise ValueError(f"{name}: not 16-byte aligned")
+
+
 def fp4_weight(w):
     """FP4 form (codes [n][k/2], scales [n][k/16]) of bf16 weights w [n][k], k a multiple of 128, on the current stream."""
     n, k = w.shape
@@ -224,6 +230,7 @@ class PagedLatents:
             raise ValueError(f"{max_q} nodes of a request: up to {abi.TREE_NODES}, and to the {self.max_tokens} tokens of a step")
         for name, (x, n, dtype) in per_node.items():
             _rows(name, x, n, (), self.dev, dtype)
+            _at16(name, x)
 
     def tree(self, parent, n_tokens, max_q, stream=None):
         """Behind plan(): the step's tokens are trees.  parent [n_tokens] int32: the place of a node's parent among its
@@ -355,6 +362,7 @@ class PagedLayer:
         for name, w in (("q_norm", q_norm), ("latent_norm", latent_norm)):
             if w is not None:
                 _rows(name, w, LATENT, (), d)
+                _at16(name, w)  # (no step gets as far as its append otherwise)
         self.q_norm, self.latent_norm, self.heads_pass = q_norm, latent_norm, turn or q_norm is not None or latent_norm is not None
         self.cache, self.hidden, self.eps, self.norm_weight = cache, hidden, eps, norm_weight.contiguous()
         self.wq, self.wlatent = fp4_weight(wq), fp4_weight(wlatent)

@@ -124,6 +124,27 @@ def test_steps_without_tokens_are_committed(abi, added):
         assert st[0] == abi.OK, (name, st)
 
 
+def test_step_of_a_view_off_a_boundary_changes_nothing(abi):
+    """parents that the masks' call would refuse, once residual and pages had changed: refused before, and the next step is as
+    if nothing had been."""
+    paged, g, cache, layer = tree_layer(abi, abi.FMT_FP4, 0, True)
+    nodes = [5, 0, 7]
+    cache.added.copy_(torch.tensor(nodes, dtype=torch.int32))
+    par = torch.zeros(16, dtype=torch.int32, device="cuda")
+    par[3:15] = dev(trees(np.random.default_rng(0), nodes))
+    x = torch.randn(12, 256, generator=g).to(torch.bfloat16).cuda()
+    held = (layer.residual, cache.cached, cache.n_free, cache.free, cache.table, cache.kv_len, cache.q_start, cache.pos, cache.codes)
+    before = [t.clone() for t in held]
+    with pytest.raises(ValueError, match="not 16-byte aligned"):
+        layer.step(x, 12, 7, 10, parent=par[3:])
+    torch.cuda.synchronize()
+    for a, b in zip(held, before):
+        assert torch.equal(a, b)
+    layer.step(x, 12, 7, 10, parent=par[3:].clone())
+    torch.cuda.synchronize()
+    assert cache.kv_len.tolist() == nodes
+
+
 def test_commit_of_no_tokens_records_what_is_left_of_others(abi):
     """Without tokens, token bounds of an earlier step do not hold: recorded, and nothing is read or moved."""
     c = Commit(abi, np.random.default_rng(22), [20, 9], [3, 7], 8, "fp4").upload()

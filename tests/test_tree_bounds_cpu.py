@@ -1,5 +1,6 @@
 """Refusals of the calls of a step of trees beyond those of test_tree_cpu.py: no launch, no pointer that is valid."""
 import pytest
+import torch
 
 from tests.test_tree_cpu import COMMIT, abi, refused  # noqa: F401
 
@@ -36,3 +37,20 @@ PAGES = dict(cached=FAR, added=2 * FAR, n_req=2, page=16, table=3 * FAR, max_pag
 @pytest.mark.parametrize("by", [1, 2, 3])
 def test_page_plan_numbers_that_no_load_can_reach_are_refused(abi, name, by):
     refused(abi, "csa2_page_plan", PAGES, {name: 11 * FAR + by}, "I")
+
+
+def test_views_off_a_boundary_are_refused_before_a_step(abi):
+    """Nodes' values and weights that the calls would refuse in the middle of a step."""
+    from csa2_sparse_attention_gb300 import paged
+    c = paged.PagedLatents(2, 8, 4, 16, 2, heads=1, fmt=abi.FMT_FP8, device="cpu")
+    bf = torch.bfloat16
+    par, tok = torch.zeros(12, dtype=torch.int32), torch.zeros(12, dtype=torch.int64)
+    w = lambda *shape: torch.zeros(shape, dtype=bf)  # noqa: E731
+    c0 = abi.csa2_launch_count()
+    for bad in (lambda: c.tree(par[1:], 8, 4), lambda: c.tree(par[3:], 8, 4), lambda: c.commit(par[2:], tok, tok, 8, 4),
+                lambda: c.commit(par, tok[1:], tok, 8, 4), lambda: c.commit(par, tok, tok[1:], 8, 4),
+                lambda: paged.PagedLayer(c, 256, w(256), w(512, 256), w(512, 256), q_norm=w(520)[3:515]),
+                lambda: paged.PagedLayer(c, 256, w(256), w(512, 256), w(512, 256), latent_norm=w(520)[4:516])):
+        with pytest.raises(ValueError, match="not 16-byte aligned"):
+            bad()
+    assert abi.csa2_launch_count() == c0
