@@ -144,8 +144,9 @@ __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
 // launched directly behind paged_decode_kernel, and paged_rows_kernel behind
 // both.  Every CTA of the decode kernel lets its dependents start only after its
 // own wait, so when a CTA of either runs, all work before the call is done and
-// visible: they read the call's inputs and write the status word, the split count
-// and (the second one) outputs that none of the three kernels reads.  What the
+// visible: they read the call's inputs and write the status word, the split
+// length, the cuts of items and (the second one) outputs, of which none of the
+// three kernels reads any.  What the
 // decode kernel writes is read after grid_dep_wait(), and every CTA waits before
 // it ends, so that whatever comes behind them finds all of it.  Their shared
 // memory keeps two of these kernels' CTAs, and so their TMEM, off one

@@ -1,6 +1,8 @@
 // Causal attention over paged latents: the call's plan, its entry points and
 // the join of its splits (the kernels: csa2_paged_rows.cu for requests of up to
-// 256 (token, head) rows or four key tiles, csa2_paged_tiles.cu for more).
+// 256 (token, head) rows or four key tiles, csa2_paged_tiles.cu for more; trees of
+// several requests that are laid out by their lengths go to one of them together,
+// by their rows on average: kWalkMost).
 #include "csa2_paged.cuh"
 #include "csa2_timer.cuh"
 
@@ -234,14 +236,23 @@ static_assert(kPSms <= 256, "a thread a cut");
 // took 42.0 us without that and 34.6 us with it.
 // Trees of several requests that see enough key tiles are laid out by their real
 // lengths (walk_first): in the few-row kernel with 512 rows each or less on average
-// and enough rows for most multiprocessors, in row tiles with more, up to three
-// items for each group of four CTAs.  64 heads, up to so many nodes over so many
-// entries, us in the few-row kernel, in row tiles and as above:
+// (kWalkMost), in row tiles with more, up to three items for each group of four
+// CTAs.  64 heads, up to so many nodes over so many entries, us in the few-row
+// kernel, in row tiles and as above:
 //   16 requests, 2K to 8K: 3 nodes 58 - 55, 5 79 100 200, 8 110 123 188, 12 154 160 185, 16 194 187 222, 24 275 256 292,
 //     32 352 318 317, 64 - 565 520
 //   4, 2K to 8K: 6 46 49 75, 8 51 52 63, 12 67 63 70, 16 76 71 91, 32 129 108 157;  2: 8 38 39 37, 32 73 70 81
 //   8: 8 of 512 to 2K 37 37 57, 32 of them - 72 65, 64 of them - 113 110;  64: 8 of 512 to 2K 132 147 147, 16 233 221 220
 //   24 of up to 45 x 16 heads, window 128: 26 - 21
+// Where no request has more than 256 rows the call has to have the rows of 45 full
+// items as well (kWalkRows): with fewer items than that, one split length for all
+// fills the multiprocessors as evenly, without the search for cuts and their join.
+// Requests of a quarter of so many nodes to all of them, as many entries likewise,
+// us over up to 2K / up to 8K with one split length and as above:
+//   64 heads: 4 requests, 4 nodes (704 rows) 24 / 33, 26 / 34; 8, 4 (1344) 26 / 42, 28 / 44; 16, 3 (1984) 30 / 56, 31 / 56;
+//     32, 2 (2752) 38 / 76, 36 / 66; 24, 3 (3008) 39 / 82, 36 / 71; 32, 3 (3968) 63 / 94, 41 / 84; 64, 1 (4096) 51 / 129, 44 / 94
+//   16 heads: 8, 16 (1376) 28 / 45, 29 / 47; 24, 8 (1968) 33 / 67, 32 / 59; 16, 16 (2656) 38 / 93, 35 / 66; 24, 16 (3936) 63 / 118, 42 / 90
+// (Between 2000 rows and the border long contexts would gain already.)
 constexpr int64_t kWalkRows = 45 * 64, kWalkMost = 512, kWalkTileRows = 3 * 38 * 256;
 constexpr int32_t kWalkKeys = 8, kWalkTileKeys = 24;  // key tiles
 struct PagedShare {  // of one of the kernels

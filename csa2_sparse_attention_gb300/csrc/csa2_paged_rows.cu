@@ -1,5 +1,6 @@
 // Causal attention over paged latents for requests of few rows (single tokens
-// and short chunks) and for chunks that see few keys: 64 (token, head) rows per
+// and short chunks), for chunks that see few keys, and for several requests' trees
+// of up to 512 rows on average (one may have many more): 64 (token, head) rows per
 // CTA, all 512 channels.
 //
 // With few rows every key is decoded for one or a few CTAs only, and the

@@ -100,8 +100,10 @@ __global__ void __launch_bounds__(kPTileThreads, 1) paged_tiles_kernel(const Pag
     grid_dep_launch();
     // The set-up and Q come before the wait for the decode kernel, this launch's
     // predecessor: it starts its dependents only after its own wait, so all that
-    // the call's inputs come from is done by then, and nothing but the status word
-    // is written before.
+    // the call's inputs come from is done by then.  What is written before the wait
+    // is the status word, the split length (paged_find) and the cuts of items
+    // (walk_first): the join of an earlier call, which reads the last two, is among
+    // what the decode kernel has waited for, and the decode kernel reads neither.
 
     if (WALK) {
         walk_first<kPTileThreads / 32>(a, blockIdx.x >> 2, blockIdx.x == 0, S.work[0], S.sums);
